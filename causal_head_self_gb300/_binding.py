@@ -7,7 +7,9 @@ implementation to fall back to.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 import threading
 
@@ -32,7 +34,8 @@ ATTN_ERR_CHECK = 7
 # every symbol include/attn.h declares
 ABI_SYMBOLS = ("attn_fwd", "attn_fwd_lse", "attn_fwd_chunk", "attn_bwd", "attn_decode",
                "attn_decode_ring", "attn_decode_noalloc", "attn_status", "attn_error_string",
-               "attn_version", "attn_debug_inject_fault")
+               "attn_version", "attn_debug_inject_fault", "attn_paged_append", "attn_decode_paged",
+               "attn_decode_paged_workspace", "attn_key_weights", "attn_cache_evict")
 
 _lib = None
 _lock = threading.Lock()
@@ -68,6 +71,18 @@ def load():
             lib.attn_decode_ring.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, f, vp]
             lib.attn_decode_noalloc.restype = i
             lib.attn_decode_noalloc.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, f, vp]
+            lib.attn_paged_append.restype = i
+            lib.attn_paged_append.argtypes = [vp] * 7 + [i] * 7 + [vp]
+            lib.attn_decode_paged.restype = i
+            lib.attn_decode_paged.argtypes = ([vp] * 7 + [i, i, vp, ctypes.c_size_t] + [i] * 8
+                                              + [f, vp])
+            lib.attn_decode_paged_workspace.restype = i
+            lib.attn_decode_paged_workspace.argtypes = [i] * 7 + [ctypes.POINTER(ctypes.c_size_t)]
+            lib.attn_key_weights.restype = i
+            lib.attn_key_weights.argtypes = [vp] * 5 + [i] * 10 + [f, vp]
+            lib.attn_cache_evict.restype = i
+            lib.attn_cache_evict.argtypes = [vp, vp, vp, i, vp, vp, i, i, vp, i, vp, i, vp, vp] \
+                + [i] * 6 + [vp]
             lib.attn_status.restype = i
             lib.attn_status.argtypes = [vp]
             lib.attn_error_string.restype = ctypes.c_char_p
@@ -315,3 +330,198 @@ def attn_debug_inject_fault(kind: int) -> None:
 def attn_status(stream=None) -> int:
     """Synchronise the stream; return and clear the device's latched error code."""
     return int(load().attn_status(_stream_handle(stream)))
+
+
+# ---------------------------------------------------------------------------
+# the paged cache (include/attn.h)
+
+def _this_device() -> int:
+    return _current_device() if _current_device is not None else torch.cuda.current_device()
+
+
+def _check(name, t, dtype, shape, device):
+    """A contiguous tensor of that type and shape, on the same GPU as the others."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA {dtype} tensor")
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor, got {list(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the same device as the other tensors")
+
+
+def _check_pools(kpages, vpages, table, seqlens):
+    """The checks that every paged call makes: (B, Hkv, num_pages, page, cols, Dh, device)."""
+    _check_bf16("kpages", kpages, 4)
+    P, Hkv, page, Dh = kpages.shape
+    device = kpages.get_device()
+    if device != _this_device():
+        raise ValueError("the tensors must be on the current device (torch.cuda.device)")
+    _check("vpages", vpages, torch.bfloat16, (P, Hkv, page, Dh), device)
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("table must be a [B, cols] tensor")
+    B, cols = table.shape
+    _check("table", table, torch.int32, (B, cols), device)
+    _check("seqlens", seqlens, torch.int32, (B,), device)
+    return B, Hkv, P, page, cols, Dh, device
+
+
+def _rows_of(name, t, lead, device):
+    """A contiguous float32 [*lead, stride] tensor: its stride."""
+    if not isinstance(t, torch.Tensor) or t.dim() != len(lead) + 1:
+        raise ValueError(f"{name} must be a float32 [B, Hkv, rows] tensor")
+    _check(name, t, torch.float32, (*lead, t.shape[-1]), device)
+    return t.shape[-1]
+
+
+def _on(stream):
+    """Allocations of a call belong to the stream that it runs on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def attn_paged_append(k, v, kpages, vpages, table, seqlens, newlens=None, *, stream=None):
+    """Write new keys and values k, v [B,Hkv,S,Dh] to a paged cache: pools
+    [P,Hkv,page,Dh] bf16, table [B,cols] int32, seqlens [B] int32 = keys held
+    after the append, newlens [B] int32 = real rows of k and v (None: all S).
+    Returns (kpages, vpages), which are written in place."""
+    B, Hkv, P, page, cols, Dh, device = _check_pools(kpages, vpages, table, seqlens)
+    _check_bf16("k", k, 4)
+    S = k.shape[2]
+    _check("k", k, torch.bfloat16, (B, Hkv, S, Dh), device)
+    _check("v", v, torch.bfloat16, (B, Hkv, S, Dh), device)
+    if newlens is not None:
+        _check("newlens", newlens, torch.int32, (B,), device)
+    rc = load().attn_paged_append(k.data_ptr(), v.data_ptr(), kpages.data_ptr(), vpages.data_ptr(),
+                                  table.data_ptr(), seqlens.data_ptr(),
+                                  None if newlens is None else newlens.data_ptr(), B, Hkv, S, P,
+                                  page, cols, Dh, _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_paged_append")
+    return kpages, vpages
+
+
+@functools.lru_cache(maxsize=4096)
+def _decode_paged_workspace(device, B, Hq, Hkv, page, cols, Dh, with_weights):
+    size = ctypes.c_size_t()
+    rc = load().attn_decode_paged_workspace(B, Hq, Hkv, page, cols, Dh, int(with_weights),
+                                            ctypes.byref(size))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_decode_paged_workspace")
+    return size.value
+
+
+def attn_decode_paged_workspace(q, kpages, table, *, weights=False):
+    """Bytes of workspace that attn_decode_paged needs for tensors of these
+    shapes, with or without weights."""
+    return _decode_paged_workspace(_this_device(), q.shape[0], q.shape[1],
+                                   kpages.shape[1], kpages.shape[2], table.shape[1], q.shape[3],
+                                   bool(weights))
+
+
+def attn_decode_paged(q, kpages, vpages, table, seqlens, o=None, *, window=0, scale=0.0,
+                      weights=None, accumulate=True, workspace=None, stream=None):
+    """One decode step over a paged cache (see attn_paged_append).  q
+    [B,Hq,1,Dh]; a length of 0 gives a zero output.  weights [B,Hkv,rows]
+    fp32 (rows >= cols * page) receives each key's softmax weight summed over
+    its query heads, added to what is there or, with accumulate=False, in its
+    place.  workspace: a uint8 tensor of attn_decode_paged_workspace() bytes
+    (None: allocated here by torch, on the call's stream).  Returns o."""
+    B, Hkv, P, page, cols, Dh, device = _check_pools(kpages, vpages, table, seqlens)
+    _check_bf16("q", q, 4)
+    Hq = q.shape[1]
+    _check("q", q, torch.bfloat16, (B, Hq, 1, Dh), device)
+    stride = 0 if weights is None else _rows_of("weights", weights, (B, Hkv), device)
+    need = _decode_paged_workspace(device, B, Hq, Hkv, page, cols, Dh, weights is not None)
+    if o is not None:
+        _check("o", o, torch.bfloat16, (B, Hq, 1, Dh), device)
+    if workspace is not None and (not isinstance(workspace, torch.Tensor)
+                                  or workspace.dtype != torch.uint8
+                                  or workspace.get_device() != device
+                                  or not workspace.is_contiguous()):
+        raise TypeError("workspace must be a contiguous CUDA uint8 tensor on the same device")
+    if o is None or workspace is None:
+        with _on(stream):
+            if o is None:
+                o = torch.empty_like(q)
+            if workspace is None:
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    rc = load().attn_decode_paged(q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(),
+                                  table.data_ptr(), seqlens.data_ptr(), o.data_ptr(),
+                                  None if weights is None else weights.data_ptr(), stride,
+                                  int(bool(accumulate)), workspace.data_ptr(), workspace.numel(),
+                                  B, Hq, Hkv, P, page, cols, Dh, int(window), float(scale),
+                                  _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_decode_paged")
+    return o
+
+
+def attn_key_weights(q, k, lse, weights, seqlens=None, *, queries=0, causal=True, window=0,
+                     scale=0.0, accumulate=True, stream=None):
+    """The softmax weight that each key of a prompt received, summed over the
+    query heads of its K/V head and over the last `queries` queries (0: all):
+    weights [B,Hkv,rows] fp32, rows >= S, is added to, or replaced with
+    accumulate=False.  q [B,Hq,S,Dh], k [B,Hkv,S,Dh] and lse [B,Hq,S] as
+    attn_fwd_lse took and returned them; seqlens [B] int32: the real rows of a
+    padded prompt.  Returns weights."""
+    _check_bf16("q", q, 4)
+    _check_bf16("k", k, 4)
+    B, Hq, S, Dh = q.shape
+    Hkv = k.shape[1]
+    device = q.get_device()
+    if device != _this_device():
+        raise ValueError("the tensors must be on the current device (torch.cuda.device)")
+    _check("k", k, torch.bfloat16, (B, Hkv, S, Dh), device)
+    _check("lse", lse, torch.float32, (B, Hq, S), device)
+    stride = _rows_of("weights", weights, (B, Hkv), device)
+    if seqlens is not None:
+        _check("seqlens", seqlens, torch.int32, (B,), device)
+    rc = load().attn_key_weights(q.data_ptr(), k.data_ptr(), lse.data_ptr(),
+                                 None if seqlens is None else seqlens.data_ptr(),
+                                 weights.data_ptr(), stride, B, Hq, Hkv, S, Dh, int(queries),
+                                 int(bool(causal)), int(window), int(bool(accumulate)),
+                                 float(scale), _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_key_weights")
+    return weights
+
+
+def attn_cache_evict(kpages, vpages, weights, table, seqlens, budget, recent=0, *, table_out=None,
+                     weights_out=None, newlens=None, keep=None, stream=None):
+    """Shrink each sequence of a paged cache to at most `budget` keys: the last
+    `recent` rows and those with the largest weights [B,Hkv,rows] fp32 before
+    them, per K/V head, in their order.  The kept rows move to the pages of
+    table_out [B,cols_out] int32 (None: in place), their weights to
+    weights_out (None: in place).  Returns (newlens [B], keep [B,Hkv,budget]):
+    the new lengths, and each kept row's former number (then -1)."""
+    B, Hkv, P, page, cols, Dh, device = _check_pools(kpages, vpages, table, seqlens)
+    stride = _rows_of("weights", weights, (B, Hkv), device)
+    budget, recent = int(budget), int(recent)
+    cols_out, stride_out = cols, stride
+    if table_out is not None:
+        if not isinstance(table_out, torch.Tensor) or table_out.dim() != 2:
+            raise ValueError("table_out must be a [B, cols] tensor")
+        cols_out = table_out.shape[1]
+        _check("table_out", table_out, torch.int32, (B, cols_out), device)
+    if weights_out is not None:
+        stride_out = _rows_of("weights_out", weights_out, (B, Hkv), device)
+    if budget < 1:
+        raise AttnError(ATTN_ERR_INVALID_ARG, "attn_cache_evict")
+    if newlens is not None:
+        _check("newlens", newlens, torch.int32, (B,), device)
+    if keep is not None:
+        _check("keep", keep, torch.int32, (B, Hkv, budget), device)
+    if newlens is None or keep is None:
+        with _on(stream):
+            if newlens is None:
+                newlens = torch.empty_like(seqlens)
+            if keep is None:
+                keep = torch.empty((B, Hkv, budget), dtype=torch.int32, device=seqlens.device)
+    rc = load().attn_cache_evict(kpages.data_ptr(), vpages.data_ptr(), weights.data_ptr(), stride,
+                                 table.data_ptr(), seqlens.data_ptr(), budget, recent,
+                                 None if table_out is None else table_out.data_ptr(), cols_out,
+                                 None if weights_out is None else weights_out.data_ptr(),
+                                 stride_out, newlens.data_ptr(), keep.data_ptr(), B, Hkv, P, page,
+                                 cols, Dh, _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_cache_evict")
+    return newlens, keep

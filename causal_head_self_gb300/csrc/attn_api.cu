@@ -494,3 +494,227 @@ extern "C" int attn_decode_noalloc(const void* q, const void* kcache, const void
                                      launch_info(st), stream);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
+
+// ---------------------------------------------------------------------------
+// The paged cache: append, decode, key weights, eviction.
+namespace {
+
+// Shape checks that every paged entry point shares.
+int paged_check(int B, int Hkv, const chs::PagedCache& c, int Dh) {
+  if (B < 0 || Hkv < 1 || c.num_pages < 1 || c.cols < 1 || c.page < 1) return ATTN_ERR_INVALID_ARG;
+  if (Dh != 64 && Dh != 128 && Dh != 256) return ATTN_ERR_UNSUPPORTED;
+  if (c.page % 8 != 0) return ATTN_ERR_UNSUPPORTED;
+  // positions, and a pool's (page, head) pairs, are 32-bit
+  if ((long long)c.cols * c.page > 0x7fffffffLL - 1024) return ATTN_ERR_INVALID_ARG;
+  if ((long long)c.num_pages * Hkv > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+
+// Pointers that a kernel reads or writes: none null, aligned to `align`.
+bool usable(const void* p, uintptr_t align) {
+  return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (align - 1)) == 0;
+}
+
+// Does `out` overlap any of the others?
+template <size_t N>
+bool overlaps_any(const Span& out, const Span (&others)[N]) {
+  for (const Span& s : others)
+    if (s.p && overlaps(out.p, out.bytes, s.p, s.bytes)) return true;
+  return false;
+}
+
+size_t pool_bytes(int Hkv, const chs::PagedCache& c, int Dh) {
+  return (size_t)c.num_pages * Hkv * c.page * Dh * 2;
+}
+
+}  // namespace
+
+extern "C" int attn_paged_append(const void* k, const void* v, void* kpages, void* vpages,
+                                 const int* table, const int* seqlens, const int* newlens, int B,
+                                 int Hkv, int S, int num_pages, int page, int cols, int Dh,
+                                 cudaStream_t stream) {
+  const chs::PagedCache cache{num_pages, page, cols};
+  int rc = paged_check(B, Hkv, cache, Dh);
+  if (rc != ATTN_OK) return rc;
+  if (S < 0) return ATTN_ERR_INVALID_ARG;
+  if (B == 0 || S == 0) return ATTN_OK;
+  if (!usable(k, 16) || !usable(v, 16) || !usable(kpages, 16) || !usable(vpages, 16) ||
+      !usable(table, 4) || !usable(seqlens, 4) || (newlens && !usable(newlens, 4)))
+    return ATTN_ERR_INVALID_ARG;
+  if ((long long)B * Hkv * S > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+  const size_t in = (size_t)B * Hkv * S * Dh * 2, pool = pool_bytes(Hkv, cache, Dh);
+  const Span rest[] = {{k, in}, {v, in}, {table, (size_t)B * cols * 4}, {seqlens, (size_t)B * 4},
+                       {newlens, (size_t)B * 4}};
+  if (overlaps_any({kpages, pool}, rest) || overlaps_any({vpages, pool}, rest) ||
+      overlaps(kpages, pool, vpages, pool))
+    return ATTN_ERR_INVALID_ARG;
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&st)) != ATTN_OK) return rc;
+  const cudaError_t e = chs::launch_paged_append(k, v, kpages, vpages, table, seqlens, newlens, B,
+                                                 Hkv, S, cache, Dh, launch_info(st), stream);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+// The size rules of a paged decode call, shared with its workspace query.
+static int decode_paged_check(int B, int Hq, int Hkv, const chs::PagedCache& cache, int Dh) {
+  const int rc = paged_check(B, Hkv, cache, Dh);
+  if (rc != ATTN_OK) return rc;
+  if (Hq < 1 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+  // the line of tiles (64 keys at least) and the grids are 32-bit
+  const long long rows = (long long)cache.cols * cache.page;
+  const long long units = (long long)B * Hkv * ((Hq / Hkv + 127) / 128);
+  if (units > (1 << 24) || units * ((rows + 63) / 64) > 0x7fffffffLL - 1024)
+    return ATTN_ERR_INVALID_ARG;
+  if ((long long)B * Hq + (long long)B * Hkv * ((rows + 511) / 512) > 0x7fffffffLL)
+    return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+extern "C" int attn_decode_paged_workspace(int B, int Hq, int Hkv, int page, int cols, int Dh,
+                                           int with_weights, size_t* bytes) {
+  const chs::PagedCache cache{1, page, cols};
+  int rc = decode_paged_check(B, Hq, Hkv, cache, Dh);
+  if (rc != ATTN_OK) return rc;
+  if (!bytes) return ATTN_ERR_INVALID_ARG;
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&st)) != ATTN_OK) return rc;
+  *bytes = chs::decode_paged_workspace_bytes(B, Hq, Hkv, cache, Dh, with_weights != 0,
+                                             st->info.num_sms);
+  return ATTN_OK;
+}
+
+extern "C" int attn_decode_paged(const void* q, const void* kpages, const void* vpages,
+                                 const int* table, const int* seqlens, void* o, float* weights,
+                                 int weights_stride, int accumulate, void* workspace,
+                                 size_t workspace_bytes, int B, int Hq, int Hkv, int num_pages,
+                                 int page, int cols, int Dh, int window, float scale,
+                                 cudaStream_t stream) {
+  const chs::PagedCache cache{num_pages, page, cols};
+  int rc = decode_paged_check(B, Hq, Hkv, cache, Dh);
+  if (rc != ATTN_OK) return rc;
+  if (window < 0) window = 0;
+  if (weights && weights_stride < cols * page) return ATTN_ERR_INVALID_ARG;
+  if (accumulate != 0 && accumulate != 1) return ATTN_ERR_INVALID_ARG;
+  float scale_log2 = 0.f;
+  if (!resolve_scale(scale, Dh, &scale_log2)) return ATTN_ERR_INVALID_ARG;
+  if (B == 0) return ATTN_OK;
+  if (!usable(q, 16) || !usable(kpages, 16) || !usable(vpages, 16) || !usable(o, 16) ||
+      !usable(table, 4) || !usable(seqlens, 4) || (weights && !usable(weights, 4)) ||
+      !usable(workspace, 256))
+    return ATTN_ERR_INVALID_ARG;
+  const size_t qo = (size_t)B * Hq * Dh * 2, pool = pool_bytes(Hkv, cache, Dh);
+  const size_t wb = weights ? (size_t)B * Hkv * weights_stride * 4 : 0;
+  const Span in[] = {{q, qo}, {kpages, pool}, {vpages, pool}, {table, (size_t)B * cols * 4},
+                     {seqlens, (size_t)B * 4}};
+  if (overlaps_any({o, qo}, in) || overlaps_any({workspace, workspace_bytes}, in) ||
+      overlaps(o, qo, workspace, workspace_bytes))
+    return ATTN_ERR_INVALID_ARG;
+  if (weights && (overlaps_any({weights, wb}, in) || overlaps(weights, wb, o, qo) ||
+                  overlaps(weights, wb, workspace, workspace_bytes)))
+    return ATTN_ERR_INVALID_ARG;
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&st)) != ATTN_OK) return rc;
+  if (workspace_bytes < chs::decode_paged_workspace_bytes(B, Hq, Hkv, cache, Dh,
+                                                          weights != nullptr, st->info.num_sms))
+    return ATTN_ERR_SCRATCH_LIMIT;
+  const cudaError_t e = chs::launch_decode_paged(
+      q, kpages, vpages, table, seqlens, o, weights, weights_stride, accumulate, workspace, B, Hq,
+      Hkv, cache, Dh, window, scale_log2, launch_info(st), stream);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+extern "C" int attn_key_weights(const void* q, const void* k, const float* lse, const int* seqlens,
+                                float* weights, int weights_stride, int B, int Hq, int Hkv, int S,
+                                int Dh, int queries, int causal, int window, int accumulate,
+                                float scale, cudaStream_t stream) {
+  if (B < 0 || S < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+  if (Dh != 64 && Dh != 128 && Dh != 256) return ATTN_ERR_UNSUPPORTED;
+  if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
+  if (accumulate != 0 && accumulate != 1) return ATTN_ERR_INVALID_ARG;
+  if (window < 0) window = 0;
+  if (window > 0 && !causal) return ATTN_ERR_INVALID_ARG;
+  if (queries < 0) queries = 0;
+  if (weights_stride < S) return ATTN_ERR_INVALID_ARG;
+  float scale_log2 = 0.f;
+  if (!resolve_scale(scale, Dh, &scale_log2)) return ATTN_ERR_INVALID_ARG;
+  if (B == 0 || S == 0) return ATTN_OK;
+  if (!usable(q, 16) || !usable(k, 16) || !usable(lse, 4) || !usable(weights, 4) ||
+      (seqlens && !usable(seqlens, 4)))
+    return ATTN_ERR_INVALID_ARG;
+  const long long key_blocks = ((long long)S + 127) / 128;
+  if (key_blocks * B * Hkv > 0x7fffffffLL || (long long)S > 0x7fffffffLL - 1024 ||
+      key_blocks * (Hq / Hkv) > 0x7fffffffLL || (long long)B * Hq > 0x7fffffffLL)
+    return ATTN_ERR_INVALID_ARG;
+  const size_t qb = (size_t)B * Hq * S * Dh * 2, kb = (size_t)B * Hkv * S * Dh * 2;
+  const Span in[] = {{q, qb}, {k, kb}, {lse, (size_t)B * Hq * S * 4}, {seqlens, (size_t)B * 4}};
+  if (overlaps_any({weights, (size_t)B * Hkv * weights_stride * 4}, in)) return ATTN_ERR_INVALID_ARG;
+  DeviceState* st = nullptr;
+  const int rc = device_state(&st);
+  if (rc != ATTN_OK) return rc;
+  const cudaError_t e = chs::launch_key_weights(q, k, lse, seqlens, weights, weights_stride, B, Hq,
+                                                Hkv, S, Dh, causal, window, queries, accumulate,
+                                                scale_log2, launch_info(st), stream);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+extern "C" int attn_cache_evict(void* kpages, void* vpages, float* weights, int weights_stride,
+                                const int* table, const int* seqlens, int budget, int recent,
+                                const int* table_out, int cols_out, float* weights_out,
+                                int weights_out_stride, int* newlens, int* keep, int B, int Hkv,
+                                int num_pages, int page, int cols, int Dh, cudaStream_t stream) {
+  const chs::PagedCache cache{num_pages, page, cols};
+  int rc = paged_check(B, Hkv, cache, Dh);
+  if (rc != ATTN_OK) return rc;
+  if (table_out == nullptr) {
+    table_out = table;
+    cols_out = cols;
+  }
+  if (weights_out == nullptr) {
+    weights_out = weights;
+    weights_out_stride = weights_stride;
+  }
+  if (budget < 1 || recent < 0 || recent > budget) return ATTN_ERR_INVALID_ARG;
+  const long long rows = (long long)cols * page;
+  const long long most = budget < rows ? budget : rows;   // rows that a sequence may end with
+  if (weights_stride < rows || weights_out_stride < most || cols_out < 1 ||
+      (long long)cols_out * page > 0x7fffffffLL - 1024 || (long long)cols_out * page < most)
+    return ATTN_ERR_INVALID_ARG;
+  if (table_out == table && cols_out != cols) return ATTN_ERR_INVALID_ARG;
+  if (weights_out == weights && weights_out_stride != weights_stride) return ATTN_ERR_INVALID_ARG;
+  if ((long long)B * Hkv > 0xffffffLL ||
+      (long long)B * Hkv * (((long long)budget + 31) / 32 + 1) > 0x7fffffffLL)
+    return ATTN_ERR_INVALID_ARG;
+  if (B == 0) return ATTN_OK;
+  if (!usable(kpages, 16) || !usable(vpages, 16) || !usable(weights, 4) || !usable(table, 4) ||
+      !usable(seqlens, 4) || !usable(table_out, 4) || !usable(weights_out, 4) ||
+      !usable(newlens, 4) || !usable(keep, 4))
+    return ATTN_ERR_INVALID_ARG;
+  const size_t pool = pool_bytes(Hkv, cache, Dh), lens = (size_t)B * 4;
+  const size_t wb = (size_t)B * Hkv * weights_stride * 4;
+  const size_t wob = (size_t)B * Hkv * weights_out_stride * 4;
+  const size_t kb = (size_t)B * Hkv * budget * 4;
+  const Span in[] = {{table, (size_t)B * cols * 4}, {table_out, (size_t)B * cols_out * 4},
+                     {seqlens, lens}};
+  const Span out[] = {{kpages, pool}, {vpages, pool}, {newlens, lens}, {keep, kb},
+                      {weights_out, wob}};
+  for (size_t i = 0; i < 5; ++i) {
+    if (overlaps_any(out[i], in)) return ATTN_ERR_INVALID_ARG;
+    for (size_t j = 0; j < i; ++j)
+      if (overlaps(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return ATTN_ERR_INVALID_ARG;
+    // the weights: read, and written only where they are weights_out too
+    if (!(i == 4 && weights_out == weights) && overlaps(out[i].p, out[i].bytes, weights, wb))
+      return ATTN_ERR_INVALID_ARG;
+  }
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&st)) != ATTN_OK) return rc;
+  const cudaError_t e = chs::launch_cache_evict(
+      kpages, vpages, table, table_out, cols_out, seqlens, newlens, weights, weights_stride,
+      weights_out, weights_out_stride, keep, B, Hkv, cache, Dh, budget, recent, launch_info(st),
+      stream);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}

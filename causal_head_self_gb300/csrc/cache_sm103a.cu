@@ -1,0 +1,132 @@
+// cache_sm103a.cu -- host launchers of the paged cache's kernels: append, key
+// weights of a prompt, eviction.
+#include "cache_sm103a.cuh"
+#include "key_weights_sm103a.cuh"
+#include "launch.h"
+
+namespace chs {
+
+cudaError_t launch_paged_append(const void* k, const void* v, void* kpages, void* vpages,
+                                const int* table, const int* seqlens, const int* newlens, int B,
+                                int Hkv, int S, const PagedCache& cache, int Dh,
+                                const DeviceInfo& dev, cudaStream_t stream) {
+  AppendParams prm;
+  prm.k = static_cast<const uint4*>(k);
+  prm.v = static_cast<const uint4*>(v);
+  prm.kpages = static_cast<uint4*>(kpages);
+  prm.vpages = static_cast<uint4*>(vpages);
+  prm.table = table;
+  prm.seqlens = seqlens;
+  prm.newlens = newlens;
+  prm.rows = (long long)B * Hkv * S;
+  prm.Hkv = Hkv;
+  prm.S = S;
+  prm.vecs = Dh / 8;
+  prm.num_pages = cache.num_pages;
+  prm.page = cache.page;
+  prm.cols = cache.cols;
+  prm.error_word = dev.error_word;
+  const int per_pass = kAppendThreads / prm.vecs;
+  constexpr int U = 4;
+  const long long blocks1 = (prm.rows + per_pass - 1) / per_pass;
+  if (blocks1 <= 8LL * dev.num_sms)
+    return launch_pdl(attn_paged_append_sm103a<1>, dim3((unsigned)blocks1), dim3(kAppendThreads), 0,
+                      stream, prm);
+  return launch_pdl(attn_paged_append_sm103a<U>, dim3((unsigned)((blocks1 + U - 1) / U)),
+                    dim3(kAppendThreads), 0, stream, prm);
+}
+
+template <int DH>
+static cudaError_t launch_key_weights_dh(const CUtensorMap& mq, const CUtensorMap& mk,
+                                         const KeyWeightsParams& prm, int device,
+                                         cudaStream_t stream) {
+  constexpr size_t smem = key_weights_smem_bytes<DH>();
+  static_assert(smem * KeyWeightsCfg<DH>::kCtasPerSm <= 232448, "shared memory of one SM");
+  static std::atomic<int> configured[kMaxDevices];
+  cudaError_t e = configure_once(configured, device, [] {
+    return cudaFuncSetAttribute(attn_key_weights_sm103a<DH>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  });
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attn_key_weights_sm103a<DH>, dim3((unsigned)(prm.key_blocks * prm.B * prm.Hkv)),
+                    dim3(KeyWeightsCfg<DH>::kThreads), smem, stream, mq, mk, prm);
+}
+
+cudaError_t launch_key_weights(const void* q, const void* k, const float* lse, const int* seqlens,
+                               float* weights, int stride, int B, int Hq, int Hkv, int S, int Dh,
+                               int causal, int window, int queries, int accumulate,
+                               float scale_log2, const DeviceInfo& dev, cudaStream_t stream) {
+  CUtensorMap mq, mk;
+  if (!encode_bf16_map(&mq, q, Dh, S, (long long)B * Hq, 128) ||
+      !encode_bf16_map(&mk, k, Dh, S, (long long)B * Hkv, 128))
+    return cudaErrorInvalidValue;
+  KeyWeightsParams prm;
+  prm.B = B;
+  prm.Hq = Hq;
+  prm.Hkv = Hkv;
+  prm.G = Hq / Hkv;
+  prm.S = S;
+  prm.causal = causal;
+  prm.window = window;
+  prm.queries = queries;
+  prm.accumulate = accumulate;
+  prm.key_blocks = (S + 127) / 128;
+  prm.scale_log2 = scale_log2;
+  prm.lse = lse;
+  prm.seqlens = seqlens;
+  prm.weights = weights;
+  prm.stride = stride;
+  prm.error_word = dev.error_word;
+  return Dh == 256   ? launch_key_weights_dh<256>(mq, mk, prm, dev.device, stream)
+         : Dh == 128 ? launch_key_weights_dh<128>(mq, mk, prm, dev.device, stream)
+                     : launch_key_weights_dh<64>(mq, mk, prm, dev.device, stream);
+}
+
+cudaError_t launch_cache_evict(void* kpages, void* vpages, const int* table, const int* table_out,
+                               int cols_out, const int* seqlens, int* newlens,
+                               const float* weights, int stride, float* weights_out,
+                               int stride_out, int* keep, int B, int Hkv, const PagedCache& cache,
+                               int Dh, int budget, int recent, const DeviceInfo& dev,
+                               cudaStream_t stream) {
+  EvictParams prm;
+  prm.kpages = static_cast<uint4*>(kpages);
+  prm.vpages = static_cast<uint4*>(vpages);
+  prm.table = table;
+  prm.table_out = table_out;
+  prm.seqlens = seqlens;
+  prm.newlens = newlens;
+  prm.weights = weights;
+  prm.weights_out = weights_out;
+  prm.keep = keep;
+  prm.B = B;
+  prm.Hkv = Hkv;
+  prm.vecs = Dh / 8;
+  prm.num_pages = cache.num_pages;
+  prm.page = cache.page;
+  prm.cols = cache.cols;
+  prm.cols_out = cols_out;
+  prm.stride = stride;
+  prm.stride_out = stride_out;
+  prm.budget = budget;
+  prm.recent = recent;
+  prm.error_word = dev.error_word;
+  cudaError_t e = launch_pdl(attn_cache_select_sm103a, dim3(B * Hkv), dim3(kSelectThreads), 0,
+                             stream, prm);
+  if (e != cudaSuccess) return e;
+  if (table_out == table) {
+    constexpr int U = 4;
+    // column slices of 64 bytes at least, as few as give every SM two blocks
+    int piece = prm.vecs;
+    while (piece > 4 && 2LL * B * Hkv * (prm.vecs / piece) < 2LL * dev.num_sms) piece /= 2;
+    return launch_pdl(attn_cache_move_in_place_sm103a<U>,
+                      dim3((unsigned)(2 * B * Hkv * (prm.vecs / piece))), dim3(kMoveThreads), 0,
+                      stream, prm, piece);
+  }
+  constexpr int U = 4;
+  const int per_pass = kMoveThreads / prm.vecs;
+  const int blocks = (budget + per_pass * U - 1) / (per_pass * U);
+  return launch_pdl(attn_cache_move_sm103a<U>, dim3((unsigned)B * Hkv * blocks), dim3(kMoveThreads),
+                    0, stream, prm);
+}
+
+}  // namespace chs

@@ -1,0 +1,789 @@
+// decode_paged_sm103a.cuh -- one decode step over a paged key-value cache, on
+// the 5th-generation tensor cores (sm_103a).
+//
+// For sequence b of L = seqlens[b] keys and query head h of K/V head g,
+//   s_t = scale q_h . k_t,  p = softmax over t in [lo, L),  o_h = sum_t p_t v_t,
+// with row t of the sequence in page table[b, t / page] at row t % page.  The
+// step reads every visible K and V row once for a few FLOPs per byte, so it is
+// bound by HBM bandwidth; everything here serves to keep loads in flight.
+//
+// Work split.  The lengths are known only on the device and differ from
+// sequence to sequence, so a split fixed on the host leaves SMs idle.  Instead
+// the tiles (kKeys keys) of all units (sequence, K/V head, block of 128 query
+// heads) form one line, in unit order, and CTA c of the grid (one per SM) takes
+// tiles [c * share, (c + 1) * share) of it, whatever units they belong to.  A
+// unit thus is cut at most where a CTA's share ends.  The part of a unit that a
+// CTA holds is a segment; the segment of CTA c and unit u has the number u + c
+// (along the line one of the two grows from segment to segment, so no two
+// share a number), which is its place in the partial results.  A second kernel
+// joins the segments of each unit.
+//
+// Pipeline.  One warp loads (TMA), one issues the tensor-core work, four run
+// the softmax.  Q, K and V tiles pass through one ring of equal slots in the
+// order Q, K0, V0, K1, V1, ... of each segment, and the loading warp runs ahead
+// into the next segments.  Q moves on to tensor memory at once (tcgen05.cp), so
+// its slot is soon free again.  A page holds `page` rows of one head in a row,
+// so a tile is gathered in boxes of box_rows = gcd(page, kKeys) rows, each of
+// them in one page; the lanes of the loading warp each take one box.
+//
+// Softmax.  A warp reaches only its own 32 lanes (rows) of tensor memory.  A
+// group of up to 32 query heads is therefore copied four times into the 128
+// rows (REP = 4), and warp w works on keys [w kKeys / 4, (w + 1) kKeys / 4) of
+// the tile for its copy, with P = 0 at the other keys: a quarter of the work
+// each, and four partial results per segment.  Larger groups use every row
+// (REP = 1).
+//
+// Rows outside [lo, L) are never used: boxes without a visible row are not
+// loaded (their table entries may hold anything), scores of invisible rows are
+// replaced by -inf, and their V rows are zeroed in shared memory before the
+// product (stale rows may hold NaN, and 0 * NaN is NaN).
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "sm103a_ptx.cuh"
+
+namespace chs {
+
+struct DecodePagedParams {
+  int B, Hq, Hkv, G, window;
+  int num_pages, page, cols;   // pool pages, rows per page, table columns
+  int box_rows;                // rows per TMA box
+  int row_blocks;              // blocks of 128 query heads per K/V head
+  int ctas;                    // CTAs of the grid
+  int score_stride;            // row length of `scores`
+  float scale_log2;
+  int accumulate;
+  const int* seqlens;          // [B], device
+  const int* table;            // [B, cols], device
+  float* o_part;               // [segments, REP, rows, DH] unnormalised
+  float* m_part;               // [segments, REP, rows]     (log2 domain)
+  float* l_part;               // [segments, REP, rows]
+  int2* unit_ctas;             // [units]: first and last CTA of a unit
+  float* scores;               // [B, Hq, score_stride] raw q . k, or null
+  float* weights;              // [B, Hkv, weights_stride], or null
+  int weights_stride;
+  __nv_bfloat16* o;            // [B, Hq, 1, DH]
+  int* error_word;
+  int fault;                   // test hook: 3 = the first K tile is never loaded
+};
+
+template <int DH>
+struct DecodePagedCfg {
+  static constexpr int kKeys = DH <= 128 ? 128 : 64;   // keys per tile
+  static constexpr int kBoxes = DH / 64;               // 64-column boxes per row
+  static constexpr int kKvBox = kKeys * 128;           // bytes: kKeys rows of 64 columns
+  static constexpr int kQBox = 128 * 128;              // bytes: 128 rows of 64 columns
+  static constexpr int kSlot = kBoxes * kKvBox;        // ring slot: one K or V tile
+  static constexpr int kQSlots = kBoxes * kQBox / kSlot;   // slots that Q takes: 1, at Dh 256 2
+  static constexpr int kSlots = 224 * 1024 / kSlot;    // 14 (Dh 64) or 7
+  static constexpr int kThreads = 192;                 // warps 0-3 softmax, 4 loads, 5 MMA
+  static constexpr int kWarpProducer = 4, kWarpIssuer = 5;
+  // tensor memory: S0, S1 | Q | O
+  static constexpr uint32_t kColQ = DH == 256 ? 128 : 384, kColO = 256, kCols = 512;
+  static_assert(2 * kKeys <= 256 && kColO + DH <= (DH == 256 ? 512u : kColQ), "tensor memory");
+};
+
+template <int DH>
+struct DecodePagedSmem {
+  using Cfg = DecodePagedCfg<DH>;
+  uint8_t slot[Cfg::kSlots][Cfg::kSlot];
+  uint64_t full[Cfg::kSlots], empty[Cfg::kSlots];
+  uint64_t s_full[2], p_full[2], pv_done, o_final, qt_free, mma_done;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+// Keys that a sequence may hold at most.
+__device__ __forceinline__ int paged_rows(const DecodePagedParams& p) { return p.cols * p.page; }
+
+// A sequence's visible keys [lo, L) and its tiles: n of them from tile `first`
+// on (tile i holds positions kKeys * i ...).  None for a length of 0 or one
+// outside [0, cols * page].
+struct PagedSeq {
+  int L, lo, first, n;
+};
+template <int KEYS>
+__device__ __forceinline__ PagedSeq paged_seq(const DecodePagedParams& p, int b) {
+  PagedSeq s;
+  s.L = __ldcg(p.seqlens + b);
+  if (s.L < 0 || s.L > paged_rows(p)) s.L = 0;
+  s.lo = p.window > 0 ? max(0, s.L - p.window) : 0;
+  s.first = s.lo / KEYS;
+  s.n = (s.L + KEYS - 1) / KEYS - s.first;
+  return s;
+}
+
+// One segment: tiles [tile0, tile0 + count) of unit gi (K/V head and row
+// block) of sequence b.
+struct PagedSegment {
+  int b, gi, L, lo, tile0, count;
+  bool starts;        // holds the unit's first tile
+  int unit, last_cta;
+};
+
+// The segments of one CTA in order.  Every warp walks them for itself.
+template <int KEYS>
+struct PagedWalk {
+  int cur, end, share;   // places on the line of tiles
+  int b, gi, j0;         // next segment: unit and first tile in it
+  PagedSeq seq;
+
+  // Places [cur, end) of CTA `cta`.  One whole warp.
+  __device__ __forceinline__ void init(const DecodePagedParams& p, int cta) {
+    const int lane = threadIdx.x % 32;
+    const int per_seq = p.Hkv * p.row_blocks;   // units per sequence
+    int total = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const int bb = b0 + lane;
+      total += bb < p.B ? paged_seq<KEYS>(p, bb).n * per_seq : 0;
+    }
+    total = __reduce_add_sync(0xffffffffu, total);
+    share = max(1, (total + p.ctas - 1) / p.ctas);
+    cur = (int)min((long long)total, (long long)cta * share);
+    end = min(total, cur + share);
+    b = gi = j0 = 0;
+    if (cur >= end) return;
+    int before = 0;   // tiles of the sequences before b0
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const int bb = b0 + lane;
+      const int mine = bb < p.B ? paged_seq<KEYS>(p, bb).n * per_seq : 0;
+      int upto = mine;   // inclusive scan
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += y;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, before + upto > cur);
+      if (past) {
+        const int at = __ffs(past) - 1;
+        b = b0 + at;
+        const int offset = cur - before - __shfl_sync(0xffffffffu, upto - mine, at);
+        seq = paged_seq<KEYS>(p, b);
+        gi = offset / seq.n;
+        j0 = offset - gi * seq.n;
+        return;
+      }
+      before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+  }
+
+  __device__ __forceinline__ bool next(const DecodePagedParams& p, PagedSegment& s) {
+    if (cur >= end) return false;
+    const int per_seq = p.Hkv * p.row_blocks;
+    if (gi == per_seq) {
+      gi = 0;
+      do {
+        seq = paged_seq<KEYS>(p, ++b);
+      } while (seq.n == 0);
+    }
+    s.b = b;
+    s.gi = gi;
+    s.L = seq.L;
+    s.lo = seq.lo;
+    s.tile0 = seq.first + j0;
+    s.count = min(seq.n - j0, end - cur);
+    s.starts = j0 == 0;
+    s.unit = b * per_seq + gi;
+    s.last_cta = (cur - j0 + seq.n - 1) / share;
+    cur += s.count;
+    j0 += s.count;
+    if (j0 == seq.n) {
+      j0 = 0;
+      ++gi;
+    }
+    return true;
+  }
+};
+
+// A place in the ring: slot and the parity of its current use.
+template <int SLOTS>
+struct PagedRing {
+  int slot = 0;
+  uint32_t par = 0;
+  __device__ __forceinline__ void step() {
+    if (++slot == SLOTS) {
+      slot = 0;
+      par ^= 1u;
+    }
+  }
+};
+
+__device__ __forceinline__ void mbar_wait_drain_paged(uint64_t* bar, uint32_t parity) {
+  const uint32_t a = smem_u32(bar);
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(a, parity)) {
+    if (globaltimer_ns() - t0 > kWaitLimitNs) return;
+  }
+}
+
+// Loading warp.  Lane l takes box l % boxes of rows and 64-column block
+// l / boxes of every K and V tile (at most 32 boxes per tile: 128 rows / 8 x 2,
+// 64 rows / 8 x 4); the table entry of its box is fetched a tile ahead.
+template <int DH, int REP>
+__device__ __forceinline__ void decode_paged_producer(DecodePagedSmem<DH>& sm,
+                                                      const DecodePagedParams& p,
+                                                      const CUtensorMap* map_q,
+                                                      const CUtensorMap* map_k,
+                                                      const CUtensorMap* map_v,
+                                                      PagedWalk<DecodePagedCfg<DH>::kKeys> walk,
+                                                      int lane, volatile int* abort) {
+  using Cfg = DecodePagedCfg<DH>;
+  const uint64_t once = policy_evict_first();   // each cached row is read by one CTA
+  const int boxes = Cfg::kKeys / p.box_rows;
+  const int box = lane % boxes, half = lane / boxes;
+  const bool has_box = half < Cfg::kBoxes;
+  const int box_bytes = p.box_rows * 128;
+  const uint32_t dst_off = (uint32_t)(half * Cfg::kKvBox + box * box_bytes);
+  PagedRing<Cfg::kSlots> r;
+  uint32_t loaded = 0, pars = 0;
+  bool ok = true, first = true;
+  auto wait_slot = [&]() -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(&sm.empty[r.slot], r.par ^ 1u, abort));
+  };
+  auto mark_slot = [&] {
+    loaded |= 1u << r.slot;
+    pars = (pars & ~(1u << r.slot)) | (r.par << r.slot);
+    r.step();
+  };
+  PagedSegment s;
+  while (ok && walk.next(p, s)) {
+    const int g = s.gi / p.row_blocks, rb = s.gi - g * p.row_blocks;
+    if (lane == 0 && s.starts) p.unit_ctas[s.unit] = make_int2(blockIdx.x, s.last_cta);
+    const int* row = p.table + (size_t)s.b * p.cols;
+    // this lane's box of a tile: the page that holds it (-1: no visible row)
+    auto page_of = [&](int tile) -> int {
+      const int pos = tile * Cfg::kKeys + box * p.box_rows;
+      if (!has_box || pos >= s.L || pos + p.box_rows <= s.lo) return -1;
+      const int id = __ldcg(row + pos / p.page);
+      if (id >= 0 && id < p.num_pages) return id;
+      atomicExch(p.error_word, 1);   // ATTN_ERR_INVALID_ARG: no such page
+      return 0;
+    };
+    int id = page_of(s.tile0);
+    // Q: REP copies of the group's rows
+    constexpr int kPerBox = REP, kRows = 128 / REP;
+    for (int e = 0; ok && e < Cfg::kQSlots; ++e) {
+      if (!(ok = wait_slot())) break;
+      constexpr int kBoxesPerSlot = Cfg::kBoxes / Cfg::kQSlots;
+      if (lane == 0) mbar_arrive_expect_tx(&sm.full[r.slot], kBoxesPerSlot * Cfg::kQBox);
+      __syncwarp();
+      if (lane < kBoxesPerSlot * kPerBox) {
+        const int bx = lane / kPerBox, copy = lane % kPerBox;
+        tma_load_3d(sm.slot[r.slot] + bx * Cfg::kQBox + copy * kRows * 128, map_q,
+                    &sm.full[r.slot], (e * kBoxesPerSlot + bx) * 64, 128 * rb, s.b * p.Hkv + g);
+      }
+      mark_slot();
+    }
+    for (int j = 0; ok && j < s.count; ++j) {
+      const int tile = s.tile0 + j, pos0 = tile * Cfg::kKeys;
+      const int my = id;
+      const int pos = pos0 + box * p.box_rows;
+      const int c1 = pos % p.page, c2 = my * p.Hkv + g;
+      // (checked builds: a box lies inside one page of the pool)
+      const bool load = my >= 0 && attn_check(my < p.num_pages && c1 >= 0 &&
+                                                  c1 + p.box_rows <= p.page && g < p.Hkv,
+                                              p.error_word);
+      const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, load)) * box_bytes);
+      if (j + 1 < s.count) id = page_of(tile + 1);
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        if (!(ok = wait_slot())) break;
+        if (kv == 0 && first && p.fault == 3) {   // (the test hook withholds one tile)
+          first = false;
+          r.step();
+          continue;
+        }
+        first = false;
+        if (lane == 0) mbar_arrive_expect_tx(&sm.full[r.slot], bytes);
+        __syncwarp();
+        if (load)
+          tma_load_3d_hint(sm.slot[r.slot] + dst_off, kv ? map_v : map_k, &sm.full[r.slot],
+                           half * 64, c1, c2, once);
+        mark_slot();
+      }
+    }
+  }
+  // every copy this warp started has landed before the CTA may exit
+  if (lane == 0)
+    for (int i = 0; i < Cfg::kSlots; ++i)
+      if (loaded & (1u << i)) mbar_wait_drain_paged(&sm.full[i], (pars >> i) & 1u);
+}
+
+// Tensor-core warp.  Per segment: Q to tensor memory, S of the first two tiles,
+// then per tile P.V and the S two tiles on, into the buffer that P came from.
+template <int DH>
+__device__ __forceinline__ void decode_paged_issuer(DecodePagedSmem<DH>& sm,
+                                                    const DecodePagedParams& p, uint32_t tbase,
+                                                    PagedWalk<DecodePagedCfg<DH>::kKeys> walk,
+                                                    volatile int* abort) {
+  using Cfg = DecodePagedCfg<DH>;
+  constexpr uint32_t idesc_qk = idesc_bf16_f32(128, Cfg::kKeys, false, false);
+  constexpr uint32_t idesc_pv = idesc_bf16_f32(128, DH, false, true);
+  const uint64_t base = smem_u32(sm.slot[0]) >> 4;
+  const uint64_t kmajor = smem_desc_sw128(0, 16, 1024) | base;
+  const uint64_t mnmajor = smem_desc_sw128(0, Cfg::kKvBox, 1024) | base;
+  const uint32_t dO = tbase + Cfg::kColO;
+  auto wait = [&](uint64_t* bar, uint32_t par) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(bar, par, abort));
+  };
+  PagedRing<Cfg::kSlots> rk, rv;   // next K and next V entry of the ring
+  uint32_t t = 0;                  // tiles so far, over all segments
+  uint32_t nseg = 0;
+  bool ok = true;
+  PagedSegment s;
+  while (ok && walk.next(p, s)) {
+    // the ring holds Q, K0, V0, K1, V1, ...; rv stands at the segment's first entry
+    rk = rv;
+    if (nseg > 0 && !(ok = wait(&sm.qt_free, (nseg - 1) & 1u))) break;
+    for (int e = 0; ok && e < Cfg::kQSlots; ++e, rk.step()) {
+      if (!(ok = wait(&sm.full[rk.slot], rk.par))) break;
+      tc_fence_after_sync();
+      constexpr int kSteps = DH / 16 / Cfg::kQSlots;
+      const uint64_t q = kmajor + (uint64_t)rk.slot * (Cfg::kSlot >> 4);
+#pragma unroll
+      for (int kk = 0; kk < kSteps; ++kk)
+        tmem_cp_128x256b_warp(tbase + Cfg::kColQ + 8 * (e * kSteps + kk),
+                              q + (((kk / 4) * Cfg::kQBox + (kk % 4) * 32) >> 4));
+      mma_commit_warp(&sm.empty[rk.slot]);
+    }
+    if (!ok) break;
+    ++nseg;
+    rv = rk;
+    rv.step();
+    auto issue_s = [&](uint32_t tt) -> bool {
+      if (!wait(&sm.full[rk.slot], rk.par)) return false;
+      tc_fence_after_sync();
+      const uint32_t dS = tbase + (uint32_t)Cfg::kKeys * (tt & 1u);
+      const uint64_t k = kmajor + (uint64_t)rk.slot * (Cfg::kSlot >> 4);
+#pragma unroll
+      for (int kk = 0; kk < DH / 16; ++kk)
+        mma_bf16_ts_warp(dS, tbase + Cfg::kColQ + 8 * kk,
+                         k + (((kk / 4) * Cfg::kKvBox + (kk % 4) * 32) >> 4), idesc_qk,
+                         kk > 0 ? 1u : 0u);
+      mma_commit_warp(&sm.s_full[tt & 1u]);
+      mma_commit_warp(&sm.empty[rk.slot]);
+      rk.step();
+      rk.step();
+      return true;
+    };
+    if (!(ok = issue_s(t))) break;
+    if (s.count > 1 && !(ok = issue_s(t + 1))) break;
+    if (s.count <= 2) mma_commit_warp(&sm.qt_free);
+    for (int j = 0; j < s.count; ++j, ++t) {
+      if (!(ok = wait(&sm.full[rv.slot], rv.par))) break;
+      if (!(ok = wait(&sm.p_full[t & 1u], (t >> 1) & 1u))) break;
+      tc_fence_after_sync();
+      const uint32_t dP = tbase + (uint32_t)Cfg::kKeys * (t & 1u);
+      const uint64_t v = mnmajor + (uint64_t)rv.slot * (Cfg::kSlot >> 4);
+#pragma unroll
+      for (int kk = 0; kk < Cfg::kKeys / 16; ++kk)
+        mma_bf16_ts_warp(dO, dP + kk * 8, v + kk * (2048 >> 4), idesc_pv,
+                         (j > 0 || kk > 0) ? 1u : 0u);
+      mma_commit_warp(&sm.pv_done);
+      mma_commit_warp(&sm.empty[rv.slot]);
+      rv.step();
+      if (j + 1 < s.count) rv.step();
+      if (j + 2 < s.count) {
+        if (!(ok = issue_s(t + 2))) break;
+        if (j + 3 == s.count) mma_commit_warp(&sm.qt_free);
+      }
+    }
+    if (ok) mma_commit_warp(&sm.o_final);
+  }
+  // nothing of this warp's may still run on the tensor core at teardown
+  mma_commit_warp(&sm.mma_done);
+  mbar_wait_drain_paged(&sm.mma_done, 0);
+}
+
+// Softmax warps: thread t owns row t (tensor-memory lane t).  With REP = 4 row
+// 32 w + i is query head i of the block, for the keys of quarter w.
+template <int DH, int REP>
+__device__ __forceinline__ void decode_paged_softmax(DecodePagedSmem<DH>& sm,
+                                                     const DecodePagedParams& p, uint32_t tbase,
+                                                     PagedWalk<DecodePagedCfg<DH>::kKeys> walk,
+                                                     int warp, int lane, int active_warps,
+                                                     volatile int* abort) {
+  using Cfg = DecodePagedCfg<DH>;
+  constexpr int kMine = Cfg::kKeys / REP;             // keys of a tile per warp
+  constexpr int kChunk = kMine < 32 ? kMine : 32;     // columns per load
+  constexpr int kChunks = kMine / kChunk;
+  const int col0 = REP == 4 ? warp * kMine : 0;
+  const int head = REP == 4 ? lane : warp * 32 + lane;   // in the block of query heads
+  const int copy = REP == 4 ? warp : 0;
+  const int tid = warp * 32 + lane;
+  const uint32_t lane_addr = tbase + ((uint32_t)(warp * 32) << 16);
+  const uint32_t colO = lane_addr + Cfg::kColO;
+  const float sl2 = p.scale_log2;
+  PagedRing<Cfg::kSlots> r;   // the ring entry of the current tile's V
+  uint32_t t = 0;             // tiles so far, over all segments
+  uint32_t nseg = 0;
+  bool ok = true;
+  PagedSegment s;
+  while (ok && walk.next(p, s)) {
+    for (int e = 0; e < Cfg::kQSlots; ++e) r.step();
+    const int g = s.gi / p.row_blocks, rb = s.gi - g * p.row_blocks;
+    const int rows = min(128, p.G - 128 * rb);
+    const bool real = head < rows;
+    const size_t bh = (size_t)s.b * p.Hq + (size_t)g * p.G + 128 * rb + head;
+    float m_run = -INFINITY, l_run = 0.f;
+    for (int j = 0; j < s.count; ++j, ++t) {
+      r.step();   // past K
+      const int pos0 = (s.tile0 + j) * Cfg::kKeys;
+      const int clo = max(0, s.lo - pos0), chi = min(Cfg::kKeys, s.L - pos0);   // visible columns
+      const bool partial = clo > 0 || chi < Cfg::kKeys;
+      if (!(ok = mbar_wait(&sm.s_full[t & 1u], (t >> 1) & 1u, abort))) break;
+      tc_fence_after_sync();
+      const uint32_t colS = lane_addr + (uint32_t)Cfg::kKeys * (t & 1u);
+      float x[kMine];
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        uint32_t y[kChunk];
+        if constexpr (kChunk == 32) tmem_ld_32x32b_x32(colS + col0 + 32 * c, y);
+        else tmem_ld_32x32b_x16(colS + col0 + 16 * c, y);
+        tmem_ld_wait(y);
+#pragma unroll
+        for (int e = 0; e < kChunk; ++e) x[kChunk * c + e] = __uint_as_float(y[e]);
+      }
+      if (partial) {
+        // invisible keys become -inf, whatever was there
+#pragma unroll
+        for (int e = 0; e < kMine; ++e)
+          x[e] = keep_if_le(x[e], (uint32_t)(col0 + e - clo), (uint32_t)(chi - 1 - clo));
+      }
+      if (p.scores != nullptr && real) {
+        // raw scores (rows of the buffer are whole tiles, 32-byte aligned)
+        float* dst = p.scores + bh * (size_t)p.score_stride + pos0 + col0;
+#pragma unroll
+        for (int e = 0; e < kMine / 8; ++e) {
+          uint32_t w8[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w8[i] = __float_as_uint(x[8 * e + i]);
+          st_global_v8(dst + 8 * e, w8);
+        }
+      }
+      float mx[2] = {x[0], x[1]};
+#pragma unroll
+      for (int e = 2; e + 3 < kMine; e += 4) {
+        mx[0] = fmax3(mx[0], x[e], x[e + 1]);
+        mx[1] = fmax3(mx[1], x[e + 2], x[e + 3]);
+      }
+      mx[0] = fmax3(mx[0], x[kMine - 2], x[kMine - 1]);
+      const float m_tile = fmaxf(mx[0], mx[1]) * sl2;
+      // lazy maximum (raised only past +8 in log2 units; exact either way)
+      const float m_new = fmaxf(m_run, m_tile);
+      const bool fresh = m_run == -INFINITY;
+      const bool upd = fresh || (m_new > m_run + 8.0f);
+      const float m_use = upd ? m_new : m_run;
+      const float corr = (upd && !fresh) ? ex2_approx(m_run - m_new) : 1.0f;
+      const float msub = (m_use == -INFINITY) ? 0.f : m_use;
+      const float2 scale2 = make_float2(sl2, sl2), neg_m2 = make_float2(-msub, -msub);
+      float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      // P in bf16 (the tensor core's operand type; a rounding of 2^-9 relative
+      // per weight, the sum l is taken before it) over the first kKeys / 2
+      // columns of S, zero at the keys of the other quarters.  Those columns
+      // hold scores of this warp's rows only, which are all read by now.
+      if constexpr (REP == 4) {
+        uint32_t zero[kMine / 2];
+#pragma unroll
+        for (int e = 0; e < kMine / 2; ++e) zero[e] = 0u;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c == warp) continue;
+          if constexpr (kMine == 32) tmem_st_32x32b_x16(colS + 16 * c, zero);
+          else tmem_st_32x32b_x8(colS + 8 * c, zero);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        uint32_t pk[kChunk / 2];
+#pragma unroll
+        for (int e = 0; e < kChunk / 2; ++e) {
+          const int i = kChunk * c + 2 * e;
+          const float2 xs = __ffma2_rn(make_float2(x[i], x[i + 1]), scale2, neg_m2);
+          const float2 pp = make_float2(ex2_approx(xs.x), ex2_approx(xs.y));
+          ls[e & 1] = __fadd2_rn(ls[e & 1], pp);
+          pk[e] = pack_bf16x2(pp.x, pp.y);
+        }
+        if constexpr (kChunk == 32) tmem_st_32x32b_x16(colS + col0 / 2 + 16 * c, pk);
+        else tmem_st_32x32b_x8(colS + col0 / 2 + 8 * c, pk);
+      }
+      const float lsum = (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+      // a raised maximum rescales the row's O once P.V of the tile before has
+      // written it (none before the segment's first tile)
+      if (j > 0 && __any_sync(0xffffffffu, corr != 1.0f)) {
+        if (!(ok = mbar_wait(&sm.pv_done, (t - 1) & 1u, abort))) break;
+        tc_fence_after_sync();
+#pragma unroll 1
+        for (int c = 0; c < DH / 16; ++c) {
+          uint32_t o[16];
+          tmem_ld_32x32b_x16(colO + 16 * c, o);
+          tmem_ld_wait(o);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+          tmem_st_32x32b_x16(colO + 16 * c, o);
+        }
+      }
+      l_run = l_run * corr + lsum;
+      m_run = m_use;
+      if (partial) {
+        // zero the V rows outside [clo, chi): never loaded, or stale.  (A row's
+        // 128 bytes per box are swizzled among themselves.)
+        if (!(ok = mbar_wait(&sm.full[r.slot], r.par, abort))) break;
+        const uint32_t vbase = smem_u32(sm.slot[r.slot]);
+        const int out_rows = clo + Cfg::kKeys - chi;
+        for (int i = tid; i < out_rows * Cfg::kBoxes * 8; i += 32 * active_warps) {
+          const int c16 = i % 8, bx = (i / 8) % Cfg::kBoxes, k = i / (8 * Cfg::kBoxes);
+          const int row = k < clo ? k : chi + (k - clo);
+          st_shared_v4(vbase + bx * Cfg::kKvBox + row * 128 + c16 * 16, 0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+      }
+      tmem_st_wait();
+      tc_fence_before_sync();
+      mbar_arrive(&sm.p_full[t & 1u]);
+      r.step();   // past V
+    }
+    // (o_final, not pv_done: two P.V may still be running here, and the parity of
+    // a barrier tells only one phase from the next)
+    if (!ok || !(ok = mbar_wait(&sm.o_final, nseg++ & 1u, abort))) break;
+    tc_fence_after_sync();
+    const int part_rows = REP == 4 ? p.G : 128;
+    const size_t ps = ((size_t)(s.unit + blockIdx.x) * REP + copy) * part_rows + head;
+    float* dst = p.o_part + ps * DH;
+#pragma unroll 1
+    for (int c = 0; c < DH / 32; ++c) {
+      uint32_t o[32];
+      tmem_ld_32x32b_x32(colO + 32 * c, o);
+      tmem_ld_wait(o);
+      if (real) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t w8[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w8[i] = o[8 * e + i];
+          st_global_v8(dst + 32 * c + 8 * e, w8);
+        }
+      }
+    }
+    if (real) {
+      p.m_part[ps] = m_run;
+      p.l_part[ps] = l_run;
+    }
+    tc_fence_before_sync();   // (the next segment's P.V overwrites O after p_full)
+  }
+}
+
+template <int DH, int REP>
+__global__ void __launch_bounds__(192, 1)
+    attn_decode_paged_sm103a(const __grid_constant__ CUtensorMap map_q,
+                             const __grid_constant__ CUtensorMap map_k,
+                             const __grid_constant__ CUtensorMap map_v,
+                             const DecodePagedParams p) {
+  using Cfg = DecodePagedCfg<DH>;
+  using Smem = DecodePagedSmem<DH>;
+  extern __shared__ uint8_t smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                      ~uintptr_t(1023));
+  volatile int* abort = &sm.abort_flag;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int active_warps = REP == 4 ? 4 : (min(128, p.G) + 31) / 32;
+  if (threadIdx.x == 0) {
+    sm.abort_flag = 0;
+    for (int i = 0; i < Cfg::kSlots; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], 32 * active_warps);
+    }
+    mbar_init(&sm.pv_done, 1);
+    mbar_init(&sm.o_final, 1);
+    mbar_init(&sm.qt_free, 1);
+    mbar_init(&sm.mma_done, 1);
+    fence_mbarrier_init();
+  }
+  if (warp == Cfg::kWarpIssuer) {
+    tmem_alloc(&sm.tmem_base, Cfg::kCols);
+    tmem_relinquish();
+  }
+  if (warp == Cfg::kWarpProducer && lane == 0) {
+    prefetch_tensormap(&map_q);
+    prefetch_tensormap(&map_k);
+    prefetch_tensormap(&map_v);
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tbase = sm.tmem_base;
+  // the lengths, the table and the cache may come from the previous kernel
+  griddep_wait();
+  PagedWalk<Cfg::kKeys> walk;
+  walk.init(p, blockIdx.x);
+  if (warp == Cfg::kWarpProducer)
+    decode_paged_producer<DH, REP>(sm, p, &map_q, &map_k, &map_v, walk, lane, abort);
+  else if (warp == Cfg::kWarpIssuer)
+    decode_paged_issuer<DH>(sm, p, tbase, walk, abort);
+  else if (warp < active_warps)
+    decode_paged_softmax<DH, REP>(sm, p, tbase, walk, warp, lane, active_warps, abort);
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == Cfg::kWarpIssuer) {
+    tc_fence_after_sync();
+    tmem_dealloc(tbase, Cfg::kCols);
+  }
+  if (threadIdx.x == 0 && sm.abort_flag) atomicExch(p.error_word, 4);   // ATTN_ERR_TIMEOUT
+  if (threadIdx.x == 0) griddep_launch_dependents();
+}
+
+// Joins a unit's partial results, in the order of its CTAs and copies:
+//   o = sum_i 2^(m_i - M) o_i / l,  l = sum_i 2^(m_i - M) l_i,  M = max m_i.
+// Blocks [0, B * Hq) each write one query head's output.  The blocks after
+// them, launched when weights are asked for, each write kPagedWeightKeys of
+// the weights of one (sequence, K/V head): sum over the group's heads of
+// 2^(s - M) / l, from the scores that the first kernel left.
+constexpr int kPagedJoinThreads = 128;
+constexpr int kPagedWeightKeys = 4 * kPagedJoinThreads;
+
+template <int DH, int REP>
+__global__ void __launch_bounds__(kPagedJoinThreads)
+    attn_decode_paged_join(const DecodePagedParams p) {
+  constexpr int KEYS = DecodePagedCfg<DH>::kKeys;
+  const int tid = threadIdx.x;
+  const int part_rows = REP == 4 ? p.G : 128;
+  griddep_wait();
+  if ((int)blockIdx.x < p.B * p.Hq) {
+    const int bh = blockIdx.x, b = bh / p.Hq, h = bh - b * p.Hq;
+    const int L = __ldcg(p.seqlens + b);
+    if (L < 1 || L > paged_rows(p)) {
+      // no keys: zero; a length that no sequence can have is an error
+      for (int d = tid; d < DH; d += kPagedJoinThreads)
+        p.o[(size_t)bh * DH + d] = __float2bfloat16(0.f);
+      if (L != 0 && tid == 0) atomicExch(p.error_word, 1);   // ATTN_ERR_INVALID_ARG
+      return;
+    }
+    const int g = h / p.G, hg = h - g * p.G, rb = hg / 128;
+    const int unit = (b * p.Hkv + g) * p.row_blocks + rb;
+    const int2 ctas = __ldcg(p.unit_ctas + unit);
+    const int n = (ctas.y - ctas.x + 1) * REP;
+    const size_t at0 = (size_t)(unit + ctas.x) * REP * part_rows + (hg - 128 * rb);
+    constexpr int kCols = DH > kPagedJoinThreads ? DH / kPagedJoinThreads : 1;
+    const bool mine = tid < DH;
+    constexpr int kG = 8;   // partials per round: their loads are all in flight together
+    float M = -INFINITY, l = 0.f, o[kCols];
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) o[c] = 0.f;
+    for (int i0 = 0; i0 < n; i0 += kG) {
+      float mv[kG], lv[kG], ov[kG][kCols];
+#pragma unroll
+      for (int e = 0; e < kG; ++e) {
+        const bool in = i0 + e < n;
+        const size_t at = at0 + (size_t)(i0 + e) * part_rows;
+        mv[e] = in ? __ldcg(p.m_part + at) : -INFINITY;
+        lv[e] = in ? __ldcg(p.l_part + at) : 0.f;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+          ov[e][c] = in && mine ? __ldcg(p.o_part + at * DH + tid + c * kPagedJoinThreads) : 0.f;
+      }
+      float Mg = M;
+#pragma unroll
+      for (int e = 0; e < kG; ++e) Mg = fmaxf(Mg, mv[e]);
+      const float f0 = (M == -INFINITY) ? 0.f : ex2_approx(M - Mg);
+      l *= f0;
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) o[c] *= f0;
+#pragma unroll
+      for (int e = 0; e < kG; ++e) {
+        const float f = (mv[e] == -INFINITY) ? 0.f : ex2_approx(mv[e] - Mg);
+        l = fmaf(f, lv[e], l);
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) o[c] = fmaf(f, ov[e][c], o[c]);
+      }
+      M = Mg;
+    }
+    if (mine)
+#pragma unroll
+      for (int c = 0; c < kCols; ++c)
+        p.o[(size_t)bh * DH + tid + c * kPagedJoinThreads] = __float2bfloat16(o[c] / l);
+    return;
+  }
+  // weights
+  const int T = paged_rows(p);
+  const int chunks = (T + kPagedWeightKeys - 1) / kPagedWeightKeys;
+  const int wi = blockIdx.x - p.B * p.Hq;
+  const int bg = wi / chunks, chunk = wi - bg * chunks;
+  const int b = bg / p.Hkv, g = bg - b * p.Hkv;
+  const PagedSeq seq = paged_seq<KEYS>(p, b);
+  const int k0 = chunk * kPagedWeightKeys;
+  if (k0 >= seq.L) return;
+  const bool any = k0 + kPagedWeightKeys > seq.lo;   // some key of the chunk is visible
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  if (any) {
+    // the heads' maxima and sums, 32 heads at a time (one warp per head)
+    __shared__ float sh_m[32], sh_f[32];
+    const int warp = tid / 32, lane = tid % 32;
+    for (int h0 = 0; h0 < p.G; h0 += 32) {
+      const int nh = min(32, p.G - h0);
+      __syncthreads();
+      for (int i = warp; i < nh; i += kPagedJoinThreads / 32) {
+        const int hg = h0 + i, rb = hg / 128;
+        const int unit = bg * p.row_blocks + rb;
+        const int2 ctas = __ldcg(p.unit_ctas + unit);
+        const int n = (ctas.y - ctas.x + 1) * REP;
+        const size_t at0 = (size_t)(unit + ctas.x) * REP * part_rows + (hg - 128 * rb);
+        float M = -INFINITY, l = 0.f;
+        for (int e = lane; e < n; e += 32)
+          M = fmaxf(M, __ldcg(p.m_part + at0 + (size_t)e * part_rows));
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+        for (int e = lane; e < n; e += 32) {
+          const float m = __ldcg(p.m_part + at0 + (size_t)e * part_rows);
+          l += (m == -INFINITY) ? 0.f
+                                : ex2_approx(m - M) * __ldcg(p.l_part + at0 + (size_t)e * part_rows);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
+        if (lane == 0) {
+          sh_m[i] = M;
+          sh_f[i] = 1.0f / l;
+        }
+      }
+      __syncthreads();
+      const float* src = p.scores + ((size_t)b * p.Hq + (size_t)g * p.G + h0) * p.score_stride +
+                         k0 + 4 * tid;
+      // (a score row is whole tiles long: the last keys of the chunk may lie past it)
+      if (k0 + 4 * tid < seq.L)
+        for (int i = 0; i < nh; ++i) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(src + (size_t)i * p.score_stride));
+          const float M = sh_m[i], f = sh_f[i];
+          acc[0] = fmaf(ex2_approx(fmaf(x.x, p.scale_log2, -M)), f, acc[0]);
+          acc[1] = fmaf(ex2_approx(fmaf(x.y, p.scale_log2, -M)), f, acc[1]);
+          acc[2] = fmaf(ex2_approx(fmaf(x.z, p.scale_log2, -M)), f, acc[2]);
+          acc[3] = fmaf(ex2_approx(fmaf(x.w, p.scale_log2, -M)), f, acc[3]);
+        }
+    }
+  }
+  float* out = p.weights + (size_t)bg * p.weights_stride;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = k0 + 4 * tid + i;
+    if (t >= seq.L) break;
+    const bool seen = t >= seq.lo;
+    if (p.accumulate) {
+      if (seen) out[t] += acc[i];
+    } else {
+      out[t] = seen ? acc[i] : 0.f;
+    }
+  }
+}
+
+template <int DH>
+constexpr size_t decode_paged_smem_bytes() {
+  return sizeof(DecodePagedSmem<DH>) + 1024;   // + alignment slack
+}
+
+}  // namespace chs

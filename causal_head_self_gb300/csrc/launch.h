@@ -114,4 +114,47 @@ cudaError_t launch_bwd(const void* q, const void* k, const void* v, const void* 
                        float* workspace, int B, int Hq, int Hkv, int S, int Dh, int causal,
                        int window, float scale, const DeviceInfo& dev, cudaStream_t stream);
 
+// ---------------------------------------------------------------- paged cache
+// K and V pools [num_pages, Hkv, page, Dh]; row t of sequence b in page
+// table[b, t / page] at row t % page (include/attn.h).
+struct PagedCache {
+  int num_pages, page, cols;   // cols: table columns
+};
+
+// Rows per TMA box: the largest that divides both a page and a key tile.
+int paged_box_rows(int page, int Dh);
+
+// Device memory that a paged decode call needs: partial results, and with
+// `scores` the raw score of every (query head, key).
+size_t decode_paged_workspace_bytes(int B, int Hq, int Hkv, const PagedCache& cache, int Dh,
+                                    bool scores, int num_sms);
+
+// One decode step over a paged cache; weights (optional, [B, Hkv,
+// weights_stride] fp32) receive each key's weight summed over its head group.
+cudaError_t launch_decode_paged(const void* q, const void* kpages, const void* vpages,
+                                const int* table, const int* seqlens, void* o, float* weights,
+                                int weights_stride, int accumulate, void* workspace, int B, int Hq,
+                                int Hkv, const PagedCache& cache, int Dh, int window,
+                                float scale_log2, const DeviceInfo& dev, cudaStream_t stream);
+
+// Rows of k, v [B, Hkv, S, Dh] to the cache; newlens null: all S rows.
+cudaError_t launch_paged_append(const void* k, const void* v, void* kpages, void* vpages,
+                                const int* table, const int* seqlens, const int* newlens, int B,
+                                int Hkv, int S, const PagedCache& cache, int Dh,
+                                const DeviceInfo& dev, cudaStream_t stream);
+
+// The weights that a prompt's keys received: [B, Hkv, stride] fp32.
+cudaError_t launch_key_weights(const void* q, const void* k, const float* lse, const int* seqlens,
+                               float* weights, int stride, int B, int Hq, int Hkv, int S, int Dh,
+                               int causal, int window, int queries, int accumulate,
+                               float scale_log2, const DeviceInfo& dev, cudaStream_t stream);
+
+// Keeps `budget` rows of each (sequence, K/V head); table_out == table: in place.
+cudaError_t launch_cache_evict(void* kpages, void* vpages, const int* table, const int* table_out,
+                               int cols_out, const int* seqlens, int* newlens,
+                               const float* weights, int stride, float* weights_out,
+                               int stride_out, int* keep, int B, int Hkv, const PagedCache& cache,
+                               int Dh, int budget, int recent, const DeviceInfo& dev,
+                               cudaStream_t stream);
+
 }  // namespace chs

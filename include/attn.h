@@ -51,6 +51,8 @@
 #ifndef CAUSAL_HEAD_SELF_ATTN_H_
 #define CAUSAL_HEAD_SELF_ATTN_H_
 
+#include <stddef.h>
+
 #include <cuda_runtime_api.h>
 
 #ifdef __cplusplus
@@ -243,6 +245,135 @@ int attn_decode_ring(const void* q, const void* kcache, const void* vcache, cons
 int attn_decode_noalloc(const void* q, const void* kcache, const void* vcache,
                         const int* seqlens, void* o, int B, int Hq, int Hkv, int Tmax, int Dh,
                         int window, float scale, cudaStream_t stream);
+
+/*
+ * The paged key-value cache.  A serving runtime that holds many sequences of
+ * different and growing lengths keeps their keys and values in pages of one
+ * pool instead of a [B, Hkv, Tmax, Dh] block per sequence:
+ *   kpages, vpages [num_pages, Hkv, page, Dh]  the pools (device, bf16)
+ *   table          [B, cols]  page numbers (device, int32): row t of sequence
+ *                  b is row t % page of page table[b * cols + t / page]
+ *   seqlens        [B]        keys held per sequence (device, int32)
+ * `page` is a multiple of 8 (ATTN_ERR_UNSUPPORTED otherwise).  A linear cache
+ * [B, Hkv, Tmax, Dh] is the special case of num_pages = B, page = Tmax,
+ * cols = 1, table = 0 .. B - 1.  In every call below:
+ *   - A length of 0 is a sequence without keys (an empty slot of a padded
+ *     batch): nothing of it is read or written but a zero output.  A length
+ *     outside [0, cols * page] latches ATTN_ERR_INVALID_ARG for attn_status().
+ *   - Only table entries of rows that the call uses are read; the others may
+ *     hold anything.  An entry outside [0, num_pages) that is used latches
+ *     ATTN_ERR_INVALID_ARG (nothing outside the pools is touched).  Sequences
+ *     may share pages that the call only reads; a page that it writes must
+ *     belong to one sequence and appear there once (the contents are
+ *     undefined otherwise).
+ *   - Rows outside a sequence's visible keys are never used, whatever they
+ *     hold (infinities and NaN included), and rows that the call does not
+ *     write keep their bits.
+ *   - The library keeps no workspace for these calls: they may run at the
+ *     same time on several streams and in several captured graphs, each with
+ *     its own workspace where one is asked for.
+ */
+
+/*
+ * attn_paged_append -- write new keys and values to the cache.
+ *   k, v     [B, Hkv, S, Dh]  new rows (device, bf16, read)
+ *   seqlens  [B]  keys held AFTER the append
+ *   newlens  [B]  rows of k and v that are real, the first newlens[b] of S
+ *                 (device, int32, or NULL: all S), 0 <= newlens[b] <=
+ *                 min(S, seqlens[b]); another value latches
+ *                 ATTN_ERR_INVALID_ARG and appends nothing to the sequence
+ * Row i becomes row seqlens[b] - newlens[b] + i of sequence b.  With S = 1 the
+ * call is a decode step's append (seqlens as attn_decode_paged takes them).
+ * With NULL a length below S latches the error too, except 0 (an empty slot).
+ */
+int attn_paged_append(const void* k, const void* v, void* kpages, void* vpages, const int* table,
+                      const int* seqlens, const int* newlens, int B, int Hkv, int S, int num_pages,
+                      int page, int cols, int Dh, cudaStream_t stream);
+
+/*
+ * attn_decode_paged -- attn_decode over a paged cache: one query per sequence,
+ * at position seqlens[b] - 1, against keys [max(0, seqlens[b] - window),
+ * seqlens[b]) (all of them when window <= 0).
+ *   q, o     [B, Hq, 1, Dh]  queries, output (device, bf16; o is all zero
+ *                            for a length of 0)
+ *   weights  [B, Hkv, weights_stride] (device, fp32) or NULL: the softmax
+ *            weight of each key, summed over the query heads of its K/V head,
+ *            is added to weights[b, g, t] (accumulate = 1) or stored there
+ *            (accumulate = 0, which also stores 0 for keys before the
+ *            window), for t < seqlens[b]; entries from seqlens[b] on are left
+ *            as they are.  weights_stride >= cols * page.
+ *   workspace  device, 256-byte aligned, of at least the bytes that
+ *            attn_decode_paged_workspace gives for the same shapes
+ *            (ATTN_ERR_SCRATCH_LIMIT otherwise).  Its contents need not be
+ *            kept between calls; calls that may overlap on the GPU need one
+ *            each.
+ * Any Hq / Hkv runs on the tensor cores.  The same inputs give the same bits.
+ */
+int attn_decode_paged(const void* q, const void* kpages, const void* vpages, const int* table,
+                      const int* seqlens, void* o, float* weights, int weights_stride,
+                      int accumulate, void* workspace, size_t workspace_bytes, int B, int Hq,
+                      int Hkv, int num_pages, int page, int cols, int Dh, int window, float scale,
+                      cudaStream_t stream);
+
+/* The workspace of an attn_decode_paged call on the current device, in bytes:
+ * partial results, and with weights the step's scores (4 bytes for each query
+ * head and row that the table has room for). */
+int attn_decode_paged_workspace(int B, int Hq, int Hkv, int page, int cols, int Dh,
+                                int with_weights, size_t* bytes);
+
+/*
+ * attn_key_weights -- the attention weight that the keys of a prompt received:
+ *   weights[b, g, j] (+)= sum over query heads h of K/V head g and voting
+ *                         queries i that see key j of exp(s_hij - lse[b, h, i])
+ * with s the scaled scores of attn_fwd_lse and lse its log-sum-exps, so that
+ * each term is a softmax weight.  Nothing of size S x S is stored.
+ *   q, k     [B, Hq | Hkv, S, Dh]   as attn_fwd_lse took them (device, bf16)
+ *   lse      [B, Hq, S]             (device, fp32); only voting rows are read
+ *   seqlens  [B] or NULL            real rows of a padded prompt, in [0, S]
+ *                                   (device, int32; NULL: all S)
+ *   weights  [B, Hkv, weights_stride]  (device, fp32), weights_stride >= S;
+ *            entries [0, seqlens[b]) are written, the others left alone
+ *   queries  the last `queries` rows of each sequence vote (0 or more than
+ *            there are: every row)
+ *   causal, window, scale  as in attn_fwd_lse;  accumulate as above
+ * (With causal = 0 a padded prompt's lse has to be that of its real rows.)
+ */
+int attn_key_weights(const void* q, const void* k, const float* lse, const int* seqlens,
+                     float* weights, int weights_stride, int B, int Hq, int Hkv, int S, int Dh,
+                     int queries, int causal, int window, int accumulate, float scale,
+                     cudaStream_t stream);
+
+/*
+ * attn_cache_evict -- shrink each sequence of a paged cache to at most
+ * `budget` keys.  A sequence of n > budget keys keeps, for each K/V head on
+ * its own, the last `recent` rows and, of the rows before them, the
+ * budget - recent with the largest weights (equal weights: the lower row; NaN
+ * counts below every number).  The kept rows keep their order and become rows
+ * 0 .. budget - 1; keys were rotated by position before they were cached, if
+ * at all, so attention does not see the move.  Shorter sequences keep all.
+ *   weights      [B, Hkv, weights_stride]  accumulated weights (device, fp32);
+ *                weights_stride >= cols * page
+ *   seqlens      [B]  read
+ *   table_out    [B, cols_out]  pages that receive the kept rows; they must not
+ *                be among the pages in use by the sequences' rows.  NULL (or
+ *                table itself): in place.
+ *   weights_out  [B, Hkv, weights_out_stride]  receives the kept rows' weights,
+ *                and zeros in entries [newlens[b], seqlens[b]), so that rows
+ *                appended later start from nothing.  NULL (or weights itself):
+ *                in place.
+ *   newlens      [B]  written: min(seqlens[b], budget).  Not seqlens itself.
+ *   keep         [B, Hkv, budget]  written: the former row of each kept row,
+ *                ascending, then -1
+ * budget >= 1, 0 <= recent <= budget, and cols_out * page and
+ * weights_out_stride hold min(budget, cols * page) rows
+ * (ATTN_ERR_INVALID_ARG otherwise).  A length outside its range leaves the
+ * sequence alone.
+ */
+int attn_cache_evict(void* kpages, void* vpages, float* weights, int weights_stride,
+                     const int* table, const int* seqlens, int budget, int recent,
+                     const int* table_out, int cols_out, float* weights_out,
+                     int weights_out_stride, int* newlens, int* keep, int B, int Hkv, int num_pages,
+                     int page, int cols, int Dh, cudaStream_t stream);
 
 /*
  * attn_status -- synchronise `stream`, then return (and clear) the current
