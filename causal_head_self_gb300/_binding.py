@@ -7,7 +7,6 @@ implementation to fall back to.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import os
@@ -341,41 +340,57 @@ def _this_device() -> int:
 
 def _check(name, t, dtype, shape, device):
     """A contiguous tensor of that type and shape, on the same GPU as the others."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == device >= 0 and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA {dtype} tensor")
-    if tuple(t.shape) != shape or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {list(shape)} tensor, got {list(t.shape)}")
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be on the same device as the other tensors")
+    raise ValueError(f"{name} must be on the same device as the other tensors")
+
+
+def _check_current(device):
+    """The library launches on the current device (a stream belongs to one)."""
+    if device != _this_device():
+        raise ValueError("the tensors must be on the current device (torch.cuda.device)")
+
+
+def _shape(name, t, ndim):
+    """The shape of a tensor of ndim axes."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} axes")
+    return t.shape
 
 
 def _check_pools(kpages, vpages, table, seqlens):
     """The checks that every paged call makes: (B, Hkv, num_pages, page, cols, Dh, device)."""
-    _check_bf16("kpages", kpages, 4)
-    P, Hkv, page, Dh = kpages.shape
+    P, Hkv, page, Dh = shape = _shape("kpages", kpages, 4)
+    B, cols = table_shape = _shape("table", table, 2)
     device = kpages.get_device()
-    if device != _this_device():
-        raise ValueError("the tensors must be on the current device (torch.cuda.device)")
-    _check("vpages", vpages, torch.bfloat16, (P, Hkv, page, Dh), device)
-    if not isinstance(table, torch.Tensor) or table.dim() != 2:
-        raise ValueError("table must be a [B, cols] tensor")
-    B, cols = table.shape
-    _check("table", table, torch.int32, (B, cols), device)
+    _check("kpages", kpages, torch.bfloat16, shape, device)
+    _check_current(device)
+    _check("vpages", vpages, torch.bfloat16, shape, device)
+    _check("table", table, torch.int32, table_shape, device)
     _check("seqlens", seqlens, torch.int32, (B,), device)
     return B, Hkv, P, page, cols, Dh, device
 
 
-def _rows_of(name, t, lead, device):
-    """A contiguous float32 [*lead, stride] tensor: its stride."""
-    if not isinstance(t, torch.Tensor) or t.dim() != len(lead) + 1:
-        raise ValueError(f"{name} must be a float32 [B, Hkv, rows] tensor")
-    _check(name, t, torch.float32, (*lead, t.shape[-1]), device)
-    return t.shape[-1]
+def _rows_of(name, t, B, Hkv, device):
+    """A contiguous float32 [B, Hkv, stride] tensor: its stride."""
+    stride = _shape(name, t, 3)[2]
+    _check(name, t, torch.float32, (B, Hkv, stride), device)
+    return stride
 
 
-def _on(stream):
-    """Allocations of a call belong to the stream that it runs on."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _empty(shape, dtype, device, stream):
+    """A tensor whose memory belongs to the stream that the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def attn_paged_append(k, v, kpages, vpages, table, seqlens, newlens=None, *, stream=None):
@@ -384,8 +399,7 @@ def attn_paged_append(k, v, kpages, vpages, table, seqlens, newlens=None, *, str
     after the append, newlens [B] int32 = real rows of k and v (None: all S).
     Returns (kpages, vpages), which are written in place."""
     B, Hkv, P, page, cols, Dh, device = _check_pools(kpages, vpages, table, seqlens)
-    _check_bf16("k", k, 4)
-    S = k.shape[2]
+    S = _shape("k", k, 4)[2]
     _check("k", k, torch.bfloat16, (B, Hkv, S, Dh), device)
     _check("v", v, torch.bfloat16, (B, Hkv, S, Dh), device)
     if newlens is not None:
@@ -426,10 +440,9 @@ def attn_decode_paged(q, kpages, vpages, table, seqlens, o=None, *, window=0, sc
     place.  workspace: a uint8 tensor of attn_decode_paged_workspace() bytes
     (None: allocated here by torch, on the call's stream).  Returns o."""
     B, Hkv, P, page, cols, Dh, device = _check_pools(kpages, vpages, table, seqlens)
-    _check_bf16("q", q, 4)
-    Hq = q.shape[1]
+    Hq = _shape("q", q, 4)[1]
     _check("q", q, torch.bfloat16, (B, Hq, 1, Dh), device)
-    stride = 0 if weights is None else _rows_of("weights", weights, (B, Hkv), device)
+    stride = 0 if weights is None else _rows_of("weights", weights, B, Hkv, device)
     need = _decode_paged_workspace(device, B, Hq, Hkv, page, cols, Dh, weights is not None)
     if o is not None:
         _check("o", o, torch.bfloat16, (B, Hq, 1, Dh), device)
@@ -438,12 +451,10 @@ def attn_decode_paged(q, kpages, vpages, table, seqlens, o=None, *, window=0, sc
                                   or workspace.get_device() != device
                                   or not workspace.is_contiguous()):
         raise TypeError("workspace must be a contiguous CUDA uint8 tensor on the same device")
-    if o is None or workspace is None:
-        with _on(stream):
-            if o is None:
-                o = torch.empty_like(q)
-            if workspace is None:
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if o is None:
+        o = _empty((B, Hq, 1, Dh), torch.bfloat16, q.device, stream)
+    if workspace is None:
+        workspace = _empty((need,), torch.uint8, q.device, stream)
     rc = load().attn_decode_paged(q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(),
                                   table.data_ptr(), seqlens.data_ptr(), o.data_ptr(),
                                   None if weights is None else weights.data_ptr(), stride,
@@ -463,16 +474,14 @@ def attn_key_weights(q, k, lse, weights, seqlens=None, *, queries=0, causal=True
     accumulate=False.  q [B,Hq,S,Dh], k [B,Hkv,S,Dh] and lse [B,Hq,S] as
     attn_fwd_lse took and returned them; seqlens [B] int32: the real rows of a
     padded prompt.  Returns weights."""
-    _check_bf16("q", q, 4)
-    _check_bf16("k", k, 4)
-    B, Hq, S, Dh = q.shape
-    Hkv = k.shape[1]
+    B, Hq, S, Dh = shape = _shape("q", q, 4)
+    Hkv = _shape("k", k, 4)[1]
     device = q.get_device()
-    if device != _this_device():
-        raise ValueError("the tensors must be on the current device (torch.cuda.device)")
+    _check("q", q, torch.bfloat16, shape, device)
+    _check_current(device)
     _check("k", k, torch.bfloat16, (B, Hkv, S, Dh), device)
     _check("lse", lse, torch.float32, (B, Hq, S), device)
-    stride = _rows_of("weights", weights, (B, Hkv), device)
+    stride = _rows_of("weights", weights, B, Hkv, device)
     if seqlens is not None:
         _check("seqlens", seqlens, torch.int32, (B,), device)
     rc = load().attn_key_weights(q.data_ptr(), k.data_ptr(), lse.data_ptr(),
@@ -494,28 +503,24 @@ def attn_cache_evict(kpages, vpages, weights, table, seqlens, budget, recent=0, 
     weights_out (None: in place).  Returns (newlens [B], keep [B,Hkv,budget]):
     the new lengths, and each kept row's former number (then -1)."""
     B, Hkv, P, page, cols, Dh, device = _check_pools(kpages, vpages, table, seqlens)
-    stride = _rows_of("weights", weights, (B, Hkv), device)
+    stride = _rows_of("weights", weights, B, Hkv, device)
     budget, recent = int(budget), int(recent)
     cols_out, stride_out = cols, stride
     if table_out is not None:
-        if not isinstance(table_out, torch.Tensor) or table_out.dim() != 2:
-            raise ValueError("table_out must be a [B, cols] tensor")
-        cols_out = table_out.shape[1]
+        cols_out = _shape("table_out", table_out, 2)[1]
         _check("table_out", table_out, torch.int32, (B, cols_out), device)
     if weights_out is not None:
-        stride_out = _rows_of("weights_out", weights_out, (B, Hkv), device)
+        stride_out = _rows_of("weights_out", weights_out, B, Hkv, device)
     if budget < 1:
         raise AttnError(ATTN_ERR_INVALID_ARG, "attn_cache_evict")
     if newlens is not None:
         _check("newlens", newlens, torch.int32, (B,), device)
     if keep is not None:
         _check("keep", keep, torch.int32, (B, Hkv, budget), device)
-    if newlens is None or keep is None:
-        with _on(stream):
-            if newlens is None:
-                newlens = torch.empty_like(seqlens)
-            if keep is None:
-                keep = torch.empty((B, Hkv, budget), dtype=torch.int32, device=seqlens.device)
+    if newlens is None:
+        newlens = _empty((B,), torch.int32, seqlens.device, stream)
+    if keep is None:
+        keep = _empty((B, Hkv, budget), torch.int32, seqlens.device, stream)
     rc = load().attn_cache_evict(kpages.data_ptr(), vpages.data_ptr(), weights.data_ptr(), stride,
                                  table.data_ptr(), seqlens.data_ptr(), budget, recent,
                                  None if table_out is None else table_out.data_ptr(), cols_out,

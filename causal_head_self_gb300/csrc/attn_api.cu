@@ -505,7 +505,7 @@ int paged_check(int B, int Hkv, const chs::PagedCache& c, int Dh) {
   if (Dh != 64 && Dh != 128 && Dh != 256) return ATTN_ERR_UNSUPPORTED;
   if (c.page % 8 != 0) return ATTN_ERR_UNSUPPORTED;
   // positions, and a pool's (page, head) pairs, are 32-bit
-  if ((long long)c.cols * c.page > 0x7fffffffLL - 1024) return ATTN_ERR_INVALID_ARG;
+  if ((long long)c.cols * c.page > 0x7fffffffLL - 16384) return ATTN_ERR_INVALID_ARG;
   if ((long long)c.num_pages * Hkv > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
 }
@@ -682,7 +682,7 @@ extern "C" int attn_cache_evict(void* kpages, void* vpages, float* weights, int 
   const long long rows = (long long)cols * page;
   const long long most = budget < rows ? budget : rows;   // rows that a sequence may end with
   if (weights_stride < rows || weights_out_stride < most || cols_out < 1 ||
-      (long long)cols_out * page > 0x7fffffffLL - 1024 || (long long)cols_out * page < most)
+      (long long)cols_out * page > 0x7fffffffLL - 16384 || (long long)cols_out * page < most)
     return ATTN_ERR_INVALID_ARG;
   if (table_out == table && cols_out != cols) return ATTN_ERR_INVALID_ARG;
   if (weights_out == weights && weights_out_stride != weights_stride) return ATTN_ERR_INVALID_ARG;

@@ -18,13 +18,13 @@
 // share a number), which is its place in the partial results.  A second kernel
 // joins the segments of each unit.
 //
-// Pipeline.  One warp loads (TMA), one issues the tensor-core work, four run
-// the softmax.  Q, K and V tiles pass through one ring of equal slots in the
-// order Q, K0, V0, K1, V1, ... of each segment, and the loading warp runs ahead
-// into the next segments.  Q moves on to tensor memory at once (tcgen05.cp), so
-// its slot is soon free again.  A page holds `page` rows of one head in a row,
+// Pipeline.  Four warps load (TMA), one issues the tensor-core work, four run
+// the softmax.  Q and K tiles pass through one ring of slots (Q, K0, K1, ... of
+// each segment), V tiles through another, and the loading warps run ahead into
+// the next segments.  Q moves on to tensor memory at once (tcgen05.cp), so its
+// slot is soon free again.  A page holds `page` rows of one head in a row,
 // so a tile is gathered in boxes of box_rows = gcd(page, kKeys) rows, each of
-// them in one page; the lanes of the loading warp each take one box.
+// them in one page.
 //
 // Softmax.  A warp reaches only its own 32 lanes (rows) of tensor memory.  A
 // group of up to 32 query heads is therefore copied four times into the 128
@@ -40,6 +40,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -79,8 +80,10 @@ struct DecodePagedCfg {
   static constexpr int kSlot = kBoxes * kKvBox;        // ring slot: one K or V tile
   static constexpr int kQSlots = kBoxes * kQBox / kSlot;   // slots that Q takes: 1, at Dh 256 2
   static constexpr int kSlots = 224 * 1024 / kSlot;    // 14 (Dh 64) or 7
-  static constexpr int kThreads = 192;                 // warps 0-3 softmax, 4 loads, 5 MMA
-  static constexpr int kWarpProducer = 4, kWarpIssuer = 5;
+  static constexpr int kSlotsV = kSlots / 2, kSlotsK = kSlots - kSlotsV;
+  // warps 0-3 softmax, 4 MMA, 5-8 loads
+  static constexpr int kThreads = 288;
+  static constexpr int kWarpIssuer = 4, kWarpProducer = 5;
   // tensor memory: S0, S1 | Q | O
   static constexpr uint32_t kColQ = DH == 256 ? 128 : 384, kColO = 256, kCols = 512;
   static_assert(2 * kKeys <= 256 && kColO + DH <= (DH == 256 ? 512u : kColQ), "tensor memory");
@@ -198,18 +201,24 @@ struct PagedWalk {
   }
 };
 
-// A place in the ring: slot and the parity of its current use.
-template <int SLOTS>
+// A place in a ring of slots [FIRST, FIRST + N): slot and parity of its current
+// use.  Whoever waits on a ring's barriers passes every use of every slot in
+// turn, so that it is never more than one phase off and the parity is enough.
+template <int FIRST, int N>
 struct PagedRing {
-  int slot = 0;
+  int slot = FIRST;
   uint32_t par = 0;
   __device__ __forceinline__ void step() {
-    if (++slot == SLOTS) {
-      slot = 0;
+    if (++slot == FIRST + N) {
+      slot = FIRST;
       par ^= 1u;
     }
   }
 };
+template <int DH>
+using PagedRingK = PagedRing<0, DecodePagedCfg<DH>::kSlotsK>;
+template <int DH>
+using PagedRingV = PagedRing<DecodePagedCfg<DH>::kSlotsK, DecodePagedCfg<DH>::kSlotsV>;
 
 __device__ __forceinline__ void mbar_wait_drain_paged(uint64_t* bar, uint32_t parity) {
   const uint32_t a = smem_u32(bar);
@@ -219,25 +228,31 @@ __device__ __forceinline__ void mbar_wait_drain_paged(uint64_t* bar, uint32_t pa
   }
 }
 
-// Loading warp.  Lane l takes box l % boxes of rows and 64-column block
-// l / boxes of every K and V tile (at most 32 boxes per tile: 128 rows / 8 x 2,
-// 64 rows / 8 x 4); the table entry of its box is fetched a tile ahead.
-template <int DH, int REP>
+// Loading warps: two load Q and K, two V, each (`part`) every other box (64 columns of box_rows rows; at most 32 per tile: 128 rows / 8 x 2, 64
+// rows / 8 x 4), one lane per box.  A warp takes about 90 cycles to issue one
+// copy, so at a page of 16 rows one warp alone is slower than the memory:
+// B = 8, 32 heads of 64, 4096 keys ran at 4470 GB/s with one loading warp
+// (page 8: 3041).
+template <int DH, int REP, bool V>
 __device__ __forceinline__ void decode_paged_producer(DecodePagedSmem<DH>& sm,
                                                       const DecodePagedParams& p,
                                                       const CUtensorMap* map_q,
-                                                      const CUtensorMap* map_k,
-                                                      const CUtensorMap* map_v,
+                                                      const CUtensorMap* map_kv,
                                                       PagedWalk<DecodePagedCfg<DH>::kKeys> walk,
-                                                      int lane, volatile int* abort) {
+                                                      int part, int lane, volatile int* abort) {
   using Cfg = DecodePagedCfg<DH>;
   const uint64_t once = policy_evict_first();   // each cached row is read by one CTA
   const int boxes = Cfg::kKeys / p.box_rows;
-  const int box = lane % boxes, half = lane / boxes;
+  const int mine = 2 * lane + part;   // of the tile's boxes
+  const int box = mine % boxes, half = mine / boxes;
   const bool has_box = half < Cfg::kBoxes;
   const int box_bytes = p.box_rows * 128;
+  // tiles per group (below), and the table columns and rows of one
+  const int group = 32 / boxes;
+  const int cols_per_group = group * Cfg::kKeys / p.page;
+  const int rows_per_group = group * Cfg::kKeys % p.page;
   const uint32_t dst_off = (uint32_t)(half * Cfg::kKvBox + box * box_bytes);
-  PagedRing<Cfg::kSlots> r;
+  std::conditional_t<V, PagedRingV<DH>, PagedRingK<DH>> r;
   uint32_t loaded = 0, pars = 0;
   bool ok = true, first = true;
   auto wait_slot = [&]() -> bool {
@@ -251,59 +266,79 @@ __device__ __forceinline__ void decode_paged_producer(DecodePagedSmem<DH>& sm,
   PagedSegment s;
   while (ok && walk.next(p, s)) {
     const int g = s.gi / p.row_blocks, rb = s.gi - g * p.row_blocks;
-    if (lane == 0 && s.starts) p.unit_ctas[s.unit] = make_int2(blockIdx.x, s.last_cta);
+    if (!V && part == 0 && lane == 0 && s.starts) p.unit_ctas[s.unit] = make_int2(blockIdx.x, s.last_cta);
     const int* row = p.table + (size_t)s.b * p.cols;
-    // this lane's box of a tile: the page that holds it (-1: no visible row)
-    auto page_of = [&](int tile) -> int {
-      const int pos = tile * Cfg::kKeys + box * p.box_rows;
-      if (!has_box || pos >= s.L || pos + p.box_rows <= s.lo) return -1;
-      const int id = __ldcg(row + pos / p.page);
-      if (id >= 0 && id < p.num_pages) return id;
-      atomicExch(p.error_word, 1);   // ATTN_ERR_INVALID_ARG: no such page
-      return 0;
-    };
-    int id = page_of(s.tile0);
+    // The table is read for `group` tiles at a time, a group ahead: lane l holds
+    // the entry of box l % boxes of the group's tile l / boxes.  (Under load an
+    // entry takes longer to arrive than a tile takes to load.)
+    int pos = (s.tile0 + lane / boxes) * Cfg::kKeys + (lane % boxes) * p.box_rows;
+    int col = pos / p.page, c1 = pos - col * p.page;
+    const int end = min(s.L, (s.tile0 + s.count) * Cfg::kKeys);
+    auto in_use = [&] { return pos < end && pos + p.box_rows > s.lo; };
+    bool group_use = in_use();
+    int group_c1 = c1, group_id = group_use ? __ldcg(row + col) : 0;
+    bool next_use = false;
+    int next_c1 = 0, next_id = 0;
     // Q: REP copies of the group's rows
-    constexpr int kPerBox = REP, kRows = 128 / REP;
-    for (int e = 0; ok && e < Cfg::kQSlots; ++e) {
+    constexpr int kRows = 128 / REP, kBoxesPerSlot = Cfg::kBoxes / Cfg::kQSlots;
+    constexpr int kCopies = kBoxesPerSlot * REP;   // per slot, shared by two warps
+    for (int e = 0; !V && ok && e < Cfg::kQSlots; ++e) {
       if (!(ok = wait_slot())) break;
-      constexpr int kBoxesPerSlot = Cfg::kBoxes / Cfg::kQSlots;
-      if (lane == 0) mbar_arrive_expect_tx(&sm.full[r.slot], kBoxesPerSlot * Cfg::kQBox);
+      if (lane == 0)
+        mbar_arrive_expect_tx(&sm.full[r.slot], (kCopies + 1 - part) / 2 * (Cfg::kQBox / REP));
       __syncwarp();
-      if (lane < kBoxesPerSlot * kPerBox) {
-        const int bx = lane / kPerBox, copy = lane % kPerBox;
+      if (mine < kCopies) {
+        const int bx = mine / REP, copy = mine % REP;
         tma_load_3d(sm.slot[r.slot] + bx * Cfg::kQBox + copy * kRows * 128, map_q,
                     &sm.full[r.slot], (e * kBoxesPerSlot + bx) * 64, 128 * rb, s.b * p.Hkv + g);
       }
       mark_slot();
     }
     for (int j = 0; ok && j < s.count; ++j) {
-      const int tile = s.tile0 + j, pos0 = tile * Cfg::kKeys;
-      const int my = id;
-      const int pos = pos0 + box * p.box_rows;
-      const int c1 = pos % p.page, c2 = my * p.Hkv + g;
-      // (checked builds: a box lies inside one page of the pool)
-      const bool load = my >= 0 && attn_check(my < p.num_pages && c1 >= 0 &&
-                                                  c1 + p.box_rows <= p.page && g < p.Hkv,
-                                              p.error_word);
-      const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, load)) * box_bytes);
-      if (j + 1 < s.count) id = page_of(tile + 1);
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        if (!(ok = wait_slot())) break;
-        if (kv == 0 && first && p.fault == 3) {   // (the test hook withholds one tile)
-          first = false;
-          r.step();
-          continue;
+      const int in_group = j & (group - 1);   // (group is a power of two)
+      if (in_group == 0) {
+        if (j > 0) {
+          group_use = next_use;
+          group_c1 = next_c1;
+          group_id = next_id;
         }
-        first = false;
+        pos += group * Cfg::kKeys;
+        col += cols_per_group;
+        c1 += rows_per_group;
+        if (c1 >= p.page) {
+          c1 -= p.page;
+          ++col;
+        }
+        next_use = in_use();
+        next_c1 = c1;
+        next_id = next_use ? __ldcg(row + col) : 0;
+      }
+      const int from = in_group * boxes + box;
+      bool load = __shfl_sync(0xffffffffu, (int)group_use, from) != 0 && has_box;
+      int id = __shfl_sync(0xffffffffu, group_id, from);
+      const int row_in_page = __shfl_sync(0xffffffffu, group_c1, from);
+      if (load && (id < 0 || id >= p.num_pages)) {
+        atomicExch(p.error_word, 1);   // ATTN_ERR_INVALID_ARG: no such page
+        id = 0;
+      }
+      const int c2 = id * p.Hkv + g;
+      // (checked builds: a box lies inside one page of the pool)
+      load = load && attn_check(id < p.num_pages && row_in_page >= 0 &&
+                                    row_in_page + p.box_rows <= p.page && g < p.Hkv,
+                                p.error_word);
+      const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, load)) * box_bytes);
+      if (!(ok = wait_slot())) break;
+      if (!V && first && p.fault == 3) {   // (the test hook withholds one tile)
+        r.step();
+      } else {
         if (lane == 0) mbar_arrive_expect_tx(&sm.full[r.slot], bytes);
         __syncwarp();
         if (load)
-          tma_load_3d_hint(sm.slot[r.slot] + dst_off, kv ? map_v : map_k, &sm.full[r.slot],
-                           half * 64, c1, c2, once);
+          tma_load_3d_hint(sm.slot[r.slot] + dst_off, map_kv, &sm.full[r.slot], half * 64,
+                           row_in_page, c2, once);
         mark_slot();
       }
+      first = false;
     }
   }
   // every copy this warp started has landed before the CTA may exit
@@ -329,14 +364,13 @@ __device__ __forceinline__ void decode_paged_issuer(DecodePagedSmem<DH>& sm,
   auto wait = [&](uint64_t* bar, uint32_t par) -> bool {
     return __all_sync(0xffffffffu, mbar_wait(bar, par, abort));
   };
-  PagedRing<Cfg::kSlots> rk, rv;   // next K and next V entry of the ring
+  PagedRingK<DH> rk;               // next Q or K
+  PagedRingV<DH> rv;               // next V
   uint32_t t = 0;                  // tiles so far, over all segments
   uint32_t nseg = 0;
   bool ok = true;
   PagedSegment s;
   while (ok && walk.next(p, s)) {
-    // the ring holds Q, K0, V0, K1, V1, ...; rv stands at the segment's first entry
-    rk = rv;
     if (nseg > 0 && !(ok = wait(&sm.qt_free, (nseg - 1) & 1u))) break;
     for (int e = 0; ok && e < Cfg::kQSlots; ++e, rk.step()) {
       if (!(ok = wait(&sm.full[rk.slot], rk.par))) break;
@@ -351,8 +385,6 @@ __device__ __forceinline__ void decode_paged_issuer(DecodePagedSmem<DH>& sm,
     }
     if (!ok) break;
     ++nseg;
-    rv = rk;
-    rv.step();
     auto issue_s = [&](uint32_t tt) -> bool {
       if (!wait(&sm.full[rk.slot], rk.par)) return false;
       tc_fence_after_sync();
@@ -365,7 +397,6 @@ __device__ __forceinline__ void decode_paged_issuer(DecodePagedSmem<DH>& sm,
                          kk > 0 ? 1u : 0u);
       mma_commit_warp(&sm.s_full[tt & 1u]);
       mma_commit_warp(&sm.empty[rk.slot]);
-      rk.step();
       rk.step();
       return true;
     };
@@ -385,7 +416,6 @@ __device__ __forceinline__ void decode_paged_issuer(DecodePagedSmem<DH>& sm,
       mma_commit_warp(&sm.pv_done);
       mma_commit_warp(&sm.empty[rv.slot]);
       rv.step();
-      if (j + 1 < s.count) rv.step();
       if (j + 2 < s.count) {
         if (!(ok = issue_s(t + 2))) break;
         if (j + 3 == s.count) mma_commit_warp(&sm.qt_free);
@@ -417,20 +447,18 @@ __device__ __forceinline__ void decode_paged_softmax(DecodePagedSmem<DH>& sm,
   const uint32_t lane_addr = tbase + ((uint32_t)(warp * 32) << 16);
   const uint32_t colO = lane_addr + Cfg::kColO;
   const float sl2 = p.scale_log2;
-  PagedRing<Cfg::kSlots> r;   // the ring entry of the current tile's V
+  PagedRingV<DH> r;           // the current tile's V
   uint32_t t = 0;             // tiles so far, over all segments
   uint32_t nseg = 0;
   bool ok = true;
   PagedSegment s;
   while (ok && walk.next(p, s)) {
-    for (int e = 0; e < Cfg::kQSlots; ++e) r.step();
     const int g = s.gi / p.row_blocks, rb = s.gi - g * p.row_blocks;
     const int rows = min(128, p.G - 128 * rb);
     const bool real = head < rows;
     const size_t bh = (size_t)s.b * p.Hq + (size_t)g * p.G + 128 * rb + head;
     float m_run = -INFINITY, l_run = 0.f;
     for (int j = 0; j < s.count; ++j, ++t) {
-      r.step();   // past K
       const int pos0 = (s.tile0 + j) * Cfg::kKeys;
       const int clo = max(0, s.lo - pos0), chi = min(Cfg::kKeys, s.L - pos0);   // visible columns
       const bool partial = clo > 0 || chi < Cfg::kKeys;
@@ -544,7 +572,7 @@ __device__ __forceinline__ void decode_paged_softmax(DecodePagedSmem<DH>& sm,
       tmem_st_wait();
       tc_fence_before_sync();
       mbar_arrive(&sm.p_full[t & 1u]);
-      r.step();   // past V
+      r.step();
     }
     // (o_final, not pv_done: two P.V may still be running here, and the parity of
     // a barrier tells only one phase from the next)
@@ -577,7 +605,7 @@ __device__ __forceinline__ void decode_paged_softmax(DecodePagedSmem<DH>& sm,
 }
 
 template <int DH, int REP>
-__global__ void __launch_bounds__(192, 1)
+__global__ void __launch_bounds__(288, 1)
     attn_decode_paged_sm103a(const __grid_constant__ CUtensorMap map_q,
                              const __grid_constant__ CUtensorMap map_k,
                              const __grid_constant__ CUtensorMap map_v,
@@ -593,7 +621,7 @@ __global__ void __launch_bounds__(192, 1)
   if (threadIdx.x == 0) {
     sm.abort_flag = 0;
     for (int i = 0; i < Cfg::kSlots; ++i) {
-      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.full[i], 2);   // two loading warps
       mbar_init(&sm.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -623,8 +651,10 @@ __global__ void __launch_bounds__(192, 1)
   griddep_wait();
   PagedWalk<Cfg::kKeys> walk;
   walk.init(p, blockIdx.x);
-  if (warp == Cfg::kWarpProducer)
-    decode_paged_producer<DH, REP>(sm, p, &map_q, &map_k, &map_v, walk, lane, abort);
+  if (warp >= Cfg::kWarpProducer + 2)
+    decode_paged_producer<DH, REP, true>(sm, p, &map_q, &map_v, walk, warp & 1, lane, abort);
+  else if (warp >= Cfg::kWarpProducer)
+    decode_paged_producer<DH, REP, false>(sm, p, &map_q, &map_k, walk, warp & 1, lane, abort);
   else if (warp == Cfg::kWarpIssuer)
     decode_paged_issuer<DH>(sm, p, tbase, walk, abort);
   else if (warp < active_warps)

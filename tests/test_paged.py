@@ -580,3 +580,31 @@ def test_withheld_tile_times_out_then_recovers():
     _step(s)
     status_ok()
     assert _all_same(s, want)
+
+
+@pytest.mark.parametrize("Dh", [64, 128, 256])
+def test_decode_of_more_tiles_than_the_ring_holds(Dh):
+    # shares of about 30 tiles per CTA, several units each: the ring of tiles wraps
+    # many times, also inside a unit
+    B, Hkv, page, cols = 16, 8, 16, 256
+    gen = torch.Generator(device="cuda").manual_seed(Dh)
+    kp, vp = (torch.randn((B * cols, Hkv, page, Dh), generator=gen, device="cuda").to(torch.bfloat16)
+              for _ in range(2))
+    table = torch.randperm(B * cols, generator=gen, device="cuda").to(torch.int32).view(B, cols)
+    sl = torch.randint(1, cols * page + 1, (B,), generator=gen, device="cuda", dtype=torch.int32)
+    sl[0] = cols * page
+    q = torch.randn((B, 16, 1, Dh), generator=gen, device="cuda").to(torch.bfloat16)
+    weights = torch.zeros(B, Hkv, cols * page, device="cuda")
+    got = chs.attn_decode_paged(q, kp, vp, table, sl, weights=weights)
+    status_ok()
+    for b, n in enumerate(sl.tolist()):
+        k, v = (x[table[b].long()].transpose(0, 1).reshape(Hkv, cols * page, Dh)[:, :n].double()
+                for x in (kp, vp))
+        z = q[b, :, 0].view(Hkv, 2, Dh).double() @ k.transpose(1, 2) * Dh ** -0.5
+        p = torch.softmax(z, -1)
+        o, a = (p @ v).view(16, Dh), (p @ v.abs()).view(16, Dh)
+        # (delta of paged_ref.decode with |q| . |k| <= 6 Dh: 2 * 6 Dh^1.5 2^-23)
+        rel = 12 * Dh ** 1.5 * 2.0 ** -23 + 2.0 ** -18
+        assert ((got[b, :, 0].double() - o).abs() <= ref.HALF_BF16 * (o.abs() + a) + rel * a).all()
+        w = p.sum(1)
+        assert ((weights[b, :, :n].double() - w).abs() <= rel * w).all()
