@@ -565,10 +565,10 @@ static int decode_paged_check(int B, int Hq, int Hkv, const chs::PagedCache& cac
   const int rc = paged_check(B, Hkv, cache, Dh);
   if (rc != ATTN_OK) return rc;
   if (Hq < 1 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
-  // the line of tiles (64 keys at least) and the grids are 32-bit
+  // the line of tiles (64 keys at least, and a place per unit) and the grids are 32-bit
   const long long rows = (long long)cache.cols * cache.page;
   const long long units = (long long)B * Hkv * ((Hq / Hkv + 127) / 128);
-  if (units > (1 << 24) || units * ((rows + 63) / 64) > 0x7fffffffLL - 1024)
+  if (units > (1 << 24) || units * ((rows + 63) / 64 + 1) > 0x7fffffffLL - 1024)
     return ATTN_ERR_INVALID_ARG;
   if ((long long)B * Hq + (long long)B * Hkv * ((rows + 511) / 512) > 0x7fffffffLL)
     return ATTN_ERR_INVALID_ARG;

@@ -105,8 +105,8 @@ cudaError_t launch_decode_paged(const void* q, const void* kpages, const void* v
   long long tiles = (rows + keys - 1) / keys;   // at most, per unit
   if (window > 0 && tiles > ((long long)window + keys - 2) / keys + 1)
     tiles = ((long long)window + keys - 2) / keys + 1;
-  tiles *= (long long)B * Hkv * prm.row_blocks;
-  prm.ctas = tiles < dev.num_sms ? (int)tiles : dev.num_sms;
+  const long long places = (tiles + 1) * B * Hkv * prm.row_blocks;
+  prm.ctas = places < dev.num_sms ? (int)places : dev.num_sms;
   prm.score_stride = score_stride(cache);
   prm.scale_log2 = scale_log2;
   prm.accumulate = accumulate;

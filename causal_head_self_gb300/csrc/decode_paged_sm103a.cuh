@@ -11,8 +11,10 @@
 // sequence to sequence, so a split fixed on the host leaves SMs idle.  Instead
 // the tiles (kKeys keys) of all units (sequence, K/V head, block of 128 query
 // heads) form one line, in unit order, and CTA c of the grid (one per SM) takes
-// tiles [c * share, (c + 1) * share) of it, whatever units they belong to.  A
-// unit thus is cut at most where a CTA's share ends.  The part of a unit that a
+// places [c * share, (c + 1) * share) of it, whatever units they belong to.  A
+// unit's first place holds no tile: it stands for the cost of starting and
+// ending a unit, about that of a tile, so that a CTA of many short units gets
+// fewer keys.  A unit is cut only where a CTA's share ends.  The part of a unit that a
 // CTA holds is a segment; the segment of CTA c and unit u has the number u + c
 // (along the line one of the two grows from segment to segment, so no two
 // share a number), which is its place in the partial results.  A second kernel
@@ -130,29 +132,35 @@ struct PagedSegment {
 // The segments of one CTA in order.  Every warp walks them for itself.
 template <int KEYS>
 struct PagedWalk {
-  int cur, end, share;   // places on the line of tiles
-  int b, gi, j0;         // next segment: unit and first tile in it
+  int cur, end, share;   // places on the line
+  int b, gi, at;         // next segment: unit and place in it (0: before its tiles)
   PagedSeq seq;
+
+  // places of a unit of n tiles
+  static __device__ __forceinline__ int places(int n) { return n > 0 ? n + 1 : 0; }
 
   // Places [cur, end) of CTA `cta`.  One whole warp.
   __device__ __forceinline__ void init(const DecodePagedParams& p, int cta) {
     const int lane = threadIdx.x % 32;
     const int per_seq = p.Hkv * p.row_blocks;   // units per sequence
-    int total = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const int bb = b0 + lane;
-      total += bb < p.B ? paged_seq<KEYS>(p, bb).n * per_seq : 0;
-    }
+    // the first 32 sequences (mostly all of them) are read once and kept
+    PagedSeq held = {0, 0, 0, 0};
+    if (lane < p.B) held = paged_seq<KEYS>(p, lane);
+    int total = places(held.n) * per_seq;
+    for (int bb = 32 + lane; bb < p.B; bb += 32) total += places(paged_seq<KEYS>(p, bb).n) * per_seq;
     total = __reduce_add_sync(0xffffffffu, total);
     share = max(1, (total + p.ctas - 1) / p.ctas);
     cur = (int)min((long long)total, (long long)cta * share);
     end = min(total, cur + share);
-    b = gi = j0 = 0;
+    b = gi = at = 0;
     if (cur >= end) return;
-    int before = 0;   // tiles of the sequences before b0
+    int before = 0;   // places of the sequences before b0
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const int bb = b0 + lane;
-      const int mine = bb < p.B ? paged_seq<KEYS>(p, bb).n * per_seq : 0;
+      if (b0 > 0) {
+        held = {0, 0, 0, 0};
+        if (b0 + lane < p.B) held = paged_seq<KEYS>(p, b0 + lane);
+      }
+      const int mine = places(held.n) * per_seq;
       int upto = mine;   // inclusive scan
 #pragma unroll
       for (int d = 1; d < 32; d *= 2) {
@@ -161,12 +169,15 @@ struct PagedWalk {
       }
       const uint32_t past = __ballot_sync(0xffffffffu, before + upto > cur);
       if (past) {
-        const int at = __ffs(past) - 1;
-        b = b0 + at;
-        const int offset = cur - before - __shfl_sync(0xffffffffu, upto - mine, at);
-        seq = paged_seq<KEYS>(p, b);
-        gi = offset / seq.n;
-        j0 = offset - gi * seq.n;
+        const int from = __ffs(past) - 1;
+        b = b0 + from;
+        const int offset = cur - before - __shfl_sync(0xffffffffu, upto - mine, from);
+        seq.L = __shfl_sync(0xffffffffu, held.L, from);
+        seq.lo = __shfl_sync(0xffffffffu, held.lo, from);
+        seq.first = __shfl_sync(0xffffffffu, held.first, from);
+        seq.n = __shfl_sync(0xffffffffu, held.n, from);
+        gi = offset / places(seq.n);
+        at = offset - gi * places(seq.n);
         return;
       }
       before += __shfl_sync(0xffffffffu, upto, 31);
@@ -174,30 +185,34 @@ struct PagedWalk {
   }
 
   __device__ __forceinline__ bool next(const DecodePagedParams& p, PagedSegment& s) {
-    if (cur >= end) return false;
     const int per_seq = p.Hkv * p.row_blocks;
-    if (gi == per_seq) {
-      gi = 0;
-      do {
-        seq = paged_seq<KEYS>(p, ++b);
-      } while (seq.n == 0);
+    while (cur < end) {
+      if (gi == per_seq) {
+        gi = 0;
+        do {
+          seq = paged_seq<KEYS>(p, ++b);
+        } while (seq.n == 0);
+      }
+      const int take = min(seq.n + 1 - at, end - cur);   // places of this unit
+      const int skip = max(at - 1, 0);                   // its tiles before them
+      s.b = b;
+      s.gi = gi;
+      s.L = seq.L;
+      s.lo = seq.lo;
+      s.tile0 = seq.first + skip;
+      s.count = at == 0 ? take - 1 : take;
+      s.starts = skip == 0;
+      s.unit = b * per_seq + gi;
+      s.last_cta = (cur - at + seq.n) / share;           // the CTA of its last tile
+      cur += take;
+      at += take;
+      if (at == seq.n + 1) {
+        at = 0;
+        ++gi;
+      }
+      if (s.count > 0) return true;
     }
-    s.b = b;
-    s.gi = gi;
-    s.L = seq.L;
-    s.lo = seq.lo;
-    s.tile0 = seq.first + j0;
-    s.count = min(seq.n - j0, end - cur);
-    s.starts = j0 == 0;
-    s.unit = b * per_seq + gi;
-    s.last_cta = (cur - j0 + seq.n - 1) / share;
-    cur += s.count;
-    j0 += s.count;
-    if (j0 == seq.n) {
-      j0 = 0;
-      ++gi;
-    }
-    return true;
+    return false;
   }
 };
 
@@ -451,6 +466,40 @@ __device__ __forceinline__ void decode_paged_softmax(DecodePagedSmem<DH>& sm,
   uint32_t t = 0;             // tiles so far, over all segments
   uint32_t nseg = 0;
   bool ok = true;
+  // the partial results of the segment before: still in tensor memory, m and l here
+  bool pending = false, pend_rows = false;
+  float pend_m = 0.f, pend_l = 0.f;
+  size_t pend_at = 0;
+  auto flush = [&]() -> bool {
+    // (o_final, not pv_done: two P.V may still be running here, and the parity of
+    // a barrier tells only one phase from the next)
+    if (!mbar_wait(&sm.o_final, nseg++ & 1u, abort)) return false;
+    tc_fence_after_sync();
+    float* dst = p.o_part + pend_at * DH;
+#pragma unroll 1
+    for (int c = 0; c < DH / 64; ++c) {
+      uint32_t o[2][32];
+      tmem_ld_32x32b_x32(colO + 64 * c, o[0]);
+      tmem_ld_32x32b_x32(colO + 64 * c + 32, o[1]);
+      tmem_ld_wait(o[0]);
+      tmem_ld_wait(o[1]);
+      if (pend_rows) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          uint32_t w8[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w8[i] = o[e / 4][8 * (e % 4) + i];
+          st_global_v8(dst + 64 * c + 8 * e, w8);
+        }
+      }
+    }
+    if (pend_rows) {
+      p.m_part[pend_at] = pend_m;
+      p.l_part[pend_at] = pend_l;
+    }
+    pending = false;
+    return true;
+  };
   PagedSegment s;
   while (ok && walk.next(p, s)) {
     const int g = s.gi / p.row_blocks, rb = s.gi - g * p.row_blocks;
@@ -569,39 +618,22 @@ __device__ __forceinline__ void decode_paged_softmax(DecodePagedSmem<DH>& sm,
         }
         fence_proxy_async_smem();
       }
+      // the first P.V of a segment overwrites O, which must have been read out
+      if (j == 0 && pending && !(ok = flush())) break;
       tmem_st_wait();
       tc_fence_before_sync();
       mbar_arrive(&sm.p_full[t & 1u]);
       r.step();
     }
-    // (o_final, not pv_done: two P.V may still be running here, and the parity of
-    // a barrier tells only one phase from the next)
-    if (!ok || !(ok = mbar_wait(&sm.o_final, nseg++ & 1u, abort))) break;
-    tc_fence_after_sync();
-    const int part_rows = REP == 4 ? p.G : 128;
-    const size_t ps = ((size_t)(s.unit + blockIdx.x) * REP + copy) * part_rows + head;
-    float* dst = p.o_part + ps * DH;
-#pragma unroll 1
-    for (int c = 0; c < DH / 32; ++c) {
-      uint32_t o[32];
-      tmem_ld_32x32b_x32(colO + 32 * c, o);
-      tmem_ld_wait(o);
-      if (real) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t w8[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w8[i] = o[8 * e + i];
-          st_global_v8(dst + 32 * c + 8 * e, w8);
-        }
-      }
-    }
-    if (real) {
-      p.m_part[ps] = m_run;
-      p.l_part[ps] = l_run;
-    }
-    tc_fence_before_sync();   // (the next segment's P.V overwrites O after p_full)
+    if (!ok) break;
+    // the segment's results are read out beside the next segment's first tile
+    pend_rows = real;
+    pend_m = m_run;
+    pend_l = l_run;
+    pend_at = ((size_t)(s.unit + blockIdx.x) * REP + copy) * (REP == 4 ? p.G : 128) + head;
+    pending = true;
   }
+  if (ok && pending) flush();
 }
 
 template <int DH, int REP>
@@ -649,6 +681,9 @@ __global__ void __launch_bounds__(288, 1)
   const uint32_t tbase = sm.tmem_base;
   // the lengths, the table and the cache may come from the previous kernel
   griddep_wait();
+  // the join kernel's blocks may be placed beside this grid's (every CTA of
+  // which is running by then): they wait for the whole grid, but not for a launch
+  if (threadIdx.x == 0) griddep_launch_dependents();
   PagedWalk<Cfg::kKeys> walk;
   walk.init(p, blockIdx.x);
   if (warp >= Cfg::kWarpProducer + 2)
@@ -667,7 +702,6 @@ __global__ void __launch_bounds__(288, 1)
     tmem_dealloc(tbase, Cfg::kCols);
   }
   if (threadIdx.x == 0 && sm.abort_flag) atomicExch(p.error_word, 4);   // ATTN_ERR_TIMEOUT
-  if (threadIdx.x == 0) griddep_launch_dependents();
 }
 
 // Joins a unit's partial results, in the order of its CTAs and copies:
@@ -688,6 +722,9 @@ __global__ void __launch_bounds__(kPagedJoinThreads)
   griddep_wait();
   if ((int)blockIdx.x < p.B * p.Hq) {
     const int bh = blockIdx.x, b = bh / p.Hq, h = bh - b * p.Hq;
+    const int g = h / p.G, hg = h - g * p.G, rb = hg / 128;
+    const int unit = (b * p.Hkv + g) * p.row_blocks + rb;
+    const int2 ctas = __ldcg(p.unit_ctas + unit);   // (only written for a unit with keys)
     const int L = __ldcg(p.seqlens + b);
     if (L < 1 || L > paged_rows(p)) {
       // no keys: zero; a length that no sequence can have is an error
@@ -696,9 +733,6 @@ __global__ void __launch_bounds__(kPagedJoinThreads)
       if (L != 0 && tid == 0) atomicExch(p.error_word, 1);   // ATTN_ERR_INVALID_ARG
       return;
     }
-    const int g = h / p.G, hg = h - g * p.G, rb = hg / 128;
-    const int unit = (b * p.Hkv + g) * p.row_blocks + rb;
-    const int2 ctas = __ldcg(p.unit_ctas + unit);
     const int n = (ctas.y - ctas.x + 1) * REP;
     const size_t at0 = (size_t)(unit + ctas.x) * REP * part_rows + (hg - 128 * rb);
     constexpr int kCols = DH > kPagedJoinThreads ? DH / kPagedJoinThreads : 1;
