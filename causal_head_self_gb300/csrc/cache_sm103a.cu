@@ -38,26 +38,48 @@ cudaError_t launch_paged_append(const void* k, const void* v, void* kpages, void
 
 template <int DH>
 static cudaError_t launch_key_weights_dh(const CUtensorMap& mq, const CUtensorMap& mk,
-                                         const KeyWeightsParams& prm, int device,
+                                         const KeyWeightsParams& prm, const DeviceInfo& dev,
                                          cudaStream_t stream) {
   constexpr size_t smem = key_weights_smem_bytes<DH>();
-  static_assert(smem * KeyWeightsCfg<DH>::kCtasPerSm <= 232448, "shared memory of one SM");
+  static_assert(smem <= 232448, "shared memory budget of one sm_103a CTA");
   static std::atomic<int> configured[kMaxDevices];
-  cudaError_t e = configure_once(configured, device, [] {
+  cudaError_t e = configure_once(configured, dev.device, [] {
     return cudaFuncSetAttribute(attn_key_weights_sm103a<DH>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   });
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_key_weights_sm103a<DH>, dim3((unsigned)(prm.key_blocks * prm.B * prm.Hkv)),
-                    dim3(KeyWeightsCfg<DH>::kThreads), smem, stream, mq, mk, prm);
+  const dim3 block(KeyWeightsCfg<DH>::kThreads);
+  if (prm.split == 1)
+    return launch_pdl(attn_key_weights_sm103a<DH>,
+                      dim3(prm.items < dev.num_sms ? prm.items : dev.num_sms), block, smem, stream,
+                      mq, mk, prm);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(prm.items * prm.split);
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = prm.split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, attn_key_weights_sm103a<DH>, mq, mk, prm);
 }
 
 cudaError_t launch_key_weights(const void* q, const void* k, const float* lse, const int* seqlens,
                                float* weights, int stride, int B, int Hq, int Hkv, int S, int Dh,
                                int causal, int window, int queries, int accumulate,
                                float scale_log2, const DeviceInfo& dev, cudaStream_t stream) {
+  // with up to 64 voting queries a tile holds those of several heads
+  int pad = 128;
+  if (queries > 0)
+    while (pad > 16 && pad / 2 >= queries) pad /= 2;
   CUtensorMap mq, mk;
-  if (!encode_bf16_map(&mq, q, Dh, S, (long long)B * Hq, 128) ||
+  if (!encode_bf16_map(&mq, q, Dh, S, (long long)B * Hq, pad) ||
       !encode_bf16_map(&mk, k, Dh, S, (long long)B * Hkv, 128))
     return cudaErrorInvalidValue;
   KeyWeightsParams prm;
@@ -70,16 +92,29 @@ cudaError_t launch_key_weights(const void* q, const void* k, const float* lse, c
   prm.window = window;
   prm.queries = queries;
   prm.accumulate = accumulate;
-  prm.key_blocks = (S + 127) / 128;
+  prm.items = (S + 127) / 128 * B * Hkv;
+  prm.pad = pad;
+  prm.by_heads = make_fast_div((uint32_t)Hkv);
+  prm.by_batch = make_fast_div((uint32_t)(B * Hkv));
+  // a cluster per item where that fills the SMs no more than once, and leaves
+  // each CTA a tile
+  const long long tiles = pad < 128 ? (prm.G * pad + 127) / 128
+                                    : (long long)prm.G * ((queries ? queries : S) + 127) / 128;
+  prm.split = 1;
+  prm.split_log2 = 0;
+  while (prm.split < 8 && 2LL * prm.split * prm.items <= dev.num_sms && 2LL * prm.split <= tiles) {
+    prm.split *= 2;
+    ++prm.split_log2;
+  }
   prm.scale_log2 = scale_log2;
   prm.lse = lse;
   prm.seqlens = seqlens;
   prm.weights = weights;
   prm.stride = stride;
   prm.error_word = dev.error_word;
-  return Dh == 256   ? launch_key_weights_dh<256>(mq, mk, prm, dev.device, stream)
-         : Dh == 128 ? launch_key_weights_dh<128>(mq, mk, prm, dev.device, stream)
-                     : launch_key_weights_dh<64>(mq, mk, prm, dev.device, stream);
+  return Dh == 256   ? launch_key_weights_dh<256>(mq, mk, prm, dev, stream)
+         : Dh == 128 ? launch_key_weights_dh<128>(mq, mk, prm, dev, stream)
+                     : launch_key_weights_dh<64>(mq, mk, prm, dev, stream);
 }
 
 cudaError_t launch_cache_evict(void* kpages, void* vpages, const int* table, const int* table_out,

@@ -10,21 +10,35 @@
 // 2 Dh FLOPs per visible pair on the tensor cores and one exponential, so the
 // kernel is bound by those two, which run side by side.
 //
-// A CTA takes 128 keys of one (sequence, K/V head) and walks the tiles of 128
-// queries that see any of them, head after head.  The product is taken
-// transposed, S^T = K Q^T (keys as rows): a thread then owns a key, and the sum
-// over queries stays in its registers -- no atomics, no shuffles, and the same
-// bits every time.  The queries' -lse / ln 2 are laid out in shared memory, one
-// tile after another, and read as broadcasts.
+// An item is 128 keys of one (sequence, K/V head) with the tiles of 128 queries
+// that see any of them, head after head.  The product is taken transposed,
+// S^T = K Q^T (keys as rows): a thread then owns a key, and the sum over
+// queries stays in its registers -- no atomics, no shuffles, and the same bits
+// every time.  The queries' -lse / ln 2 are laid out in shared memory, one tile
+// after another, and read as broadcasts.  With few voting queries a tile holds
+// those of several heads (`pad` columns each).
 //
-// Two CTAs share an SM (one at Dh = 256), so that one's exponentials run beside
-// the other's products.
+// One CTA per SM: one warp loads K and Q tiles through a ring (TMA), one issues
+// the tensor-core work, and two groups of four warps take turns at the tiles.
+// Everything that the summing warps have to know of a tile is prepared for them
+// by a warp per group, with the log-sum-exps: eight warps would each pay for
+// working it out, and instructions are what this kernel runs short of (a tile
+// costs a scheduler 290 of them for the sums alone, beside 512 cycles of
+// exponentials).  K goes to tensor memory once per item (tcgen05.cp), so that the
+// MMAs stream only Q from shared memory; three S buffers keep the tensor core
+// ahead.  At the end of an item the two groups' sums are added.
+//
+// With enough items the CTAs walk them, heaviest first (`split` = 1).  Few and
+// long items (few K/V heads, short prompts) are each shared by a cluster of
+// `split` CTAs, which take equal parts of its tiles; their sums meet in the
+// first one's shared memory and are added in order.
 #pragma once
 
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include "fast_div.h"
 #include "sm103a_ptx.cuh"
 
 namespace chs {
@@ -32,7 +46,10 @@ namespace chs {
 struct KeyWeightsParams {
   int B, Hq, Hkv, G, S;
   int causal, window, queries, accumulate;
-  int key_blocks;
+  int items;             // key blocks * B * Hkv
+  FastDiv by_heads, by_batch;   // by Hkv, by B * Hkv
+  int pad;               // columns of a tile per head: 128, or less with few voting queries
+  int split, split_log2; // CTAs per item, a power of two
   float scale_log2;
   const float* lse;      // [B, Hq, S]
   const int* seqlens;    // [B] or null (every sequence holds S)
@@ -45,50 +62,126 @@ template <int DH>
 struct KeyWeightsCfg {
   static constexpr int kBoxes = DH / 64;
   static constexpr int kBox = 128 * 128;              // bytes: 128 rows of 64 columns
-  static constexpr int kTile = kBoxes * kBox;
-  static constexpr int kStages = DH == 64 ? 4 : 2;    // Q tiles
-  static constexpr int kCtasPerSm = DH == 256 ? 1 : 2;
-  static constexpr uint32_t kCols = 256;              // S0, S1
-  static constexpr int kThreads = 192;                // warps 0-3 sums, 4 loads, 5 MMA
-  static constexpr int kLse = 4;                      // tiles of log-sum-exps held
+  static constexpr int kTile = kBoxes * kBox;         // ring slot: a K or Q tile
+  static constexpr int kSlots = DH == 64 ? 8 : DH == 128 ? 6 : 3;
+  static constexpr int kBuffers = 3;                  // S
+  static constexpr int kLse = 4;                      // entries per group
+  static constexpr int kHand = 8;                     // hand-over buffers
+  static constexpr uint32_t kColK = 384, kCols = 512; // S0, S1, S2 | K
+  // warps 0-7 sums, 8 MMA, 9 K and Q, 10 and 11 entries
+  static constexpr int kThreads = 384;
+  static constexpr int kWarpIssuer = 8, kWarpProducer = 9, kWarpLse = 10;
+  static constexpr int kLseAhead = 2;                 // entries per warp on the way
+  static constexpr int kMaxSplit = 8;
+  static constexpr int kLens = 256;                   // lengths kept in shared memory
 };
+
+// What the summing warps have to know of a tile.  Column c of a tile is visible
+// to key k0 + t where max(0, lo + t) <= c mod pad < min(end, hi + t) and
+// c < cols.
+struct __align__(16) KeyWeightsEntry {
+  int flags;            // of kKw...
+  int lo, hi, end;
+  long long out;        // the item's first key in `weights`
+  int rows;             // its keys
+  int cols;
+};
+constexpr int kKwWhole = 1;    // every column is visible to every key
+constexpr int kKwNone = 2;     // no tile: an item whose keys no query of this CTA sees
+constexpr int kKwLast = 4;     // this group's last tile of the item
+constexpr int kKwFinish = 8;   // ... and the item's: this group writes the sums
+constexpr int kKwPair = 16;    // the other group has tiles of the item too
+constexpr int kKwEnd = 32;     // nothing follows
+// S buffer (2 bits) and its parity, hand-over buffer (3 bits) and its parity
+constexpr int kKwS = 8, kKwSPar = 10, kKwHand = 12, kKwHandPar = 15;
 
 template <int DH>
 struct KeyWeightsSmem {
   using Cfg = KeyWeightsCfg<DH>;
-  uint8_t k[Cfg::kTile];
-  uint8_t q[Cfg::kStages][Cfg::kTile];
-  float nlse[Cfg::kLse][128];
-  uint64_t k_full, q_full[Cfg::kStages], q_empty[Cfg::kStages];
-  uint64_t l_full[Cfg::kLse], l_empty[Cfg::kLse];
-  uint64_t s_full[2], s_empty[2], mma_done;
+  uint8_t slot[Cfg::kSlots][Cfg::kTile];
+  float nlse[2][Cfg::kLse][128];
+  KeyWeightsEntry entry[2][Cfg::kLse];
+  float hand[Cfg::kHand][128];               // one group's sums for the other
+  float parts[Cfg::kMaxSplit][128];          // the cluster's sums (first CTA)
+  uint64_t full[Cfg::kSlots], empty[Cfg::kSlots];
+  uint64_t l_full[2][Cfg::kLse], l_empty[2][Cfg::kLse];
+  uint64_t s_full[Cfg::kBuffers], s_empty[Cfg::kBuffers];
+  uint64_t hand_full[Cfg::kHand], hand_empty[Cfg::kHand];
+  uint64_t k_free, mma_done;
   uint32_t tmem_base;
   int abort_flag;
+  int lens[Cfg::kLens];
 };
 
-// The tiles of one CTA: query rows [q0 + 128 i, ...) below q_end, i < n, for
-// each head of the group.
+// The work of one CTA on one item: tiles [t0, t1).  Tile t holds, with pad =
+// 128, queries q0 + 128 (t % n) ... of head t / n; otherwise queries q0 ... of
+// heads (128 / pad) t ....
 struct KeyWeightsItem {
-  int b, g, kb, L, q0, q_end, n;
+  int b, g, k0, L, q0, q_end, n, t0, t1;
 };
 
-__device__ __forceinline__ KeyWeightsItem key_weights_item(const KeyWeightsParams& p, int item) {
+// `lens`: the lengths of the first KeyWeightsCfg::kLens sequences.
+__device__ __forceinline__ int key_weights_len(const KeyWeightsParams& p, int b) {
+  const int n = p.seqlens ? __ldcg(p.seqlens + b) : p.S;
+  return n < 0 || n > p.S ? 0 : n;
+}
+
+template <int LENS>
+__device__ __forceinline__ KeyWeightsItem key_weights_item(const KeyWeightsParams& p,
+                                                           const int (&lens)[LENS], int item,
+                                                           int rank) {
   KeyWeightsItem it;
-  const int per = p.B * p.Hkv;
-  it.kb = item / per;   // the first key blocks have the most queries: they come first
-  const int bg = item - it.kb * per;
-  it.b = bg / p.Hkv;
-  it.g = bg - it.b * p.Hkv;
-  it.L = p.seqlens ? __ldcg(p.seqlens + it.b) : p.S;
-  if (it.L < 0 || it.L > p.S) it.L = 0;
-  const int k0 = 128 * it.kb;
+  const int kb = p.by_batch.div(item);   // the first key blocks have the most queries: first
+  const int bg = p.by_batch.mod(item);
+  it.b = p.by_heads.div(bg);
+  it.g = p.by_heads.mod(bg);
+  it.L = it.b < LENS ? lens[it.b] : key_weights_len(p, it.b);
+  it.k0 = 128 * kb;
   it.q0 = p.queries > 0 ? max(0, it.L - p.queries) : 0;
-  if (p.causal) it.q0 = max(it.q0, k0);
+  if (p.causal) it.q0 = max(it.q0, it.k0);
   it.q_end = it.L;
-  if (p.window > 0) it.q_end = (int)min((long long)it.L, (long long)k0 + 127 + p.window);
-  it.n = it.q_end > it.q0 ? (it.q_end - it.q0 + 127) / 128 : 0;
+  if (p.window > 0) it.q_end = (int)min((long long)it.L, (long long)it.k0 + 127 + p.window);
+  it.n = it.q_end > it.q0 && it.k0 < it.L ? (it.q_end - it.q0 + 127) / 128 : 0;
+  int tiles = it.n * p.G;
+  if (p.pad < 128 && tiles > 0) tiles = (p.G * p.pad + 127) / 128;
+  // (split is a power of two)
+  it.t0 = (int)((long long)tiles * rank >> p.split_log2);
+  it.t1 = (int)((long long)tiles * (rank + 1) >> p.split_log2);
   return it;
 }
+
+// Item `i` of a CTA (items or more: none).  Walking CTAs go through the items
+// forwards and backwards in turn, so that who had a heavy one gets a light one.
+__device__ __forceinline__ int key_weights_cta_item(const KeyWeightsParams& p, int i) {
+  if (p.split > 1) return i == 0 ? (int)blockIdx.x / p.split : p.items;
+  const int G = gridDim.x, c = blockIdx.x;
+  return i * G + ((i & 1) ? G - 1 - c : c);
+}
+
+// Walks the tiles of an item: the head and query of a tile's first column.
+struct KeyWeightsTile {
+  int head, query;
+  __device__ __forceinline__ KeyWeightsTile(const KeyWeightsParams& p, const KeyWeightsItem& it) {
+    if (p.pad == 128) {
+      head = it.n > 0 ? it.t0 / it.n : 0;
+      query = it.q0 + 128 * (it.t0 - head * it.n);
+    } else {
+      head = (128 / p.pad) * it.t0;
+      query = it.q0;
+    }
+  }
+  __device__ __forceinline__ void step(const KeyWeightsParams& p, const KeyWeightsItem& it) {
+    if (p.pad == 128) {
+      query += 128;
+      if (query >= it.q_end) {
+        query = it.q0;
+        ++head;
+      }
+    } else {
+      head += 128 / p.pad;
+    }
+  }
+};
 
 __device__ __forceinline__ void mbar_wait_drain_kw(uint64_t* bar, uint32_t parity) {
   const uint32_t a = smem_u32(bar);
@@ -98,8 +191,356 @@ __device__ __forceinline__ void mbar_wait_drain_kw(uint64_t* bar, uint32_t parit
   }
 }
 
+// Position in a ring of N: index and the parity of its current use.
+template <int N>
+struct KwRing {
+  int i = 0;
+  uint32_t par = 0;
+  __device__ __forceinline__ void step() {
+    if (++i == N) {
+      i = 0;
+      par ^= 1u;
+    }
+  }
+};
+
 template <int DH>
-__global__ void __launch_bounds__(192, KeyWeightsCfg<DH>::kCtasPerSm)
+__device__ __forceinline__ void key_weights_producer(KeyWeightsSmem<DH>& sm,
+                                                     const KeyWeightsParams& p,
+                                                     const CUtensorMap* map_q,
+                                                     const CUtensorMap* map_k, int rank, int lane,
+                                                     volatile int* abort) {
+  using Cfg = KeyWeightsCfg<DH>;
+  KwRing<Cfg::kSlots> r;
+  uint32_t loaded = 0, pars = 0;
+  bool ok = true;
+  auto wait_slot = [&]() -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(&sm.empty[r.i], r.par ^ 1u, abort));
+  };
+  auto mark_slot = [&] {
+    loaded |= 1u << r.i;
+    pars = (pars & ~(1u << r.i)) | (r.par << r.i);
+    r.step();
+  };
+  const int heads_per_tile = 128 / p.pad;
+  const int box_bytes = p.pad * 128;
+  for (int i = 0; ok; ++i) {
+    const int item = key_weights_cta_item(p, i);
+    if (item >= p.items) break;
+    const KeyWeightsItem it = key_weights_item(p, sm.lens, item, rank);
+    if (it.t0 >= it.t1) continue;
+    if (!(ok = wait_slot())) break;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&sm.full[r.i], Cfg::kTile);
+      for (int b = 0; b < Cfg::kBoxes; ++b)
+        tma_load_3d(sm.slot[r.i] + b * Cfg::kBox, map_k, &sm.full[r.i], 64 * b, it.k0,
+                    it.b * p.Hkv + it.g);
+    }
+    mark_slot();
+    KeyWeightsTile at(p, it);
+    for (int t = it.t0; t < it.t1; ++t, at.step(p, it)) {
+      if (!(ok = wait_slot())) break;
+      if (lane == 0) {
+        const int heads = min(heads_per_tile, p.G - at.head);
+        // (checked builds: a query row of the prompt)
+        const bool in = attn_check(at.query < p.S && heads > 0, p.error_word);
+        mbar_arrive_expect_tx(&sm.full[r.i], in ? heads * Cfg::kBoxes * box_bytes : 0);
+        for (int h = 0; in && h < heads; ++h)
+          for (int b = 0; b < Cfg::kBoxes; ++b)
+            tma_load_3d(sm.slot[r.i] + b * Cfg::kBox + h * box_bytes, map_q, &sm.full[r.i], 64 * b,
+                        at.query, it.b * p.Hq + it.g * p.G + at.head + h);
+      }
+      mark_slot();
+    }
+  }
+  // every copy this warp started has landed before the CTA may exit
+  if (lane == 0)
+    for (int i = 0; i < Cfg::kSlots; ++i)
+      if (loaded & (1u << i)) mbar_wait_drain_kw(&sm.full[i], (pars >> i) & 1u);
+}
+
+// The entries of one group: its tiles' descriptions and log-sum-exps (-lse / ln 2
+// of each column, 0 where there is no voting query: such a column is masked).
+// The tiles of all items are dealt to the groups in turn.  kLseAhead of them are
+// on the way at any time, since a load takes longer than a tile.
+template <int DH>
+__device__ __forceinline__ void key_weights_lse(KeyWeightsSmem<DH>& sm, const KeyWeightsParams& p,
+                                                int rank, int group, int lane,
+                                                volatile int* abort) {
+  using Cfg = KeyWeightsCfg<DH>;
+  constexpr int D = Cfg::kLseAhead;
+  float x[D][4];
+  int flags[D], lo[D], hi[D], end[D], cols[D], rows[D];
+  long long out[D];
+  KwRing<Cfg::kLse> l;
+  // where the walk stands: item, tile, the tile's first head's log-sum-exps
+  int i = -1, t = 0;
+  uint32_t tiles = 0, pairs = 0;   // tiles and shared items before it
+  KwRing<Cfg::kBuffers> s;         // the tile's S buffer
+  KeyWeightsItem it;
+  it.t0 = it.t1 = it.q_end = 0;
+  KeyWeightsTile at(p, it);
+  const float* row = p.lse;
+  bool ended = false;
+  const int head_step = (p.pad == 128 ? 1 : 128 / p.pad);
+  int col_row[4], col_query[4];   // this lane's columns: head (of the tile's), query
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    col_row[k] = (32 * k + lane) / p.pad;
+    col_query[k] = (32 * k + lane) % p.pad;
+  }
+  auto fetch = [&](float (&y)[4], int& f, int& e_lo, int& e_hi, int& e_end, int& e_cols,
+                   int& e_rows, long long& e_out) {
+    for (;;) {
+      if (t >= it.t1) {   // the next item that has keys
+        do {
+          const int item = key_weights_cta_item(p, ++i);
+          if (ended || item >= p.items) {
+            ended = true;
+            f = kKwEnd;
+            return;
+          }
+          it = key_weights_item(p, sm.lens, item, rank);
+        } while (it.k0 >= it.L);
+        t = it.t0;
+        at = KeyWeightsTile(p, it);
+        row = p.lse + ((size_t)it.b * p.Hq + it.g * p.G + at.head) * p.S;
+      }
+      const bool none = t >= it.t1;
+      const bool mine = (tiles & 1u) == (uint32_t)group;
+      const bool pair = it.t1 - it.t0 > 1;
+      if (mine) {
+        e_rows = it.L - it.k0;
+        e_out = ((long long)it.b * p.Hkv + it.g) * p.stride + it.k0;
+        const int c0 = it.k0 - at.query;   // (window: columns below c0 + t + window)
+        e_lo = p.causal ? c0 : -(1 << 30);
+        e_hi = p.window > 0 && p.window < 128 - c0 ? c0 + p.window : 128;
+        e_end = min(it.q_end - at.query, p.pad);
+        e_cols = min(128, (p.G - at.head) * p.pad);   // of heads that there are
+        f = (none ? kKwNone : 0) | (t + 2 >= it.t1 ? kKwLast : 0) |
+            (t + 1 >= it.t1 ? kKwFinish : 0) | (pair ? kKwPair : 0) |
+            (e_lo <= -127 && e_hi >= p.pad && e_end == p.pad && e_cols == 128 ? kKwWhole : 0) |
+            (s.i << kKwS) | ((int)s.par << kKwSPar) | ((int)(pairs % Cfg::kHand) << kKwHand) |
+            ((int)(pairs / Cfg::kHand & 1u) << kKwHandPar);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const bool in = !none && at.query + col_query[k] < it.q_end &&
+                          (p.pad == 128 || at.head + col_row[k] < p.G);
+          y[k] = in ? __ldcg(row + (size_t)col_row[k] * p.S + (at.query + col_query[k])) : 0.f;
+        }
+      }
+      if (!none) {
+        if (t + 1 == it.t1 && pair) ++pairs;
+        ++tiles;
+        s.step();
+        if (p.pad < 128 || at.query + 128 >= it.q_end) row += (size_t)head_step * p.S;
+        at.step(p, it);
+      }
+      ++t;
+      if (mine) return;
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+    fetch(x[d], flags[d], lo[d], hi[d], end[d], cols[d], rows[d], out[d]);
+  for (;;) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&sm.l_empty[group][l.i], l.par ^ 1u, abort))) return;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        sm.nlse[group][l.i][32 * k + lane] = x[d][k] * -1.4426950408889634f;
+      if (lane == 0)
+        sm.entry[group][l.i] =
+            KeyWeightsEntry{flags[d], lo[d], hi[d], end[d], out[d], rows[d], cols[d]};
+      mbar_arrive(&sm.l_full[group][l.i]);
+      l.step();
+      if (flags[d] & kKwEnd) return;
+      fetch(x[d], flags[d], lo[d], hi[d], end[d], cols[d], rows[d], out[d]);
+    }
+  }
+}
+
+template <int DH>
+__device__ __forceinline__ void key_weights_issuer(KeyWeightsSmem<DH>& sm,
+                                                   const KeyWeightsParams& p, uint32_t tbase,
+                                                   int rank, volatile int* abort) {
+  using Cfg = KeyWeightsCfg<DH>;
+  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, false);
+  const uint64_t desc = smem_desc_sw128(0, 16, 1024) | (smem_u32(sm.slot[0]) >> 4);
+  auto wait = [&](uint64_t* bar, uint32_t par) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(bar, par, abort));
+  };
+  KwRing<Cfg::kSlots> r;
+  KwRing<Cfg::kBuffers> s;
+  uint32_t done = 0;   // items begun
+  bool ok = true;
+  for (int i = 0; ok; ++i) {
+    const int item = key_weights_cta_item(p, i);
+    if (item >= p.items) break;
+    const KeyWeightsItem it = key_weights_item(p, sm.lens, item, rank);
+    if (it.t0 >= it.t1) continue;
+    // K to tensor memory, once the last item's MMAs have read theirs
+    if (done > 0 && !(ok = wait(&sm.k_free, (done - 1) & 1u))) break;
+    ++done;
+    if (!(ok = wait(&sm.full[r.i], r.par))) break;
+    tc_fence_after_sync();
+    const uint64_t k = desc + (uint64_t)r.i * (Cfg::kTile >> 4);
+#pragma unroll
+    for (int kk = 0; kk < DH / 16; ++kk)
+      tmem_cp_128x256b_warp(tbase + Cfg::kColK + 8 * kk,
+                            k + (((kk / 4) * Cfg::kBox + (kk % 4) * 32) >> 4));
+    mma_commit_warp(&sm.empty[r.i]);
+    r.step();
+    for (int t = it.t0; t < it.t1; ++t) {
+      if (!(ok = wait(&sm.full[r.i], r.par))) break;
+      if (!(ok = wait(&sm.s_empty[s.i], s.par ^ 1u))) break;
+      tc_fence_after_sync();
+      const uint64_t q = desc + (uint64_t)r.i * (Cfg::kTile >> 4);
+#pragma unroll
+      for (int kk = 0; kk < DH / 16; ++kk)
+        mma_bf16_ts_warp(tbase + 128u * s.i, tbase + Cfg::kColK + 8 * kk,
+                         q + (((kk / 4) * Cfg::kBox + (kk % 4) * 32) >> 4), idesc,
+                         kk > 0 ? 1u : 0u);
+      mma_commit_warp(&sm.s_full[s.i]);
+      mma_commit_warp(&sm.empty[r.i]);
+      r.step();
+      s.step();
+    }
+    mma_commit_warp(&sm.k_free);
+  }
+  // nothing of this warp's may still run on the tensor core at teardown
+  mma_commit_warp(&sm.mma_done);
+  mbar_wait_drain_kw(&sm.mma_done, 0);
+}
+
+// The sum over columns of 2^(s scale - lse) of one 32-column piece.
+__device__ __forceinline__ void key_weights_add(const uint32_t (&y)[32], const float4* nl,
+                                                float2 scale2, float2 (&sum)[2]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float4 n4 = nl[e];
+    const float2 a =
+        __ffma2_rn(make_float2(__uint_as_float(y[4 * e]), __uint_as_float(y[4 * e + 1])), scale2,
+                   make_float2(n4.x, n4.y));
+    const float2 b =
+        __ffma2_rn(make_float2(__uint_as_float(y[4 * e + 2]), __uint_as_float(y[4 * e + 3])),
+                   scale2, make_float2(n4.z, n4.w));
+    sum[0] = __fadd2_rn(sum[0], make_float2(ex2_approx(a.x), ex2_approx(a.y)));
+    sum[1] = __fadd2_rn(sum[1], make_float2(ex2_approx(b.x), ex2_approx(b.y)));
+  }
+}
+
+// Summing warps: thread tid (0 .. 127) of a group owns key k0 + tid.
+template <int DH>
+__device__ __forceinline__ void key_weights_sums(KeyWeightsSmem<DH>& sm, const KeyWeightsParams& p,
+                                                 uint32_t tbase, int group, int rank,
+                                                 volatile int* abort) {
+  using Cfg = KeyWeightsCfg<DH>;
+  const int tid = threadIdx.x % 128;
+  const uint32_t lane_addr = tbase + ((uint32_t)(tid & ~31) << 16);
+  const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
+  KwRing<Cfg::kLse> l;
+  // one arrival per warp, when all of it is done with what `bar` guards
+  auto release = [&](uint64_t* bar) {
+    __syncwarp();
+    if ((tid & 31) == 0) mbar_arrive(bar);
+  };
+  float total = 0.f;
+  for (;; l.step()) {
+    if (!mbar_wait(&sm.l_full[group][l.i], l.par, abort)) return;
+    const KeyWeightsEntry& entry = sm.entry[group][l.i];
+    const int4 en = *reinterpret_cast<const int4*>(&entry);   // flags, lo, hi, end
+    if (en.x & kKwEnd) return;
+    if (!(en.x & kKwNone)) {
+      // (the tiles alternate between the groups and S is computed in order, so the
+      // use of this buffer before this one is over: one parity bit is enough)
+      const int sb = (en.x >> kKwS) & 3;
+      if (!mbar_wait(&sm.s_full[sb], (uint32_t)(en.x >> kKwSPar) & 1u, abort)) return;
+      tc_fence_after_sync();
+      const uint32_t colS = lane_addr + 128u * sb;
+      const float4* nl = reinterpret_cast<const float4*>(sm.nlse[group][l.i]);
+      // a tile's sum is taken by itself and then added: the error of a long sum
+      // grows with the number of tiles, not of queries
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      if (en.x & kKwWhole) {
+        uint32_t y0[32], y1[32], y2[32], y3[32];
+        tmem_ld_32x32b_x32(colS, y0);
+        tmem_ld_32x32b_x32(colS + 32, y1);
+        tmem_ld_wait(y0);
+        tmem_ld_wait(y1);
+        tmem_ld_32x32b_x32(colS + 64, y2);
+        tmem_ld_32x32b_x32(colS + 96, y3);
+        key_weights_add(y0, nl, scale2, sum);
+        key_weights_add(y1, nl + 8, scale2, sum);
+        tmem_ld_wait(y2);
+        tmem_ld_wait(y3);
+        tc_fence_before_sync();
+        release(&sm.s_empty[sb]);   // S is in registers
+        key_weights_add(y2, nl + 16, scale2, sum);
+        key_weights_add(y3, nl + 24, scale2, sum);
+      } else {
+        int clo = max(0, en.y + tid);
+        const int chi = min(en.w, en.z + tid), cols = entry.cols;
+        const uint32_t span = chi > clo ? (uint32_t)(chi - clo - 1) : 0u;
+        if (chi <= clo) clo = 1 << 30;   // no column is visible
+        const int in_head = p.pad - 1;   // (a power of two less one)
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t y[32];
+          tmem_ld_32x32b_x32(colS + 32 * c, y);
+          tmem_ld_wait(y);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int col = 32 * c + e;
+            const float v =
+                keep_if_le(__uint_as_float(y[e]), (uint32_t)((col & in_head) - clo), span);
+            y[e] = col < cols ? __float_as_uint(v) : 0xff800000u;
+          }
+          key_weights_add(y, nl + 8 * c, scale2, sum);
+        }
+        tc_fence_before_sync();
+        release(&sm.s_empty[sb]);
+      }
+      total += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+    }
+    if (en.x & kKwLast) {
+      const int hb = (en.x >> kKwHand) & (Cfg::kHand - 1);
+      const uint32_t hpar = (uint32_t)(en.x >> kKwHandPar) & 1u;
+      if (!(en.x & kKwFinish)) {
+        if (!mbar_wait(&sm.hand_empty[hb], hpar ^ 1u, abort)) return;
+        sm.hand[hb][tid] = total;
+        release(&sm.hand_full[hb]);
+      } else {
+        if (en.x & kKwPair) {
+          if (!mbar_wait(&sm.hand_full[hb], hpar, abort)) return;
+          total += sm.hand[hb][tid];
+          release(&sm.hand_empty[hb]);
+        }
+        if (p.split > 1) {
+          // to the cluster's first CTA
+          const uint32_t mine = smem_u32(&sm.parts[rank][tid]);
+          uint32_t there;
+          asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(there) : "r"(mine));
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(total) : "memory");
+        } else if (tid < entry.rows) {
+          float* w = p.weights + entry.out + tid;
+          *w = p.accumulate ? *w + total : total;
+        }
+      }
+      total = 0.f;
+    }
+    release(&sm.l_empty[group][l.i]);
+  }
+}
+
+__device__ __forceinline__ void key_weights_cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// (No early exit: the CTAs of a cluster meet at its end.)
+template <int DH>
+__global__ void __launch_bounds__(384, 1)
     attn_key_weights_sm103a(const __grid_constant__ CUtensorMap map_q,
                             const __grid_constant__ CUtensorMap map_k, const KeyWeightsParams p) {
   using Cfg = KeyWeightsCfg<DH>;
@@ -109,203 +550,79 @@ __global__ void __launch_bounds__(192, KeyWeightsCfg<DH>::kCtasPerSm)
                                       ~uintptr_t(1023));
   volatile int* abort = &sm.abort_flag;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  griddep_wait();
-  const KeyWeightsItem it = key_weights_item(p, blockIdx.x);
-  const int k0 = 128 * it.kb;
-  if (k0 >= it.L) {
-    // (an empty sequence has no keys; an impossible length is an error)
-    if (it.L == 0 && it.kb == 0 && threadIdx.x == 0 && p.seqlens && __ldcg(p.seqlens + it.b) != 0)
-      atomicExch(p.error_word, 1);   // ATTN_ERR_INVALID_ARG
-    return;
-  }
-  const int tiles = it.n * p.G;
-  if (tiles == 0) {   // no voting query sees these keys
-    const int j = k0 + threadIdx.x;
-    if (!p.accumulate && threadIdx.x < 128 && j < it.L)
-      p.weights[((size_t)it.b * p.Hkv + it.g) * p.stride + j] = 0.f;
-    return;
-  }
+  const int rank = p.split > 1 ? (int)blockIdx.x % p.split : 0;
   if (threadIdx.x == 0) {
     sm.abort_flag = 0;
-    mbar_init(&sm.k_full, 1);
-    for (int i = 0; i < Cfg::kStages; ++i) {
-      mbar_init(&sm.q_full[i], 1);
-      mbar_init(&sm.q_empty[i], 1);
+    for (int i = 0; i < Cfg::kSlots; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 1);
     }
-    for (int i = 0; i < Cfg::kLse; ++i) {
-      mbar_init(&sm.l_full[i], 32);
-      mbar_init(&sm.l_empty[i], 128);
+    for (int i = 0; i < 2 * Cfg::kLse; ++i) {
+      mbar_init(&sm.l_full[0][i], 32);   // (both groups' rings lie in a row)
+      mbar_init(&sm.l_empty[0][i], 4);   // one arrival per summing warp of a group
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < Cfg::kBuffers; ++i) {
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.s_empty[i], 128);
+      mbar_init(&sm.s_empty[i], 4);
     }
+    for (int i = 0; i < Cfg::kHand; ++i) {
+      mbar_init(&sm.hand_full[i], 4);
+      mbar_init(&sm.hand_empty[i], 4);
+    }
+    mbar_init(&sm.k_free, 1);
     mbar_init(&sm.mma_done, 1);
     fence_mbarrier_init();
   }
-  if (warp == 5) {
+  if (warp == Cfg::kWarpIssuer) {
     tmem_alloc(&sm.tmem_base, Cfg::kCols);
     tmem_relinquish();
+  }
+  // (the lengths may come from the previous kernel)
+  griddep_wait();
+  for (int b = threadIdx.x; b < p.B; b += Cfg::kThreads) {
+    if (b < Cfg::kLens) sm.lens[b] = key_weights_len(p, b);
+    if (blockIdx.x == 0 && p.seqlens) {   // an impossible length is an error
+      const int n = __ldcg(p.seqlens + b);
+      if (n < 0 || n > p.S) atomicExch(p.error_word, 1);   // ATTN_ERR_INVALID_ARG
+    }
   }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tbase = sm.tmem_base;
-
-  if (warp == 4) {
-    // loads: K once, then per tile Q (one lane) and the log-sum-exps (the warp,
-    // fetched a tile ahead)
-    const int bg = it.b * p.Hkv + it.g;
-    if (lane == 0) {
-      mbar_arrive_expect_tx(&sm.k_full, Cfg::kTile);
-      for (int x = 0; x < Cfg::kBoxes; ++x)
-        tma_load_3d(sm.k + x * Cfg::kBox, &map_k, &sm.k_full, 64 * x, k0, bg);
-    }
-    uint32_t q_loads = 0;
-    bool ok = true;
-    float l[4];
-    auto fetch = [&](int h, int qt) {
-      const float* src = p.lse + ((size_t)it.b * p.Hq + it.g * p.G + h) * p.S;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = it.q0 + 128 * qt + 32 * e + lane;
-        l[e] = i < it.q_end ? __ldcg(src + i) : 0.f;
-      }
-    };
-    fetch(0, 0);
-    int t = 0;
-    for (int h = 0; ok && h < p.G; ++h)
-      for (int qt = 0; qt < it.n; ++qt, ++t) {
-        const int st = t % Cfg::kStages, ls = t % Cfg::kLse;
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_empty[st],
-                                                     ((t / Cfg::kStages) & 1) ^ 1u, abort))))
-          break;
-        if (lane == 0) {
-          // (checked builds: a query row of the prompt)
-          const bool in = attn_check(it.q0 + 128 * qt < p.S, p.error_word);
-          mbar_arrive_expect_tx(&sm.q_full[st], in ? Cfg::kTile : 0);
-          for (int x = 0; in && x < Cfg::kBoxes; ++x)
-            tma_load_3d(sm.q[st] + x * Cfg::kBox, &map_q, &sm.q_full[st], 64 * x,
-                        it.q0 + 128 * qt, it.b * p.Hq + it.g * p.G + h);
-        }
-        ++q_loads;
-        if (!(ok = __all_sync(0xffffffffu,
-                              mbar_wait(&sm.l_empty[ls], ((t / Cfg::kLse) & 1) ^ 1u, abort))))
-          break;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sm.nlse[ls][32 * e + lane] = l[e] * -1.4426950408889634f;
-        mbar_arrive(&sm.l_full[ls]);
-        if (qt + 1 < it.n) fetch(h, qt + 1);
-        else if (h + 1 < p.G) fetch(h + 1, 0);
-      }
-    // every copy this warp started has landed before the CTA may exit
-    if (lane == 0) {
-      mbar_wait_drain_kw(&sm.k_full, 0);
-      for (uint32_t i = 0; i < (uint32_t)Cfg::kStages; ++i)
-        if (q_loads > i) {
-          const uint32_t last = (q_loads - 1 - i) / Cfg::kStages;   // last use of stage i
-          mbar_wait_drain_kw(&sm.q_full[i], last & 1u);
-        }
-    }
-  } else if (warp == 5) {
-    constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, false);
-    const uint64_t dk = smem_desc_sw128(0, 16, 1024) | (smem_u32(sm.k) >> 4);
-    const uint64_t dq = smem_desc_sw128(0, 16, 1024) | (smem_u32(sm.q[0]) >> 4);
-    bool ok = __all_sync(0xffffffffu, mbar_wait(&sm.k_full, 0, abort));
-    for (int t = 0; ok && t < tiles; ++t) {
-      const int st = t % Cfg::kStages;
-      if (!(ok = __all_sync(0xffffffffu,
-                            mbar_wait(&sm.q_full[st], (t / Cfg::kStages) & 1, abort))))
-        break;
-      if (!(ok = __all_sync(0xffffffffu,
-                            mbar_wait(&sm.s_empty[t & 1], ((t >> 1) & 1) ^ 1u, abort))))
-        break;
-      tc_fence_after_sync();
-      const uint32_t dS = tbase + 128u * (t & 1);
-      const uint64_t b = dq + (uint64_t)st * (Cfg::kTile >> 4);
-#pragma unroll
-      for (int kk = 0; kk < DH / 16; ++kk) {
-        const uint32_t off = ((kk / 4) * Cfg::kBox + (kk % 4) * 32) >> 4;
-        mma_bf16_ss_warp(dS, dk + off, b + off, idesc, kk > 0 ? 1u : 0u);
-      }
-      mma_commit_warp(&sm.s_full[t & 1]);
-      mma_commit_warp(&sm.q_empty[st]);
-    }
-    // nothing of this warp's may still run on the tensor core at teardown
-    mma_commit_warp(&sm.mma_done);
-    mbar_wait_drain_kw(&sm.mma_done, 0);
+  if (p.split > 1) key_weights_cluster_sync();   // (every CTA runs before any writes to another)
+  if (warp == Cfg::kWarpProducer) {
+    key_weights_producer<DH>(sm, p, &map_q, &map_k, rank, lane, abort);
+  } else if (warp >= Cfg::kWarpLse) {
+    key_weights_lse<DH>(sm, p, rank, warp - Cfg::kWarpLse, lane, abort);
+  } else if (warp == Cfg::kWarpIssuer) {
+    key_weights_issuer<DH>(sm, p, tbase, rank, abort);
   } else {
-    const int j = k0 + threadIdx.x;   // this thread's key
-    const uint32_t lane_addr = tbase + ((uint32_t)(warp * 32) << 16);
-    const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
-    float total = 0.f;
-    bool ok = true;
-    int t = 0;
-    for (int h = 0; ok && h < p.G; ++h)
-      for (int qt = 0; qt < it.n; ++qt, ++t) {
-        const int ls = t % Cfg::kLse;
-        if (!(ok = mbar_wait(&sm.l_full[ls], (t / Cfg::kLse) & 1, abort))) break;
-        if (!(ok = mbar_wait(&sm.s_full[t & 1], (t >> 1) & 1, abort))) break;
-        tc_fence_after_sync();
-        const uint32_t colS = lane_addr + 128u * (t & 1);
-        // visible columns [clo, chi) of this key: queries at or after it, inside
-        // the window, below the end
-        const int q0 = it.q0 + 128 * qt;
-        int clo = p.causal ? max(0, j - q0) : 0;
-        int chi = it.q_end - q0;
-        if (p.window > 0) chi = (int)min((long long)chi, (long long)j + p.window - q0);
-        chi = min(chi, 128);
-        const bool full = __all_sync(0xffffffffu, clo == 0 && chi == 128);
-        const uint32_t span = chi > clo ? (uint32_t)(chi - clo - 1) : 0u;
-        if (chi <= clo) clo = 1 << 30;   // no column is visible
-        // a tile's sum is taken by itself and then added: the error of a long
-        // sum grows with the number of tiles, not of queries
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        const float4* nl = reinterpret_cast<const float4*>(sm.nlse[ls]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t y[32];
-          tmem_ld_32x32b_x32(colS + 32 * c, y);
-          tmem_ld_wait(y);
-          if (c == 3) {   // S is in registers: its buffer is free
-            tc_fence_before_sync();
-            mbar_arrive(&sm.s_empty[t & 1]);
-          }
-          if (!full) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              y[e] = __float_as_uint(
-                  keep_if_le(__uint_as_float(y[e]), (uint32_t)(32 * c + e - clo), span));
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 n4 = nl[8 * c + e];
-            const float2 a = __ffma2_rn(make_float2(__uint_as_float(y[4 * e]),
-                                                    __uint_as_float(y[4 * e + 1])),
-                                        scale2, make_float2(n4.x, n4.y));
-            const float2 b = __ffma2_rn(make_float2(__uint_as_float(y[4 * e + 2]),
-                                                    __uint_as_float(y[4 * e + 3])),
-                                        scale2, make_float2(n4.z, n4.w));
-            sum[0] = __fadd2_rn(sum[0], make_float2(ex2_approx(a.x), ex2_approx(a.y)));
-            sum[1] = __fadd2_rn(sum[1], make_float2(ex2_approx(b.x), ex2_approx(b.y)));
-          }
-        }
-        mbar_arrive(&sm.l_empty[ls]);
-        total += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-      }
-    if (ok && j < it.L) {
-      float* w = p.weights + ((size_t)it.b * p.Hkv + it.g) * p.stride + j;
-      *w = p.accumulate ? *w + total : total;
-    }
+    key_weights_sums<DH>(sm, p, tbase, warp / 4, rank, abort);
   }
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == Cfg::kWarpIssuer) {
     tc_fence_after_sync();
     tmem_dealloc(tbase, Cfg::kCols);
   }
   if (threadIdx.x == 0 && sm.abort_flag) atomicExch(p.error_word, 4);   // ATTN_ERR_TIMEOUT
+  if (p.split > 1) {
+    // every CTA's sums are in the first one's shared memory (all waits before
+    // this one are bounded, so every thread of the cluster comes here)
+    key_weights_cluster_sync();
+    if (rank == 0 && threadIdx.x < 128) {
+      const KeyWeightsItem it = key_weights_item(p, sm.lens, (int)blockIdx.x / p.split, 0);
+      const int j = it.k0 + threadIdx.x;
+      if (j < it.L) {
+        float total = 0.f;
+        for (int r = 0; r < p.split; ++r) total += sm.parts[r][threadIdx.x];
+        float* w = p.weights + ((size_t)it.b * p.Hkv + it.g) * p.stride + j;
+        *w = p.accumulate ? *w + total : total;
+      }
+    }
+  }
 }
 
 template <int DH>

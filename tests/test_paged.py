@@ -276,6 +276,10 @@ KEY_WEIGHTS = [
     (4, 2, 400, 64, [400, 300], 64, True, 129),           # keys that no voting query sees
     (4, 2, 257, 128, [257, 100], 0, False, 0),
     (4, 2, 257, 256, [257, 100], 17, False, 0),
+    (32, 1, 600, 64, [600, 513], 0, True, 0),             # one K/V head: a cluster per item
+    (12, 1, 300, 128, [300, 130], 40, True, 0),           # several heads per tile, the last not full
+    (5, 1, 300, 256, [300, 299], 64, True, 70),
+    (3, 3, 500, 64, [500, 3], 5, True, 0),
 ]
 
 
@@ -311,6 +315,42 @@ def test_key_weights_match_the_definition(Hq, Hkv, S, Dh, lens, nq, causal, wind
     for b, n in enumerate(lens):
         assert torch.equal(weights[b, :, :n], first[b, :, :n] + first[b, :, :n])
         assert (weights[b, :, n:] == 3.0).all()
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,S,Dh,nq,window", [
+    (3, 32, 8, 2500, 64, 0, 0),          # CTAs walk several items
+    (2, 16, 8, 1900, 256, 0, 500),
+    (8, 32, 32, 1030, 128, 33, 0),
+    (1, 8, 8, 2000, 128, 0, 0),          # a cluster of two per item
+    (1, 8, 1, 4000, 64, 0, 0),
+])
+def test_key_weights_of_many_tiles(B, Hq, Hkv, S, Dh, nq, window):
+    gen = torch.Generator(device="cuda").manual_seed(S)
+    q = torch.randn((B, Hq, S, Dh), generator=gen, device="cuda").to(torch.bfloat16)
+    k = torch.randn((B, Hkv, S, Dh), generator=gen, device="cuda").to(torch.bfloat16)
+    lens = [S - 137 * b for b in range(B)]
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    # any normaliser will do: the true ones, in 32 bits
+    _, lse = chs.attn_fwd_lse(q, k, k, window=window)
+    w = torch.zeros(B, Hkv, S, device="cuda")
+    chs.attn_key_weights(q, k, lse, w, sl, queries=nq, window=window)
+    status_ok()
+    again = torch.zeros_like(w)
+    chs.attn_key_weights(q, k, lse, again, sl, queries=nq, window=window, accumulate=False)
+    assert same_bits(w, again)
+    j = torch.arange(S, device="cuda")
+    for b, n in enumerate(lens):
+        i = torch.arange(max(0, n - nq) if nq else 0, n, device="cuda")[:, None]
+        seen = (j[:n] <= i) & ((j[:n] > i - window) if window else True)
+        want = torch.zeros(Hkv, n, dtype=torch.float64, device="cuda")
+        for h in range(Hq):
+            z = q[b, h, i[:, 0]].double() @ k[b, h * Hkv // Hq, :n].double().t() * Dh ** -0.5
+            p = torch.exp(z - lse[b, h, i].double())
+            want[h * Hkv // Hq] += torch.where(seen, p, 0.0).sum(0)
+        # as in paged_ref.key_weights with |q| . |k| <= 6 Dh and |lse| <= 20
+        rel = (Dh + 1) * 2.0 ** -23 * (6 * Dh ** 0.5 + 20) + 2.0 ** -18
+        assert ((w[b, :, :n].double() - want).abs() <= rel * want).all()
+        assert (w[b, :, n:] == 0).all()
 
 
 def test_key_weights_of_a_whole_prompt_from_its_forward_pass():
