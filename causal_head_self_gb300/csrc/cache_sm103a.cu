@@ -107,6 +107,9 @@ cudaError_t launch_key_weights(const void* q, const void* k, const float* lse, c
     ++prm.split_log2;
   }
   prm.scale_log2 = scale_log2;
+  const double per_lse = -1.4426950408889634 / (double)scale_log2;   // -log2(e) / scale_log2
+  prm.lse_hi = (float)per_lse;
+  prm.lse_lo = (float)(per_lse - (double)prm.lse_hi);
   prm.lse = lse;
   prm.seqlens = seqlens;
   prm.weights = weights;

@@ -14,9 +14,17 @@
 // that see any of them, head after head.  The product is taken transposed,
 // S^T = K Q^T (keys as rows): a thread then owns a key, and the sum over
 // queries stays in its registers -- no atomics, no shuffles, and the same bits
-// every time.  The queries' -lse / ln 2 are laid out in shared memory, one tile
-// after another, and read as broadcasts.  With few voting queries a tile holds
-// those of several heads (`pad` columns each).
+// every time.  With few voting queries a tile holds those of several heads (`pad`
+// columns each).
+//
+// The log-sum-exps enter through the product too: one more step of 16 columns
+// multiplies ones (in tensor memory, where K is) with -lse / scale, split into
+// three bf16 parts that together hold its 24 bits.  It comes last, so only its own
+// addition rounds at the size of lse / scale: 2^-24 |lse| on the exponent, what a
+// subtraction in 32 bits costs as well.  Read from shared memory by the summing
+// warps instead (as broadcasts, 512 bytes for four columns and warp), the
+// log-sum-exps kept shared memory, which feeds the MMAs, busy for 512 cycles a
+// tile.
 //
 // One CTA per SM: one warp loads K and Q tiles through a ring (TMA), one issues
 // the tensor-core work, and two groups of four warps take turns at the tiles.
@@ -51,6 +59,7 @@ struct KeyWeightsParams {
   int pad;               // columns of a tile per head: 128, or less with few voting queries
   int split, split_log2; // CTAs per item, a power of two
   float scale_log2;
+  float lse_hi, lse_lo;  // ln 2-free: -log2(e) / scale_log2 in two parts
   const float* lse;      // [B, Hq, S]
   const int* seqlens;    // [B] or null (every sequence holds S)
   float* weights;        // [B, Hkv, stride]
@@ -64,10 +73,12 @@ struct KeyWeightsCfg {
   static constexpr int kBox = 128 * 128;              // bytes: 128 rows of 64 columns
   static constexpr int kTile = kBoxes * kBox;         // ring slot: a K or Q tile
   static constexpr int kSlots = DH == 64 ? 8 : DH == 128 ? 6 : 3;
-  static constexpr int kBuffers = 3;                  // S
+  static constexpr int kBuffers = DH == 256 ? 2 : 3;  // S
   static constexpr int kLse = 4;                      // entries per group
   static constexpr int kHand = 8;                     // hand-over buffers
-  static constexpr uint32_t kColK = 384, kCols = 512; // S0, S1, S2 | K
+  // tensor memory: S buffers | K | ones
+  static constexpr uint32_t kColK = 128 * kBuffers, kColOne = kColK + DH / 2, kCols = 512;
+  static_assert(kColOne + 8 <= kCols, "tensor memory");
   // warps 0-7 sums, 8 MMA, 9 K and Q, 10 and 11 entries
   static constexpr int kThreads = 384;
   static constexpr int kWarpIssuer = 8, kWarpProducer = 9, kWarpLse = 10;
@@ -99,7 +110,9 @@ template <int DH>
 struct KeyWeightsSmem {
   using Cfg = KeyWeightsCfg<DH>;
   uint8_t slot[Cfg::kSlots][Cfg::kTile];
-  float nlse[2][Cfg::kLse][128];
+  // three bf16 parts per column and five zeros: the first eight of the step's 16
+  // columns (8-row core matrices, one after another)
+  uint4 nlse[2][Cfg::kLse][128];
   KeyWeightsEntry entry[2][Cfg::kLse];
   float hand[Cfg::kHand][128];               // one group's sums for the other
   float parts[Cfg::kMaxSplit][128];          // the cluster's sums (first CTA)
@@ -163,7 +176,7 @@ struct KeyWeightsTile {
   int head, query;
   __device__ __forceinline__ KeyWeightsTile(const KeyWeightsParams& p, const KeyWeightsItem& it) {
     if (p.pad == 128) {
-      head = it.n > 0 ? it.t0 / it.n : 0;
+      head = it.t0 > 0 ? it.t0 / it.n : 0;
       query = it.q0 + 128 * (it.t0 - head * it.n);
     } else {
       head = (128 / p.pad) * it.t0;
@@ -191,7 +204,9 @@ __device__ __forceinline__ void mbar_wait_drain_kw(uint64_t* bar, uint32_t parit
   }
 }
 
-// Position in a ring of N: index and the parity of its current use.
+// Position in a ring of N: index and the parity of its current use.  Whoever
+// waits on a ring's barriers passes every use in turn, or can tell otherwise that
+// the use before is over: the parity tells only one phase from the next.
 template <int N>
 struct KwRing {
   int i = 0;
@@ -259,10 +274,10 @@ __device__ __forceinline__ void key_weights_producer(KeyWeightsSmem<DH>& sm,
       if (loaded & (1u << i)) mbar_wait_drain_kw(&sm.full[i], (pars >> i) & 1u);
 }
 
-// The entries of one group: its tiles' descriptions and log-sum-exps (-lse / ln 2
-// of each column, 0 where there is no voting query: such a column is masked).
-// The tiles of all items are dealt to the groups in turn.  kLseAhead of them are
-// on the way at any time, since a load takes longer than a tile.
+// The entries of one group: its tiles' descriptions and log-sum-exps (0 where
+// there is no voting query: such a column is masked).  The tiles of all items are
+// dealt to the groups in turn.  kLseAhead of them are on the way at any time,
+// since a load takes longer than a tile.
 template <int DH>
 __device__ __forceinline__ void key_weights_lse(KeyWeightsSmem<DH>& sm, const KeyWeightsParams& p,
                                                 int rank, int group, int lane,
@@ -273,72 +288,70 @@ __device__ __forceinline__ void key_weights_lse(KeyWeightsSmem<DH>& sm, const Ke
   int flags[D], lo[D], hi[D], end[D], cols[D], rows[D];
   long long out[D];
   KwRing<Cfg::kLse> l;
-  // where the walk stands: item, tile, the tile's first head's log-sum-exps
-  int i = -1, t = 0;
-  uint32_t tiles = 0, pairs = 0;   // tiles and shared items before it
-  KwRing<Cfg::kBuffers> s;         // the tile's S buffer
+  // where the walk stands: the item and this group's next tile t in it, which
+  // begins at tile `part` of n of head block `head`
+  int i = -1, t = 0, n = 1, head = 0, part = 0;
+  uint32_t before = 0, pairs = 0;   // tiles and shared items before the item
   KeyWeightsItem it;
-  it.t0 = it.t1 = it.q_end = 0;
-  KeyWeightsTile at(p, it);
-  const float* row = p.lse;
-  bool ended = false;
-  const int head_step = (p.pad == 128 ? 1 : 128 / p.pad);
-  int col_row[4], col_query[4];   // this lane's columns: head (of the tile's), query
+  it.t0 = it.t1 = 0;
+  it.k0 = it.L = it.q_end = it.q0 = it.b = it.g = 0;
+  const float* base = p.lse;        // the item's first head
+  const int heads_per_tile = 128 / p.pad;
+  int col_query[4];                 // this lane's columns: query, place from the tile's first
+  long long col_at[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    col_row[k] = (32 * k + lane) / p.pad;
     col_query[k] = (32 * k + lane) % p.pad;
+    col_at[k] = (long long)((32 * k + lane) / p.pad) * p.S + col_query[k];
   }
   auto fetch = [&](float (&y)[4], int& f, int& e_lo, int& e_hi, int& e_end, int& e_cols,
                    int& e_rows, long long& e_out) {
-    for (;;) {
-      if (t >= it.t1) {   // the next item that has keys
-        do {
-          const int item = key_weights_cta_item(p, ++i);
-          if (ended || item >= p.items) {
-            ended = true;
-            f = kKwEnd;
-            return;
-          }
-          it = key_weights_item(p, sm.lens, item, rank);
-        } while (it.k0 >= it.L);
-        t = it.t0;
-        at = KeyWeightsTile(p, it);
-        row = p.lse + ((size_t)it.b * p.Hq + it.g * p.G + at.head) * p.S;
-      }
-      const bool none = t >= it.t1;
-      const bool mine = (tiles & 1u) == (uint32_t)group;
-      const bool pair = it.t1 - it.t0 > 1;
-      if (mine) {
+    while (t >= it.t1) {   // the next item with a tile for this group
+      before += (uint32_t)(it.t1 - it.t0);
+      pairs += it.t1 - it.t0 > 1 ? 1 : 0;
+      do {
+        const int item = key_weights_cta_item(p, ++i);
+        if (item >= p.items) {
+          f = kKwEnd;
+          return;
+        }
+        it = key_weights_item(p, sm.lens, item, rank);
+      } while (it.k0 >= it.L);
+      t = it.t0 + (int)((before ^ (uint32_t)group) & 1u);
+      n = p.pad == 128 ? it.n : 1;
+      head = t > 0 ? t / n : 0;
+      part = t - head * n;
+      base = p.lse + ((size_t)it.b * p.Hq + it.g * p.G) * p.S;
+      if (it.t0 == it.t1 && t == it.t0) {   // no query sees its keys
+        f = kKwNone | kKwLast | kKwFinish;
         e_rows = it.L - it.k0;
         e_out = ((long long)it.b * p.Hkv + it.g) * p.stride + it.k0;
-        const int c0 = it.k0 - at.query;   // (window: columns below c0 + t + window)
-        e_lo = p.causal ? c0 : -(1 << 30);
-        e_hi = p.window > 0 && p.window < 128 - c0 ? c0 + p.window : 128;
-        e_end = min(it.q_end - at.query, p.pad);
-        e_cols = min(128, (p.G - at.head) * p.pad);   // of heads that there are
-        f = (none ? kKwNone : 0) | (t + 2 >= it.t1 ? kKwLast : 0) |
-            (t + 1 >= it.t1 ? kKwFinish : 0) | (pair ? kKwPair : 0) |
-            (e_lo <= -127 && e_hi >= p.pad && e_end == p.pad && e_cols == 128 ? kKwWhole : 0) |
-            (s.i << kKwS) | ((int)s.par << kKwSPar) | ((int)(pairs % Cfg::kHand) << kKwHand) |
-            ((int)(pairs / Cfg::kHand & 1u) << kKwHandPar);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const bool in = !none && at.query + col_query[k] < it.q_end &&
-                          (p.pad == 128 || at.head + col_row[k] < p.G);
-          y[k] = in ? __ldcg(row + (size_t)col_row[k] * p.S + (at.query + col_query[k])) : 0.f;
-        }
+        return;   // (t >= t1: the next call goes on)
       }
-      if (!none) {
-        if (t + 1 == it.t1 && pair) ++pairs;
-        ++tiles;
-        s.step();
-        if (p.pad < 128 || at.query + 128 >= it.q_end) row += (size_t)head_step * p.S;
-        at.step(p, it);
-      }
-      ++t;
-      if (mine) return;
     }
+    const int query = it.q0 + 128 * part, first = head * heads_per_tile;
+    const int c0 = it.k0 - query;   // (window: columns below c0 + t + window)
+    e_lo = p.causal ? c0 : -(1 << 30);
+    e_hi = p.window > 0 && p.window < 128 - c0 ? c0 + p.window : 128;
+    e_end = min(it.q_end - query, p.pad);
+    e_cols = min(128, (p.G - first) * p.pad);   // of heads that there are
+    const uint32_t tile = before + (uint32_t)(t - it.t0), use = tile / Cfg::kBuffers;
+    f = (it.t1 - it.t0 > 1 ? kKwPair : 0) |
+        (e_lo <= -127 && e_hi >= p.pad && e_end == p.pad && e_cols == 128 ? kKwWhole : 0) |
+        ((int)(tile - use * Cfg::kBuffers) << kKwS) | ((int)(use & 1u) << kKwSPar) |
+        ((int)(pairs % Cfg::kHand) << kKwHand) | ((int)(pairs / Cfg::kHand & 1u) << kKwHandPar);
+    if (t + 2 >= it.t1) f |= kKwLast;
+    if (t + 1 >= it.t1) {
+      f |= kKwFinish;
+      e_rows = it.L - it.k0;
+      e_out = ((long long)it.b * p.Hkv + it.g) * p.stride + it.k0;
+    }
+    const float* src = base + (size_t)first * p.S + query;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      y[k] = col_query[k] < e_end && 32 * k + lane < e_cols ? __ldcg(src + col_at[k]) : 0.f;
+    t += 2;
+    for (part += 2; part >= n; part -= n) ++head;
   };
 #pragma unroll
   for (int d = 0; d < D; ++d)
@@ -348,8 +361,16 @@ __device__ __forceinline__ void key_weights_lse(KeyWeightsSmem<DH>& sm, const Ke
     for (int d = 0; d < D; ++d) {
       if (!__all_sync(0xffffffffu, mbar_wait(&sm.l_empty[group][l.i], l.par ^ 1u, abort))) return;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        sm.nlse[group][l.i][32 * k + lane] = x[d][k] * -1.4426950408889634f;
+      for (int k = 0; k < 4; ++k) {
+        // -lse / scale to more than 32 bits, and its three bf16 parts
+        const float v = x[d][k] * p.lse_hi;
+        const float rest = fmaf(x[d][k], p.lse_hi, -v) + x[d][k] * p.lse_lo;
+        const float a = __bfloat162float(__float2bfloat16_rn(v));
+        const float b = __bfloat162float(__float2bfloat16_rn(v - a));
+        sm.nlse[group][l.i][32 * k + lane] =
+            make_uint4(pack_bf16x2(a, b), pack_bf16x2((v - a - b) + rest, 0.f), 0u, 0u);
+      }
+      fence_proxy_async_smem();   // (the MMA reads them)
       if (lane == 0)
         sm.entry[group][l.i] =
             KeyWeightsEntry{flags[d], lo[d], hi[d], end[d], out[d], rows[d], cols[d]};
@@ -367,19 +388,32 @@ __device__ __forceinline__ void key_weights_issuer(KeyWeightsSmem<DH>& sm,
                                                    int rank, volatile int* abort) {
   using Cfg = KeyWeightsCfg<DH>;
   constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, false);
-  const uint64_t desc = smem_desc_sw128(0, 16, 1024) | (smem_u32(sm.slot[0]) >> 4);
+  const uint64_t desc = smem_desc_sw128(smem_u32(sm.slot[0]), 16, 1024);
   auto wait = [&](uint64_t* bar, uint32_t par) -> bool {
     return __all_sync(0xffffffffu, mbar_wait(bar, par, abort));
   };
+  // the log-sum-exps' step: no swizzle, core matrices of 8 rows of 16 bytes
+  // 128 bytes apart; the second eight columns, which meet zeros, are the first again
+  const uint64_t plain = ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
   KwRing<Cfg::kSlots> r;
   KwRing<Cfg::kBuffers> s;
-  uint32_t done = 0;   // items begun
+  KwRing<Cfg::kLse> l0, l1;   // the groups' entries
+  uint32_t done = 0;    // items begun
+  uint32_t group = 0;   // whose tile is next
+  auto wait_entry = [&]() -> bool {
+    return wait(&sm.l_full[group][group ? l1.i : l0.i], group ? l1.par : l0.par);
+  };
   bool ok = true;
   for (int i = 0; ok; ++i) {
     const int item = key_weights_cta_item(p, i);
     if (item >= p.items) break;
     const KeyWeightsItem it = key_weights_item(p, sm.lens, item, rank);
-    if (it.t0 >= it.t1) continue;
+    if (it.t0 >= it.t1) {
+      // (an entry without a tile is passed in its turn: see KwRing's parity)
+      if (it.k0 < it.L && !(ok = wait_entry())) break;
+      if (it.k0 < it.L) (group ? l1 : l0).step();
+      continue;
+    }
     // K to tensor memory, once the last item's MMAs have read theirs
     if (done > 0 && !(ok = wait(&sm.k_free, (done - 1) & 1u))) break;
     ++done;
@@ -402,9 +436,16 @@ __device__ __forceinline__ void key_weights_issuer(KeyWeightsSmem<DH>& sm,
         mma_bf16_ts_warp(tbase + 128u * s.i, tbase + Cfg::kColK + 8 * kk,
                          q + (((kk / 4) * Cfg::kBox + (kk % 4) * 32) >> 4), idesc,
                          kk > 0 ? 1u : 0u);
-      mma_commit_warp(&sm.s_full[s.i]);
       mma_commit_warp(&sm.empty[r.i]);
       r.step();
+      if (!(ok = wait_entry())) break;
+      tc_fence_after_sync();
+      // (a shared address of a cluster's CTA has its rank above the descriptor's bits)
+      const uint64_t lse = plain | ((smem_u32(sm.nlse[group][group ? l1.i : l0.i]) >> 4) & 0x3FFFu);
+      mma_bf16_ts_warp(tbase + 128u * s.i, tbase + Cfg::kColOne, lse, idesc, 1u);
+      mma_commit_warp(&sm.s_full[s.i]);
+      (group ? l1 : l0).step();
+      group ^= 1u;
       s.step();
     }
     mma_commit_warp(&sm.k_free);
@@ -414,20 +455,14 @@ __device__ __forceinline__ void key_weights_issuer(KeyWeightsSmem<DH>& sm,
   mbar_wait_drain_kw(&sm.mma_done, 0);
 }
 
-// The sum over columns of 2^(s scale - lse) of one 32-column piece.
-__device__ __forceinline__ void key_weights_add(const uint32_t (&y)[32], const float4* nl,
-                                                float2 scale2, float2 (&sum)[2]) {
+// The sum of 2^(s scale_log2) over 32 columns.
+__device__ __forceinline__ void key_weights_add(const uint32_t (&y)[32], float2 scale2,
+                                                float2 (&sum)[2]) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float4 n4 = nl[e];
+  for (int e = 0; e < 16; ++e) {
     const float2 a =
-        __ffma2_rn(make_float2(__uint_as_float(y[4 * e]), __uint_as_float(y[4 * e + 1])), scale2,
-                   make_float2(n4.x, n4.y));
-    const float2 b =
-        __ffma2_rn(make_float2(__uint_as_float(y[4 * e + 2]), __uint_as_float(y[4 * e + 3])),
-                   scale2, make_float2(n4.z, n4.w));
-    sum[0] = __fadd2_rn(sum[0], make_float2(ex2_approx(a.x), ex2_approx(a.y)));
-    sum[1] = __fadd2_rn(sum[1], make_float2(ex2_approx(b.x), ex2_approx(b.y)));
+        __fmul2_rn(make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])), scale2);
+    sum[e & 1] = __fadd2_rn(sum[e & 1], make_float2(ex2_approx(a.x), ex2_approx(a.y)));
   }
 }
 
@@ -459,7 +494,6 @@ __device__ __forceinline__ void key_weights_sums(KeyWeightsSmem<DH>& sm, const K
       if (!mbar_wait(&sm.s_full[sb], (uint32_t)(en.x >> kKwSPar) & 1u, abort)) return;
       tc_fence_after_sync();
       const uint32_t colS = lane_addr + 128u * sb;
-      const float4* nl = reinterpret_cast<const float4*>(sm.nlse[group][l.i]);
       // a tile's sum is taken by itself and then added: the error of a long sum
       // grows with the number of tiles, not of queries
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -471,14 +505,14 @@ __device__ __forceinline__ void key_weights_sums(KeyWeightsSmem<DH>& sm, const K
         tmem_ld_wait(y1);
         tmem_ld_32x32b_x32(colS + 64, y2);
         tmem_ld_32x32b_x32(colS + 96, y3);
-        key_weights_add(y0, nl, scale2, sum);
-        key_weights_add(y1, nl + 8, scale2, sum);
+        key_weights_add(y0, scale2, sum);
+        key_weights_add(y1, scale2, sum);
         tmem_ld_wait(y2);
         tmem_ld_wait(y3);
         tc_fence_before_sync();
         release(&sm.s_empty[sb]);   // S is in registers
-        key_weights_add(y2, nl + 16, scale2, sum);
-        key_weights_add(y3, nl + 24, scale2, sum);
+        key_weights_add(y2, scale2, sum);
+        key_weights_add(y3, scale2, sum);
       } else {
         int clo = max(0, en.y + tid);
         const int chi = min(en.w, en.z + tid), cols = entry.cols;
@@ -497,7 +531,7 @@ __device__ __forceinline__ void key_weights_sums(KeyWeightsSmem<DH>& sm, const K
                 keep_if_le(__uint_as_float(y[e]), (uint32_t)((col & in_head) - clo), span);
             y[e] = col < cols ? __float_as_uint(v) : 0xff800000u;
           }
-          key_weights_add(y, nl + 8 * c, scale2, sum);
+          key_weights_add(y, scale2, sum);
         }
         tc_fence_before_sync();
         release(&sm.s_empty[sb]);
@@ -586,10 +620,17 @@ __global__ void __launch_bounds__(384, 1)
       if (n < 0 || n > p.S) atomicExch(p.error_word, 1);   // ATTN_ERR_INVALID_ARG
     }
   }
-  tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tbase = sm.tmem_base;
+  if (warp < 4) {   // 1, 1, 1, 0, ... in each row
+    const uint32_t ones[8] = {0x3f803f80u, 0x00003f80u, 0u, 0u, 0u, 0u, 0u, 0u};
+    tmem_st_32x32b_x8(tbase + ((uint32_t)(warp * 32) << 16) + Cfg::kColOne, ones);
+    tmem_st_wait();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
   if (p.split > 1) key_weights_cluster_sync();   // (every CTA runs before any writes to another)
   if (warp == Cfg::kWarpProducer) {
     key_weights_producer<DH>(sm, p, &map_q, &map_k, rank, lane, abort);
