@@ -124,7 +124,7 @@ namespace {
 struct MapKey {
   const void* base;
   long long outer;
-  int Dh, rows, box_rows, stride_rows;
+  int Dh, rows, box_rows, stride_rows;   // stride_rows 0: the 4-D form (whole rows)
   bool operator==(const MapKey& o) const {
     return base == o.base && outer == o.outer && Dh == o.Dh && rows == o.rows &&
            box_rows == o.box_rows && stride_rows == o.stride_rows;
@@ -137,13 +137,9 @@ struct MapCache {
   int used = 0, next = 0;
 };
 thread_local MapCache t_maps;
-}  // namespace
 
-bool encode_bf16_map(CUtensorMap* map, const void* base, int Dh, int rows, long long outer,
-                     int box_rows, int stride_rows) {
-  if (stride_rows == 0) stride_rows = rows;
-  if (rows < 1 || stride_rows < rows) return false;
-  const MapKey key{base, outer, Dh, rows, box_rows, stride_rows};
+bool cached_map(CUtensorMap* map, const MapKey& key, int rank, const cuuint64_t* dims,
+                const cuuint64_t* strides, const cuuint32_t* box) {
   MapCache& c = t_maps;
   for (int i = 0; i < c.used; ++i) {
     if (c.key[i] == key) {
@@ -151,13 +147,12 @@ bool encode_bf16_map(CUtensorMap* map, const void* base, int Dh, int rows, long 
       return true;
     }
   }
-  cuuint64_t dims[3] = {(cuuint64_t)Dh, (cuuint64_t)rows, (cuuint64_t)outer};
-  cuuint64_t strides[2] = {(cuuint64_t)Dh * 2, (cuuint64_t)Dh * 2 * (cuuint64_t)stride_rows};
-  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
-  cuuint32_t elem[3] = {1, 1, 1};
-  if (g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
-               box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+  const cuuint32_t elem[4] = {1, 1, 1, 1};
+  if (g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
+               const_cast<void*>(key.base), dims, strides, box, elem,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return false;
   const int slot = c.next;
   c.key[slot] = key;
@@ -165,6 +160,28 @@ bool encode_bf16_map(CUtensorMap* map, const void* base, int Dh, int rows, long 
   c.next = (slot + 1) % MapCache::kEntries;
   if (c.used < MapCache::kEntries) ++c.used;
   return true;
+}
+}  // namespace
+
+bool encode_bf16_map(CUtensorMap* map, const void* base, int Dh, int rows, long long outer,
+                     int box_rows, int stride_rows) {
+  if (stride_rows == 0) stride_rows = rows;
+  if (rows < 1 || stride_rows < rows) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)Dh, (cuuint64_t)rows, (cuuint64_t)outer};
+  const cuuint64_t strides[2] = {(cuuint64_t)Dh * 2, (cuuint64_t)Dh * 2 * (cuuint64_t)stride_rows};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+  return cached_map(map, MapKey{base, outer, Dh, rows, box_rows, stride_rows}, 3, dims, strides,
+                    box);
+}
+
+bool encode_bf16_rows_map(CUtensorMap* map, const void* base, int Dh, int rows, long long outer,
+                          int box_rows) {
+  if (rows < 1) return false;
+  const cuuint64_t row = (cuuint64_t)Dh * 2;
+  const cuuint64_t dims[4] = {64, (cuuint64_t)rows, (cuuint64_t)Dh / 64, (cuuint64_t)outer};
+  const cuuint64_t strides[3] = {row, 128, row * (cuuint64_t)rows};
+  const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, (cuuint32_t)Dh / 64, 1};
+  return cached_map(map, MapKey{base, outer, Dh, rows, box_rows, 0}, 4, dims, strides, box);
 }
 
 }  // namespace chs

@@ -79,8 +79,9 @@ cudaError_t launch_key_weights(const void* q, const void* k, const float* lse, c
   if (queries > 0)
     while (pad > 16 && pad / 2 >= queries) pad /= 2;
   CUtensorMap mq, mk;
-  if (!encode_bf16_map(&mq, q, Dh, S, (long long)B * Hq, pad) ||
-      !encode_bf16_map(&mk, k, Dh, S, (long long)B * Hkv, 128))
+  if (!(pad == 128 ? encode_bf16_rows_map(&mq, q, Dh, S, (long long)B * Hq, 128)
+                   : encode_bf16_map(&mq, q, Dh, S, (long long)B * Hq, pad)) ||
+      !encode_bf16_rows_map(&mk, k, Dh, S, (long long)B * Hkv, 128))
     return cudaErrorInvalidValue;
   KeyWeightsParams prm;
   prm.B = B;

@@ -247,9 +247,7 @@ __device__ __forceinline__ void key_weights_producer(KeyWeightsSmem<DH>& sm,
     if (!(ok = wait_slot())) break;
     if (lane == 0) {
       mbar_arrive_expect_tx(&sm.full[r.i], Cfg::kTile);
-      for (int b = 0; b < Cfg::kBoxes; ++b)
-        tma_load_3d(sm.slot[r.i] + b * Cfg::kBox, map_k, &sm.full[r.i], 64 * b, it.k0,
-                    it.b * p.Hkv + it.g);
+      tma_load_4d(sm.slot[r.i], map_k, &sm.full[r.i], 0, it.k0, 0, it.b * p.Hkv + it.g);
     }
     mark_slot();
     KeyWeightsTile at(p, it);
@@ -260,10 +258,16 @@ __device__ __forceinline__ void key_weights_producer(KeyWeightsSmem<DH>& sm,
         // (checked builds: a query row of the prompt)
         const bool in = attn_check(at.query < p.S && heads > 0, p.error_word);
         mbar_arrive_expect_tx(&sm.full[r.i], in ? heads * Cfg::kBoxes * box_bytes : 0);
-        for (int h = 0; in && h < heads; ++h)
-          for (int b = 0; b < Cfg::kBoxes; ++b)
-            tma_load_3d(sm.slot[r.i] + b * Cfg::kBox + h * box_bytes, map_q, &sm.full[r.i], 64 * b,
-                        at.query, it.b * p.Hq + it.g * p.G + at.head + h);
+        if (p.pad == 128) {
+          if (in)
+            tma_load_4d(sm.slot[r.i], map_q, &sm.full[r.i], 0, at.query, 0,
+                        it.b * p.Hq + it.g * p.G + at.head);
+        } else {   // (a copy of whole rows would put a head's 64-column boxes together)
+          for (int h = 0; in && h < heads; ++h)
+            for (int b = 0; b < Cfg::kBoxes; ++b)
+              tma_load_3d(sm.slot[r.i] + b * Cfg::kBox + h * box_bytes, map_q, &sm.full[r.i],
+                          64 * b, at.query, it.b * p.Hq + it.g * p.G + at.head + h);
+        }
       }
       mark_slot();
     }
@@ -427,8 +431,17 @@ __device__ __forceinline__ void key_weights_issuer(KeyWeightsSmem<DH>& sm,
     mma_commit_warp(&sm.empty[r.i]);
     r.step();
     for (int t = it.t0; t < it.t1; ++t) {
-      if (!(ok = wait(&sm.full[r.i], r.par))) break;
-      if (!(ok = wait(&sm.s_empty[s.i], s.par ^ 1u))) break;
+      // (looked at together: one wait after another took 100 cycles each)
+      uint64_t* const entry = &sm.l_full[group][group ? l1.i : l0.i];
+      const uint32_t entry_par = group ? l1.par : l0.par;
+      const bool q_here = mbar_try_wait(smem_u32(&sm.full[r.i]), r.par);
+      const bool s_free = mbar_try_wait(smem_u32(&sm.s_empty[s.i]), s.par ^ 1u);
+      const bool e_here = mbar_try_wait(smem_u32(entry), entry_par);
+      if (!__all_sync(0xffffffffu, q_here && s_free && e_here)) {
+        if (!(ok = wait(&sm.full[r.i], r.par))) break;
+        if (!(ok = wait(&sm.s_empty[s.i], s.par ^ 1u))) break;
+        if (!(ok = wait(entry, entry_par))) break;
+      }
       tc_fence_after_sync();
       const uint64_t q = desc + (uint64_t)r.i * (Cfg::kTile >> 4);
 #pragma unroll
@@ -436,14 +449,12 @@ __device__ __forceinline__ void key_weights_issuer(KeyWeightsSmem<DH>& sm,
         mma_bf16_ts_warp(tbase + 128u * s.i, tbase + Cfg::kColK + 8 * kk,
                          q + (((kk / 4) * Cfg::kBox + (kk % 4) * 32) >> 4), idesc,
                          kk > 0 ? 1u : 0u);
-      mma_commit_warp(&sm.empty[r.i]);
-      r.step();
-      if (!(ok = wait_entry())) break;
-      tc_fence_after_sync();
       // (a shared address of a cluster's CTA has its rank above the descriptor's bits)
       const uint64_t lse = plain | ((smem_u32(sm.nlse[group][group ? l1.i : l0.i]) >> 4) & 0x3FFFu);
       mma_bf16_ts_warp(tbase + 128u * s.i, tbase + Cfg::kColOne, lse, idesc, 1u);
       mma_commit_warp(&sm.s_full[s.i]);
+      mma_commit_warp(&sm.empty[r.i]);
+      r.step();
       (group ? l1 : l0).step();
       group ^= 1u;
       s.step();

@@ -57,6 +57,12 @@ struct DeviceInfo {
 bool encode_bf16_map(CUtensorMap* map, const void* base, int Dh, int rows, long long outer,
                      int box_rows, int stride_rows = 0);
 
+// The same tensor as a 4-D map, dims {64, rows, Dh / 64, outer}, box {64,
+// box_rows, Dh / 64, 1}: one copy brings whole rows, laid out in shared memory as
+// the 64-column boxes of the 3-D map one after another.
+bool encode_bf16_rows_map(CUtensorMap* map, const void* base, int Dh, int rows, long long outer,
+                          int box_rows);
+
 // Queries: Sq rows per (b, h), at positions start_pos .. start_pos + Sq - 1.
 // K, V: Tkv rows per (b, K/V head) in memory, of which the first
 // start_pos + Sq are visible (a plain prefill: Tkv = Sq, start_pos = 0).
