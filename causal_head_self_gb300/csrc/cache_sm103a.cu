@@ -25,6 +25,9 @@ cudaError_t launch_paged_append(const void* k, const void* v, void* kpages, void
   prm.num_pages = cache.num_pages;
   prm.page = cache.page;
   prm.cols = cache.cols;
+  prm.by_s = make_fast_div((uint32_t)S);
+  prm.by_heads = make_fast_div((uint32_t)Hkv);
+  prm.by_page = make_fast_div((uint32_t)cache.page);
   prm.error_word = dev.error_word;
   const int per_pass = kAppendThreads / prm.vecs;
   constexpr int U = 4;
@@ -149,6 +152,7 @@ cudaError_t launch_cache_evict(void* kpages, void* vpages, const int* table, con
   prm.budget = budget;
   prm.recent = recent;
   prm.error_word = dev.error_word;
+  prm.by_page = make_fast_div((uint32_t)cache.page);
   cudaError_t e = launch_pdl(attn_cache_select_sm103a, dim3(B * Hkv), dim3(kSelectThreads), 0,
                              stream, prm);
   if (e != cudaSuccess) return e;

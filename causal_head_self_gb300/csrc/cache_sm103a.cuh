@@ -5,6 +5,7 @@
 
 #include <cstdint>
 
+#include "fast_div.h"
 #include "sm103a_ptx.cuh"
 
 namespace chs {
@@ -20,6 +21,7 @@ struct AppendParams {
   long long rows;        // B * Hkv * S
   int Hkv, S, vecs;      // vecs: 16-byte pieces per row
   int num_pages, page, cols;
+  FastDiv by_s, by_heads, by_page;
   int* error_word;
 };
 
@@ -27,44 +29,54 @@ constexpr int kAppendThreads = 256;
 
 // Row i < newlens[b] of the new keys and values becomes row seqlens[b] -
 // newlens[b] + i of the sequence.  A thread copies a 16-byte piece of K and V
-// of U rows; all its loads are issued before its stores.
+// of U rows.  Where a row goes takes two dependent loads (its sequence's lengths,
+// then the table), so the loads of all U rows go out together, and the row's own
+// bytes, whose place is known, beside the table's.
 template <int U>
 __global__ void __launch_bounds__(kAppendThreads) attn_paged_append_sm103a(const AppendParams p) {
   griddep_wait();
   const int per_pass = kAppendThreads / p.vecs;   // rows per pass of the block
   const int vec = threadIdx.x % p.vecs, r = threadIdx.x / p.vecs;
-  uint4 k[U], v[U];
-  long long dst[U];
+  const long long row0 = (long long)blockIdx.x * U * per_pass + r;
+  int b[U], g[U], i[U], n[U], add[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    dst[u] = -1;
-    const long long row = ((long long)blockIdx.x * U + u) * per_pass + r;
-    if (row >= p.rows) continue;
-    const int i = (int)(row % p.S);
-    const long long bg = row / p.S;
-    const int b = (int)(bg / p.Hkv), g = (int)(bg % p.Hkv);
-    const int n = __ldcg(p.seqlens + b), add = p.newlens ? __ldcg(p.newlens + b) : p.S;
-    if (n == 0 && !p.newlens) continue;   // an empty slot
-    if (add < 0 || add > p.S || n < add || n > p.cols * p.page) {
-      if (i == 0 && g == 0 && vec == 0) atomicExch(p.error_word, 1);   // ATTN_ERR_INVALID_ARG
-      continue;
+    const long long row = row0 + u * per_pass;   // (the number of rows is 32-bit)
+    const int bg = p.by_s.div(row < p.rows ? (int)row : 0);
+    i[u] = (int)row - bg * p.S;
+    b[u] = p.by_heads.div(bg);
+    g[u] = bg - b[u] * p.Hkv;
+    n[u] = p.seqlens[b[u]];
+    add[u] = p.newlens ? p.newlens[b[u]] : p.S;
+    if (row >= p.rows) add[u] = n[u] = 0;
+  }
+  uint4 k[U], v[U];
+  int id[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (n[u] == 0 && !p.newlens) add[u] = 0;   // an empty slot
+    if (add[u] < 0 || add[u] > p.S || n[u] < add[u] || n[u] > p.cols * p.page) {
+      if (i[u] == 0 && g[u] == 0 && vec == 0) atomicExch(p.error_word, 1);   // ATTN_ERR_INVALID_ARG
+      add[u] = 0;
     }
-    if (i >= add) continue;
-    const int t = n - add + i;
-    const int id = __ldcg(p.table + (long long)b * p.cols + t / p.page);
-    if (id < 0 || id >= p.num_pages) {
+    id[u] = -1;
+    if (i[u] >= add[u]) continue;
+    const long long from = (row0 + u * per_pass) * p.vecs + vec;
+    k[u] = __ldcs(p.k + from);
+    v[u] = __ldcs(p.v + from);
+    id[u] = p.table[(long long)b[u] * p.cols + p.by_page.div(n[u] - add[u] + i[u])];
+    if (id[u] < 0 || id[u] >= p.num_pages) {
       atomicExch(p.error_word, 1);
-      continue;
+      id[u] = -1;
     }
-    k[u] = __ldcg(p.k + row * p.vecs + vec);
-    v[u] = __ldcg(p.v + row * p.vecs + vec);
-    dst[u] = (((long long)id * p.Hkv + g) * p.page + t % p.page) * p.vecs + vec;
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    if (dst[u] < 0) continue;
-    p.kpages[dst[u]] = k[u];
-    p.vpages[dst[u]] = v[u];
+    if (id[u] < 0) continue;
+    const int row = p.by_page.mod(n[u] - add[u] + i[u]);
+    const long long to = (((long long)id[u] * p.Hkv + g[u]) * p.page + row) * p.vecs + vec;
+    p.kpages[to] = k[u];
+    p.vpages[to] = v[u];
   }
 }
 
@@ -80,6 +92,7 @@ struct EvictParams {
   int* keep;              // [B, Hkv, budget]
   int B, Hkv, vecs;
   int num_pages, page, cols, cols_out, stride, stride_out, budget, recent;
+  FastDiv by_page;
   int* error_word;
 };
 
@@ -92,18 +105,23 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 }
 
 constexpr int kSelectThreads = 1024;
-
+constexpr int kSelectBins = 8192;
 // Which rows stay.  One block per (sequence, K/V head): of the rows before the
 // last `recent`, the budget - recent with the largest weights, equal ones from
 // the lowest row on; and the last `recent`.  The smallest weight that stays is
-// found digit by digit (11, 11 and 10 bits of the ordered integer) from
+// found digit by digit (13, 10 and 9 bits of the ordered integer) from
 // histograms in shared memory; one more pass writes the rows' numbers and
 // weights in order.  In place, row i's weight moves to a place at or before i,
 // and a tile is read before anything of it is overwritten.
+//
+// The first digit's counts are what takes time: weights of one size fall into few
+// bins, whose atomics wait for one another.  So it is as long as the block's
+// scan allows; with 11 bits the selection took 29 us for 16 sequences of 16384 to
+// 32768 rows and 8 heads.
 __global__ void __launch_bounds__(kSelectThreads, 1) attn_cache_select_sm103a(const EvictParams p) {
-  __shared__ uint32_t hist[2048];
+  __shared__ uint32_t hist[kSelectBins];
   __shared__ uint32_t warp_sum[32];
-  __shared__ uint32_t sh_bin, sh_left;
+  __shared__ uint32_t sh_bin, sh_left, sh_all;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   griddep_wait();
   const int bg = blockIdx.x, b = bg / p.Hkv, g = bg - b * p.Hkv;
@@ -132,10 +150,10 @@ __global__ void __launch_bounds__(kSelectThreads, 1) attn_cache_select_sm103a(co
   if (left > 0) {
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-      const uint32_t digit = pass < 2 ? 0x7ffu : 0x3ffu;
-      hist[tid] = 0;
-      hist[tid + 1024] = 0;
+      const int shift = pass == 0 ? 19 : pass == 1 ? 9 : 0;
+      const uint32_t digit = pass == 0 ? 0x1fffu : pass == 1 ? 0x3ffu : 0x1ffu;
+      const int bins = (int)digit + 1, per = pass == 0 ? bins / kSelectThreads : 1;   // per thread
+      for (int i = tid; i < bins; i += kSelectThreads) hist[i] = 0;
       __syncthreads();
       constexpr int kLoads = 8;   // rows per thread and round: their loads are in flight together
       for (int i0 = 0; i0 < old; i0 += kLoads * kSelectThreads) {
@@ -163,9 +181,11 @@ __global__ void __launch_bounds__(kSelectThreads, 1) attn_cache_select_sm103a(co
       }
       __syncthreads();
       // the bin in which the count from the top reaches `left`: thread t holds
-      // bins 2047 - 2t and 2046 - 2t
-      const uint32_t a = hist[2047 - 2 * tid], c = hist[2046 - 2 * tid];
-      uint32_t upto = a + c;
+      // `per` bins from bins - 1 - t * per down
+      const int top = bins - 1 - tid * per;
+      uint32_t mine = 0;
+      for (int j = 0; j < per; ++j) mine += top >= j ? hist[top - j] : 0u;
+      uint32_t upto = mine;
 #pragma unroll
       for (int d = 1; d < 32; d *= 2) {
         const uint32_t y = __shfl_up_sync(0xffffffffu, upto, d);
@@ -173,20 +193,22 @@ __global__ void __launch_bounds__(kSelectThreads, 1) attn_cache_select_sm103a(co
       }
       if (lane == 31) warp_sum[warp] = upto;
       __syncthreads();
-      uint32_t before = lane < warp ? warp_sum[lane] : 0u;
-      before = __reduce_add_sync(0xffffffffu, before);
-      const uint32_t above = before + upto - (a + c);   // rows in higher bins
-      if (above < left && above + a >= left) {
-        sh_bin = 2047 - 2 * tid;
+      const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0u);
+      uint32_t above = before + upto - mine;   // rows in higher bins
+      if (above < left && above + mine >= left) {
+        int j = 0;
+        while (above + hist[top - j] < left) above += hist[top - j++];
+        sh_bin = (uint32_t)(top - j);
         sh_left = left - above;
-      } else if (above + a < left && above + a + c >= left) {
-        sh_bin = 2046 - 2 * tid;
-        sh_left = left - above - a;
+        sh_all = hist[top - j] == left - above ? 1 : 0;
       }
       __syncthreads();
       prefix |= sh_bin << shift;
       known |= digit << shift;
       left = sh_left;
+      // the whole bin stays: what is above or equal to `prefix` does, whatever the
+      // digits that follow
+      if (sh_all) break;
     }
   } else {
     prefix = 0xffffffffu;   // above every weight: none of the old rows stays
@@ -243,53 +265,61 @@ __global__ void __launch_bounds__(kSelectThreads, 1) attn_cache_select_sm103a(co
   for (int i = p.budget + tid; i < min(n, p.stride_out); i += kSelectThreads) w_out[i] = 0.f;
 }
 
-// 16-byte piece `vec` of row t of (b, g), or -1 for a page that is not there.
-__device__ __forceinline__ long long cache_piece(const EvictParams& p, const int* table, int cols,
-                                                 int b, int g, int t, int vec) {
-  const int id = __ldcg(table + (long long)b * cols + t / p.page);
-  if (id < 0 || id >= p.num_pages) {
-    atomicExch(p.error_word, 1);   // ATTN_ERR_INVALID_ARG
-    return -1;
-  }
-  return (((long long)id * p.Hkv + g) * p.page + t % p.page) * p.vecs + vec;
+// The page of row t of sequence b, or -1 for one that is not there.
+__device__ __forceinline__ int cache_page(const EvictParams& p, const int* table, int cols, int b,
+                                          int t) {
+  return __ldcg(table + (long long)b * cols + p.by_page.div(t));
+}
+__device__ __forceinline__ bool cache_page_ok(const EvictParams& p, int id) {
+  if (id >= 0 && id < p.num_pages) return true;
+  atomicExch(p.error_word, 1);   // ATTN_ERR_INVALID_ARG
+  return false;
+}
+// 16-byte piece `vec` of row t of head g, in page id.
+__device__ __forceinline__ long long cache_piece(const EvictParams& p, int id, int g, int t,
+                                                 int vec) {
+  return (((long long)id * p.Hkv + g) * p.page + p.by_page.mod(t)) * p.vecs + vec;
 }
 
 constexpr int kMoveThreads = 256;
 
 // K and V rows to other pages: row i of the output is row keep[i].  A thread
-// moves a 16-byte piece of K and V of U rows.
+// moves a 16-byte piece of K and V of U rows; each step's loads for all of them
+// go out together (keep and the target's page, the source's page, the rows).
 template <int U>
 __global__ void __launch_bounds__(kMoveThreads) attn_cache_move_sm103a(const EvictParams p) {
   griddep_wait();
   const int per_pass = kMoveThreads / p.vecs;
   const int vec = threadIdx.x % p.vecs, r = threadIdx.x / p.vecs;
   const int blocks = (p.budget + per_pass * U - 1) / (per_pass * U);
-  const int bg = blockIdx.x / blocks, blk = blockIdx.x - bg * blocks;
+  const int bg = blockIdx.x / blocks, i0 = (blockIdx.x - bg * blocks) * U * per_pass + r;
   const int b = bg / p.Hkv, g = bg - b * p.Hkv;
-  uint4 k[U], v[U];
-  int src[U];
+  int src[U], from[U], to[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int i = (blk * U + u) * per_pass + r;
+    const int i = i0 + u * per_pass;
     src[u] = i < p.budget ? __ldcg(p.keep + (size_t)bg * p.budget + i) : -1;
+    to[u] = i < p.cols_out * p.page ? cache_page(p, p.table_out, p.cols_out, b, i) : -1;
   }
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    from[u] = src[u] >= 0 ? cache_page(p, p.table, p.cols, b, src[u]) : 0;
+  uint4 k[U], v[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (src[u] < 0) continue;
-    const long long at = cache_piece(p, p.table, p.cols, b, g, src[u], vec);
-    if (at < 0) {
+    if (!cache_page_ok(p, from[u]) || !cache_page_ok(p, to[u])) {
       src[u] = -1;
       continue;
     }
-    k[u] = __ldcg(p.kpages + at);
-    v[u] = __ldcg(p.vpages + at);
+    const long long at = cache_piece(p, from[u], g, src[u], vec);
+    k[u] = __ldcs(p.kpages + at);
+    v[u] = __ldcs(p.vpages + at);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (src[u] < 0) continue;
-    const int i = (blk * U + u) * per_pass + r;
-    const long long at = cache_piece(p, p.table_out, p.cols_out, b, g, i, vec);
-    if (at < 0) continue;
+    const long long at = cache_piece(p, to[u], g, i0 + u * per_pass, vec);
     p.kpages[at] = k[u];
     p.vpages[at] = v[u];
   }
@@ -316,28 +346,27 @@ __global__ void __launch_bounds__(kMoveThreads)
 #pragma unroll 1
   for (int i0 = 0; i0 < p.budget; i0 += per_pass * U) {
     uint4 x[U];
-    int src[U];
+    int src[U], from[U], to[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * per_pass + r;
       src[u] = i < p.budget ? __ldcg(keep + i) : -1;
       if (src[u] == i) src[u] = -1;   // it is there already
+      to[u] = i < p.cols * p.page ? cache_page(p, p.table, p.cols, b, i) : -1;
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      from[u] = src[u] >= 0 ? cache_page(p, p.table, p.cols, b, src[u]) : 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (src[u] < 0) continue;
-      const long long at = cache_piece(p, p.table, p.cols, b, g, src[u], vec);
-      if (at < 0) src[u] = -1;
-      else x[u] = __ldcg(pool + at);
+      if (!cache_page_ok(p, from[u]) || !cache_page_ok(p, to[u])) src[u] = -1;
+      else x[u] = __ldcg(pool + cache_piece(p, from[u], g, src[u], vec));
     }
     __syncthreads();
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (src[u] < 0) continue;
-      const long long at =
-          cache_piece(p, p.table, p.cols, b, g, i0 + u * per_pass + r, vec);
-      if (at >= 0) pool[at] = x[u];
-    }
+    for (int u = 0; u < U; ++u)
+      if (src[u] >= 0) pool[cache_piece(p, to[u], g, i0 + u * per_pass + r, vec)] = x[u];
   }
 }
 
