@@ -106,20 +106,41 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 
 constexpr int kSelectThreads = 1024;
 constexpr int kSelectBins = 8192;
+constexpr int kSelectHeld = 45056;   // rows: 176 KiB beside the 32 KiB of counts
+
+// Four consecutive rows' ordered integers, from row i (a multiple of 4) on; rows
+// from `end` on are not read.
+__device__ __forceinline__ uint4 order_keys(const float* w, int i, int end, bool wide) {
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (wide && i + 4 <= end) {
+    x = __ldcs(reinterpret_cast<const float4*>(w + i));
+  } else {
+    if (i < end) x.x = w[i];
+    if (i + 1 < end) x.y = w[i + 1];
+    if (i + 2 < end) x.z = w[i + 2];
+    if (i + 3 < end) x.w = w[i + 3];
+  }
+  return make_uint4(order_key(x.x), order_key(x.y), order_key(x.z), order_key(x.w));
+}
+
 // Which rows stay.  One block per (sequence, K/V head): of the rows before the
 // last `recent`, the budget - recent with the largest weights, equal ones from
 // the lowest row on; and the last `recent`.  The smallest weight that stays is
 // found digit by digit (13, 10 and 9 bits of the ordered integer) from
-// histograms in shared memory; one more pass writes the rows' numbers and
-// weights in order.  In place, row i's weight moves to a place at or before i,
-// and a tile is read before anything of it is overwritten.
+// histograms in shared memory, ending as soon as a whole bin stays.  Then each
+// warp numbers the rows of its part of the sequence, and the kept rows' weights
+// are gathered.  In place, row i's weight comes from a row at or after i, and a
+// piece of the list is read before anything of it is written.
 //
-// The first digit's counts are what takes time: weights of one size fall into few
-// bins, whose atomics wait for one another.  So it is as long as the block's
-// scan allows; with 11 bits the selection took 29 us for 16 sequences of 16384 to
-// 32768 rows and 8 heads.
+// The weights are read once where a sequence fits in shared memory (HELD), with
+// all loads of a thread in flight together; a block per SM is bound by the latency
+// of what it does in turn, not by the bytes.  (With the weights read again for
+// every digit, and a block-wide count for every 4096 rows, 16 sequences of 16384 to
+// 32768 rows with 8 heads took 29 us.)
+template <bool HELD>
 __global__ void __launch_bounds__(kSelectThreads, 1) attn_cache_select_sm103a(const EvictParams p) {
-  __shared__ uint32_t hist[kSelectBins];
+  extern __shared__ uint4 held[];
+  __shared__ __align__(16) uint32_t hist[kSelectBins];
   __shared__ uint32_t warp_sum[32];
   __shared__ uint32_t sh_bin, sh_left, sh_all;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -145,9 +166,14 @@ __global__ void __launch_bounds__(kSelectThreads, 1) attn_cache_select_sm103a(co
   }
   if (tid == 0 && g == 0) p.newlens[b] = p.budget;
   const int old = n - p.recent;
+  const bool wide = (reinterpret_cast<uintptr_t>(w) & 15) == 0;   // 16-byte loads
   uint32_t left = (uint32_t)(p.budget - p.recent);   // rows still to be chosen
+  const bool choose = left > 0;
   uint32_t prefix = 0, known = 0;                    // digits found so far, and their mask
-  if (left > 0) {
+  // groups of four rows, kLoads of them per thread and round
+  constexpr int kLoads = 8;
+  const int groups = (old + 3) / 4;
+  if (choose) {
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 19 : pass == 1 ? 9 : 0;
@@ -155,28 +181,35 @@ __global__ void __launch_bounds__(kSelectThreads, 1) attn_cache_select_sm103a(co
       const int bins = (int)digit + 1, per = pass == 0 ? bins / kSelectThreads : 1;   // per thread
       for (int i = tid; i < bins; i += kSelectThreads) hist[i] = 0;
       __syncthreads();
-      constexpr int kLoads = 8;   // rows per thread and round: their loads are in flight together
-      for (int i0 = 0; i0 < old; i0 += kLoads * kSelectThreads) {
-        float x[kLoads];
+      for (int q0 = 0; q0 < groups; q0 += kLoads * kSelectThreads) {
+        uint4 key[kLoads];
 #pragma unroll
         for (int e = 0; e < kLoads; ++e) {
-          const int i = i0 + e * kSelectThreads + tid;
-          x[e] = i < old ? w[i] : 0.f;
+          const int q = q0 + e * kSelectThreads + tid;
+          if (q >= groups) continue;
+          key[e] = HELD && pass > 0 ? held[q] : order_keys(w, 4 * q, old, wide);
         }
 #pragma unroll
         for (int e = 0; e < kLoads; ++e) {
-          const uint32_t key = order_key(x[e]);
-          const bool in = i0 + e * kSelectThreads + tid < old && (key & known) == prefix;
-          const uint32_t bin = (key >> shift) & digit;
-          // a warp whose rows all fall into one bin adds them at once
-          const uint32_t who = __ballot_sync(0xffffffffu, in);
-          if (who == 0) continue;
-          const uint32_t first = __shfl_sync(0xffffffffu, bin, __ffs(who) - 1);
-          if (__ballot_sync(0xffffffffu, in && bin == first) == who) {
-            if (lane == 0) atomicAdd(&hist[first], (uint32_t)__popc(who));
-          } else if (in) {
-            atomicAdd(&hist[bin], 1u);
+          const int q = q0 + e * kSelectThreads + tid;
+          if (q >= groups) continue;
+          if (HELD && pass == 0) held[q] = key[e];
+          // (a run of equal bins is added at once: where many weights are equal, their
+          // additions wait for one another)
+          const uint32_t k4[4] = {key[e].x, key[e].y, key[e].z, key[e].w};
+          uint32_t run = 0, run_bin = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (4 * q + j >= old || (k4[j] & known) != prefix) continue;
+            const uint32_t bin = (k4[j] >> shift) & digit;
+            if (run > 0 && bin != run_bin) {
+              atomicAdd(&hist[run_bin], run);
+              run = 0;
+            }
+            run_bin = bin;
+            ++run;
           }
+          if (run > 0) atomicAdd(&hist[run_bin], run);
         }
       }
       __syncthreads();
@@ -184,7 +217,14 @@ __global__ void __launch_bounds__(kSelectThreads, 1) attn_cache_select_sm103a(co
       // `per` bins from bins - 1 - t * per down
       const int top = bins - 1 - tid * per;
       uint32_t mine = 0;
-      for (int j = 0; j < per; ++j) mine += top >= j ? hist[top - j] : 0u;
+      if (pass == 0) {
+        static_assert(kSelectBins == 8 * kSelectThreads, "eight bins per thread");
+        const uint4* at = reinterpret_cast<const uint4*>(hist + top - 7);
+        const uint4 x = at[0], y = at[1];
+        mine = x.x + x.y + x.z + x.w + y.x + y.y + y.z + y.w;
+      } else if (top >= 0) {
+        mine = hist[top];
+      }
       uint32_t upto = mine;
 #pragma unroll
       for (int d = 1; d < 32; d *= 2) {
@@ -213,52 +253,70 @@ __global__ void __launch_bounds__(kSelectThreads, 1) attn_cache_select_sm103a(co
   } else {
     prefix = 0xffffffffu;   // above every weight: none of the old rows stays
   }
-  // rows above `prefix` stay, and the first `left` of those equal to it; a warp
-  // takes 128 rows of a tile of 4096
-  constexpr int kPer = 4, kTileRows = kSelectThreads * kPer;
-  uint32_t base_gt = 0, base_eq = 0;
-#pragma unroll 1
-  for (int t0 = 0; t0 < n; t0 += kTileRows) {
-    float x[kPer];
-    uint32_t gt[kPer], eq[kPer], my_gt = 0, my_eq = 0;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      const int t = t0 + warp * 32 * kPer + e * 32 + lane;
-      x[e] = t < n ? w[t] : 0.f;
-    }
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      const int t = t0 + warp * 32 * kPer + e * 32 + lane;
-      const uint32_t key = order_key(x[e]);
-      gt[e] = __ballot_sync(0xffffffffu, t < n && (t >= old || key > prefix));
-      eq[e] = __ballot_sync(0xffffffffu, t < old && key == prefix);
-      my_gt += __popc(gt[e]);
-      my_eq += __popc(eq[e]);
-    }
-    // both counts are at most 4096: one scan for the two
-    __syncthreads();   // (the tile is read, and warp_sum free)
-    if (lane == 0) warp_sum[warp] = my_gt | (my_eq << 16);
-    __syncthreads();
-    const uint32_t all = warp_sum[lane];
-    const uint32_t sum = __reduce_add_sync(0xffffffffu, all);
-    const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? all : 0u);
-    uint32_t g0 = base_gt + (before & 0xffffu), e0 = base_eq + (before >> 16);
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      const int t = t0 + warp * 32 * kPer + e * 32 + lane;
-      const uint32_t below = (1u << lane) - 1u;
-      const uint32_t my_g = g0 + __popc(gt[e] & below), my_e = e0 + __popc(eq[e] & below);
-      const bool stays = ((gt[e] >> lane) & 1u) || (((eq[e] >> lane) & 1u) && my_e < left);
-      if (stays) {
-        const uint32_t to = my_g + min(my_e, left);
-        keep[to] = t;
-        w_out[to] = x[e];
+  // Rows above `prefix` stay, and the first `left` of those equal to it.  Thread t
+  // numbers rows [t * part, (t + 1) * part): it counts them, learns how many come
+  // before, and goes over them again.  (part / 4 is odd: 16-byte reads of
+  // neighbouring threads then fall into different banks.)
+  if (choose) {
+    int part = (old + 4 * kSelectThreads - 1) / (4 * kSelectThreads) * 4;
+    if (part % 8 == 0) part += 4;
+    const int first = min(old, tid * part), last = min(old, first + part);
+    auto each = [&](auto&& take) {   // take(row, ordered integer)
+      for (int t = first; t < last; t += 4) {
+        const uint4 k = HELD ? held[t / 4] : order_keys(w, t, old, wide);
+        take(t, k.x);
+        if (t + 1 < last) take(t + 1, k.y);
+        if (t + 2 < last) take(t + 2, k.z);
+        if (t + 3 < last) take(t + 3, k.w);
       }
-      g0 += __popc(gt[e]);
-      e0 += __popc(eq[e]);
+    };
+    __syncthreads();   // (the ordered integers are another thread's)
+    uint32_t gt = 0, eq = 0;
+    each([&](int, uint32_t key) {
+      gt += key > prefix ? 1u : 0u;
+      eq += key == prefix ? 1u : 0u;
+    });
+    // (a block holds at most 2^31 rows: one scan for each of the two counts)
+    const uint32_t my_gt = gt, my_eq = eq;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, gt, d), z = __shfl_up_sync(0xffffffffu, eq, d);
+      if (lane >= d) {
+        gt += y;
+        eq += z;
+      }
     }
-    base_gt += sum & 0xffffu;
-    base_eq += sum >> 16;
+    if (lane == 31) {
+      warp_sum[warp] = gt;
+      hist[warp] = eq;
+    }
+    __syncthreads();
+    gt += __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0u) - my_gt;
+    eq += __reduce_add_sync(0xffffffffu, lane < warp ? hist[lane] : 0u) - my_eq;
+    each([&](int t, uint32_t key) {
+      if (key > prefix || (key == prefix && eq < left)) keep[gt + min(eq, left)] = t;
+      gt += key > prefix ? 1u : 0u;
+      eq += key == prefix ? 1u : 0u;
+    });
+  }
+  for (int i = tid; i < p.recent; i += kSelectThreads) keep[p.budget - p.recent + i] = old + i;
+  __syncthreads();
+  // the kept rows' weights (the list was written by this block)
+  constexpr int kMoves = 4;
+  for (int i0 = 0; i0 < p.budget; i0 += kMoves * kSelectThreads) {
+    int t[kMoves];
+    float x[kMoves];
+#pragma unroll
+    for (int e = 0; e < kMoves; ++e) {
+      const int i = i0 + e * kSelectThreads + tid;
+      t[e] = i < p.budget ? keep[i] : -1;
+    }
+#pragma unroll
+    for (int e = 0; e < kMoves; ++e) x[e] = t[e] >= 0 ? w[t[e]] : 0.f;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kMoves; ++e)
+      if (t[e] >= 0) w_out[i0 + e * kSelectThreads + tid] = x[e];
   }
   __syncthreads();
   // rows that follow start from nothing
