@@ -176,7 +176,7 @@ struct KeyWeightsTile {
   int head, query;
   __device__ __forceinline__ KeyWeightsTile(const KeyWeightsParams& p, const KeyWeightsItem& it) {
     if (p.pad == 128) {
-      head = it.t0 > 0 ? it.t0 / it.n : 0;
+      head = it.t0 < it.n ? 0 : it.t0 / it.n;
       query = it.q0 + 128 * (it.t0 - head * it.n);
     } else {
       head = (128 / p.pad) * it.t0;
@@ -323,7 +323,7 @@ __device__ __forceinline__ void key_weights_lse(KeyWeightsSmem<DH>& sm, const Ke
       } while (it.k0 >= it.L);
       t = it.t0 + (int)((before ^ (uint32_t)group) & 1u);
       n = p.pad == 128 ? it.n : 1;
-      head = t > 0 ? t / n : 0;
+      head = t < n ? 0 : n == 1 ? t : t / n;
       part = t - head * n;
       base = p.lse + ((size_t)it.b * p.Hq + it.g * p.G) * p.S;
       if (it.t0 == it.t1 && t == it.t0) {   // no query sees its keys
@@ -378,7 +378,8 @@ __device__ __forceinline__ void key_weights_lse(KeyWeightsSmem<DH>& sm, const Ke
       if (lane == 0)
         sm.entry[group][l.i] =
             KeyWeightsEntry{flags[d], lo[d], hi[d], end[d], out[d], rows[d], cols[d]};
-      mbar_arrive(&sm.l_full[group][l.i]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.l_full[group][l.i]);
       l.step();
       if (flags[d] & kKwEnd) return;
       fetch(x[d], flags[d], lo[d], hi[d], end[d], cols[d], rows[d], out[d]);
@@ -444,16 +445,19 @@ __device__ __forceinline__ void key_weights_issuer(KeyWeightsSmem<DH>& sm,
       }
       tc_fence_after_sync();
       const uint64_t q = desc + (uint64_t)r.i * (Cfg::kTile >> 4);
-#pragma unroll
-      for (int kk = 0; kk < DH / 16; ++kk)
-        mma_bf16_ts_warp(tbase + 128u * s.i, tbase + Cfg::kColK + 8 * kk,
-                         q + (((kk / 4) * Cfg::kBox + (kk % 4) * 32) >> 4), idesc,
-                         kk > 0 ? 1u : 0u);
+      const uint32_t dS = tbase + 128u * s.i;
       // (a shared address of a cluster's CTA has its rank above the descriptor's bits)
       const uint64_t lse = plain | ((smem_u32(sm.nlse[group][group ? l1.i : l0.i]) >> 4) & 0x3FFFu);
-      mma_bf16_ts_warp(tbase + 128u * s.i, tbase + Cfg::kColOne, lse, idesc, 1u);
-      mma_commit_warp(&sm.s_full[s.i]);
-      mma_commit_warp(&sm.empty[r.i]);
+      if (elect_one_sync()) {
+#pragma unroll
+        for (int kk = 0; kk < DH / 16; ++kk)
+          mma_bf16_ts(dS, tbase + Cfg::kColK + 8 * kk,
+                      q + (((kk / 4) * Cfg::kBox + (kk % 4) * 32) >> 4), idesc, kk > 0 ? 1u : 0u);
+        mma_bf16_ts(dS, tbase + Cfg::kColOne, lse, idesc, 1u);
+        mma_commit(&sm.s_full[s.i]);
+        mma_commit(&sm.empty[r.i]);
+      }
+      __syncwarp();
       r.step();
       (group ? l1 : l0).step();
       group ^= 1u;
@@ -603,7 +607,7 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(&sm.empty[i], 1);
     }
     for (int i = 0; i < 2 * Cfg::kLse; ++i) {
-      mbar_init(&sm.l_full[0][i], 32);   // (both groups' rings lie in a row)
+      mbar_init(&sm.l_full[0][i], 1);    // (both groups' rings lie in a row)
       mbar_init(&sm.l_empty[0][i], 4);   // one arrival per summing warp of a group
     }
     for (int i = 0; i < Cfg::kBuffers; ++i) {
