@@ -659,6 +659,7 @@ extern "C" int attn_key_weights(const void* q, const void* k, const float* lse, 
   if (weights_stride < S) return ATTN_ERR_INVALID_ARG;
   float scale_log2 = 0.f;
   if (!resolve_scale(scale, Dh, &scale_log2)) return ATTN_ERR_INVALID_ARG;
+  if (scale_log2 < 1e-18f) return ATTN_ERR_INVALID_ARG;   // lse / scale has to stay finite
   if (B == 0 || S == 0) return ATTN_OK;
   if (!usable(q, 16) || !usable(k, 16) || !usable(lse, 4) || !usable(weights, 4) ||
       (seqlens && !usable(seqlens, 4)))
@@ -704,7 +705,7 @@ extern "C" int attn_cache_evict(void* kpages, void* vpages, float* weights, int 
   if (table_out == table && cols_out != cols) return ATTN_ERR_INVALID_ARG;
   if (weights_out == weights && weights_out_stride != weights_stride) return ATTN_ERR_INVALID_ARG;
   if ((long long)B * Hkv > 0xffffffLL ||
-      (long long)B * Hkv * (((long long)budget + 31) / 32 + 1) > 0x7fffffffLL)
+      (long long)B * Hkv * (((long long)budget + 15) / 16 + 1) > 0x7fffffffLL)
     return ATTN_ERR_INVALID_ARG;
   if (B == 0) return ATTN_OK;
   if (!usable(kpages, 16) || !usable(vpages, 16) || !usable(weights, 4) || !usable(table, 4) ||

@@ -42,8 +42,9 @@ __global__ void __launch_bounds__(kAppendThreads) attn_paged_append_sm103a(const
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const long long row = row0 + u * per_pass;   // (the number of rows is 32-bit)
-    const int bg = p.by_s.div(row < p.rows ? (int)row : 0);
-    i[u] = (int)row - bg * p.S;
+    const int at = row < p.rows ? (int)row : 0;
+    const int bg = p.by_s.div(at);
+    i[u] = at - bg * p.S;
     b[u] = p.by_heads.div(bg);
     g[u] = bg - b[u] * p.Hkv;
     n[u] = p.seqlens[b[u]];

@@ -335,7 +335,8 @@ int attn_decode_paged_workspace(int B, int Hq, int Hkv, int page, int cols, int 
  *            entries [0, seqlens[b]) are written, the others left alone
  *   queries  the last `queries` rows of each sequence vote (0 or more than
  *            there are: every row)
- *   causal, window, scale  as in attn_fwd_lse;  accumulate as above
+ *   causal, window, scale  as in attn_fwd_lse (a scale below 1e-18 is
+ *            ATTN_ERR_INVALID_ARG here);  accumulate as above
  * (With causal = 0 a padded prompt's lse has to be that of its real rows.)
  */
 int attn_key_weights(const void* q, const void* k, const float* lse, const int* seqlens,

@@ -366,6 +366,41 @@ def test_key_weights_of_a_whole_prompt_from_its_forward_pass():
     assert ((total / (Hq // Hkv * S) - 1).abs() <= 2 * (128 + 1) * 2.0 ** -23 * 20 + 2.0 ** -17).all()
 
 
+def test_key_weights_of_many_sequences():
+    # more sequences than a CTA keeps lengths of; most of them short or empty
+    B, Hq, Hkv, S, Dh = 300, 2, 1, 130, 64
+    lens = [(37 * b) % 131 for b in range(B)]
+    q, k, _ = inputs.prefill_inputs(B, Hq, Hkv, S, Dh, seed=9)
+    lse = torch.full((B, Hq, S), 5.0)
+    want, rtol = ref.key_weights(q, k, lse, lens)
+    w = torch.zeros(B, Hkv, S, device="cuda")
+    chs.attn_key_weights(*gpu(q, k, lse), w, torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    status_ok()
+    assert ((w.cpu().double() - want).abs() <= rtol * want).all()
+
+
+def test_key_weights_offsets_past_32_bits():
+    # queries of 2^31 elements: the last head's lie past a 32-bit offset
+    B, Hq, Hkv, S, Dh, nq = 2, 256, 2, 32768, 128, 16
+    q = torch.empty(B, Hq, S, Dh, dtype=torch.bfloat16, device="cuda")
+    assert q.numel() >= 2 ** 31
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    q[:, :, S - nq:] = torch.randn((B, Hq, nq, Dh), generator=gen, device="cuda").to(torch.bfloat16)
+    k = torch.randn((B, Hkv, S, Dh), generator=gen, device="cuda").to(torch.bfloat16)
+    lse = torch.full((B, Hq, S), 10.0, device="cuda")
+    w = torch.zeros(B, Hkv, S, device="cuda")
+    chs.attn_key_weights(q, k, lse, w, queries=nq)
+    status_ok()
+    i = torch.arange(S - nq, S, device="cuda")[:, None]
+    for g in range(Hkv):
+        want = torch.zeros(S, dtype=torch.float64, device="cuda")
+        for h in range(g * 128, g * 128 + 128):
+            p = torch.exp(q[1, h, S - nq:].double() @ k[1, g].double().t() * Dh ** -0.5 - 10)
+            want += torch.where(torch.arange(S, device="cuda") <= i, p, 0.0).sum(0)
+        rel = (Dh + 1) * 2.0 ** -23 * (6 * Dh ** 0.5 + 10) + 2.0 ** -18   # (as above)
+        assert ((w[1, g].double() - want).abs() <= rel * want).all()
+
+
 def test_key_weights_report_impossible_lengths():
     q, k, _ = gpu(*inputs.prefill_inputs(2, 2, 2, 140, 64, seed=1))
     lse = torch.zeros(2, 2, 140, device="cuda")
@@ -426,15 +461,18 @@ def test_evict_keeps_the_largest_weights(Hkv, Dh, page, cols, lens, budget, rece
         assert same_bits(dw, w)
 
 
-def test_evict_of_long_sequences_matches_a_sort():
-    # 70000 rows: several tiles; clustered values, so that every digit decides
-    n, budget, recent = 70001, 20000, 1000
+# rows that fit in a block's shared memory, and more; clustered values, so that
+# every digit decides, and equal ones
+@pytest.mark.parametrize("n,budget,recent,steps", [(70001, 20000, 1000, 4000), (45056, 9000, 0, 9),
+                                                   (45041, 45040, 7, 1), (60000, 1, 0, 2 ** 20)])
+def test_evict_of_long_sequences_matches_a_sort(n, budget, recent, steps):
     gen = torch.Generator(device="cuda").manual_seed(3)
-    w = 1.0 + torch.randint(0, 4000, (1, 2, 70016), generator=gen, device="cuda") * 2.0 ** -23
-    kp, vp = (torch.randn(4376, 2, 16, 64, generator=gen, device="cuda").to(torch.bfloat16)
+    pages = -(-n // 16)
+    w = 1.0 + torch.randint(0, steps, (1, 2, 16 * pages), generator=gen, device="cuda") * 2.0 ** -23
+    kp, vp = (torch.randn(pages, 2, 16, 64, generator=gen, device="cuda").to(torch.bfloat16)
               for _ in range(2))
     k0 = kp.clone()
-    table = torch.randperm(4376, generator=gen, device="cuda").to(torch.int32).view(1, 4376)
+    table = torch.randperm(pages, generator=gen, device="cuda").to(torch.int32).view(1, pages)
     sl = torch.tensor([n], dtype=torch.int32, device="cuda")
     w0 = w.clone()
     newlens, keep = chs.attn_cache_evict(kp, vp, w, table, sl, budget, recent)

@@ -124,6 +124,7 @@ def key_weights(lib, ptrs=None, stride=40, B=2, Hq=4, Hkv=2, S=40, Dh=128, queri
     (dict(B=-1), INVALID), (dict(S=-1), INVALID), (dict(Hq=3), INVALID), (dict(Hkv=0), INVALID),
     (dict(Dh=96), UNSUPPORTED), (dict(causal=2), INVALID), (dict(causal=0, window=3), INVALID),
     (dict(stride=39), INVALID), (dict(acc=-1), INVALID), (dict(scale=-1.0), INVALID),
+    (dict(scale=1e-19), INVALID),   # lse / scale would not stay finite
     (dict(B=0), OK), (dict(S=0), OK),
 ])
 def test_key_weights_argument_checks(lib, change, code):
