@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(288, 1)
 // them, launched when weights are asked for, each write kPagedWeightKeys of
 // the weights of one (sequence, K/V head): sum over the group's heads of
 // 2^(s - M) / l, from the scores that the first kernel left.
-constexpr int kPagedJoinThreads = 128;
+constexpr int kPagedJoinThreads = 256;
 constexpr int kPagedWeightKeys = 4 * kPagedJoinThreads;
 
 template <int DH, int REP>
@@ -735,44 +735,61 @@ __global__ void __launch_bounds__(kPagedJoinThreads)
     }
     const int n = (ctas.y - ctas.x + 1) * REP;
     const size_t at0 = (size_t)(unit + ctas.x) * REP * part_rows + (hg - 128 * rb);
-    constexpr int kCols = DH > kPagedJoinThreads ? DH / kPagedJoinThreads : 1;
-    const bool mine = tid < DH;
-    constexpr int kG = 8;   // partials per round: their loads are all in flight together
-    float M = -INFINITY, l = 0.f, o[kCols];
-#pragma unroll
-    for (int c = 0; c < kCols; ++c) o[c] = 0.f;
-    for (int i0 = 0; i0 < n; i0 += kG) {
-      float mv[kG], lv[kG], ov[kG][kCols];
+    // DH threads hold a row, a column each; the block's groups of them take every
+    // kGroups-th partial and are joined in turn
+    constexpr int kGroups = kPagedJoinThreads / DH;
+    const int group = tid / DH, d = tid % DH;
+    // partials per round, their loads in flight together (at Dh = 256, 40 partials: 8
+    // 22.7 us, 4 23.1, 16 26.0 for the whole step)
+    constexpr int kG = 8;
+    float M = -INFINITY, l = 0.f, o = 0.f;
+    for (int i0 = group; i0 < n; i0 += kG * kGroups) {
+      float mv[kG], lv[kG], ov[kG];
 #pragma unroll
       for (int e = 0; e < kG; ++e) {
-        const bool in = i0 + e < n;
-        const size_t at = at0 + (size_t)(i0 + e) * part_rows;
-        mv[e] = in ? __ldcg(p.m_part + at) : -INFINITY;
-        lv[e] = in ? __ldcg(p.l_part + at) : 0.f;
-#pragma unroll
-        for (int c = 0; c < kCols; ++c)
-          ov[e][c] = in && mine ? __ldcg(p.o_part + at * DH + tid + c * kPagedJoinThreads) : 0.f;
+        // (past the end the last one again, with the weight 0: a load under a
+        // condition is not issued together with the others)
+        const int i = i0 + e * kGroups;
+        const size_t at = at0 + (size_t)min(i, n - 1) * part_rows;
+        mv[e] = __ldcg(p.m_part + at);
+        lv[e] = __ldcg(p.l_part + at);
+        ov[e] = __ldcg(p.o_part + at * DH + d);
+        if (i >= n) mv[e] = -INFINITY;
       }
       float Mg = M;
 #pragma unroll
       for (int e = 0; e < kG; ++e) Mg = fmaxf(Mg, mv[e]);
       const float f0 = (M == -INFINITY) ? 0.f : ex2_approx(M - Mg);
       l *= f0;
-#pragma unroll
-      for (int c = 0; c < kCols; ++c) o[c] *= f0;
+      o *= f0;
 #pragma unroll
       for (int e = 0; e < kG; ++e) {
         const float f = (mv[e] == -INFINITY) ? 0.f : ex2_approx(mv[e] - Mg);
         l = fmaf(f, lv[e], l);
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) o[c] = fmaf(f, ov[e][c], o[c]);
+        o = fmaf(f, ov[e], o);
       }
       M = Mg;
     }
-    if (mine)
+    if constexpr (kGroups > 1) {
+      __shared__ float sh_o[kGroups][DH], sh_M[kGroups], sh_l[kGroups];
+      sh_o[group][d] = o;
+      if (d == 0) {
+        sh_M[group] = M;
+        sh_l[group] = l;
+      }
+      __syncthreads();
+      if (group > 0) return;
 #pragma unroll
-      for (int c = 0; c < kCols; ++c)
-        p.o[(size_t)bh * DH + tid + c * kPagedJoinThreads] = __float2bfloat16(o[c] / l);
+      for (int k = 1; k < kGroups; ++k) M = fmaxf(M, sh_M[k]);
+      l = o = 0.f;
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) {
+        const float f = (sh_M[k] == -INFINITY) ? 0.f : ex2_approx(sh_M[k] - M);
+        l = fmaf(f, sh_l[k], l);
+        o = fmaf(f, sh_o[k][d], o);
+      }
+    }
+    p.o[(size_t)bh * DH + d] = __float2bfloat16(o / l);
     return;
   }
   // weights
@@ -821,6 +838,7 @@ __global__ void __launch_bounds__(kPagedJoinThreads)
                          k0 + 4 * tid;
       // (a score row is whole tiles long: the last keys of the chunk may lie past it)
       if (k0 + 4 * tid < seq.L)
+#pragma unroll 4
         for (int i = 0; i < nh; ++i) {
           const float4 x = __ldcg(reinterpret_cast<const float4*>(src + (size_t)i * p.score_stride));
           const float M = sh_m[i], f = sh_f[i];
