@@ -25,9 +25,9 @@ cudaError_t launch_paged_append(const void* k, const void* v, void* kpages, void
   prm.num_pages = cache.num_pages;
   prm.page = cache.page;
   prm.cols = cache.cols;
-  prm.by_s = make_fast_div((uint32_t)S);
-  prm.by_heads = make_fast_div((uint32_t)Hkv);
-  prm.by_page = make_fast_div((uint32_t)cache.page);
+  prm.by_s = make_fixed_div((uint32_t)S);
+  prm.by_heads = make_fixed_div((uint32_t)Hkv);
+  prm.by_page = make_fixed_div((uint32_t)cache.page);
   prm.error_word = dev.error_word;
   const int per_pass = kAppendThreads / prm.vecs;
   constexpr int U = 4;
@@ -98,8 +98,8 @@ cudaError_t launch_key_weights(const void* q, const void* k, const float* lse, c
   prm.accumulate = accumulate;
   prm.items = (S + 127) / 128 * B * Hkv;
   prm.pad = pad;
-  prm.by_heads = make_fast_div((uint32_t)Hkv);
-  prm.by_batch = make_fast_div((uint32_t)(B * Hkv));
+  prm.by_heads = make_fixed_div((uint32_t)Hkv);
+  prm.by_batch = make_fixed_div((uint32_t)(B * Hkv));
   // a cluster per item where that fills the SMs no more than once, and leaves
   // each CTA a tile
   const long long tiles = pad < 128 ? (prm.G * pad + 127) / 128
@@ -152,7 +152,7 @@ cudaError_t launch_cache_evict(void* kpages, void* vpages, const int* table, con
   prm.budget = budget;
   prm.recent = recent;
   prm.error_word = dev.error_word;
-  prm.by_page = make_fast_div((uint32_t)cache.page);
+  prm.by_page = make_fixed_div((uint32_t)cache.page);
   const long long rows = (long long)cache.cols * cache.page;
   cudaError_t e;
   if (rows <= kSelectHeld) {

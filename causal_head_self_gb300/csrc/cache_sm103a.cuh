@@ -5,7 +5,7 @@
 
 #include <cstdint>
 
-#include "fast_div.h"
+#include "fixed_div.h"
 #include "sm103a_ptx.cuh"
 
 namespace chs {
@@ -21,7 +21,7 @@ struct AppendParams {
   long long rows;        // B * Hkv * S
   int Hkv, S, vecs;      // vecs: 16-byte pieces per row
   int num_pages, page, cols;
-  FastDiv by_s, by_heads, by_page;
+  FixedDiv by_s, by_heads, by_page;
   int* error_word;
 };
 
@@ -93,7 +93,7 @@ struct EvictParams {
   int* keep;              // [B, Hkv, budget]
   int B, Hkv, vecs;
   int num_pages, page, cols, cols_out, stride, stride_out, budget, recent;
-  FastDiv by_page;
+  FixedDiv by_page;
   int* error_word;
 };
 

@@ -46,7 +46,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
-#include "fast_div.h"
+#include "fixed_div.h"
 #include "sm103a_ptx.cuh"
 
 namespace chs {
@@ -55,7 +55,7 @@ struct KeyWeightsParams {
   int B, Hq, Hkv, G, S;
   int causal, window, queries, accumulate;
   int items;             // key blocks * B * Hkv
-  FastDiv by_heads, by_batch;   // by Hkv, by B * Hkv
+  FixedDiv by_heads, by_batch;   // by Hkv, by B * Hkv
   int pad;               // columns of a tile per head: 128, or less with few voting queries
   int split, split_log2; // CTAs per item, a power of two
   float scale_log2;

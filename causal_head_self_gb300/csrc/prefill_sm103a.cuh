@@ -42,10 +42,22 @@
 // and fed to the P.V MMA straight from TMEM.
 #pragma once
 
-#include "fast_div.h"
 #include "sm103a_ptx.cuh"
 
 namespace chs {
+
+// Exact division of a non-negative int n < 2^31 by a fixed divisor d >= 1:
+// n / d == (n * m) >> (31 + l) with l = ceil(log2 d) and m = ceil(2^(31+l) / d)
+// (the rounding error n*(m*d - 2^(31+l)) / (d * 2^(31+l)) stays below 1/d).
+// The multiplier is made on the host; the device pays one wide multiply
+// instead of a division sequence.
+struct FastDiv {
+  uint32_t m, shift, d;
+  __device__ __forceinline__ int div(int n) const {
+    return (int)(((uint64_t)(uint32_t)n * m) >> shift);
+  }
+  __device__ __forceinline__ int mod(int n) const { return n - div(n) * (int)d; }
+};
 
 struct PrefillParams {
   int B, Hq, Hkv;

@@ -75,6 +75,28 @@ WORKLOADS = {
     # the same decode step for 4 sequences (0.5 GB of cache: a profiler-sized case)
     "decode_gqa_b4_h32kv8_t32768_d128": dict(kind="decode", B=4, Hq=32, Hkv=8, Tmax=32768,
                                              Dh=128, lmin=16384, lmax=32768, window=0, seed=5),
+    # the same decode steps over a paged cache (pages of 64 and of 16 rows), the
+    # second with the step's attention weights added up
+    "paged_decode_gqa_b16_h32kv8_t32768_d128": dict(kind="paged", B=16, Hq=32, Hkv=8, Tmax=32768,
+                                                    page=64, Dh=128, lmin=16384, lmax=32768,
+                                                    window=0, weights=False, seed=15),
+    "paged_decode_weights_gqa_b4_h32kv8_t32768_d128": dict(kind="paged", B=4, Hq=32, Hkv=8,
+                                                           Tmax=32768, page=16, Dh=128, lmin=16384,
+                                                           lmax=32768, window=0, weights=True,
+                                                           seed=16),
+    # the weights that a prompt's keys received: from every query, and from the last 64
+    "key_weights_gqa_b1_h32kv8_s8192_d128": dict(kind="key_weights", B=1, Hq=32, Hkv=8, S=8192,
+                                                 Dh=128, queries=0, seed=17),
+    "key_weights_gqa_b4_h32kv8_s32768_d64_last64": dict(kind="key_weights", B=4, Hq=32, Hkv=8,
+                                                        S=32768, Dh=64, queries=64, seed=18),
+    # the key weights of 16 query heads at S=4096 (a profiler-sized case)
+    "key_weights_gqa_b1_h16kv8_s4096_d128": dict(kind="key_weights", B=1, Hq=16, Hkv=8, S=4096,
+                                                 Dh=128, queries=0, seed=17),
+    # 16 sequences of a paged cache cut back to 4096 keys each, and 4 of them
+    "evict_kv8_b16_t32768_d128": dict(kind="evict", B=16, Hkv=8, Tmax=32768, page=64, Dh=128,
+                                      lmin=16384, lmax=32768, budget=4096, recent=512, seed=19),
+    "evict_kv8_b4_t32768_d128": dict(kind="evict", B=4, Hkv=8, Tmax=32768, page=64, Dh=128,
+                                     lmin=16384, lmax=32768, budget=4096, recent=512, seed=19),
 }
 
 
@@ -102,6 +124,19 @@ def device_normal_bf16(shape, seed, device):
             out[i, j] = torch.randn(tuple(shape[2:]), generator=gen, device=device,
                                     dtype=torch.float32).to(torch.bfloat16)
     return out
+
+
+def paged_inputs(B, Hkv, Tmax, Dh, page, lmin, lmax, seed, device, spare=0):
+    """A paged cache on `device`: pools [P, Hkv, page, Dh], a table [B, Tmax / page]
+    of pages in random order, `spare` further pages per sequence [B, spare], and
+    the lengths."""
+    cols = (Tmax + page - 1) // page
+    shape = (B * (cols + spare), Hkv, page, Dh)
+    kp, vp = device_normal_bf16(shape, seed, device), device_normal_bf16(shape, seed + 1, device)
+    gen = torch.Generator(device="cpu").manual_seed(int(seed))
+    order = torch.randperm(shape[0], generator=gen).to(torch.int32).to(device)
+    lens = torch.randint(int(lmin), int(lmax) + 1, (B,), generator=gen).to(torch.int32).to(device)
+    return kp, vp, order[:B * cols].view(B, cols), order[B * cols:].view(B, spare), lens
 
 
 def grad_inputs(shape, seed):

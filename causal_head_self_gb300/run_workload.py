@@ -44,6 +44,29 @@ def main(argv=None):
             w["B"], w["Hq"], w["Hkv"], w["Tmax"], w["Dh"], w["lmin"], w["lmax"], w["seed"]))
         for _ in range(args.iters):
             chs.attn_decode_ring(q, kc, vc, sl, window=w["window"])
+    elif w["kind"] == "paged":
+        kp, vp, table, _, sl = inputs.paged_inputs(w["B"], w["Hkv"], w["Tmax"], w["Dh"], w["page"],
+                                                   w["lmin"], w["lmax"], w["seed"], dev)
+        q = inputs.device_normal_bf16((w["B"], w["Hq"], 1, w["Dh"]), w["seed"] + 2, dev)
+        weights = torch.zeros((w["B"], w["Hkv"], w["Tmax"]), device=dev) if w["weights"] else None
+        for _ in range(args.iters):
+            chs.attn_decode_paged(q, kp, vp, table, sl, window=w["window"], weights=weights)
+    elif w["kind"] == "key_weights":
+        q, k, v = (inputs.device_normal_bf16((w["B"], h, w["S"], w["Dh"]), w["seed"] + i, dev)
+                   for i, h in enumerate((w["Hq"], w["Hkv"], w["Hkv"])))
+        _, lse = chs.attn_fwd_lse(q, k, v)
+        weights = torch.zeros((w["B"], w["Hkv"], w["S"]), device=dev)
+        for _ in range(args.iters):
+            chs.attn_key_weights(q, k, lse, weights, queries=w["queries"])
+    elif w["kind"] == "evict":
+        spare = (w["budget"] + w["page"] - 1) // w["page"]
+        kp, vp, table, to, sl = inputs.paged_inputs(w["B"], w["Hkv"], w["Tmax"], w["Dh"], w["page"],
+                                                    w["lmin"], w["lmax"], w["seed"], dev, spare)
+        weights = torch.rand((w["B"], w["Hkv"], w["Tmax"]), device=dev)
+        kept = torch.zeros_like(weights)
+        for _ in range(args.iters):
+            chs.attn_cache_evict(kp, vp, weights, table, sl, w["budget"], w["recent"],
+                                 table_out=to, weights_out=kept)
     else:
         q, kc, vc, sl = (x.to(dev) for x in inputs.workload_inputs(args.workload))
         o = torch.empty_like(q)
