@@ -23,7 +23,8 @@ SOURCES = ["attn_api.cu", "prefill_sm103a.cu", "decode_sm103a.cu", "backward_sm1
            "decode_paged_sm103a.cu", "cache_sm103a.cu"]
 HEADERS = ["sm103a_ptx.cuh", "prefill_sm103a.cuh", "prefill_k64_sm103a.cuh", "decode_sm103a.cuh",
            "decode_tc_sm103a.cuh", "backward_sm103a.cuh", "backward256_sm103a.cuh",
-           "decode_paged_sm103a.cuh", "key_weights_sm103a.cuh", "cache_sm103a.cuh", "fixed_div.h",
+           "decode_paged_sm103a.cuh", "key_weights_sm103a.cuh",
+           "key_weights_few_sm103a.cuh", "cache_sm103a.cuh", "fixed_div.h",
            "launch.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]

@@ -665,7 +665,7 @@ extern "C" int attn_key_weights(const void* q, const void* k, const float* lse, 
       (seqlens && !usable(seqlens, 4)))
     return ATTN_ERR_INVALID_ARG;
   const long long key_blocks = ((long long)S + 127) / 128;
-  if (key_blocks * B * Hkv > 0x7fffffffLL || (long long)S > 0x7fffffffLL - 1024 ||
+  if ((key_blocks + 1) * B * Hkv > 0x7fffffffLL - 1024 || (long long)S > 0x7fffffffLL - 1024 ||
       key_blocks * (Hq / Hkv) > 0x7fffffffLL || (long long)B * Hq > 0x7fffffffLL)
     return ATTN_ERR_INVALID_ARG;
   const size_t qb = (size_t)B * Hq * S * Dh * 2, kb = (size_t)B * Hkv * S * Dh * 2;

@@ -1,6 +1,7 @@
 // cache_sm103a.cu -- host launchers of the paged cache's kernels: append, key
 // weights of a prompt, eviction.
 #include "cache_sm103a.cuh"
+#include "key_weights_few_sm103a.cuh"
 #include "key_weights_sm103a.cuh"
 #include "launch.h"
 
@@ -73,14 +74,64 @@ static cudaError_t launch_key_weights_dh(const CUtensorMap& mq, const CUtensorMa
   return cudaLaunchKernelEx(&cfg, attn_key_weights_sm103a<DH>, mq, mk, prm);
 }
 
+template <int DH>
+static cudaError_t launch_key_few_dh(const CUtensorMap& mq, const CUtensorMap& mk,
+                                     const KeyFewParams& prm, const DeviceInfo& dev,
+                                     cudaStream_t stream) {
+  constexpr size_t smem = key_few_smem_bytes<DH>();
+  static_assert(smem <= 232448, "shared memory budget of one sm_103a CTA");
+  static std::atomic<int> configured[kMaxDevices];
+  cudaError_t e = configure_once(configured, dev.device, [] {
+    return cudaFuncSetAttribute(attn_key_weights_few_sm103a<DH>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  });
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attn_key_weights_few_sm103a<DH>, dim3(prm.ctas),
+                    dim3(KeyFewCfg<DH>::kThreads), smem, stream, mq, mk, prm);
+}
+
 cudaError_t launch_key_weights(const void* q, const void* k, const float* lse, const int* seqlens,
                                float* weights, int stride, int B, int Hq, int Hkv, int S, int Dh,
                                int causal, int window, int queries, int accumulate,
                                float scale_log2, const DeviceInfo& dev, cudaStream_t stream) {
-  // with up to 64 voting queries a tile holds those of several heads
+  // rows per head in a tile: with up to 64 voting queries it holds several heads'
   int pad = 128;
   if (queries > 0)
     while (pad > 16 && pad / 2 >= queries) pad /= 2;
+  const double per_lse = -1.4426950408889634 / (double)scale_log2;   // -log2(e) / scale_log2
+  const int G = Hq / Hkv, most = Dh == 256 ? KeyFewCfg<256>::kCols : KeyFewCfg<128>::kCols;
+  // The whole group's voting queries in one tile (and no window, which would leave
+  // most blocks of keys without any): the queries stay, the keys pass by.
+  if (queries > 0 && queries <= 128 && window == 0 && (long long)G * pad <= most) {
+    CUtensorMap mq, mk;
+    if (!encode_bf16_map(&mq, q, Dh, S, (long long)B * Hq, pad) ||
+        !encode_bf16_rows_map(&mk, k, Dh, S, (long long)B * Hkv, 128))
+      return cudaErrorInvalidValue;
+    KeyFewParams prm;
+    prm.B = B;
+    prm.Hq = Hq;
+    prm.Hkv = Hkv;
+    prm.G = G;
+    prm.S = S;
+    prm.causal = causal;
+    prm.queries = queries;
+    prm.accumulate = accumulate;
+    prm.pad = pad;
+    prm.cols = (G * pad + 31) / 32 * 32;
+    const long long places = ((long long)(S + 127) / 128 + 1) * B * Hkv;
+    prm.ctas = places < dev.num_sms ? (int)places : dev.num_sms;
+    prm.scale_log2 = scale_log2;
+    prm.lse_hi = (float)per_lse;
+    prm.lse_lo = (float)(per_lse - (double)prm.lse_hi);
+    prm.lse = lse;
+    prm.seqlens = seqlens;
+    prm.weights = weights;
+    prm.stride = stride;
+    prm.error_word = dev.error_word;
+    return Dh == 256   ? launch_key_few_dh<256>(mq, mk, prm, dev, stream)
+           : Dh == 128 ? launch_key_few_dh<128>(mq, mk, prm, dev, stream)
+                       : launch_key_few_dh<64>(mq, mk, prm, dev, stream);
+  }
   CUtensorMap mq, mk;
   if (!(pad == 128 ? encode_bf16_rows_map(&mq, q, Dh, S, (long long)B * Hq, 128)
                    : encode_bf16_map(&mq, q, Dh, S, (long long)B * Hq, pad)) ||
@@ -111,7 +162,6 @@ cudaError_t launch_key_weights(const void* q, const void* k, const float* lse, c
     ++prm.split_log2;
   }
   prm.scale_log2 = scale_log2;
-  const double per_lse = -1.4426950408889634 / (double)scale_log2;   // -log2(e) / scale_log2
   prm.lse_hi = (float)per_lse;
   prm.lse_lo = (float)(per_lse - (double)prm.lse_hi);
   prm.lse = lse;

@@ -280,6 +280,13 @@ KEY_WEIGHTS = [
     (12, 1, 300, 128, [300, 130], 40, True, 0),           # several heads per tile, the last not full
     (5, 1, 300, 256, [300, 299], 64, True, 70),
     (3, 3, 500, 64, [500, 3], 5, True, 0),
+    (8, 2, 400, 64, [400, 0, 64, 63, 129], 64, True, 0),  # one tile of 256 voting rows
+    (8, 2, 400, 128, [400, 65, 1], 50, True, 0),          # ... with rows that pad each head
+    (4, 2, 700, 64, [700, 128, 127], 128, True, 0),
+    (6, 2, 300, 128, [300, 200], 16, False, 0),           # 96 rows: one and a half pieces
+    (8, 1, 300, 256, [300, 131], 16, True, 0),            # 128 rows, the most at head size 256
+    (9, 1, 300, 256, [300, 131], 16, True, 0),            # one head too many for that
+    (2, 1, 300, 64, [300, 290], 129, True, 0),
 ]
 
 
@@ -323,6 +330,9 @@ def test_key_weights_match_the_definition(Hq, Hkv, S, Dh, lens, nq, causal, wind
     (8, 32, 32, 1030, 128, 33, 0),
     (1, 8, 8, 2000, 128, 0, 0),          # a cluster of two per item
     (1, 8, 1, 4000, 64, 0, 0),
+    (6, 32, 8, 5000, 64, 64, 0),         # queries that stay: shares of several units
+    (3, 16, 8, 3000, 256, 60, 0),
+    (7, 8, 8, 1024, 128, 7, 0),
 ])
 def test_key_weights_of_many_tiles(B, Hq, Hkv, S, Dh, nq, window):
     gen = torch.Generator(device="cuda").manual_seed(S)
@@ -373,8 +383,14 @@ def test_key_weights_of_many_sequences():
     q, k, _ = inputs.prefill_inputs(B, Hq, Hkv, S, Dh, seed=9)
     lse = torch.full((B, Hq, S), 5.0)
     want, rtol = ref.key_weights(q, k, lse, lens)
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
     w = torch.zeros(B, Hkv, S, device="cuda")
-    chs.attn_key_weights(*gpu(q, k, lse), w, torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    chs.attn_key_weights(*gpu(q, k, lse), w, sl)
+    status_ok()
+    assert ((w.cpu().double() - want).abs() <= rtol * want).all()
+    want, rtol = ref.key_weights(q, k, lse, lens, queries=9)
+    w.zero_()
+    chs.attn_key_weights(*gpu(q, k, lse), w, sl, queries=9)
     status_ok()
     assert ((w.cpu().double() - want).abs() <= rtol * want).all()
 
