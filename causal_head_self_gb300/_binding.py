@@ -357,12 +357,22 @@ def _check_current(device):
 
 
 def _shape(name, t, ndim):
-    """The shape of a tensor of ndim axes."""
+    """The shape of a tensor of ndim axes (each of them a 32-bit int of the library's)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} axes")
+    if max(t.shape) > 0x7fffffff:
+        raise ValueError(f"{name} must have less than 2^31 entries along each axis")
     return t.shape
+
+
+def _int32(name, x):
+    """An int that the library takes: a larger one would lose its upper bits."""
+    x = int(x)
+    if not -0x80000000 <= x <= 0x7fffffff:
+        raise ValueError(f"{name} must fit in 32 bits")
+    return x
 
 
 def _check_pools(kpages, vpages, table, seqlens):
@@ -439,6 +449,7 @@ def attn_decode_paged(q, kpages, vpages, table, seqlens, o=None, *, window=0, sc
     its query heads, added to what is there or, with accumulate=False, in its
     place.  workspace: a uint8 tensor of attn_decode_paged_workspace() bytes
     (None: allocated here by torch, on the call's stream).  Returns o."""
+    window = _int32("window", window)
     B, Hkv, P, page, cols, Dh, device = _check_pools(kpages, vpages, table, seqlens)
     Hq = _shape("q", q, 4)[1]
     _check("q", q, torch.bfloat16, (B, Hq, 1, Dh), device)
@@ -459,7 +470,7 @@ def attn_decode_paged(q, kpages, vpages, table, seqlens, o=None, *, window=0, sc
                                   table.data_ptr(), seqlens.data_ptr(), o.data_ptr(),
                                   None if weights is None else weights.data_ptr(), stride,
                                   int(bool(accumulate)), workspace.data_ptr(), workspace.numel(),
-                                  B, Hq, Hkv, P, page, cols, Dh, int(window), float(scale),
+                                  B, Hq, Hkv, P, page, cols, Dh, window, float(scale),
                                   _stream_handle(stream))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_decode_paged")
@@ -474,6 +485,7 @@ def attn_key_weights(q, k, lse, weights, seqlens=None, *, queries=0, causal=True
     accumulate=False.  q [B,Hq,S,Dh], k [B,Hkv,S,Dh] and lse [B,Hq,S] as
     attn_fwd_lse took and returned them; seqlens [B] int32: the real rows of a
     padded prompt.  Returns weights."""
+    queries, window = _int32("queries", queries), _int32("window", window)
     B, Hq, S, Dh = shape = _shape("q", q, 4)
     Hkv = _shape("k", k, 4)[1]
     device = q.get_device()
@@ -486,8 +498,8 @@ def attn_key_weights(q, k, lse, weights, seqlens=None, *, queries=0, causal=True
         _check("seqlens", seqlens, torch.int32, (B,), device)
     rc = load().attn_key_weights(q.data_ptr(), k.data_ptr(), lse.data_ptr(),
                                  None if seqlens is None else seqlens.data_ptr(),
-                                 weights.data_ptr(), stride, B, Hq, Hkv, S, Dh, int(queries),
-                                 int(bool(causal)), int(window), int(bool(accumulate)),
+                                 weights.data_ptr(), stride, B, Hq, Hkv, S, Dh, queries,
+                                 int(bool(causal)), window, int(bool(accumulate)),
                                  float(scale), _stream_handle(stream))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_key_weights")
@@ -502,9 +514,9 @@ def attn_cache_evict(kpages, vpages, weights, table, seqlens, budget, recent=0, 
     table_out [B,cols_out] int32 (None: in place), their weights to
     weights_out (None: in place).  Returns (newlens [B], keep [B,Hkv,budget]):
     the new lengths, and each kept row's former number (then -1)."""
+    budget, recent = _int32("budget", budget), _int32("recent", recent)
     B, Hkv, P, page, cols, Dh, device = _check_pools(kpages, vpages, table, seqlens)
     stride = _rows_of("weights", weights, B, Hkv, device)
-    budget, recent = int(budget), int(recent)
     cols_out, stride_out = cols, stride
     if table_out is not None:
         cols_out = _shape("table_out", table_out, 2)[1]

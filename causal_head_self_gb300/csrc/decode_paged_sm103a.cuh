@@ -243,8 +243,9 @@ __device__ __forceinline__ void mbar_wait_drain_paged(uint64_t* bar, uint32_t pa
   }
 }
 
-// Loading warps: two load Q and K, two V, each (`part`) every other box (64 columns of box_rows rows; at most 32 per tile: 128 rows / 8 x 2, 64
-// rows / 8 x 4), one lane per box.  A warp takes about 90 cycles to issue one
+// Loading warps: two load Q and K, two V, each (`part`) every other box (64
+// columns of box_rows rows; at most 32 per tile: 128 rows / 8 x 2, 64 rows / 8 x
+// 4), one lane per box.  A warp takes about 90 cycles to issue one
 // copy, so at a page of 16 rows one warp alone is slower than the memory:
 // B = 8, 32 heads of 64, 4096 keys ran at 4470 GB/s with one loading warp
 // (page 8: 3041).
@@ -558,8 +559,8 @@ __device__ __forceinline__ void decode_paged_softmax(DecodePagedSmem<DH>& sm,
       const float msub = (m_use == -INFINITY) ? 0.f : m_use;
       const float2 scale2 = make_float2(sl2, sl2), neg_m2 = make_float2(-msub, -msub);
       float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      // P in bf16 (the tensor core's operand type; a rounding of 2^-9 relative
-      // per weight, the sum l is taken before it) over the first kKeys / 2
+      // P in bf16 (the tensor core's operand type; a rounding of 2^-8 relative
+      // per weight at most, the sum l is taken before it) over the first kKeys / 2
       // columns of S, zero at the keys of the other quarters.  Those columns
       // hold scores of this warp's rows only, which are all read by now.
       if constexpr (REP == 4) {

@@ -308,6 +308,8 @@ int attn_paged_append(const void* k, const void* v, void* kpages, void* vpages, 
  *            kept between calls; calls that may overlap on the GPU need one
  *            each.
  * Any Hq / Hkv runs on the tensor cores.  The same inputs give the same bits.
+ * An infinity in a visible V row can make that column of the output NaN (a key
+ * may also meet weights of exactly 0 in the tensor-core product).
  */
 int attn_decode_paged(const void* q, const void* kpages, const void* vpages, const int* table,
                       const int* seqlens, void* o, float* weights, int weights_stride,

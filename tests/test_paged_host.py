@@ -193,6 +193,22 @@ def test_the_binding_refuses_cpu_tensors_and_wrong_types(lib):
             call()
 
 
+def test_the_binding_refuses_what_32_bits_cannot_hold():
+    # (2^32 + 5 would reach the library as 5)
+    kp, vp, table, sl = ref.make_cache([5, 9], 2, 64, 8, 2, seed=0)
+    q, w, big = torch.zeros(2, 4, 1, 64, dtype=torch.bfloat16), torch.zeros(2, 2, 16), 2**32 + 5
+    wide = torch.zeros(1, dtype=torch.int32).expand(2, big)
+    for call in (lambda: chs.attn_decode_paged(q, kp, vp, table, sl, window=big),
+                 lambda: chs.attn_decode_paged(q, kp, vp, wide, sl),
+                 lambda: chs.attn_cache_evict(kp, vp, w, table, sl, big),
+                 lambda: chs.attn_cache_evict(kp, vp, w, table, sl, 4, -big),
+                 lambda: chs.attn_key_weights(q, q, w, w, queries=big),
+                 lambda: chs.attn_key_weights(q, q, w, w, window=big),
+                 lambda: _binding._rows_of("weights", torch.zeros(1).expand(2, 2, big), 2, 2, 0)):
+        with pytest.raises(ValueError):
+            call()
+
+
 def test_reference_eviction_by_hand():
     w = torch.tensor([[[5.0, 1.0, 5.0, 2.0, 9.0, 0.0, 0.0]]])
     newlens, keep = ref.evict(w, torch.tensor([6], dtype=torch.int32), 4, 1)
