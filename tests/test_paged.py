@@ -661,6 +661,69 @@ def test_calls_on_two_streams_at_once():
     assert all(same_bits(o, s["o"]) for o, s in zip(outs, eager))
 
 
+@pytest.mark.parametrize("queries,Hq", [(0, 8), (40, 8), (40, 40)])
+def test_key_weights_replay_bit_for_bit_on_two_streams(queries, Hq):
+    B, Hkv, S, Dh = 2, 2, 700, 64
+    q, k, v = gpu(*inputs.prefill_inputs(B, Hq, Hkv, S, Dh, seed=31))
+    sl = torch.tensor([700, 333], dtype=torch.int32, device="cuda")
+    _, lse = chs.attn_fwd_lse(q, k, v)
+    weights = torch.zeros(3, B, Hkv, S, device="cuda")
+    for _ in range(3):
+        chs.attn_key_weights(q, k, lse, weights[0], sl, queries=queries)
+    graphs = []
+    for w in weights[1:]:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            chs.attn_key_weights(q, k, lse, w, sl, queries=queries)
+        graphs.append(g)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):   # both at once; each replay adds
+        graphs[0].replay()
+        with torch.cuda.stream(side):
+            graphs[1].replay()
+    torch.cuda.synchronize()
+    status_ok()
+    assert weights[0].any() and all(same_bits(w, weights[0]) for w in weights[1:])
+
+
+@pytest.mark.parametrize("Hq", [4, 40])
+def test_sequences_may_share_pages(Hq):
+    # a common prefix, and one page again and again
+    lens, Hkv, Dh, page, cols = [200, 150, 96], 1, 128, 16, 13
+    kp, vp, table, sl = gpu(*ref.make_cache(lens, Hkv, Dh, page, cols, seed=3))
+    table[1, :6] = table[0, :6]
+    table[2, :6] = table[0, 0]
+    q = queries(3, Hq, Dh, seed=4).cuda()
+    w = torch.zeros(3, Hkv, cols * page, device="cuda")
+    got = chs.attn_decode_paged(q, kp, vp, table, sl, weights=w)
+    # the same rows in pages of their own
+    own = torch.arange(3 * cols, dtype=torch.int32, device="cuda").view(3, cols)
+    used = torch.arange(cols, device="cuda") * page < sl[:, None]
+    at = torch.where(used, table, 0).long().flatten()
+    w2 = torch.zeros_like(w)
+    want = chs.attn_decode_paged(q, kp[at].contiguous(), vp[at].contiguous(), own, sl, weights=w2)
+    status_ok()
+    assert same_bits(got, want) and same_bits(w, w2)
+
+
+def test_empty_batches():
+    kp, vp, table, sl = gpu(*ref.make_cache([5], 2, 64, 8, 2, seed=0))
+    none, no_lens = table[:0], sl[:0]
+    q = torch.zeros(0, 4, 1, 64, dtype=torch.bfloat16, device="cuda")
+    kv, w = torch.zeros(0, 2, 1, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(0, 2, 16).cuda()
+    before = kp.clone()
+    assert chs.attn_decode_paged(q, kp, vp, none, no_lens, weights=w).shape == q.shape
+    chs.attn_paged_append(kv, kv, kp, vp, none, no_lens)
+    chs.attn_paged_append(torch.zeros(1, 2, 0, 64, dtype=torch.bfloat16).cuda(),
+                          torch.zeros(1, 2, 0, 64, dtype=torch.bfloat16).cuda(), kp, vp, table, sl)
+    new, keep = chs.attn_cache_evict(kp, vp, w, none, no_lens, 4)
+    assert new.shape == (0,) and keep.shape == (0, 2, 4)
+    chs.attn_key_weights(q, kv, torch.zeros(0, 4, 1, device="cuda"), w, no_lens)
+    status_ok()
+    assert same_bits(kp, before)
+
+
 def test_withheld_tile_times_out_then_recovers():
     s, want = _state(20, [300, 20, 129]), _state(20, [300, 20, 129])
     _step(want)
