@@ -464,12 +464,14 @@ def attn_decode_paged(q, kpages, vpages, table, seqlens, o=None, *, window=0, sc
         raise TypeError("workspace must be a contiguous CUDA uint8 tensor on the same device")
     if o is None:
         o = _empty((B, Hq, 1, Dh), torch.bfloat16, q.device, stream)
-    if workspace is None:
+    if workspace is None and need > 0:
         workspace = _empty((need,), torch.uint8, q.device, stream)
     rc = load().attn_decode_paged(q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(),
                                   table.data_ptr(), seqlens.data_ptr(), o.data_ptr(),
                                   None if weights is None else weights.data_ptr(), stride,
-                                  int(bool(accumulate)), workspace.data_ptr(), workspace.numel(),
+                                  int(bool(accumulate)),
+                                  None if workspace is None else workspace.data_ptr(),
+                                  0 if workspace is None else workspace.numel(),
                                   B, Hq, Hkv, P, page, cols, Dh, window, float(scale),
                                   _stream_handle(stream))
     if rc != ATTN_OK:

@@ -600,8 +600,9 @@ extern "C" int attn_decode_paged_workspace(int B, int Hq, int Hkv, int page, int
   if (!bytes) return ATTN_ERR_INVALID_ARG;
   DeviceState* st = nullptr;
   if ((rc = device_state(&st)) != ATTN_OK) return rc;
-  *bytes = chs::decode_paged_workspace_bytes(B, Hq, Hkv, cache, Dh, with_weights != 0,
-                                             st->info.num_sms);
+  // (a call with a window needs no more than one without)
+  *bytes = chs::decode_paged_workspace_bytes(B, Hq, Hkv, cache, Dh, 0, with_weights != 0,
+                                             launch_info(st));
   return ATTN_OK;
 }
 
@@ -622,7 +623,7 @@ extern "C" int attn_decode_paged(const void* q, const void* kpages, const void* 
   if (B == 0) return ATTN_OK;
   if (!usable(q, 16) || !usable(kpages, 16) || !usable(vpages, 16) || !usable(o, 16) ||
       !usable(table, 4) || !usable(seqlens, 4) || (weights && !usable(weights, 4)) ||
-      !usable(workspace, 256))
+      (workspace_bytes > 0 && !usable(workspace, 256)))
     return ATTN_ERR_INVALID_ARG;
   const size_t qo = (size_t)B * Hq * Dh * 2, pool = pool_bytes(Hkv, cache, Dh);
   const size_t wb = weights ? (size_t)B * Hkv * weights_stride * 4 : 0;
@@ -636,12 +637,13 @@ extern "C" int attn_decode_paged(const void* q, const void* kpages, const void* 
     return ATTN_ERR_INVALID_ARG;
   DeviceState* st = nullptr;
   if ((rc = device_state(&st)) != ATTN_OK) return rc;
-  if (workspace_bytes < chs::decode_paged_workspace_bytes(B, Hq, Hkv, cache, Dh,
-                                                          weights != nullptr, st->info.num_sms))
+  const chs::DeviceInfo dev = launch_info(st);
+  if (workspace_bytes < chs::decode_paged_workspace_bytes(B, Hq, Hkv, cache, Dh, window,
+                                                          weights != nullptr, dev))
     return ATTN_ERR_SCRATCH_LIMIT;
   const cudaError_t e = chs::launch_decode_paged(
       q, kpages, vpages, table, seqlens, o, weights, weights_stride, accumulate, workspace, B, Hq,
-      Hkv, cache, Dh, window, scale_log2, launch_info(st), stream);
+      Hkv, cache, Dh, window, scale_log2, dev, stream);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

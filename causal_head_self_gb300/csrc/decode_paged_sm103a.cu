@@ -17,47 +17,147 @@ struct Layout {
 
 int score_stride(const PagedCache& c) { return (c.cols * c.page + 127) / 128 * 128; }
 
-Layout layout(int B, int Hq, int Hkv, const PagedCache& c, int Dh, bool scores, int num_sms) {
+template <int DH>
+cudaError_t allow_short(int device) {
+  static std::atomic<int> configured[kMaxDevices];
+  return configure_once(configured, device, [] {
+    return cudaFuncSetAttribute(attn_decode_paged_sm103a<DH, 4, true>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)decode_paged_smem_bytes<DH>());
+  });
+}
+
+struct ShortLaunch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  ShortLaunch(int ctas, int split, size_t smem, cudaStream_t stream) {
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(DecodePagedCfg<128>::kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+  }
+};
+
+// How many clusters of 1 << log2 CTAs run at once (every head size takes a whole SM
+// per CTA).
+int clusters_at_once(int log2, const DeviceInfo& dev) {
+  static std::atomic<int> known[kMaxDevices][4];
+  const bool tracked = dev.device >= 0 && dev.device < kMaxDevices;
+  int n = tracked ? known[dev.device][log2].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
+  ShortLaunch l(8 * dev.num_sms, 1 << log2, decode_paged_smem_bytes<128>(), nullptr);
+  l.cfg.numAttrs = 1;
+  if (allow_short<128>(dev.device) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, attn_decode_paged_sm103a<128, 4, true>, &l.cfg) !=
+          cudaSuccess)
+    return 0;
+  if (tracked) known[dev.device][log2].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// Tiles of a unit, at most.
+long long most_tiles(const PagedCache& c, int Dh, int window) {
+  const int keys = tile_keys(Dh);
+  const long long rows = (long long)c.cols * c.page, tiles = (rows + keys - 1) / keys;
+  const long long seen = window > 0 ? ((long long)window + keys - 2) / keys + 1 : tiles;
+  return tiles < seen ? tiles : seen;
+}
+
+// The CTAs per unit (a cluster) of a call that runs in the short form, or 0.  All
+// clusters run at once, and no CTA gets more than kShortTiles tiles: up to there the
+// short form was the faster one at equal and at ragged lengths, with all head
+// layouts that were tried but 32 query heads on one K/V head.  GPU time, line of
+// tiles -> short form (8 K/V heads of 128, 32 query heads): 4 x 1024 keys 11.4 ->
+// 8.9 us, 16 x 1024 16.8 -> 13.1 (ragged 15.1 -> 13.0), 1 x 8192 13.6 -> 12.5; with
+// 16 tiles per CTA 1 x 16384 16.6 -> 18.2 us.
+constexpr int kShortTiles = 8;
+
+int short_split(int B, int Hq, int Hkv, const PagedCache& c, int Dh, int window,
+                const DeviceInfo& dev) {
+  if (Hq / Hkv > kCopiesMaxGroup) return 0;
+  const long long units = (long long)B * Hkv, tiles = most_tiles(c, Dh, window);
+  if (units > dev.num_sms || tiles > 8 * kShortTiles) return 0;
+  int log2 = 0;
+  while (log2 < 3 && (1 << log2) < tiles && units <= clusters_at_once(log2 + 1, dev)) ++log2;
+  return tiles <= (long long)kShortTiles << log2 ? 1 << log2 : 0;
+}
+
+Layout layout(int B, int Hq, int Hkv, const PagedCache& c, int Dh, bool scores, bool one_launch,
+              int num_sms) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const int G = Hq / Hkv;
   const size_t units = (size_t)B * Hkv * ((G + 127) / 128);
-  const size_t rows = (units + num_sms) * (G <= kCopiesMaxGroup ? 4 * (size_t)G : 128);
+  // (the short form keeps its partial results in shared memory)
+  const size_t rows =
+      one_launch ? 0 : (units + num_sms) * (G <= kCopiesMaxGroup ? 4 * (size_t)G : 128);
   Layout w;
   w.m_off = up(rows * Dh * sizeof(float));
   w.l_off = w.m_off + up(rows * sizeof(float));
   w.units_off = w.l_off + up(rows * sizeof(float));
-  w.scores_off = w.units_off + up(units * sizeof(int2));
+  w.scores_off = w.units_off + (rows > 0 ? up(units * sizeof(int2)) : 0);
   w.total = w.scores_off + (scores ? (size_t)B * Hq * score_stride(c) * sizeof(float) : 0);
   return w;
 }
 
-template <int DH, int REP>
-cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                   const DecodePagedParams& prm, int device, cudaStream_t stream) {
-  constexpr size_t smem = decode_paged_smem_bytes<DH>();
-  static_assert(smem <= 232448, "shared memory budget of one sm_103a CTA");
-  static std::atomic<int> configured[kMaxDevices];
-  cudaError_t e = configure_once(configured, device, [] {
-    return cudaFuncSetAttribute(attn_decode_paged_sm103a<DH, REP>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  });
+template <int DH>
+cudaError_t launch_short(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                         const DecodePagedParams& prm, const DeviceInfo& dev, cudaStream_t stream) {
+  const cudaError_t e = allow_short<DH>(dev.device);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(attn_decode_paged_sm103a<DH, REP>, dim3(prm.ctas),
-                 dim3(DecodePagedCfg<DH>::kThreads), smem, stream, mq, mk, mv, prm);
-  if (e != cudaSuccess) return e;
+  const ShortLaunch l(prm.ctas, prm.split, decode_paged_smem_bytes<DH>(), stream);
+  return cudaLaunchKernelEx(&l.cfg, attn_decode_paged_sm103a<DH, 4, true>, mq, mk, mv, prm);
+}
+
+template <int DH, int REP, int THREADS>
+cudaError_t launch_join(const DecodePagedParams& prm, cudaStream_t stream) {
   unsigned blocks = (unsigned)prm.B * prm.Hq;
   if (prm.weights)
     blocks += (unsigned)prm.B * prm.Hkv *
-              ((prm.cols * prm.page + kPagedWeightKeys - 1) / kPagedWeightKeys);
-  return launch_pdl(attn_decode_paged_join<DH, REP>, dim3(blocks), dim3(kPagedJoinThreads), 0,
+              ((prm.cols * prm.page + 4 * THREADS - 1) / (4 * THREADS));
+  return launch_pdl(attn_decode_paged_join<DH, REP, THREADS>, dim3(blocks), dim3(THREADS), 0,
                     stream, prm);
+}
+
+template <int DH, int REP>
+cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                   const DecodePagedParams& prm, const DeviceInfo& dev, cudaStream_t stream) {
+  constexpr size_t smem = decode_paged_smem_bytes<DH>();
+  static_assert(smem <= 232448, "shared memory budget of one sm_103a CTA");
+  static std::atomic<int> configured[kMaxDevices];
+  cudaError_t e = configure_once(configured, dev.device, [] {
+    return cudaFuncSetAttribute(attn_decode_paged_sm103a<DH, REP, false>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  });
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(attn_decode_paged_sm103a<DH, REP, false>, dim3(prm.ctas),
+                 dim3(DecodePagedCfg<DH>::kThreads), smem, stream, mq, mk, mv, prm);
+  if (e != cudaSuccess) return e;
+  // Many partial results in few units take more threads, as long as each SM has a
+  // block at most: 4 x 32 heads on 8, 8192 keys 29.2 -> 27.3 us for the step, 8 heads
+  // on 1, 16384 keys 44 -> 31.7; 16 x 32 heads on 8, 512 keys would go 12.9 -> 17.9.
+  // With weights, whose blocks are then larger too, it takes more of them: 4 x 32 heads
+  // on 8, 16384 to 32768 keys (20 partial results) 69 us with 256 threads, 72 with 1024;
+  // 2 x 32 on 8, 1024 keys (40) 13.1 -> 11.7.
+  const int partials = REP * (prm.ctas / (prm.B * prm.Hkv * prm.row_blocks) + 1);
+  return partials > (prm.weights ? 32 : 16) && prm.B * prm.Hq <= dev.num_sms
+             ? launch_join<DH, REP, 1024>(prm, stream)
+             : launch_join<DH, REP, 256>(prm, stream);
 }
 
 template <int DH>
 cudaError_t launch_rep(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                       const DecodePagedParams& prm, int device, cudaStream_t stream) {
-  return prm.G <= kCopiesMaxGroup ? launch<DH, 4>(mq, mk, mv, prm, device, stream)
-                                  : launch<DH, 1>(mq, mk, mv, prm, device, stream);
+                       const DecodePagedParams& prm, const DeviceInfo& dev, cudaStream_t stream) {
+  if (prm.split > 0) return launch_short<DH>(mq, mk, mv, prm, dev, stream);
+  return prm.G <= kCopiesMaxGroup ? launch<DH, 4>(mq, mk, mv, prm, dev, stream)
+                                  : launch<DH, 1>(mq, mk, mv, prm, dev, stream);
 }
 
 }  // namespace
@@ -73,8 +173,9 @@ int paged_box_rows(int page, int Dh) {
 }
 
 size_t decode_paged_workspace_bytes(int B, int Hq, int Hkv, const PagedCache& cache, int Dh,
-                                    bool scores, int num_sms) {
-  return layout(B, Hq, Hkv, cache, Dh, scores, num_sms).total;
+                                    int window, bool scores, const DeviceInfo& dev) {
+  const bool one_launch = short_split(B, Hq, Hkv, cache, Dh, window, dev) > 0;
+  return layout(B, Hq, Hkv, cache, Dh, scores, one_launch, dev.num_sms).total;
 }
 
 cudaError_t launch_decode_paged(const void* q, const void* kpages, const void* vpages,
@@ -82,7 +183,7 @@ cudaError_t launch_decode_paged(const void* q, const void* kpages, const void* v
                                 int weights_stride, int accumulate, void* workspace, int B, int Hq,
                                 int Hkv, const PagedCache& cache, int Dh, int window,
                                 float scale_log2, const DeviceInfo& dev, cudaStream_t stream) {
-  const int G = Hq / Hkv, keys = tile_keys(Dh);
+  const int G = Hq / Hkv;
   const int box = paged_box_rows(cache.page, Dh);
   const long long pages = (long long)cache.num_pages * Hkv;
   CUtensorMap mq, mk, mv;
@@ -101,18 +202,15 @@ cudaError_t launch_decode_paged(const void* q, const void* kpages, const void* v
   prm.cols = cache.cols;
   prm.box_rows = box;
   prm.row_blocks = (G + 127) / 128;
-  const long long rows = (long long)cache.cols * cache.page;
-  long long tiles = (rows + keys - 1) / keys;   // at most, per unit
-  if (window > 0 && tiles > ((long long)window + keys - 2) / keys + 1)
-    tiles = ((long long)window + keys - 2) / keys + 1;
-  const long long places = (tiles + 1) * B * Hkv * prm.row_blocks;
-  prm.ctas = places < dev.num_sms ? (int)places : dev.num_sms;
+  prm.split = short_split(B, Hq, Hkv, cache, Dh, window, dev);
+  const long long places = (most_tiles(cache, Dh, window) + 1) * B * Hkv * prm.row_blocks;
+  prm.ctas = prm.split > 0 ? B * Hkv * prm.split : places < dev.num_sms ? (int)places : dev.num_sms;
   prm.score_stride = score_stride(cache);
   prm.scale_log2 = scale_log2;
   prm.accumulate = accumulate;
   prm.seqlens = seqlens;
   prm.table = table;
-  const Layout w = layout(B, Hq, Hkv, cache, Dh, weights != nullptr, dev.num_sms);
+  const Layout w = layout(B, Hq, Hkv, cache, Dh, weights != nullptr, prm.split > 0, dev.num_sms);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   prm.o_part = reinterpret_cast<float*>(ws);
   prm.m_part = reinterpret_cast<float*>(ws + w.m_off);
@@ -124,9 +222,9 @@ cudaError_t launch_decode_paged(const void* q, const void* kpages, const void* v
   prm.o = static_cast<__nv_bfloat16*>(o);
   prm.error_word = dev.error_word;
   prm.fault = dev.fault;
-  return Dh == 256   ? launch_rep<256>(mq, mk, mv, prm, dev.device, stream)
-         : Dh == 128 ? launch_rep<128>(mq, mk, mv, prm, dev.device, stream)
-                     : launch_rep<64>(mq, mk, mv, prm, dev.device, stream);
+  return Dh == 256   ? launch_rep<256>(mq, mk, mv, prm, dev, stream)
+         : Dh == 128 ? launch_rep<128>(mq, mk, mv, prm, dev, stream)
+                     : launch_rep<64>(mq, mk, mv, prm, dev, stream);
 }
 
 }  // namespace chs

@@ -35,6 +35,13 @@
 // each, and four partial results per segment.  Larger groups use every row
 // (REP = 1).
 //
+// Short form (SHORT).  Where the table has room for few tiles a unit, starting up
+// and joining cost more than reading.  A unit then belongs to a cluster of up to
+// eight CTAs, each with an equal part of its tiles; the partial results stay in
+// shared memory, the CTAs read each other's there, and the step is one launch
+// without a workspace (but for the scores, with weights).  One sequence of 1024
+// keys with 8 K/V heads: 9.1 -> 7.8 us on the GPU, 21 -> 15 us on the host.
+//
 // Rows outside [lo, L) are never used: boxes without a visible row are not
 // loaded (their table entries may hold anything), scores of invisible rows are
 // replaced by -inf, and their V rows are zeroed in shared memory before the
@@ -56,6 +63,7 @@ struct DecodePagedParams {
   int box_rows;                // rows per TMA box
   int row_blocks;              // blocks of 128 query heads per K/V head
   int ctas;                    // CTAs of the grid
+  int split;                   // SHORT: CTAs per unit, a cluster
   int score_stride;            // row length of `scores`
   float scale_log2;
   int accumulate;
@@ -129,9 +137,32 @@ struct PagedSegment {
   int unit, last_cta;
 };
 
+// SHORT: the CTA of rank r in its unit's cluster holds a split-th of its tiles.
+template <int KEYS>
+struct PagedShortWalk {
+  int b, gi, from, to;   // tiles [from, to) of the unit's, none once they are taken
+  PagedSeq seq;
+
+  __device__ __forceinline__ void init(const DecodePagedParams& p, int cta) {
+    const int unit = cta / p.split, rank = cta - unit * p.split;
+    b = unit / p.Hkv;
+    gi = unit - b * p.Hkv;
+    seq = paged_seq<KEYS>(p, b);
+    from = seq.n * rank / p.split;   // (a few tiles)
+    to = seq.n * (rank + 1) / p.split;
+  }
+
+  __device__ __forceinline__ bool next(const DecodePagedParams& p, PagedSegment& s) {
+    if (from == to) return false;
+    s = {b, gi, seq.L, seq.lo, seq.first + from, to - from, from == 0, b * p.Hkv + gi, 0};
+    from = to;
+    return true;
+  }
+};
+
 // The segments of one CTA in order.  Every warp walks them for itself.
 template <int KEYS>
-struct PagedWalk {
+struct PagedLineWalk {
   int cur, end, share;   // places on the line
   int b, gi, at;         // next segment: unit and place in it (0: before its tiles)
   PagedSeq seq;
@@ -216,6 +247,21 @@ struct PagedWalk {
   }
 };
 
+template <int KEYS, bool SHORT>
+using PagedWalk = std::conditional_t<SHORT, PagedShortWalk<KEYS>, PagedLineWalk<KEYS>>;
+
+// SHORT: one segment's partial results, in the ring's place once nothing of it is
+// in use.  Row copy * G + head; four floats more per row keep neighbouring rows in
+// different banks.
+template <int DH>
+struct PagedPart {
+  float o[128][DH + 4];
+  float m[128], l[128];
+  float m_all[32], l_all[32];   // of the four copies together
+  float share[32][8];           // [head][CTA]: its part of the head's result
+  float top[32], inv[32];
+};
+
 // A place in a ring of slots [FIRST, FIRST + N): slot and parity of its current
 // use.  Whoever waits on a ring's barriers passes every use of every slot in
 // turn, so that it is never more than one phase off and the parity is enough.
@@ -249,12 +295,12 @@ __device__ __forceinline__ void mbar_wait_drain_paged(uint64_t* bar, uint32_t pa
 // copy, so at a page of 16 rows one warp alone is slower than the memory:
 // B = 8, 32 heads of 64, 4096 keys ran at 4470 GB/s with one loading warp
 // (page 8: 3041).
-template <int DH, int REP, bool V>
+template <int DH, int REP, bool SHORT, bool V>
 __device__ __forceinline__ void decode_paged_producer(DecodePagedSmem<DH>& sm,
                                                       const DecodePagedParams& p,
                                                       const CUtensorMap* map_q,
                                                       const CUtensorMap* map_kv,
-                                                      PagedWalk<DecodePagedCfg<DH>::kKeys> walk,
+                                                      PagedWalk<DecodePagedCfg<DH>::kKeys, SHORT> walk,
                                                       int part, int lane, volatile int* abort) {
   using Cfg = DecodePagedCfg<DH>;
   const uint64_t once = policy_evict_first();   // each cached row is read by one CTA
@@ -282,7 +328,8 @@ __device__ __forceinline__ void decode_paged_producer(DecodePagedSmem<DH>& sm,
   PagedSegment s;
   while (ok && walk.next(p, s)) {
     const int g = s.gi / p.row_blocks, rb = s.gi - g * p.row_blocks;
-    if (!V && part == 0 && lane == 0 && s.starts) p.unit_ctas[s.unit] = make_int2(blockIdx.x, s.last_cta);
+    if (!SHORT && !V && part == 0 && lane == 0 && s.starts)
+      p.unit_ctas[s.unit] = make_int2(blockIdx.x, s.last_cta);
     const int* row = p.table + (size_t)s.b * p.cols;
     // The table is read for `group` tiles at a time, a group ahead: lane l holds
     // the entry of box l % boxes of the group's tile l / boxes.  (Under load an
@@ -365,15 +412,16 @@ __device__ __forceinline__ void decode_paged_producer(DecodePagedSmem<DH>& sm,
 
 // Tensor-core warp.  Per segment: Q to tensor memory, S of the first two tiles,
 // then per tile P.V and the S two tiles on, into the buffer that P came from.
-template <int DH>
+template <int DH, bool SHORT>
 __device__ __forceinline__ void decode_paged_issuer(DecodePagedSmem<DH>& sm,
                                                     const DecodePagedParams& p, uint32_t tbase,
-                                                    PagedWalk<DecodePagedCfg<DH>::kKeys> walk,
+                                                    PagedWalk<DecodePagedCfg<DH>::kKeys, SHORT> walk,
                                                     volatile int* abort) {
   using Cfg = DecodePagedCfg<DH>;
   constexpr uint32_t idesc_qk = idesc_bf16_f32(128, Cfg::kKeys, false, false);
   constexpr uint32_t idesc_pv = idesc_bf16_f32(128, DH, false, true);
-  const uint64_t base = smem_u32(sm.slot[0]) >> 4;
+  // (a shared address of a cluster's CTA has its rank above the descriptor's bits)
+  const uint64_t base = (smem_u32(sm.slot[0]) >> 4) & 0x3FFFu;
   const uint64_t kmajor = smem_desc_sw128(0, 16, 1024) | base;
   const uint64_t mnmajor = smem_desc_sw128(0, Cfg::kKvBox, 1024) | base;
   const uint32_t dO = tbase + Cfg::kColO;
@@ -446,10 +494,10 @@ __device__ __forceinline__ void decode_paged_issuer(DecodePagedSmem<DH>& sm,
 
 // Softmax warps: thread t owns row t (tensor-memory lane t).  With REP = 4 row
 // 32 w + i is query head i of the block, for the keys of quarter w.
-template <int DH, int REP>
+template <int DH, int REP, bool SHORT>
 __device__ __forceinline__ void decode_paged_softmax(DecodePagedSmem<DH>& sm,
                                                      const DecodePagedParams& p, uint32_t tbase,
-                                                     PagedWalk<DecodePagedCfg<DH>::kKeys> walk,
+                                                     PagedWalk<DecodePagedCfg<DH>::kKeys, SHORT> walk,
                                                      int warp, int lane, int active_warps,
                                                      volatile int* abort) {
   using Cfg = DecodePagedCfg<DH>;
@@ -476,6 +524,7 @@ __device__ __forceinline__ void decode_paged_softmax(DecodePagedSmem<DH>& sm,
     // a barrier tells only one phase from the next)
     if (!mbar_wait(&sm.o_final, nseg++ & 1u, abort)) return false;
     tc_fence_after_sync();
+    PagedPart<DH>& part = *reinterpret_cast<PagedPart<DH>*>(sm.slot[0]);
     float* dst = p.o_part + pend_at * DH;
 #pragma unroll 1
     for (int c = 0; c < DH / 64; ++c) {
@@ -484,7 +533,14 @@ __device__ __forceinline__ void decode_paged_softmax(DecodePagedSmem<DH>& sm,
       tmem_ld_32x32b_x32(colO + 64 * c + 32, o[1]);
       tmem_ld_wait(o[0]);
       tmem_ld_wait(o[1]);
-      if (pend_rows) {
+      if (SHORT && pend_rows) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const uint32_t* x = &o[e / 8][4 * (e % 8)];
+          *reinterpret_cast<uint4*>(&part.o[pend_at][64 * c + 4 * e]) =
+              make_uint4(x[0], x[1], x[2], x[3]);
+        }
+      } else if (pend_rows) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           uint32_t w8[8];
@@ -495,8 +551,8 @@ __device__ __forceinline__ void decode_paged_softmax(DecodePagedSmem<DH>& sm,
       }
     }
     if (pend_rows) {
-      p.m_part[pend_at] = pend_m;
-      p.l_part[pend_at] = pend_l;
+      (SHORT ? part.m : p.m_part)[pend_at] = pend_m;
+      (SHORT ? part.l : p.l_part)[pend_at] = pend_l;
     }
     pending = false;
     return true;
@@ -631,13 +687,126 @@ __device__ __forceinline__ void decode_paged_softmax(DecodePagedSmem<DH>& sm,
     pend_rows = real;
     pend_m = m_run;
     pend_l = l_run;
-    pend_at = ((size_t)(s.unit + blockIdx.x) * REP + copy) * (REP == 4 ? p.G : 128) + head;
+    pend_at = ((SHORT ? 0 : (size_t)(s.unit + blockIdx.x) * REP) + copy) * (REP == 4 ? p.G : 128) +
+              head;
     pending = true;
   }
-  if (ok && pending) flush();
+  if (ok && pending) {
+    flush();
+  } else if (SHORT && head < p.G) {   // no tile: nothing of this CTA's counts
+    reinterpret_cast<PagedPart<DH>*>(sm.slot[0])->m[copy * p.G + head] = -INFINITY;
+  }
 }
 
-template <int DH, int REP>
+__device__ __forceinline__ void paged_cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// *x in the shared memory of the cluster's CTA `rank`.
+__device__ __forceinline__ float paged_peer(const float* x, int rank) {
+  uint32_t at;
+  float y;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(x)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(y) : "r"(at) : "memory");
+  return y;
+}
+
+// SHORT: joins the four copies of this CTA's partial results, into the first.
+template <int DH>
+__device__ __forceinline__ void decode_paged_short_copies(PagedPart<DH>& part,
+                                                          const DecodePagedParams& p) {
+  for (int i = threadIdx.x; i < p.G * DH; i += DecodePagedCfg<DH>::kThreads) {
+    const int h = i / DH, d = i % DH;
+    float m[4], M = -INFINITY, l = 0.f, o = 0.f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) M = fmaxf(M, m[c] = part.m[c * p.G + h]);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      // (where the CTA has no tile only m was written)
+      const float f = m[c] == -INFINITY ? 0.f : ex2_approx(m[c] - M);
+      if (f != 0.f) {
+        l = fmaf(f, part.l[c * p.G + h], l);
+        o = fmaf(f, part.o[c * p.G + h][d], o);
+      }
+    }
+    part.o[h][d] = o;   // (this thread alone reads these columns)
+    if (d == 0) {
+      part.m_all[h] = M;
+      part.l_all[h] = l;
+    }
+  }
+}
+
+// SHORT: joins the unit's partial results (as attn_decode_paged_join does), each
+// CTA of the cluster a part of the outputs and, with weights, those of its keys.
+template <int DH>
+__device__ __forceinline__ void decode_paged_short_join(PagedPart<DH>& part,
+                                                        const DecodePagedParams& p) {
+  using Cfg = DecodePagedCfg<DH>;
+  const int tid = threadIdx.x;
+  PagedShortWalk<Cfg::kKeys> walk;
+  walk.init(p, blockIdx.x);
+  const int rank = (int)blockIdx.x % p.split;
+  const size_t bh0 = (size_t)walk.b * p.Hq + (size_t)walk.gi * p.G;   // the unit's first head
+  if (walk.seq.n == 0) {
+    // no keys: zero; a length that no sequence can have is an error
+    if (rank > 0) return;
+    for (int i = tid; i < p.G * DH; i += Cfg::kThreads) p.o[bh0 * DH + i] = __float2bfloat16(0.f);
+    if (tid == 0 && __ldcg(p.seqlens + walk.b) != 0) atomicExch(p.error_word, 1);   // ATTN_ERR_INVALID_ARG
+    return;
+  }
+  // eight lanes per head, one for each CTA
+  const int head = tid / 8, from = tid % 8;
+  static_assert(Cfg::kThreads >= 8 * 32, "all heads at once");
+  float m = -INFINITY, l = 0.f;
+  if (head < p.G && from < p.split) {
+    m = paged_peer(&part.m_all[head], from);
+    l = paged_peer(&part.l_all[head], from);
+  }
+  float M = m;
+#pragma unroll
+  for (int d = 4; d > 0; d /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  const float f = m == -INFINITY ? 0.f : ex2_approx(m - M);
+  l *= f;
+#pragma unroll
+  for (int d = 4; d > 0; d /= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
+  if (head < p.G) {
+    part.share[head][from] = f / l;
+    if (from == 0) {
+      part.top[head] = M;
+      part.inv[head] = 1.0f / l;
+    }
+  }
+  __syncthreads();
+  for (int i = rank * Cfg::kThreads + tid; i < p.G * DH; i += p.split * Cfg::kThreads) {
+    const int h = i / DH, d = i % DH;
+    float x[8], o = 0.f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) x[r] = r < p.split ? paged_peer(&part.o[h][d], r) : 0.f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) o = fmaf(part.share[h][r], x[r], o);
+    p.o[bh0 * DH + i] = __float2bfloat16(o);
+  }
+  if (p.weights == nullptr) return;
+  float* out = p.weights + ((size_t)walk.b * p.Hkv + walk.gi) * p.weights_stride;
+  const int first = walk.seq.first * Cfg::kKeys;   // of a tile
+  const int end = min(walk.seq.L, first + walk.to * Cfg::kKeys);
+  for (int t = first + walk.from * Cfg::kKeys + tid; t < end; t += Cfg::kThreads) {
+    if (t < walk.seq.lo) continue;
+    const float* src = p.scores + bh0 * p.score_stride + t;
+    float w = 0.f;
+#pragma unroll 4
+    for (int h = 0; h < p.G; ++h)
+      w = fmaf(ex2_approx(fmaf(__ldcg(src + (size_t)h * p.score_stride), p.scale_log2,
+                               -part.top[h])),
+               part.inv[h], w);
+    out[t] = p.accumulate ? out[t] + w : w;
+  }
+  if (!p.accumulate && rank == 0)   // keys before the window
+    for (int t = tid; t < walk.seq.lo; t += Cfg::kThreads) out[t] = 0.f;
+}
+
+template <int DH, int REP, bool SHORT>
 __global__ void __launch_bounds__(288, 1)
     attn_decode_paged_sm103a(const __grid_constant__ CUtensorMap map_q,
                              const __grid_constant__ CUtensorMap map_k,
@@ -684,17 +853,17 @@ __global__ void __launch_bounds__(288, 1)
   griddep_wait();
   // the join kernel's blocks may be placed beside this grid's (every CTA of
   // which is running by then): they wait for the whole grid, but not for a launch
-  if (threadIdx.x == 0) griddep_launch_dependents();
-  PagedWalk<Cfg::kKeys> walk;
+  if (!SHORT && threadIdx.x == 0) griddep_launch_dependents();
+  PagedWalk<Cfg::kKeys, SHORT> walk;
   walk.init(p, blockIdx.x);
   if (warp >= Cfg::kWarpProducer + 2)
-    decode_paged_producer<DH, REP, true>(sm, p, &map_q, &map_v, walk, warp & 1, lane, abort);
+    decode_paged_producer<DH, REP, SHORT, true>(sm, p, &map_q, &map_v, walk, warp & 1, lane, abort);
   else if (warp >= Cfg::kWarpProducer)
-    decode_paged_producer<DH, REP, false>(sm, p, &map_q, &map_k, walk, warp & 1, lane, abort);
+    decode_paged_producer<DH, REP, SHORT, false>(sm, p, &map_q, &map_k, walk, warp & 1, lane, abort);
   else if (warp == Cfg::kWarpIssuer)
-    decode_paged_issuer<DH>(sm, p, tbase, walk, abort);
+    decode_paged_issuer<DH, SHORT>(sm, p, tbase, walk, abort);
   else if (warp < active_warps)
-    decode_paged_softmax<DH, REP>(sm, p, tbase, walk, warp, lane, active_warps, abort);
+    decode_paged_softmax<DH, REP, SHORT>(sm, p, tbase, walk, warp, lane, active_warps, abort);
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
@@ -703,20 +872,25 @@ __global__ void __launch_bounds__(288, 1)
     tmem_dealloc(tbase, Cfg::kCols);
   }
   if (threadIdx.x == 0 && sm.abort_flag) atomicExch(p.error_word, 4);   // ATTN_ERR_TIMEOUT
+  if constexpr (SHORT) {
+    // (all waits before this one are bounded, so every thread of the cluster comes here)
+    PagedPart<DH>& part = *reinterpret_cast<PagedPart<DH>*>(sm.slot[0]);
+    decode_paged_short_copies<DH>(part, p);
+    paged_cluster_sync();
+    decode_paged_short_join<DH>(part, p);
+    paged_cluster_sync();   // no CTA goes while another reads its results
+  }
 }
 
 // Joins a unit's partial results, in the order of its CTAs and copies:
 //   o = sum_i 2^(m_i - M) o_i / l,  l = sum_i 2^(m_i - M) l_i,  M = max m_i.
 // Blocks [0, B * Hq) each write one query head's output.  The blocks after
-// them, launched when weights are asked for, each write kPagedWeightKeys of
+// them, launched when weights are asked for, each write 4 * THREADS of
 // the weights of one (sequence, K/V head): sum over the group's heads of
 // 2^(s - M) / l, from the scores that the first kernel left.
-constexpr int kPagedJoinThreads = 256;
-constexpr int kPagedWeightKeys = 4 * kPagedJoinThreads;
-
-template <int DH, int REP>
-__global__ void __launch_bounds__(kPagedJoinThreads)
-    attn_decode_paged_join(const DecodePagedParams p) {
+template <int DH, int REP, int THREADS>
+__global__ void __launch_bounds__(THREADS) attn_decode_paged_join(const DecodePagedParams p) {
+  constexpr int kKeysPerBlock = 4 * THREADS;
   constexpr int KEYS = DecodePagedCfg<DH>::kKeys;
   const int tid = threadIdx.x;
   const int part_rows = REP == 4 ? p.G : 128;
@@ -729,7 +903,7 @@ __global__ void __launch_bounds__(kPagedJoinThreads)
     const int L = __ldcg(p.seqlens + b);
     if (L < 1 || L > paged_rows(p)) {
       // no keys: zero; a length that no sequence can have is an error
-      for (int d = tid; d < DH; d += kPagedJoinThreads)
+      for (int d = tid; d < DH; d += THREADS)
         p.o[(size_t)bh * DH + d] = __float2bfloat16(0.f);
       if (L != 0 && tid == 0) atomicExch(p.error_word, 1);   // ATTN_ERR_INVALID_ARG
       return;
@@ -738,7 +912,7 @@ __global__ void __launch_bounds__(kPagedJoinThreads)
     const size_t at0 = (size_t)(unit + ctas.x) * REP * part_rows + (hg - 128 * rb);
     // DH threads hold a row, a column each; the block's groups of them take every
     // kGroups-th partial and are joined in turn
-    constexpr int kGroups = kPagedJoinThreads / DH;
+    constexpr int kGroups = THREADS / DH;
     const int group = tid / DH, d = tid % DH;
     // partials per round, their loads in flight together (at Dh = 256, 40 partials: 8
     // 22.7 us, 4 23.1, 16 26.0 for the whole step)
@@ -795,14 +969,14 @@ __global__ void __launch_bounds__(kPagedJoinThreads)
   }
   // weights
   const int T = paged_rows(p);
-  const int chunks = (T + kPagedWeightKeys - 1) / kPagedWeightKeys;
+  const int chunks = (T + kKeysPerBlock - 1) / kKeysPerBlock;
   const int wi = blockIdx.x - p.B * p.Hq;
   const int bg = wi / chunks, chunk = wi - bg * chunks;
   const int b = bg / p.Hkv, g = bg - b * p.Hkv;
   const PagedSeq seq = paged_seq<KEYS>(p, b);
-  const int k0 = chunk * kPagedWeightKeys;
+  const int k0 = chunk * kKeysPerBlock;
   if (k0 >= seq.L) return;
-  const bool any = k0 + kPagedWeightKeys > seq.lo;   // some key of the chunk is visible
+  const bool any = k0 + kKeysPerBlock > seq.lo;   // some key of the chunk is visible
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   if (any) {
     // the heads' maxima and sums, 32 heads at a time (one warp per head)
@@ -811,7 +985,7 @@ __global__ void __launch_bounds__(kPagedJoinThreads)
     for (int h0 = 0; h0 < p.G; h0 += 32) {
       const int nh = min(32, p.G - h0);
       __syncthreads();
-      for (int i = warp; i < nh; i += kPagedJoinThreads / 32) {
+      for (int i = warp; i < nh; i += THREADS / 32) {
         const int hg = h0 + i, rb = hg / 128;
         const int unit = bg * p.row_blocks + rb;
         const int2 ctas = __ldcg(p.unit_ctas + unit);
@@ -866,6 +1040,7 @@ __global__ void __launch_bounds__(kPagedJoinThreads)
 
 template <int DH>
 constexpr size_t decode_paged_smem_bytes() {
+  static_assert(sizeof(PagedPart<DH>) <= 224 * 1024, "the partial results lie in the ring");
   return sizeof(DecodePagedSmem<DH>) + 1024;   // + alignment slack
 }
 

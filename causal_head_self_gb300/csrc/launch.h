@@ -133,7 +133,7 @@ int paged_box_rows(int page, int Dh);
 // Device memory that a paged decode call needs: partial results, and with
 // `scores` the raw score of every (query head, key).
 size_t decode_paged_workspace_bytes(int B, int Hq, int Hkv, const PagedCache& cache, int Dh,
-                                    bool scores, int num_sms);
+                                    int window, bool scores, const DeviceInfo& dev);
 
 // One decode step over a paged cache; weights (optional, [B, Hkv,
 // weights_stride] fp32) receive each key's weight summed over its head group.

@@ -319,7 +319,8 @@ int attn_decode_paged(const void* q, const void* kpages, const void* vpages, con
 
 /* The workspace of an attn_decode_paged call on the current device, in bytes:
  * partial results, and with weights the step's scores (4 bytes for each query
- * head and row that the table has room for). */
+ * head and row that the table has room for).  0 for a small table without
+ * weights: the workspace may be NULL then. */
 int attn_decode_paged_workspace(int B, int Hq, int Hkv, int page, int cols, int Dh,
                                 int with_weights, size_t* bytes);
 

@@ -149,6 +149,31 @@ def test_decode_matches_the_definition(Hq, Hkv, Dh, page, cols, lens, window):
             assert (x[b, :, n:] == 7.0).all()   # behind the sequence: left alone
 
 
+def widen(table, page, rows=9000):
+    """The table with unused columns behind it, for more keys than a short step holds."""
+    more = -(-rows // page) - table.shape[1]
+    return torch.cat([table, torch.full((table.shape[0], more), -1, dtype=torch.int32)], 1)
+
+
+@pytest.mark.parametrize("Hq,Hkv,Dh,page,cols,lens,window", DECODE)
+def test_decode_with_a_wide_table_matches_the_definition(Hq, Hkv, Dh, page, cols, lens, window):
+    first = [n - window if window else 0 for n in lens]
+    kp, vp, table, sl = ref.make_cache(lens, Hkv, Dh, page, cols, seed=Hq + page, first_used=first)
+    q = queries(len(lens), Hq, Dh, seed=page)
+    o, tol, w, rtol = ref.decode(q, kp, vp, table, sl, window=window)
+    args = gpu(q, kp, vp, widen(table, page), sl)
+    got = chs.attn_decode_paged(*args, window=window)
+    weights = torch.full((len(lens), Hkv, args[3].shape[1] * page), 7.0, device="cuda")
+    again = chs.attn_decode_paged(*args, window=window, weights=weights, accumulate=False)
+    status_ok()
+    assert same_bits(again, got)
+    assert ((got.cpu().double() - o).abs() <= tol).all()
+    x = weights.cpu().double()
+    for b, n in enumerate(lens):
+        assert ((x[b, :, :n] - w[b, :, :n]).abs() <= (rtol + 2.0 ** -24) * w[b, :, :n]).all()
+        assert (x[b, :, n:] == 7.0).all()
+
+
 def test_decode_with_a_scale_and_large_scores():
     # scores of about +-1000: only the largest weights survive, none overflows
     lens = [300, 129]
@@ -722,6 +747,74 @@ def test_empty_batches():
     chs.attn_key_weights(q, kv, torch.zeros(0, 4, 1, device="cuda"), w, no_lens)
     status_ok()
     assert same_bits(kp, before)
+
+
+def _wide_state(seed, lens):
+    s = _state(seed, lens)
+    s["table"] = widen(s["table"].cpu(), 16).cuda()
+    for name in ("w", "wo"):
+        s[name] = torch.zeros(*s[name].shape[:2], s["table"].shape[1] * 16, device="cuda")
+    return s
+
+
+def test_steps_with_wide_tables_share_nothing():
+    lens = [[600, 64, 30], [100, 640, 5]]
+    eager = [_wide_state(i, x) for i, x in enumerate(lens)]
+    states = [_wide_state(i, x) for i, x in enumerate(lens)]
+    for s in eager:
+        _step(s)
+    status_ok()
+    graphs = []
+    for s in states:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            _step(s)
+        graphs.append(g)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        graphs[0].replay()
+        with torch.cuda.stream(side):
+            graphs[1].replay()
+    torch.cuda.synchronize()
+    status_ok()
+    assert all(_all_same(a, b) for a, b in zip(states, eager))
+
+
+def test_wide_tables_withheld_tile_times_out_then_recovers():
+    s, want = _wide_state(20, [300, 20, 129]), _wide_state(20, [300, 20, 129])
+    _step(want)
+    status_ok()
+    chs.attn_debug_inject_fault(3)
+    try:
+        chs.attn_decode_paged(s["q"], s["kp"], s["vp"], s["table"], s["sl"])
+        assert chs.attn_status() == chs.ATTN_ERR_TIMEOUT
+    finally:
+        chs.attn_debug_inject_fault(0)
+    _step(s)
+    status_ok()
+    assert _all_same(s, want)
+
+
+def test_workspace_of_a_decode_step():
+    q, sl = queries(2, 8, 128, seed=1).cuda(), torch.tensor([70, 9], dtype=torch.int32, device="cuda")
+    kp, vp, table, _ = ref.make_cache([70, 9], 2, 128, 16, 5, seed=2)
+    kp, vp, table, wide = gpu(kp, vp, table, widen(table, 16))
+    assert chs.attn_decode_paged_workspace(q, kp, table) == 0
+    assert chs.attn_decode_paged_workspace(q, kp, table, weights=True) > 0
+    want = chs.attn_decode_paged(q, kp, vp, table, sl)
+    need = chs.attn_decode_paged_workspace(q, kp, wide)
+    # a workspace of just that size, and nothing written behind it
+    ws = torch.full((need + 256,), 0x5a, dtype=torch.uint8, device="cuda")
+    got = chs.attn_decode_paged(q, kp, vp, wide, sl, workspace=ws[:need])
+    assert (ws[need:] == 0x5a).all()
+    assert torch.allclose(got.float(), want.float(), rtol=2.0 ** -7, atol=1e-4)
+    with pytest.raises(chs.AttnError) as e:
+        chs.attn_decode_paged(q, kp, vp, wide, sl, workspace=ws[:need - 1])
+    assert e.value.code == chs.ATTN_ERR_SCRATCH_LIMIT
+    # a window makes the step short again
+    chs.attn_decode_paged(q, kp, vp, wide, sl, window=64, workspace=ws[:0])
+    status_ok()
 
 
 def test_withheld_tile_times_out_then_recovers():
