@@ -340,9 +340,12 @@ def _this_device() -> int:
 
 def _check(name, t, dtype, shape, device):
     """A contiguous tensor of that type and shape, on the same GPU as the others."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.get_device() == device >= 0 and t.is_contiguous()):
-        return
+    try:   # (most of a small call's time is checks: isinstance on a Tensor is not cheap)
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == device >= 0
+                and t.is_contiguous()):
+            return
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA {dtype} tensor")
     if t.shape != shape or not t.is_contiguous():
@@ -357,14 +360,13 @@ def _check_current(device):
 
 
 def _shape(name, t, ndim):
-    """The shape of a tensor of ndim axes (each of them a 32-bit int of the library's)."""
-    if not isinstance(t, torch.Tensor):
+    """The shape of a tensor of ndim axes."""
+    shape = getattr(t, "shape", None)
+    if shape is None:
         raise TypeError(f"{name} must be a tensor")
-    if t.dim() != ndim:
+    if len(shape) != ndim:
         raise ValueError(f"{name} must have {ndim} axes")
-    if max(t.shape) > 0x7fffffff:
-        raise ValueError(f"{name} must have less than 2^31 entries along each axis")
-    return t.shape
+    return shape
 
 
 def _int32(name, x):
@@ -379,6 +381,8 @@ def _check_pools(kpages, vpages, table, seqlens):
     """The checks that every paged call makes: (B, Hkv, num_pages, page, cols, Dh, device)."""
     P, Hkv, page, Dh = shape = _shape("kpages", kpages, 4)
     B, cols = table_shape = _shape("table", table, 2)
+    if B > 0x7fffffff or cols > 0x7fffffff:
+        raise ValueError("table must have less than 2^31 entries along each axis")
     device = kpages.get_device()
     _check("kpages", kpages, torch.bfloat16, shape, device)
     _check_current(device)
@@ -391,6 +395,8 @@ def _check_pools(kpages, vpages, table, seqlens):
 def _rows_of(name, t, B, Hkv, device):
     """A contiguous float32 [B, Hkv, stride] tensor: its stride."""
     stride = _shape(name, t, 3)[2]
+    if stride > 0x7fffffff:
+        raise ValueError(f"{name} must have less than 2^31 entries per row")
     _check(name, t, torch.float32, (B, Hkv, stride), device)
     return stride
 
