@@ -7,6 +7,7 @@ namespace chs {
 namespace {
 
 constexpr int kCopiesMaxGroup = 32;   // head groups up to this run with REP = 4
+constexpr int kShortCtas = 8;         // of a cluster, at most
 
 int tile_keys(int Dh) { return Dh == 256 ? DecodePagedCfg<256>::kKeys : DecodePagedCfg<128>::kKeys; }
 
@@ -46,20 +47,20 @@ struct ShortLaunch {
   }
 };
 
-// How many clusters of 1 << log2 CTAs run at once (every head size takes a whole SM
-// per CTA).
-int clusters_at_once(int log2, const DeviceInfo& dev) {
-  static std::atomic<int> known[kMaxDevices][4];
+// How many clusters of `split` CTAs run at once (every head size takes a whole SM per
+// CTA).
+int clusters_at_once(int split, const DeviceInfo& dev) {
+  static std::atomic<int> known[kMaxDevices][kShortCtas + 1];
   const bool tracked = dev.device >= 0 && dev.device < kMaxDevices;
-  int n = tracked ? known[dev.device][log2].load(std::memory_order_relaxed) : 0;
+  int n = tracked ? known[dev.device][split].load(std::memory_order_relaxed) : 0;
   if (n > 0) return n;
-  ShortLaunch l(8 * dev.num_sms, 1 << log2, decode_paged_smem_bytes<128>(), nullptr);
+  ShortLaunch l(split * dev.num_sms, split, decode_paged_smem_bytes<128>(), nullptr);
   l.cfg.numAttrs = 1;
   if (allow_short<128>(dev.device) != cudaSuccess ||
       cudaOccupancyMaxActiveClusters(&n, attn_decode_paged_sm103a<128, 4, true>, &l.cfg) !=
           cudaSuccess)
     return 0;
-  if (tracked) known[dev.device][log2].store(n, std::memory_order_relaxed);
+  if (tracked) known[dev.device][split].store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -73,21 +74,22 @@ long long most_tiles(const PagedCache& c, int Dh, int window) {
 
 // The CTAs per unit (a cluster) of a call that runs in the short form, or 0.  All
 // clusters run at once, and no CTA gets more than kShortTiles tiles: up to there the
-// short form was the faster one at equal and at ragged lengths, with all head
-// layouts that were tried but 32 query heads on one K/V head.  GPU time, line of
-// tiles -> short form (8 K/V heads of 128, 32 query heads): 4 x 1024 keys 11.4 ->
-// 8.9 us, 16 x 1024 16.8 -> 13.1 (ragged 15.1 -> 13.0), 1 x 8192 13.6 -> 12.5; with
-// 16 tiles per CTA 1 x 16384 16.6 -> 18.2 us.
-constexpr int kShortTiles = 8;
+// short form was no slower at equal or at ragged lengths, with all head layouts that
+// were tried but 32 query heads on one K/V head.  GPU time, line of tiles -> short
+// form (32 query heads, 8 K/V heads of 128): 4 x 1024 keys 11.4 -> 8.9 us, 16 x 1024
+// 16.8 -> 13.2 (ragged 15.1 -> 13.1), 1 x 8192 13.6 -> 12.5; 8 query heads on one of
+// 256, 16 sequences with a window of 4096: 22.7 -> 20.5.  With 16 tiles per CTA
+// 1 x 16384 keys 16.6 -> 18.2.
+constexpr int kShortTiles = 12;
 
 int short_split(int B, int Hq, int Hkv, const PagedCache& c, int Dh, int window,
                 const DeviceInfo& dev) {
   if (Hq / Hkv > kCopiesMaxGroup) return 0;
   const long long units = (long long)B * Hkv, tiles = most_tiles(c, Dh, window);
-  if (units > dev.num_sms || tiles > 8 * kShortTiles) return 0;
-  int log2 = 0;
-  while (log2 < 3 && (1 << log2) < tiles && units <= clusters_at_once(log2 + 1, dev)) ++log2;
-  return tiles <= (long long)kShortTiles << log2 ? 1 << log2 : 0;
+  if (units > dev.num_sms || tiles > kShortCtas * kShortTiles) return 0;
+  int split = tiles < kShortCtas ? (int)tiles : kShortCtas;
+  while (split > 1 && units > clusters_at_once(split, dev)) --split;
+  return tiles <= (long long)kShortTiles * split ? split : 0;
 }
 
 Layout layout(int B, int Hq, int Hkv, const PagedCache& c, int Dh, bool scores, bool one_launch,

@@ -149,7 +149,7 @@ def test_decode_matches_the_definition(Hq, Hkv, Dh, page, cols, lens, window):
             assert (x[b, :, n:] == 7.0).all()   # behind the sequence: left alone
 
 
-def widen(table, page, rows=9000):
+def widen(table, page, rows=13000):
     """The table with unused columns behind it, for more keys than a short step holds."""
     more = -(-rows // page) - table.shape[1]
     return torch.cat([table, torch.full((table.shape[0], more), -1, dtype=torch.int32)], 1)
