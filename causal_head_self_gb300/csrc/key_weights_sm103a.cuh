@@ -534,17 +534,26 @@ __device__ __forceinline__ void key_weights_sums(KeyWeightsSmem<DH>& sm, const K
         const uint32_t span = chi > clo ? (uint32_t)(chi - clo - 1) : 0u;
         if (chi <= clo) clo = 1 << 30;   // no column is visible
         const int in_head = p.pad - 1;   // (a power of two less one)
+        // columns that some, and that all, of this warp's keys see, with one head's
+        // queries in the tile: on the diagonal most 32 columns are one or the other
+        const int t0 = tid & ~31;
+        // (2 x 32 heads of 1024: 18.4 -> 17.6 us)
+        const bool one = p.pad == 128;
+        const int any_lo = one ? en.y + t0 : 0, any_hi = one ? min(en.w, en.z + t0 + 31) : 128;
+        const int all_lo = one ? en.y + t0 + 31 : 128, all_hi = min(en.w, en.z + t0);
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 128; c += 32) {
+          if (c + 32 <= any_lo || c >= any_hi) continue;
           uint32_t y[32];
-          tmem_ld_32x32b_x32(colS + 32 * c, y);
+          tmem_ld_32x32b_x32(colS + c, y);
           tmem_ld_wait(y);
+          if (c < all_lo || c + 32 > all_hi) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int col = 32 * c + e;
-            const float v =
-                keep_if_le(__uint_as_float(y[e]), (uint32_t)((col & in_head) - clo), span);
-            y[e] = col < cols ? __float_as_uint(v) : 0xff800000u;
+            for (int e = 0; e < 32; ++e) {
+              const float v = keep_if_le(__uint_as_float(y[e]),
+                                         (uint32_t)(((c + e) & in_head) - clo), span);
+              y[e] = c + e < cols ? __float_as_uint(v) : 0xff800000u;
+            }
           }
           key_weights_add(y, scale2, sum);
         }

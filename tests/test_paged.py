@@ -3,6 +3,9 @@ eviction against their definitions in 64 bits (tests/paged_ref.py).  Rows that
 hold no key are NaN or infinite and unused table entries are not page numbers,
 so any use of either shows."""
 import math
+import subprocess
+import sys
+from pathlib import Path
 
 import pytest
 import torch
@@ -794,6 +797,37 @@ def test_wide_tables_withheld_tile_times_out_then_recovers():
     _step(s)
     status_ok()
     assert _all_same(s, want)
+
+
+FIRST_CALL_CAPTURED = """
+import torch, causal_head_self_gb300 as chs
+assert chs.attn_status() == chs.ATTN_OK      # (the library's own state is made here)
+q = torch.ones(3, 8, 1, 64, dtype=torch.bfloat16, device="cuda")
+kv = torch.ones(3, 2, 20, 64, dtype=torch.bfloat16, device="cuda")
+pages = torch.zeros(2, 9, 2, 8, 64, dtype=torch.bfloat16, device="cuda")
+table = torch.arange(9, dtype=torch.int32, device="cuda").view(3, 3)
+sl = torch.full((3,), 20, dtype=torch.int32, device="cuda")
+w, w_out = torch.zeros(2, 3, 2, 24, device="cuda")
+lse = torch.zeros(3, 8, 20, device="cuda")
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    chs.attn_paged_append(kv, kv, *pages, table, sl)
+    o = chs.attn_decode_paged(q, *pages, table, sl, weights=w)
+    chs.attn_key_weights(q.expand(3, 8, 20, 64).contiguous(), kv, lse, w_out[..., :20].contiguous(), sl)
+    new, keep = chs.attn_cache_evict(*pages, w, table, sl, 10, 2, weights_out=w_out)
+graph.replay()
+torch.cuda.synchronize()
+assert chs.attn_status() == chs.ATTN_OK
+assert (o == 1).all() and new.tolist() == [10] * 3
+assert keep[0, 0].tolist() == list(range(8)) + [18, 19]
+print("captured")
+"""
+
+
+def test_every_call_may_be_captured_at_its_first_use():
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL_CAPTURED], capture_output=True, text=True,
+                       timeout=120, cwd=Path(__file__).resolve().parent.parent)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr
 
 
 def test_workspace_of_a_decode_step():
