@@ -19,7 +19,9 @@
 // Split: as in the paged decode, the blocks of all (sequence, K/V head) units
 // form a line, a unit's first place standing for the cost of its start, and each
 // CTA (one per SM) takes an equal part.  Blocks alternate between two groups of
-// four summing warps, each with an S buffer of its own.
+// four summing warps, each with an S buffer of its own, which is filled and freed by
+// halves of 128 columns: one half's next block is computed while the other half is
+// summed (whole buffers: XX us).
 //
 // Query rows past the end of the sequence, and rows that pad the tile, are zeroed
 // in shared memory and get -inf for a log-sum-exp, so they weigh nothing; only
@@ -58,7 +60,7 @@ struct KeyFewSmem {
   uint4 ones[2][128];
   uint64_t full[Cfg::kSlots], empty[Cfg::kSlots];
   uint64_t q_loaded, q_ready, q_free;
-  uint64_t s_full[2], s_empty[2], mma_done;
+  uint64_t s_full[2][2], s_empty[2][2], mma_done;   // [buffer][half]
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -176,9 +178,9 @@ __global__ void __launch_bounds__(KeyFewCfg<DH>::kThreads, 1)
     mbar_init(&sm.q_loaded, 1);
     mbar_init(&sm.q_ready, 1);
     mbar_init(&sm.q_free, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.s_empty[i], 4);   // one arrival per warp of a group
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sm.s_full[i / 2][i % 2], 1);
+      mbar_init(&sm.s_empty[i / 2][i % 2], 4);   // one arrival per warp of a group
     }
     mbar_init(&sm.mma_done, 1);
     fence_mbarrier_init();
@@ -289,7 +291,7 @@ __global__ void __launch_bounds__(KeyFewCfg<DH>::kThreads, 1)
       if (lane == 0) mbar_arrive(&sm.q_ready);
     }
   } else if (warp == Cfg::kWarpIssuer) {
-    const uint32_t idesc = idesc_bf16_f32(128, 0, false, false) | (uint32_t)(p.cols >> 3) << 17;
+    const int halves = p.cols > 128 ? 2 : 1;
     const uint64_t dk = smem_desc_sw128(smem_u32(sm.k[0]), 16, 1024);
     const uint64_t dq = smem_desc_sw128(smem_u32(sm.q), 16, 1024);
     // no swizzle: core matrices of 8 rows of 16 bytes 128 bytes apart, the second
@@ -306,21 +308,31 @@ __global__ void __launch_bounds__(KeyFewCfg<DH>::kThreads, 1)
       if (!(ok = wait(&sm.q_loaded, nseg & 1u)) || !(ok = wait(&sm.q_ready, nseg & 1u))) break;
       ++nseg;
       for (int j = 0; j < s.count; ++j) {
-        if (!(ok = wait(&sm.full[r.i], r.par)) || !(ok = wait(&sm.s_empty[b.i], b.par ^ 1u))) break;
-        tc_fence_after_sync();
+        if (!(ok = wait(&sm.full[r.i], r.par))) break;
         const uint64_t k = dk + (uint64_t)r.i * (Cfg::kKTile >> 4);
-        const uint32_t dS = tbase + 256u * b.i;
-        if (elect_one_sync()) {
+        for (int h = 0; h < halves; ++h) {
+          if (!(ok = wait(&sm.s_empty[b.i][h], b.par ^ 1u))) break;
+          tc_fence_after_sync();
+          const uint32_t dS = tbase + 256u * b.i + 128u * h;
+          const uint32_t idesc = idesc_bf16_f32(128, 0, false, false) |
+                                 (uint32_t)(min(128, p.cols - 128 * h) >> 3) << 17;
+          const uint64_t qh = dq + (uint64_t)h * (128 * 128 >> 4), lh = dl + (uint64_t)h * 128;
+          if (elect_one_sync()) {
 #pragma unroll
-          for (int kk = 0; kk < DH / 16; ++kk)
-            mma_bf16_ss(dS, k + (((kk / 4) * Cfg::kKBox + (kk % 4) * 32) >> 4),
-                        dq + (((kk / 4) * Cfg::kQBox + (kk % 4) * 32) >> 4), idesc,
-                        kk > 0 ? 1u : 0u);
-          mma_bf16_ss(dS, d1, dl, idesc, 1u);
-          mma_commit(&sm.s_full[b.i]);
-          mma_commit(&sm.empty[r.i]);
-          if (j + 1 == s.count) mma_commit(&sm.q_free);
+            for (int kk = 0; kk < DH / 16; ++kk)
+              mma_bf16_ss(dS, k + (((kk / 4) * Cfg::kKBox + (kk % 4) * 32) >> 4),
+                          qh + (((kk / 4) * Cfg::kQBox + (kk % 4) * 32) >> 4), idesc,
+                          kk > 0 ? 1u : 0u);
+            mma_bf16_ss(dS, d1, lh, idesc, 1u);
+            mma_commit(&sm.s_full[b.i][h]);
+            if (h + 1 == halves) {
+              mma_commit(&sm.empty[r.i]);
+              if (j + 1 == s.count) mma_commit(&sm.q_free);
+            }
+          }
+          __syncwarp();
         }
+        if (!ok) break;
         __syncwarp();
         r.step();
         b.step();
@@ -335,53 +347,62 @@ __global__ void __launch_bounds__(KeyFewCfg<DH>::kThreads, 1)
     const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
     const uint32_t in_head = (uint32_t)p.pad - 1u;   // (a power of two less one)
     uint32_t count = 0, par = 0;
-    auto release = [&] {
+    const int halves = p.cols > 128 ? 2 : 1;
+    auto release = [&](int h) {
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.s_empty[group]);
+      if (lane == 0) mbar_arrive(&sm.s_empty[group][h]);
     };
     while (ok && walk.next(p, s)) {
       for (int j = 0; j < s.count; ++j, ++count) {
         if ((count & 1u) != (uint32_t)group) continue;
         const int key0 = 128 * (s.block + j), key = key0 + tid;
-        if (!(ok = mbar_wait(&sm.s_full[group], par, abort))) break;
-        par ^= 1u;
-        tc_fence_after_sync();
-        // columns are summed by 64, and those sums added: the error of a long sum
-        // grows with their number
-        float total = 0.f;
-        uint32_t y0[32], y1[32];
-        tmem_ld_32x32b_x32(colS, y0);
-        tmem_ld_wait(y0);
         const bool masked = p.causal && key0 + 127 > s.q0;   // it reaches into the voting queries
         const uint32_t hidden = (uint32_t)max(0, key - s.q0);   // of a head's columns, the first
+        // columns are summed by 128 at most, and those sums added: the error of a long
+        // sum grows with their number
+        float total = 0.f;
 #pragma unroll 1
-        for (int c = 0; c < p.cols; c += 64) {   // the next 32 columns arrive meanwhile
+        for (int h = 0; h < halves; ++h) {
+          if (!(ok = mbar_wait(&sm.s_full[group][h], par, abort))) break;
+          tc_fence_after_sync();
+          const uint32_t col = colS + 128u * h;
+          const int cols = min(128, p.cols - 128 * h);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          const bool two = c + 32 < p.cols, more = c + 64 < p.cols;
-          if (two) tmem_ld_32x32b_x32(colS + c + 32, y1);
-          if (masked) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (((uint32_t)(c + e) & in_head) < hidden) y0[e] = 0xff800000u;
-          }
-          key_weights_add(y0, scale2, sum);
-          if (two) {
+          if (cols == 128 && !masked) {
+            uint32_t y0[32], y1[32], y2[32], y3[32];
+            tmem_ld_32x32b_x32(col, y0);
+            tmem_ld_32x32b_x32(col + 32, y1);
+            tmem_ld_wait(y0);
             tmem_ld_wait(y1);
-            if (more) tmem_ld_32x32b_x32(colS + c + 64, y0);
-            else release();   // S is in registers
-            if (masked) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (((uint32_t)(c + 32 + e) & in_head) < hidden) y1[e] = 0xff800000u;
-            }
+            tmem_ld_32x32b_x32(col + 64, y2);
+            tmem_ld_32x32b_x32(col + 96, y3);
+            key_weights_add(y0, scale2, sum);
             key_weights_add(y1, scale2, sum);
-            if (more) tmem_ld_wait(y0);
+            tmem_ld_wait(y2);
+            tmem_ld_wait(y3);
+            release(h);   // S is in registers
+            key_weights_add(y2, scale2, sum);
+            key_weights_add(y3, scale2, sum);
           } else {
-            release();
+#pragma unroll 1
+            for (int c = 0; c < cols; c += 32) {
+              uint32_t y[32];
+              tmem_ld_32x32b_x32(col + c, y);
+              tmem_ld_wait(y);
+              if (masked) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (((uint32_t)(128 * h + c + e) & in_head) < hidden) y[e] = 0xff800000u;
+              }
+              key_weights_add(y, scale2, sum);
+            }
+            release(h);
           }
           total += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         }
+        if (!ok) break;
+        par ^= 1u;
         if (key < s.L) {
           float* w = p.weights + ((size_t)s.b * p.Hkv + s.g) * p.stride + key;
           *w = p.accumulate ? *w + total : total;
