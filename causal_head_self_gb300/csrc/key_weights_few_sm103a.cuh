@@ -13,15 +13,17 @@
 // loaded, one S computed, one sum taken, and nothing is handed over.  (Walking
 // queries, a block of keys cost two tiles with a K, Q and log-sum-exp set of
 // their own: 61 us for 4 x 8 heads of 16384 to 32768 keys and 64 queries, against
-// 15 us of memory traffic.)  What bounds it are the exponentials: 1024 cycles per
-// SM for 128 keys and 256 queries.
+// 15 us of memory traffic.)  Now 43 us: the exponentials alone are 1024 cycles per SM
+// for 128 keys and 256 queries, 22 us in all, and a step of MMAs and waits, 382 cycles
+// to issue per 128 columns, feeds them; without the sums 36 us are left.
 //
 // Split: as in the paged decode, the blocks of all (sequence, K/V head) units
 // form a line, a unit's first place standing for the cost of its start, and each
 // CTA (one per SM) takes an equal part.  Blocks alternate between two groups of
 // four summing warps, each with an S buffer of its own, which is filled and freed by
 // halves of 128 columns: one half's next block is computed while the other half is
-// summed (whole buffers: XX us).
+// summed (by whole buffers 46 us instead of
+// 43; with four groups of summing warps 49).
 //
 // Query rows past the end of the sequence, and rows that pad the tile, are zeroed
 // in shared memory and get -inf for a log-sum-exp, so they weigh nothing; only
