@@ -390,7 +390,7 @@ __device__ __forceinline__ void key_weights_lse(KeyWeightsSmem<DH>& sm, const Ke
 template <int DH>
 __device__ __forceinline__ void key_weights_issuer(KeyWeightsSmem<DH>& sm,
                                                    const KeyWeightsParams& p, uint32_t tbase,
-                                                   int rank, volatile int* abort) {
+                                                   int rank, int lane, volatile int* abort) {
   using Cfg = KeyWeightsCfg<DH>;
   constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, false);
   const uint64_t desc = smem_desc_sw128(smem_u32(sm.slot[0]), 16, 1024);
@@ -414,9 +414,12 @@ __device__ __forceinline__ void key_weights_issuer(KeyWeightsSmem<DH>& sm,
     if (item >= p.items) break;
     const KeyWeightsItem it = key_weights_item(p, sm.lens, item, rank);
     if (it.t0 >= it.t1) {
-      // (an entry without a tile is passed in its turn: see KwRing's parity)
-      if (it.k0 < it.L && !(ok = wait_entry())) break;
-      if (it.k0 < it.L) (group ? l1 : l0).step();
+      // (an entry without a tile is passed in its turn: see KwRing's parity.  Nothing
+      // else would keep its group from running several rounds of entries ahead)
+      if (it.k0 >= it.L) continue;
+      if (!(ok = wait_entry())) break;
+      if (lane == 0) mbar_arrive(&sm.l_empty[group][group ? l1.i : l0.i]);
+      (group ? l1 : l0).step();
       continue;
     }
     // K to tensor memory, once the last item's MMAs have read theirs
@@ -589,6 +592,8 @@ __device__ __forceinline__ void key_weights_sums(KeyWeightsSmem<DH>& sm, const K
       total = 0.f;
     }
     release(&sm.l_empty[group][l.i]);
+    // a tile's S was there, so its issuing warp has passed the entry
+    if (!(en.x & kKwNone) && tid == 0) mbar_arrive(&sm.l_empty[group][l.i]);
   }
 }
 
@@ -617,7 +622,9 @@ __global__ void __launch_bounds__(384, 1)
     }
     for (int i = 0; i < 2 * Cfg::kLse; ++i) {
       mbar_init(&sm.l_full[0][i], 1);    // (both groups' rings lie in a row)
-      mbar_init(&sm.l_empty[0][i], 4);   // one arrival per summing warp of a group
+      // one arrival per summing warp of a group, and one for the issuing warp: an entry
+      // may be written again once both have passed it
+      mbar_init(&sm.l_empty[0][i], 5);
     }
     for (int i = 0; i < Cfg::kBuffers; ++i) {
       mbar_init(&sm.s_full[i], 1);
@@ -661,7 +668,7 @@ __global__ void __launch_bounds__(384, 1)
   } else if (warp >= Cfg::kWarpLse) {
     key_weights_lse<DH>(sm, p, rank, warp - Cfg::kWarpLse, lane, abort);
   } else if (warp == Cfg::kWarpIssuer) {
-    key_weights_issuer<DH>(sm, p, tbase, rank, abort);
+    key_weights_issuer<DH>(sm, p, tbase, rank, lane, abort);
   } else {
     key_weights_sums<DH>(sm, p, tbase, warp / 4, rank, abort);
   }

@@ -689,6 +689,35 @@ def test_calls_on_two_streams_at_once():
     assert all(same_bits(o, s["o"]) for o, s in zip(outs, eager))
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,S,Dh,queries,window", [
+    (50, 40, 8, 663, 64, 6, 83), (60, 24, 8, 1283, 64, 7, 171), (120, 8, 8, 280, 256, 38, 25),
+    (100, 8, 8, 512, 256, 126, 13), (33, 3, 3, 2493, 128, 12, 15), (188, 33, 3, 150, 128, 70, 8)])
+def test_key_weights_where_most_keys_have_no_query(B, Hq, Hkv, S, Dh, queries, window):
+    # long runs of key blocks without a tile, between blocks that have some
+    gen = torch.Generator(device="cuda").manual_seed(S)
+    q, k = (torch.randn((B, h, S, Dh), generator=gen, device="cuda").to(torch.bfloat16)
+            for h in (Hq, Hkv))
+    lse = torch.randn((B, Hq, S), generator=gen, device="cuda") + 6
+    sl = torch.randint(0, S + 1, (B,), generator=gen, device="cuda", dtype=torch.int32)
+    w = torch.full((B, Hkv, S), 3.0, device="cuda")
+    chs.attn_key_weights(q, k, lse, w, sl, queries=queries, window=window, accumulate=False)
+    status_ok()
+    worst = 0.0
+    for b, n in enumerate(sl.tolist()):
+        first = max(0, n - queries)
+        lo = max(0, first - window + 1)   # the first key that any of them sees
+        assert (w[b, :, n:] == 3.0).all() and (w[b, :, :min(lo, n)] == 0.0).all()
+        i, j = (torch.arange(x, n, device="cuda") for x in (first, lo))
+        seen = (j <= i[:, None]) & (j > i[:, None] - window)
+        kg = k[b, :, lo:n].double().repeat_interleave(Hq // Hkv, 0)
+        qh = q[b, :, first:n].double()
+        p = torch.exp(qh @ kg.transpose(1, 2) * Dh ** -0.5 - lse[b, :, first:n, None].double())
+        want = torch.where(seen, p, 0.0).sum(1).view(Hkv, Hq // Hkv, -1).sum(1)
+        # (paged_ref.key_weights' bound, with |q| . |k| / sqrt(Dh) <= 6 sqrt(Dh) and |lse| <= 12)
+        rel = (Dh + 1) * 2.0 ** -23 * (6 * Dh ** 0.5 + 12) + 2.0 ** -18
+        assert ((w[b, :, lo:n].double() - want).abs() <= rel * want).all()
+
+
 @pytest.mark.parametrize("queries,Hq", [(0, 8), (40, 8), (40, 40)])
 def test_key_weights_replay_bit_for_bit_on_two_streams(queries, Hq):
     B, Hkv, S, Dh = 2, 2, 700, 64
