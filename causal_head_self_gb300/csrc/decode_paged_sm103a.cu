@@ -143,13 +143,12 @@ cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorM
                  dim3(DecodePagedCfg<DH>::kThreads), smem, stream, mq, mk, mv, prm);
   if (e != cudaSuccess) return e;
   // Many partial results in few units take more threads, as long as each SM has a
-  // block at most: 4 x 32 heads on 8, 8192 keys 29.2 -> 27.3 us for the step, 8 heads
-  // on 1, 16384 keys 44 -> 31.7; 16 x 32 heads on 8, 512 keys would go 12.9 -> 17.9.
-  // With weights, whose blocks are then larger too, it takes more of them: 4 x 32 heads
-  // on 8, 16384 to 32768 keys (20 partial results) 69 us with 256 threads, 72 with 1024;
-  // 2 x 32 on 8, 1024 keys (40) 13.1 -> 11.7.
+  // block at most: 8 heads on 1, 16384 keys 44 -> 32 us for the step; 2 x 32 heads on 8,
+  // 8192 keys 19.8 -> 15.5.  Few do not: 4 x 32 heads on 8 with weights, 16384 to 32768
+  // keys (20 partial results) 69 -> 72 us.  (Weights have no say: the output's bits do
+  // not depend on whether they are asked for.)
   const int partials = REP * (prm.ctas / (prm.B * prm.Hkv * prm.row_blocks) + 1);
-  return partials > (prm.weights ? 32 : 16) && prm.B * prm.Hq <= dev.num_sms
+  return partials > 32 && prm.B * prm.Hq <= dev.num_sms
              ? launch_join<DH, REP, 1024>(prm, stream)
              : launch_join<DH, REP, 256>(prm, stream);
 }

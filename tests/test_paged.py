@@ -789,6 +789,21 @@ def _wide_state(seed, lens):
     return s
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,Dh", [(2, 16, 16, 256), (4, 32, 8, 128), (12, 6, 3, 64), (1, 130, 1, 128)])
+def test_asking_for_weights_does_not_change_the_output(B, Hq, Hkv, Dh):
+    gen = torch.Generator(device="cuda").manual_seed(Dh)
+    page, cols = 64, 220
+    kp, vp = (torch.randn((B * cols, Hkv, page, Dh), generator=gen, device="cuda").to(torch.bfloat16)
+              for _ in range(2))
+    table = torch.randperm(B * cols, generator=gen, device="cuda").to(torch.int32).view(B, cols)
+    sl = torch.randint(1, cols * page + 1, (B,), generator=gen, device="cuda", dtype=torch.int32)
+    q = queries(B, Hq, Dh, seed=Dh).cuda()
+    weights = torch.zeros(B, Hkv, cols * page, device="cuda")
+    o = chs.attn_decode_paged(q, kp, vp, table, sl)
+    assert same_bits(o, chs.attn_decode_paged(q, kp, vp, table, sl, weights=weights))
+    status_ok()
+
+
 def test_steps_with_wide_tables_share_nothing():
     lens = [[600, 64, 30], [100, 640, 5]]
     eager = [_wide_state(i, x) for i, x in enumerate(lens)]
