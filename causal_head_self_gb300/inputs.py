@@ -84,6 +84,11 @@ WORKLOADS = {
                                                            Tmax=32768, page=16, Dh=128, lmin=16384,
                                                            lmax=32768, window=0, weights=True,
                                                            seed=16),
+    # one K/V head under a sliding window: a step in one launch
+    "paged_decode_mqa_b16_h8kv1_t32768_d256_w4096": dict(kind="paged", B=16, Hq=8, Hkv=1,
+                                                         Tmax=32768, page=32, Dh=256, lmin=16384,
+                                                         lmax=32768, window=4096, weights=False,
+                                                         seed=20),
     # the weights that a prompt's keys received: from every query, and from the last 64
     "key_weights_gqa_b1_h32kv8_s8192_d128": dict(kind="key_weights", B=1, Hq=32, Hkv=8, S=8192,
                                                  Dh=128, queries=0, seed=17),
