@@ -516,13 +516,17 @@ extern "C" int attn_decode_noalloc(const void* q, const void* kcache, const void
 // The paged cache: append, decode, key weights, eviction.
 namespace {
 
+// Rows of a sequence, or of a list of them, at most: positions are 32-bit, and the kernels
+// count a few thousand past the end.
+constexpr int kMostRows = 0x7fffffff - 16384;
+
 // Shape checks that every paged entry point shares.
 int paged_check(int B, int Hkv, const chs::PagedCache& c, int Dh) {
   if (B < 0 || Hkv < 1 || c.num_pages < 1 || c.cols < 1 || c.page < 1) return ATTN_ERR_INVALID_ARG;
   if (Dh != 64 && Dh != 128 && Dh != 256) return ATTN_ERR_UNSUPPORTED;
   if (c.page % 8 != 0) return ATTN_ERR_UNSUPPORTED;
-  // positions, and a pool's (page, head) pairs, are 32-bit
-  if ((long long)c.cols * c.page > 0x7fffffffLL - 16384) return ATTN_ERR_INVALID_ARG;
+  if ((long long)c.cols * c.page > kMostRows) return ATTN_ERR_INVALID_ARG;
+  // a pool's (page, head) pairs are 32-bit
   if ((long long)c.num_pages * Hkv > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
 }
@@ -699,10 +703,12 @@ extern "C" int attn_cache_evict(void* kpages, void* vpages, float* weights, int 
     weights_out_stride = weights_stride;
   }
   if (budget < 1 || recent < 0 || recent > budget) return ATTN_ERR_INVALID_ARG;
+  // the kernels step through `keep` in 32 bits, up to a block's rows past its end
+  if (budget > kMostRows) return ATTN_ERR_INVALID_ARG;
   const long long rows = (long long)cols * page;
   const long long most = budget < rows ? budget : rows;   // rows that a sequence may end with
   if (weights_stride < rows || weights_out_stride < most || cols_out < 1 ||
-      (long long)cols_out * page > 0x7fffffffLL - 16384 || (long long)cols_out * page < most)
+      (long long)cols_out * page > kMostRows || (long long)cols_out * page < most)
     return ATTN_ERR_INVALID_ARG;
   if (table_out == table && cols_out != cols) return ATTN_ERR_INVALID_ARG;
   if (weights_out == weights && weights_out_stride != weights_stride) return ATTN_ERR_INVALID_ARG;

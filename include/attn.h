@@ -368,7 +368,7 @@ int attn_key_weights(const void* q, const void* k, const float* lse, const int* 
  *   newlens      [B]  written: min(seqlens[b], budget).  Not seqlens itself.
  *   keep         [B, Hkv, budget]  written: the former row of each kept row,
  *                ascending, then -1
- * budget >= 1, 0 <= recent <= budget, and cols_out * page and
+ * 1 <= budget <= 2^31 - 16385, 0 <= recent <= budget, and cols_out * page and
  * weights_out_stride hold min(budget, cols * page) rows
  * (ATTN_ERR_INVALID_ARG otherwise).  A length outside its range leaves the
  * sequence alone.
