@@ -153,7 +153,7 @@ cudaError_t launch_key_weights(const void* q, const void* k, const float* lse, c
   prm.by_batch = make_fixed_div((uint32_t)(B * Hkv));
   // a cluster per item where that fills the SMs no more than once, and leaves
   // each CTA a tile
-  const long long tiles = pad < 128 ? (prm.G * pad + 127) / 128
+  const long long tiles = pad < 128 ? key_weights_head_tiles(G, pad)
                                     : (long long)prm.G * ((queries ? queries : S) + 127) / 128;
   prm.split = 1;
   prm.split_log2 = 0;

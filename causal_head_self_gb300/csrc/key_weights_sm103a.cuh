@@ -133,6 +133,13 @@ struct KeyWeightsItem {
   int b, g, k0, L, q0, q_end, n, t0, t1;
 };
 
+// Tiles of G heads of `pad` columns (a power of two up to 128) each.  Counted in heads:
+// their columns together may pass 32 bits.
+__host__ __device__ __forceinline__ int key_weights_head_tiles(int G, int pad) {
+  const int heads = 128 / pad;
+  return (G - 1) / heads + 1;
+}
+
 // `lens`: the lengths of the first KeyWeightsCfg::kLens sequences.
 __device__ __forceinline__ int key_weights_len(const KeyWeightsParams& p, int b) {
   const int n = p.seqlens ? __ldcg(p.seqlens + b) : p.S;
@@ -156,7 +163,7 @@ __device__ __forceinline__ KeyWeightsItem key_weights_item(const KeyWeightsParam
   if (p.window > 0) it.q_end = (int)min((long long)it.L, (long long)it.k0 + 127 + p.window);
   it.n = it.q_end > it.q0 && it.k0 < it.L ? (it.q_end - it.q0 + 127) / 128 : 0;
   int tiles = it.n * p.G;
-  if (p.pad < 128 && tiles > 0) tiles = (p.G * p.pad + 127) / 128;
+  if (p.pad < 128 && tiles > 0) tiles = key_weights_head_tiles(p.G, p.pad);
   // (split is a power of two)
   it.t0 = (int)((long long)tiles * rank >> p.split_log2);
   it.t1 = (int)((long long)tiles * (rank + 1) >> p.split_log2);
@@ -338,7 +345,7 @@ __device__ __forceinline__ void key_weights_lse(KeyWeightsSmem<DH>& sm, const Ke
     e_lo = p.causal ? c0 : -(1 << 30);
     e_hi = p.window > 0 && p.window < 128 - c0 ? c0 + p.window : 128;
     e_end = min(it.q_end - query, p.pad);
-    e_cols = min(128, (p.G - first) * p.pad);   // of heads that there are
+    e_cols = min(heads_per_tile, p.G - first) * p.pad;   // of heads that there are
     const uint32_t tile = before + (uint32_t)(t - it.t0), use = tile / Cfg::kBuffers;
     f = (it.t1 - it.t0 > 1 ? kKwPair : 0) |
         (e_lo <= -127 && e_hi >= p.pad && e_end == p.pad && e_cols == 128 ? kKwWhole : 0) |
