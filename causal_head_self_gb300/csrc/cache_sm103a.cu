@@ -1,5 +1,7 @@
 // cache_sm103a.cu -- host launchers of the paged cache's kernels: append, key
 // weights of a prompt, eviction.
+#include <algorithm>
+
 #include "cache_sm103a.cuh"
 #include "key_weights_few_sm103a.cuh"
 #include "key_weights_sm103a.cuh"
@@ -94,12 +96,20 @@ cudaError_t launch_key_weights(const void* q, const void* k, const float* lse, c
                                float* weights, int stride, int B, int Hq, int Hkv, int S, int Dh,
                                int causal, int window, int queries, int accumulate,
                                float scale_log2, const DeviceInfo& dev, cudaStream_t stream) {
+  const int G = Hq / Hkv;
+  // Every row votes: one form, however it is asked for.  With short prompts and grouped
+  // heads the form for few voting queries, with others the general one; GPU time, general
+  // -> few: 64 prompts of 8, 17, 32 rows, 32 heads on 8: 14.3 -> 10.8, 14.4 -> 13.5, 14.4
+  // -> 11.1 us; of 33 rows 16.8 -> 20.5, of 64 rows 15.8 -> 18.1.  32 heads on 32: 17
+  // rows 18.1 -> 19.4, 64 rows 18.8 -> 26.  (300 prompts, 8 heads on one: 8 rows 13.0 ->
+  // 11.0, 17 rows 13.1 -> 14.2, 32 rows 13.1 -> 11.4.)
+  if (queries == 0 || queries >= S) queries = S <= 32 && G > 1 ? S : 0;
   // rows per head in a tile: with up to 64 voting queries it holds several heads'
   int pad = 128;
   if (queries > 0)
     while (pad > 16 && pad / 2 >= queries) pad /= 2;
   const double per_lse = -1.4426950408889634 / (double)scale_log2;   // -log2(e) / scale_log2
-  const int G = Hq / Hkv, most = Dh == 256 ? KeyFewCfg<256>::kCols : KeyFewCfg<128>::kCols;
+  const int most = Dh == 256 ? KeyFewCfg<256>::kCols : KeyFewCfg<128>::kCols;
   // The whole group's voting queries in one tile (and no window, which would leave
   // most blocks of keys without any): the queries stay, the keys pass by.
   if (queries > 0 && queries <= 128 && window == 0 && (long long)G * pad <= most) {
@@ -141,7 +151,7 @@ cudaError_t launch_key_weights(const void* q, const void* k, const float* lse, c
   prm.B = B;
   prm.Hq = Hq;
   prm.Hkv = Hkv;
-  prm.G = Hq / Hkv;
+  prm.G = G;
   prm.S = S;
   prm.causal = causal;
   prm.window = window;
@@ -149,12 +159,14 @@ cudaError_t launch_key_weights(const void* q, const void* k, const float* lse, c
   prm.accumulate = accumulate;
   prm.items = (S + 127) / 128 * B * Hkv;
   prm.pad = pad;
+  prm.head_tiles = (G - 1) / (128 / pad) + 1;   // (heads: their columns may pass 32 bits)
   prm.by_heads = make_fixed_div((uint32_t)Hkv);
   prm.by_batch = make_fixed_div((uint32_t)(B * Hkv));
   // a cluster per item where that fills the SMs no more than once, and leaves
-  // each CTA a tile
-  const long long tiles = pad < 128 ? key_weights_head_tiles(G, pad)
-                                    : (long long)prm.G * ((queries ? queries : S) + 127) / 128;
+  // each CTA a tile (of the longest sequence's first keys: those have the most)
+  long long voting = queries ? queries : S;
+  if (window > 0) voting = std::min(voting, (long long)window + 127);
+  const long long tiles = pad < 128 ? prm.head_tiles : G * ((voting + 127) / 128);
   prm.split = 1;
   prm.split_log2 = 0;
   while (prm.split < 8 && 2LL * prm.split * prm.items <= dev.num_sms && 2LL * prm.split <= tiles) {

@@ -57,6 +57,7 @@ struct KeyWeightsParams {
   int items;             // key blocks * B * Hkv
   FixedDiv by_heads, by_batch;   // by Hkv, by B * Hkv
   int pad;               // columns of a tile per head: 128, or less with few voting queries
+  int head_tiles;        // tiles that the group's heads take, `pad` columns each
   int split, split_log2; // CTAs per item, a power of two
   float scale_log2;
   float lse_hi, lse_lo;  // ln 2-free: -log2(e) / scale_log2 in two parts
@@ -133,13 +134,6 @@ struct KeyWeightsItem {
   int b, g, k0, L, q0, q_end, n, t0, t1;
 };
 
-// Tiles of G heads of `pad` columns (a power of two up to 128) each.  Counted in heads:
-// their columns together may pass 32 bits.
-__host__ __device__ __forceinline__ int key_weights_head_tiles(int G, int pad) {
-  const int heads = 128 / pad;
-  return (G - 1) / heads + 1;
-}
-
 // `lens`: the lengths of the first KeyWeightsCfg::kLens sequences.
 __device__ __forceinline__ int key_weights_len(const KeyWeightsParams& p, int b) {
   const int n = p.seqlens ? __ldcg(p.seqlens + b) : p.S;
@@ -163,7 +157,7 @@ __device__ __forceinline__ KeyWeightsItem key_weights_item(const KeyWeightsParam
   if (p.window > 0) it.q_end = (int)min((long long)it.L, (long long)it.k0 + 127 + p.window);
   it.n = it.q_end > it.q0 && it.k0 < it.L ? (it.q_end - it.q0 + 127) / 128 : 0;
   int tiles = it.n * p.G;
-  if (p.pad < 128 && tiles > 0) tiles = key_weights_head_tiles(p.G, p.pad);
+  if (p.pad < 128 && tiles > 0) tiles = p.head_tiles;
   // (split is a power of two)
   it.t0 = (int)((long long)tiles * rank >> p.split_log2);
   it.t1 = (int)((long long)tiles * (rank + 1) >> p.split_log2);
