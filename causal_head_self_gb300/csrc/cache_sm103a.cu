@@ -97,13 +97,13 @@ cudaError_t launch_key_weights(const void* q, const void* k, const float* lse, c
                                int causal, int window, int queries, int accumulate,
                                float scale_log2, const DeviceInfo& dev, cudaStream_t stream) {
   const int G = Hq / Hkv;
-  // Every row votes: one form, however it is asked for.  With short prompts and grouped
-  // heads the form for few voting queries, with others the general one; GPU time, general
-  // -> few: 64 prompts of 8, 17, 32 rows, 32 heads on 8: 14.3 -> 10.8, 14.4 -> 13.5, 14.4
-  // -> 11.1 us; of 33 rows 16.8 -> 20.5, of 64 rows 15.8 -> 18.1.  32 heads on 32: 17
-  // rows 18.1 -> 19.4, 64 rows 18.8 -> 26.  (300 prompts, 8 heads on one: 8 rows 13.0 ->
-  // 11.0, 17 rows 13.1 -> 14.2, 32 rows 13.1 -> 11.4.)
-  if (queries == 0 || queries >= S) queries = S <= 32 && G > 1 ? S : 0;
+  // Every row votes: one form, however it is asked for; short prompts take the one for few
+  // voting queries, others the general one.  GPU time in us, general -> few, at 8, 17, 32,
+  // 33 and 64 rows: 64 prompts, 32 heads on 8: 14.3 -> 10.4, 14.4 -> 13.5, 14.4 -> 9.6,
+  // 16.8 -> 17.2, 15.7 -> 16.5; 32 heads on 32: 18.1 -> 17.8, 18.1 -> 17.8, 18.1 -> 16.4,
+  // 18.8 -> 19.8, 18.8 -> 22.9; 300 prompts, 8 heads on one: 13.0 -> 10.6, 13.0 -> 14.2,
+  // 13.1 -> 10.4, 16.2 -> 14.9, 14.9 -> 15.9.
+  if (queries == 0 || queries >= S) queries = S <= 32 ? S : 0;
   // rows per head in a tile: with up to 64 voting queries it holds several heads'
   int pad = 128;
   if (queries > 0)

@@ -25,9 +25,12 @@
 // summed (by whole buffers 46 us instead of
 // 43; with four groups of summing warps 49).
 //
-// Query rows past the end of the sequence, and rows that pad the tile, are zeroed
-// in shared memory and get -inf for a log-sum-exp, so they weigh nothing; only
-// blocks that reach into the voting queries themselves are masked.
+// Rows that pad the tile, and those past the end of a head's queries, become copies of the
+// head's last voting query (its first head's, past the last head), which every key of the
+// sequence is visible to, with a log-sum-exp of 3e38: their terms are 0 whenever that
+// query's own are a number.  (Rows of zeros would meet an infinite key as 0 * inf = NaN,
+// and -inf would make NaN of an infinite score.)  Only blocks that reach into the voting
+// queries themselves are masked.
 #pragma once
 
 #include <cstdint>
@@ -257,35 +260,40 @@ __global__ void __launch_bounds__(KeyFewCfg<DH>::kThreads, 1)
     }
   } else if (warp == Cfg::kWarpLse) {
     uint32_t nseg = 0;
+    const int pad_log2 = 31 - __clz(p.pad);   // (a power of two)
     while (ok && walk.next(p, s)) {
       const int n = s.L - s.q0;   // voting queries
       const float* lse = p.lse + ((size_t)s.b * p.Hq + (size_t)s.g * p.G) * p.S + s.q0;
       float x[Cfg::kCols / 32];
 #pragma unroll
       for (int k = 0; k < Cfg::kCols / 32; ++k) {
-        const int col = 32 * k + lane, h = col / p.pad, i = col - h * p.pad;
-        x[k] = h < p.G && i < n ? __ldcg(lse + (size_t)h * p.S + i) : INFINITY;
+        const int col = 32 * k + lane, h = col >> pad_log2, i = col - h * p.pad;
+        x[k] = h < p.G && i < n ? __ldcg(lse + (size_t)h * p.S + i) : 0.f;
       }
       if (nseg > 0 && !(ok = wait(&sm.q_free, (nseg - 1) & 1u))) break;
+#pragma unroll
+      for (int k = 0; k < Cfg::kCols / 32; ++k)
+        sm.nlse[0][32 * k + lane] = key_weights_lse_parts(x[k], p.lse_hi, p.lse_lo);
       if (!(ok = wait(&sm.q_loaded, nseg & 1u))) break;
       ++nseg;
+      if (n < p.pad || p.G * p.pad < p.cols) {   // there are rows without a query
+#pragma unroll 1
+        for (int col = lane; col < p.cols; col += 32) {
+          const int h = col >> pad_log2;
+          if (h < p.G && col - h * p.pad < n) continue;
+          sm.nlse[0][col] = make_uint4(0x0000ff7fu, 0u, 0u, 0u);   // the lowest bf16 number
+          const int from = (h < p.G ? h * p.pad : 0) + n - 1;
+#pragma unroll 1
+          for (int box = 0; box < Cfg::kBoxes; ++box) {
+            uint8_t* q = sm.q + box * Cfg::kQBox;
+            uint4 y[8];   // (a row's 16-byte pieces are swizzled by its number)
 #pragma unroll
-      for (int k = 0; k < Cfg::kCols / 32; ++k) {
-        const int col = 32 * k + lane;
-        if (col >= p.cols) continue;
-        if (x[k] == INFINITY) {   // no query: a zero row, and 2^-inf
-          for (int e = 0; e < Cfg::kBoxes * 8; ++e)
-            st_shared_v4(smem_u32(sm.q) + (e / 8) * Cfg::kQBox + col * 128 + (e % 8) * 16, 0u, 0u,
-                         0u, 0u);
-          sm.nlse[0][col] = make_uint4(0x0000ff80u, 0u, 0u, 0u);
-        } else {
-          // -lse / scale to more than 32 bits, and its three bf16 parts
-          const float v = x[k] * p.lse_hi;
-          const float rest = fmaf(x[k], p.lse_hi, -v) + x[k] * p.lse_lo;
-          const float a = __bfloat162float(__float2bfloat16_rn(v));
-          const float b = __bfloat162float(__float2bfloat16_rn(v - a));
-          sm.nlse[0][col] =
-              make_uint4(pack_bf16x2(a, b), pack_bf16x2((v - a - b) + rest, 0.f), 0u, 0u);
+            for (int e = 0; e < 8; ++e)
+              y[e] = *reinterpret_cast<const uint4*>(q + from * 128 + ((e ^ from) & 7) * 16);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<uint4*>(q + col * 128 + ((e ^ col) & 7) * 16) = y[e];
+          }
         }
       }
       fence_proxy_async_smem();   // (the MMA reads them)

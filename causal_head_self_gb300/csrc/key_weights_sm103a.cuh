@@ -114,6 +114,7 @@ struct KeyWeightsSmem {
   // three bf16 parts per column and five zeros: the first eight of the step's 16
   // columns (8-row core matrices, one after another)
   uint4 nlse[2][Cfg::kLse][128];
+  uint4 zero[128];                           // its second eight, of every entry
   KeyWeightsEntry entry[2][Cfg::kLse];
   float hand[Cfg::kHand][128];               // one group's sums for the other
   float parts[Cfg::kMaxSplit][128];          // the cluster's sums (first CTA)
@@ -219,6 +220,19 @@ struct KwRing {
     }
   }
 };
+
+// A log-sum-exp's eight columns of the extra step: -lse / scale to more than 32 bits in
+// three bf16 parts, and zeros.  An infinite one is its first part alone (the others would
+// be NaN): a row with lse = +inf then weighs exp(s - inf) = 0, as the definition has it.
+__device__ __forceinline__ uint4 key_weights_lse_parts(float lse, float hi, float lo) {
+  const float v = lse * hi;
+  const float rest = fmaf(lse, hi, -v) + lse * lo;
+  const float a = __bfloat162float(__float2bfloat16_rn(v));
+  const float b = __bfloat162float(__float2bfloat16_rn(v - a));
+  const bool whole = isinf(a);
+  return make_uint4(pack_bf16x2(a, whole ? 0.f : b),
+                    whole ? 0u : pack_bf16x2((v - a - b) + rest, 0.f), 0u, 0u);
+}
 
 template <int DH>
 __device__ __forceinline__ void key_weights_producer(KeyWeightsSmem<DH>& sm,
@@ -365,17 +379,12 @@ __device__ __forceinline__ void key_weights_lse(KeyWeightsSmem<DH>& sm, const Ke
 #pragma unroll
     for (int d = 0; d < D; ++d) {
       if (!__all_sync(0xffffffffu, mbar_wait(&sm.l_empty[group][l.i], l.par ^ 1u, abort))) return;
+      if (!(flags[d] & (kKwNone | kKwEnd))) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        // -lse / scale to more than 32 bits, and its three bf16 parts
-        const float v = x[d][k] * p.lse_hi;
-        const float rest = fmaf(x[d][k], p.lse_hi, -v) + x[d][k] * p.lse_lo;
-        const float a = __bfloat162float(__float2bfloat16_rn(v));
-        const float b = __bfloat162float(__float2bfloat16_rn(v - a));
-        sm.nlse[group][l.i][32 * k + lane] =
-            make_uint4(pack_bf16x2(a, b), pack_bf16x2((v - a - b) + rest, 0.f), 0u, 0u);
+        for (int k = 0; k < 4; ++k)
+          sm.nlse[group][l.i][32 * k + lane] = key_weights_lse_parts(x[d][k], p.lse_hi, p.lse_lo);
+        fence_proxy_async_smem();   // (the MMA reads them)
       }
-      fence_proxy_async_smem();   // (the MMA reads them)
       if (lane == 0)
         sm.entry[group][l.i] =
             KeyWeightsEntry{flags[d], lo[d], hi[d], end[d], out[d], rows[d], cols[d]};
@@ -399,8 +408,10 @@ __device__ __forceinline__ void key_weights_issuer(KeyWeightsSmem<DH>& sm,
     return __all_sync(0xffffffffu, mbar_wait(bar, par, abort));
   };
   // the log-sum-exps' step: no swizzle, core matrices of 8 rows of 16 bytes
-  // 128 bytes apart; the second eight columns, which meet zeros, are the first again
+  // 128 bytes apart; the second eight columns, which meet zeros too, lie apart (the
+  // first again would do but for infinite ones: 0 * inf is NaN)
   const uint64_t plain = ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
+  const uint32_t zero = smem_u32(sm.zero);
   KwRing<Cfg::kSlots> r;
   KwRing<Cfg::kBuffers> s;
   KwRing<Cfg::kLse> l0, l1;   // the groups' entries
@@ -451,7 +462,8 @@ __device__ __forceinline__ void key_weights_issuer(KeyWeightsSmem<DH>& sm,
       const uint64_t q = desc + (uint64_t)r.i * (Cfg::kTile >> 4);
       const uint32_t dS = tbase + 128u * s.i;
       // (a shared address of a cluster's CTA has its rank above the descriptor's bits)
-      const uint64_t lse = plain | ((smem_u32(sm.nlse[group][group ? l1.i : l0.i]) >> 4) & 0x3FFFu);
+      const uint32_t parts = smem_u32(sm.nlse[group][group ? l1.i : l0.i]);
+      const uint64_t lse = plain | ((parts >> 4) & 0x3FFFu) | ((zero - parts) >> 4 << 16);
       if (elect_one_sync()) {
 #pragma unroll
         for (int kk = 0; kk < DH / 16; ++kk)
@@ -643,6 +655,8 @@ __global__ void __launch_bounds__(384, 1)
     tmem_alloc(&sm.tmem_base, Cfg::kCols);
     tmem_relinquish();
   }
+  for (int i = threadIdx.x; i < 128; i += Cfg::kThreads) sm.zero[i] = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();   // (the MMA reads them)
   // (the lengths may come from the previous kernel)
   griddep_wait();
   for (int b = threadIdx.x; b < p.B; b += Cfg::kThreads) {

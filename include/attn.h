@@ -341,6 +341,8 @@ int attn_decode_paged_workspace(int B, int Hq, int Hkv, int page, int cols, int 
  *   causal, window, scale  as in attn_fwd_lse (a scale below 1e-18 is
  *            ATTN_ERR_INVALID_ARG here);  accumulate as above
  * (With causal = 0 a padded prompt's lse has to be that of its real rows.)
+ * Infinities and NaN in q, k and lse give what the formula gives, to the keys
+ * that see them alone: a voting row with lse = +inf weighs nothing.
  */
 int attn_key_weights(const void* q, const void* k, const float* lse, const int* seqlens,
                      float* weights, int weights_stride, int B, int Hq, int Hkv, int S, int Dh,

@@ -57,3 +57,54 @@ def test_every_row_votes_however_it_is_said(Hq, Hkv, S, Dh, window):
         got.append(w)
     assert ((got[0].cpu().double() - want).abs() <= rtol * want).all()
     assert all(same_bits(w, got[0]) for w in got)
+
+
+# (Hq, Hkv, S, Dh, queries, causal, window): the general kernel, the same with several heads
+# per tile, and the one for few voting queries, whose tiles are padded here
+SPECIAL = [(2, 2, 300, 64, 0, True, 0), (4, 2, 260, 128, 0, True, 90), (2, 1, 200, 256, 0, False, 0),
+           (12, 1, 300, 128, 40, True, 0), (5, 1, 300, 64, 20, True, 70),
+           (8, 2, 300, 64, 20, True, 0), (3, 1, 150, 128, 7, True, 0), (5, 1, 200, 256, 9, True, 0),
+           (6, 2, 300, 64, 33, False, 0), (4, 2, 300, 128, 128, True, 0)]
+
+
+@pytest.mark.parametrize("kind", ["lse +inf", "lse -inf", "lse nan", "key -inf", "key +inf", "query nan"])
+@pytest.mark.parametrize("Hq,Hkv,S,Dh,queries,causal,window", SPECIAL)
+def test_key_weights_of_values_that_are_not_numbers(Hq, Hkv, S, Dh, queries, causal, window, kind):
+    gen = torch.Generator().manual_seed(S + Hq)
+    lens, G = [S, S - 30], Hq // Hkv
+    q, k = (torch.randn((2, h, S, Dh), generator=gen).to(torch.bfloat16) for h in (Hq, Hkv))
+    lse = 5 + torch.randn((2, Hq, S), generator=gen)
+    for b, n in enumerate(lens):
+        first = n - (queries or n)
+        rows = torch.arange(first, n)[torch.rand(n - first, generator=gen) < 0.3]
+        if kind.startswith("lse"):
+            lse[b, 0, rows] = float(kind[4:])
+            lse[b, Hq - 1, n - 1] = float(kind[4:])
+        elif kind.startswith("key"):
+            # its scores are infinite, not NaN: each query has the same sign there
+            q[b, :, :, 0] = q[b, :, :, 0].abs().clamp(min=0.1)
+            k[b, 0, ::7, 0] = float(kind[4:])
+        else:
+            q[b, 0, first + (n - first) // 2] = math.nan
+        lse[b, :, n:], q[b, :, n:], k[b, :, n:] = math.nan, math.nan, math.nan
+    want = torch.zeros(2, Hkv, S, dtype=torch.float64)
+    for b, n in enumerate(lens):
+        i = torch.arange(n - (queries or n), n)[:, None]
+        j = torch.arange(n)[None]
+        seen = (j <= i) if causal else torch.ones(len(i), n, dtype=torch.bool)
+        if window:
+            seen &= j > i - window
+        for h in range(Hq):
+            z = q[b, h, i[:, 0]].double() @ k[b, h // G, :n].double().t() * Dh ** -0.5
+            p = torch.exp(z - lse[b, h, i].double())
+            want[b, h // G, :n] += torch.where(seen, p, 0.0).sum(0)
+    w = torch.zeros(2, Hkv, S, device="cuda")
+    chs.attn_key_weights(q.cuda(), k.cuda(), lse.cuda(), w, torch.tensor(lens, dtype=torch.int32).cuda(),
+                         queries=queries, causal=causal, window=window, accumulate=False)
+    status_ok()
+    got = w.cpu().double()
+    assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.isinf(), want.isinf())
+    finite = want.isfinite()
+    # (paged_ref.key_weights' bound, with |q| . |k| / sqrt(Dh) <= 6 sqrt(Dh) and |lse| <= 12)
+    rel = (Dh + 1) * 2.0 ** -23 * (6 * Dh ** 0.5 + 12) + 2.0 ** -18
+    assert ((got - want).abs()[finite] <= rel * want[finite]).all()
