@@ -108,3 +108,62 @@ def test_key_weights_of_values_that_are_not_numbers(Hq, Hkv, S, Dh, queries, cau
     # (paged_ref.key_weights' bound, with |q| . |k| / sqrt(Dh) <= 6 sqrt(Dh) and |lse| <= 12)
     rel = (Dh + 1) * 2.0 ** -23 * (6 * Dh ** 0.5 + 12) + 2.0 ** -18
     assert ((got - want).abs()[finite] <= rel * want[finite]).all()
+
+
+# ---------------------------------------------------------------- decode
+
+def widen(table, page, rows=13000):
+    """The table with unused columns behind it: more rows than the one-launch form takes."""
+    more = -(-rows // page) - table.shape[1]
+    return torch.cat([table, torch.full((table.shape[0], more), -1, dtype=torch.int32)], 1)
+
+
+def course(name, n, gen):
+    """Scores over n keys: rising by far more than 2^8 a tile, by less than that, falling, any."""
+    t = torch.arange(n) / max(n - 1, 1)
+    return {"rising": 400 * t, "creeping": 3.0 / 128 * torch.arange(n), "falling": 400 - 400 * t,
+            "any": 100 * torch.randn(n, generator=gen)}[name]
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("scores", ["rising", "creeping", "falling", "any"])
+@pytest.mark.parametrize("Hq,Hkv,Dh,page,cols,lens", [
+    (8, 2, 128, 16, 40, [640, 300, 2]), (4, 4, 64, 24, 30, [719, 130]), (4, 1, 256, 32, 12, [384, 65]),
+    (40, 1, 128, 16, 30, [470, 129]), (160, 1, 64, 8, 40, [320, 7])])
+def test_decode_of_scores_that_move_the_maximum(Hq, Hkv, Dh, page, cols, lens, scores, wide):
+    gen = torch.Generator().manual_seed(Hq + Dh)
+    B, G = len(lens), Hq // Hkv
+    kp, vp, table, sl = ref.make_cache(lens, Hkv, Dh, page, cols, seed=Dh)
+    u = torch.randint(0, 2, (Dh,), generator=gen) * 2.0 - 1
+    # q . k = 8 f a about, with a head's factor f in [1/2, 1] and a key's score a
+    f = 0.5 + 0.5 * torch.rand((B, Hq, 1, 1), generator=gen)
+    q = (f * u + torch.randn((B, Hq, 1, Dh), generator=gen) / 50).to(torch.bfloat16)
+    for b, n in enumerate(lens):
+        a = course(scores, n, gen)
+        for t in range(n):
+            kp[table[b, t // page], :, t % page] = (
+                a[t] / 8 * u + torch.randn((Hkv, Dh), generator=gen) / 50).to(torch.bfloat16)
+    args = [x.cuda() for x in (q, kp, vp, widen(table, page) if wide else table, sl)]
+    weights = torch.zeros(B, Hkv, args[3].shape[1] * page, device="cuda")
+    got = chs.attn_decode_paged(*args, scale=8.0 / Dh, weights=weights, accumulate=False)
+    status_ok()
+    got, weights = got.cpu().double(), weights.cpu().double()
+    for b, n in enumerate(lens):
+        for g in range(Hkv):
+            k, v = ref.rows(kp, table[b], 0, n, g), ref.rows(vp, table[b], 0, n, g)
+            qg = q[b, g * G:(g + 1) * G, 0].double()
+            p = torch.softmax(8.0 / Dh * qg @ k.t(), -1)
+            # As in paged_ref.decode, with the sizes of this head's and these keys' products
+            # (Dh additions in 32 bits, and 2^-22 for the scaling and the maximum's removal);
+            # a weight is off by e to twice that, and 2^-18 for exp2 and the sums.  P is rounded
+            # to bf16 and n products are added in 32 bits.
+            size = 8.0 / Dh * qg.abs() @ k.abs().t()
+            rel = torch.expm1(2 * size.max() * (Dh * 2.0 ** -23 + 2.0 ** -22)) + 2.0 ** -18
+            assert rel < 1 / 16   # (so that no zero and no other row's result would do)
+            o, a = p @ v, p @ v.abs()
+            tol = ref.HALF_BF16 * (o.abs() + a) + (rel + n * 2.0 ** -23) * a
+            assert ((got[b, g * G:(g + 1) * G, 0] - o).abs() <= tol).all()
+            assert n < 2 or (tol < o.abs()).double().mean() > 0.5
+            w = p.sum(0)
+            # (a weight below 2^-126, the least normal number, may be 0)
+            assert ((weights[b, g, :n] - w).abs() <= rel * w + G * 2.0 ** -126).all()
