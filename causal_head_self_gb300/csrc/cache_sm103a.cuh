@@ -62,6 +62,13 @@ __global__ void __launch_bounds__(kAppendThreads) attn_paged_append_sm103a(const
     }
     id[u] = -1;
     if (i[u] >= add[u]) continue;
+    // (checked builds: a row of k and v, an entry of the table and a row of a page)
+    if (!attn_check(row0 + u * per_pass < p.rows && vec < p.vecs && b[u] >= 0 && g[u] >= 0 &&
+                        g[u] < p.Hkv && i[u] >= 0 &&
+                        p.by_page.div(n[u] - add[u] + i[u]) < p.cols &&
+                        p.by_page.mod(n[u] - add[u] + i[u]) < p.page,
+                    p.error_word))
+      continue;
     const long long from = (row0 + u * per_pass) * p.vecs + vec;
     k[u] = __ldcs(p.k + from);
     v[u] = __ldcs(p.v + from);
@@ -324,15 +331,23 @@ __global__ void __launch_bounds__(kSelectThreads, 1) attn_cache_select_sm103a(co
   for (int i = p.budget + tid; i < min(n, p.stride_out); i += kSelectThreads) w_out[i] = 0.f;
 }
 
-// The page of row t of sequence b, or -1 for one that is not there.
+// The page of row t of sequence b.
 __device__ __forceinline__ int cache_page(const EvictParams& p, const int* table, int cols, int b,
                                           int t) {
+  // (checked builds: an entry of the table)
+  if (!attn_check(b >= 0 && b < p.B && t >= 0 && p.by_page.div(t) < cols, p.error_word)) return -1;
   return __ldcg(table + (long long)b * cols + p.by_page.div(t));
 }
 __device__ __forceinline__ bool cache_page_ok(const EvictParams& p, int id) {
   if (id >= 0 && id < p.num_pages) return true;
   atomicExch(p.error_word, 1);   // ATTN_ERR_INVALID_ARG
   return false;
+}
+// A row and a piece that there are (checked builds).
+__device__ __forceinline__ bool cache_row_ok(const EvictParams& p, int g, int t, int vec) {
+  return attn_check(g >= 0 && g < p.Hkv && t >= 0 && p.by_page.mod(t) < p.page && vec >= 0 &&
+                        vec < p.vecs,
+                    p.error_word);
 }
 // 16-byte piece `vec` of row t of head g, in page id.
 __device__ __forceinline__ long long cache_piece(const EvictParams& p, int id, int g, int t,
@@ -367,7 +382,8 @@ __global__ void __launch_bounds__(kMoveThreads) attn_cache_move_sm103a(const Evi
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (src[u] < 0) continue;
-    if (!cache_page_ok(p, from[u]) || !cache_page_ok(p, to[u])) {
+    if (!cache_page_ok(p, from[u]) || !cache_page_ok(p, to[u]) ||
+        !cache_row_ok(p, g, src[u], vec)) {
       src[u] = -1;
       continue;
     }
@@ -419,7 +435,9 @@ __global__ void __launch_bounds__(kMoveThreads)
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (src[u] < 0) continue;
-      if (!cache_page_ok(p, from[u]) || !cache_page_ok(p, to[u])) src[u] = -1;
+      if (!cache_page_ok(p, from[u]) || !cache_page_ok(p, to[u]) ||
+          !cache_row_ok(p, g, src[u], vec))
+        src[u] = -1;
       else x[u] = __ldcg(pool + cache_piece(p, from[u], g, src[u], vec));
     }
     __syncthreads();

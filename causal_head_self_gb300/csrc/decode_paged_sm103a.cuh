@@ -347,10 +347,14 @@ __device__ __forceinline__ void decode_paged_producer(DecodePagedSmem<DH>& sm,
     constexpr int kCopies = kBoxesPerSlot * REP;   // per slot, shared by two warps
     for (int e = 0; !V && ok && e < Cfg::kQSlots; ++e) {
       if (!(ok = wait_slot())) break;
+      // (checked builds: query heads of this K/V head)
+      const bool in = attn_check(s.b >= 0 && s.b < p.B && g >= 0 && g < p.Hkv && 128 * rb < p.G,
+                                 p.error_word);
       if (lane == 0)
-        mbar_arrive_expect_tx(&sm.full[r.slot], (kCopies + 1 - part) / 2 * (Cfg::kQBox / REP));
+        mbar_arrive_expect_tx(&sm.full[r.slot],
+                              in ? (kCopies + 1 - part) / 2 * (Cfg::kQBox / REP) : 0);
       __syncwarp();
-      if (mine < kCopies) {
+      if (in && mine < kCopies) {
         const int bx = mine / REP, copy = mine % REP;
         tma_load_3d(sm.slot[r.slot] + bx * Cfg::kQBox + copy * kRows * 128, map_q,
                     &sm.full[r.slot], (e * kBoxesPerSlot + bx) * 64, 128 * rb, s.b * p.Hkv + g);

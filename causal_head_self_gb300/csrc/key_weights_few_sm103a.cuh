@@ -230,9 +230,14 @@ __global__ void __launch_bounds__(KeyFewCfg<DH>::kThreads, 1)
       // the group's voting queries, once the last unit's MMAs have read theirs
       if (nseg > 0 && !(ok = wait(&sm.q_free, (nseg - 1) & 1u))) break;
       ++nseg;
-      if (lane == 0) mbar_arrive_expect_tx(&sm.q_loaded, p.G * Cfg::kBoxes * p.pad * 128);
+      // (checked builds: rows of a K/V head and its query heads)
+      const bool head_in = attn_check(s.b >= 0 && s.b < p.B && s.g >= 0 && s.g < p.Hkv,
+                                      p.error_word);
+      const bool q_in = attn_check(s.q0 >= 0 && s.q0 < p.S, p.error_word) && head_in;
+      if (lane == 0)
+        mbar_arrive_expect_tx(&sm.q_loaded, q_in ? p.G * Cfg::kBoxes * p.pad * 128 : 0);
       __syncwarp();
-      for (int i = lane; i < p.G * Cfg::kBoxes; i += 32) {
+      for (int i = lane; q_in && i < p.G * Cfg::kBoxes; i += 32) {
         const int h = i / Cfg::kBoxes, x = i - h * Cfg::kBoxes;
         tma_load_3d(sm.q + x * Cfg::kQBox + h * p.pad * 128, &map_q, &sm.q_loaded, 64 * x, s.q0,
                     s.b * p.Hq + s.g * p.G + h);
@@ -240,8 +245,8 @@ __global__ void __launch_bounds__(KeyFewCfg<DH>::kThreads, 1)
       for (int j = 0; j < s.count; ++j) {
         if (!(ok = wait(&sm.empty[r.i], r.par ^ 1u))) break;
         if (lane == 0) {
-          // (checked builds: a key row of the prompt)
-          const bool in = attn_check(128 * (s.block + j) < p.S, p.error_word);
+          const bool in =
+              attn_check(s.block >= 0 && 128 * (s.block + j) < p.S, p.error_word) && head_in;
           mbar_arrive_expect_tx(&sm.full[r.i], in ? Cfg::kKTile : 0);
           if (in)
             tma_load_4d(sm.k[r.i], &map_k, &sm.full[r.i], 0, 128 * (s.block + j), 0,

@@ -260,9 +260,13 @@ __device__ __forceinline__ void key_weights_producer(KeyWeightsSmem<DH>& sm,
     const KeyWeightsItem it = key_weights_item(p, sm.lens, item, rank);
     if (it.t0 >= it.t1) continue;
     if (!(ok = wait_slot())) break;
+    // (checked builds: key rows of a K/V head)
+    const bool head_in = attn_check(it.b >= 0 && it.b < p.B && it.g >= 0 && it.g < p.Hkv,
+                                    p.error_word);
     if (lane == 0) {
-      mbar_arrive_expect_tx(&sm.full[r.i], Cfg::kTile);
-      tma_load_4d(sm.slot[r.i], map_k, &sm.full[r.i], 0, it.k0, 0, it.b * p.Hkv + it.g);
+      const bool in = attn_check(it.k0 >= 0 && it.k0 < p.S, p.error_word) && head_in;
+      mbar_arrive_expect_tx(&sm.full[r.i], in ? Cfg::kTile : 0);
+      if (in) tma_load_4d(sm.slot[r.i], map_k, &sm.full[r.i], 0, it.k0, 0, it.b * p.Hkv + it.g);
     }
     mark_slot();
     KeyWeightsTile at(p, it);
@@ -270,8 +274,9 @@ __device__ __forceinline__ void key_weights_producer(KeyWeightsSmem<DH>& sm,
       if (!(ok = wait_slot())) break;
       if (lane == 0) {
         const int heads = min(heads_per_tile, p.G - at.head);
-        // (checked builds: a query row of the prompt)
-        const bool in = attn_check(at.query < p.S && heads > 0, p.error_word);
+        // (checked builds: query rows of the group's heads)
+        const bool in = attn_check(at.query >= 0 && at.query < p.S && at.head >= 0 && heads > 0,
+                                   p.error_word) && head_in;
         mbar_arrive_expect_tx(&sm.full[r.i], in ? heads * Cfg::kBoxes * box_bytes : 0);
         if (p.pad == 128) {
           if (in)
