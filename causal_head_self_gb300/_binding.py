@@ -440,11 +440,17 @@ def _decode_paged_workspace(device, B, Hq, Hkv, page, cols, Dh, with_weights):
 
 
 def attn_decode_paged_workspace(q, kpages, table, *, weights=False):
-    """Bytes of workspace that attn_decode_paged needs for tensors of these
-    shapes, with or without weights."""
-    return _decode_paged_workspace(_this_device(), q.shape[0], q.shape[1],
-                                   kpages.shape[1], kpages.shape[2], table.shape[1], q.shape[3],
-                                   bool(weights))
+    """Bytes of workspace that attn_decode_paged needs on the current device for
+    tensors of these shapes, with or without weights."""
+    B, Hq, one, Dh = _shape("q", q, 4)
+    _, Hkv, page, cache_Dh = _shape("kpages", kpages, 4)
+    table_B, cols = _shape("table", table, 2)
+    if one != 1 or cache_Dh != Dh or table_B != B:
+        raise ValueError("q must be [B,Hq,1,Dh], kpages [P,Hkv,page,Dh] and table [B,cols]")
+    for name, x in (("q", max(B, Hq, Dh)), ("kpages", max(Hkv, page)), ("table", cols)):
+        if x > 0x7fffffff:
+            raise ValueError(f"{name} must have less than 2^31 entries along each axis")
+    return _decode_paged_workspace(_this_device(), B, Hq, Hkv, page, cols, Dh, bool(weights))
 
 
 def attn_decode_paged(q, kpages, vpages, table, seqlens, o=None, *, window=0, scale=0.0,
