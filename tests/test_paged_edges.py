@@ -167,3 +167,39 @@ def test_decode_of_scores_that_move_the_maximum(Hq, Hkv, Dh, page, cols, lens, s
             w = p.sum(0)
             # (a weight below 2^-126, the least normal number, may be 0)
             assert ((weights[b, g, :n] - w).abs() <= rel * w + G * 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("kind", ["key -inf", "every key -inf", "key +inf", "query nan"])
+@pytest.mark.parametrize("Hq,Hkv,Dh,page,cols,lens", [
+    (8, 2, 128, 16, 40, [640, 300, 2]), (4, 1, 256, 32, 12, [384, 65]), (40, 1, 64, 16, 30, [470, 129])])
+def test_decode_of_visible_keys_that_are_not_numbers(Hq, Hkv, Dh, page, cols, lens, kind, wide):
+    gen = torch.Generator().manual_seed(Hq)
+    B, G = len(lens), Hq // Hkv
+    kp, vp, table, sl = ref.make_cache(lens, Hkv, Dh, page, cols, seed=Hq)
+    # (a score is infinite, not NaN: each query has the same sign there)
+    q = torch.randn((B, Hq, 1, Dh), generator=gen).to(torch.bfloat16)
+    q[..., 0] = q[..., 0].abs().clamp(min=0.1)
+    if kind == "query nan":
+        q[0, 1] = math.nan
+    else:
+        value = math.inf if kind == "key +inf" else -math.inf
+        for t in range(0, lens[0], 1 if kind == "every key -inf" else 3):
+            kp[table[0, t // page], 0, t % page, 0] = value
+    args = [x.cuda() for x in (q, kp, vp, widen(table, page) if wide else table, sl)]
+    weights = torch.zeros(B, Hkv, args[3].shape[1] * page, device="cuda")
+    got = chs.attn_decode_paged(*args, weights=weights, accumulate=False)
+    status_ok()
+    got, weights = got.cpu().double(), weights.cpu().double()
+    for b, n in enumerate(lens):
+        for g in range(Hkv):
+            k, v = ref.rows(kp, table[b], 0, n, g), ref.rows(vp, table[b], 0, n, g)
+            p = torch.softmax(Dh ** -0.5 * q[b, g * G:(g + 1) * G, 0].double() @ k.t(), -1)
+            o, a, w = p @ v, p @ v.abs(), p.sum(0)
+            # (paged_ref.decode's bound, with |q| . |k| <= 6 Dh)
+            rel = 12 * Dh ** 1.5 * 2.0 ** -23 + 2.0 ** -18
+            for x, y, tol in ((got[b, g * G:(g + 1) * G, 0], o,
+                               ref.HALF_BF16 * (o.abs() + a) + (rel + n * 2.0 ** -23) * a),
+                              (weights[b, g, :n], w, rel * w)):
+                assert torch.equal(x.isnan(), y.isnan())
+                assert ((x - y).abs() <= tol)[~y.isnan()].all()
