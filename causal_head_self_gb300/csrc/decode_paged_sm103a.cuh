@@ -281,14 +281,6 @@ using PagedRingK = PagedRing<0, DecodePagedCfg<DH>::kSlotsK>;
 template <int DH>
 using PagedRingV = PagedRing<DecodePagedCfg<DH>::kSlotsK, DecodePagedCfg<DH>::kSlotsV>;
 
-__device__ __forceinline__ void mbar_wait_drain_paged(uint64_t* bar, uint32_t parity) {
-  const uint32_t a = smem_u32(bar);
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(a, parity)) {
-    if (globaltimer_ns() - t0 > kWaitLimitNs) return;
-  }
-}
-
 // Loading warps: two load Q and K, two V, each (`part`) every other box (64
 // columns of box_rows rows; at most 32 per tile: 128 rows / 8 x 2, 64 rows / 8 x
 // 4), one lane per box.  A warp takes about 90 cycles to issue one
@@ -411,7 +403,7 @@ __device__ __forceinline__ void decode_paged_producer(DecodePagedSmem<DH>& sm,
   // every copy this warp started has landed before the CTA may exit
   if (lane == 0)
     for (int i = 0; i < Cfg::kSlots; ++i)
-      if (loaded & (1u << i)) mbar_wait_drain_paged(&sm.full[i], (pars >> i) & 1u);
+      if (loaded & (1u << i)) mbar_wait_drain(&sm.full[i], (pars >> i) & 1u);
 }
 
 // Tensor-core warp.  Per segment: Q to tensor memory, S of the first two tiles,
@@ -493,7 +485,7 @@ __device__ __forceinline__ void decode_paged_issuer(DecodePagedSmem<DH>& sm,
   }
   // nothing of this warp's may still run on the tensor core at teardown
   mma_commit_warp(&sm.mma_done);
-  mbar_wait_drain_paged(&sm.mma_done, 0);
+  mbar_wait_drain(&sm.mma_done, 0);
 }
 
 // Softmax warps: thread t owns row t (tensor-memory lane t).  With REP = 4 row
@@ -702,10 +694,6 @@ __device__ __forceinline__ void decode_paged_softmax(DecodePagedSmem<DH>& sm,
   }
 }
 
-__device__ __forceinline__ void paged_cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
-}
-
 // *x in the shared memory of the cluster's CTA `rank`.
 __device__ __forceinline__ float paged_peer(const float* x, int rank) {
   uint32_t at;
@@ -880,9 +868,9 @@ __global__ void __launch_bounds__(288, 1)
     // (all waits before this one are bounded, so every thread of the cluster comes here)
     PagedPart<DH>& part = *reinterpret_cast<PagedPart<DH>*>(sm.slot[0]);
     decode_paged_short_copies<DH>(part, p);
-    paged_cluster_sync();
+    cluster_sync();
     decode_paged_short_join<DH>(part, p);
-    paged_cluster_sync();   // no CTA goes while another reads its results
+    cluster_sync();   // no CTA goes while another reads its results
   }
 }
 

@@ -1,4 +1,4 @@
-// fixed_div.h -- division by a number that the host knows.
+// fixed_div.h -- division by a number that the host knows (prefill and paged cache).
 #pragma once
 
 #include <cstdint>

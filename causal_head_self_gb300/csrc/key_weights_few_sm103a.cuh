@@ -259,9 +259,9 @@ __global__ void __launch_bounds__(KeyFewCfg<DH>::kThreads, 1)
     }
     // every copy this warp started has landed before the CTA may exit
     if (lane == 0) {
-      if (nseg > 0) mbar_wait_drain_kw(&sm.q_loaded, (nseg - 1) & 1u);
+      if (nseg > 0) mbar_wait_drain(&sm.q_loaded, (nseg - 1) & 1u);
       for (int i = 0; i < Cfg::kSlots; ++i)
-        if (loaded & (1u << i)) mbar_wait_drain_kw(&sm.full[i], (pars >> i) & 1u);
+        if (loaded & (1u << i)) mbar_wait_drain(&sm.full[i], (pars >> i) & 1u);
     }
   } else if (warp == Cfg::kWarpLse) {
     uint32_t nseg = 0;
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(KeyFewCfg<DH>::kThreads, 1)
     }
     // nothing of this warp's may still run on the tensor core at teardown
     mma_commit_warp(&sm.mma_done);
-    mbar_wait_drain_kw(&sm.mma_done, 0);
+    mbar_wait_drain(&sm.mma_done, 0);
   } else {
     const int group = warp / 4, tid = threadIdx.x % 128;
     const uint32_t colS = tbase + ((uint32_t)(tid & ~31) << 16) + 256u * group;

@@ -60,7 +60,7 @@ struct KeyWeightsParams {
   int head_tiles;        // tiles that the group's heads take, `pad` columns each
   int split, split_log2; // CTAs per item, a power of two
   float scale_log2;
-  float lse_hi, lse_lo;  // ln 2-free: -log2(e) / scale_log2 in two parts
+  float lse_hi, lse_lo;  // -log2(e) / scale_log2 in two parts
   const float* lse;      // [B, Hq, S]
   const int* seqlens;    // [B] or null (every sequence holds S)
   float* weights;        // [B, Hkv, stride]
@@ -198,14 +198,6 @@ struct KeyWeightsTile {
   }
 };
 
-__device__ __forceinline__ void mbar_wait_drain_kw(uint64_t* bar, uint32_t parity) {
-  const uint32_t a = smem_u32(bar);
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(a, parity)) {
-    if (globaltimer_ns() - t0 > kWaitLimitNs) return;
-  }
-}
-
 // Position in a ring of N: index and the parity of its current use.  Whoever
 // waits on a ring's barriers passes every use in turn, or can tell otherwise that
 // the use before is over: the parity tells only one phase from the next.
@@ -295,7 +287,7 @@ __device__ __forceinline__ void key_weights_producer(KeyWeightsSmem<DH>& sm,
   // every copy this warp started has landed before the CTA may exit
   if (lane == 0)
     for (int i = 0; i < Cfg::kSlots; ++i)
-      if (loaded & (1u << i)) mbar_wait_drain_kw(&sm.full[i], (pars >> i) & 1u);
+      if (loaded & (1u << i)) mbar_wait_drain(&sm.full[i], (pars >> i) & 1u);
 }
 
 // The entries of one group: its tiles' descriptions and log-sum-exps (0 where
@@ -488,7 +480,7 @@ __device__ __forceinline__ void key_weights_issuer(KeyWeightsSmem<DH>& sm,
   }
   // nothing of this warp's may still run on the tensor core at teardown
   mma_commit_warp(&sm.mma_done);
-  mbar_wait_drain_kw(&sm.mma_done, 0);
+  mbar_wait_drain(&sm.mma_done, 0);
 }
 
 // The sum of 2^(s scale_log2) over 32 columns.
@@ -615,10 +607,6 @@ __device__ __forceinline__ void key_weights_sums(KeyWeightsSmem<DH>& sm, const K
   }
 }
 
-__device__ __forceinline__ void key_weights_cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
-}
-
 // (No early exit: the CTAs of a cluster meet at its end.)
 template <int DH>
 __global__ void __launch_bounds__(384, 1)
@@ -682,7 +670,7 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  if (p.split > 1) key_weights_cluster_sync();   // (every CTA runs before any writes to another)
+  if (p.split > 1) cluster_sync();   // (every CTA runs before any writes to another)
   if (warp == Cfg::kWarpProducer) {
     key_weights_producer<DH>(sm, p, &map_q, &map_k, rank, lane, abort);
   } else if (warp >= Cfg::kWarpLse) {
@@ -703,7 +691,7 @@ __global__ void __launch_bounds__(384, 1)
   if (p.split > 1) {
     // every CTA's sums are in the first one's shared memory (all waits before
     // this one are bounded, so every thread of the cluster comes here)
-    key_weights_cluster_sync();
+    cluster_sync();
     if (rank == 0 && threadIdx.x < 128) {
       const KeyWeightsItem it = key_weights_item(p, sm.lens, (int)blockIdx.x / p.split, 0);
       const int j = it.k0 + threadIdx.x;

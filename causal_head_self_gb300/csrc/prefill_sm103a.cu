@@ -35,15 +35,6 @@ static cudaError_t launch_prefill_dh(const CUtensorMap& mq, const CUtensorMap& m
                     stream, mq, mk, mv, mo, prm);
 }
 
-// Multiplier and shift for FastDiv (exact for dividends below 2^31).
-static FastDiv make_fast_div(uint32_t d) {
-  uint32_t l = 0;
-  while ((1ull << l) < d) ++l;
-  const unsigned __int128 one = 1;
-  const uint64_t m = (uint64_t)(((one << (31 + l)) + d - 1) / d);
-  return FastDiv{(uint32_t)m, 31 + l, d};
-}
-
 // One 128-row sub-tile per work item, 64-key tiles: head size 256, and head
 // size 128 on short sequences (two CTAs per SM).
 template <int DH>
@@ -141,9 +132,9 @@ cudaError_t launch_prefill(const void* q, const void* k, const void* v, void* o,
   prm.lse = lse;
   prm.error_word = dev.error_word;
   prm.fault = dev.fault;
-  prm.div_bh = make_fast_div((uint32_t)(B * Hq));
-  prm.div_hq = make_fast_div((uint32_t)Hq);
-  prm.div_group = make_fast_div((uint32_t)(Hq / Hkv));
+  prm.div_bh = make_fixed_div((uint32_t)(B * Hq));
+  prm.div_hq = make_fixed_div((uint32_t)Hq);
+  prm.div_group = make_fixed_div((uint32_t)(Hq / Hkv));
   return Dh == 128 ? launch_prefill_dh<128>(mq, mk, mv, mo, prm, dev.num_sms, dev.device, stream)
                    : launch_prefill_dh<64>(mq, mk, mv, mo, prm, dev.num_sms, dev.device, stream);
 }

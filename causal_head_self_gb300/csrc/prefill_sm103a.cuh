@@ -42,22 +42,10 @@
 // and fed to the P.V MMA straight from TMEM.
 #pragma once
 
+#include "fixed_div.h"
 #include "sm103a_ptx.cuh"
 
 namespace chs {
-
-// Exact division of a non-negative int n < 2^31 by a fixed divisor d >= 1:
-// n / d == (n * m) >> (31 + l) with l = ceil(log2 d) and m = ceil(2^(31+l) / d)
-// (the rounding error n*(m*d - 2^(31+l)) / (d * 2^(31+l)) stays below 1/d).
-// The multiplier is made on the host; the device pays one wide multiply
-// instead of a division sequence.
-struct FastDiv {
-  uint32_t m, shift, d;
-  __device__ __forceinline__ int div(int n) const {
-    return (int)(((uint64_t)(uint32_t)n * m) >> shift);
-  }
-  __device__ __forceinline__ int mod(int n) const { return n - div(n) * (int)d; }
-};
 
 struct PrefillParams {
   int B, Hq, Hkv;
@@ -72,9 +60,9 @@ struct PrefillParams {
   float* lse;         // optional [B, Hq, Sq]: log sum_j exp(s_ij) per row (natural log)
   int* error_word;    // set to a nonzero status when a wait gives up
   int fault;          // test hook: 1 = the first K tile is never loaded
-  FastDiv div_bh;     // by B * Hq (work items per query block)
-  FastDiv div_hq;     // by Hq
-  FastDiv div_group;  // by Hq / Hkv (query heads per K/V head)
+  FixedDiv div_bh;     // by B * Hq (work items per query block)
+  FixedDiv div_hq;     // by Hq
+  FixedDiv div_group;  // by Hq / Hkv (query heads per K/V head)
 };
 
 template <int DH>
@@ -220,16 +208,6 @@ __device__ __forceinline__ PrefillItem prefill_item_of(const PrefillParams& p, i
   it.tile = prefill_tile_of(p, qb);
   return it;
 }
-
-// Drain wait used at teardown: ignores the abort flag, bounded by time.
-__device__ __forceinline__ void mbar_wait_drain(uint64_t* bar, uint32_t parity) {
-  const uint32_t a = smem_u32(bar);
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(a, parity)) {
-    if (globaltimer_ns() - t0 > kWaitLimitNs) return;
-  }
-}
-
 
 // One MMA issuer: the chain of sub-tile S (0 or 1) over all of the CTA's work
 // items, run by a whole warp that stays converged; one elected lane issues
