@@ -456,7 +456,8 @@ def attn_decode_paged_workspace(q, kpages, table, *, weights=False):
 def attn_decode_paged(q, kpages, vpages, table, seqlens, o=None, *, window=0, scale=0.0,
                       weights=None, accumulate=True, workspace=None, stream=None):
     """One decode step over a paged cache (see attn_paged_append).  q
-    [B,Hq,1,Dh]; a length of 0 gives a zero output.  weights [B,Hkv,rows]
+    [B,Hq,1,Dh]; a length of 0 gives a zero output.  The softmax weights are
+    rounded to bf16 where they meet V.  weights [B,Hkv,rows]
     fp32 (rows >= cols * page) receives each key's softmax weight summed over
     its query heads, added to what is there or, with accumulate=False, in its
     place.  workspace: a uint8 tensor of attn_decode_paged_workspace() bytes
