@@ -456,12 +456,13 @@ def attn_decode_paged_workspace(q, kpages, table, *, weights=False):
 def attn_decode_paged(q, kpages, vpages, table, seqlens, o=None, *, window=0, scale=0.0,
                       weights=None, accumulate=True, workspace=None, stream=None):
     """One decode step over a paged cache (see attn_paged_append).  q
-    [B,Hq,1,Dh]; a length of 0 gives a zero output.  The softmax weights are
-    rounded to bf16 where they meet V.  weights [B,Hkv,rows]
-    fp32 (rows >= cols * page) receives each key's softmax weight summed over
-    its query heads, added to what is there or, with accumulate=False, in its
-    place.  workspace: a uint8 tensor of attn_decode_paged_workspace() bytes
-    (None: allocated here by torch, on the call's stream).  Returns o."""
+    [B,Hq,1,Dh]; a length of 0 gives a zero output.  Where the softmax weights
+    meet V they are rounded to bf16, or with up to 16 query heads per K/V head
+    held to two parts of it.  weights [B,Hkv,rows] fp32 (rows >= cols * page)
+    receives each key's softmax weight summed over its query heads, added to
+    what is there or, with accumulate=False, in its place.  workspace: a uint8
+    tensor of attn_decode_paged_workspace() bytes (None: allocated here by
+    torch, on the call's stream).  Returns o."""
     window = _int32("window", window)
     B, Hkv, P, page, cols, Dh, device = _check_pools(kpages, vpages, table, seqlens)
     Hq = _shape("q", q, 4)[1]

@@ -101,7 +101,7 @@ Layout layout(int B, int Hq, int Hkv, const PagedCache& c, int Dh, bool scores, 
   const size_t rows =
       one_launch ? 0 : (units + num_sms) * (G <= kCopiesMaxGroup ? 4 * (size_t)G : 128);
   Layout w;
-  w.m_off = up(rows * Dh * sizeof(float));
+  w.m_off = up(rows * (G <= kPagedTwoParts ? 2 : 1) * Dh * sizeof(float));
   w.l_off = w.m_off + up(rows * sizeof(float));
   w.units_off = w.l_off + up(rows * sizeof(float));
   w.scores_off = w.units_off + (rows > 0 ? up(units * sizeof(int2)) : 0);
@@ -118,13 +118,13 @@ cudaError_t launch_short(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
   return cudaLaunchKernelEx(&l.cfg, attn_decode_paged_sm103a<DH, 4, true>, mq, mk, mv, prm);
 }
 
-template <int DH, int REP, int THREADS>
+template <int DH, int REP, bool TWICE, int THREADS>
 cudaError_t launch_join(const DecodePagedParams& prm, cudaStream_t stream) {
   unsigned blocks = (unsigned)prm.B * prm.Hq;
   if (prm.weights)
     blocks += (unsigned)prm.B * prm.Hkv *
               ((prm.cols * prm.page + 4 * THREADS - 1) / (4 * THREADS));
-  return launch_pdl(attn_decode_paged_join<DH, REP, THREADS>, dim3(blocks), dim3(THREADS), 0,
+  return launch_pdl(attn_decode_paged_join<DH, REP, TWICE, THREADS>, dim3(blocks), dim3(THREADS), 0,
                     stream, prm);
 }
 
@@ -148,9 +148,12 @@ cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorM
   // keys (20 partial results) 69 -> 72 us.  (Weights have no say: the output's bits do
   // not depend on whether they are asked for.)
   const int partials = REP * (prm.ctas / (prm.B * prm.Hkv * prm.row_blocks) + 1);
-  return partials > 32 && prm.B * prm.Hq <= dev.num_sms
-             ? launch_join<DH, REP, 1024>(prm, stream)
-             : launch_join<DH, REP, 256>(prm, stream);
+  const bool wide = partials > 32 && prm.B * prm.Hq <= dev.num_sms;
+  if (REP == 4 && prm.G <= kPagedTwoParts)
+    return wide ? launch_join<DH, REP, REP == 4, 1024>(prm, stream)
+                : launch_join<DH, REP, REP == 4, 256>(prm, stream);
+  return wide ? launch_join<DH, REP, false, 1024>(prm, stream)
+              : launch_join<DH, REP, false, 256>(prm, stream);
 }
 
 template <int DH>
@@ -188,7 +191,8 @@ cudaError_t launch_decode_paged(const void* q, const void* kpages, const void* v
   const int box = paged_box_rows(cache.page, Dh);
   const long long pages = (long long)cache.num_pages * Hkv;
   CUtensorMap mq, mk, mv;
-  if (!encode_bf16_map(&mq, q, Dh, G, (long long)B * Hkv, G <= kCopiesMaxGroup ? 32 : 128) ||
+  const int q_rows = G <= kPagedTwoParts ? kPagedTwoParts : G <= kCopiesMaxGroup ? 32 : 128;   // (see the kernel)
+  if (!encode_bf16_map(&mq, q, Dh, G, (long long)B * Hkv, q_rows) ||
       !encode_bf16_map(&mk, kpages, Dh, cache.page, pages, box) ||
       !encode_bf16_map(&mv, vpages, Dh, cache.page, pages, box))
     return cudaErrorInvalidValue;

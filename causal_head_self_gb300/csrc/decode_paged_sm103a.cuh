@@ -35,6 +35,14 @@
 // each, and four partial results per segment.  Larger groups use every row
 // (REP = 1).
 //
+// P meets V in bf16, the tensor core's operand type, which alone would cost 2^-8 of
+// each weight, as much as the output's own rounding.  A group of up to 16 heads has
+// room to spare in its 32 rows: rows 16 .. 31 of a copy hold the same heads again.  The
+// first 16 have the upper 16 bits of p, a bf16 number, the others those of what is
+// left; the two rows' products add up to those of p to 2^-14.  They are added where
+// the partial results are joined.  It costs 1 % of a step (29.9 -> 30.4 us for 8 x 32
+// heads of 64; a second product per tile instead, 32.5).  Larger groups round P.
+//
 // Short form (SHORT).  Where the table has room for few tiles a unit, starting up
 // and joining cost more than reading.  A unit then belongs to a cluster of up to
 // eight CTAs, each with an equal part of its tiles; the partial results stay in
@@ -57,6 +65,8 @@
 
 namespace chs {
 
+constexpr int kPagedTwoParts = 16;   // query heads per K/V head with P in two parts, at most
+
 struct DecodePagedParams {
   int B, Hq, Hkv, G, window;
   int num_pages, page, cols;   // pool pages, rows per page, table columns
@@ -69,7 +79,8 @@ struct DecodePagedParams {
   int accumulate;
   const int* seqlens;          // [B], device
   const int* table;            // [B, cols], device
-  float* o_part;               // [segments, REP, rows, DH] unnormalised
+  float* o_part;               // [segments, REP, rows, DH] unnormalised; with up to 16 heads
+                               // [segments, 2, REP, rows, DH], from both parts of P
   float* m_part;               // [segments, REP, rows]     (log2 domain)
   float* l_part;               // [segments, REP, rows]
   int2* unit_ctas;             // [units]: first and last CTA of a unit
@@ -255,7 +266,7 @@ using PagedWalk = std::conditional_t<SHORT, PagedShortWalk<KEYS>, PagedLineWalk<
 // different banks.
 template <int DH>
 struct PagedPart {
-  float o[128][DH + 4];
+  float o[128][DH + 4];         // with up to 16 heads P's second part from row 4 G on
   float m[128], l[128];
   float m_all[32], l_all[32];   // of the four copies together
   float share[32][8];           // [head][CTA]: its part of the head's result
@@ -334,9 +345,11 @@ __device__ __forceinline__ void decode_paged_producer(DecodePagedSmem<DH>& sm,
     int group_c1 = c1, group_id = group_use ? __ldcg(row + col) : 0;
     bool next_use = false;
     int next_c1 = 0, next_id = 0;
-    // Q: REP copies of the group's rows
-    constexpr int kRows = 128 / REP, kBoxesPerSlot = Cfg::kBoxes / Cfg::kQSlots;
-    constexpr int kCopies = kBoxesPerSlot * REP;   // per slot, shared by two warps
+    // Q: the group's rows (128, or the 32 that are copied four times on their way to
+    // tensor memory), with up to 16 heads twice
+    constexpr int kBoxesPerSlot = Cfg::kBoxes / Cfg::kQSlots;
+    const int rep = REP == 4 && p.G <= kPagedTwoParts ? 2 : 1, rows = 128 / REP / rep;
+    const int copies = kBoxesPerSlot * rep;   // per slot, shared by two warps
     for (int e = 0; !V && ok && e < Cfg::kQSlots; ++e) {
       if (!(ok = wait_slot())) break;
       // (checked builds: query heads of this K/V head)
@@ -344,11 +357,11 @@ __device__ __forceinline__ void decode_paged_producer(DecodePagedSmem<DH>& sm,
                                  p.error_word);
       if (lane == 0)
         mbar_arrive_expect_tx(&sm.full[r.slot],
-                              in ? (kCopies + 1 - part) / 2 * (Cfg::kQBox / REP) : 0);
+                              in ? (copies + 1 - part) / 2 * (rows * 128) : 0);
       __syncwarp();
-      if (in && mine < kCopies) {
-        const int bx = mine / REP, copy = mine % REP;
-        tma_load_3d(sm.slot[r.slot] + bx * Cfg::kQBox + copy * kRows * 128, map_q,
+      if (in && mine < copies) {
+        const int bx = mine / rep, copy = mine % rep;
+        tma_load_3d(sm.slot[r.slot] + bx * Cfg::kQBox + copy * rows * 128, map_q,
                     &sm.full[r.slot], (e * kBoxesPerSlot + bx) * 64, 128 * rb, s.b * p.Hkv + g);
       }
       mark_slot();
@@ -408,7 +421,7 @@ __device__ __forceinline__ void decode_paged_producer(DecodePagedSmem<DH>& sm,
 
 // Tensor-core warp.  Per segment: Q to tensor memory, S of the first two tiles,
 // then per tile P.V and the S two tiles on, into the buffer that P came from.
-template <int DH, bool SHORT>
+template <int DH, int REP, bool SHORT>
 __device__ __forceinline__ void decode_paged_issuer(DecodePagedSmem<DH>& sm,
                                                     const DecodePagedParams& p, uint32_t tbase,
                                                     PagedWalk<DecodePagedCfg<DH>::kKeys, SHORT> walk,
@@ -438,9 +451,16 @@ __device__ __forceinline__ void decode_paged_issuer(DecodePagedSmem<DH>& sm,
       constexpr int kSteps = DH / 16 / Cfg::kQSlots;
       const uint64_t q = kmajor + (uint64_t)rk.slot * (Cfg::kSlot >> 4);
 #pragma unroll
-      for (int kk = 0; kk < kSteps; ++kk)
-        tmem_cp_128x256b_warp(tbase + Cfg::kColQ + 8 * (e * kSteps + kk),
-                              q + (((kk / 4) * Cfg::kQBox + (kk % 4) * 32) >> 4));
+      for (int kk = 0; kk < kSteps; ++kk) {
+        const uint32_t to = tbase + Cfg::kColQ + 8 * (e * kSteps + kk);
+        const uint64_t from = q + (((kk / 4) * Cfg::kQBox + (kk % 4) * 32) >> 4);
+        if constexpr (REP == 4) {
+          tmem_cp_32x128b_x4_warp(to, from);
+          tmem_cp_32x128b_x4_warp(to + 4, from + 1);
+        } else {
+          tmem_cp_128x256b_warp(to, from);
+        }
+      }
       mma_commit_warp(&sm.empty[rk.slot]);
     }
     if (!ok) break;
@@ -488,8 +508,14 @@ __device__ __forceinline__ void decode_paged_issuer(DecodePagedSmem<DH>& sm,
   mbar_wait_drain(&sm.mma_done, 0);
 }
 
+// The bf16 number of x's upper 16 bits: x rounded towards zero.
+__device__ __forceinline__ float top_half(float x) {
+  return __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+}
+
 // Softmax warps: thread t owns row t (tensor-memory lane t).  With REP = 4 row
-// 32 w + i is query head i of the block, for the keys of quarter w.
+// 32 w + i is query head i of the block, for the keys of quarter w; with up to 16
+// heads rows 32 w + 16 + i are the same, for the rest of P.
 template <int DH, int REP, bool SHORT>
 __device__ __forceinline__ void decode_paged_softmax(DecodePagedSmem<DH>& sm,
                                                      const DecodePagedParams& p, uint32_t tbase,
@@ -501,7 +527,10 @@ __device__ __forceinline__ void decode_paged_softmax(DecodePagedSmem<DH>& sm,
   constexpr int kChunk = kMine < 32 ? kMine : 32;     // columns per load
   constexpr int kChunks = kMine / kChunk;
   const int col0 = REP == 4 ? warp * kMine : 0;
-  const int head = REP == 4 ? lane : warp * 32 + lane;   // in the block of query heads
+  const bool twice = REP == 4 && p.G <= kPagedTwoParts;
+  const bool rest = twice && lane >= kPagedTwoParts;
+  const int head = REP != 4 ? warp * 32 + lane : twice ? lane % kPagedTwoParts : lane;   // in the block
+  const float2 part2 = rest ? make_float2(-1.f, -1.f) : make_float2(0.f, 0.f);
   const int copy = REP == 4 ? warp : 0;
   const int tid = warp * 32 + lane;
   const uint32_t lane_addr = tbase + ((uint32_t)(warp * 32) << 16);
@@ -515,13 +544,16 @@ __device__ __forceinline__ void decode_paged_softmax(DecodePagedSmem<DH>& sm,
   bool pending = false, pend_rows = false;
   float pend_m = 0.f, pend_l = 0.f;
   size_t pend_at = 0;
+  // a segment's rows: those of m and l, and of O twice as many where P has two parts
+  const int part_rows = REP == 4 ? 4 * p.G : 128, pend_row = copy * p.G + head;
+  const int rest_rows = rest ? part_rows : 0;
   auto flush = [&]() -> bool {
     // (o_final, not pv_done: two P.V may still be running here, and the parity of
     // a barrier tells only one phase from the next)
     if (!mbar_wait(&sm.o_final, nseg++ & 1u, abort)) return false;
     tc_fence_after_sync();
     PagedPart<DH>& part = *reinterpret_cast<PagedPart<DH>*>(sm.slot[0]);
-    float* dst = p.o_part + pend_at * DH;
+    float* dst = p.o_part + (twice ? 2 * pend_at - pend_row + rest_rows : pend_at) * DH;
 #pragma unroll 1
     for (int c = 0; c < DH / 64; ++c) {
       uint32_t o[2][32];
@@ -533,7 +565,7 @@ __device__ __forceinline__ void decode_paged_softmax(DecodePagedSmem<DH>& sm,
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const uint32_t* x = &o[e / 8][4 * (e % 8)];
-          *reinterpret_cast<uint4*>(&part.o[pend_at][64 * c + 4 * e]) =
+          *reinterpret_cast<uint4*>(&part.o[pend_at + rest_rows][64 * c + 4 * e]) =
               make_uint4(x[0], x[1], x[2], x[3]);
         }
       } else if (pend_rows) {
@@ -546,7 +578,7 @@ __device__ __forceinline__ void decode_paged_softmax(DecodePagedSmem<DH>& sm,
         }
       }
     }
-    if (pend_rows) {
+    if (pend_rows && !rest) {
       (SHORT ? part.m : p.m_part)[pend_at] = pend_m;
       (SHORT ? part.l : p.l_part)[pend_at] = pend_l;
     }
@@ -583,7 +615,7 @@ __device__ __forceinline__ void decode_paged_softmax(DecodePagedSmem<DH>& sm,
         for (int e = 0; e < kMine; ++e)
           x[e] = keep_if_le(x[e], (uint32_t)(col0 + e - clo), (uint32_t)(chi - 1 - clo));
       }
-      if (p.scores != nullptr && real) {
+      if (p.scores != nullptr && real && !rest) {
         // raw scores (rows of the buffer are whole tiles, 32-byte aligned)
         float* dst = p.scores + bh * (size_t)p.score_stride + pos0 + col0;
 #pragma unroll
@@ -611,10 +643,10 @@ __device__ __forceinline__ void decode_paged_softmax(DecodePagedSmem<DH>& sm,
       const float msub = (m_use == -INFINITY) ? 0.f : m_use;
       const float2 scale2 = make_float2(sl2, sl2), neg_m2 = make_float2(-msub, -msub);
       float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      // P in bf16 (the tensor core's operand type; a rounding of 2^-8 relative
-      // per weight at most, the sum l is taken before it) over the first kKeys / 2
-      // columns of S, zero at the keys of the other quarters.  Those columns
-      // hold scores of this warp's rows only, which are all read by now.
+      // P in bf16 (both parts of it, or a rounding of 2^-8 relative per weight at most;
+      // the sum l is of p itself) over the first kKeys / 2 columns of S, zero at the keys
+      // of the other quarters.  Those columns hold scores of this warp's rows only, which
+      // are all read by now.
       if constexpr (REP == 4) {
         uint32_t zero[kMine / 2];
 #pragma unroll
@@ -635,7 +667,12 @@ __device__ __forceinline__ void decode_paged_softmax(DecodePagedSmem<DH>& sm,
           const float2 xs = __ffma2_rn(make_float2(x[i], x[i + 1]), scale2, neg_m2);
           const float2 pp = make_float2(ex2_approx(xs.x), ex2_approx(xs.y));
           ls[e & 1] = __fadd2_rn(ls[e & 1], pp);
-          pk[e] = pack_bf16x2(pp.x, pp.y);
+          if (twice) {
+            const float2 v = __ffma2_rn(make_float2(top_half(pp.x), top_half(pp.y)), part2, pp);
+            pk[e] = __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632);
+          } else {
+            pk[e] = pack_bf16x2(pp.x, pp.y);
+          }
         }
         if constexpr (kChunk == 32) tmem_st_32x32b_x16(colS + col0 / 2 + 16 * c, pk);
         else tmem_st_32x32b_x8(colS + col0 / 2 + 8 * c, pk);
@@ -683,13 +720,12 @@ __device__ __forceinline__ void decode_paged_softmax(DecodePagedSmem<DH>& sm,
     pend_rows = real;
     pend_m = m_run;
     pend_l = l_run;
-    pend_at = ((SHORT ? 0 : (size_t)(s.unit + blockIdx.x) * REP) + copy) * (REP == 4 ? p.G : 128) +
-              head;
+    pend_at = SHORT ? pend_row : (size_t)(s.unit + blockIdx.x) * part_rows + pend_row;
     pending = true;
   }
   if (ok && pending) {
     flush();
-  } else if (SHORT && head < p.G) {   // no tile: nothing of this CTA's counts
+  } else if (SHORT && head < p.G && !rest) {   // no tile: nothing of this CTA's counts
     reinterpret_cast<PagedPart<DH>*>(sm.slot[0])->m[copy * p.G + head] = -INFINITY;
   }
 }
@@ -707,18 +743,25 @@ __device__ __forceinline__ float paged_peer(const float* x, int rank) {
 template <int DH>
 __device__ __forceinline__ void decode_paged_short_copies(PagedPart<DH>& part,
                                                           const DecodePagedParams& p) {
+  const bool twice = p.G <= kPagedTwoParts;
   for (int i = threadIdx.x; i < p.G * DH; i += DecodePagedCfg<DH>::kThreads) {
     const int h = i / DH, d = i % DH;
-    float m[4], M = -INFINITY, l = 0.f, o = 0.f;
+    float m[4], lc[4], oc[4], rest[4], M = -INFINITY, l = 0.f, o = 0.f;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) M = fmaxf(M, m[c] = part.m[c * p.G + h]);
+    for (int c = 0; c < 4; ++c) {   // (the loads together)
+      m[c] = part.m[c * p.G + h];
+      lc[c] = part.l[c * p.G + h];
+      oc[c] = part.o[c * p.G + h][d];
+      rest[c] = twice ? part.o[(4 + c) * p.G + h][d] : 0.f;
+      M = fmaxf(M, m[c]);
+    }
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       // (where the CTA has no tile only m was written)
       const float f = m[c] == -INFINITY ? 0.f : ex2_approx(m[c] - M);
       if (f != 0.f) {
-        l = fmaf(f, part.l[c * p.G + h], l);
-        o = fmaf(f, part.o[c * p.G + h][d], o);
+        l = fmaf(f, lc[c], l);
+        o = fmaf(f, oc[c] + rest[c], o);
       }
     }
     part.o[h][d] = o;   // (this thread alone reads these columns)
@@ -853,7 +896,7 @@ __global__ void __launch_bounds__(288, 1)
   else if (warp >= Cfg::kWarpProducer)
     decode_paged_producer<DH, REP, SHORT, false>(sm, p, &map_q, &map_k, walk, warp & 1, lane, abort);
   else if (warp == Cfg::kWarpIssuer)
-    decode_paged_issuer<DH, SHORT>(sm, p, tbase, walk, abort);
+    decode_paged_issuer<DH, REP, SHORT>(sm, p, tbase, walk, abort);
   else if (warp < active_warps)
     decode_paged_softmax<DH, REP, SHORT>(sm, p, tbase, walk, warp, lane, active_warps, abort);
   __syncwarp();
@@ -880,7 +923,8 @@ __global__ void __launch_bounds__(288, 1)
 // them, launched when weights are asked for, each write 4 * THREADS of
 // the weights of one (sequence, K/V head): sum over the group's heads of
 // 2^(s - M) / l, from the scores that the first kernel left.
-template <int DH, int REP, int THREADS>
+// TWICE: a segment has twice as many rows of O, the products of P's second part last.
+template <int DH, int REP, bool TWICE, int THREADS>
 __global__ void __launch_bounds__(THREADS) attn_decode_paged_join(const DecodePagedParams p) {
   constexpr int kKeysPerBlock = 4 * THREADS;
   constexpr int KEYS = DecodePagedCfg<DH>::kKeys;
@@ -901,26 +945,30 @@ __global__ void __launch_bounds__(THREADS) attn_decode_paged_join(const DecodePa
       return;
     }
     const int n = (ctas.y - ctas.x + 1) * REP;
-    const size_t at0 = (size_t)(unit + ctas.x) * REP * part_rows + (hg - 128 * rb);
+    const size_t segments0 = (size_t)(unit + ctas.x) * REP * part_rows;
+    const size_t at0 = segments0 + (hg - 128 * rb);
     // DH threads hold a row, a column each; the block's groups of them take every
     // kGroups-th partial and are joined in turn
     constexpr int kGroups = THREADS / DH;
     const int group = tid / DH, d = tid % DH;
     // partials per round, their loads in flight together (at Dh = 256, 40 partials: 8
     // 22.7 us, 4 23.1, 16 26.0 for the whole step)
-    constexpr int kG = 8;
+    constexpr int kG = TWICE ? 4 : 8;
     float M = -INFINITY, l = 0.f, o = 0.f;
     for (int i0 = group; i0 < n; i0 += kG * kGroups) {
-      float mv[kG], lv[kG], ov[kG];
+      float mv[kG], lv[kG], ov[kG], rest[kG];
 #pragma unroll
       for (int e = 0; e < kG; ++e) {
         // (past the end the last one again, with the weight 0: a load under a
         // condition is not issued together with the others)
         const int i = i0 + e * kGroups;
-        const size_t at = at0 + (size_t)min(i, n - 1) * part_rows;
+        const int k = min(i, n - 1);
+        const size_t at = at0 + (size_t)k * part_rows;
+        const size_t o_at = TWICE ? segments0 + at + (size_t)(k & ~3) * part_rows : at;
         mv[e] = __ldcg(p.m_part + at);
         lv[e] = __ldcg(p.l_part + at);
-        ov[e] = __ldcg(p.o_part + at * DH + d);
+        ov[e] = __ldcg(p.o_part + o_at * DH + d);
+        rest[e] = TWICE ? __ldcg(p.o_part + (o_at + 4 * part_rows) * DH + d) : 0.f;
         if (i >= n) mv[e] = -INFINITY;
       }
       float Mg = M;
@@ -933,7 +981,7 @@ __global__ void __launch_bounds__(THREADS) attn_decode_paged_join(const DecodePa
       for (int e = 0; e < kG; ++e) {
         const float f = (mv[e] == -INFINITY) ? 0.f : ex2_approx(mv[e] - Mg);
         l = fmaf(f, lv[e], l);
-        o = fmaf(f, ov[e], o);
+        o = fmaf(f, ov[e] + rest[e], o);
       }
       M = Mg;
     }

@@ -331,6 +331,15 @@ __device__ __forceinline__ void tmem_cp_128x256b_warp(uint32_t taddr, uint64_t s
       : "memory");
 }
 
+// The same for 32 rows x 128 bits (8 bf16 per row): row r to lanes r, 32 + r, 64 + r and
+// 96 + r, four 32-bit columns from taddr.
+__device__ __forceinline__ void tmem_cp_32x128b_x4_warp(uint32_t taddr, uint64_t s_desc) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n}" ::"r"(taddr), "l"(s_desc)
+      : "memory");
+}
+
 __device__ __forceinline__ void mma_commit_warp(uint64_t* bar) {
   asm volatile(
       "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"

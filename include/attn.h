@@ -308,10 +308,10 @@ int attn_paged_append(const void* k, const void* v, void* kpages, void* vpages, 
  *            kept between calls; calls that may overlap on the GPU need one
  *            each.
  * Any Hq / Hkv runs on the tensor cores.  The same inputs give the same bits.
- * Where the softmax weights meet V they are rounded to bf16, by up to 2^-8 of
- * each (as in attn_fwd, and in attn_decode with grouped heads; with Hq = Hkv
- * attn_decode keeps them in fp32, so the output of such a caller moves by
- * about a rounding of its own).  Their sum, and `weights`, are of fp32 ones.
+ * Where the softmax weights meet V they are held to 2^-14 of each (two bf16
+ * parts) with up to 16 query heads per K/V head, and rounded to bf16 (2^-8, as
+ * in attn_fwd and attn_decode) with more.  Their sum, and `weights`, are of
+ * fp32 ones.
  * An infinity in a visible V row can make that column of the output NaN (a key
  * may also meet weights of exactly 0 in the tensor-core product).
  */
