@@ -191,7 +191,8 @@ cudaError_t launch_decode_paged(const void* q, const void* kpages, const void* v
   const int box = paged_box_rows(cache.page, Dh);
   const long long pages = (long long)cache.num_pages * Hkv;
   CUtensorMap mq, mk, mv;
-  const int q_rows = G <= kPagedTwoParts ? kPagedTwoParts : G <= kCopiesMaxGroup ? 32 : 128;   // (see the kernel)
+  // rows per load: the kernel's rows, or half of the 32 that hold the heads twice
+  const int q_rows = G <= kPagedTwoParts ? kPagedTwoParts : G <= kCopiesMaxGroup ? 32 : 128;
   if (!encode_bf16_map(&mq, q, Dh, G, (long long)B * Hkv, q_rows) ||
       !encode_bf16_map(&mk, kpages, Dh, cache.page, pages, box) ||
       !encode_bf16_map(&mv, vpages, Dh, cache.page, pages, box))

@@ -529,7 +529,8 @@ __device__ __forceinline__ void decode_paged_softmax(DecodePagedSmem<DH>& sm,
   const int col0 = REP == 4 ? warp * kMine : 0;
   const bool twice = REP == 4 && p.G <= kPagedTwoParts;
   const bool rest = twice && lane >= kPagedTwoParts;
-  const int head = REP != 4 ? warp * 32 + lane : twice ? lane % kPagedTwoParts : lane;   // in the block
+  // in the block of query heads
+  const int head = REP != 4 ? warp * 32 + lane : twice ? lane % kPagedTwoParts : lane;
   const float2 part2 = rest ? make_float2(-1.f, -1.f) : make_float2(0.f, 0.f);
   const int copy = REP == 4 ? warp : 0;
   const int tid = warp * 32 + lane;
