@@ -1,6 +1,7 @@
 // key_weights_few_sm103a.cuh -- the attention weight that each key of a prompt
 // received from a few voting queries (sm_103a): attn_key_weights with `queries`
-// set, where the voting queries of a K/V head's whole group fit in one tile.
+// set, or of a prompt of up to 32 rows, where the voting queries of a K/V head's
+// whole group fit in one tile.
 //
 //   w[b, g, j] (+)= sum over heads h of the group and the last `queries` queries
 //                   i >= j of  exp(scale q_hi . k_j - lse_hi)
