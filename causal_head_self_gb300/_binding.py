@@ -11,6 +11,7 @@ import ctypes
 import functools
 import os
 import threading
+import typing
 
 import torch
 
@@ -34,10 +35,19 @@ ATTN_ERR_CHECK = 7
 ABI_SYMBOLS = ("attn_fwd", "attn_fwd_lse", "attn_fwd_chunk", "attn_bwd", "attn_decode",
                "attn_decode_ring", "attn_decode_noalloc", "attn_status", "attn_error_string",
                "attn_version", "attn_debug_inject_fault", "attn_paged_append", "attn_decode_paged",
-               "attn_decode_paged_workspace", "attn_key_weights", "attn_cache_evict")
+               "attn_decode_paged_workspace", "attn_key_weights", "attn_cache_evict",
+               "attn_fwd_packed", "attn_fwd_packed_workspace", "attn_bwd_packed",
+               "attn_bwd_packed_workspace", "attn_rope", "attn_rope_append",
+               "attn_rope_frequencies", "attn_cache_plan")
 
 _lib = None
 _lock = threading.Lock()
+
+
+class Rows(ctypes.Structure):
+    """attn_rows_t: rows of heads at any strides, in elements."""
+    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_longlong),
+                ("row", ctypes.c_longlong), ("head", ctypes.c_longlong)]
 
 
 class AttnError(RuntimeError):
@@ -82,6 +92,28 @@ def load():
             lib.attn_cache_evict.restype = i
             lib.attn_cache_evict.argtypes = [vp, vp, vp, i, vp, vp, i, i, vp, i, vp, i, vp, vp] \
                 + [i] * 6 + [vp]
+            size = ctypes.POINTER(ctypes.c_size_t)
+            rows = ctypes.POINTER(Rows)
+            lib.attn_fwd_packed.restype = i
+            lib.attn_fwd_packed.argtypes = ([rows] * 4 + [vp, vp, vp, ctypes.c_size_t] + [i] * 7
+                                            + [f, vp])
+            lib.attn_fwd_packed_workspace.restype = i
+            lib.attn_fwd_packed_workspace.argtypes = [i, i, size]
+            lib.attn_bwd_packed.restype = i
+            lib.attn_bwd_packed.argtypes = ([rows] * 5 + [vp] + [rows] * 3
+                                            + [vp, vp, ctypes.c_size_t] + [i] * 7 + [f, vp])
+            lib.attn_bwd_packed_workspace.restype = i
+            lib.attn_bwd_packed_workspace.argtypes = [i, i, i, size]
+            lib.attn_rope.restype = i
+            lib.attn_rope.argtypes = [rows, rows, i, rows, rows, i, vp, vp, f] + [i] * 6 + [vp]
+            lib.attn_rope_append.restype = i
+            lib.attn_rope_append.argtypes = ([rows, rows, i, rows, rows, rows, i, vp, vp, f, vp, vp,
+                                              vp] + [i] * 7 + [vp])
+            lib.attn_rope_frequencies.restype = i
+            lib.attn_rope_frequencies.argtypes = [vp, vp, i, ctypes.c_double, i] \
+                + [ctypes.c_double] * 4
+            lib.attn_cache_plan.restype = i
+            lib.attn_cache_plan.argtypes = [vp] * 10 + [i] * 6 + [vp]
             lib.attn_status.restype = i
             lib.attn_status.argtypes = [vp]
             lib.attn_error_string.restype = ctypes.c_char_p
@@ -558,3 +590,284 @@ def attn_cache_evict(kpages, vpages, weights, table, seqlens, budget, recent=0, 
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_cache_evict")
     return newlens, keep
+
+
+# ---------------------------------------------------------------------------
+# packed sequences, rotary positions, the plan of a serving step (include/attn.h)
+
+def _check_heads(name, t, shape, device):
+    """A bf16 tensor of that shape on that GPU, the values of a head side by side."""
+    try:
+        if (t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == device >= 0
+                and t.stride(-1) == 1):
+            return
+    except AttributeError:
+        pass
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA bfloat16 tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.stride(-1) != 1:
+        raise ValueError(f"the values of a head must lie side by side in {name}")
+    raise ValueError(f"{name} must be on the same device as the other tensors")
+
+
+def _heads(name, t, shape, device):
+    """That tensor [T, H, Dh], or a batch [B, H, S, Dh], as the library takes it."""
+    _check_heads(name, t, shape, device)
+    if len(shape) == 3:
+        return Rows(t.data_ptr(), 0, t.stride(0), t.stride(1))
+    return Rows(t.data_ptr(), t.stride(0), t.stride(2), t.stride(1))
+
+
+def _packed_shape(q, k, cu_seqlens):
+    """B, Hq, Hkv, T, Dh and device of a packed call."""
+    T, Hq, Dh = _shape("q", q, 3)
+    Hkv = _shape("k", k, 3)[1]
+    n = _shape("cu_seqlens", cu_seqlens, 1)[0]
+    if n < 1 or n > 0x7fffffff or T > 0x7fffffff:
+        raise ValueError("cu_seqlens must have B + 1 entries, and less than 2^31 rows")
+    device = q.get_device()
+    if device < 0:
+        raise TypeError("q must be a CUDA bfloat16 tensor")
+    _check_current(device)
+    _check("cu_seqlens", cu_seqlens, torch.int32, (n,), device)
+    return n - 1, Hq, Hkv, T, Dh, device
+
+
+@functools.lru_cache(maxsize=4096)
+def _packed_workspace(B, Hq, T, backward):
+    size = ctypes.c_size_t()
+    if backward:
+        rc = load().attn_bwd_packed_workspace(B, Hq, T, ctypes.byref(size))
+    else:
+        rc = load().attn_fwd_packed_workspace(B, T, ctypes.byref(size))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_bwd_packed_workspace" if backward else "attn_fwd_packed_workspace")
+    return size.value
+
+
+def attn_packed_workspace(q, cu_seqlens, *, backward=False):
+    """Bytes of workspace that attn_fwd_packed, or attn_bwd_packed, needs for
+    tensors of these shapes."""
+    T, Hq, _ = _shape("q", q, 3)
+    n = _shape("cu_seqlens", cu_seqlens, 1)[0]
+    return _packed_workspace(_int32("the number of sequences", n - 1), _int32("heads", Hq),
+                             _int32("rows", T), bool(backward))
+
+
+def _workspace(workspace, need, device, tensor, stream):
+    if workspace is None:
+        return _empty((need,), torch.uint8, tensor.device, stream)
+    if (not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8
+            or workspace.get_device() != device or not workspace.is_contiguous()):
+        raise TypeError("workspace must be a contiguous CUDA uint8 tensor on the same device")
+    return workspace
+
+
+def attn_fwd_packed(q, k, v, cu_seqlens, o=None, lse=None, *, causal=True, window=0, scale=0.0,
+                    workspace=None, stream=None):
+    """attn_fwd of sequences that lie one behind another: q [T,Hq,Dh], k and v
+    [T,Hkv,Dh] bf16 at any strides (slices of one projection's output as they
+    are), cu_seqlens [B+1] int32 the first row of each sequence and the last
+    one's end.  lse [Hq,T] fp32, where given, receives the log-sum-exps.  Rows
+    of no sequence keep what o and lse hold (nothing, where o is allocated
+    here).  workspace: a uint8 tensor of attn_packed_workspace() bytes (None:
+    allocated here by torch, on the call's stream).  Returns o."""
+    window = _int32("window", window)
+    B, Hq, Hkv, T, Dh, device = _packed_shape(q, k, cu_seqlens)
+    rq = _heads("q", q, (T, Hq, Dh), device)
+    rk = _heads("k", k, (T, Hkv, Dh), device)
+    rv = _heads("v", v, (T, Hkv, Dh), device)
+    if lse is not None:
+        _check("lse", lse, torch.float32, (Hq, T), device)
+    if o is None:
+        o = _empty((T, Hq, Dh), torch.bfloat16, q.device, stream)
+    ro = _heads("o", o, (T, Hq, Dh), device)
+    workspace = _workspace(workspace, _packed_workspace(B, 1, T, False), device, q, stream)
+    rc = load().attn_fwd_packed(rq, rk, rv, ro, None if lse is None else lse.data_ptr(),
+                                cu_seqlens.data_ptr(), workspace.data_ptr(), workspace.numel(), B,
+                                Hq, Hkv, T, Dh, int(bool(causal)), window, float(scale),
+                                _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_fwd_packed")
+    return o
+
+
+def attn_bwd_packed(q, k, v, o, dout, lse, cu_seqlens, dq=None, dk=None, dv=None, *, causal=True,
+                    window=0, scale=0.0, workspace=None, stream=None):
+    """Backward pass of attn_fwd_packed: (dq, dk, dv) from its inputs, the o and
+    lse [Hq,T] it gave, and dout = dL/do.  The gradients may be slices of one
+    wider tensor, as q, k and v may; rows of no sequence are not written."""
+    window = _int32("window", window)
+    B, Hq, Hkv, T, Dh, device = _packed_shape(q, k, cu_seqlens)
+    wide, narrow = (T, Hq, Dh), (T, Hkv, Dh)
+    _check("lse", lse, torch.float32, (Hq, T), device)
+    ins = [_heads(name, t, shape, device) for name, t, shape in (
+        ("q", q, wide), ("k", k, narrow), ("v", v, narrow), ("o", o, wide), ("dout", dout, wide))]
+    dq = _empty(wide, torch.bfloat16, q.device, stream) if dq is None else dq
+    dk = _empty(narrow, torch.bfloat16, q.device, stream) if dk is None else dk
+    dv = _empty(narrow, torch.bfloat16, q.device, stream) if dv is None else dv
+    outs = [_heads(name, t, shape, device) for name, t, shape in (
+        ("dq", dq, wide), ("dk", dk, narrow), ("dv", dv, narrow))]
+    workspace = _workspace(workspace, _packed_workspace(B, Hq, T, True), device, q, stream)
+    rc = load().attn_bwd_packed(*ins, lse.data_ptr(), *outs, cu_seqlens.data_ptr(),
+                                workspace.data_ptr(), workspace.numel(), B, Hq, Hkv, T, Dh,
+                                int(bool(causal)), window, float(scale), _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_bwd_packed")
+    return dq, dk, dv
+
+
+class RopeFrequencies(typing.NamedTuple):
+    """turns [rotary_dim/2] int64 on the GPU (2^-64 turns per token) and the
+    factor on the turned values."""
+    turns: torch.Tensor
+    amplitude: float
+
+
+_SCALINGS = {"none": 0, "linear": 1, "base": 2, "turns": 3, "yarn": 4}
+
+
+def attn_rope_frequencies(rotary_dim, base=10000.0, *, scaling="none", factor=1.0, low=1.0,
+                          high=None, original_len=8192, device="cuda"):
+    """What attn_rope turns by: base^(-2 i / rotary_dim) radians per token for
+    pair i, scaled for a longer context by "linear", "base", "turns" (pairs by
+    the turns they make over original_len: kept from `high` on, divided by
+    factor up to `low`, blended between; high is 4) or "yarn" (the same with an
+    amplitude, high 32); see include/attn.h."""
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}")
+    if high is None:
+        high = 32.0 if scaling == "yarn" else 4.0
+    rotary_dim = _int32("rotary_dim", rotary_dim)
+    turns = torch.zeros(max(rotary_dim // 2, 1), dtype=torch.int64)
+    amplitude = ctypes.c_float()
+    rc = load().attn_rope_frequencies(turns.data_ptr() if 0 < rotary_dim <= 256 else None,
+                                      ctypes.addressof(amplitude), rotary_dim, float(base),
+                                      _SCALINGS[scaling], float(factor), float(low), float(high),
+                                      float(original_len))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_rope_frequencies")
+    return RopeFrequencies(turns.to(device), amplitude.value)
+
+
+def _rope_shape(q, k, positions, frequencies):
+    """What both rotations check: B, S, Hq, Hkv, Dh, rotary_dim, device and the shapes."""
+    shape = getattr(q, "shape", None)
+    if shape is None or len(shape) not in (3, 4):
+        raise ValueError("q must be [T,Hq,Dh] or [B,Hq,S,Dh]")
+    packed = len(shape) == 3
+    Hkv = _shape("k", k, len(shape))[1]
+    Hq, Dh = shape[1], shape[-1]
+    B, S = (1, shape[0]) if packed else (shape[0], shape[2])
+    for name, x in (("batch", B), ("rows", S), ("heads", max(Hq, Hkv))):
+        _int32(name, x)
+    kshape = (S, Hkv, Dh) if packed else (B, Hkv, S, Dh)
+    device = q.get_device()
+    if device < 0:
+        raise TypeError("q must be a CUDA bfloat16 tensor")
+    _check_current(device)
+    _check("positions", positions, torch.int32, (S,) if packed else (B, S), device)
+    turns = frequencies.turns
+    n = _shape("turns", turns, 1)[0]
+    _check("turns", turns, torch.int64, (n,), device)
+    return B, S, Hq, Hkv, Dh, 2 * n, device, tuple(shape), kshape
+
+
+def attn_rope(q, k, positions, frequencies, q_out=None, k_out=None, *, interleaved=False,
+              inverse=False, stream=None):
+    """Rotary positions: the first rotary_dim values of each head of q and k,
+    packed [T,H,Dh] or batches [B,H,S,Dh] at any strides, turned in pairs
+    (halves, or with interleaved=True neighbours) by positions [T] or [B,S]
+    int32 times `frequencies` (attn_rope_frequencies).  A negative position
+    leaves the row out.  q_out and k_out may be q and k (in place); None:
+    allocated here.  inverse=True turns the other way: the gradients of q and
+    k from those of the outputs.  Returns (q_out, k_out)."""
+    B, S, Hq, Hkv, Dh, rot, device, qs, ks = _rope_shape(q, k, positions, frequencies)
+    rq, rk = _heads("q", q, qs, device), _heads("k", k, ks, device)
+    q_out = _empty(qs, torch.bfloat16, q.device, stream) if q_out is None else q_out
+    k_out = _empty(ks, torch.bfloat16, q.device, stream) if k_out is None else k_out
+    rc = load().attn_rope(rq, _heads("q_out", q_out, qs, device), Hq, rk,
+                          _heads("k_out", k_out, ks, device), Hkv, positions.data_ptr(),
+                          frequencies.turns.data_ptr(), float(frequencies.amplitude), B, S, Dh,
+                          rot, int(bool(interleaved)), int(bool(inverse)), _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_rope")
+    return q_out, k_out
+
+
+def attn_rope_append(q, k, v, positions, frequencies, kpages, vpages, slots, q_out=None,
+                     k_out=None, *, interleaved=False, stream=None):
+    """attn_rope of q and k, and the write of the turned k and of v to a paged
+    cache (pools [P,Hkv,page,Dh]) in the same pass: slots [T] or [B,S] int32
+    (attn_cache_plan gives them), a negative one writes nothing there.  q_out
+    None: in place.  k_out None: the turned keys go to the cache alone.  Returns
+    (q_out, k_out)."""
+    B, S, Hq, Hkv, Dh, rot, device, qs, ks = _rope_shape(q, k, positions, frequencies)
+    P, _, page, _ = pools = _shape("kpages", kpages, 4)
+    if pools[1] != Hkv or pools[3] != Dh:
+        raise ValueError("kpages must be [P, Hkv, page, Dh] matching k")
+    _int32("pages", P), _int32("page", page)
+    _check("kpages", kpages, torch.bfloat16, pools, device)
+    _check("vpages", vpages, torch.bfloat16, pools, device)
+    _check("slots", slots, torch.int32, positions.shape, device)
+    rq, rk, rv = (_heads("q", q, qs, device), _heads("k", k, ks, device),
+                  _heads("v", v, ks, device))
+    q_out = q if q_out is None else q_out
+    rc = load().attn_rope_append(rq, _heads("q_out", q_out, qs, device), Hq, rk,
+                                 None if k_out is None else _heads("k_out", k_out, ks, device), rv,
+                                 Hkv, positions.data_ptr(), frequencies.turns.data_ptr(),
+                                 float(frequencies.amplitude), kpages.data_ptr(),
+                                 vpages.data_ptr(), slots.data_ptr(), P, page, B, S, Dh, rot,
+                                 int(bool(interleaved)), _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_rope_append")
+    return q_out, k_out
+
+
+def attn_cache_plan(delta, seqlens, table, free_pages, num_free, *, rows, page, num_pages,
+                    seqlens_out=None, num_free_out=None, cu_seqlens=None, positions=None,
+                    slots=None, stream=None):
+    """The pages, slots and positions of a serving step, from the lengths on the
+    GPU: sequence b of a paged cache (table [B,cols], seqlens [B]) changes by
+    delta[b] rows, new tokens or (negative) rows taken back.  Free pages are a
+    stack: the first num_free [1] entries of free_pages.  Pages given back go
+    onto it, then pages that new rows need come off it, into table.  Lengths
+    and num_free change in place (or go to seqlens_out, num_free_out).  Returns
+    (cu_seqlens [B+1], positions [rows], slots [rows]) of the packed new tokens,
+    -1 behind the last; where they are more than `rows`, or pages do not
+    suffice, nothing changes and attn_status() says so.  All int32."""
+    rows, page = _int32("rows", rows), _int32("page", page)
+    num_pages = _int32("num_pages", num_pages)
+    B, cols = shape = _shape("table", table, 2)
+    capacity = _shape("free_pages", free_pages, 1)[0]
+    for name, x in (("table", max(B, cols)), ("free_pages", capacity)):
+        _int32(name, x)
+    device = table.get_device()
+    _check("table", table, torch.int32, shape, device)
+    _check_current(device)
+    for name, t, n in (("delta", delta, B), ("seqlens", seqlens, B),
+                       ("free_pages", free_pages, capacity), ("num_free", num_free, 1)):
+        _check(name, t, torch.int32, (n,), device)
+    if rows < 0:
+        raise AttnError(ATTN_ERR_INVALID_ARG, "attn_cache_plan")
+    seqlens_out = seqlens if seqlens_out is None else seqlens_out
+    num_free_out = num_free if num_free_out is None else num_free_out
+    cu_seqlens = _empty((B + 1,), torch.int32, table.device, stream) if cu_seqlens is None \
+        else cu_seqlens
+    positions = _empty((rows,), torch.int32, table.device, stream) if positions is None \
+        else positions
+    slots = _empty((rows,), torch.int32, table.device, stream) if slots is None else slots
+    for name, t, n in (("seqlens_out", seqlens_out, B), ("num_free_out", num_free_out, 1),
+                       ("cu_seqlens", cu_seqlens, B + 1), ("positions", positions, rows),
+                       ("slots", slots, rows)):
+        _check(name, t, torch.int32, (n,), device)
+    rc = load().attn_cache_plan(delta.data_ptr(), seqlens.data_ptr(), seqlens_out.data_ptr(),
+                                table.data_ptr(), free_pages.data_ptr(), num_free.data_ptr(),
+                                num_free_out.data_ptr(), cu_seqlens.data_ptr(),
+                                positions.data_ptr(), slots.data_ptr(), B, cols, page, num_pages,
+                                capacity, rows, _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_cache_plan")
+    return cu_seqlens, positions, slots

@@ -125,9 +125,11 @@ struct MapKey {
   const void* base;
   long long outer;
   int Dh, rows, box_rows, stride_rows;   // stride_rows 0: the 4-D form (whole rows)
+  long long row = 0, head = 0;           // packed rows: their strides (0: the other forms)
   bool operator==(const MapKey& o) const {
     return base == o.base && outer == o.outer && Dh == o.Dh && rows == o.rows &&
-           box_rows == o.box_rows && stride_rows == o.stride_rows;
+           box_rows == o.box_rows && stride_rows == o.stride_rows && row == o.row &&
+           head == o.head;
   }
 };
 struct MapCache {
@@ -182,6 +184,33 @@ bool encode_bf16_rows_map(CUtensorMap* map, const void* base, int Dh, int rows, 
   const cuuint64_t strides[3] = {row, 128, row * (cuuint64_t)rows};
   const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, (cuuint32_t)Dh / 64, 1};
   return cached_map(map, MapKey{base, outer, Dh, rows, box_rows, 0}, 4, dims, strides, box);
+}
+
+bool encode_packed_map(CUtensorMap* map, const PackedRows& x, int Dh, int T, int box_rows,
+                       bool padded, bool* heads_inner) {
+  // strides of an axis with one entry do not matter: any that the map takes
+  const long long head = x.H == 1 ? (x.row > Dh ? x.row : Dh) : x.head;
+  const long long row = T == 1 ? (x.H == 1 ? Dh : x.head) : x.row;
+  // the axes in the order of their strides
+  *heads_inner = x.H > 1 && head < row;
+  const cuuint64_t R = (cuuint64_t)row * 2, H = (cuuint64_t)head * 2;
+  const cuuint64_t rows = (cuuint64_t)T, heads = (cuuint64_t)x.H, height = (cuuint64_t)box_rows;
+  const cuuint32_t b = (cuuint32_t)box_rows;
+  const MapKey key{x.data, x.H, Dh, T, box_rows, padded ? -1 : -2, row, head};
+  const cuuint64_t d = (cuuint64_t)Dh;
+  if (padded) {
+    // the row axis twice (packed_sm103a.cuh)
+    const cuuint64_t dims_in[4] = {d, heads, height, rows}, dims[4] = {d, height, rows, heads};
+    const cuuint64_t strides_in[3] = {H, R, R}, strides[3] = {R, R, H};
+    const cuuint32_t box_in[4] = {64, 1, b, 1}, box[4] = {64, b, 1, 1};
+    return *heads_inner ? cached_map(map, key, 4, dims_in, strides_in, box_in)
+                        : cached_map(map, key, 4, dims, strides, box);
+  }
+  const cuuint64_t dims_in[3] = {d, heads, rows}, dims[3] = {d, rows, heads};
+  const cuuint64_t strides_in[2] = {H, R}, strides[2] = {R, H};
+  const cuuint32_t box_in[3] = {64, 1, b}, box[3] = {64, b, 1};
+  return *heads_inner ? cached_map(map, key, 3, dims_in, strides_in, box_in)
+                      : cached_map(map, key, 3, dims, strides, box);
 }
 
 }  // namespace chs
@@ -742,5 +771,376 @@ extern "C" int attn_cache_evict(void* kpages, void* vpages, float* weights, int 
       kpages, vpages, table, table_out, cols_out, seqlens, newlens, weights, weights_stride,
       weights_out, weights_out_stride, keep, B, Hkv, cache, Dh, budget, recent, launch_info(st),
       stream);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------------------
+// Packed sequences and tokens: attention over sequences of different lengths, rotary
+// positions, the plan of a serving step.
+namespace {
+
+// A tensor of B x S rows of H heads, as a call got it.
+struct Rows {
+  const attn_rows_t* t;
+  int B, S, H, Dh;
+  long long batch() const { return B > 1 ? t->batch_stride : 0; }
+  long long row() const { return S > 1 ? t->row_stride : 0; }
+  long long head() const { return H > 1 ? t->head_stride : 0; }
+  // elements from the first to behind the last
+  long long extent() const {
+    return (B - 1) * batch() + (S - 1) * row() + (H - 1) * head() + Dh;
+  }
+  size_t bytes() const { return (size_t)extent() * 2; }
+  bool empty() const { return B == 0 || S == 0 || H == 0; }
+};
+
+// A map's strides are of 40 bits, in bytes; no tensor on a GPU reaches 2^46 elements.
+constexpr long long kMostStride = 1ll << 38, kMostExtent = 1ll << 46;
+
+// Aligned, with strides that are whole 16 bytes and (of axes with more than one entry) at
+// least `least`.
+bool rows_usable(const Rows& x, long long least) {
+  if (x.empty()) return true;
+  if (!x.t || !x.t->data || !aligned16(x.t->data)) return false;
+  const long long stride[] = {x.t->batch_stride, x.t->row_stride, x.t->head_stride};
+  const int n[] = {x.B, x.S, x.H};
+  for (int i = 0; i < 3; ++i)
+    if (n[i] > 1 && (stride[i] % 8 != 0 || stride[i] < least || stride[i] > kMostStride ||
+                     (stride[i] > 0 && n[i] - 1 > kMostExtent / stride[i])))
+      return false;
+  return true;
+}
+
+// No two elements at one place: each axis steps over everything of the axes below it.
+bool rows_distinct(const Rows& x) {
+  if (x.empty()) return true;
+  long long stride[] = {x.batch(), x.row(), x.head()};
+  long long n[] = {x.B, x.S, x.H};
+  long long extent = x.Dh;
+  for (int pass = 0; pass < 3; ++pass) {
+    int at = -1;
+    for (int i = 0; i < 3; ++i)
+      if (n[i] > 1 && (at < 0 || stride[i] < stride[at])) at = i;
+    if (at < 0) break;
+    if (stride[at] < extent) return false;
+    extent += (n[at] - 1) * stride[at];
+    n[at] = 1;
+  }
+  return true;
+}
+
+bool rows_same(const Rows& a, const Rows& b) {
+  return a.t->data == b.t->data && a.batch() == b.batch() && a.row() == b.row() &&
+         a.head() == b.head();
+}
+
+// May the two share an element?  Heads of one wider tensor (a projection's output, split into
+// queries, keys and values) lie between one another: rows at one stride, each within its own
+// part of it.
+bool rows_overlap(const Rows& a, const Rows& b) {
+  if (a.empty() || b.empty()) return false;
+  if (!overlaps(a.t->data, a.bytes(), b.t->data, b.bytes())) return false;
+  const long long R = a.row();
+  const bool one_stride = a.S > 1 && b.row() == R && (a.B == 1 || a.batch() == a.S * R) &&
+                          (b.B == 1 || b.batch() == b.S * R);
+  if (!one_stride) return true;
+  const long long wa = (a.H - 1) * a.head() + a.Dh, wb = (b.H - 1) * b.head() + b.Dh;
+  const long long bytes = (long long)(reinterpret_cast<uintptr_t>(b.t->data) -
+                                      reinterpret_cast<uintptr_t>(a.t->data));
+  const long long step = 2 * R;
+  const long long d = ((bytes % step) + step) % step / 2;   // b's place in a's row
+  return !(wa <= R && wb <= R && d >= wa && d + wb <= R);
+}
+
+bool rows_overlap(const Rows& a, const void* p, size_t bytes) {
+  return !a.empty() && p != nullptr && bytes > 0 && overlaps(a.t->data, a.bytes(), p, bytes);
+}
+
+chs::PackedRows packed_rows(const Rows& x) {
+  return chs::PackedRows{x.t->data, x.t->row_stride, x.t->head_stride, x.H};
+}
+chs::RopeRows rope_rows(const Rows& x) {
+  if (x.empty() || !x.t) return chs::RopeRows{};
+  return chs::RopeRows{x.t->data, x.batch(), x.row(), x.head()};
+}
+
+// The size rules of the packed calls, shared with their workspace queries.
+int packed_check(int B, int Hq, int T) {
+  if (B < 0 || T < 0 || Hq < 1) return ATTN_ERR_INVALID_ARG;
+  // rows of the statistics, tiles and work items are 32-bit
+  if ((long long)T + 127ll * B > kMostRows) return ATTN_ERR_INVALID_ARG;
+  if (chs::packed_max_tiles(B, T) * Hq > kMostRows) return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+int packed_shape(chs::PackedShape* s, float* scale_log2, const int* cu, int B, int Hq, int Hkv,
+                 int T, int Dh, int causal, int window, float scale) {
+  if (Hkv < 1 || Hq < 1 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+  if (Dh != 64 && Dh != 128 && Dh != 256) return ATTN_ERR_UNSUPPORTED;
+  const int rc = packed_check(B, Hq, T);
+  if (rc != ATTN_OK) return rc;
+  if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
+  if (window < 0) window = 0;
+  if (window > 0 && !causal) return ATTN_ERR_INVALID_ARG;
+  if (window > T) window = T;   // (the same, and sums of positions and windows stay in 32 bits)
+  if (!resolve_scale(scale, Dh, scale_log2)) return ATTN_ERR_INVALID_ARG;
+  *s = chs::PackedShape{B, Hq, Hkv, T, Dh, causal, window, cu};
+  return ATTN_OK;
+}
+
+}  // namespace
+
+extern "C" int attn_fwd_packed_workspace(int B, int T, size_t* bytes) {
+  const int rc = packed_check(B, 1, T);
+  if (rc != ATTN_OK) return rc;
+  if (!bytes) return ATTN_ERR_INVALID_ARG;
+  *bytes = chs::fwd_packed_workspace_bytes(B, T);
+  return ATTN_OK;
+}
+
+extern "C" int attn_bwd_packed_workspace(int B, int Hq, int T, size_t* bytes) {
+  const int rc = packed_check(B, Hq, T);
+  if (rc != ATTN_OK) return rc;
+  if (!bytes) return ATTN_ERR_INVALID_ARG;
+  *bytes = chs::bwd_packed_workspace_bytes(B, Hq, T);
+  return ATTN_OK;
+}
+
+extern "C" int attn_fwd_packed(const attn_rows_t* q, const attn_rows_t* k, const attn_rows_t* v,
+                               const attn_rows_t* o, float* lse, const int* cu_seqlens,
+                               void* workspace, size_t workspace_bytes, int B, int Hq, int Hkv,
+                               int T, int Dh, int causal, int window, float scale,
+                               cudaStream_t stream) {
+  chs::PackedShape s;
+  float scale_log2 = 0.f;
+  int rc = packed_shape(&s, &scale_log2, cu_seqlens, B, Hq, Hkv, T, Dh, causal, window, scale);
+  if (rc != ATTN_OK) return rc;
+  if (B == 0 || T == 0) return ATTN_OK;
+  const Rows Q{q, 1, T, Hq, Dh}, K{k, 1, T, Hkv, Dh}, V{v, 1, T, Hkv, Dh}, O{o, 1, T, Hq, Dh};
+  for (const Rows* x : {&Q, &K, &V, &O})
+    if (!rows_usable(*x, Dh)) return ATTN_ERR_INVALID_ARG;
+  if (!rows_distinct(O)) return ATTN_ERR_INVALID_ARG;
+  if (!usable(cu_seqlens, 4) || (lse && !usable(lse, 4)) || !usable(workspace, 256))
+    return ATTN_ERR_INVALID_ARG;
+  const size_t lb = lse ? (size_t)Hq * T * 4 : 0, cb = ((size_t)B + 1) * 4;
+  for (const Rows* x : {&Q, &K, &V}) {
+    if (rows_overlap(O, *x) || rows_overlap(*x, lse, lb) ||
+        rows_overlap(*x, workspace, workspace_bytes))
+      return ATTN_ERR_INVALID_ARG;
+  }
+  if (rows_overlap(O, lse, lb) || rows_overlap(O, cu_seqlens, cb) ||
+      rows_overlap(O, workspace, workspace_bytes) ||
+      overlaps(workspace, workspace_bytes, cu_seqlens, cb) ||
+      (lse && (overlaps(lse, lb, cu_seqlens, cb) || overlaps(lse, lb, workspace, workspace_bytes))))
+    return ATTN_ERR_INVALID_ARG;
+  if (workspace_bytes < chs::fwd_packed_workspace_bytes(B, T)) return ATTN_ERR_SCRATCH_LIMIT;
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&st)) != ATTN_OK) return rc;
+  const cudaError_t e = chs::launch_fwd_packed(s, packed_rows(Q), packed_rows(K), packed_rows(V),
+                                               packed_rows(O), lse, workspace, scale_log2,
+                                               launch_info(st), stream);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+extern "C" int attn_bwd_packed(const attn_rows_t* q, const attn_rows_t* k, const attn_rows_t* v,
+                               const attn_rows_t* o, const attn_rows_t* dout, const float* lse,
+                               const attn_rows_t* dq, const attn_rows_t* dk, const attn_rows_t* dv,
+                               const int* cu_seqlens, void* workspace, size_t workspace_bytes,
+                               int B, int Hq, int Hkv, int T, int Dh, int causal, int window,
+                               float scale, cudaStream_t stream) {
+  chs::PackedShape s;
+  float scale_log2 = 0.f;
+  int rc = packed_shape(&s, &scale_log2, cu_seqlens, B, Hq, Hkv, T, Dh, causal, window, scale);
+  if (rc != ATTN_OK) return rc;
+  if (B == 0 || T == 0) return ATTN_OK;
+  const Rows in[] = {{q, 1, T, Hq, Dh}, {k, 1, T, Hkv, Dh}, {v, 1, T, Hkv, Dh}, {o, 1, T, Hq, Dh},
+                     {dout, 1, T, Hq, Dh}};
+  const Rows out[] = {{dq, 1, T, Hq, Dh}, {dk, 1, T, Hkv, Dh}, {dv, 1, T, Hkv, Dh}};
+  for (const Rows& x : in)
+    if (!rows_usable(x, Dh)) return ATTN_ERR_INVALID_ARG;
+  for (const Rows& x : out)
+    if (!rows_usable(x, Dh) || !rows_distinct(x)) return ATTN_ERR_INVALID_ARG;
+  if (!usable(cu_seqlens, 4) || !usable(lse, 4) || !usable(workspace, 256))
+    return ATTN_ERR_INVALID_ARG;
+  const size_t lb = (size_t)Hq * T * 4, cb = ((size_t)B + 1) * 4;
+  for (const Rows& x : in)
+    if (rows_overlap(x, workspace, workspace_bytes)) return ATTN_ERR_INVALID_ARG;
+  for (int a = 0; a < 3; ++a) {
+    for (const Rows& x : in)
+      if (rows_overlap(out[a], x)) return ATTN_ERR_INVALID_ARG;
+    for (int b = a + 1; b < 3; ++b)
+      if (rows_overlap(out[a], out[b])) return ATTN_ERR_INVALID_ARG;
+    if (rows_overlap(out[a], lse, lb) || rows_overlap(out[a], cu_seqlens, cb) ||
+        rows_overlap(out[a], workspace, workspace_bytes))
+      return ATTN_ERR_INVALID_ARG;
+  }
+  if (overlaps(workspace, workspace_bytes, cu_seqlens, cb) ||
+      overlaps(workspace, workspace_bytes, lse, lb))
+    return ATTN_ERR_INVALID_ARG;
+  if (workspace_bytes < chs::bwd_packed_workspace_bytes(B, Hq, T)) return ATTN_ERR_SCRATCH_LIMIT;
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&st)) != ATTN_OK) return rc;
+  const float sc = scale == 0.f ? (float)(1.0 / std::sqrt((double)Dh)) : scale;
+  const cudaError_t e = chs::launch_bwd_packed(
+      s, packed_rows(in[0]), packed_rows(in[1]), packed_rows(in[2]), packed_rows(in[3]),
+      packed_rows(in[4]), lse, packed_rows(out[0]), packed_rows(out[1]), packed_rows(out[2]),
+      workspace, sc, launch_info(st), stream);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+extern "C" int attn_rope_frequencies(unsigned long long* turns, float* amplitude, int rotary_dim,
+                                     double base, int scaling, double factor, double low,
+                                     double high, double original_len) {
+  if (!turns || !amplitude || rotary_dim < 16 || rotary_dim > 256 || rotary_dim % 16 != 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (scaling < ATTN_ROPE_NONE || scaling > ATTN_ROPE_YARN) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(base) || base < 1.0) return ATTN_ERR_INVALID_ARG;
+  if (scaling != ATTN_ROPE_NONE && (!std::isfinite(factor) || factor < 1.0))
+    return ATTN_ERR_INVALID_ARG;
+  const bool blend = scaling == ATTN_ROPE_TURNS || scaling == ATTN_ROPE_YARN;
+  if (blend && (!std::isfinite(low) || !std::isfinite(high) || !(high > low) ||
+                !std::isfinite(original_len) || !(original_len > 0.0)))
+    return ATTN_ERR_INVALID_ARG;
+  if (scaling == ATTN_ROPE_BASE) base *= std::pow(factor, rotary_dim / (rotary_dim - 2.0));
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    // at most 1 / (2 pi)
+    double f = std::pow(base, -2.0 * i / rotary_dim) / 6.283185307179586476925;
+    if (scaling == ATTN_ROPE_LINEAR) f /= factor;
+    if (blend) {
+      const double keep = std::fmin(1.0, std::fmax(0.0, (original_len * f - low) / (high - low)));
+      f *= keep + (1.0 - keep) / factor;
+    }
+    turns[i] = (unsigned long long)std::ldexp(f, 64);
+  }
+  *amplitude = scaling == ATTN_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+  return ATTN_OK;
+}
+
+namespace {
+
+// Shared by attn_rope and attn_rope_append.
+int rope_common(const attn_rows_t* q, const attn_rows_t* q_out, int Hq, const attn_rows_t* k,
+                const attn_rows_t* k_out, int Hkv, const attn_rows_t* v, const int* positions,
+                const unsigned long long* turns, float amplitude, void* kpages, void* vpages,
+                const int* slots, int num_pages, int page, bool append, int B, int S, int Dh,
+                int rot, int interleaved, int inverse, cudaStream_t stream) {
+  if (B < 0 || S < 0 || Hq < 0 || Hkv < 0 || Hq + Hkv < 1) return ATTN_ERR_INVALID_ARG;
+  if (Dh != 64 && Dh != 128 && Dh != 256) return ATTN_ERR_UNSUPPORTED;
+  if (rot < 0 || rot > Dh || rot % 16 != 0) return ATTN_ERR_INVALID_ARG;
+  if ((interleaved != 0 && interleaved != 1) || (inverse != 0 && inverse != 1) ||
+      !std::isfinite(amplitude))
+    return ATTN_ERR_INVALID_ARG;
+  if ((long long)B * S > kMostRows || Hq > (1 << 24) || Hkv > (1 << 24))
+    return ATTN_ERR_INVALID_ARG;
+  if (append) {
+    const int rc = paged_check(B, Hkv, chs::PagedCache{num_pages, page, 1}, Dh);
+    if (rc != ATTN_OK) return rc;
+    if ((long long)num_pages * page > kMostRows) return ATTN_ERR_INVALID_ARG;   // slots are 32-bit
+  }
+  if (B == 0 || S == 0) return ATTN_OK;
+  const int n = B * S;
+  const Rows Q{q, B, S, Hq, Dh}, QO{q_out, B, S, Hq, Dh}, K{k, B, S, Hkv, Dh},
+      KO{k_out, B, S, k_out || !append ? Hkv : 0, Dh}, V{v, B, S, append ? Hkv : 0, Dh};
+  for (const Rows* x : {&Q, &K, &V})
+    if (!rows_usable(*x, 0)) return ATTN_ERR_INVALID_ARG;
+  for (const Rows* x : {&QO, &KO})
+    if (!rows_usable(*x, Dh) || !rows_distinct(*x)) return ATTN_ERR_INVALID_ARG;
+  if (!usable(positions, 4) || (rot > 0 && !usable(turns, 8))) return ATTN_ERR_INVALID_ARG;
+  if (append && (!usable(kpages, 16) || !usable(vpages, 16) || !usable(slots, 4)))
+    return ATTN_ERR_INVALID_ARG;
+  const size_t lens = (size_t)n * 4, tb = (size_t)rot / 2 * 8;
+  const size_t pool = append ? pool_bytes(Hkv, chs::PagedCache{num_pages, page, 1}, Dh) : 0;
+  // an output is its own input, or apart from every tensor
+  if ((!QO.empty() && !rows_same(Q, QO) && rows_overlap(QO, Q)) || rows_overlap(QO, K) ||
+      rows_overlap(QO, V) || rows_overlap(QO, KO) || rows_overlap(KO, Q) || rows_overlap(KO, V) ||
+      (!KO.empty() && !rows_same(K, KO) && rows_overlap(KO, K)))
+    return ATTN_ERR_INVALID_ARG;
+  for (const Rows* x : {&QO, &KO})
+    if (rows_overlap(*x, positions, lens) || rows_overlap(*x, turns, tb) ||
+        rows_overlap(*x, slots, append ? lens : 0))
+      return ATTN_ERR_INVALID_ARG;
+  if (append) {
+    for (const void* x : {kpages, vpages}) {
+      for (const Rows* y : {&Q, &QO, &K, &KO, &V})
+        if (rows_overlap(*y, x, pool)) return ATTN_ERR_INVALID_ARG;
+      if (overlaps(x, pool, positions, lens) || overlaps(x, pool, slots, lens) ||
+          (tb > 0 && overlaps(x, pool, turns, tb)))
+        return ATTN_ERR_INVALID_ARG;
+    }
+    if (overlaps(kpages, pool, vpages, pool)) return ATTN_ERR_INVALID_ARG;
+  }
+  DeviceState* st = nullptr;
+  const int rc = device_state(&st);
+  if (rc != ATTN_OK) return rc;
+  const chs::RopeShape s{B, S, Hq, Hkv, Dh, rot, positions, turns, amplitude, interleaved, inverse};
+  const chs::RopeRows qi = rope_rows(Q), qo = rope_rows(QO), ki = rope_rows(K), ko = rope_rows(KO);
+  const chs::RopeAppend a{rope_rows(V), kpages, vpages, slots, num_pages, page};
+  const cudaError_t e = chs::launch_rope(s, qi, QO.empty() ? nullptr : &qo, ki,
+                                         KO.empty() ? nullptr : &ko, append ? &a : nullptr,
+                                         launch_info(st), stream);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" int attn_rope(const attn_rows_t* q, const attn_rows_t* q_out, int Hq,
+                         const attn_rows_t* k, const attn_rows_t* k_out, int Hkv,
+                         const int* positions, const unsigned long long* turns, float amplitude,
+                         int B, int S, int Dh, int rotary_dim, int interleaved, int inverse,
+                         cudaStream_t stream) {
+  return rope_common(q, q_out, Hq, k, k_out, Hkv, nullptr, positions, turns, amplitude, nullptr,
+                     nullptr, nullptr, 0, 0, false, B, S, Dh, rotary_dim, interleaved, inverse,
+                     stream);
+}
+
+extern "C" int attn_rope_append(const attn_rows_t* q, const attn_rows_t* q_out, int Hq,
+                                const attn_rows_t* k, const attn_rows_t* k_out,
+                                const attn_rows_t* v, int Hkv, const int* positions,
+                                const unsigned long long* turns, float amplitude, void* kpages,
+                                void* vpages, const int* slots, int num_pages, int page, int B,
+                                int S, int Dh, int rotary_dim, int interleaved,
+                                cudaStream_t stream) {
+  return rope_common(q, q_out, Hq, k, k_out, Hkv, v, positions, turns, amplitude, kpages, vpages,
+                     slots, num_pages, page, true, B, S, Dh, rotary_dim, interleaved, 0, stream);
+}
+
+extern "C" int attn_cache_plan(const int* delta, const int* seqlens, int* seqlens_out, int* table,
+                               int* free_pages, const int* num_free, int* num_free_out,
+                               int* cu_seqlens, int* positions, int* slots, int B, int cols,
+                               int page, int num_pages, int capacity, int T,
+                               cudaStream_t stream) {
+  int rc = paged_check(B, 1, chs::PagedCache{num_pages, page, cols}, 64);
+  if (rc != ATTN_OK) return rc;
+  if (T < 0 || T > kMostRows || capacity < 1 || capacity > kMostRows) return ATTN_ERR_INVALID_ARG;
+  if ((long long)num_pages * page > kMostRows) return ATTN_ERR_INVALID_ARG;   // slots are 32-bit
+  if (B > chs::cache_plan_max_sequences()) return ATTN_ERR_UNSUPPORTED;
+  if (B == 0) return ATTN_OK;
+  if (!usable(delta, 4) || !usable(seqlens, 4) || !usable(seqlens_out, 4) || !usable(table, 4) ||
+      !usable(free_pages, 4) || !usable(num_free, 4) || !usable(num_free_out, 4) ||
+      !usable(cu_seqlens, 4) || (T > 0 && (!usable(positions, 4) || !usable(slots, 4))))
+    return ATTN_ERR_INVALID_ARG;
+  const size_t lens = (size_t)B * 4, rows = (size_t)T * 4;
+  const Span in[] = {{delta, lens}, {seqlens, lens}, {num_free, 4}};
+  const Span out[] = {{seqlens_out, lens}, {num_free_out, 4}, {table, (size_t)B * cols * 4},
+                      {free_pages, (size_t)capacity * 4}, {cu_seqlens, lens + 4},
+                      {T > 0 ? positions : nullptr, rows}, {T > 0 ? slots : nullptr, rows}};
+  for (int i = 0; i < 7; ++i) {
+    if (!out[i].p) continue;
+    for (int j = 0; j < 3; ++j) {
+      const bool in_place = (i == 0 && j == 1 && seqlens_out == seqlens) ||
+                            (i == 1 && j == 2 && num_free_out == num_free);
+      if (!in_place && overlaps(out[i].p, out[i].bytes, in[j].p, in[j].bytes))
+        return ATTN_ERR_INVALID_ARG;
+    }
+    for (int j = 0; j < i; ++j)
+      if (out[j].p && overlaps(out[i].p, out[i].bytes, out[j].p, out[j].bytes))
+        return ATTN_ERR_INVALID_ARG;
+  }
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&st)) != ATTN_OK) return rc;
+  const cudaError_t e = chs::launch_cache_plan(
+      chs::CachePlan{delta, seqlens, seqlens_out, table, free_pages, num_free, num_free_out,
+                     cu_seqlens, positions, slots, B, cols, page, num_pages, capacity, T},
+      launch_info(st), stream);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }

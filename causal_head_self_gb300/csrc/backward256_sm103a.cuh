@@ -71,23 +71,25 @@ __host__ __device__ constexpr uint32_t bwd256_packed_col(int kk) {
 }
 
 // 64-row query blocks [lo, hi] that see some key of 128-key block kb.
-__device__ __forceinline__ void bwd256_qblocks_of(const BwdParams& p, int kb, int& lo, int& hi) {
-  const int nq = (p.S + 63) / 64;
-  lo = 0;
+__device__ __forceinline__ void bwd256_qblocks_of(const BwdParams& p, const BwdSeq& q, int kb,
+                                                  int& lo, int& hi) {
+  const int nq = (q.S + 63) / 64;
+  lo = q.pad / 64;   // (the first block may be padding alone)
   hi = nq - 1;
   if (!p.causal) return;
-  lo = 2 * kb;   // query i sees key j only if j <= i
+  lo = max(lo, 2 * kb);   // query i sees key j only if j <= i
   if (p.window > 0) hi = min(hi, (128 * kb + 127 + p.window - 1) / 64);   // i - j < W
 }
 
 // 64-key blocks [lo, hi] that 128-row query block qb sees.
-__device__ __forceinline__ void bwd256_kblocks_of(const BwdParams& p, int qb, int& lo, int& hi) {
-  const int nk = (p.S + 63) / 64;
-  lo = 0;
+__device__ __forceinline__ void bwd256_kblocks_of(const BwdParams& p, const BwdSeq& q, int qb,
+                                                  int& lo, int& hi) {
+  const int nk = (q.S + 63) / 64;
+  lo = q.pad / 64;
   hi = nk - 1;
   if (!p.causal) return;
   hi = min(hi, (128 * qb + 127) / 64);
-  if (p.window > 0) lo = max(0, 128 * qb - p.window + 1) / 64;
+  if (p.window > 0) lo = max(lo, max(0, 128 * qb - p.window + 1) / 64);
 }
 
 // ============================================================ dV and dK passes
@@ -120,18 +122,14 @@ struct __align__(1024) Bwd256KvSmem {
 
 // Item w: 128-key block kb (earliest, i.e. heaviest under a causal mask,
 // first) of K/V head bkv = b * Hkv + g.
+template <bool PK>
 __device__ __forceinline__ BwdKvItem bwd256_kv_item_of(const BwdParams& p, int w) {
-  BwdKvItem r;
-  const int per = p.B * p.Hkv;
-  r.kb = w / per;
-  r.bkv = w - r.kb * per;
-  r.b = r.bkv / p.Hkv;
-  r.g = r.bkv - r.b * p.Hkv;
-  bwd256_qblocks_of(p, r.kb, r.lo, r.hi);
+  BwdKvItem r = bwd_kv_place_of<PK>(p, w);
+  bwd256_qblocks_of(p, r.seq, r.kb, r.lo, r.hi);
   return r;
 }
 
-template <bool DK>
+template <bool DK, bool PK>
 __device__ __forceinline__ void bwd256_kv_producer(Bwd256KvSmem<DK>& sm, const BwdParams& p,
                                                    const CUtensorMap* map_q,
                                                    const CUtensorMap* map_k,
@@ -144,21 +142,24 @@ __device__ __forceinline__ void bwd256_kv_producer(Bwd256KvSmem<DK>& sm, const B
   uint32_t u = 0, q_loaded = 0, q_par = 0, d_loaded = 0, d_par = 0;
   int items = 0;
   bool ok = true;
+  const int num_items = bwd_num_items<PK>(p, p.Hkv);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
-    if (w >= p.num_items) break;
-    const BwdKvItem I = bwd256_kv_item_of(p, w);
+    if (w >= num_items) break;
+    const BwdKvItem I = bwd256_kv_item_of<PK>(p, w);
     if (items > 0 && !(ok = mbar_wait(&sm.kv_empty, (uint32_t)(items - 1) & 1u, abort))) break;
     // (checked builds: a key block of the sequence, of a K/V head of the batch)
-    const bool kv_in_range = attn_check(I.kb >= 0 && 128 * I.kb < p.S && I.bkv >= 0 &&
-                                            I.bkv < p.B * p.Hkv,
+    const bool kv_in_range = attn_check(I.kb >= 0 && 128 * I.kb < I.seq.S && I.bkv >= 0 &&
+                                            I.bkv < p.B * p.Hkv && bwd_inside<PK>(p, I.seq),
                                         p.error_word);
     mbar_arrive_expect_tx(&sm.kv_full, kv_in_range ? (DK ? 2u : 1u) * Cfg::kBigTile : 0u);
     if (kv_in_range && (p.fault != 4 || it != 0)) {   // (the test hook withholds one K/V block)
       for (int hf = 0; hf < 4; ++hf) {
-        tma_load_3d(sm.k + hf * Cfg::kBigBox, map_k, &sm.kv_full, 64 * hf, 128 * I.kb, I.bkv);
+        bwd_load_once<PK>(sm.k + hf * Cfg::kBigBox, map_k, &sm.kv_full, 64 * hf, 128 * I.kb,
+                               I.bkv, p, I.seq, kPackedK);
         if (DK)
-          tma_load_3d(sm.v + hf * Cfg::kBigBox, map_v, &sm.kv_full, 64 * hf, 128 * I.kb, I.bkv);
+          bwd_load_once<PK>(sm.v + hf * Cfg::kBigBox, map_v, &sm.kv_full, 64 * hf,
+                                 128 * I.kb, I.bkv, p, I.seq, kPackedV);
       }
     }
     ++items;
@@ -167,10 +168,10 @@ __device__ __forceinline__ void bwd256_kv_producer(Bwd256KvSmem<DK>& sm, const B
       for (int qb = I.lo; qb <= I.hi; ++qb, ++u) {
         const uint32_t st = u % Smem::kStagesQ, ph = (u / Smem::kStagesQ) & 1u;
         const uint32_t ds = u % Smem::kStagesDO, dph = (u / Smem::kStagesDO) & 1u;
-        const size_t row0 = (size_t)bh * p.S_pad + 64 * qb;
+        const size_t row0 = (size_t)bh * p.S_pad + (I.seq.stat + 64 * qb);
         // (checked builds: a query block of the sequence, of a query head of
         // the batch, whose per-row statistics lie inside the workspace)
-        const bool in_range = attn_check(qb >= 0 && 64 * qb < p.S && bh >= 0 && bh < p.B * p.Hq &&
+        const bool in_range = attn_check(qb >= 0 && 64 * qb < I.seq.S && bh >= 0 && bh < p.B * p.Hq &&
                                              row0 + 64 <= (size_t)p.B * p.Hq * p.S_pad,
                                          p.error_word);
         // the per-row statistics ride with Q (dK pass) or dO (dV pass)
@@ -179,8 +180,8 @@ __device__ __forceinline__ void bwd256_kv_producer(Bwd256KvSmem<DK>& sm, const B
         mbar_arrive_expect_tx(&sm.q_full[st],
                               in_range ? Cfg::kSmallTile + (DK ? kStatBytes : 0u) : 0u);
         for (int hf = 0; in_range && hf < 4; ++hf)
-          tma_load_3d_hint(sm.q[st] + hf * Cfg::kSmallBox, map_q, &sm.q_full[st], 64 * hf,
-                           64 * qb, bh, keep);
+          bwd_load<PK>(sm.q[st] + hf * Cfg::kSmallBox, map_q, &sm.q_full[st], 64 * hf,
+                           64 * qb, bh, p, I.seq, kPackedQ, keep);
         if (DK && in_range) {
           bulk_load(sm.lse2[st], p.lse2 + row0, 256, &sm.q_full[st], keep);
           bulk_load(sm.dlt[st], p.delta + row0, 256, &sm.q_full[st], keep);
@@ -191,8 +192,8 @@ __device__ __forceinline__ void bwd256_kv_producer(Bwd256KvSmem<DK>& sm, const B
         mbar_arrive_expect_tx(&sm.do_full[ds],
                               in_range ? Cfg::kSmallTile + (DK ? 0u : kStatBytes) : 0u);
         for (int hf = 0; in_range && hf < 4; ++hf)
-          tma_load_3d_hint(sm.dO[ds] + hf * Cfg::kSmallBox, map_do, &sm.do_full[ds], 64 * hf,
-                           64 * qb, bh, keep);
+          bwd_load<PK>(sm.dO[ds] + hf * Cfg::kSmallBox, map_do, &sm.do_full[ds], 64 * hf,
+                           64 * qb, bh, p, I.seq, kPackedDO, keep);
         if (!DK && in_range) {
           bulk_load(sm.lse2[ds], p.lse2 + row0, 256, &sm.do_full[ds], keep);
           bulk_load(sm.dlt[ds], p.delta + row0, 256, &sm.do_full[ds], keep);
@@ -218,7 +219,7 @@ __device__ __forceinline__ void bwd256_kv_producer(Bwd256KvSmem<DK>& sm, const B
 // overwritten two steps later, after the accumulation MMA that read it
 // (issued before, in order) and after the element-wise warps are done with
 // it (the accumulation waited for them).
-template <bool DK>
+template <bool DK, bool PK>
 __device__ __forceinline__ void bwd256_kv_issuer(Bwd256KvSmem<DK>& sm, const BwdParams& p,
                                                  volatile int* abort) {
   using Cfg = Bwd256Cfg;
@@ -286,10 +287,11 @@ __device__ __forceinline__ void bwd256_kv_issuer(Bwd256KvSmem<DK>& sm, const Bwd
   uint32_t u = 0;
   int items = 0;
   bool ok = true;
+  const int num_items = bwd_num_items<PK>(p, p.Hkv);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
-    if (w >= p.num_items) break;
-    const BwdKvItem I = bwd256_kv_item_of(p, w);
+    if (w >= num_items) break;
+    const BwdKvItem I = bwd256_kv_item_of<PK>(p, w);
     const int N = p.group * (I.hi - I.lo + 1);
     if (!(ok = wait_all(&sm.kv_full, (uint32_t)items & 1u))) break;
     tc_fence_after_sync();
@@ -345,7 +347,7 @@ __device__ __forceinline__ void bwd256_kv_issuer(Bwd256KvSmem<DK>& sm, const Bwd
 // writes it as bf16 pairs over S^T, the dK pass keeps it in fp32 and writes
 // dS^T = P^T o (dP^T - D[query]) as bf16 pairs over dP^T.  Per item: dV, or
 // scale * dK, out (the two warpgroups take alternate 32-column chunks).
-template <bool DK>
+template <bool DK, bool PK>
 __device__ __forceinline__ void bwd256_kv_softmax(Bwd256KvSmem<DK>& sm, const BwdParams& p,
                                                   uint32_t tbase, volatile int* abort, int warp,
                                                   int lane) {
@@ -358,10 +360,11 @@ __device__ __forceinline__ void bwd256_kv_softmax(Bwd256KvSmem<DK>& sm, const Bw
   uint32_t u = 0;
   int items = 0;
   bool ok = true;
+  const int num_items = bwd_num_items<PK>(p, p.Hkv);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
-    if (w >= p.num_items) break;
-    const BwdKvItem I = bwd256_kv_item_of(p, w);
+    if (w >= num_items) break;
+    const BwdKvItem I = bwd256_kv_item_of<PK>(p, w);
     const int j = 128 * I.kb + t;   // this thread's key
     for (int hh = 0; ok && hh < p.group; ++hh) {
       for (int qb = I.lo; qb <= I.hi; ++qb, ++u) {
@@ -377,7 +380,7 @@ __device__ __forceinline__ void bwd256_kv_softmax(Bwd256KvSmem<DK>& sm, const Bw
         int clo = 0, chi = Cfg::kCols - 1;
         if (p.causal) clo = j - i0;                                     // i >= j
         if (p.window > 0) chi = min(chi, j - i0 + p.window - 1);        // i - j < W
-        chi = min(chi, p.S - 1 - i0);                                   // i < S
+        chi = min(chi, I.seq.S - 1 - i0);                                   // i < S
         const uint32_t span = chi >= clo ? (uint32_t)(chi - clo) : 0u;
         if (chi < clo) clo = 1 << 30;
         const bool msk = clo > 0 || chi < Cfg::kCols - 1;
@@ -446,8 +449,10 @@ __device__ __forceinline__ void bwd256_kv_softmax(Bwd256KvSmem<DK>& sm, const Bw
     if (!(ok = mbar_wait(&sm.acc_final, (uint32_t)items & 1u, abort))) break;
     ++items;
     tc_fence_after_sync();
-    const bool store = j < p.S;
-    __nv_bfloat16* dst = (DK ? p.dk : p.dv) + ((size_t)I.bkv * p.S + j) * Cfg::DH;
+    const bool store = bwd_real<PK>(I.seq, j);
+    __nv_bfloat16* dst = (DK ? p.dk : p.dv) + bwd_row<PK>(I.seq, I.bkv, j, Cfg::DH,
+                                                          DK ? p.dk_row : p.dv_row,
+                                                          DK ? p.dk_head : p.dv_head);
     const float mul = DK ? p.scale : 1.0f;
 #pragma unroll 1
     for (int c = wg; c < Cfg::DH / 32; c += Cfg::kWG) {
@@ -462,7 +467,7 @@ __device__ __forceinline__ void bwd256_kv_softmax(Bwd256KvSmem<DK>& sm, const Bw
   }
 }
 
-template <bool DK>
+template <bool DK, bool PK = false>
 __global__ void __launch_bounds__(Bwd256Cfg::kThreads, 1)
     attn_bwd256_kv(const __grid_constant__ CUtensorMap map_q,
                    const __grid_constant__ CUtensorMap map_k,
@@ -524,11 +529,11 @@ __global__ void __launch_bounds__(Bwd256Cfg::kThreads, 1)
   if (tbase != 0 && threadIdx.x == 0) sm.abort_flag = 1;
   if (tbase == 0) {
     if (warp == Cfg::kWarpProducer) {
-      if (lane == 0) bwd256_kv_producer<DK>(sm, p, &map_q, &map_k, &map_v, &map_do, abort);
+      if (lane == 0) bwd256_kv_producer<DK, PK>(sm, p, &map_q, &map_k, &map_v, &map_do, abort);
     } else if (warp == Cfg::kWarpIssuer) {
-      bwd256_kv_issuer<DK>(sm, p, abort);
+      bwd256_kv_issuer<DK, PK>(sm, p, abort);
     } else {
-      bwd256_kv_softmax<DK>(sm, p, tbase, abort, warp, lane);
+      bwd256_kv_softmax<DK, PK>(sm, p, tbase, abort, warp, lane);
     }
   }
   __syncwarp();
@@ -565,18 +570,14 @@ struct __align__(1024) Bwd256QSmem {
 
 // Item w: 128-row query block qb (latest, i.e. heaviest under a causal
 // mask, first) of query head bh.
+template <bool PK>
 __device__ __forceinline__ BwdQItem bwd256_q_item_of(const BwdParams& p, int w) {
-  BwdQItem r;
-  const int per = p.B * p.Hq;
-  const int blk = w / per;
-  r.qb = p.nblk - 1 - blk;
-  r.bh = w - blk * per;
-  const int b = r.bh / p.Hq;
-  r.bkv = b * p.Hkv + (r.bh - b * p.Hq) / p.group;   // g(h) = floor(h / (H/G))
-  bwd256_kblocks_of(p, r.qb, r.lo, r.hi);
+  BwdQItem r = bwd_q_place_of<PK>(p, w);
+  bwd256_kblocks_of(p, r.seq, r.qb, r.lo, r.hi);
   return r;
 }
 
+template <bool PK>
 __device__ __forceinline__ void bwd256_dq_producer(Bwd256QSmem& sm, const BwdParams& p,
                                                    const CUtensorMap* map_q,
                                                    const CUtensorMap* map_k,
@@ -589,24 +590,27 @@ __device__ __forceinline__ void bwd256_dq_producer(Bwd256QSmem& sm, const BwdPar
   uint32_t u = 0, k_loaded = 0, k_par = 0, v_loaded = 0, v_par = 0;
   int items = 0;
   bool ok = true;
+  const int num_items = bwd_num_items<PK>(p, p.Hq);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
-    if (w >= p.num_items) break;
-    const BwdQItem I = bwd256_q_item_of(p, w);
+    if (w >= num_items) break;
+    const BwdQItem I = bwd256_q_item_of<PK>(p, w);
     if (items > 0 && !(ok = mbar_wait(&sm.q_empty, (uint32_t)(items - 1) & 1u, abort))) break;
     // (checked builds: a query block of the sequence, of a query head of the batch)
-    const bool q_in_range = attn_check(I.qb >= 0 && 128 * I.qb < p.S && I.bh >= 0 &&
-                                           I.bh < p.B * p.Hq,
+    const bool q_in_range = attn_check(I.qb >= 0 && 128 * I.qb < I.seq.S && I.bh >= 0 &&
+                                           I.bh < p.B * p.Hq && bwd_inside<PK>(p, I.seq),
                                        p.error_word);
     mbar_arrive_expect_tx(&sm.q_full, q_in_range ? 2u * Cfg::kBigTile : 0u);
     for (int hf = 0; q_in_range && hf < 4; ++hf) {
-      tma_load_3d(sm.q + hf * Cfg::kBigBox, map_q, &sm.q_full, 64 * hf, 128 * I.qb, I.bh);
-      tma_load_3d(sm.dO + hf * Cfg::kBigBox, map_do, &sm.q_full, 64 * hf, 128 * I.qb, I.bh);
+      bwd_load_once<PK>(sm.q + hf * Cfg::kBigBox, map_q, &sm.q_full, 64 * hf, 128 * I.qb,
+                             I.bh, p, I.seq, kPackedQ);
+      bwd_load_once<PK>(sm.dO + hf * Cfg::kBigBox, map_do, &sm.q_full, 64 * hf, 128 * I.qb,
+                             I.bh, p, I.seq, kPackedDO);
     }
     ++items;
     for (int kb = I.lo; kb <= I.hi; ++kb, ++u) {
       // (checked builds: a key block of the sequence, of a K/V head of the batch)
-      const bool in_range = attn_check(kb >= 0 && 64 * kb < p.S && I.bkv >= 0 &&
+      const bool in_range = attn_check(kb >= 0 && 64 * kb < I.seq.S && I.bkv >= 0 &&
                                            I.bkv < p.B * p.Hkv,
                                        p.error_word);
       const uint32_t bytes = in_range ? (uint32_t)Cfg::kSmallTile : 0u;
@@ -614,16 +618,16 @@ __device__ __forceinline__ void bwd256_dq_producer(Bwd256QSmem& sm, const BwdPar
       if (!(ok = mbar_wait(&sm.k_empty[ks], kph ^ 1u, abort))) break;
       mbar_arrive_expect_tx(&sm.k_full[ks], bytes);
       for (int hf = 0; in_range && hf < 4; ++hf)
-        tma_load_3d_hint(sm.k[ks] + hf * Cfg::kSmallBox, map_k, &sm.k_full[ks], 64 * hf, 64 * kb,
-                         I.bkv, keep);
+        bwd_load<PK>(sm.k[ks] + hf * Cfg::kSmallBox, map_k, &sm.k_full[ks], 64 * hf, 64 * kb,
+                         I.bkv, p, I.seq, kPackedK, keep);
       k_loaded |= 1u << ks;
       k_par = (k_par & ~(1u << ks)) | (kph << ks);
       const uint32_t vs = u % Smem::kStagesV, vph = (u / Smem::kStagesV) & 1u;
       if (!(ok = mbar_wait(&sm.v_empty[vs], vph ^ 1u, abort))) break;
       mbar_arrive_expect_tx(&sm.v_full[vs], bytes);
       for (int hf = 0; in_range && hf < 4; ++hf)
-        tma_load_3d_hint(sm.v[vs] + hf * Cfg::kSmallBox, map_v, &sm.v_full[vs], 64 * hf, 64 * kb,
-                         I.bkv, keep);
+        bwd_load<PK>(sm.v[vs] + hf * Cfg::kSmallBox, map_v, &sm.v_full[vs], 64 * hf, 64 * kb,
+                         I.bkv, p, I.seq, kPackedV, keep);
       v_loaded |= 1u << vs;
       v_par = (v_par & ~(1u << vs)) | (vph << vs);
     }
@@ -639,6 +643,7 @@ __device__ __forceinline__ void bwd256_dq_producer(Bwd256QSmem& sm, const BwdPar
 // S(n+1) once the element-wise warps have read S(n), dP(n+1) into the other
 // dP buffer, then dQ(n) once dS(n) is written over dP(n) (as in the Dh <= 128
 // dQ pass).  A key block is released after dQ, a value block after its dP.
+template <bool PK>
 __device__ __forceinline__ void bwd256_dq_issuer(Bwd256QSmem& sm, const BwdParams& p,
                                                  volatile int* abort) {
   using Cfg = Bwd256Cfg;
@@ -693,10 +698,11 @@ __device__ __forceinline__ void bwd256_dq_issuer(Bwd256QSmem& sm, const BwdParam
   uint32_t u = 0;
   int items = 0;
   bool ok = true;
+  const int num_items = bwd_num_items<PK>(p, p.Hq);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
-    if (w >= p.num_items) break;
-    const BwdQItem I = bwd256_q_item_of(p, w);
+    if (w >= num_items) break;
+    const BwdQItem I = bwd256_q_item_of<PK>(p, w);
     const int N = I.hi - I.lo + 1;
     if (!(ok = wait_all(&sm.q_full, (uint32_t)items & 1u))) break;
     // Q's first half into tensor memory, once the previous item's S MMAs
@@ -749,6 +755,7 @@ __device__ __forceinline__ void bwd256_dq_issuer(Bwd256QSmem& sm, const BwdParam
 // query row 128 qb + t and key columns 32 wg .. 32 wg + 31 of each 64-key
 // block): P = exp2(S * scale*log2e - lse2_i) (0 where masked), kept in fp32;
 // dS = P o (dP - D_i) as bf16 pairs over dP.  Per item: scale * dQ out.
+template <bool PK>
 __device__ __forceinline__ void bwd256_dq_softmax(Bwd256QSmem& sm, const BwdParams& p,
                                                   uint32_t tbase, volatile int* abort, int warp,
                                                   int lane) {
@@ -761,22 +768,24 @@ __device__ __forceinline__ void bwd256_dq_softmax(Bwd256QSmem& sm, const BwdPara
   uint32_t u = 0;
   int items = 0;
   bool ok = true;
+  const int num_items = bwd_num_items<PK>(p, p.Hq);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
-    if (w >= p.num_items) break;
-    const BwdQItem I = bwd256_q_item_of(p, w);
+    if (w >= num_items) break;
+    const BwdQItem I = bwd256_q_item_of<PK>(p, w);
     const int i = 128 * I.qb + t;   // this thread's query
-    const float L = p.lse2[(size_t)I.bh * p.S_pad + i];
-    const float Di = p.delta[(size_t)I.bh * p.S_pad + i];
+    const float L = p.lse2[(size_t)I.bh * p.S_pad + (I.seq.stat + i)];
+    const float Di = p.delta[(size_t)I.bh * p.S_pad + (I.seq.stat + i)];
     const float2 negL = make_float2(-L, -L), negD = make_float2(-Di, -Di);
     for (int kb = I.lo; kb <= I.hi; ++kb, ++u) {
       if (!(ok = mbar_wait(&sm.s_full, u & 1u, abort))) break;
       tc_fence_after_sync();
       // visible keys of query i: [klo, khi], as columns [clo, chi] of this warpgroup's
       const int j0 = 64 * kb + Cfg::kCols * wg;
-      int khi = p.S - 1;
+      int khi = I.seq.S - 1;
       if (p.causal) khi = min(khi, i);
-      const int klo = p.window > 0 ? i - p.window + 1 : 0;
+      int klo = p.window > 0 ? i - p.window + 1 : 0;
+      if (PK) klo = max(klo, I.seq.pad);
       int clo = klo - j0;
       const int chi = khi - j0;
       const uint32_t span = chi >= clo ? (uint32_t)(chi - clo) : 0u;
@@ -829,8 +838,8 @@ __device__ __forceinline__ void bwd256_dq_softmax(Bwd256QSmem& sm, const BwdPara
     if (!(ok = mbar_wait(&sm.acc_final, (uint32_t)items & 1u, abort))) break;
     ++items;
     tc_fence_after_sync();
-    const bool store = i < p.S;
-    const size_t row = ((size_t)I.bh * p.S + i) * Cfg::DH;
+    const bool store = bwd_real<PK>(I.seq, i);
+    const size_t row = bwd_row<PK>(I.seq, I.bh, i, Cfg::DH, p.dq_row, p.dq_head);
 #pragma unroll 1
     for (int c = wg; c < Cfg::DH / 32; c += Cfg::kWG) {
       uint32_t r[32];
@@ -841,6 +850,7 @@ __device__ __forceinline__ void bwd256_dq_softmax(Bwd256QSmem& sm, const BwdPara
   }
 }
 
+template <bool PK = false>
 __global__ void __launch_bounds__(Bwd256Cfg::kThreads, 1)
     attn_bwd256_dq(const __grid_constant__ CUtensorMap map_q,
                    const __grid_constant__ CUtensorMap map_k,
@@ -899,11 +909,11 @@ __global__ void __launch_bounds__(Bwd256Cfg::kThreads, 1)
   if (tbase != 0 && threadIdx.x == 0) sm.abort_flag = 1;
   if (tbase == 0) {
     if (warp == Cfg::kWarpProducer) {
-      if (lane == 0) bwd256_dq_producer(sm, p, &map_q, &map_k, &map_v, &map_do, abort);
+      if (lane == 0) bwd256_dq_producer<PK>(sm, p, &map_q, &map_k, &map_v, &map_do, abort);
     } else if (warp == Cfg::kWarpIssuer) {
-      bwd256_dq_issuer(sm, p, abort);
+      bwd256_dq_issuer<PK>(sm, p, abort);
     } else {
-      bwd256_dq_softmax(sm, p, tbase, abort, warp, lane);
+      bwd256_dq_softmax<PK>(sm, p, tbase, abort, warp, lane);
     }
   }
   __syncwarp();

@@ -81,7 +81,7 @@ static cudaError_t launch_bwd256(const void* q, const void* k, const void* v, co
     r = cudaFuncSetAttribute(attn_bwd256_kv<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)smem_dk);
     if (r != cudaSuccess) return r;
-    return cudaFuncSetAttribute(attn_bwd256_dq, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(attn_bwd256_dq<>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)smem_dq);
   });
   if (e != cudaSuccess) return e;
@@ -104,7 +104,7 @@ static cudaError_t launch_bwd256(const void* q, const void* k, const void* v, co
   BwdParams pq = prm;
   pq.num_items = prm.nblk * prm.B * prm.Hq;
   const int grid_q = pq.num_items < dev.num_sms ? pq.num_items : dev.num_sms;
-  return launch_pdl(attn_bwd256_dq, dim3(grid_q), dim3(Cfg::kThreads), smem_dq, stream, mq128,
+  return launch_pdl(attn_bwd256_dq<>, dim3(grid_q), dim3(Cfg::kThreads), smem_dq, stream, mq128,
                     mk64, mv64, mdo128, pq);
 }
 

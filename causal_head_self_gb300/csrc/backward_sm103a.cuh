@@ -37,12 +37,19 @@
 // exponentials and the shares run side by side (kWG = 2: two halves); the
 // next warp's lane 0 issues every TMA copy, the last warp every MMA (one
 // elected lane).  Every wait is bounded.
+//
+// PK = true is the same over packed sequences (packed_sm103a.cuh): an item's
+// rows, keys and place come from the lists of tiles (one heaviest first for
+// each pass) instead of the launch's shape; rows are counted with the
+// sequence's padding in front, for lse2 and D too.  Padded queries have
+// lse2 = +inf and so weigh nothing; padded keys are masked.
 #pragma once
 
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include "packed_sm103a.cuh"
 #include "sm103a_ptx.cuh"
 
 namespace chs {
@@ -63,7 +70,75 @@ struct BwdParams {
   __nv_bfloat16* dv;      // [B, Hkv, S, DH]
   int* error_word;
   int fault;              // test hook: 4 = the dK/dV pass never loads its first K/V block
+  // PK: the pass's tiles of 128 rows; S, nblk and num_items are then each
+  // item's own; strides in elements between rows and heads of dq, dk and dv
+  PackedRef pk;
+  long long dq_row, dq_head, dk_row, dk_head, dv_row, dv_head;
 };
+
+// The rows that an item belongs to: a (batch, head)'s, or a packed sequence's.
+struct BwdSeq {
+  int S;       // rows (PK: with the padding)
+  int nblk;    // ceil(S / 128)
+  int start;   // PK: first row
+  int pad;     // PK: rows of padding ahead of it
+  int stat;    // PK: first row of its lse2 and D
+};
+
+template <bool PK>
+__device__ __forceinline__ int bwd_num_items(const BwdParams& p, int heads) {
+  return PK ? packed_num_tiles(p.pk) * heads : p.num_items;
+}
+
+template <bool PK>
+__device__ __forceinline__ BwdSeq bwd_seq_of(const BwdParams& p, const PackedTile& e) {
+  if constexpr (PK)
+    return BwdSeq{e.len + e.pad(), (e.len + 127) / 128, e.start, e.pad(), e.stat};
+  return BwdSeq{p.S, p.nblk, 0, 0, 0};
+}
+
+// Rows [row, row + R), columns c .. c + 63 of a head: of `bh` in a batch, of
+// head bh of the packed sequence.
+template <bool PK>
+__device__ __forceinline__ void bwd_load(void* dst, const CUtensorMap* map, uint64_t* bar, int c,
+                                         int row, int bh, const BwdParams& p, const BwdSeq& q,
+                                         int tensor, uint64_t policy) {
+  if constexpr (PK)
+    packed_load(dst, map, bar, c, q.start, q.pad, row, bh, p.pk.heads_inner & tensor, policy);
+  else
+    tma_load_3d_hint(dst, map, bar, c, row, bh, policy);
+}
+// (the resident blocks, loaded once per item)
+template <bool PK>
+__device__ __forceinline__ void bwd_load_once(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                              int c, int row, int bh, const BwdParams& p,
+                                              const BwdSeq& q, int tensor) {
+  if constexpr (PK)
+    packed_load(dst, map, bar, c, q.start, q.pad, row, bh, p.pk.heads_inner & tensor,
+                policy_evict_first());
+  else
+    tma_load_3d(dst, map, bar, c, row, bh);
+}
+
+// (checked builds: a packed sequence lies inside the packed tensors)
+template <bool PK>
+__device__ __forceinline__ bool bwd_inside(const BwdParams& p, const BwdSeq& q) {
+  return !PK || (q.start >= 0 && q.start <= p.pk.T - (q.S - q.pad));
+}
+
+// Is row i one whose gradient is stored?
+template <bool PK>
+__device__ __forceinline__ bool bwd_real(const BwdSeq& q, int i) {
+  return PK ? i >= q.pad : i < q.S;
+}
+
+// Where row i of a gradient lies.
+template <bool PK>
+__device__ __forceinline__ size_t bwd_row(const BwdSeq& q, int bh, int i, int DH, long long row,
+                                          long long head) {
+  if constexpr (PK) return (size_t)((q.start + (long long)(i - q.pad)) * row + bh * head);
+  return ((size_t)bh * q.S + i) * DH;
+}
 
 template <int DH>
 struct BwdCfg {
@@ -153,6 +228,65 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// The same over packed sequences: one block per listed tile of 128 rows and
+// query head, o and dO at their strides, lse [Hq, T].
+template <int DH>
+__global__ void __launch_bounds__(256)
+    attn_bwd_prep_packed(const __nv_bfloat16* __restrict__ o,
+                         const __nv_bfloat16* __restrict__ dout, const float* __restrict__ lse,
+                         float* __restrict__ lse2, float* __restrict__ delta, const PackedRef pk,
+                         int Hq, long long S_pad, long long o_row, long long o_head,
+                         long long do_row, long long do_head) {
+  constexpr int kLanes = DH / 8;
+  constexpr int kRowsPerSet = 256 / kLanes;
+  constexpr int kSets = 128 / kRowsPerSet;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tile = blockIdx.x / Hq, h = blockIdx.x - tile * Hq;
+  if (tile >= packed_num_tiles(pk)) return;
+  const PackedTile e = packed_tile(pk, tile);
+  const int sub = threadIdx.x % kLanes, r0 = threadIdx.x / kLanes;
+  const __nv_bfloat16* po = o + h * o_head + 8 * sub;
+  const __nv_bfloat16* pd = dout + h * do_head + 8 * sub;
+  const size_t to = (size_t)h * S_pad + (e.stat + 128 * e.blk);
+  constexpr int kBatch = kSets < kPrepRowSets ? kSets : kPrepRowSets;
+#pragma unroll 1
+  for (int s = 0; s < kSets; s += kBatch) {
+    uint4 a[kBatch], b[kBatch];
+    bool valid[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = 128 * e.blk + (s + k) * kRowsPerSet + r0 - e.pad();
+      valid[k] = i >= 0;
+      a[k] = b[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (valid[k]) {
+        a[k] = *reinterpret_cast<const uint4*>(po + (e.start + (long long)i) * o_row);
+        b[k] = *reinterpret_cast<const uint4*>(pd + (e.start + (long long)i) * do_row);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const uint32_t wa[4] = {a[k].x, a[k].y, a[k].z, a[k].w};
+      const uint32_t wb[4] = {b[k].x, b[k].y, b[k].z, b[k].w};
+      float acc = 0.f;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        acc = fmaf(__uint_as_float(wa[x] << 16), __uint_as_float(wb[x] << 16), acc);
+        acc = fmaf(__uint_as_float(wa[x] & 0xffff0000u), __uint_as_float(wb[x] & 0xffff0000u), acc);
+      }
+#pragma unroll
+      for (int m = kLanes / 2; m > 0; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
+      const int r = (s + k) * kRowsPerSet + r0;
+      if (sub == 0) {
+        delta[to + r] = valid[k] ? acc : 0.f;
+        lse2[to + r] = valid[k] ? lse[(size_t)h * pk.T + e.start + 128 * e.blk + r - e.pad()] *
+                                      1.4426950408889634f
+                                : __int_as_float(0x7f800000);
+      }
+    }
+  }
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
@@ -178,22 +312,24 @@ __device__ __forceinline__ int bwd_item(int k, int c, int G) {
 }
 
 // Query blocks [lo, hi] that see some key of key block kb (128-row blocks).
-__device__ __forceinline__ void bwd_qblocks_of(const BwdParams& p, int kb, int& lo, int& hi) {
+__device__ __forceinline__ void bwd_qblocks_of(const BwdParams& p, const BwdSeq& q, int kb,
+                                               int& lo, int& hi) {
   if (!p.causal) {
     lo = 0;
-    hi = p.nblk - 1;
+    hi = q.nblk - 1;
     return;
   }
   lo = kb;   // query i sees key j only if j <= i
-  hi = p.nblk - 1;
+  hi = q.nblk - 1;
   if (p.window > 0) hi = min(hi, (128 * kb + 127 + p.window - 1) / 128);   // i - j < W
 }
 
 // Key blocks [lo, hi] that query block qb sees.
-__device__ __forceinline__ void bwd_kblocks_of(const BwdParams& p, int qb, int& lo, int& hi) {
+__device__ __forceinline__ void bwd_kblocks_of(const BwdParams& p, const BwdSeq& q, int qb,
+                                               int& lo, int& hi) {
   if (!p.causal) {
     lo = 0;
-    hi = p.nblk - 1;
+    hi = q.nblk - 1;
     return;
   }
   hi = qb;
@@ -202,8 +338,8 @@ __device__ __forceinline__ void bwd_kblocks_of(const BwdParams& p, int qb, int& 
 
 // Does some (query, key) pair of query block qb x key block kb fall outside
 // the mask (or past S)?
-__device__ __forceinline__ bool bwd_needs_mask(const BwdParams& p, int qb, int kb) {
-  if (128 * kb + 127 >= p.S || 128 * qb + 127 >= p.S) return true;
+__device__ __forceinline__ bool bwd_needs_mask(const BwdParams& p, const BwdSeq& q, int qb, int kb) {
+  if (128 * kb + 127 >= q.S || 128 * qb + 127 >= q.S || 128 * kb < q.pad) return true;
   if (!p.causal) return false;
   if (128 * kb + 127 > 128 * qb) return true;                                  // j > i somewhere
   if (p.window > 0 && 128 * qb + 127 - 128 * kb >= p.window) return true;      // i - j >= W somewhere
@@ -231,21 +367,40 @@ struct __align__(1024) BwdKvSmem {
 // Item w of the dK/dV pass: key block kb (heaviest, i.e. earliest, first
 // under a causal mask) of K/V head bkv = b * Hkv + g.
 struct BwdKvItem {
-  int kb, bkv, b, g, lo, hi;
+  int kb, bkv, b, g, lo, hi;   // PK: b = 0, bkv = g
+  BwdSeq seq;
 };
 
-__device__ __forceinline__ BwdKvItem bwd_kv_item_of(const BwdParams& p, int w) {
+// (without lo and hi)
+template <bool PK>
+__device__ __forceinline__ BwdKvItem bwd_kv_place_of(const BwdParams& p, int w) {
   BwdKvItem r;
+  if constexpr (PK) {
+    const int i = w / p.Hkv;
+    const PackedTile e = packed_tile(p.pk, i);
+    r.kb = e.blk;
+    r.b = 0;
+    r.g = r.bkv = w - i * p.Hkv;
+    r.seq = bwd_seq_of<PK>(p, e);
+    return r;
+  }
   const int per = p.B * p.Hkv;
   r.kb = w / per;
   r.bkv = w - r.kb * per;
   r.b = r.bkv / p.Hkv;
   r.g = r.bkv - r.b * p.Hkv;
-  bwd_qblocks_of(p, r.kb, r.lo, r.hi);
+  r.seq = bwd_seq_of<PK>(p, PackedTile{});
   return r;
 }
 
-template <int DH>
+template <bool PK>
+__device__ __forceinline__ BwdKvItem bwd_kv_item_of(const BwdParams& p, int w) {
+  BwdKvItem r = bwd_kv_place_of<PK>(p, w);
+  bwd_qblocks_of(p, r.seq, r.kb, r.lo, r.hi);
+  return r;
+}
+
+template <int DH, bool PK>
 __device__ __forceinline__ void bwd_dkdv_producer(BwdKvSmem<DH>& sm, const BwdParams& p,
                                                   const CUtensorMap* map_q,
                                                   const CUtensorMap* map_k,
@@ -257,20 +412,23 @@ __device__ __forceinline__ void bwd_dkdv_producer(BwdKvSmem<DH>& sm, const BwdPa
   uint32_t u = 0, loaded = 0, par = 0;
   int items = 0;
   bool ok = true;
+  const int num_items = bwd_num_items<PK>(p, p.Hkv);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
-    if (w >= p.num_items) break;
-    const BwdKvItem I = bwd_kv_item_of(p, w);
+    if (w >= num_items) break;
+    const BwdKvItem I = bwd_kv_item_of<PK>(p, w);
     if (items > 0 && !(ok = mbar_wait(&sm.kv_empty, (uint32_t)(items - 1) & 1u, abort))) break;
     // (checked builds: a key block of the sequence, of a K/V head of the batch)
-    const bool kv_in_range = attn_check(I.kb >= 0 && 128 * I.kb < p.S && I.bkv >= 0 &&
-                                            I.bkv < p.B * p.Hkv,
+    const bool kv_in_range = attn_check(I.kb >= 0 && 128 * I.kb < I.seq.S && I.bkv >= 0 &&
+                                            I.bkv < p.B * p.Hkv && bwd_inside<PK>(p, I.seq),
                                         p.error_word);
     mbar_arrive_expect_tx(&sm.kv_full, kv_in_range ? 2u * Cfg::kTile : 0u);
     if (kv_in_range && (p.fault != 4 || it != 0)) {   // (the test hook withholds one K/V block)
       for (int hf = 0; hf < kBoxes; ++hf) {
-        tma_load_3d(sm.k + hf * Cfg::kBox, map_k, &sm.kv_full, 64 * hf, 128 * I.kb, I.bkv);
-        tma_load_3d(sm.v + hf * Cfg::kBox, map_v, &sm.kv_full, 64 * hf, 128 * I.kb, I.bkv);
+        bwd_load_once<PK>(sm.k + hf * Cfg::kBox, map_k, &sm.kv_full, 64 * hf, 128 * I.kb,
+                               I.bkv, p, I.seq, kPackedK);
+        bwd_load_once<PK>(sm.v + hf * Cfg::kBox, map_v, &sm.kv_full, 64 * hf, 128 * I.kb,
+                               I.bkv, p, I.seq, kPackedV);
       }
     }
     ++items;
@@ -280,18 +438,18 @@ __device__ __forceinline__ void bwd_dkdv_producer(BwdKvSmem<DH>& sm, const BwdPa
         const int st = (int)(u & 1u);
         const uint32_t ph = (u >> 1) & 1u;
         if (!(ok = mbar_wait(&sm.q_empty[st], ph ^ 1u, abort))) break;
-        const size_t row0 = (size_t)bh * p.S_pad + 128 * qb;
+        const size_t row0 = (size_t)bh * p.S_pad + (I.seq.stat + 128 * qb);
         // (checked builds: a query block of the sequence, of a query head of
         // the batch, whose per-row statistics lie inside the workspace)
-        const bool in_range = attn_check(qb >= 0 && 128 * qb < p.S && bh >= 0 && bh < p.B * p.Hq &&
+        const bool in_range = attn_check(qb >= 0 && 128 * qb < I.seq.S && bh >= 0 && bh < p.B * p.Hq &&
                                              row0 + 128 <= (size_t)p.B * p.Hq * p.S_pad,
                                          p.error_word);
         mbar_arrive_expect_tx(&sm.q_full[st], in_range ? 2u * Cfg::kTile + 2u * 512u : 0u);
         for (int hf = 0; in_range && hf < kBoxes; ++hf) {
-          tma_load_3d_hint(sm.q[st] + hf * Cfg::kBox, map_q, &sm.q_full[st], 64 * hf, 128 * qb, bh,
-                           keep);
-          tma_load_3d_hint(sm.dO[st] + hf * Cfg::kBox, map_do, &sm.q_full[st], 64 * hf, 128 * qb,
-                           bh, keep);
+          bwd_load<PK>(sm.q[st] + hf * Cfg::kBox, map_q, &sm.q_full[st], 64 * hf, 128 * qb,
+                            bh, p, I.seq, kPackedQ, keep);
+          bwd_load<PK>(sm.dO[st] + hf * Cfg::kBox, map_do, &sm.q_full[st], 64 * hf, 128 * qb,
+                            bh, p, I.seq, kPackedDO, keep);
         }
         if (in_range) {
           bulk_load(sm.lse2[st], p.lse2 + row0, 512, &sm.q_full[st], keep);
@@ -313,7 +471,7 @@ __device__ __forceinline__ void bwd_dkdv_producer(BwdKvSmem<DH>& sm, const BwdPa
 // S(n+1) (its columns held P(n), which dV(n), issued before it, reads),
 // dK(n) once dS(n) is written, dP(n+1) (its columns held dS(n)).  The
 // element-wise work of step n+1 therefore overlaps dK(n) and dP(n+1).
-template <int DH>
+template <int DH, bool PK>
 __device__ __forceinline__ void bwd_dkdv_issuer(BwdKvSmem<DH>& sm, const BwdParams& p,
                                                 volatile int* abort) {
   using Cfg = BwdCfg<DH>;
@@ -350,10 +508,11 @@ __device__ __forceinline__ void bwd_dkdv_issuer(BwdKvSmem<DH>& sm, const BwdPara
   uint32_t u = 0;
   int items = 0;
   bool ok = true;
+  const int num_items = bwd_num_items<PK>(p, p.Hkv);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
-    if (w >= p.num_items) break;
-    const BwdKvItem I = bwd_kv_item_of(p, w);
+    if (w >= num_items) break;
+    const BwdKvItem I = bwd_kv_item_of<PK>(p, w);
     const int N = p.group * (I.hi - I.lo + 1);
     if (!(ok = wait_all(&sm.kv_full, (uint32_t)items & 1u))) break;
     ++items;
@@ -411,7 +570,7 @@ __device__ __forceinline__ void bwd_store32(__nv_bfloat16* dst, const uint32_t (
 // (0 where masked), written as bf16 pairs (see bwd_packed_col) and kept in
 // fp32 registers; then dS^T = P^T o (dP^T - D[query]), as bf16 pairs over dP^T.
 // Per item: the first half of the warpgroups write dV, the second scale * dK.
-template <int DH>
+template <int DH, bool PK>
 __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdParams& p,
                                                  uint32_t tbase, volatile int* abort, int warp,
                                                  int lane) {
@@ -425,10 +584,11 @@ __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdPar
   uint32_t u = 0;
   int items = 0;
   bool ok = true;
+  const int num_items = bwd_num_items<PK>(p, p.Hkv);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
-    if (w >= p.num_items) break;
-    const BwdKvItem I = bwd_kv_item_of(p, w);
+    if (w >= num_items) break;
+    const BwdKvItem I = bwd_kv_item_of<PK>(p, w);
     const int j = 128 * I.kb + t;   // this thread's key
     for (int hh = 0; ok && hh < p.group; ++hh) {
       for (int qb = I.lo; qb <= I.hi; ++qb, ++u) {
@@ -441,12 +601,12 @@ __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdPar
         const float4* D4 = reinterpret_cast<const float4*>(sm.dlt[st] + Cfg::kCols * wg);
         // visible query columns of key j: c in [clo, chi] of this warpgroup's
         // columns (query i = 128 qb + kCols wg + c)
-        const bool msk = bwd_needs_mask(p, qb, I.kb);
+        const bool msk = bwd_needs_mask(p, I.seq, qb, I.kb);
         const int i0 = 128 * qb + Cfg::kCols * wg;
         int clo = 0, chi = Cfg::kCols - 1;
         if (p.causal) clo = j - i0;                                     // i >= j
         if (p.window > 0) chi = min(chi, j - i0 + p.window - 1);        // i - j < W
-        chi = min(chi, p.S - 1 - i0);                                   // i < S
+        chi = min(chi, I.seq.S - 1 - i0);                                   // i < S
         const uint32_t span = chi >= clo ? (uint32_t)(chi - clo) : 0u;
         if (chi < clo) clo = 1 << 30;
 
@@ -519,11 +679,11 @@ __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdPar
     if (!(ok = mbar_wait(&sm.acc_final, (uint32_t)items & 1u, abort))) break;
     ++items;
     tc_fence_after_sync();
-    const bool store = j < p.S;
-    const size_t row = ((size_t)I.bkv * p.S + j) * DH;
+    const bool store = bwd_real<PK>(I.seq, j);
     constexpr int kHalf = Cfg::kWG / 2;              // warpgroups per accumulator
     const bool is_dv = wg < kHalf;
-    __nv_bfloat16* dst = (is_dv ? p.dv : p.dk) + row;
+    __nv_bfloat16* dst = is_dv ? p.dv + bwd_row<PK>(I.seq, I.bkv, j, DH, p.dv_row, p.dv_head)
+                               : p.dk + bwd_row<PK>(I.seq, I.bkv, j, DH, p.dk_row, p.dk_head);
     const uint32_t colA = lane_addr + (is_dv ? Cfg::kColA0 : Cfg::kColA1);
     const float mul = is_dv ? 1.0f : p.scale;
 #pragma unroll 1
@@ -538,7 +698,7 @@ __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdPar
   }
 }
 
-template <int DH>
+template <int DH, bool PK = false>
 __global__ void __launch_bounds__(BwdCfg<DH>::kThreads, 1)
     attn_bwd_dkdv(const __grid_constant__ CUtensorMap map_q,
                   const __grid_constant__ CUtensorMap map_k,
@@ -591,11 +751,11 @@ __global__ void __launch_bounds__(BwdCfg<DH>::kThreads, 1)
   if (tbase != 0 && threadIdx.x == 0) sm.abort_flag = 1;
   if (tbase == 0) {
     if (warp == Cfg::kWarpProducer) {
-      if (lane == 0) bwd_dkdv_producer<DH>(sm, p, &map_q, &map_k, &map_v, &map_do, abort);
+      if (lane == 0) bwd_dkdv_producer<DH, PK>(sm, p, &map_q, &map_k, &map_v, &map_do, abort);
     } else if (warp == Cfg::kWarpIssuer) {
-      bwd_dkdv_issuer<DH>(sm, p, abort);
+      bwd_dkdv_issuer<DH, PK>(sm, p, abort);
     } else {
-      bwd_dkdv_softmax<DH>(sm, p, tbase, abort, warp, lane);
+      bwd_dkdv_softmax<DH, PK>(sm, p, tbase, abort, warp, lane);
     }
   }
   __syncwarp();
@@ -630,22 +790,41 @@ struct __align__(1024) BwdQSmem {
 // Item w of the dQ pass: query block qb (heaviest, i.e. last, first under a
 // causal mask) of query head bh = b * Hq + h.
 struct BwdQItem {
-  int qb, bh, bkv, lo, hi;
+  int qb, bh, bkv, lo, hi;   // PK: bh and bkv are the heads alone
+  BwdSeq seq;
 };
 
-__device__ __forceinline__ BwdQItem bwd_q_item_of(const BwdParams& p, int w) {
+// (without lo and hi)
+template <bool PK>
+__device__ __forceinline__ BwdQItem bwd_q_place_of(const BwdParams& p, int w) {
   BwdQItem r;
+  if constexpr (PK) {
+    const int i = w / p.Hq;
+    const PackedTile e = packed_tile(p.pk, i);
+    r.qb = e.blk;
+    r.bh = w - i * p.Hq;
+    r.bkv = r.bh / p.group;
+    r.seq = bwd_seq_of<PK>(p, e);
+    return r;
+  }
   const int per = p.B * p.Hq;
   const int blk = w / per;
   r.qb = p.nblk - 1 - blk;
   r.bh = w - blk * per;
   const int b = r.bh / p.Hq;
   r.bkv = b * p.Hkv + (r.bh - b * p.Hq) / p.group;   // g(h) = floor(h / (H/G))
-  bwd_kblocks_of(p, r.qb, r.lo, r.hi);
+  r.seq = bwd_seq_of<PK>(p, PackedTile{});
   return r;
 }
 
-template <int DH>
+template <bool PK>
+__device__ __forceinline__ BwdQItem bwd_q_item_of(const BwdParams& p, int w) {
+  BwdQItem r = bwd_q_place_of<PK>(p, w);
+  bwd_kblocks_of(p, r.seq, r.qb, r.lo, r.hi);
+  return r;
+}
+
+template <int DH, bool PK>
 __device__ __forceinline__ void bwd_dq_producer(BwdQSmem<DH>& sm, const BwdParams& p,
                                                 const CUtensorMap* map_q, const CUtensorMap* map_k,
                                                 const CUtensorMap* map_v,
@@ -658,32 +837,35 @@ __device__ __forceinline__ void bwd_dq_producer(BwdQSmem<DH>& sm, const BwdParam
   uint32_t ks = 0, kph = 0;   // K stage and its phase for block u (u % 3, (u / 3) & 1)
   int items = 0;
   bool ok = true;
+  const int num_items = bwd_num_items<PK>(p, p.Hq);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
-    if (w >= p.num_items) break;
-    const BwdQItem I = bwd_q_item_of(p, w);
+    if (w >= num_items) break;
+    const BwdQItem I = bwd_q_item_of<PK>(p, w);
     if (items > 0 && !(ok = mbar_wait(&sm.q_empty, (uint32_t)(items - 1) & 1u, abort))) break;
     // (checked builds: a query block of the sequence, of a query head of the batch)
-    const bool q_in_range = attn_check(I.qb >= 0 && 128 * I.qb < p.S && I.bh >= 0 &&
-                                           I.bh < p.B * p.Hq,
+    const bool q_in_range = attn_check(I.qb >= 0 && 128 * I.qb < I.seq.S && I.bh >= 0 &&
+                                           I.bh < p.B * p.Hq && bwd_inside<PK>(p, I.seq),
                                        p.error_word);
     mbar_arrive_expect_tx(&sm.q_full, q_in_range ? 2u * Cfg::kTile : 0u);
     for (int hf = 0; q_in_range && hf < kBoxes; ++hf) {
-      tma_load_3d(sm.q + hf * Cfg::kBox, map_q, &sm.q_full, 64 * hf, 128 * I.qb, I.bh);
-      tma_load_3d(sm.dO + hf * Cfg::kBox, map_do, &sm.q_full, 64 * hf, 128 * I.qb, I.bh);
+      bwd_load_once<PK>(sm.q + hf * Cfg::kBox, map_q, &sm.q_full, 64 * hf, 128 * I.qb, I.bh,
+                             p, I.seq, kPackedQ);
+      bwd_load_once<PK>(sm.dO + hf * Cfg::kBox, map_do, &sm.q_full, 64 * hf, 128 * I.qb,
+                             I.bh, p, I.seq, kPackedDO);
     }
     ++items;
     for (int kb = I.lo; kb <= I.hi; ++kb, ++u) {
       // (checked builds: a key block of the sequence, of a K/V head of the batch)
-      const bool in_range = attn_check(kb >= 0 && 128 * kb < p.S && I.bkv >= 0 &&
+      const bool in_range = attn_check(kb >= 0 && 128 * kb < I.seq.S && I.bkv >= 0 &&
                                            I.bkv < p.B * p.Hkv,
                                        p.error_word);
       const uint32_t bytes = in_range ? (uint32_t)Cfg::kTile : 0u;
       if (!(ok = mbar_wait(&sm.k_empty[ks], kph ^ 1u, abort))) break;
       mbar_arrive_expect_tx(&sm.k_full[ks], bytes);
       for (int hf = 0; in_range && hf < kBoxes; ++hf)
-        tma_load_3d_hint(sm.k[ks] + hf * Cfg::kBox, map_k, &sm.k_full[ks], 64 * hf, 128 * kb,
-                         I.bkv, keep);
+        bwd_load<PK>(sm.k[ks] + hf * Cfg::kBox, map_k, &sm.k_full[ks], 64 * hf, 128 * kb,
+                          I.bkv, p, I.seq, kPackedK, keep);
       k_loaded |= 1u << ks;
       k_par = (k_par & ~(1u << ks)) | (kph << ks);
       if (++ks == Smem::kStagesK) { ks = 0; kph ^= 1u; }
@@ -691,8 +873,8 @@ __device__ __forceinline__ void bwd_dq_producer(BwdQSmem<DH>& sm, const BwdParam
       if (!(ok = mbar_wait(&sm.v_empty[vs], vph ^ 1u, abort))) break;
       mbar_arrive_expect_tx(&sm.v_full[vs], bytes);
       for (int hf = 0; in_range && hf < kBoxes; ++hf)
-        tma_load_3d_hint(sm.v[vs] + hf * Cfg::kBox, map_v, &sm.v_full[vs], 64 * hf, 128 * kb,
-                         I.bkv, keep);
+        bwd_load<PK>(sm.v[vs] + hf * Cfg::kBox, map_v, &sm.v_full[vs], 64 * hf, 128 * kb,
+                          I.bkv, p, I.seq, kPackedV, keep);
       v_loaded |= 1u << vs;
       v_par = (v_par & ~(1u << vs)) | (vph << vs);
     }
@@ -713,7 +895,7 @@ __device__ __forceinline__ void bwd_dq_producer(BwdQSmem<DH>& sm, const BwdParam
 // it, has read dS(n) there.  A value block is released when its dP is done,
 // a key block only after dQ: three key stages let block n+2's keys load
 // while blocks n and n+1 are in use.
-template <int DH>
+template <int DH, bool PK>
 __device__ __forceinline__ void bwd_dq_issuer(BwdQSmem<DH>& sm, const BwdParams& p,
                                               volatile int* abort) {
   using Cfg = BwdCfg<DH>;
@@ -741,10 +923,11 @@ __device__ __forceinline__ void bwd_dq_issuer(BwdQSmem<DH>& sm, const BwdParams&
   uint32_t u = 0;
   int items = 0;
   bool ok = true;
+  const int num_items = bwd_num_items<PK>(p, p.Hq);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
-    if (w >= p.num_items) break;
-    const BwdQItem I = bwd_q_item_of(p, w);
+    if (w >= num_items) break;
+    const BwdQItem I = bwd_q_item_of<PK>(p, w);
     const int N = I.hi - I.lo + 1;
     if (!(ok = wait_all(&sm.q_full, (uint32_t)items & 1u))) break;
     ++items;
@@ -798,7 +981,7 @@ __device__ __forceinline__ void bwd_dq_issuer(BwdQSmem<DH>& sm, const BwdParams&
 // P = exp2(S * scale*log2e - lse2_i) (0 where masked), kept in fp32
 // registers; dS = P o (dP - D_i) as bf16 pairs over dP (see bwd_packed_col).
 // Per item: scale * dQ out, the 32-column chunks dealt to the warpgroups.
-template <int DH>
+template <int DH, bool PK>
 __device__ __forceinline__ void bwd_dq_softmax(BwdQSmem<DH>& sm, const BwdParams& p,
                                                uint32_t tbase, volatile int* abort, int warp,
                                                int lane) {
@@ -813,23 +996,25 @@ __device__ __forceinline__ void bwd_dq_softmax(BwdQSmem<DH>& sm, const BwdParams
   uint32_t u = 0;
   int items = 0;
   bool ok = true;
+  const int num_items = bwd_num_items<PK>(p, p.Hq);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
-    if (w >= p.num_items) break;
-    const BwdQItem I = bwd_q_item_of(p, w);
+    if (w >= num_items) break;
+    const BwdQItem I = bwd_q_item_of<PK>(p, w);
     const int i = 128 * I.qb + t;   // this thread's query
-    const float L = p.lse2[(size_t)I.bh * p.S_pad + i];
-    const float Di = p.delta[(size_t)I.bh * p.S_pad + i];
+    const float L = p.lse2[(size_t)I.bh * p.S_pad + (I.seq.stat + i)];
+    const float Di = p.delta[(size_t)I.bh * p.S_pad + (I.seq.stat + i)];
     const float2 negL = make_float2(-L, -L), negD = make_float2(-Di, -Di);
     for (int kb = I.lo; kb <= I.hi; ++kb, ++u) {
       if (!(ok = mbar_wait(&sm.s_full, u & 1u, abort))) break;
       tc_fence_after_sync();
       // visible keys of query i: [klo, khi], as columns [clo, chi] of this warpgroup's
-      const bool msk = bwd_needs_mask(p, I.qb, kb);
+      const bool msk = bwd_needs_mask(p, I.seq, I.qb, kb);
       const int j0 = 128 * kb + Cfg::kCols * wg;
-      int khi = p.S - 1;
+      int khi = I.seq.S - 1;
       if (p.causal) khi = min(khi, i);
-      const int klo = p.window > 0 ? i - p.window + 1 : 0;
+      int klo = p.window > 0 ? i - p.window + 1 : 0;
+      if (PK) klo = max(klo, I.seq.pad);
       int clo = klo - j0;
       const int chi = khi - j0;
       const uint32_t span = chi >= clo ? (uint32_t)(chi - clo) : 0u;
@@ -888,8 +1073,8 @@ __device__ __forceinline__ void bwd_dq_softmax(BwdQSmem<DH>& sm, const BwdParams
     if (!(ok = mbar_wait(&sm.acc_final, (uint32_t)items & 1u, abort))) break;
     ++items;
     tc_fence_after_sync();
-    const bool store = i < p.S;
-    const size_t row = ((size_t)I.bh * p.S + i) * DH;
+    const bool store = bwd_real<PK>(I.seq, i);
+    const size_t row = bwd_row<PK>(I.seq, I.bh, i, DH, p.dq_row, p.dq_head);
 #pragma unroll 1
     for (int c = wg; c < DH / 32; c += Cfg::kWG) {
       uint32_t r[32];
@@ -900,7 +1085,7 @@ __device__ __forceinline__ void bwd_dq_softmax(BwdQSmem<DH>& sm, const BwdParams
   }
 }
 
-template <int DH>
+template <int DH, bool PK = false>
 __global__ void __launch_bounds__(BwdCfg<DH>::kThreads, 1)
     attn_bwd_dq(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                 const __grid_constant__ CUtensorMap map_v,
@@ -952,11 +1137,11 @@ __global__ void __launch_bounds__(BwdCfg<DH>::kThreads, 1)
   if (tbase != 0 && threadIdx.x == 0) sm.abort_flag = 1;
   if (tbase == 0) {
     if (warp == Cfg::kWarpProducer) {
-      if (lane == 0) bwd_dq_producer<DH>(sm, p, &map_q, &map_k, &map_v, &map_do, abort);
+      if (lane == 0) bwd_dq_producer<DH, PK>(sm, p, &map_q, &map_k, &map_v, &map_do, abort);
     } else if (warp == Cfg::kWarpIssuer) {
-      bwd_dq_issuer<DH>(sm, p, abort);
+      bwd_dq_issuer<DH, PK>(sm, p, abort);
     } else {
-      bwd_dq_softmax<DH>(sm, p, tbase, abort, warp, lane);
+      bwd_dq_softmax<DH, PK>(sm, p, tbase, abort, warp, lane);
     }
   }
   __syncwarp();

@@ -120,6 +120,85 @@ cudaError_t launch_bwd(const void* q, const void* k, const void* v, const void* 
                        float* workspace, int B, int Hq, int Hkv, int S, int Dh, int causal,
                        int window, float scale, const DeviceInfo& dev, cudaStream_t stream);
 
+// ---------------------------------------------------------------- packed sequences
+// Rows of heads [T, H, Dh] bf16 at any strides, in elements (include/attn.h).
+struct PackedRows {
+  const void* data;
+  long long row, head;
+  int H;
+};
+
+// A map over such a tensor with boxes of box_rows x 64, with the row axis once or (padded, for
+// loads that begin with padding) twice: packed_sm103a.cuh.  *heads_inner says in which order
+// its axes lie.
+bool encode_packed_map(CUtensorMap* map, const PackedRows& x, int Dh, int T, int box_rows,
+                       bool padded, bool* heads_inner);
+
+struct PackedShape {
+  int B, Hq, Hkv, T, Dh;
+  int causal, window;
+  const int* cu;   // [B + 1] first rows of the sequences, and the last one's end
+};
+
+// Device memory that the calls need: the lists of tiles, and the backward's row statistics.
+size_t fwd_packed_workspace_bytes(int B, int T);
+size_t bwd_packed_workspace_bytes(int B, int Hq, int T);
+// Most 128-row tiles that B sequences of T rows in all can have.
+inline long long packed_max_tiles(int B, int T) { return (long long)T / 128 + B; }
+
+cudaError_t launch_fwd_packed(const PackedShape& s, const PackedRows& q, const PackedRows& k,
+                              const PackedRows& v, const PackedRows& o, float* lse,
+                              void* workspace, float scale_log2, const DeviceInfo& dev,
+                              cudaStream_t stream);
+cudaError_t launch_bwd_packed(const PackedShape& s, const PackedRows& q, const PackedRows& k,
+                              const PackedRows& v, const PackedRows& o, const PackedRows& dout,
+                              const float* lse, const PackedRows& dq, const PackedRows& dk,
+                              const PackedRows& dv, void* workspace, float scale,
+                              const DeviceInfo& dev, cudaStream_t stream);
+// Lists of tiles of `block` rows, heaviest first: list[i] for order[i] (PackedOrder); tiles and
+// counts lie in device memory.
+cudaError_t launch_packed_schedule(const PackedShape& s, int block, int lists, const int* order,
+                                   void* const* tiles, int* const* counts, const DeviceInfo& dev,
+                                   cudaStream_t stream);
+
+// ---------------------------------------------------------------- tokens
+// [B, S, H, Dh] bf16 at any strides, in elements.
+struct RopeRows {
+  const void* data;
+  long long batch, row, head;
+};
+
+struct RopeShape {
+  int B, S, Hq, Hkv, Dh, rot;
+  const int* positions;              // [B * S]
+  const unsigned long long* turns;   // [rot / 2], 2^-64 turns per token
+  float amplitude;
+  int interleaved, inverse;
+};
+
+struct RopeAppend {
+  RopeRows v;
+  void *kpages, *vpages;
+  const int* slots;   // [B * S]
+  int num_pages, page;
+};
+
+// q_out and k_out may be the inputs, or null (k_out with append: k goes to the cache alone).
+cudaError_t launch_rope(const RopeShape& s, const RopeRows& q, const RopeRows* q_out,
+                        const RopeRows& k, const RopeRows* k_out, const RopeAppend* append,
+                        const DeviceInfo& dev, cudaStream_t stream);
+
+// The pages, slots and positions of a step (include/attn.h).
+struct CachePlan {
+  const int *delta, *seqlens;
+  int *seqlens_out, *table, *free_pages;
+  const int* num_free;
+  int *num_free_out, *cu, *positions, *slots;
+  int B, cols, page, num_pages, capacity, T;
+};
+int cache_plan_max_sequences();
+cudaError_t launch_cache_plan(const CachePlan& c, const DeviceInfo& dev, cudaStream_t stream);
+
 // ---------------------------------------------------------------- paged cache
 // K and V pools [num_pages, Hkv, page, Dh]; row t of sequence b in page
 // table[b, t / page] at row t % page (include/attn.h).

@@ -1,0 +1,107 @@
+// packed_sm103a.cuh -- packed sequences: what the attention kernels need to
+// walk sequences of different lengths that lie one behind another.
+//
+// Sequence b holds rows cu[b] .. cu[b+1] - 1 of tensors [T, H, Dh] whose rows
+// and heads lie at any strides.  Two things differ from a [B, H, S, Dh] batch:
+//
+//   Sequences end inside tiles.  What lies next to a sequence in memory is
+//   another one's rows, and those must not reach the tensor core: a masked
+//   score hides a foreign key, but a weight of 0 times an infinity in a foreign
+//   V row is NaN.  So a sequence is padded to whole 128-row blocks at its
+//   front, with rows that no copy reads: its last row ends a block, and only
+//   its first block is short.  The tensor maps carry the row axis twice, both
+//   times with the row's stride: an axis of R rows (the box's height) and one
+//   of T.  A box over padded rows [t, t + R) of a sequence that starts at row a
+//   behind `pad` of them is copied from
+//       (t - pad, a)      where t < pad: the rows ahead of a lie before the
+//                         R-row axis, and a load fills them with zeros;
+//       (0, a + t - pad)  otherwise.
+//   One map serves every sequence, and no row but the sequence's own is read.
+//   Positions are counted with the padding: masks that compare positions do
+//   not see a common shift.  Padded keys are masked; padded queries compute
+//   rows that nobody stores.  (Padding at the end would need boxes that end at
+//   any row, whose map starts ahead of the tensor.)
+//
+//   The work is known on the GPU alone.  A launch ahead of the attention
+//   kernel lists the tiles, heaviest first (attn_packed_schedule).
+#pragma once
+
+#include "sm103a_ptx.cuh"
+
+namespace chs {
+
+// One block of rows of a sequence.
+struct __align__(16) PackedTile {
+  int start;   // the sequence's first row
+  int len;     // its rows
+  int blk;     // which block of its padded rows
+  int stat;    // its first padded row among those of all sequences
+  __device__ __forceinline__ int pad() const { return -len & 127; }
+};
+
+// Tensors, as bits of PackedRef::heads_inner.
+constexpr int kPackedQ = 1, kPackedK = 2, kPackedV = 4, kPackedO = 8, kPackedDO = 16;
+
+struct PackedRef {
+  const PackedTile* tiles;   // heaviest first
+  const int* num_tiles;
+  int T;                     // rows of the packed tensors
+  int heads_inner;           // tensors whose heads lie closer than their rows: map axes
+                             // {Dh, head, rows, start} instead of {Dh, rows, start, head}
+};
+
+// Read past L1: the list was written by the launch before this one.
+__device__ __forceinline__ PackedTile packed_tile(const PackedRef& p, int i) {
+  const int4 e = __ldcg(reinterpret_cast<const int4*>(p.tiles + i));
+  return PackedTile{e.x, e.y, e.z, e.w};
+}
+__device__ __forceinline__ int packed_num_tiles(const PackedRef& p) { return __ldcg(p.num_tiles); }
+
+__device__ __forceinline__ void tma_load_4d_hint(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                                 int c0, int c1, int c2, int c3, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
+      "l"(policy)
+      : "memory");
+}
+
+// Padded rows [row, row + R) of the sequence that starts at row `start` behind `pad` of them,
+// columns c .. c + 63 of one head; padded rows are zeros.
+__device__ __forceinline__ void packed_load(void* dst, const CUtensorMap* map, uint64_t* bar, int c,
+                                            int start, int pad, int row, int head, bool heads_inner,
+                                            uint64_t policy) {
+  const int y = min(row - pad, 0), z = start + max(row - pad, 0);
+  tma_load_4d_hint(dst, map, bar, c, heads_inner ? head : y, heads_inner ? y : z,
+                   heads_inner ? z : head, policy);
+}
+
+// Rows of the sequence from padded row `row` (>= pad) on, through a map with one row axis.
+__device__ __forceinline__ void packed_store(const CUtensorMap* map, const void* src, int c,
+                                             int start, int pad, int row, int head,
+                                             bool heads_inner, uint64_t policy) {
+  const int z = start + row - pad;
+  tma_store_3d_hint(map, src, c, heads_inner ? head : z, heads_inner ? z : head, policy);
+}
+
+// ---------------------------------------------------------------- the list of tiles
+
+// What a tile's time goes by (its 128-row partner blocks).
+enum PackedOrder {
+  kByKeys = 0,      // a block of queries: the keys it sees
+  kByQueries = 1,   // a block of keys: the queries that see it
+};
+
+struct PackedSchedule {
+  const int* cu;   // [B + 1]
+  int B, T;
+  int block;       // rows per tile: 128 or 256
+  int causal, window;
+  PackedTile* tiles[2];   // one list per order (block x of the grid makes list x)
+  int order[2];
+  int* num_tiles[2];
+  int* error_word;
+};
+
+}  // namespace chs

@@ -32,13 +32,15 @@
 // roles of the ping-pong kernel (prefill_sm103a.cuh): one thread issues every
 // TMA load, one warp issues every MMA, four warps run the softmax and the
 // epilogue (thread t owns row t).  Masks, the lazy maximum and the
-// chunked-prefill offset follow that kernel.  Every wait is bounded.
+// chunked-prefill offset follow that kernel, and so does the form over packed
+// sequences (PK = true).  Every wait is bounded.
 #pragma once
 
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include "packed_sm103a.cuh"
 #include "sm103a_ptx.cuh"
 
 namespace chs {
@@ -57,6 +59,8 @@ struct PrefillK64Params {
   float* lse;           // optional [B, Hq, Sq]: log sum_j exp(s_ij) per row (natural log)
   int* error_word;
   int fault;            // test hook: 1 = the first K tile is never loaded
+  PackedRef pk;         // PK: the sequences' tiles (128 rows each), and o's strides in elements
+  long long o_row, o_head;
 };
 
 template <int DH_>
@@ -117,15 +121,17 @@ struct PrefillK64Smem {
 // at positions q_off + row; key tiles lo..hi of 64 keys.
 struct PrefillK64Tile {
   int q0, lo, hi;
-  int bh, bh_kv;
-  __device__ __forceinline__ int pos_first(const PrefillK64Params& p) const { return p.q_off + q0; }
+  int bh, bh_kv;             // PK: the heads alone
+  int Sq, Skv, q_off;
+  int start, pad;            // PK: the sequence's first row, and the rows of padding ahead of it
+  __device__ __forceinline__ int pos_first(const PrefillK64Params& p) const { return q_off + q0; }
   __device__ __forceinline__ int pos_last(const PrefillK64Params& p) const {
-    return p.q_off + min(q0 + 127, p.Sq - 1);
+    return q_off + min(q0 + 127, Sq - 1);
   }
   // is any (row, key) pair of tile j masked?
   __device__ __forceinline__ bool needs_mask(const PrefillK64Params& p, int j) const {
     const int c0 = 64 * j, c1 = 64 * j + 63;
-    if (c1 >= p.Skv) return true;
+    if (c1 >= Skv || c0 < pad) return true;
     if (p.causal && c1 > pos_first(p)) return true;
     if (p.window > 0 && c0 < pos_last(p) - p.window + 1) return true;
     return false;
@@ -148,18 +154,44 @@ __device__ __forceinline__ int prefill_k64_cta_item(int k, int num_items) {
   return k < n ? prefill_k64_item(n - 1 - k, c, G) : num_items;
 }
 
+// Work items of the launch (PK: known on the GPU alone; there may be none for a CTA).
+template <bool PK>
+__device__ __forceinline__ int prefill_k64_num_items(const PrefillK64Params& p) {
+  return PK ? packed_num_tiles(p.pk) * p.Hq : p.num_items;
+}
+
+template <bool PK>
 __device__ __forceinline__ PrefillK64Tile prefill_k64_tile_of(const PrefillK64Params& p, int w) {
   PrefillK64Tile t;
-  const int blk = w / p.per_qb;
-  const int qb = p.num_qblocks - 1 - blk;
-  t.bh = w - blk * p.per_qb;
-  const int b = t.bh / p.Hq, h = t.bh - (t.bh / p.Hq) * p.Hq;
-  t.bh_kv = b * p.Hkv + h / p.group;   // g(h) = floor(h / (H/G))
+  int qb;
+  if constexpr (PK) {
+    // a tile's heads one after another: those of a group share their K/V tiles in L2
+    const int i = w / p.Hq;
+    const PackedTile e = packed_tile(p.pk, i);
+    t.bh = w - i * p.Hq;
+    t.bh_kv = t.bh / p.group;
+    t.Sq = t.Skv = e.len + e.pad();
+    t.q_off = 0;
+    t.start = e.start;
+    t.pad = e.pad();
+    qb = e.blk;
+  } else {
+    const int blk = w / p.per_qb;
+    qb = p.num_qblocks - 1 - blk;
+    t.bh = w - blk * p.per_qb;
+    const int b = t.bh / p.Hq, h = t.bh - (t.bh / p.Hq) * p.Hq;
+    t.bh_kv = b * p.Hkv + h / p.group;   // g(h) = floor(h / (H/G))
+    t.Sq = p.Sq;
+    t.Skv = p.Skv;
+    t.q_off = p.q_off;
+    t.start = t.pad = 0;
+  }
   t.q0 = qb * 128;
-  const int nkv = (p.Skv + 63) / 64;
-  const int last_pos = p.q_off + min(t.q0 + 127, p.Sq - 1);
+  const int nkv = (t.Skv + 63) / 64;
+  const int last_pos = t.q_off + min(t.q0 + 127, t.Sq - 1);
   t.hi = p.causal ? min(nkv - 1, last_pos / 64) : nkv - 1;
-  t.lo = (p.causal && p.window > 0) ? max(0, p.q_off + t.q0 - p.window + 1) / 64 : 0;
+  t.lo = (p.causal && p.window > 0) ? max(0, t.q_off + t.q0 - p.window + 1) / 64 : 0;
+  if constexpr (PK) t.lo = max(t.lo, t.pad / 64);   // (the first tile may be padding alone)
   return t;
 }
 
@@ -174,7 +206,7 @@ __device__ __forceinline__ void mbar_wait_drain_k64(uint64_t* bar, uint32_t pari
 // TMA producer (one thread): per item, Q (Dh/64 boxes of 128 x 64) once its
 // previous item's last S is done, then the item's K and V tiles (Dh/64 boxes
 // of 64 x 64 each) through the K and V rings.
-template <int DH>
+template <int DH, bool PK>
 __device__ __forceinline__ void prefill_k64_producer(PrefillK64Smem<DH>& sm, const PrefillK64Params& p,
                                                     const CUtensorMap* map_q,
                                                     const CUtensorMap* map_k,
@@ -186,26 +218,34 @@ __device__ __forceinline__ void prefill_k64_producer(PrefillK64Smem<DH>& sm, con
   uint32_t k_loaded = 0, k_par = 0, v_loaded = 0, v_par = 0;
   int nq = 0;
   bool ok = true;
+  const int num_items = prefill_k64_num_items<PK>(p);
   for (int it = 0; ok; ++it) {
-    const int w = prefill_k64_cta_item(it, p.num_items);
-    if (w >= p.num_items) break;
-    const PrefillK64Tile tile = prefill_k64_tile_of(p, w);
+    const int w = prefill_k64_cta_item(it, num_items);
+    if (w >= num_items) break;
+    const PrefillK64Tile tile = prefill_k64_tile_of<PK>(p, w);
     if (nq > 0 && !(ok = mbar_wait(&sm.q_empty, (uint32_t)(nq - 1) & 1u, abort))) break;
     // (checked builds: a query row of the chunk and a query head of the batch)
-    const bool q_in_range = attn_check(tile.q0 >= 0 && tile.q0 < p.Sq && tile.bh >= 0 &&
-                                           tile.bh < p.B * p.Hq,
+    const bool q_in_range = attn_check(tile.q0 >= 0 && tile.q0 < tile.Sq && tile.bh >= 0 &&
+                                           tile.bh < p.B * p.Hq &&
+                                           (!PK ||
+                                            (tile.start >= 0 &&
+                                             tile.start <= p.pk.T - (tile.Sq - tile.pad))),
                                        p.error_word);
     mbar_arrive_expect_tx(&sm.q_full, q_in_range ? (uint32_t)Cfg::kQBytes : 0u);
     for (int hf = 0; q_in_range && hf < Cfg::kBoxes; ++hf)
       // (read once: evict-first, leaving L2 to the K/V tiles that are re-read)
-      tma_load_3d_hint(sm.q + hf * Cfg::kQBox, map_q, &sm.q_full, hf * 64, tile.q0, tile.bh,
-                       policy_evict_first());
+      if constexpr (PK)
+        packed_load(sm.q + hf * Cfg::kQBox, map_q, &sm.q_full, hf * 64, tile.start, tile.pad,
+                    tile.q0, tile.bh, p.pk.heads_inner & kPackedQ, policy_evict_first());
+      else
+        tma_load_3d_hint(sm.q + hf * Cfg::kQBox, map_q, &sm.q_full, hf * 64, tile.q0, tile.bh,
+                         policy_evict_first());
     ++nq;
     for (int j = tile.lo; j <= tile.hi; ++j, ++t) {
       const int st = (int)(t % Cfg::kStagesK);
       const uint32_t ph = (t / Cfg::kStagesK) & 1u;
       // (checked builds: a key tile that starts inside the keys, of a K/V head of the batch)
-      const bool in_range = attn_check(j >= 0 && 64 * j < p.Skv && tile.bh_kv >= 0 &&
+      const bool in_range = attn_check(j >= 0 && 64 * j < tile.Skv && tile.bh_kv >= 0 &&
                                            tile.bh_kv < p.B * p.Hkv,
                                        p.error_word);
       const uint32_t bytes = in_range ? (uint32_t)Cfg::kTileBytes : 0u;
@@ -213,8 +253,12 @@ __device__ __forceinline__ void prefill_k64_producer(PrefillK64Smem<DH>& sm, con
       mbar_arrive_expect_tx(&sm.k_full[st], bytes);
       if (p.fault != 1 || it != 0 || j != tile.lo) {   // (the test hook withholds one tile)
         for (int hf = 0; in_range && hf < Cfg::kBoxes; ++hf)
-          tma_load_3d_hint(sm.k[st] + hf * Cfg::kKBox, map_k, &sm.k_full[st], hf * 64, 64 * j,
-                           tile.bh_kv, keep);
+          if constexpr (PK)
+            packed_load(sm.k[st] + hf * Cfg::kKBox, map_k, &sm.k_full[st], hf * 64, tile.start,
+                        tile.pad, 64 * j, tile.bh_kv, p.pk.heads_inner & kPackedK, keep);
+          else
+            tma_load_3d_hint(sm.k[st] + hf * Cfg::kKBox, map_k, &sm.k_full[st], hf * 64, 64 * j,
+                             tile.bh_kv, keep);
       }
       k_loaded |= 1u << st;
       k_par = (k_par & ~(1u << st)) | (ph << st);
@@ -223,8 +267,12 @@ __device__ __forceinline__ void prefill_k64_producer(PrefillK64Smem<DH>& sm, con
       if (!(ok = mbar_wait(&sm.v_empty[sv], pv ^ 1u, abort))) break;
       mbar_arrive_expect_tx(&sm.v_full[sv], bytes);
       for (int hf = 0; in_range && hf < Cfg::kBoxes; ++hf)
-        tma_load_3d_hint(sm.v[sv] + hf * Cfg::kKBox, map_v, &sm.v_full[sv], hf * 64, 64 * j,
-                         tile.bh_kv, keep);
+        if constexpr (PK)
+          packed_load(sm.v[sv] + hf * Cfg::kKBox, map_v, &sm.v_full[sv], hf * 64, tile.start,
+                      tile.pad, 64 * j, tile.bh_kv, p.pk.heads_inner & kPackedV, keep);
+        else
+          tma_load_3d_hint(sm.v[sv] + hf * Cfg::kKBox, map_v, &sm.v_full[sv], hf * 64, 64 * j,
+                           tile.bh_kv, keep);
       v_loaded |= 1u << sv;
       v_par = (v_par & ~(1u << sv)) | (pv << sv);
     }
@@ -245,7 +293,7 @@ __device__ __forceinline__ void prefill_k64_producer(PrefillK64Smem<DH>& sm, con
 // Dh 256 an item starts with the copy of Q into tensor memory; a copy issued
 // after an MMA is not ordered behind it, so the copy waits (qt_free) for the
 // previous item's last S MMA, which is long done by then.
-template <int DH>
+template <int DH, bool PK>
 __device__ __forceinline__ void prefill_k64_issuer(PrefillK64Smem<DH>& sm, const PrefillK64Params& p,
                                                    uint32_t tbase, volatile int* abort) {
   using Cfg = PrefillK64Cfg<DH>;
@@ -281,10 +329,11 @@ __device__ __forceinline__ void prefill_k64_issuer(PrefillK64Smem<DH>& sm, const
   uint32_t t = 0;   // global tile counter
   int nq = 0;
   bool ok = true;
+  const int num_items = prefill_k64_num_items<PK>(p);
   for (int it = 0; ok; ++it) {
-    const int w = prefill_k64_cta_item(it, p.num_items);
-    if (w >= p.num_items) break;
-    const PrefillK64Tile tile = prefill_k64_tile_of(p, w);
+    const int w = prefill_k64_cta_item(it, num_items);
+    if (w >= num_items) break;
+    const PrefillK64Tile tile = prefill_k64_tile_of<PK>(p, w);
     const int n = tile.hi - tile.lo + 1;
     if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_full, (uint32_t)nq & 1u, abort)))) break;
     tc_fence_after_sync();
@@ -339,7 +388,7 @@ __device__ __forceinline__ void prefill_k64_issuer(PrefillK64Smem<DH>& sm, const
 // Softmax and epilogue (warps 0-3; thread t owns row t of the item, TMEM lane
 // t): the online softmax of "Online normalizer calculation for softmax" with
 // the lazy maximum of the ping-pong kernel, 64 scores per tile.
-template <int DH>
+template <int DH, bool PK>
 __device__ __forceinline__ void prefill_k64_softmax(PrefillK64Smem<DH>& sm, const PrefillK64Params& p,
                                                     const CUtensorMap* map_o, uint32_t tbase,
                                                     volatile int* abort, int warp, int lane) {
@@ -351,10 +400,11 @@ __device__ __forceinline__ void prefill_k64_softmax(PrefillK64Smem<DH>& sm, cons
   uint32_t tt = 0;      // global tile counter (the issuer's t)
   uint32_t items = 0;   // items finished (o_final phases)
   bool ok = true;
+  const int num_items = prefill_k64_num_items<PK>(p);
   for (int it = 0; ok; ++it) {
-    const int w = prefill_k64_cta_item(it, p.num_items);
-    if (w >= p.num_items) break;
-    const PrefillK64Tile tile = prefill_k64_tile_of(p, w);
+    const int w = prefill_k64_cta_item(it, num_items);
+    if (w >= num_items) break;
+    const PrefillK64Tile tile = prefill_k64_tile_of<PK>(p, w);
     const int row = tile.pos_first(p) + t;   // this thread's query position
 
     float m_run = -INFINITY, l_run = 0.f;
@@ -369,9 +419,10 @@ __device__ __forceinline__ void prefill_k64_softmax(PrefillK64Smem<DH>& sm, cons
         // ping-pong kernel): visible keys [klo, khi] as column offsets
         // [clo, chi] of this 64-key tile
         const int kv0 = 64 * j;
-        int khi = p.Skv - 1;
+        int khi = tile.Skv - 1;
         if (p.causal) khi = min(khi, row);
-        const int klo = p.window > 0 ? row - p.window + 1 : 0;
+        int klo = p.window > 0 ? row - p.window + 1 : 0;
+        if (PK) klo = max(klo, tile.pad);
         int clo = klo - kv0;
         const int chi = khi - kv0;
         const uint32_t span = chi >= clo ? (uint32_t)(chi - clo) : 0u;
@@ -456,11 +507,17 @@ __device__ __forceinline__ void prefill_k64_softmax(PrefillK64Smem<DH>& sm, cons
     tc_fence_after_sync();
     const float inv_l = 1.0f / l_run;
     const int orow = tile.q0 + t;   // output row within the chunk
-    uint4* dst = reinterpret_cast<uint4*>(p.o + ((size_t)tile.bh * p.Sq + orow) * Cfg::DH);
-    const bool store = orow < p.Sq;
+    uint4* dst = reinterpret_cast<uint4*>(
+        p.o + (PK ? (tile.start + orow - tile.pad) * p.o_row + tile.bh * p.o_head
+                  : ((long long)tile.bh * p.Sq + orow) * Cfg::DH));
+    const bool store = PK ? orow >= tile.pad : orow < tile.Sq;
+    // PK: a warp whose rows begin with padding stores the others itself
+    const bool mixed = PK && orow - lane < tile.pad;
     // sum_j exp(s_ij) = 2^m_run * l_run (m_run in units of log2)
     if (p.lse != nullptr && store)
-      p.lse[(size_t)tile.bh * p.Sq + orow] = (m_run + __log2f(l_run)) * 0.69314718055994531f;
+      p.lse[PK ? (size_t)tile.bh * p.pk.T + tile.start + orow - tile.pad
+               : (size_t)tile.bh * p.Sq + orow] =
+          (m_run + __log2f(l_run)) * 0.69314718055994531f;
     // (the output is not read again by this kernel: evict-first, leaving L2
     // to the K/V tiles the other query blocks re-read)
     const uint64_t out_policy = policy_evict_first();
@@ -488,12 +545,20 @@ __device__ __forceinline__ void prefill_k64_softmax(PrefillK64Smem<DH>& sm, cons
           for (int e = 0; e < 4; ++e)
             v[e] = pack_bf16x2(__uint_as_float(x8[2 * e]) * inv_l,
                                __uint_as_float(x8[2 * e + 1]) * inv_l);
+          if (PK && mixed && store) dst[8 * h + c] = make_uint4(v[0], v[1], v[2], v[3]);
           st_shared_v4(stage + lane * 128 + ((c ^ (lane & 7)) << 4), v[0], v[1], v[2], v[3]);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tma_store_3d_hint(map_o, stg, 64 * h, tile.q0 + 32 * warp, tile.bh, out_policy);
+          const int row = tile.q0 + 32 * warp;
+          if constexpr (PK) {
+            if (!mixed)
+              packed_store(map_o, stg, 64 * h, tile.start, tile.pad, row, tile.bh,
+                           p.pk.heads_inner & kPackedO, out_policy);
+          } else {
+            tma_store_3d_hint(map_o, stg, 64 * h, row, tile.bh, out_policy);
+          }
           bulk_commit_group();
         }
       }
@@ -533,7 +598,7 @@ __device__ __forceinline__ void prefill_k64_softmax(PrefillK64Smem<DH>& sm, cons
   }
 }
 
-template <int DH>
+template <int DH, bool PK = false>
 __global__ void __launch_bounds__(PrefillK64Cfg<DH>::kThreads, PrefillK64Cfg<DH>::kCtasPerSm)
     attn_prefill_k64_sm103a(const __grid_constant__ CUtensorMap map_q,
                             const __grid_constant__ CUtensorMap map_k,
@@ -597,11 +662,11 @@ __global__ void __launch_bounds__(PrefillK64Cfg<DH>::kThreads, PrefillK64Cfg<DH>
   // Dh 128 two CTAs share an SM's 512 columns)
   const uint32_t tbase = sm.tmem_base;
   if (warp == Cfg::kWarpProducer) {
-    if (lane == 0) prefill_k64_producer<DH>(sm, p, &map_q, &map_k, &map_v, abort);
+    if (lane == 0) prefill_k64_producer<DH, PK>(sm, p, &map_q, &map_k, &map_v, abort);
   } else if (warp == Cfg::kWarpIssuer) {
-    prefill_k64_issuer<DH>(sm, p, tbase, abort);
+    prefill_k64_issuer<DH, PK>(sm, p, tbase, abort);
   } else {
-    prefill_k64_softmax<DH>(sm, p, &map_o, tbase, abort, warp, lane);
+    prefill_k64_softmax<DH, PK>(sm, p, &map_o, tbase, abort, warp, lane);
   }
 
   // ---- teardown (every wait above is bounded)

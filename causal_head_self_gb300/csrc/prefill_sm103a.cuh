@@ -22,6 +22,9 @@
 // block) in "snake" order over the CTAs (a CTA with only two items takes the
 // lighter one first), and the TMA producer runs ahead into the next item
 // (its Q and K/V tiles) while the current one finishes.
+// PK = true is the same kernel over packed sequences (packed_sm103a.cuh): an
+// item's rows, keys and place come from the list of tiles instead of the
+// launch's shape, and rows are counted with the sequence's padding in front.
 // Roles (384 threads):
 //   warps 0-3  softmax + epilogue of sub-tile 0 (thread t owns row t, TMEM lane t;
 //              each warp writes its 32 output rows with bulk tensor stores)
@@ -43,6 +46,7 @@
 #pragma once
 
 #include "fixed_div.h"
+#include "packed_sm103a.cuh"
 #include "sm103a_ptx.cuh"
 
 namespace chs {
@@ -63,6 +67,9 @@ struct PrefillParams {
   FixedDiv div_bh;     // by B * Hq (work items per query block)
   FixedDiv div_hq;     // by Hq
   FixedDiv div_group;  // by Hq / Hkv (query heads per K/V head)
+  PackedRef pk;        // PK: the sequences' tiles (256 rows each); o and its strides in elements
+  __nv_bfloat16* o;
+  long long o_row, o_head;
 };
 
 template <int DH>
@@ -113,6 +120,7 @@ struct PrefillTile {
   int q0;        // first query row of the item
   int lo, hi;    // K/V tile range loaded (union over the two sub-tiles)
   int Sq, Skv, q_off, causal, window;
+  int pad;       // PK: the first so many rows and keys are padding (0 in a batch)
   __device__ __forceinline__ int row_first(int s) const { return q0 + 128 * s; }
   __device__ __forceinline__ int pos_first(int s) const { return q_off + q0 + 128 * s; }
   __device__ __forceinline__ int pos_last(int s) const {
@@ -135,24 +143,27 @@ struct PrefillTile {
   __device__ __forceinline__ bool needs_mask(int s, int j) const {
     const int c0 = 128 * j, c1 = 128 * j + 127;
     if (c1 >= Skv) return true;
+    if (c0 < pad) return true;
     if (causal && c1 > pos_first(s)) return true;
     if (window > 0 && c0 < pos_last(s) - window + 1) return true;
     return false;
   }
 };
 
-__device__ __forceinline__ PrefillTile prefill_tile_of(const PrefillParams& p, int qb) {
+__device__ __forceinline__ PrefillTile prefill_tile_of(const PrefillParams& p, int qb, int Sq,
+                                                       int Skv, int q_off, int pad) {
   PrefillTile t;
+  t.pad = pad;
   t.q0 = qb * 256;
-  t.Sq = p.Sq;
-  t.Skv = p.Skv;
-  t.q_off = p.q_off;
+  t.Sq = Sq;
+  t.Skv = Skv;
+  t.q_off = q_off;
   t.causal = p.causal;
   t.window = p.window;
-  const int nkv = (p.Skv + 127) / 128;
-  const int last_pos = p.q_off + min(t.q0 + 255, p.Sq - 1);
+  const int nkv = (Skv + 127) / 128;
+  const int last_pos = q_off + min(t.q0 + 255, Sq - 1);
   t.hi = p.causal ? min(nkv - 1, last_pos / 128) : nkv - 1;
-  t.lo = (p.causal && p.window > 0) ? max(0, p.q_off + t.q0 - p.window + 1) / 128 : 0;
+  t.lo = (p.causal && p.window > 0) ? max(0, q_off + t.q0 - p.window + 1) / 128 : 0;
   return t;
 }
 
@@ -193,19 +204,40 @@ __device__ __forceinline__ int prefill_cta_item(int k, int num_items) {
 }
 
 struct PrefillItem {
-  int b, h, bh, bh_kv;
+  int b, h, bh, bh_kv;   // PK: b = 0, bh = h and bh_kv the K/V head
+  int start;             // PK: the sequence's first row
   PrefillTile tile;
 };
 
+// Work items of the launch (PK: known on the GPU alone; there may be none for a CTA).
+template <bool PK>
+__device__ __forceinline__ int prefill_num_items(const PrefillParams& p) {
+  return PK ? packed_num_tiles(p.pk) * p.Hq : p.num_items;
+}
+
+template <bool PK>
 __device__ __forceinline__ PrefillItem prefill_item_of(const PrefillParams& p, int w) {
   PrefillItem it;
+  if constexpr (PK) {
+    // a tile's heads one after another: those of a group share their K/V tiles in L2
+    const int i = p.div_hq.div(w);
+    const PackedTile e = packed_tile(p.pk, i);
+    it.b = 0;
+    it.h = it.bh = w - i * p.Hq;
+    it.bh_kv = p.div_group.div(it.h);
+    it.start = e.start;
+    const int rows = e.len + e.pad();
+    it.tile = prefill_tile_of(p, e.blk, rows, rows, 0, e.pad());
+    return it;
+  }
   const int blk = p.div_bh.div(w);
   const int qb = p.num_qblocks - 1 - blk;
   it.bh = w - blk * (int)p.div_bh.d;
   it.b = p.div_hq.div(it.bh);
   it.h = it.bh - it.b * p.Hq;
   it.bh_kv = it.b * p.Hkv + p.div_group.div(it.h);   // g(h) = floor(h / (H/G))
-  it.tile = prefill_tile_of(p, qb);
+  it.start = 0;
+  it.tile = prefill_tile_of(p, qb, p.Sq, p.Skv, p.q_off, 0);
   return it;
 }
 
@@ -217,7 +249,7 @@ __device__ __forceinline__ PrefillItem prefill_item_of(const PrefillParams& p, i
 // only about as fast as the tensor core runs it, so every instruction
 // between two of them is a bubble.  Wait results are made warp-uniform so
 // the warp never diverges.
-template <int DH, int S>
+template <int DH, int S, bool PK>
 __device__ __forceinline__ void prefill_issuer(PrefillSmem<DH>& sm, const PrefillParams& p,
                                                volatile int* abort, int lane) {
   using Cfg = PrefillCfg<DH>;
@@ -252,10 +284,11 @@ __device__ __forceinline__ void prefill_issuer(PrefillSmem<DH>& sm, const Prefil
   int g_base = 0;         // groups of the earlier items
   uint32_t pph = 0, qph = 0;
   bool ok = true;
+  const int num_items = prefill_num_items<PK>(p);
   for (int it = 0; ok; ++it) {
-    const int w = prefill_cta_item(it, p.num_items);
-    if (w >= p.num_items) break;
-    const PrefillTile tile = prefill_item_of(p, w).tile;
+    const int w = prefill_cta_item(it, num_items);
+    if (w >= num_items) break;
+    const PrefillTile tile = prefill_item_of<PK>(p, w).tile;
     const int n_tiles = tile.hi - tile.lo + 1;
     const bool valid = tile.valid(S);
     // the group of this sub-tile's last S, after which its Q buffer is free
@@ -350,7 +383,7 @@ __device__ __forceinline__ void prefill_issuer(PrefillSmem<DH>& sm, const Prefil
 // Q sub-tile 1, then the K/V tiles in order.  A Q sub-tile is reloaded once
 // its issuer's last S MMA of the previous item is done, so the next item's
 // first tiles arrive while the current one finishes.
-template <int DH>
+template <int DH, bool PK>
 __device__ __forceinline__ void prefill_producer(PrefillSmem<DH>& sm, const PrefillParams& p,
                                                  const CUtensorMap* map_q,
                                                  const CUtensorMap* map_k,
@@ -363,22 +396,37 @@ __device__ __forceinline__ void prefill_producer(PrefillSmem<DH>& sm, const Pref
   uint32_t k_loaded = 0, k_par = 0, v_loaded = 0, v_par = 0;
   uint32_t nq0 = 0, nq1 = 0;   // Q loads per sub-tile so far
   bool ok = true;
-  // the grid is no larger than the number of items, so every CTA has a first one
+  // the grid is no larger than the number of items, so every CTA has a first
+  // one; over packed sequences it may have none
   PrefillItem item = first;
+  const int num_items = prefill_num_items<PK>(p);
+  if constexpr (PK) {
+    const int w = prefill_cta_item(0, num_items);
+    ok = w < num_items;
+    if (ok) item = prefill_item_of<PK>(p, w);
+  }
   for (int it = 0; ok; ++it) {
     const PrefillTile& tile = item.tile;
     auto load_q = [&](int s, uint32_t& n) {
       if (n > 0 && !mbar_wait(&sm.q_empty[s], (n - 1) & 1u, abort)) return false;
       // (checked builds: a query row of the chunk and a query head of the batch)
-      const bool in_range = attn_check(tile.row_first(s) >= 0 && tile.row_first(s) < p.Sq &&
-                                           item.bh >= 0 && item.bh < p.B * p.Hq,
+      const bool in_range = attn_check(tile.row_first(s) >= 0 && tile.row_first(s) < tile.Sq &&
+                                           item.bh >= 0 && item.bh < p.B * p.Hq &&
+                                           (!PK ||
+                                            (item.start >= 0 &&
+                                             item.start <= p.pk.T - (tile.Sq - tile.pad))),
                                        p.error_word);
       mbar_arrive_expect_tx(&sm.q_full[s], in_range ? (uint32_t)Cfg::kTileBytes : 0u);
       for (int hf = 0; in_range && hf < Cfg::kHalves; ++hf)
         // Q is read once: evict-first, so that it leaves the K/V tiles the
         // other query blocks of the head re-read in L2
-        tma_load_3d_hint(sm.q[s] + hf * Cfg::kBoxBytes, map_q, &sm.q_full[s], hf * 64,
-                         tile.row_first(s), item.bh, policy_evict_first());
+        if constexpr (PK)
+          packed_load(sm.q[s] + hf * Cfg::kBoxBytes, map_q, &sm.q_full[s], hf * 64, item.start,
+                      tile.pad, tile.row_first(s), item.bh, p.pk.heads_inner & kPackedQ,
+                      policy_evict_first());
+        else
+          tma_load_3d_hint(sm.q[s] + hf * Cfg::kBoxBytes, map_q, &sm.q_full[s], hf * 64,
+                           tile.row_first(s), item.bh, policy_evict_first());
       ++n;
       return true;
     };
@@ -393,8 +441,13 @@ __device__ __forceinline__ void prefill_producer(PrefillSmem<DH>& sm, const Pref
       if (p.fault != 1 || it != 0 || j != tile.lo) {   // (the test hook withholds one tile)
         mbar_arrive_expect_tx(&sm.k_full[kst], bytes);
         for (int hf = 0; in_range && hf < Cfg::kHalves; ++hf)
-          tma_load_3d_hint(sm.k[kst] + hf * Cfg::kBoxBytes, map_k, &sm.k_full[kst], hf * 64,
-                           128 * j, item.bh_kv, keep);
+          if constexpr (PK)
+            packed_load(sm.k[kst] + hf * Cfg::kBoxBytes, map_k, &sm.k_full[kst], hf * 64,
+                        item.start, tile.pad, 128 * j, item.bh_kv,
+                        p.pk.heads_inner & kPackedK, keep);
+          else
+            tma_load_3d_hint(sm.k[kst] + hf * Cfg::kBoxBytes, map_k, &sm.k_full[kst], hf * 64,
+                             128 * j, item.bh_kv, keep);
         k_loaded |= 1u << kst;
         k_par = (k_par & ~(1u << kst)) | (kph << kst);
       }
@@ -405,16 +458,21 @@ __device__ __forceinline__ void prefill_producer(PrefillSmem<DH>& sm, const Pref
       if (!(ok = mbar_wait(&sm.v_empty[vst], vph ^ 1, abort))) break;
       mbar_arrive_expect_tx(&sm.v_full[vst], bytes);
       for (int hf = 0; in_range && hf < Cfg::kHalves; ++hf)
-        tma_load_3d_hint(sm.v[vst] + hf * Cfg::kBoxBytes, map_v, &sm.v_full[vst], hf * 64,
-                         128 * j, item.bh_kv, keep);
+        if constexpr (PK)
+          packed_load(sm.v[vst] + hf * Cfg::kBoxBytes, map_v, &sm.v_full[vst], hf * 64,
+                      item.start, tile.pad, 128 * j, item.bh_kv,
+                      p.pk.heads_inner & kPackedV, keep);
+        else
+          tma_load_3d_hint(sm.v[vst] + hf * Cfg::kBoxBytes, map_v, &sm.v_full[vst], hf * 64,
+                           128 * j, item.bh_kv, keep);
       v_loaded |= 1u << vst;
       v_par = (v_par & ~(1u << vst)) | (vph << vst);
       if (++vst == Cfg::kStagesV) { vst = 0; vph ^= 1; }
     }
     // decode the next item while this one's copies are in flight
-    const int w = prefill_cta_item(it + 1, p.num_items);
-    if (w >= p.num_items) break;
-    item = prefill_item_of(p, w);
+    const int w = prefill_cta_item(it + 1, num_items);
+    if (w >= num_items) break;
+    item = prefill_item_of<PK>(p, w);
   }
   // every copy this thread started has landed before the CTA may exit
   if (nq0 > 0) mbar_wait_drain(&sm.q_full[0], (nq0 - 1) & 1u);
@@ -429,7 +487,7 @@ __device__ __forceinline__ void prefill_producer(PrefillSmem<DH>& sm, const Pref
 // sub-tile (TMEM lane t) in every work item.  Per visible key tile: the
 // online softmax of "Online normalizer calculation for softmax" with a lazy
 // maximum; per item: O / l written straight from registers to global memory.
-template <int DH>
+template <int DH, bool PK>
 __device__ __forceinline__ void prefill_softmax(PrefillSmem<DH>& sm, const PrefillParams& p,
                                                 const CUtensorMap* map_o, uint32_t tbase,
                                                 volatile int* abort, int warp, int lane) {
@@ -443,10 +501,12 @@ __device__ __forceinline__ void prefill_softmax(PrefillSmem<DH>& sm, const Prefi
   const float sl2 = p.scale_log2;
   uint32_t ph = 0;   // bit 0: s_full phase, bit 1: o_final phase
   bool ok = true;
+  const int num_items = prefill_num_items<PK>(p);
   for (int it = 0; ok; ++it) {
-    const int w = prefill_cta_item(it, p.num_items);
-    if (w >= p.num_items) break;
-    const PrefillTile tile = prefill_item_of(p, w).tile;
+    const int w = prefill_cta_item(it, num_items);
+    if (w >= num_items) break;
+    const PrefillItem item = prefill_item_of<PK>(p, w);
+    const PrefillTile& tile = item.tile;
     if (!tile.valid(s)) continue;           // a ragged last block: no rows here
     const int row = tile.pos_first(s) + t;  // this thread's query position
 
@@ -472,7 +532,8 @@ __device__ __forceinline__ void prefill_softmax(PrefillSmem<DH>& sm, const Prefi
         const int kv0 = 128 * j;
         int khi = tile.Skv - 1;
         if (tile.causal) khi = min(khi, row);
-        const int klo = tile.window > 0 ? row - tile.window + 1 : 0;
+        int klo = tile.window > 0 ? row - tile.window + 1 : 0;
+        if (PK) klo = max(klo, tile.pad);
         int clo = klo - kv0;
         const int chi = khi - kv0;
         const uint32_t span = chi >= clo ? (uint32_t)(chi - clo) : 0u;
@@ -581,11 +642,15 @@ __device__ __forceinline__ void prefill_softmax(PrefillSmem<DH>& sm, const Prefi
     ph ^= 2u;
     tc_fence_after_sync();
     const float inv_l = 1.0f / l_run;
-    const int bh = p.div_bh.mod(w);
+    const int bh = PK ? item.bh : p.div_bh.mod(w);
     const int orow = tile.row_first(s) + t;  // output row within the chunk
     // sum_j exp(s_ij) = 2^m_run * l_run (m_run in units of log2)
-    if (p.lse != nullptr && orow < p.Sq)
-      p.lse[(size_t)bh * p.Sq + orow] = (m_run + __log2f(l_run)) * 0.69314718055994531f;
+    if (p.lse != nullptr && orow < tile.Sq && (!PK || orow >= tile.pad))
+      p.lse[PK ? (size_t)bh * p.pk.T + item.start + orow - tile.pad : (size_t)bh * p.Sq + orow] =
+          (m_run + __log2f(l_run)) * 0.69314718055994531f;
+    // PK: a warp whose rows begin with padding stores the others itself
+    const bool mixed = PK && orow - lane < tile.pad;
+    const bool own_row = mixed && orow >= tile.pad;
     const uint32_t stage = smem_u32(sm.ostage[warp]);
 #pragma unroll
     for (int h = 0; h < Cfg::kHalves; ++h) {
@@ -605,6 +670,10 @@ __device__ __forceinline__ void prefill_softmax(PrefillSmem<DH>& sm, const Prefi
         for (int e = 0; e < 4; ++e)
           v[e] = pack_bf16x2(__uint_as_float(x8[2 * e]) * inv_l,
                              __uint_as_float(x8[2 * e + 1]) * inv_l);
+        if (PK && own_row)
+          *reinterpret_cast<uint4*>(p.o + (item.start + orow - tile.pad) * p.o_row +
+                                    bh * p.o_head + 64 * h + 8 * c) =
+              make_uint4(v[0], v[1], v[2], v[3]);
         st_shared_v4(stage + lane * 128 + ((c ^ (lane & 7)) << 4), v[0], v[1], v[2], v[3]);
       }
       fence_proxy_async_smem();
@@ -612,8 +681,14 @@ __device__ __forceinline__ void prefill_softmax(PrefillSmem<DH>& sm, const Prefi
       // rows past the end of the chunk are clipped by the tensor map
       if (lane == 0) {
         // (evict-first: the output is not read again by this kernel)
-        tma_store_3d_hint(map_o, sm.ostage[warp], 64 * h, tile.row_first(s) + 32 * wl, bh,
-                          policy_evict_first());
+        const int row = tile.row_first(s) + 32 * wl;
+        if constexpr (PK) {
+          if (!mixed)
+            packed_store(map_o, sm.ostage[warp], 64 * h, item.start, tile.pad, row, bh,
+                         p.pk.heads_inner & kPackedO, policy_evict_first());
+        } else {
+          tma_store_3d_hint(map_o, sm.ostage[warp], 64 * h, row, bh, policy_evict_first());
+        }
         bulk_commit_group();
       }
     }
@@ -624,7 +699,7 @@ __device__ __forceinline__ void prefill_softmax(PrefillSmem<DH>& sm, const Prefi
   if (lane == 0) bulk_wait_group0();
 }
 
-template <int DH>
+template <int DH, bool PK = false>
 __global__ void __launch_bounds__(384, 1)
     attn_prefill_sm103a(const __grid_constant__ CUtensorMap map_q,
                         const __grid_constant__ CUtensorMap map_k,
@@ -650,7 +725,7 @@ __global__ void __launch_bounds__(384, 1)
     prefetch_tensormap(&map_k);
     prefetch_tensormap(&map_v);
     prefetch_tensormap(&map_o);
-    first = prefill_item_of(p, prefill_cta_item(0, p.num_items));
+    if constexpr (!PK) first = prefill_item_of<PK>(p, prefill_cta_item(0, p.num_items));
   }
   if (threadIdx.x == 0) {
     sm.abort_flag = 0;
@@ -694,16 +769,16 @@ __global__ void __launch_bounds__(384, 1)
     setmaxnreg_dec<Cfg::kRegsControl>();
     if (tbase == 0) {
       if (warp == Cfg::kWarpProducer) {
-        if (lane == 0) prefill_producer<DH>(sm, p, &map_q, &map_k, &map_v, first, abort);
+        if (lane == 0) prefill_producer<DH, PK>(sm, p, &map_q, &map_k, &map_v, first, abort);
       } else if (warp == Cfg::kWarpIssuer0) {
-        prefill_issuer<DH, 0>(sm, p, abort, lane);
+        prefill_issuer<DH, 0, PK>(sm, p, abort, lane);
       } else if (warp == Cfg::kWarpIssuer1) {
-        prefill_issuer<DH, 1>(sm, p, abort, lane);
+        prefill_issuer<DH, 1, PK>(sm, p, abort, lane);
       }
     }
   } else {
     setmaxnreg_inc<Cfg::kRegsSoftmax>();
-    if (tbase == 0) prefill_softmax<DH>(sm, p, &map_o, tbase, abort, warp, lane);
+    if (tbase == 0) prefill_softmax<DH, PK>(sm, p, &map_o, tbase, abort, warp, lane);
   }
 
   // ---- teardown (every thread gets here; all waits above are bounded)

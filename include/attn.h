@@ -386,6 +386,167 @@ int attn_cache_evict(void* kpages, void* vpages, float* weights, int weights_str
                      int page, int cols, int Dh, cudaStream_t stream);
 
 /*
+ * Packed sequences.  A batch of sequences of different lengths lies one behind
+ * another, without padding: tokens are rows of [T, H, Dh], and sequence b holds
+ * rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (device, int32, [B + 1],
+ * ascending within [0, T]; a length of 0 is an empty place).  Rows of no
+ * sequence (ahead of the first, behind the last) are neither used, whatever
+ * they hold, nor written.  Tensors come at any strides of whole 16 bytes, so
+ * that a projection's output [T, Hq + 2 Hkv, Dh] is taken as it lies, and
+ * heads-first tensors [H, T, Dh] too:
+ */
+typedef struct {
+  void* data;             /* device, bf16, 16-byte aligned (inputs are only read) */
+  /* elements (multiples of 8) between batches, rows and heads; an axis of one
+     entry has any.  The packed calls have no batch axis.  The Dh values of a
+     head lie side by side. */
+  long long batch_stride, row_stride, head_stride;
+} attn_rows_t;
+/*
+ * In the packed calls below:
+ *   - Strides are at least Dh.  The elements of an output are distinct, and
+ *     apart from every other tensor's (ATTN_ERR_INVALID_ARG otherwise);
+ *     tensors between one another (slices of one wider tensor along its heads)
+ *     are apart.
+ *   - Offsets that are not ascending within [0, T] latch ATTN_ERR_INVALID_ARG
+ *     for attn_status(), and nothing is written.
+ *   - workspace: device, 256-byte aligned, of at least the bytes that the
+ *     query gives (ATTN_ERR_SCRATCH_LIMIT otherwise).  Its contents need not be
+ *     kept; calls that may overlap on the GPU need one each.  The library keeps
+ *     none, so the calls may run on several streams at the same time and in
+ *     several captured graphs.
+ *   - No sequence's result depends on another's rows, infinities and NaN
+ *     included.  Within a sequence an infinity or NaN in K or V can reach the
+ *     rows of its 128-row block that the mask hides it from, as in attn_fwd.
+ *   - The same inputs give the same bits.
+ *   - B == 0 or T == 0 is a no-op.
+ */
+
+/*
+ * attn_fwd_packed -- attn_fwd of every sequence: row i of a sequence sees its
+ * own rows j <= i (causal = 1; i - j < window where a window is given) or all
+ * of them (causal = 0).
+ *   q, o  [T, Hq, Dh],  k, v  [T, Hkv, Dh]
+ *   lse   [Hq, T]  (device, fp32, written) or NULL: as in attn_fwd_lse
+ * Work is listed on the GPU, so the call reads no lengths on the host.
+ */
+int attn_fwd_packed(const attn_rows_t* q, const attn_rows_t* k, const attn_rows_t* v,
+                    const attn_rows_t* o, float* lse, const int* cu_seqlens, void* workspace,
+                    size_t workspace_bytes, int B, int Hq, int Hkv, int T, int Dh, int causal,
+                    int window, float scale, cudaStream_t stream);
+
+/* The workspace of an attn_fwd_packed call, in bytes. */
+int attn_fwd_packed_workspace(int B, int T, size_t* bytes);
+
+/*
+ * attn_bwd_packed -- attn_bwd of every sequence: dq [T, Hq, Dh], dk and dv
+ * [T, Hkv, Dh] (summed over the query heads of each group) from q, k, v, the
+ * o and lse that attn_fwd_packed gave for them, and dout = dL/do.
+ */
+int attn_bwd_packed(const attn_rows_t* q, const attn_rows_t* k, const attn_rows_t* v,
+                    const attn_rows_t* o, const attn_rows_t* dout, const float* lse,
+                    const attn_rows_t* dq, const attn_rows_t* dk, const attn_rows_t* dv,
+                    const int* cu_seqlens, void* workspace, size_t workspace_bytes, int B, int Hq,
+                    int Hkv, int T, int Dh, int causal, int window, float scale,
+                    cudaStream_t stream);
+
+/* The workspace of an attn_bwd_packed call, in bytes. */
+int attn_bwd_packed_workspace(int B, int Hq, int T, size_t* bytes);
+
+/*
+ * attn_rope -- rotary positions.  Of each head of q and k the first rotary_dim
+ * values (a multiple of 16, at most Dh; 0: none) are turned in pairs: at
+ * position p, pair i by the angle 2 pi p turns[i] / 2^64,
+ *     (x, y) -> amplitude (x cos - y sin, y cos + x sin).
+ *   interleaved = 0: pair i is values i and i + rotary_dim / 2;
+ *   interleaved = 1: values 2 i and 2 i + 1.
+ *   q, q_out  [B, S, Hq, Dh], k, k_out  [B, S, Hkv, Dh], each at its own
+ *         strides: packed tokens with B = 1, heads-first batches
+ *         [B, H, S, Dh] as they lie.  An output is its input or apart from
+ *         every tensor.  Inputs may have strides of 0.  Hq or Hkv may be 0.
+ *   positions  [B, S]  (device, int32); a negative one leaves the row out:
+ *         nothing of it is written
+ *   turns  [rotary_dim / 2]  (device, 64-bit, 8-byte aligned): turns per token
+ *         in units of 2^-64, as attn_rope_frequencies makes them.  p turns[i]
+ *         is reduced to one turn exactly, whatever the position.
+ *   inverse = 1: the other way, as a gradient goes back (with the same
+ *         amplitude)
+ * The turned values are computed in fp32 and rounded once.
+ */
+int attn_rope(const attn_rows_t* q, const attn_rows_t* q_out, int Hq, const attn_rows_t* k,
+              const attn_rows_t* k_out, int Hkv, const int* positions,
+              const unsigned long long* turns, float amplitude, int B, int S, int Dh,
+              int rotary_dim, int interleaved, int inverse, cudaStream_t stream);
+
+/*
+ * attn_rope_append -- attn_rope, and the write to a paged cache in the same
+ * pass: the turned k and v [B, S, Hkv, Dh] of row r go to row slots[r] % page
+ * of page slots[r] / page of the pools (see above; any page size that is a
+ * multiple of 8).
+ *   slots  [B, S]  (device, int32): attn_cache_plan gives them; a negative one
+ *         writes nothing to the cache, one of num_pages * page or more latches
+ *         ATTN_ERR_INVALID_ARG and writes nothing there either.  Two rows have
+ *         one slot in no call.
+ *   k_out  NULL: the turned keys go to the cache alone
+ * A row with a negative position is left out altogether.
+ */
+int attn_rope_append(const attn_rows_t* q, const attn_rows_t* q_out, int Hq, const attn_rows_t* k,
+                     const attn_rows_t* k_out, const attn_rows_t* v, int Hkv, const int* positions,
+                     const unsigned long long* turns, float amplitude, void* kpages, void* vpages,
+                     const int* slots, int num_pages, int page, int B, int S, int Dh,
+                     int rotary_dim, int interleaved, cudaStream_t stream);
+
+/*
+ * attn_rope_frequencies -- turns per token of each pair, and the amplitude:
+ * f_i = base^(-2 i / rotary_dim) / (2 pi), for longer contexts scaled by
+ *   ATTN_ROPE_LINEAR  f_i / factor (positions pressed together);
+ *   ATTN_ROPE_BASE    base * factor^(rotary_dim / (rotary_dim - 2)) for base;
+ *   ATTN_ROPE_TURNS   by the turns r = original_len f_i that a pair makes over
+ *                     the context it was trained on: f_i from r = high on,
+ *                     f_i / factor up to r = low, linear in r between them;
+ *   ATTN_ROPE_YARN    the same, with amplitude 0.1 ln(factor) + 1.
+ * A host call: turns [rotary_dim / 2] and amplitude are host memory.
+ */
+enum { ATTN_ROPE_NONE = 0, ATTN_ROPE_LINEAR, ATTN_ROPE_BASE, ATTN_ROPE_TURNS, ATTN_ROPE_YARN };
+int attn_rope_frequencies(unsigned long long* turns, float* amplitude, int rotary_dim, double base,
+                          int scaling, double factor, double low, double high,
+                          double original_len);
+
+/*
+ * attn_cache_plan -- the pages, slots and positions of a serving step, made on
+ * the GPU from the lengths alone (no length is read on the host).  Sequence b
+ * of a paged cache holds seqlens[b] rows and changes by delta[b]: so many new
+ * tokens, or (negative) rows taken back from its end.
+ *   1. Pages that no row needs any more go onto the stack of free pages, by
+ *      sequence, then by column.
+ *   2. Pages that new rows need come off its top, in the same order, into the
+ *      table.
+ *   3. The new tokens of all sequences, packed in their order, get their
+ *      position and their slot (page number * page + row in the page).
+ *   delta, seqlens     [B]           (device, int32, read)
+ *   seqlens_out        [B]           written: seqlens + delta; may be seqlens
+ *   table              [B, cols]     columns that a sequence gains are written
+ *   free_pages         [capacity]    the stack; its first *num_free entries are
+ *                                    free pages, entries that it gains are written
+ *   num_free, num_free_out  [1]      its height before and after; may be the same
+ *   cu_seqlens         [B + 1]       written: first packed row of each
+ *                                    sequence's new tokens, then their number
+ *   positions, slots   [T]           written: for each packed row, then -1
+ * (all device, int32).  All or nothing: where there are more than T new tokens
+ * or the stack would pass capacity (ATTN_ERR_INVALID_ARG), or free pages do
+ * not suffice (ATTN_ERR_NO_MEMORY, both latched for attn_status()), lengths,
+ * table and stack stay as they were, cu_seqlens is all 0 and the rest -1.  A
+ * length outside [0, cols * page], before or after, latches
+ * ATTN_ERR_INVALID_ARG and leaves that sequence as it is.  A used page number
+ * outside [0, num_pages) latches it too and gives slots of -1.
+ * Up to 8192 sequences (ATTN_ERR_UNSUPPORTED).  B == 0 is a no-op.
+ */
+int attn_cache_plan(const int* delta, const int* seqlens, int* seqlens_out, int* table,
+                    int* free_pages, const int* num_free, int* num_free_out, int* cu_seqlens,
+                    int* positions, int* slots, int B, int cols, int page, int num_pages,
+                    int capacity, int T, cudaStream_t stream);
+
+/*
  * attn_status -- synchronise `stream`, then return (and clear) the current
  * device's latched error word: ATTN_OK, ATTN_ERR_TIMEOUT, ATTN_ERR_INVALID_ARG,
  * or ATTN_ERR_CUDA if the synchronisation itself failed (or a prefill kernel

@@ -1,0 +1,241 @@
+"""Attention over packed sequences on the GPU, against the 64-bit reference."""
+import pytest
+import torch
+
+import causal_head_self_gb300 as chs
+import packed_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+LENS = {
+    "one": [1],
+    "edges": [1, 2, 127, 128, 129, 0, 255, 256, 257, 1, 0],
+    "ragged": [300, 7, 1023, 64, 65, 511],
+    "long": [2100, 33, 1700],
+}
+HEADS = [(4, 2), (3, 3), (6, 1), (8, 2)]
+AHEAD, BEHIND = 5, 9
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def case(lens, Hq, Hkv, Dh, kind="fused", seed=0):
+    """Inputs whose rows of no sequence are NaN, outputs of another value."""
+    gen = torch.Generator("cuda").manual_seed(seed)
+    cu = ref.offsets(lens, AHEAD)
+    T = cu[-1] + BEHIND
+    q, k, v = ref.layouts(T, Hq, Hkv, Dh, kind, gen)
+    dout = ref.layouts(T, Hq, Hkv, Dh, kind, gen)[0]
+    for x in (q, k, v, dout):
+        x[:AHEAD] = x[cu[-1]:] = float("nan")
+    return q, k, v, dout, cu, T
+
+
+def outside_is(x, value, cu, rows=0):
+    x = x.transpose(0, rows)
+    return bool((x[:cu[0]] == value).all()) and bool((x[cu[-1]:] == value).all())
+
+
+def run(q, k, v, dout, cu, causal, window, scale=0.0, kind="fused"):
+    T, Hq, Dh = q.shape
+    Hkv = k.shape[1]
+    o, lse = torch.full_like(q, 7), torch.full((Hq, T), 7.0, device="cuda")
+    if kind == "fused":
+        dx = torch.full((T, Hq + 2 * Hkv, Dh), 7, dtype=torch.bfloat16, device="cuda")
+        grads = dx[:, :Hq], dx[:, Hq:Hq + Hkv], dx[:, Hq + Hkv:]
+    else:
+        grads = torch.full_like(q, 7), torch.full_like(k, 7), torch.full_like(v, 7)
+    mask = dict(causal=causal, window=window, scale=scale)
+    assert chs.attn_fwd_packed(q, k, v, i32(cu), o, lse, **mask) is o
+    chs.attn_bwd_packed(q, k, v, o, dout, lse, i32(cu), *grads, **mask)
+    assert chs.attn_status() == chs.ATTN_OK
+    return o, lse, grads
+
+
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 100)])
+@pytest.mark.parametrize("lens", LENS)
+@pytest.mark.parametrize("Dh", [64, 128, 256])
+def test_forward_and_gradients(Dh, lens, causal, window):
+    Hq, Hkv = HEADS[(len(lens) + Dh // 64) % len(HEADS)]
+    kind = ["fused", "heads_first", "contiguous", "wide"][(len(LENS[lens]) + Dh // 64) % 4]
+    q, k, v, dout, cu, T = case(LENS[lens], Hq, Hkv, Dh, kind)
+    o, lse, grads = run(q, k, v, dout, cu, causal, window, kind=kind)
+    real = slice(cu[0], cu[-1])
+    want, L, bound, dwant, dbound = ref.attention(q, k, v, cu, causal, window, dout=dout)
+    ref.check(o[real], want[real], bound[real], "o")
+    # (a relative error of every weight's is an absolute one of the logarithm)
+    assert float((lse[:, real] - L[:, real]).abs().max()) < ref.F
+    for name, got, w, b in zip(("dq", "dk", "dv"), grads, dwant, dbound):
+        ref.check(got[real], w[real], b[real], name)
+    assert all(outside_is(x, 7, cu) for x in (o, *grads)) and outside_is(lse, 7, cu, 1)
+
+
+@pytest.mark.parametrize("kind", ["fused", "heads_first", "contiguous", "wide"])
+@pytest.mark.parametrize("Dh", [64, 128, 256])
+def test_strides(Dh, kind):
+    q, k, v, dout, cu, T = case([130, 1, 258], 4, 2, Dh, kind, seed=3)
+    o, lse, grads = run(q, k, v, dout, cu, True, 0, kind=kind)
+    same = [x.contiguous() for x in (q, k, v, dout)]
+    o2, lse2, grads2 = run(*same, cu, True, 0, kind="contiguous")
+    assert torch.equal(o.contiguous(), o2) and torch.equal(lse, lse2)
+    assert all(torch.equal(a.contiguous(), b) for a, b in zip(grads, grads2))
+
+
+@pytest.mark.parametrize("Dh,n", [(64, 768), (128, 768), (128, 2560), (256, 768)])
+def test_one_sequence_is_the_batch_form(Dh, n):
+    # whole blocks: the same kernels over the same tiles, so the same bits
+    gen = torch.Generator("cuda").manual_seed(5)
+    q, k, v = ref.layouts(n, 8, 2, Dh, "heads_first", gen)
+    dout = ref.layouts(n, 8, 2, Dh, "heads_first", gen)[0]
+    lse = torch.zeros(8, n, device="cuda")
+    o = chs.attn_fwd_packed(q, k, v, i32([0, n]), None, lse, window=333)
+    grads = chs.attn_bwd_packed(q, k, v, o, dout, lse, i32([0, n]), window=333)
+    batch = [x.transpose(0, 1)[None].contiguous() for x in (q, k, v, dout)]
+    o2, lse2 = chs.attn_fwd_lse(*batch[:3], window=333)
+    grads2 = chs.attn_bwd(*batch[:3], o2, batch[3], lse2, window=333)
+    assert chs.attn_status() == chs.ATTN_OK
+    assert torch.equal(o.transpose(0, 1)[None], o2) and torch.equal(lse[None], lse2)
+    assert all(torch.equal(a.transpose(0, 1)[None], b) for a, b in zip(grads, grads2))
+
+
+@pytest.mark.parametrize("Dh", [64, 128, 256])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_sequence_keeps_to_itself(Dh, value):
+    lens = [100, 30, 200, 1, 129, 127]
+    q, k, v, dout, cu, T = case(lens, 4, 2, Dh)
+    o, lse, grads = run(q, k, v, dout, cu, True, 0)
+    for b in (1, 3, 4):
+        for x in (q, k, v, dout):
+            x[cu[b]:cu[b + 1]] = value
+    o2, lse2, grads2 = run(q, k, v, dout, cu, True, 0)
+    for b in (0, 2, 5):
+        rows = slice(cu[b], cu[b + 1])
+        assert torch.equal(o[rows], o2[rows]) and torch.equal(lse[:, rows], lse2[:, rows])
+        assert all(torch.equal(x[rows], y[rows]) for x, y in zip(grads, grads2))
+
+
+@pytest.mark.parametrize("Dh", [64, 128, 256])
+def test_many_sequences(Dh):
+    # more sequences than the listing has warps, more tiles than SMs
+    gen = torch.Generator().manual_seed(1)
+    lens = torch.randint(0, 40, (1500,), generator=gen).tolist()
+    q, k, v, dout, cu, T = case(lens, 2, 1, Dh, "contiguous")
+    o, lse, grads = run(q, k, v, dout, cu, True, 0, kind="contiguous")
+    real = slice(cu[0], cu[-1])
+    want, L, bound, dwant, dbound = ref.attention(q, k, v, cu, dout=dout)
+    ref.check(o[real], want[real], bound[real], "o")
+    for name, got, w, b in zip(("dq", "dk", "dv"), grads, dwant, dbound):
+        ref.check(got[real], w[real], b[real], name)
+
+
+def test_gradients_against_differences():
+    # a step of the loss sum(o * dout) along a direction; 64-bit reference at both ends
+    q, k, v, dout, cu, T = case([70, 130], 4, 2, 64, "contiguous", seed=9)
+    for x in (q, k, v, dout):
+        x[:AHEAD] = x[cu[-1]:] = 0
+    o, lse, grads = run(q, k, v, dout, cu, True, 50, kind="contiguous")
+    gen = torch.Generator("cuda").manual_seed(2)
+    real = slice(cu[0], cu[-1])
+    bounds = ref.attention(q, k, v, cu, True, 50, dout=dout)[4]
+    for i, g in enumerate(grads):
+        step = torch.randn(g.shape, generator=gen, device="cuda", dtype=torch.float64)
+        ends = []
+        for sign in (1, -1):
+            x = [t.double() for t in (q, k, v)]
+            x[i] = x[i] + sign * 1e-5 * step
+            y = ref.attention(*x, cu, True, 50)[0]
+            ends.append(float((y * dout.double()).sum()))
+        slope = (ends[0] - ends[1]) / 2e-5
+        got = float((g.double() * step)[real].sum())
+        # the gradient's own bound along the direction, and the difference's cubic term
+        assert abs(got - slope) <= float((bounds[i] * step.abs()).sum()) + 1e-4 * abs(slope)
+
+
+def test_no_rows_and_no_sequences():
+    x = torch.full((0, 4, 64), 1.0, dtype=torch.bfloat16, device="cuda")
+    assert chs.attn_fwd_packed(x, x, x, i32([0, 0])).shape == (0, 4, 64)
+    y = torch.ones(6, 4, 64, dtype=torch.bfloat16, device="cuda")
+    o = torch.full_like(y, 7)
+    chs.attn_fwd_packed(y, y, y, i32([0]), o)
+    assert bool((o == 7).all())
+    chs.attn_fwd_packed(y, y, y, i32([3, 3, 3]), o)
+    assert bool((o == 7).all()) and chs.attn_status() == chs.ATTN_OK
+
+
+@pytest.mark.parametrize("cu", [[0, 9, 5, 12], [-1, 4, 8, 12], [0, 4, 8, 13], [3, 2, 8, 12]])
+def test_unsound_offsets_write_nothing(cu):
+    gen = torch.Generator("cuda").manual_seed(0)
+    q, k, v = ref.layouts(12, 4, 2, 128, "fused", gen)
+    dout = torch.ones(12, 4, 128, dtype=torch.bfloat16, device="cuda")
+    o, lse = torch.full_like(dout, 7), torch.full((4, 12), 7.0, device="cuda")
+    chs.attn_fwd_packed(q, k, v, i32(cu), o, lse)
+    assert chs.attn_status() == chs.ATTN_ERR_INVALID_ARG
+    grads = [torch.full_like(x, 7) for x in (q, k, v)]
+    chs.attn_bwd_packed(q, k, v, dout, dout, lse, i32(cu), *grads)
+    assert chs.attn_status() == chs.ATTN_ERR_INVALID_ARG
+    assert all(bool((x == 7).all()) for x in (o, lse, *grads))
+
+
+def test_captured_calls_follow_new_offsets():
+    gen = torch.Generator("cuda").manual_seed(4)
+    T, Hq, Hkv, Dh = 1500, 4, 2, 128
+    q, k, v = ref.layouts(T, Hq, Hkv, Dh, "fused", gen)
+    dout = ref.layouts(T, Hq, Hkv, Dh, "contiguous", gen)[0]
+    cu = i32([0, 700, 700, 1500])
+    o, lse = torch.zeros(T, Hq, Dh, dtype=torch.bfloat16, device="cuda"), torch.zeros(Hq, T, device="cuda")
+    grads = [torch.zeros_like(x) for x in (dout, k, v)]
+    grads = [x.contiguous() for x in grads]
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+
+    def step():
+        chs.attn_fwd_packed(q, k, v, cu, o, lse)
+        chs.attn_bwd_packed(q, k, v, o, dout, lse, cu, *grads)
+    with torch.cuda.stream(stream):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        step()
+    for offsets in ([0, 1, 64, 1500], [10, 400, 1100, 1400]):
+        cu.copy_(i32(offsets))
+        for x in (o, *grads):
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in (o, *grads)]
+        want, _, bound, dwant, dbound = ref.attention(q, k, v, offsets, dout=dout)
+        for a, b, c in zip(got, (want, *dwant), (bound, *dbound)):
+            ref.check(a, b, c)
+    assert chs.attn_status() == chs.ATTN_OK
+
+
+def test_two_streams_at_once():
+    gen = torch.Generator("cuda").manual_seed(6)
+    sets = []
+    for lens in ([900, 5, 300], [64, 2000]):
+        cu = ref.offsets(lens)
+        q, k, v = ref.layouts(cu[-1], 8, 2, 128, "fused", gen)
+        sets.append((q, k, v, ref.layouts(cu[-1], 8, 2, 128, "contiguous", gen)[0], i32(cu)))
+
+    def both(s, stream=None):
+        q, k, v, dout, cu = s
+        lse = torch.zeros(8, q.shape[0], device="cuda")
+        o = torch.zeros_like(dout)
+        grads = [torch.zeros_like(x) for x in (q, k, v)]
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        for _ in range(4):
+            chs.attn_fwd_packed(q, k, v, cu, o, lse, stream=stream)
+            chs.attn_bwd_packed(q, k, v, o, dout, lse, cu, *grads, stream=stream)
+        return (o, lse, *grads)
+    alone = [both(s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    at_once = [both(s, x) for s, x in zip(sets, streams)]
+    torch.cuda.synchronize()
+    assert chs.attn_status() == chs.ATTN_OK
+    for a, b in zip(alone, at_once):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
