@@ -836,8 +836,9 @@ def attn_cache_plan(delta, seqlens, table, free_pages, num_free, *, rows, page, 
     onto it, then pages that new rows need come off it, into table.  Lengths
     and num_free change in place (or go to seqlens_out, num_free_out).  Returns
     (cu_seqlens [B+1], positions [rows], slots [rows]) of the packed new tokens,
-    -1 behind the last; where they are more than `rows`, or pages do not
-    suffice, nothing changes and attn_status() says so.  All int32."""
+    -1 behind the last (cu_seqlens[B] of them, the first `rows` of which have
+    their place here); where pages do not suffice, nothing changes and
+    attn_status() says so.  All int32."""
     rows, page = _int32("rows", rows), _int32("page", page)
     num_pages = _int32("num_pages", num_pages)
     B, cols = shape = _shape("table", table, 2)

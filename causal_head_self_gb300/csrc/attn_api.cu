@@ -1010,7 +1010,7 @@ extern "C" int attn_rope_frequencies(unsigned long long* turns, float* amplitude
       const double keep = std::fmin(1.0, std::fmax(0.0, (original_len * f - low) / (high - low)));
       f *= keep + (1.0 - keep) / factor;
     }
-    turns[i] = (unsigned long long)std::ldexp(f, 64);
+    turns[i] = (unsigned long long)std::rint(std::ldexp(f, 64));
   }
   *amplitude = scaling == ATTN_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
   return ATTN_OK;

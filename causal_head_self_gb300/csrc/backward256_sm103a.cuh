@@ -70,6 +70,11 @@ __host__ __device__ constexpr uint32_t bwd256_packed_col(int kk) {
   return (uint32_t)(32 * (16 * kk / 32) + (16 * kk % 32) / 2);
 }
 
+// PK: the low parts of P or dS (backward_sm103a.cuh) lie behind the high ones.
+__host__ __device__ constexpr uint32_t bwd256_low_col(int kk) {
+  return bwd256_packed_col(kk) + Bwd256Cfg::kCols / 2;
+}
+
 // 64-row query blocks [lo, hi] that see some key of 128-key block kb.
 __device__ __forceinline__ void bwd256_qblocks_of(const BwdParams& p, const BwdSeq& q, int kb,
                                                   int& lo, int& hi) {
@@ -245,11 +250,16 @@ __device__ __forceinline__ void bwd256_kv_issuer(Bwd256KvSmem<DK>& sm, const Bwd
     }
   };
   // Acc (128 x 256) (+)= A (tensor memory, 128 x 64 bf16 pairs) B (64 x 256, MN-major)
-  auto mma_acc = [&](uint32_t a, uint64_t b, bool first) {
+  auto mma_acc = [&](uint32_t a, uint64_t b, bool first, bool two) {
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
       mma_bf16_ts_warp(Cfg::kColAcc, a + bwd256_packed_col(kk), b + kk * (2048 >> 4), idesc_acc,
                        (!first || kk > 0) ? 1u : 0u);
+    if (PK && two) {
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma_bf16_ts_warp(Cfg::kColAcc, a + bwd256_low_col(kk), b + kk * (2048 >> 4), idesc_acc, 1u);
+    }
   };
   auto wait_all = [&](uint64_t* bar, uint32_t ph) -> bool {
     return __all_sync(0xffffffffu, mbar_wait(bar, ph, abort));
@@ -316,7 +326,10 @@ __device__ __forceinline__ void bwd256_kv_issuer(Bwd256KvSmem<DK>& sm, const Bwd
     ++items;
     if (!(ok = issue_scores(u))) break;
     if (N == 1) mma_commit_warp(k_done);
+    int qb = I.lo;   // step n's query block (of one head after another)
     for (int n = 0; n < N; ++n, ++u) {
+      const bool two = bwd_two_parts<PK>(qb / 2);
+      if (PK) qb = qb == I.hi ? I.lo : qb + 1;
       if (n + 1 < N) {
         if (!(ok = issue_scores(u + 1))) break;
         if (n + 2 == N) mma_commit_warp(k_done);   // the item's last read of K (and V)
@@ -324,13 +337,13 @@ __device__ __forceinline__ void bwd256_kv_issuer(Bwd256KvSmem<DK>& sm, const Bwd
       if (DK) {
         if (!(ok = wait_all(&sm.ds_full[u & 1u], (u >> 1) & 1u))) break;
         tc_fence_after_sync();
-        mma_acc(Cfg::kColDP + 64 * (u & 1u), dq_mn + qst(u) * kStage, n == 0);   // dK += dS^T Q
+        mma_acc(Cfg::kColDP + 64 * (u & 1u), dq_mn + qst(u) * kStage, n == 0, two);   // dK += dS^T Q
         mma_commit_warp(&sm.q_empty[qst(u)]);
       } else {
         if (!(ok = wait_all(&sm.p_full[u & 1u], (u >> 1) & 1u))) break;
         if (!(ok = wait_all(&sm.do_full[dst(u)], dph(u)))) break;
         tc_fence_after_sync();
-        mma_acc(Cfg::kColS + 64 * (u & 1u), ddo_mn + dst(u) * kStage, n == 0);   // dV += P^T dO
+        mma_acc(Cfg::kColS + 64 * (u & 1u), ddo_mn + dst(u) * kStage, n == 0, two);   // dV += P^T dO
         mma_commit_warp(&sm.do_empty[dst(u)]);
       }
     }
@@ -411,8 +424,17 @@ __device__ __forceinline__ void bwd256_kv_softmax(Bwd256KvSmem<DK>& sm, const Bw
             w16[e] = pack_bf16x2(a, c);
           }
         }
+        const bool two = bwd_two_parts<PK>(qb / 2);
+        auto low = [&](uint32_t to) {   // the low parts of pf's pairs
+          uint32_t l16[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            l16[e] = bwd_low_pair(pf[2 * e], pf[2 * e + 1], pack_bf16x2(pf[2 * e], pf[2 * e + 1]));
+          tmem_st_32x32b_x16(to + Cfg::kCols / 2, l16);
+        };
         if (!DK) {
           tmem_st_32x32b_x16(colS, w16);   // P^T pairs over this warpgroup's S^T columns
+          if (PK && two) low(colS);
           tmem_st_wait();
           tc_fence_before_sync();
           mbar_arrive(&sm.p_full[b]);
@@ -435,9 +457,14 @@ __device__ __forceinline__ void bwd256_kv_softmax(Bwd256KvSmem<DK>& sm, const Bw
                 h ? make_float2(-d.z, -d.w) : make_float2(-d.x, -d.y));
             const float2 dsv = __fmul2_rn(make_float2(pf[col], pf[col + 1]), dd);
             w16[e] = pack_bf16x2(dsv.x, dsv.y);
+            if (PK) {   // (the weights are not needed any more)
+              pf[col] = dsv.x;
+              pf[col + 1] = dsv.y;
+            }
           }
         }
         tmem_st_32x32b_x16(colDP, w16);   // dS^T pairs over this warpgroup's dP^T columns
+        if (PK && two) low(colDP);
         tmem_st_wait();
         tc_fence_before_sync();
         mbar_arrive(&sm.ds_full[b]);
@@ -743,6 +770,12 @@ __device__ __forceinline__ void bwd256_dq_issuer(Bwd256QSmem& sm, const BwdParam
         mma_bf16_ts_warp(Cfg::kColAcc, Cfg::kColDP + 64 * (u & 1u) + bwd256_packed_col(kk),
                          dk_mn + kst(u) * kStage + kk * (2048 >> 4), idesc_acc,
                          (n > 0 || kk > 0) ? 1u : 0u);
+      if (PK && bwd_two_parts<PK>(I.qb)) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_bf16_ts_warp(Cfg::kColAcc, Cfg::kColDP + 64 * (u & 1u) + bwd256_low_col(kk),
+                           dk_mn + kst(u) * kStage + kk * (2048 >> 4), idesc_acc, 1u);
+      }
       mma_commit_warp(&sm.k_empty[kst(u)]);
     }
     if (ok) mma_commit_warp(&sm.acc_final);
@@ -826,8 +859,18 @@ __device__ __forceinline__ void bwd256_dq_softmax(Bwd256QSmem& sm, const BwdPara
             make_float2(__uint_as_float(y[col]), __uint_as_float(y[col + 1])), negD);
         const float2 dsv = __fmul2_rn(make_float2(pf[col], pf[col + 1]), dd);
         w16[e] = pack_bf16x2(dsv.x, dsv.y);
+        if (PK) {
+          pf[col] = dsv.x;
+          pf[col + 1] = dsv.y;
+        }
       }
       tmem_st_32x32b_x16(colDP, w16);
+      if (PK && bwd_two_parts<PK>(I.qb)) {   // (as in the dV and dK passes)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          w16[e] = bwd_low_pair(pf[2 * e], pf[2 * e + 1], w16[e]);
+        tmem_st_32x32b_x16(colDP + Cfg::kCols / 2, w16);
+      }
       tmem_st_wait();
       tc_fence_before_sync();
       mbar_arrive(&sm.ds_full[b]);

@@ -42,7 +42,14 @@
 // rows, keys and place come from the lists of tiles (one heaviest first for
 // each pass) instead of the launch's shape; rows are counted with the
 // sequence's padding in front, for lse2 and D too.  Padded queries have
-// lse2 = +inf and so weigh nothing; padded keys are masked.
+// lse2 = +inf and so weigh nothing; padded keys are masked.  In a batch of
+// short sequences few keys share a query's weight, each term of a gradient's
+// sum is large, and so is what the terms' rounding to bf16 leaves: twice the
+// final rounding's error in squares.  P and dS of a sequence's first two query
+// blocks (where most of the gradients' size lies in long sequences too) enter
+// the products as two bf16 parts, hi + lo, 2^-16 of each: two more products for
+// those blocks.  (dQ of 24 documents of 16 to 2048 rows: 1.5 times the error of
+// a single rounding of the result before, KKKK times with it.)
 #pragma once
 
 #include <cstdint>
@@ -167,6 +174,22 @@ struct BwdCfg {
 __host__ __device__ constexpr uint32_t bwd_packed_col(int kk) {
   constexpr int cols = BwdCfg<64>::kCols;
   return (uint32_t)(cols * (16 * kk / cols) + (16 * kk % cols) / 2);
+}
+
+// PK: the low parts of columns 16 kk .. (see above) lie behind their high
+// parts, in the other half of each warpgroup's columns.
+__host__ __device__ constexpr uint32_t bwd_low_col(int kk) {
+  return bwd_packed_col(kk) + BwdCfg<64>::kCols / 2;
+}
+
+// PK: do P and dS of these query blocks (of 128 rows) enter the products in two parts?
+constexpr int kBwdExactBlocks = 2;
+template <bool PK>
+__device__ __forceinline__ bool bwd_two_parts(int qb) { return PK && qb < kBwdExactBlocks; }
+
+// What bf16 leaves of (a, b), whose rounded pair is `hi`, as a pair.
+__device__ __forceinline__ uint32_t bwd_low_pair(float a, float b, uint32_t hi) {
+  return pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
 }
 
 // D_i = sum_d dO[i, d] o[i, d] (fp32 products of the bf16 values) and
@@ -496,11 +519,16 @@ __device__ __forceinline__ void bwd_dkdv_issuer(BwdKvSmem<DH>& sm, const BwdPara
   };
   // D (128 x DH) (+)= A (tensor memory, 128 x 128 bf16 pairs at bwd_packed_col) B,
   // B MN-major (DH contiguous)
-  auto mma_acc = [&](uint32_t d, uint32_t a, uint64_t b, bool first) {
+  auto mma_acc = [&](uint32_t d, uint32_t a, uint64_t b, bool first, bool two) {
 #pragma unroll
     for (int kk = 0; kk < 128 / 16; ++kk)
       mma_bf16_ts_warp(d, a + bwd_packed_col(kk), b + kk * (2048 >> 4), idesc_acc,
                        (!first || kk > 0) ? 1u : 0u);
+    if (PK && two) {
+#pragma unroll
+      for (int kk = 0; kk < 128 / 16; ++kk)
+        mma_bf16_ts_warp(d, a + bwd_low_col(kk), b + kk * (2048 >> 4), idesc_acc, 1u);
+    }
   };
   auto wait_all = [&](uint64_t* bar, uint32_t ph) -> bool {
     return __all_sync(0xffffffffu, mbar_wait(bar, ph, abort));
@@ -523,11 +551,14 @@ __device__ __forceinline__ void bwd_dkdv_issuer(BwdKvSmem<DH>& sm, const BwdPara
     mma_nt(Cfg::kColDP, dv_, ddo_k + (u & 1u) * kStage);
     mma_commit_warp(&sm.dp_full);
     if (N == 1) mma_commit_warp(&sm.kv_empty);
+    int qb = I.lo;   // step n's query block (of one head after another)
     for (int n = 0; n < N; ++n, ++u) {
       const uint64_t st = u & 1u, st1 = (u + 1) & 1u;
+      const bool two = bwd_two_parts<PK>(qb);
+      if (PK) qb = qb == I.hi ? I.lo : qb + 1;
       if (!(ok = wait_all(&sm.p_full, u & 1u))) break;
       tc_fence_after_sync();
-      mma_acc(Cfg::kColA0, Cfg::kColS, ddo_mn + st * kStage, n == 0);   // dV += P^T dO
+      mma_acc(Cfg::kColA0, Cfg::kColS, ddo_mn + st * kStage, n == 0, two);   // dV += P^T dO
       if (n + 1 < N) {
         if (!(ok = wait_all(&sm.q_full[st1], ((u + 1) >> 1) & 1u))) break;
         tc_fence_after_sync();
@@ -536,7 +567,7 @@ __device__ __forceinline__ void bwd_dkdv_issuer(BwdKvSmem<DH>& sm, const BwdPara
       }
       if (!(ok = wait_all(&sm.ds_full, u & 1u))) break;
       tc_fence_after_sync();
-      mma_acc(Cfg::kColA1, Cfg::kColDP, dq_mn + st * kStage, n == 0);   // dK += dS^T Q
+      mma_acc(Cfg::kColA1, Cfg::kColDP, dq_mn + st * kStage, n == 0, two);   // dK += dS^T Q
       mma_commit_warp(&sm.q_empty[st]);
       if (n + 1 < N) {
         mma_nt(Cfg::kColDP, dv_, ddo_k + st1 * kStage);                 // dP^T(n+1) = V dO^T
@@ -640,6 +671,19 @@ __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdPar
           }
           tmem_st_32x32b_x16(colS + 16 * c, w16);
         }
+        const bool two = bwd_two_parts<PK>(qb);
+        if (PK && two) {   // (every score of this thread's is in registers)
+#pragma unroll
+          for (int c = 0; c < Cfg::kChunks; ++c) {
+            uint32_t w16[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float a = pf[32 * c + 2 * e], b = pf[32 * c + 2 * e + 1];
+              w16[e] = bwd_low_pair(a, b, pack_bf16x2(a, b));
+            }
+            tmem_st_32x32b_x16(colS + Cfg::kCols / 2 + 16 * c, w16);
+          }
+        }
         tmem_st_wait();
         tc_fence_before_sync();
         mbar_arrive(&sm.p_full);
@@ -663,10 +707,26 @@ __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdPar
                   h ? make_float2(-d.z, -d.w) : make_float2(-d.x, -d.y));
               const float2 ds = __fmul2_rn(make_float2(pf[col], pf[col + 1]), dd);
               w16[e] = pack_bf16x2(ds.x, ds.y);
+              if (PK) {   // (the weights are not needed any more)
+                pf[col] = ds.x;
+                pf[col + 1] = ds.y;
+              }
             }
           }
           // (the pairs land on columns this thread loaded in chunk 0)
           tmem_st_32x32b_x16(colDP + 16 * c, w16);
+        }
+        if (PK && two) {
+#pragma unroll
+          for (int c = 0; c < Cfg::kChunks; ++c) {
+            uint32_t w16[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float a = pf[32 * c + 2 * e], b = pf[32 * c + 2 * e + 1];
+              w16[e] = bwd_low_pair(a, b, pack_bf16x2(a, b));
+            }
+            tmem_st_32x32b_x16(colDP + Cfg::kCols / 2 + 16 * c, w16);
+          }
         }
         tmem_st_wait();
         tc_fence_before_sync();
@@ -968,6 +1028,12 @@ __device__ __forceinline__ void bwd_dq_issuer(BwdQSmem<DH>& sm, const BwdParams&
         mma_bf16_ts_warp(Cfg::kColA0, col_dp(st) + bwd_packed_col(kk),
                          dk_mn + kst(u) * kStage + kk * (2048 >> 4),
                          idesc_acc, (n > 0 || kk > 0) ? 1u : 0u);
+      if (PK && bwd_two_parts<PK>(I.qb)) {
+#pragma unroll
+        for (int kk = 0; kk < 128 / 16; ++kk)
+          mma_bf16_ts_warp(Cfg::kColA0, col_dp(st) + bwd_low_col(kk),
+                           dk_mn + kst(u) * kStage + kk * (2048 >> 4), idesc_acc, 1u);
+      }
       mma_commit_warp(&sm.k_empty[kst(u)]);
     }
     if (ok) mma_commit_warp(&sm.acc_final);
@@ -1060,8 +1126,24 @@ __device__ __forceinline__ void bwd_dq_softmax(BwdQSmem<DH>& sm, const BwdParams
               make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])), negD);
           const float2 ds = __fmul2_rn(make_float2(pf[col], pf[col + 1]), dd);
           w16[e] = pack_bf16x2(ds.x, ds.y);
+          if (PK) {
+            pf[col] = ds.x;
+            pf[col + 1] = ds.y;
+          }
         }
         tmem_st_32x32b_x16(colDP + 16 * c, w16);
+      }
+      if (PK && bwd_two_parts<PK>(I.qb)) {   // (as in the dK/dV pass)
+#pragma unroll
+        for (int c = 0; c < Cfg::kChunks; ++c) {
+          uint32_t w16[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float x0 = pf[32 * c + 2 * e], x1 = pf[32 * c + 2 * e + 1];
+            w16[e] = bwd_low_pair(x0, x1, pack_bf16x2(x0, x1));
+          }
+          tmem_st_32x32b_x16(colDP + Cfg::kCols / 2 + 16 * c, w16);
+        }
       }
       tmem_st_wait();
       tc_fence_before_sync();

@@ -299,8 +299,8 @@ __global__ void __launch_bounds__(kPlanThreads)
   __syncthreads();
   const long long tokens = part[0][31], taken = part[1][31], given = part[2][31];
   const bool top_ok = top >= 0 && top <= p.capacity;
-  const bool too_many = tokens > p.T || !top_ok || top + given - taken > p.capacity ||
-                        top + given > 0x7fffffff;
+  const bool too_many = tokens > 0x7fffffff || !top_ok ||
+                        top + given - taken > p.capacity || top + given > 0x7fffffff;
   const bool too_few = top + given < taken;
   const bool off = too_many || too_few;   // then nothing changes
   if (off && blockIdx.x == 0 && t == 0)

@@ -531,11 +531,12 @@ int attn_rope_frequencies(unsigned long long* turns, float* amplitude, int rotar
  *   num_free, num_free_out  [1]      its height before and after; may be the same
  *   cu_seqlens         [B + 1]       written: first packed row of each
  *                                    sequence's new tokens, then their number
- *   positions, slots   [T]           written: for each packed row, then -1
- * (all device, int32).  All or nothing: where there are more than T new tokens
- * or the stack would pass capacity (ATTN_ERR_INVALID_ARG), or free pages do
- * not suffice (ATTN_ERR_NO_MEMORY, both latched for attn_status()), lengths,
- * table and stack stay as they were, cu_seqlens is all 0 and the rest -1.  A
+ *   positions, slots   [T]           written: for each packed row, then -1 (of
+ *                                    more than T new tokens, the first T's)
+ * (all device, int32).  All or nothing: where the stack would pass capacity
+ * (ATTN_ERR_INVALID_ARG) or free pages do not suffice (ATTN_ERR_NO_MEMORY, both
+ * latched for attn_status()), lengths, table and stack stay as they were,
+ * cu_seqlens is all 0 and the rest -1.  A
  * length outside [0, cols * page], before or after, latches
  * ATTN_ERR_INVALID_ARG and leaves that sequence as it is.  A used page number
  * outside [0, num_pages) latches it too and gives slots of -1.

@@ -97,7 +97,10 @@ def test_one_sequence_is_the_batch_form(Dh, n):
     grads2 = chs.attn_bwd(*batch[:3], o2, batch[3], lse2, window=333)
     assert chs.attn_status() == chs.ATTN_OK
     assert torch.equal(o.transpose(0, 1)[None], o2) and torch.equal(lse[None], lse2)
-    assert all(torch.equal(a.transpose(0, 1)[None], b) for a, b in zip(grads, grads2))
+    # (the gradients differ by what the batch form rounds in the first two blocks)
+    bounds = ref.attention(q, k, v, [0, n], True, 333, dout=dout)[4]
+    for a, b, bound in zip(grads, grads2, bounds):
+        assert bool(((a.double() - b[0].transpose(0, 1).double()).abs() <= 2 * bound).all())
 
 
 @pytest.mark.parametrize("Dh", [64, 128, 256])

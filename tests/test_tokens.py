@@ -263,11 +263,13 @@ def test_plan_is_all_or_nothing():
     got, state, _ = plan([5, 9], [20, 1], table, [6], 30)
     assert chs.attn_status() == chs.ATTN_ERR_INVALID_ARG
     assert state["seqlens"].tolist() == [5, 10] and got[0] == [0, 0, 1]
-    for delta, stack, T, code in (([19, 1], [6], 30, chs.ATTN_ERR_NO_MEMORY),
-                                  ([3, 3], [6, 7], 5, chs.ATTN_ERR_INVALID_ARG)):
-        got, _, same = plan([5, 9], delta, table, stack, T)
-        assert chs.attn_status() == code and all(same.values())
-        assert got == [[0, 0, 0], [-1] * T, [-1] * T]
+    got, _, same = plan([5, 9], [19, 1], table, [6], 30)
+    assert chs.attn_status() == chs.ATTN_ERR_NO_MEMORY and all(same.values())
+    assert got == [[0, 0, 0], [-1] * 30, [-1] * 30]
+    # a buffer for fewer rows than there are tokens takes the first ones'
+    got, state, _ = plan([5, 9], [3, 3], table, [6, 7], 5)
+    assert chs.attn_status() == chs.ATTN_OK and state["seqlens"].tolist() == [8, 12]
+    assert got == [[0, 3, 6], [5, 6, 7, 9, 10], [29, 30, 31, 41, 42]]
     # the stack may not pass its capacity
     got, _, same = plan([5, 9], [-5, 0], table, [6], 4, capacity=1)
     assert chs.attn_status() == chs.ATTN_ERR_INVALID_ARG and all(same.values())
