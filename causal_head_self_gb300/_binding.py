@@ -98,7 +98,7 @@ def load():
             lib.attn_fwd_packed.argtypes = ([rows] * 4 + [vp, vp, vp, ctypes.c_size_t] + [i] * 7
                                             + [f, vp])
             lib.attn_fwd_packed_workspace.restype = i
-            lib.attn_fwd_packed_workspace.argtypes = [i, i, size]
+            lib.attn_fwd_packed_workspace.argtypes = [i] * 5 + [size]
             lib.attn_bwd_packed.restype = i
             lib.attn_bwd_packed.argtypes = ([rows] * 5 + [vp] + [rows] * 3
                                             + [vp, vp, ctypes.c_size_t] + [i] * 7 + [f, vp])
@@ -595,12 +595,16 @@ def attn_cache_evict(kpages, vpages, weights, table, seqlens, budget, recent=0, 
 # ---------------------------------------------------------------------------
 # packed sequences, rotary positions, the plan of a serving step (include/attn.h)
 
-def _check_heads(name, t, shape, device):
-    """A bf16 tensor of that shape on that GPU, the values of a head side by side."""
+def _heads(name, t, shape, device):
+    """A bf16 tensor of that shape, [T, H, Dh] or a batch [B, H, S, Dh], on that GPU, the values
+    of a head side by side: as the library takes it."""
     try:
+        stride = t.stride()
         if (t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == device >= 0
-                and t.stride(-1) == 1):
-            return
+                and stride[-1] == 1):
+            if len(stride) == 3:
+                return Rows(t.data_ptr(), 0, stride[0], stride[1])
+            return Rows(t.data_ptr(), stride[0], stride[2], stride[1])
     except AttributeError:
         pass
     if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda:
@@ -610,14 +614,6 @@ def _check_heads(name, t, shape, device):
     if t.stride(-1) != 1:
         raise ValueError(f"the values of a head must lie side by side in {name}")
     raise ValueError(f"{name} must be on the same device as the other tensors")
-
-
-def _heads(name, t, shape, device):
-    """That tensor [T, H, Dh], or a batch [B, H, S, Dh], as the library takes it."""
-    _check_heads(name, t, shape, device)
-    if len(shape) == 3:
-        return Rows(t.data_ptr(), 0, t.stride(0), t.stride(1))
-    return Rows(t.data_ptr(), t.stride(0), t.stride(2), t.stride(1))
 
 
 def _packed_shape(q, k, cu_seqlens):
@@ -636,33 +632,38 @@ def _packed_shape(q, k, cu_seqlens):
 
 
 @functools.lru_cache(maxsize=4096)
-def _packed_workspace(B, Hq, T, backward):
+def _packed_workspace(device, B, Hq, T, Dh, causal, backward):
     size = ctypes.c_size_t()
     if backward:
         rc = load().attn_bwd_packed_workspace(B, Hq, T, ctypes.byref(size))
     else:
-        rc = load().attn_fwd_packed_workspace(B, T, ctypes.byref(size))
+        rc = load().attn_fwd_packed_workspace(B, Hq, T, Dh, causal, ctypes.byref(size))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_bwd_packed_workspace" if backward else "attn_fwd_packed_workspace")
     return size.value
 
 
-def attn_packed_workspace(q, cu_seqlens, *, backward=False):
-    """Bytes of workspace that attn_fwd_packed, or attn_bwd_packed, needs for
-    tensors of these shapes."""
-    T, Hq, _ = _shape("q", q, 3)
+def attn_packed_workspace(q, cu_seqlens, *, causal=True, backward=False):
+    """Bytes of workspace that attn_fwd_packed, or attn_bwd_packed, needs on the
+    current device for tensors of these shapes."""
+    T, Hq, Dh = _shape("q", q, 3)
     n = _shape("cu_seqlens", cu_seqlens, 1)[0]
-    return _packed_workspace(_int32("the number of sequences", n - 1), _int32("heads", Hq),
-                             _int32("rows", T), bool(backward))
+    return _packed_workspace(_this_device(), _int32("the number of sequences", n - 1),
+                             _int32("heads", Hq), _int32("rows", T), _int32("values", Dh),
+                             int(bool(causal)), bool(backward))
 
 
 def _workspace(workspace, need, device, tensor, stream):
+    """The workspace's address and size (and the tensor, which the caller keeps)."""
     if workspace is None:
-        return _empty((need,), torch.uint8, tensor.device, stream)
+        if need == 0:
+            return None, 0, None
+        workspace = _empty((need,), torch.uint8, tensor.device, stream)
+        return workspace.data_ptr(), need, workspace
     if (not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8
             or workspace.get_device() != device or not workspace.is_contiguous()):
         raise TypeError("workspace must be a contiguous CUDA uint8 tensor on the same device")
-    return workspace
+    return workspace.data_ptr(), workspace.numel(), workspace
 
 
 def attn_fwd_packed(q, k, v, cu_seqlens, o=None, lse=None, *, causal=True, window=0, scale=0.0,
@@ -673,8 +674,9 @@ def attn_fwd_packed(q, k, v, cu_seqlens, o=None, lse=None, *, causal=True, windo
     one's end.  lse [Hq,T] fp32, where given, receives the log-sum-exps.  Rows
     of no sequence keep what o and lse hold (nothing, where o is allocated
     here).  workspace: a uint8 tensor of attn_packed_workspace() bytes (None:
-    allocated here by torch, on the call's stream).  Returns o."""
-    window = _int32("window", window)
+    allocated here by torch, on the call's stream, where any is needed).
+    Returns o."""
+    window, causal = _int32("window", window), int(bool(causal))
     B, Hq, Hkv, T, Dh, device = _packed_shape(q, k, cu_seqlens)
     rq = _heads("q", q, (T, Hq, Dh), device)
     rk = _heads("k", k, (T, Hkv, Dh), device)
@@ -684,11 +686,12 @@ def attn_fwd_packed(q, k, v, cu_seqlens, o=None, lse=None, *, causal=True, windo
     if o is None:
         o = _empty((T, Hq, Dh), torch.bfloat16, q.device, stream)
     ro = _heads("o", o, (T, Hq, Dh), device)
-    workspace = _workspace(workspace, _packed_workspace(B, 1, T, False), device, q, stream)
+    ws, size, keep = _workspace(workspace,
+                                _packed_workspace(device, B, Hq, T, Dh, causal, False), device, q,
+                                stream)
     rc = load().attn_fwd_packed(rq, rk, rv, ro, None if lse is None else lse.data_ptr(),
-                                cu_seqlens.data_ptr(), workspace.data_ptr(), workspace.numel(), B,
-                                Hq, Hkv, T, Dh, int(bool(causal)), window, float(scale),
-                                _stream_handle(stream))
+                                cu_seqlens.data_ptr(), ws, size, B, Hq, Hkv, T, Dh, causal, window,
+                                float(scale), _stream_handle(stream))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_fwd_packed")
     return o
@@ -710,10 +713,11 @@ def attn_bwd_packed(q, k, v, o, dout, lse, cu_seqlens, dq=None, dk=None, dv=None
     dv = _empty(narrow, torch.bfloat16, q.device, stream) if dv is None else dv
     outs = [_heads(name, t, shape, device) for name, t, shape in (
         ("dq", dq, wide), ("dk", dk, narrow), ("dv", dv, narrow))]
-    workspace = _workspace(workspace, _packed_workspace(B, Hq, T, True), device, q, stream)
-    rc = load().attn_bwd_packed(*ins, lse.data_ptr(), *outs, cu_seqlens.data_ptr(),
-                                workspace.data_ptr(), workspace.numel(), B, Hq, Hkv, T, Dh,
-                                int(bool(causal)), window, float(scale), _stream_handle(stream))
+    ws, size, keep = _workspace(workspace, _packed_workspace(device, B, Hq, T, Dh, 1, True), device,
+                                q, stream)
+    rc = load().attn_bwd_packed(*ins, lse.data_ptr(), *outs, cu_seqlens.data_ptr(), ws,
+                                size, B, Hq, Hkv, T, Dh, int(bool(causal)), window, float(scale),
+                                _stream_handle(stream))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_bwd_packed")
     return dq, dk, dv

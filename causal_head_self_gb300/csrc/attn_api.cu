@@ -890,11 +890,16 @@ int packed_shape(chs::PackedShape* s, float* scale_log2, const int* cu, int B, i
 
 }  // namespace
 
-extern "C" int attn_fwd_packed_workspace(int B, int T, size_t* bytes) {
-  const int rc = packed_check(B, 1, T);
+extern "C" int attn_fwd_packed_workspace(int B, int Hq, int T, int Dh, int causal,
+                                         size_t* bytes) {
+  chs::PackedShape s;
+  float scale_log2;
+  int rc = packed_shape(&s, &scale_log2, nullptr, B, Hq, Hq, T, Dh, causal, 0, 0.f);
   if (rc != ATTN_OK) return rc;
   if (!bytes) return ATTN_ERR_INVALID_ARG;
-  *bytes = chs::fwd_packed_workspace_bytes(B, T);
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&st)) != ATTN_OK) return rc;
+  *bytes = chs::fwd_packed_workspace_bytes(s, launch_info(st));
   return ATTN_OK;
 }
 
@@ -920,7 +925,8 @@ extern "C" int attn_fwd_packed(const attn_rows_t* q, const attn_rows_t* k, const
   for (const Rows* x : {&Q, &K, &V, &O})
     if (!rows_usable(*x, Dh)) return ATTN_ERR_INVALID_ARG;
   if (!rows_distinct(O)) return ATTN_ERR_INVALID_ARG;
-  if (!usable(cu_seqlens, 4) || (lse && !usable(lse, 4)) || !usable(workspace, 256))
+  if (!usable(cu_seqlens, 4) || (lse && !usable(lse, 4)) ||
+      (workspace_bytes > 0 && !usable(workspace, 256)))
     return ATTN_ERR_INVALID_ARG;
   const size_t lb = lse ? (size_t)Hq * T * 4 : 0, cb = ((size_t)B + 1) * 4;
   for (const Rows* x : {&Q, &K, &V}) {
@@ -930,15 +936,16 @@ extern "C" int attn_fwd_packed(const attn_rows_t* q, const attn_rows_t* k, const
   }
   if (rows_overlap(O, lse, lb) || rows_overlap(O, cu_seqlens, cb) ||
       rows_overlap(O, workspace, workspace_bytes) ||
-      overlaps(workspace, workspace_bytes, cu_seqlens, cb) ||
-      (lse && (overlaps(lse, lb, cu_seqlens, cb) || overlaps(lse, lb, workspace, workspace_bytes))))
+      (workspace_bytes > 0 && overlaps(workspace, workspace_bytes, cu_seqlens, cb)) ||
+      (lse && (overlaps(lse, lb, cu_seqlens, cb) || (workspace_bytes > 0 && overlaps(lse, lb, workspace, workspace_bytes)))))
     return ATTN_ERR_INVALID_ARG;
-  if (workspace_bytes < chs::fwd_packed_workspace_bytes(B, T)) return ATTN_ERR_SCRATCH_LIMIT;
   DeviceState* st = nullptr;
   if ((rc = device_state(&st)) != ATTN_OK) return rc;
+  const chs::DeviceInfo dev = launch_info(st);
+  if (workspace_bytes < chs::fwd_packed_workspace_bytes(s, dev)) return ATTN_ERR_SCRATCH_LIMIT;
   const cudaError_t e = chs::launch_fwd_packed(s, packed_rows(Q), packed_rows(K), packed_rows(V),
                                                packed_rows(O), lse, workspace, scale_log2,
-                                               launch_info(st), stream);
+                                               dev, stream);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

@@ -141,7 +141,7 @@ struct PackedShape {
 };
 
 // Device memory that the calls need: the lists of tiles, and the backward's row statistics.
-size_t fwd_packed_workspace_bytes(int B, int T);
+size_t fwd_packed_workspace_bytes(const PackedShape& s, const DeviceInfo& dev);
 size_t bwd_packed_workspace_bytes(int B, int Hq, int T);
 // Most 128-row tiles that B sequences of T rows in all can have.
 inline long long packed_max_tiles(int B, int T) { return (long long)T / 128 + B; }

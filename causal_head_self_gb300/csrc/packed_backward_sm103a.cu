@@ -149,8 +149,8 @@ cudaError_t launch_bwd_packed(const PackedShape& s, const PackedRows& q, const P
   p.error_word = dev.error_word;
   p.fault = dev.fault;
   BwdParams pk = p, pq = p;
-  pk.pk = PackedRef{static_cast<PackedTile*>(lists[0]), counts[0], s.T, m.heads_inner};
-  pq.pk = PackedRef{static_cast<PackedTile*>(lists[1]), counts[1], s.T, m.heads_inner};
+  pk.pk = PackedRef{static_cast<PackedTile*>(lists[0]), counts[0], s.cu, s.B, 0, s.T, m.heads_inner};
+  pq.pk = PackedRef{static_cast<PackedTile*>(lists[1]), counts[1], s.cu, s.B, 0, s.T, m.heads_inner};
   e = s.Dh == 256   ? launch_prep<256>(s, o, dout, lse, pq, dev, stream)
       : s.Dh == 128 ? launch_prep<128>(s, o, dout, lse, pq, dev, stream)
                     : launch_prep<64>(s, o, dout, lse, pq, dev, stream);

@@ -7,11 +7,6 @@
 
 namespace chs {
 
-// The workspace: the tile count (256 bytes), then the list.
-size_t fwd_packed_workspace_bytes(int B, int T) {
-  return 256 + ((size_t)packed_max_tiles(B, T) * sizeof(PackedTile) + 255) / 256 * 256;
-}
-
 cudaError_t launch_packed_schedule(const PackedShape& s, int block, int lists, const int* order,
                                    void* const* tiles, int* const* counts, const DeviceInfo& dev,
                                    cudaStream_t stream) {
@@ -56,7 +51,7 @@ template <int DH>
 cudaError_t launch_wide(const PackedShape& s, const PackedRows& q, const PackedRows& k,
                         const PackedRows& v, const PackedRows& o, float* lse, const PackedRef& ref,
                         float scale_log2, const DeviceInfo& dev, cudaStream_t stream) {
-  constexpr size_t smem = prefill_smem_bytes<DH>();
+  constexpr size_t smem = prefill_smem_bytes<DH, true>();
   static_assert(smem <= 232448, "shared memory budget of one sm_103a CTA");
   FwdMaps m;
   if (!fwd_maps(&m, s, q, k, v, o, 128)) return cudaErrorInvalidValue;
@@ -99,7 +94,7 @@ cudaError_t launch_k64(const PackedShape& s, const PackedRows& q, const PackedRo
                        const PackedRows& v, const PackedRows& o, float* lse, const PackedRef& ref,
                        float scale_log2, const DeviceInfo& dev, cudaStream_t stream) {
   using Cfg = PrefillK64Cfg<DH>;
-  constexpr size_t smem = prefill_k64_smem_bytes<DH>();
+  constexpr size_t smem = prefill_k64_smem_bytes<DH, true>();
   FwdMaps m;
   if (!fwd_maps(&m, s, q, k, v, o, Cfg::kKeys)) return cudaErrorInvalidValue;
   static std::atomic<int> configured[kMaxDevices];
@@ -135,21 +130,45 @@ cudaError_t launch_k64(const PackedShape& s, const PackedRows& q, const PackedRo
 // Head size 128: the 64-key kernel up to this many rows per sequence on average.
 constexpr int kPackedK64MeanRows128 = 1536;
 
+bool takes_k64(int B, int T, int Dh) {
+  return Dh == 256 || (Dh == 128 && T <= (long long)kPackedK64MeanRows128 * B);
+}
+
+// Does each CTA list its own items?  Few sequences, no more than a lane's item each per CTA, and
+// a causal mask (under which the last blocks are the heaviest).
+bool lists_own(const PackedShape& s, const DeviceInfo& dev) {
+  const bool k64 = takes_k64(s.B, s.T, s.Dh);
+  const int block = k64 ? 128 : 256;
+  const int ctas = (k64 && s.Dh == 128 ? 2 : 1) * dev.num_sms;
+  const long long items = ((long long)s.T / block + s.B) * s.Hq;
+  return s.causal && s.B <= kOwnSequences && s.T / block + 1 <= kOwnLevels &&
+         items <= (long long)ctas * kOwnItems;
+}
+
 }  // namespace
+
+// The workspace: the tile count (256 bytes), then the list.
+size_t fwd_packed_workspace_bytes(const PackedShape& s, const DeviceInfo& dev) {
+  if (lists_own(s, dev)) return 0;
+  return 256 + ((size_t)packed_max_tiles(s.B, s.T) * sizeof(PackedTile) + 255) / 256 * 256;
+}
 
 cudaError_t launch_fwd_packed(const PackedShape& s, const PackedRows& q, const PackedRows& k,
                               const PackedRows& v, const PackedRows& o, float* lse,
                               void* workspace, float scale_log2, const DeviceInfo& dev,
                               cudaStream_t stream) {
-  const bool k64 = s.Dh == 256 ||
-                   (s.Dh == 128 && s.T <= (long long)kPackedK64MeanRows128 * s.B);
-  int* count = static_cast<int*>(workspace);
-  void* tiles = static_cast<char*>(workspace) + 256;
-  const int order = kByKeys;
-  const cudaError_t e = launch_packed_schedule(s, k64 ? 128 : 256, 1, &order, &tiles, &count, dev,
-                                               stream);
-  if (e != cudaSuccess) return e;
-  const PackedRef ref{static_cast<PackedTile*>(tiles), count, s.T, 0};
+  const bool k64 = takes_k64(s.B, s.T, s.Dh);
+  const int block = k64 ? 128 : 256;
+  PackedRef ref{nullptr, nullptr, s.cu, s.B, s.T / block + 1, s.T, 0};
+  if (!lists_own(s, dev)) {
+    int* count = static_cast<int*>(workspace);
+    void* tiles = static_cast<char*>(workspace) + 256;
+    const int order = kByKeys;
+    const cudaError_t e = launch_packed_schedule(s, block, 1, &order, &tiles, &count, dev, stream);
+    if (e != cudaSuccess) return e;
+    ref.tiles = static_cast<PackedTile*>(tiles);
+    ref.num_tiles = count;
+  }
   if (s.Dh == 256) return launch_k64<256>(s, q, k, v, o, lse, ref, scale_log2, dev, stream);
   if (k64) return launch_k64<128>(s, q, k, v, o, lse, ref, scale_log2, dev, stream);
   return s.Dh == 128 ? launch_wide<128>(s, q, k, v, o, lse, ref, scale_log2, dev, stream)

@@ -99,7 +99,7 @@ struct PrefillK64Cfg {
 
 // Every array is a whole number of KiB, so each starts 1024-byte aligned once
 // the structure does (the 128-byte swizzle repeats every 1024 bytes).
-template <int DH>
+template <int DH, bool PK = false>
 struct PrefillK64Smem {
   using Cfg = PrefillK64Cfg<DH>;
   uint8_t q[Cfg::kQBytes];
@@ -115,6 +115,12 @@ struct PrefillK64Smem {
   uint64_t qt_free;   // (Q in tensor memory) the item's last S MMA is done
   uint32_t tmem_base;
   int abort_flag;
+};
+
+// PK: and the CTA's own items, where it lists them.
+template <int DH>
+struct PrefillK64Smem<DH, true> : PrefillK64Smem<DH, false> {
+  PackedOwn own;
 };
 
 // Geometry of one 128-row work item: query rows [q0, q0 + 128) of the chunk,
@@ -154,10 +160,27 @@ __device__ __forceinline__ int prefill_k64_cta_item(int k, int num_items) {
   return k < n ? prefill_k64_item(n - 1 - k, c, G) : num_items;
 }
 
-// Work items of the launch (PK: known on the GPU alone; there may be none for a CTA).
+// Rows, keys and place of a packed tile's item, without its key tiles.
+__device__ __forceinline__ void prefill_k64_place(PrefillK64Tile& t, const PackedTile& e, int h,
+                                                  int group) {
+  t.bh = h;
+  t.bh_kv = h / group;
+  t.Sq = t.Skv = e.len + e.pad();
+  t.q_off = 0;
+  t.start = e.start;
+  t.pad = e.pad();
+}
+
+// Query block qb, and the key tiles that it sees.
 template <bool PK>
-__device__ __forceinline__ int prefill_k64_num_items(const PrefillK64Params& p) {
-  return PK ? packed_num_tiles(p.pk) * p.Hq : p.num_items;
+__device__ __forceinline__ void prefill_k64_span(PrefillK64Tile& t, const PrefillK64Params& p,
+                                                 int qb) {
+  t.q0 = qb * 128;
+  const int nkv = (t.Skv + 63) / 64;
+  const int last_pos = t.q_off + min(t.q0 + 127, t.Sq - 1);
+  t.hi = p.causal ? min(nkv - 1, last_pos / 64) : nkv - 1;
+  t.lo = (p.causal && p.window > 0) ? max(0, t.q_off + t.q0 - p.window + 1) / 64 : 0;
+  if constexpr (PK) t.lo = max(t.lo, t.pad / 64);   // (the first tile may be padding alone)
 }
 
 template <bool PK>
@@ -168,12 +191,7 @@ __device__ __forceinline__ PrefillK64Tile prefill_k64_tile_of(const PrefillK64Pa
     // a tile's heads one after another: those of a group share their K/V tiles in L2
     const int i = w / p.Hq;
     const PackedTile e = packed_tile(p.pk, i);
-    t.bh = w - i * p.Hq;
-    t.bh_kv = t.bh / p.group;
-    t.Sq = t.Skv = e.len + e.pad();
-    t.q_off = 0;
-    t.start = e.start;
-    t.pad = e.pad();
+    prefill_k64_place(t, e, w - i * p.Hq, p.group);
     qb = e.blk;
   } else {
     const int blk = w / p.per_qb;
@@ -186,14 +204,38 @@ __device__ __forceinline__ PrefillK64Tile prefill_k64_tile_of(const PrefillK64Pa
     t.q_off = p.q_off;
     t.start = t.pad = 0;
   }
-  t.q0 = qb * 128;
-  const int nkv = (t.Skv + 63) / 64;
-  const int last_pos = t.q_off + min(t.q0 + 127, t.Sq - 1);
-  t.hi = p.causal ? min(nkv - 1, last_pos / 64) : nkv - 1;
-  t.lo = (p.causal && p.window > 0) ? max(0, t.q_off + t.q0 - p.window + 1) / 64 : 0;
-  if constexpr (PK) t.lo = max(t.lo, t.pad / 64);   // (the first tile may be padding alone)
+  prefill_k64_span<PK>(t, p, qb);
   return t;
 }
+
+// The CTA's work items one after another: the k-th, if there is one, and its number w.
+template <int DH, bool PK>
+struct PrefillK64Items {
+  const PrefillK64Params& p;
+  const PrefillK64Smem<DH, PK>& sm;
+  int n;   // items of the launch (PK: known on the GPU alone), or of the CTA's own list
+  __device__ __forceinline__ PrefillK64Items(const PrefillK64Params& p_,
+                                             const PrefillK64Smem<DH, PK>& sm_)
+      : p(p_), sm(sm_), n(p_.num_items) {
+    if constexpr (PK) n = p.pk.tiles ? packed_num_tiles(p.pk) * p.Hq : sm.own.count;
+  }
+  __device__ __forceinline__ bool at(int k, int& w) const {
+    w = PK && !p.pk.tiles ? k : prefill_k64_cta_item(k, n);
+    return w < n;
+  }
+  __device__ __forceinline__ PrefillK64Tile item(int w) const {
+    if constexpr (PK) {
+      if (!p.pk.tiles) {
+        const int4 e = sm.own.item[w];
+        PrefillK64Tile t;
+        prefill_k64_place(t, PackedTile{e.x, e.y, e.z, 0}, e.w, p.group);
+        prefill_k64_span<PK>(t, p, e.z);
+        return t;
+      }
+    }
+    return prefill_k64_tile_of<PK>(p, w);
+  }
+};
 
 __device__ __forceinline__ void mbar_wait_drain_k64(uint64_t* bar, uint32_t parity) {
   const uint32_t a = smem_u32(bar);
@@ -207,7 +249,7 @@ __device__ __forceinline__ void mbar_wait_drain_k64(uint64_t* bar, uint32_t pari
 // previous item's last S is done, then the item's K and V tiles (Dh/64 boxes
 // of 64 x 64 each) through the K and V rings.
 template <int DH, bool PK>
-__device__ __forceinline__ void prefill_k64_producer(PrefillK64Smem<DH>& sm, const PrefillK64Params& p,
+__device__ __forceinline__ void prefill_k64_producer(PrefillK64Smem<DH, PK>& sm, const PrefillK64Params& p,
                                                     const CUtensorMap* map_q,
                                                     const CUtensorMap* map_k,
                                                     const CUtensorMap* map_v,
@@ -218,11 +260,11 @@ __device__ __forceinline__ void prefill_k64_producer(PrefillK64Smem<DH>& sm, con
   uint32_t k_loaded = 0, k_par = 0, v_loaded = 0, v_par = 0;
   int nq = 0;
   bool ok = true;
-  const int num_items = prefill_k64_num_items<PK>(p);
+  const PrefillK64Items<DH, PK> items(p, sm);
   for (int it = 0; ok; ++it) {
-    const int w = prefill_k64_cta_item(it, num_items);
-    if (w >= num_items) break;
-    const PrefillK64Tile tile = prefill_k64_tile_of<PK>(p, w);
+    int w;
+    if (!items.at(it, w)) break;
+    const PrefillK64Tile tile = items.item(w);
     if (nq > 0 && !(ok = mbar_wait(&sm.q_empty, (uint32_t)(nq - 1) & 1u, abort))) break;
     // (checked builds: a query row of the chunk and a query head of the batch)
     const bool q_in_range = attn_check(tile.q0 >= 0 && tile.q0 < tile.Sq && tile.bh >= 0 &&
@@ -294,7 +336,7 @@ __device__ __forceinline__ void prefill_k64_producer(PrefillK64Smem<DH>& sm, con
 // after an MMA is not ordered behind it, so the copy waits (qt_free) for the
 // previous item's last S MMA, which is long done by then.
 template <int DH, bool PK>
-__device__ __forceinline__ void prefill_k64_issuer(PrefillK64Smem<DH>& sm, const PrefillK64Params& p,
+__device__ __forceinline__ void prefill_k64_issuer(PrefillK64Smem<DH, PK>& sm, const PrefillK64Params& p,
                                                    uint32_t tbase, volatile int* abort) {
   using Cfg = PrefillK64Cfg<DH>;
   constexpr uint32_t idesc_qk = idesc_bf16_f32(128, Cfg::kKeys, false, false);
@@ -329,11 +371,11 @@ __device__ __forceinline__ void prefill_k64_issuer(PrefillK64Smem<DH>& sm, const
   uint32_t t = 0;   // global tile counter
   int nq = 0;
   bool ok = true;
-  const int num_items = prefill_k64_num_items<PK>(p);
+  const PrefillK64Items<DH, PK> items(p, sm);
   for (int it = 0; ok; ++it) {
-    const int w = prefill_k64_cta_item(it, num_items);
-    if (w >= num_items) break;
-    const PrefillK64Tile tile = prefill_k64_tile_of<PK>(p, w);
+    int w;
+    if (!items.at(it, w)) break;
+    const PrefillK64Tile tile = items.item(w);
     const int n = tile.hi - tile.lo + 1;
     if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_full, (uint32_t)nq & 1u, abort)))) break;
     tc_fence_after_sync();
@@ -389,7 +431,7 @@ __device__ __forceinline__ void prefill_k64_issuer(PrefillK64Smem<DH>& sm, const
 // t): the online softmax of "Online normalizer calculation for softmax" with
 // the lazy maximum of the ping-pong kernel, 64 scores per tile.
 template <int DH, bool PK>
-__device__ __forceinline__ void prefill_k64_softmax(PrefillK64Smem<DH>& sm, const PrefillK64Params& p,
+__device__ __forceinline__ void prefill_k64_softmax(PrefillK64Smem<DH, PK>& sm, const PrefillK64Params& p,
                                                     const CUtensorMap* map_o, uint32_t tbase,
                                                     volatile int* abort, int warp, int lane) {
   using Cfg = PrefillK64Cfg<DH>;
@@ -398,13 +440,13 @@ __device__ __forceinline__ void prefill_k64_softmax(PrefillK64Smem<DH>& sm, cons
   const uint32_t colO = lane_addr + Cfg::kColO;
   const float sl2 = p.scale_log2;
   uint32_t tt = 0;      // global tile counter (the issuer's t)
-  uint32_t items = 0;   // items finished (o_final phases)
+  uint32_t finished = 0;   // items finished (o_final phases)
   bool ok = true;
-  const int num_items = prefill_k64_num_items<PK>(p);
+  const PrefillK64Items<DH, PK> items(p, sm);
   for (int it = 0; ok; ++it) {
-    const int w = prefill_k64_cta_item(it, num_items);
-    if (w >= num_items) break;
-    const PrefillK64Tile tile = prefill_k64_tile_of<PK>(p, w);
+    int w;
+    if (!items.at(it, w)) break;
+    const PrefillK64Tile tile = items.item(w);
     const int row = tile.pos_first(p) + t;   // this thread's query position
 
     float m_run = -INFINITY, l_run = 0.f;
@@ -502,8 +544,8 @@ __device__ __forceinline__ void prefill_k64_softmax(PrefillK64Smem<DH>& sm, cons
     if (!ok) break;
 
     // ---- epilogue: O / l -> bf16 -> output rows
-    if (!(ok = mbar_wait(&sm.o_final, items & 1u, abort))) break;
-    ++items;
+    if (!(ok = mbar_wait(&sm.o_final, finished & 1u, abort))) break;
+    ++finished;
     tc_fence_after_sync();
     const float inv_l = 1.0f / l_run;
     const int orow = tile.q0 + t;   // output row within the chunk
@@ -612,7 +654,8 @@ __global__ void __launch_bounds__(PrefillK64Cfg<DH>::kThreads, PrefillK64Cfg<DH>
     if (threadIdx.x == 0) atomicExch(p.error_word, 3);   // ATTN_ERR_CUDA
     return;
   }
-  PrefillK64Smem<DH>& sm = *reinterpret_cast<PrefillK64Smem<DH>*>(
+  using Smem = PrefillK64Smem<DH, PK>;
+  Smem& sm = *reinterpret_cast<Smem*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   volatile int* abort = &sm.abort_flag;
   const int warp = threadIdx.x / 32;
@@ -658,6 +701,14 @@ __global__ void __launch_bounds__(PrefillK64Cfg<DH>::kThreads, PrefillK64Cfg<DH>
   // leaves the next kernel little to take, so it may be launched now
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
+  if constexpr (PK) {
+    if (!p.pk.tiles) {
+      static_assert(Cfg::kQBytes >= kOwnScratch, "the Q tile is the scratch");
+      packed_list_own<128>(p.pk, p.Hq, sm.q, sm.own, p.error_word,
+                           [](int k, int n) { return prefill_k64_cta_item(k, n); });
+      __syncthreads();
+    }
+  }
   // every tensor-memory address is relative to this CTA's allocation (at
   // Dh 128 two CTAs share an SM's 512 columns)
   const uint32_t tbase = sm.tmem_base;
@@ -680,13 +731,14 @@ __global__ void __launch_bounds__(PrefillK64Cfg<DH>::kThreads, PrefillK64Cfg<DH>
   if (threadIdx.x == 0 && sm.abort_flag) atomicExch(p.error_word, 4);   // ATTN_ERR_TIMEOUT
 }
 
-template <int DH>
+template <int DH, bool PK = false>
 constexpr size_t prefill_k64_smem_bytes() {
-  return sizeof(PrefillK64Smem<DH>) + PrefillK64Cfg<DH>::kAlignSlack;
+  return sizeof(PrefillK64Smem<DH, PK>) + PrefillK64Cfg<DH>::kAlignSlack;
 }
 
 // two CTAs per SM at Dh 128 in the SM's 228 KiB (1 KiB of it reserved per CTA)
-static_assert(2 * (prefill_k64_smem_bytes<128>() + 1024) <= 228 * 1024, "Dh 128: two CTAs per SM");
-static_assert(prefill_k64_smem_bytes<256>() <= 227 * 1024, "Dh 256: one CTA per SM");
+static_assert(2 * (prefill_k64_smem_bytes<128, true>() + 1024) <= 228 * 1024,
+              "Dh 128: two CTAs per SM");
+static_assert(prefill_k64_smem_bytes<256, true>() <= 227 * 1024, "Dh 256: one CTA per SM");
 
 }  // namespace chs

@@ -95,7 +95,7 @@ struct PrefillCfg {
   static constexpr uint32_t kColS0 = 0, kColS1 = 128, kColO0 = 256, kColO1 = 384;
 };
 
-template <int DH>
+template <int DH, bool PK = false>
 struct __align__(1024) PrefillSmem {
   using Cfg = PrefillCfg<DH>;
   uint8_t q[2][Cfg::kTileBytes];          // Q sub-tiles of the current item
@@ -111,6 +111,12 @@ struct __align__(1024) PrefillSmem {
   uint32_t tmem_base;
   int abort_flag;
   int groups_done[2];   // MMA groups each issuer has issued (orders the two issuers)
+};
+
+// PK: and the CTA's own items, where it lists them.
+template <int DH>
+struct __align__(1024) PrefillSmem<DH, true> : PrefillSmem<DH, false> {
+  PackedOwn own;
 };
 
 // Geometry of one work item.  Query rows are counted within the chunk
@@ -209,12 +215,6 @@ struct PrefillItem {
   PrefillTile tile;
 };
 
-// Work items of the launch (PK: known on the GPU alone; there may be none for a CTA).
-template <bool PK>
-__device__ __forceinline__ int prefill_num_items(const PrefillParams& p) {
-  return PK ? packed_num_tiles(p.pk) * p.Hq : p.num_items;
-}
-
 template <bool PK>
 __device__ __forceinline__ PrefillItem prefill_item_of(const PrefillParams& p, int w) {
   PrefillItem it;
@@ -241,6 +241,39 @@ __device__ __forceinline__ PrefillItem prefill_item_of(const PrefillParams& p, i
   return it;
 }
 
+// The CTA's work items one after another: the k-th, if there is one, and its number w.
+template <int DH, bool PK>
+struct PrefillItems {
+  const PrefillParams& p;
+  const PrefillSmem<DH, PK>& sm;
+  int n;   // items of the launch (PK: known on the GPU alone), or of the CTA's own list
+  __device__ __forceinline__ PrefillItems(const PrefillParams& p_, const PrefillSmem<DH, PK>& sm_)
+      : p(p_), sm(sm_), n(p_.num_items) {
+    if constexpr (PK) n = p.pk.tiles ? packed_num_tiles(p.pk) * p.Hq : sm.own.count;
+  }
+  __device__ __forceinline__ bool at(int k, int& w) const {
+    w = PK && !p.pk.tiles ? k : prefill_cta_item(k, n);
+    return w < n;
+  }
+  __device__ __forceinline__ PrefillItem item(int w) const {
+    if constexpr (PK) {
+      if (!p.pk.tiles) {
+        const int4 e = sm.own.item[w];
+        const PackedTile tile{e.x, e.y, e.z, 0};
+        const int rows = tile.len + tile.pad();
+        PrefillItem it;
+        it.b = 0;
+        it.h = it.bh = e.w;
+        it.bh_kv = p.div_group.div(it.h);
+        it.start = tile.start;
+        it.tile = prefill_tile_of(p, tile.blk, rows, rows, 0, tile.pad());
+        return it;
+      }
+    }
+    return prefill_item_of<PK>(p, w);
+  }
+};
+
 // One MMA issuer: the chain of sub-tile S (0 or 1) over all of the CTA's work
 // items, run by a whole warp that stays converged; one elected lane issues
 // each tcgen05 instruction.  Descriptors and tensor-memory addresses descend
@@ -250,7 +283,7 @@ __device__ __forceinline__ PrefillItem prefill_item_of(const PrefillParams& p, i
 // between two of them is a bubble.  Wait results are made warp-uniform so
 // the warp never diverges.
 template <int DH, int S, bool PK>
-__device__ __forceinline__ void prefill_issuer(PrefillSmem<DH>& sm, const PrefillParams& p,
+__device__ __forceinline__ void prefill_issuer(PrefillSmem<DH, PK>& sm, const PrefillParams& p,
                                                volatile int* abort, int lane) {
   using Cfg = PrefillCfg<DH>;
   constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 128, false, false);
@@ -284,11 +317,11 @@ __device__ __forceinline__ void prefill_issuer(PrefillSmem<DH>& sm, const Prefil
   int g_base = 0;         // groups of the earlier items
   uint32_t pph = 0, qph = 0;
   bool ok = true;
-  const int num_items = prefill_num_items<PK>(p);
+  const PrefillItems<DH, PK> items(p, sm);
   for (int it = 0; ok; ++it) {
-    const int w = prefill_cta_item(it, num_items);
-    if (w >= num_items) break;
-    const PrefillTile tile = prefill_item_of<PK>(p, w).tile;
+    int w;
+    if (!items.at(it, w)) break;
+    const PrefillTile tile = items.item(w).tile;
     const int n_tiles = tile.hi - tile.lo + 1;
     const bool valid = tile.valid(S);
     // the group of this sub-tile's last S, after which its Q buffer is free
@@ -384,7 +417,7 @@ __device__ __forceinline__ void prefill_issuer(PrefillSmem<DH>& sm, const Prefil
 // its issuer's last S MMA of the previous item is done, so the next item's
 // first tiles arrive while the current one finishes.
 template <int DH, bool PK>
-__device__ __forceinline__ void prefill_producer(PrefillSmem<DH>& sm, const PrefillParams& p,
+__device__ __forceinline__ void prefill_producer(PrefillSmem<DH, PK>& sm, const PrefillParams& p,
                                                  const CUtensorMap* map_q,
                                                  const CUtensorMap* map_k,
                                                  const CUtensorMap* map_v,
@@ -399,11 +432,11 @@ __device__ __forceinline__ void prefill_producer(PrefillSmem<DH>& sm, const Pref
   // the grid is no larger than the number of items, so every CTA has a first
   // one; over packed sequences it may have none
   PrefillItem item = first;
-  const int num_items = prefill_num_items<PK>(p);
+  const PrefillItems<DH, PK> items(p, sm);
   if constexpr (PK) {
-    const int w = prefill_cta_item(0, num_items);
-    ok = w < num_items;
-    if (ok) item = prefill_item_of<PK>(p, w);
+    int w;
+    ok = items.at(0, w);
+    if (ok) item = items.item(w);
   }
   for (int it = 0; ok; ++it) {
     const PrefillTile& tile = item.tile;
@@ -470,9 +503,9 @@ __device__ __forceinline__ void prefill_producer(PrefillSmem<DH>& sm, const Pref
       if (++vst == Cfg::kStagesV) { vst = 0; vph ^= 1; }
     }
     // decode the next item while this one's copies are in flight
-    const int w = prefill_cta_item(it + 1, num_items);
-    if (w >= num_items) break;
-    item = prefill_item_of<PK>(p, w);
+    int w;
+    if (!items.at(it + 1, w)) break;
+    item = items.item(w);
   }
   // every copy this thread started has landed before the CTA may exit
   if (nq0 > 0) mbar_wait_drain(&sm.q_full[0], (nq0 - 1) & 1u);
@@ -488,7 +521,7 @@ __device__ __forceinline__ void prefill_producer(PrefillSmem<DH>& sm, const Pref
 // online softmax of "Online normalizer calculation for softmax" with a lazy
 // maximum; per item: O / l written straight from registers to global memory.
 template <int DH, bool PK>
-__device__ __forceinline__ void prefill_softmax(PrefillSmem<DH>& sm, const PrefillParams& p,
+__device__ __forceinline__ void prefill_softmax(PrefillSmem<DH, PK>& sm, const PrefillParams& p,
                                                 const CUtensorMap* map_o, uint32_t tbase,
                                                 volatile int* abort, int warp, int lane) {
   using Cfg = PrefillCfg<DH>;
@@ -501,11 +534,11 @@ __device__ __forceinline__ void prefill_softmax(PrefillSmem<DH>& sm, const Prefi
   const float sl2 = p.scale_log2;
   uint32_t ph = 0;   // bit 0: s_full phase, bit 1: o_final phase
   bool ok = true;
-  const int num_items = prefill_num_items<PK>(p);
+  const PrefillItems<DH, PK> items(p, sm);
   for (int it = 0; ok; ++it) {
-    const int w = prefill_cta_item(it, num_items);
-    if (w >= num_items) break;
-    const PrefillItem item = prefill_item_of<PK>(p, w);
+    int w;
+    if (!items.at(it, w)) break;
+    const PrefillItem item = items.item(w);
     const PrefillTile& tile = item.tile;
     if (!tile.valid(s)) continue;           // a ragged last block: no rows here
     const int row = tile.pos_first(s) + t;  // this thread's query position
@@ -706,7 +739,7 @@ __global__ void __launch_bounds__(384, 1)
                         const __grid_constant__ CUtensorMap map_v,
                         const __grid_constant__ CUtensorMap map_o, const PrefillParams p) {
   using Cfg = PrefillCfg<DH>;
-  using Smem = PrefillSmem<DH>;
+  using Smem = PrefillSmem<DH, PK>;
   extern __shared__ uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                       ~uintptr_t(1023));
@@ -758,6 +791,14 @@ __global__ void __launch_bounds__(384, 1)
   // now be launched, cannot take resources from this grid.
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
+  if constexpr (PK) {
+    if (!p.pk.tiles) {
+      static_assert(sizeof(sm.q) >= kOwnScratch, "the Q tiles are the scratch");
+      packed_list_own<256>(p.pk, p.Hq, sm.q, sm.own, p.error_word,
+                           [](int k, int n) { return prefill_cta_item(k, n); });
+      __syncthreads();
+    }
+  }
   const uint32_t tbase = sm.tmem_base;
   // all 512 columns are this CTA's, so the allocation starts at column 0;
   // the MMA issuers rely on that (compile-time tensor-memory addresses)
@@ -792,9 +833,9 @@ __global__ void __launch_bounds__(384, 1)
   if (threadIdx.x == 0 && sm.abort_flag) atomicExch(p.error_word, 4);   // ATTN_ERR_TIMEOUT
 }
 
-template <int DH>
+template <int DH, bool PK = false>
 constexpr size_t prefill_smem_bytes() {
-  return sizeof(PrefillSmem<DH>) + 1024;   // + alignment slack
+  return sizeof(PrefillSmem<DH, PK>) + 1024;   // + alignment slack
 }
 
 }  // namespace chs

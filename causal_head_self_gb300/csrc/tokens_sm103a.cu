@@ -60,6 +60,9 @@ cudaError_t launch_rope(const RopeShape& s, const RopeRows& q, const RopeRows* q
                     grid, block, smem, stream, p);
 }
 
+// Tokens that the plan's own cluster fills in: beyond, it takes longer than another launch.
+constexpr int kPlanFillRows = 16384;
+
 int cache_plan_max_sequences() { return kPlanMaxB; }
 
 cudaError_t launch_cache_plan(const CachePlan& c, const DeviceInfo& dev, cudaStream_t stream) {
@@ -88,9 +91,12 @@ cudaError_t launch_cache_plan(const CachePlan& c, const DeviceInfo& dev, cudaStr
                                 (int)plan_smem_bytes(kPlanMaxB));
   });
   if (e != cudaSuccess) return e;
-  // one CTA where its threads write no more than four entries each, else a cluster
+  // one CTA where its threads write no more than four entries each, else a cluster; more
+  // tokens than that are a second launch's
+  p.fill = c.T <= kPlanFillRows;
   int ctas = 1;
-  while (ctas < kPlanMaxCtas && (long long)c.T + c.B > 4ll * kPlanThreads * ctas) ctas *= 2;
+  while (ctas < kPlanMaxCtas && (p.fill ? c.T : 0) + c.B > 4ll * kPlanThreads * ctas) ctas *= 2;
+  if (!p.fill) ctas = kPlanMaxCtas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kPlanThreads);
@@ -105,7 +111,11 @@ cudaError_t launch_cache_plan(const CachePlan& c, const DeviceInfo& dev, cudaStr
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, attn_cache_plan_sm103a, p);
+  e = cudaLaunchKernelEx(&cfg, attn_cache_plan_sm103a, p);
+  if (e != cudaSuccess || p.fill) return e;
+  constexpr int per = kFillThreads * kFillRows;
+  return launch_pdl(attn_cache_fill_sm103a, dim3((unsigned)((c.T + (long long)per - 1) / per)),
+                    dim3(kFillThreads), 0, stream, p);
 }
 
 }  // namespace chs

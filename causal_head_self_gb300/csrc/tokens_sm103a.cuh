@@ -202,7 +202,9 @@ __global__ void __launch_bounds__(kRopeThreads)
 // and the first write, and then write a share each.  Two accesses need no
 // order: pages are read from the stack below its old top and from columns
 // that shrinking sequences leave, and written above the old top and to
-// columns that growing sequences gain.
+// columns that growing sequences gain.  Many tokens' positions and slots
+// (262144 of 2048 sequences: 63 us on eight SMs, PPPP so) are left to a second
+// launch on every SM, which finds all it needs in the first one's results.
 
 struct PlanParams {
   const int* delta;      // [B]
@@ -215,6 +217,7 @@ struct PlanParams {
   int* cu;               // [B + 1]
   int *positions, *slots;   // [T]
   int B, cols, page, num_pages, capacity, T;
+  int fill;              // the tokens' positions and slots too
   FixedDiv div_page;
   int* error_word;
 };
@@ -335,7 +338,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     for (int b = T0; b < p.B; b += TN) p.seqlens_out[b] = rows[b];
     for (int b = T0; b <= p.B; b += TN) p.cu[b] = 0;
     if (T0 == 0) *p.num_free_out = top;
-    for (int i = T0; i < p.T; i += TN) p.positions[i] = p.slots[i] = -1;
+    for (int i = T0; p.fill && i < p.T; i += TN) p.positions[i] = p.slots[i] = -1;
     return;
   }
   // entry i of the stack after the pages given back were pushed
@@ -357,7 +360,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     p.table[(size_t)b * p.cols + pages_of(rows[b]) + (i - take[b])] = pop(i);
   }
   for (int i = top + T0; i < top + (int)(given - taken); i += TN) p.free_pages[i] = stack(i);
-  for (int i = T0; i < p.T; i += TN) {
+  for (int i = T0; p.fill && i < p.T; i += TN) {
     int pos = -1, slot = -1;
     if (i < (int)tokens) {
       const int b = plan_find(tok, p.B, i), held = pages_of(rows[b]);
@@ -371,6 +374,55 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
     p.positions[i] = pos;
     p.slots[i] = slot;
+  }
+}
+
+// The tokens' positions and slots, from the plan's results: four in a row per thread.
+constexpr int kFillThreads = 256, kFillRows = 4;
+__global__ void __launch_bounds__(kFillThreads)
+    attn_cache_fill_sm103a(const PlanParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tokens = min(__ldcg(p.cu + p.B), p.T);
+  const int i0 = (blockIdx.x * kFillThreads + threadIdx.x) * kFillRows;
+  if (i0 >= p.T) return;
+  int b = 0, first = 0, next = 0;   // rows first .. next - 1 are sequence b's
+  if (i0 < tokens) {
+    int lo = 0, hi = p.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (p.cu[mid] <= i0) lo = mid; else hi = mid;
+    }
+    b = lo;
+    first = p.cu[b];
+    next = p.cu[b + 1];
+  }
+  int pos[kFillRows], slot[kFillRows];
+#pragma unroll
+  for (int e = 0; e < kFillRows; ++e) {
+    const int i = i0 + e;
+    pos[e] = slot[e] = -1;
+    if (i < tokens) {
+      while (i >= next) {
+        ++b;
+        first = next;
+        next = p.cu[b + 1];
+      }
+      pos[e] = p.seqlens_out[b] - (next - first) + (i - first);
+      const int col = p.div_page.div(pos[e]);
+      const int pg = p.table[(size_t)b * p.cols + col];
+      if ((unsigned)pg < (unsigned)p.num_pages)
+        slot[e] = pg * p.page + (pos[e] - col * p.page);
+      else
+        atomicCAS(p.error_word, 0, 1);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < kFillRows; ++e) {
+    if (i0 + e < p.T) {
+      p.positions[i0 + e] = pos[e];
+      p.slots[i0 + e] = slot[e];
+    }
   }
 }
 

@@ -435,8 +435,9 @@ int attn_fwd_packed(const attn_rows_t* q, const attn_rows_t* k, const attn_rows_
                     size_t workspace_bytes, int B, int Hq, int Hkv, int T, int Dh, int causal,
                     int window, float scale, cudaStream_t stream);
 
-/* The workspace of an attn_fwd_packed call, in bytes. */
-int attn_fwd_packed_workspace(int B, int T, size_t* bytes);
+/* The workspace of an attn_fwd_packed call on the current device, in bytes: a list of
+ * blocks; 0 for causal calls of few sequences, whose workspace may be NULL. */
+int attn_fwd_packed_workspace(int B, int Hq, int T, int Dh, int causal, size_t* bytes);
 
 /*
  * attn_bwd_packed -- attn_bwd of every sequence: dq [T, Hq, Dh], dk and dv

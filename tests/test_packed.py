@@ -133,6 +133,44 @@ def test_many_sequences(Dh):
         ref.check(got[real], w[real], b[real], name)
 
 
+@pytest.mark.parametrize("Dh,lens", [(64, [3000, 5, 2500]), (128, [3300, 2900, 900]),
+                                     (128, [700, 900, 40, 1300]), (256, [2000, 1300])])
+def test_several_items_a_cta(Dh, lens):
+    # many heads: every SM takes several blocks, of its own list and of the launch's
+    q, k, v, dout, cu, T = case(lens, 32, 4, Dh)
+    real = slice(cu[0], cu[-1])
+    want, _, bound = ref.attention(q, k, v, cu, True, 600)
+    whole, _, wide = ref.attention(q, k, v, cu, False)
+    o, p = torch.full_like(q, 7), torch.full_like(q, 7)
+    chs.attn_fwd_packed(q, k, v, i32(cu), o, window=600)
+    chs.attn_fwd_packed(q, k, v, i32(cu), p, causal=False)
+    assert chs.attn_status() == chs.ATTN_OK
+    ref.check(o[real], want[real], bound[real], "causal")
+    ref.check(p[real], whole[real], wide[real], "not causal")
+    assert outside_is(o, 7, cu) and outside_is(p, 7, cu)
+
+
+def test_workspaces():
+    gen = torch.Generator("cuda").manual_seed(0)
+    q, k, v = ref.layouts(2000, 4, 2, 128, "fused", gen)
+    cu = i32([0, 700, 2000])
+    assert chs.attn_packed_workspace(q, cu) == 0          # few sequences: none
+    many = i32(list(range(0, 2001, 20)))
+    need = chs.attn_packed_workspace(q, many)
+    assert need > 0
+    back = chs.attn_packed_workspace(q, cu, backward=True)
+    want = chs.attn_fwd_packed(q, k, v, many)
+    with pytest.raises(chs.AttnError):
+        chs.attn_fwd_packed(q, k, v, many, workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+    ws = torch.full((max(need, back),), 255, dtype=torch.uint8, device="cuda")
+    assert torch.equal(chs.attn_fwd_packed(q, k, v, many, workspace=ws), want)
+    lse = torch.zeros(4, 2000, device="cuda")
+    o = chs.attn_fwd_packed(q, k, v, cu, None, lse, workspace=ws)
+    grads = chs.attn_bwd_packed(q, k, v, o, o, lse, cu, workspace=ws)
+    again = chs.attn_bwd_packed(q, k, v, o, o, lse, cu)
+    assert all(torch.equal(a, b) for a, b in zip(grads, again)) and chs.attn_status() == chs.ATTN_OK
+
+
 def test_gradients_against_differences():
     # a step of the loss sum(o * dout) along a direction; 64-bit reference at both ends
     q, k, v, dout, cu, T = case([70, 130], 4, 2, 64, "contiguous", seed=9)

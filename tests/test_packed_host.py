@@ -87,8 +87,8 @@ def test_packed_tensors(lib, call, names):
     for bad in (dict(cu=None), dict(cu=ptr(21) + 2), dict(lse=ptr(20) + 2), dict(ws=None),
                 dict(ws=ptr(22) + 128), dict(ws=ptr(21)), dict(ws=ptr(20)), dict(ws=ptr(0))):
         assert call(lib, **bad) == INVALID, bad
-    assert call(lib, ws_bytes=255) == SCRATCH
     if call is bwd:
+        assert call(lib, ws_bytes=255) == SCRATCH
         assert call(lib, lse=None) == INVALID
 
 
@@ -101,8 +101,7 @@ def test_slices_of_one_tensor_are_apart(lib):
             out[n] = rows(0, data=base + at * 256, row=8 * 128)
             at += HEADS[n] - skip
         return out
-    few = dict(ws_bytes=0)
-    assert fwd(lib, tensors=slices(ptr(0), "qkv"), **few) == SCRATCH
+    few = dict(ws_bytes=256)
     both = dict(slices(ptr(0), "qkv"), **slices(ptr(1), ("dq", "dk", "dv")),
                 o=rows(2), dout=rows(3))
     order = ["q", "k", "v", "o", "dout", "dq", "dk", "dv"]
@@ -116,18 +115,17 @@ def test_slices_of_one_tensor_are_apart(lib):
 
 
 def test_packed_workspace_queries(lib):
+    # (the forward's answer depends on the GPU: only its refusals here)
     n = ctypes.c_size_t()
-    assert lib.attn_fwd_packed_workspace(3, 1000, ctypes.byref(n)) == OK
-    small = n.value
-    assert small >= 16 * (1000 // 128 + 3)
     assert lib.attn_bwd_packed_workspace(3, 8, 1000, ctypes.byref(n)) == OK
-    assert n.value >= 2 * small + 2 * 4 * 8 * 1000
-    for f, shape in ((lib.attn_fwd_packed_workspace, (3, 1000)),
-                     (lib.attn_bwd_packed_workspace, (3, 8, 1000))):
-        assert f(*shape, None) == INVALID
-        assert f(-1, *shape[1:], ctypes.byref(n)) == INVALID
-        assert f(*shape[:-1], -1, ctypes.byref(n)) == INVALID
-        assert f(*shape[:-1], 2 ** 31 - 1, ctypes.byref(n)) == INVALID
+    assert n.value >= 2 * 16 * (1000 // 128 + 3) + 2 * 4 * 8 * 1000
+    assert lib.attn_bwd_packed_workspace(3, 8, 1000, None) == INVALID
+    for bad in ((-1, 8, 1000), (3, 0, 1000), (3, 8, -1), (3, 8, 2 ** 31 - 1), (1 << 25, 8, 1000)):
+        assert lib.attn_bwd_packed_workspace(*bad, ctypes.byref(n)) == INVALID, bad
+        assert lib.attn_fwd_packed_workspace(*bad, 128, 1, ctypes.byref(n)) == INVALID, bad
+    assert lib.attn_fwd_packed_workspace(3, 8, 1000, 96, 1, ctypes.byref(n)) == UNSUPPORTED
+    assert lib.attn_fwd_packed_workspace(3, 8, 1000, 128, 2, ctypes.byref(n)) == INVALID
+    assert lib.attn_fwd_packed_workspace(3, 8, 1000, 128, 1, None) == INVALID
 
 
 def rope(lib, append=False, q=None, qo=None, k=None, ko="given", v=None, positions=ptr(20),

@@ -222,7 +222,7 @@ def plan_by_hand(lens, delta, table, stack, page):
 @pytest.mark.parametrize("in_place", [True, False])
 @pytest.mark.parametrize("B,page,lmax,grow", [
     (1, 8, 0, 1), (1, 16, 100, 5), (5, 24, 300, 40), (64, 16, 1000, 1), (33, 64, 200, 700),
-    (1025, 16, 60, 3), (3000, 8, 90, 20), (8192, 8, 20, 2), (2, 256, 5000, 9000)])
+    (1025, 16, 60, 3), (3000, 8, 90, 20), (8192, 8, 20, 2), (2, 256, 5000, 9000), (300, 16, 700, 400)])
 def test_plan(B, page, lmax, grow, in_place):
     rng = random.Random(B + page)
     lens, delta, table, stack, P = plan_case(rng, B, page, lmax, grow)
