@@ -616,13 +616,16 @@ def _heads(name, t, shape, device):
     raise ValueError(f"{name} must be on the same device as the other tensors")
 
 
+_MOST = 0x7fffffff
+
+
 def _packed_shape(q, k, cu_seqlens):
     """B, Hq, Hkv, T, Dh and device of a packed call."""
     T, Hq, Dh = _shape("q", q, 3)
     Hkv = _shape("k", k, 3)[1]
-    n = _shape("cu_seqlens", cu_seqlens, 1)[0]
-    if n < 1 or n > 0x7fffffff or T > 0x7fffffff:
-        raise ValueError("cu_seqlens must have B + 1 entries, and less than 2^31 rows")
+    n, = _shape("cu_seqlens", cu_seqlens, 1)
+    if n < 1 or n > _MOST or T > _MOST or Hq > _MOST:
+        raise ValueError("cu_seqlens must have B + 1 entries, and less than 2^31 rows and heads")
     device = q.get_device()
     if device < 0:
         raise TypeError("q must be a CUDA bfloat16 tensor")
@@ -676,7 +679,7 @@ def attn_fwd_packed(q, k, v, cu_seqlens, o=None, lse=None, *, causal=True, windo
     here).  workspace: a uint8 tensor of attn_packed_workspace() bytes (None:
     allocated here by torch, on the call's stream, where any is needed).
     Returns o."""
-    window, causal = _int32("window", window), int(bool(causal))
+    window, causal = _int32("window", window), 1 if causal else 0
     B, Hq, Hkv, T, Dh, device = _packed_shape(q, k, cu_seqlens)
     rq = _heads("q", q, (T, Hq, Dh), device)
     rk = _heads("k", k, (T, Hkv, Dh), device)
@@ -756,27 +759,30 @@ def attn_rope_frequencies(rotary_dim, base=10000.0, *, scaling="none", factor=1.
     return RopeFrequencies(turns.to(device), amplitude.value)
 
 
-def _rope_shape(q, k, positions, frequencies):
+def _rope_shape(q, k, positions, turns):
     """What both rotations check: B, S, Hq, Hkv, Dh, rotary_dim, device and the shapes."""
-    shape = getattr(q, "shape", None)
-    if shape is None or len(shape) not in (3, 4):
+    shape = getattr(q, "shape", ())
+    axes = len(shape)
+    if axes == 3:
+        S, Hq, Dh = shape
+        Hkv = _shape("k", k, 3)[1]
+        B, kshape, pshape = 1, (S, Hkv, Dh), (S,)
+    elif axes == 4:
+        B, Hq, S, Dh = shape
+        Hkv = _shape("k", k, 4)[1]
+        kshape, pshape = (B, Hkv, S, Dh), (B, S)
+    else:
         raise ValueError("q must be [T,Hq,Dh] or [B,Hq,S,Dh]")
-    packed = len(shape) == 3
-    Hkv = _shape("k", k, len(shape))[1]
-    Hq, Dh = shape[1], shape[-1]
-    B, S = (1, shape[0]) if packed else (shape[0], shape[2])
-    for name, x in (("batch", B), ("rows", S), ("heads", max(Hq, Hkv))):
-        _int32(name, x)
-    kshape = (S, Hkv, Dh) if packed else (B, Hkv, S, Dh)
+    if S > _MOST or B > _MOST or Hq > _MOST or Hkv > _MOST:
+        raise ValueError("q and k must have less than 2^31 entries along each axis")
     device = q.get_device()
     if device < 0:
         raise TypeError("q must be a CUDA bfloat16 tensor")
     _check_current(device)
-    _check("positions", positions, torch.int32, (S,) if packed else (B, S), device)
-    turns = frequencies.turns
-    n = _shape("turns", turns, 1)[0]
+    _check("positions", positions, torch.int32, pshape, device)
+    n, = _shape("turns", turns, 1)
     _check("turns", turns, torch.int64, (n,), device)
-    return B, S, Hq, Hkv, Dh, 2 * n, device, tuple(shape), kshape
+    return B, S, Hq, Hkv, Dh, 2 * n, device, shape, kshape
 
 
 def attn_rope(q, k, positions, frequencies, q_out=None, k_out=None, *, interleaved=False,
@@ -788,14 +794,17 @@ def attn_rope(q, k, positions, frequencies, q_out=None, k_out=None, *, interleav
     leaves the row out.  q_out and k_out may be q and k (in place); None:
     allocated here.  inverse=True turns the other way: the gradients of q and
     k from those of the outputs.  Returns (q_out, k_out)."""
-    B, S, Hq, Hkv, Dh, rot, device, qs, ks = _rope_shape(q, k, positions, frequencies)
+    turns, amplitude = frequencies
+    B, S, Hq, Hkv, Dh, rot, device, qs, ks = _rope_shape(q, k, positions, turns)
     rq, rk = _heads("q", q, qs, device), _heads("k", k, ks, device)
-    q_out = _empty(qs, torch.bfloat16, q.device, stream) if q_out is None else q_out
-    k_out = _empty(ks, torch.bfloat16, q.device, stream) if k_out is None else k_out
+    if q_out is None:
+        q_out = _empty(qs, torch.bfloat16, q.device, stream)
+    if k_out is None:
+        k_out = _empty(ks, torch.bfloat16, q.device, stream)
     rc = load().attn_rope(rq, _heads("q_out", q_out, qs, device), Hq, rk,
                           _heads("k_out", k_out, ks, device), Hkv, positions.data_ptr(),
-                          frequencies.turns.data_ptr(), float(frequencies.amplitude), B, S, Dh,
-                          rot, int(bool(interleaved)), int(bool(inverse)), _stream_handle(stream))
+                          turns.data_ptr(), amplitude, B, S, Dh, rot, 1 if interleaved else 0,
+                          1 if inverse else 0, _stream_handle(stream))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_rope")
     return q_out, k_out
@@ -808,23 +817,25 @@ def attn_rope_append(q, k, v, positions, frequencies, kpages, vpages, slots, q_o
     (attn_cache_plan gives them), a negative one writes nothing there.  q_out
     None: in place.  k_out None: the turned keys go to the cache alone.  Returns
     (q_out, k_out)."""
-    B, S, Hq, Hkv, Dh, rot, device, qs, ks = _rope_shape(q, k, positions, frequencies)
-    P, _, page, _ = pools = _shape("kpages", kpages, 4)
-    if pools[1] != Hkv or pools[3] != Dh:
+    turns, amplitude = frequencies
+    B, S, Hq, Hkv, Dh, rot, device, qs, ks = _rope_shape(q, k, positions, turns)
+    P, pool_heads, page, pool_Dh = pools = _shape("kpages", kpages, 4)
+    if pool_heads != Hkv or pool_Dh != Dh or P > _MOST or page > _MOST:
         raise ValueError("kpages must be [P, Hkv, page, Dh] matching k")
-    _int32("pages", P), _int32("page", page)
     _check("kpages", kpages, torch.bfloat16, pools, device)
     _check("vpages", vpages, torch.bfloat16, pools, device)
     _check("slots", slots, torch.int32, positions.shape, device)
     rq, rk, rv = (_heads("q", q, qs, device), _heads("k", k, ks, device),
                   _heads("v", v, ks, device))
-    q_out = q if q_out is None else q_out
-    rc = load().attn_rope_append(rq, _heads("q_out", q_out, qs, device), Hq, rk,
-                                 None if k_out is None else _heads("k_out", k_out, ks, device), rv,
-                                 Hkv, positions.data_ptr(), frequencies.turns.data_ptr(),
-                                 float(frequencies.amplitude), kpages.data_ptr(),
+    if q_out is None:
+        q_out, rqo = q, rq
+    else:
+        rqo = _heads("q_out", q_out, qs, device)
+    rko = None if k_out is None else _heads("k_out", k_out, ks, device)
+    rc = load().attn_rope_append(rq, rqo, Hq, rk, rko, rv, Hkv, positions.data_ptr(),
+                                 turns.data_ptr(), amplitude, kpages.data_ptr(),
                                  vpages.data_ptr(), slots.data_ptr(), P, page, B, S, Dh, rot,
-                                 int(bool(interleaved)), _stream_handle(stream))
+                                 1 if interleaved else 0, _stream_handle(stream))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_rope_append")
     return q_out, k_out
@@ -843,31 +854,42 @@ def attn_cache_plan(delta, seqlens, table, free_pages, num_free, *, rows, page, 
     -1 behind the last (cu_seqlens[B] of them, the first `rows` of which have
     their place here); where pages do not suffice, nothing changes and
     attn_status() says so.  All int32."""
-    rows, page = _int32("rows", rows), _int32("page", page)
-    num_pages = _int32("num_pages", num_pages)
+    rows, page, num_pages = (_int32("rows", rows), _int32("page", page),
+                             _int32("num_pages", num_pages))
     B, cols = shape = _shape("table", table, 2)
-    capacity = _shape("free_pages", free_pages, 1)[0]
-    for name, x in (("table", max(B, cols)), ("free_pages", capacity)):
-        _int32(name, x)
-    device = table.get_device()
-    _check("table", table, torch.int32, shape, device)
-    _check_current(device)
-    for name, t, n in (("delta", delta, B), ("seqlens", seqlens, B),
-                       ("free_pages", free_pages, capacity), ("num_free", num_free, 1)):
-        _check(name, t, torch.int32, (n,), device)
+    capacity, = _shape("free_pages", free_pages, 1)
+    if B > _MOST or cols > _MOST or capacity > _MOST:
+        raise ValueError("table and free_pages must have less than 2^31 entries along each axis")
     if rows < 0:
         raise AttnError(ATTN_ERR_INVALID_ARG, "attn_cache_plan")
-    seqlens_out = seqlens if seqlens_out is None else seqlens_out
-    num_free_out = num_free if num_free_out is None else num_free_out
-    cu_seqlens = _empty((B + 1,), torch.int32, table.device, stream) if cu_seqlens is None \
-        else cu_seqlens
-    positions = _empty((rows,), torch.int32, table.device, stream) if positions is None \
-        else positions
-    slots = _empty((rows,), torch.int32, table.device, stream) if slots is None else slots
-    for name, t, n in (("seqlens_out", seqlens_out, B), ("num_free_out", num_free_out, 1),
-                       ("cu_seqlens", cu_seqlens, B + 1), ("positions", positions, rows),
-                       ("slots", slots, rows)):
-        _check(name, t, torch.int32, (n,), device)
+    device = table.get_device()
+    int32, batch, one = torch.int32, (B,), (1,)
+    _check("table", table, int32, shape, device)
+    _check_current(device)
+    _check("delta", delta, int32, batch, device)
+    _check("seqlens", seqlens, int32, batch, device)
+    _check("free_pages", free_pages, int32, (capacity,), device)
+    _check("num_free", num_free, int32, one, device)
+    if seqlens_out is None:
+        seqlens_out = seqlens
+    else:
+        _check("seqlens_out", seqlens_out, int32, batch, device)
+    if num_free_out is None:
+        num_free_out = num_free
+    else:
+        _check("num_free_out", num_free_out, int32, one, device)
+    if cu_seqlens is None:
+        cu_seqlens = _empty((B + 1,), int32, table.device, stream)
+    else:
+        _check("cu_seqlens", cu_seqlens, int32, (B + 1,), device)
+    if positions is None:
+        positions = _empty((rows,), int32, table.device, stream)
+    else:
+        _check("positions", positions, int32, (rows,), device)
+    if slots is None:
+        slots = _empty((rows,), int32, table.device, stream)
+    else:
+        _check("slots", slots, int32, (rows,), device)
     rc = load().attn_cache_plan(delta.data_ptr(), seqlens.data_ptr(), seqlens_out.data_ptr(),
                                 table.data_ptr(), free_pages.data_ptr(), num_free.data_ptr(),
                                 num_free_out.data_ptr(), cu_seqlens.data_ptr(),
