@@ -156,8 +156,8 @@ cudaError_t launch_bwd_packed(const PackedShape& s, const PackedRows& q, const P
                               const PackedRows& dv, void* workspace, float scale,
                               const DeviceInfo& dev, cudaStream_t stream);
 // Lists of tiles of `block` rows, heaviest first: list[i] for order[i] (PackedOrder); tiles and
-// counts lie in device memory.
-cudaError_t launch_packed_schedule(const PackedShape& s, int block, int lists, const int* order,
+// counts (three each) lie in device memory.
+cudaError_t launch_packed_schedule(const PackedShape& s, int block, int fold_max, int lists, const int* order,
                                    void* const* tiles, int* const* counts, const DeviceInfo& dev,
                                    cudaStream_t stream);
 

@@ -101,7 +101,7 @@ cudaError_t launch_passes256(const PackedShape& s, const BwdMaps& small_q, const
 
 }  // namespace
 
-// The workspace: two tile counts (256 bytes), two lists, lse2 and D.
+// The workspace: the tile counts (256 bytes), two lists, lse2 and D.
 size_t bwd_packed_workspace_bytes(int B, int Hq, int T) {
   return 256 + 2 * list_bytes(B, T) + 2 * (size_t)Hq * stat_rows(B, T) * sizeof(float);
 }
@@ -112,7 +112,7 @@ cudaError_t launch_bwd_packed(const PackedShape& s, const PackedRows& q, const P
                               const PackedRows& dv, void* workspace, float scale,
                               const DeviceInfo& dev, cudaStream_t stream) {
   char* ws = static_cast<char*>(workspace);
-  int* counts[2] = {reinterpret_cast<int*>(ws), reinterpret_cast<int*>(ws) + 1};
+  int* counts[2] = {reinterpret_cast<int*>(ws), reinterpret_cast<int*>(ws) + 4};
   void* lists[2] = {ws + 256, ws + 256 + list_bytes(s.B, s.T)};
   const int order[2] = {kByQueries, kByKeys};
   // the maps first: nothing is launched where one cannot be made
@@ -121,7 +121,7 @@ cudaError_t launch_bwd_packed(const PackedShape& s, const PackedRows& q, const P
                         !bwd_maps(&m2, s, q, k, v, dout, 128, 64)
                   : !bwd_maps(&m, s, q, k, v, dout, 128, 128))
     return cudaErrorInvalidValue;
-  cudaError_t e = launch_packed_schedule(s, 128, 2, order, lists, counts, dev, stream);
+  cudaError_t e = launch_packed_schedule(s, 128, 0, 2, order, lists, counts, dev, stream);
   if (e != cudaSuccess) return e;
   BwdParams p{};
   p.B = 1;
@@ -149,8 +149,8 @@ cudaError_t launch_bwd_packed(const PackedShape& s, const PackedRows& q, const P
   p.error_word = dev.error_word;
   p.fault = dev.fault;
   BwdParams pk = p, pq = p;
-  pk.pk = PackedRef{static_cast<PackedTile*>(lists[0]), counts[0], s.cu, s.B, 0, s.T, m.heads_inner};
-  pq.pk = PackedRef{static_cast<PackedTile*>(lists[1]), counts[1], s.cu, s.B, 0, s.T, m.heads_inner};
+  pk.pk = PackedRef{static_cast<PackedTile*>(lists[0]), counts[0], s.cu, s.B, 0, s.T, m.heads_inner, 0};
+  pq.pk = PackedRef{static_cast<PackedTile*>(lists[1]), counts[1], s.cu, s.B, 0, s.T, m.heads_inner, 0};
   e = s.Dh == 256   ? launch_prep<256>(s, o, dout, lse, pq, dev, stream)
       : s.Dh == 128 ? launch_prep<128>(s, o, dout, lse, pq, dev, stream)
                     : launch_prep<64>(s, o, dout, lse, pq, dev, stream);

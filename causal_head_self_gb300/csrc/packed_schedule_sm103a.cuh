@@ -42,8 +42,8 @@ __global__ void __launch_bounds__(kScheduleThreads)
   if (lane == 0) atomicMax(&most, longest);
   __syncthreads();
   if (bad) {
+    if (t < 3) p.num_tiles[blockIdx.x][t] = 0;
     if (t == 0) {
-      *p.num_tiles[blockIdx.x] = 0;
       atomicExch(p.error_word, 1);   // ATTN_ERR_INVALID_ARG
     }
     return;
@@ -51,8 +51,11 @@ __global__ void __launch_bounds__(kScheduleThreads)
   // a tile's bin, the heaviest in bin 0 (rows are padded ones)
   auto padded = [](int len) { return (len + 127) / 128 * 128; };
   const int max_cost = (most + 127) / 128;
-  const int shift = max_cost < kScheduleBins ? 0 : 32 - __clz(max_cost / kScheduleBins);
-  auto bin_of = [&](int len, int blk) {
+  // (the last two bins take the tiles of two and of four heads)
+  const int shift = max_cost < kScheduleBins - 2 ? 0 : 33 - __clz(max_cost / kScheduleBins);
+  const int fold_max = p.fold_max;
+  auto bin_of = [&](int len, int blk, int fold) {
+    if (fold) return kScheduleBins - 3 + fold;
     const int nb = len / 128, r0 = blk << blk_shift, r1 = min(len, r0 + p.block) - 1;
     int lo = 0, hi = nb - 1;
     if (p.causal) {
@@ -68,8 +71,9 @@ __global__ void __launch_bounds__(kScheduleThreads)
   };
   // a warp per sequence, a lane per block
   for (int b = warp; b < p.B; b += kWarps) {
-    const int len = padded(p.cu[b + 1] - p.cu[b]), n = (len + p.block - 1) >> blk_shift;
-    for (int i = lane; i < n; i += 32) atomicAdd(&hist[bin_of(len, i)], 1);
+    const int rows = p.cu[b + 1] - p.cu[b], fold = packed_fold(rows, fold_max);
+    const int len = padded(rows), n = (len + p.block - 1) >> blk_shift;
+    for (int i = lane; i < n; i += 32) atomicAdd(&hist[bin_of(len, i, fold)], 1);
   }
   __syncthreads();
   // where each bin's tiles start
@@ -96,15 +100,21 @@ __global__ void __launch_bounds__(kScheduleThreads)
   const int before = (warp > 0 ? warp_sum[warp - 1] : 0) + run - h0 - h1;
   hist[2 * t] = before;
   hist[2 * t + 1] = before + h0;
-  if (t == kScheduleThreads - 1) *p.num_tiles[blockIdx.x] = before + h0 + h1;
+  if (t == kScheduleThreads - 1) {
+    int* n = p.num_tiles[blockIdx.x];
+    n[0] = before;
+    n[1] = h0;
+    n[2] = h1;
+  }
   __syncthreads();
   for (int b = warp; b < p.B; b += kWarps) {
     const int a = p.cu[b], len = p.cu[b + 1] - a, n = (len + p.block - 1) >> blk_shift;
     // rows of the earlier sequences, each rounded up to 128: at most a + 127 b, so a
     // sequence may start at the next multiple of 128 and no two meet
     const int stat = (int)(((long long)a + 127ll * b + 127) / 128 * 128);
+    const int fold = packed_fold(len, fold_max);
     for (int i = lane; i < n; i += 32) {
-      const int at = atomicAdd(&hist[bin_of(padded(len), i)], 1);
+      const int at = atomicAdd(&hist[bin_of(padded(len), i, fold)], 1);
       *reinterpret_cast<int4*>(tiles + at) = make_int4(a, len, i, stat);
     }
   }

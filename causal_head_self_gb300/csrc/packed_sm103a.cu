@@ -7,7 +7,7 @@
 
 namespace chs {
 
-cudaError_t launch_packed_schedule(const PackedShape& s, int block, int lists, const int* order,
+cudaError_t launch_packed_schedule(const PackedShape& s, int block, int fold_max, int lists, const int* order,
                                    void* const* tiles, int* const* counts, const DeviceInfo& dev,
                                    cudaStream_t stream) {
   PackedSchedule p{};
@@ -17,6 +17,7 @@ cudaError_t launch_packed_schedule(const PackedShape& s, int block, int lists, c
   p.block = block;
   p.causal = s.causal;
   p.window = s.window;
+  p.fold_max = fold_max;
   for (int i = 0; i < lists; ++i) {
     p.tiles[i] = static_cast<PackedTile*>(tiles[i]);
     p.order[i] = order[i];
@@ -35,9 +36,9 @@ struct FwdMaps {
 
 // Box heights: q_rows, kv_rows, 32 output rows (one softmax warp's).
 bool fwd_maps(FwdMaps* m, const PackedShape& s, const PackedRows& q, const PackedRows& k,
-              const PackedRows& v, const PackedRows& o, int kv_rows) {
+              const PackedRows& v, const PackedRows& o, int q_rows, int kv_rows) {
   bool hq, hk, hv, ho;
-  if (!encode_packed_map(&m->q, q, s.Dh, s.T, 128, true, &hq) ||
+  if (!encode_packed_map(&m->q, q, s.Dh, s.T, q_rows, true, &hq) ||
       !encode_packed_map(&m->k, k, s.Dh, s.T, kv_rows, true, &hk) ||
       !encode_packed_map(&m->v, v, s.Dh, s.T, kv_rows, true, &hv) ||
       !encode_packed_map(&m->o, o, s.Dh, s.T, 32, false, &ho))
@@ -54,7 +55,7 @@ cudaError_t launch_wide(const PackedShape& s, const PackedRows& q, const PackedR
   constexpr size_t smem = prefill_smem_bytes<DH, true>();
   static_assert(smem <= 232448, "shared memory budget of one sm_103a CTA");
   FwdMaps m;
-  if (!fwd_maps(&m, s, q, k, v, o, 128)) return cudaErrorInvalidValue;
+  if (!fwd_maps(&m, s, q, k, v, o, 128, 128)) return cudaErrorInvalidValue;
   // the register split needs the full launch registers, as in the batch form
   static std::atomic<int> configured[kMaxDevices];
   cudaError_t e = configure_once(configured, dev.device, [] {
@@ -95,8 +96,9 @@ cudaError_t launch_k64(const PackedShape& s, const PackedRows& q, const PackedRo
                        float scale_log2, const DeviceInfo& dev, cudaStream_t stream) {
   using Cfg = PrefillK64Cfg<DH>;
   constexpr size_t smem = prefill_k64_smem_bytes<DH, true>();
+  const int q_rows = ref.fold_max ? 32 : 128;
   FwdMaps m;
-  if (!fwd_maps(&m, s, q, k, v, o, Cfg::kKeys)) return cudaErrorInvalidValue;
+  if (!fwd_maps(&m, s, q, k, v, o, q_rows, Cfg::kKeys)) return cudaErrorInvalidValue;
   static std::atomic<int> configured[kMaxDevices];
   cudaError_t e = configure_once(configured, dev.device, [] {
     return cudaFuncSetAttribute(attn_prefill_k64_sm103a<DH, true>,
@@ -120,6 +122,7 @@ cudaError_t launch_k64(const PackedShape& s, const PackedRows& q, const PackedRo
   p.fault = dev.fault;
   p.pk = ref;
   p.pk.heads_inner = m.heads_inner;
+  p.q_rows = q_rows;
   const long long most = packed_max_tiles(s.B, s.T) * s.Hq;
   const int cap = Cfg::kCtasPerSm * dev.num_sms;
   const int grid = most < cap ? (int)most : cap;
@@ -127,11 +130,22 @@ cudaError_t launch_k64(const PackedShape& s, const PackedRows& q, const PackedRo
                     stream, m.q, m.k, m.v, m.o, p);
 }
 
-// Head size 128: the 64-key kernel up to this many rows per sequence on average.
-constexpr int kPackedK64MeanRows128 = 1536;
+// Head sizes 64 and 128: the 64-key kernel up to this many rows per sequence on average.
+constexpr int kPackedK64MeanRows64 = 1536, kPackedK64MeanRows128 = 1536;
 
 bool takes_k64(int B, int T, int Dh) {
-  return Dh == 256 || (Dh == 128 && T <= (long long)kPackedK64MeanRows128 * B);
+  return Dh == 256 ||
+         T <= (long long)(Dh == 64 ? kPackedK64MeanRows64 : kPackedK64MeanRows128) * B;
+}
+
+// Two or four query heads of a K/V head in one tile of a short sequence, where sequences are
+// short on average (Q then comes in boxes of 32 rows).
+constexpr int kFoldMeanRows = 256;
+
+int fold_max_of(const PackedShape& s) {
+  const int group = s.Hq / s.Hkv;
+  if (!takes_k64(s.B, s.T, s.Dh) || s.T > (long long)kFoldMeanRows * s.B) return 0;
+  return group % 4 == 0 ? 2 : group % 2 == 0 ? 1 : 0;
 }
 
 // Does each CTA list its own items?  Few sequences, no more than a lane's item each per CTA, and
@@ -139,7 +153,7 @@ bool takes_k64(int B, int T, int Dh) {
 bool lists_own(const PackedShape& s, const DeviceInfo& dev) {
   const bool k64 = takes_k64(s.B, s.T, s.Dh);
   const int block = k64 ? 128 : 256;
-  const int ctas = (k64 && s.Dh == 128 ? 2 : 1) * dev.num_sms;
+  const int ctas = (k64 && s.Dh <= 128 ? 2 : 1) * dev.num_sms;
   const long long items = ((long long)s.T / block + s.B) * s.Hq;
   return s.causal && s.B <= kOwnSequences && s.T / block + 1 <= kOwnLevels &&
          items <= (long long)ctas * kOwnItems;
@@ -147,7 +161,7 @@ bool lists_own(const PackedShape& s, const DeviceInfo& dev) {
 
 }  // namespace
 
-// The workspace: the tile count (256 bytes), then the list.
+// The workspace: the tile counts (256 bytes), then the list.
 size_t fwd_packed_workspace_bytes(const PackedShape& s, const DeviceInfo& dev) {
   if (lists_own(s, dev)) return 0;
   return 256 + ((size_t)packed_max_tiles(s.B, s.T) * sizeof(PackedTile) + 255) / 256 * 256;
@@ -159,18 +173,21 @@ cudaError_t launch_fwd_packed(const PackedShape& s, const PackedRows& q, const P
                               cudaStream_t stream) {
   const bool k64 = takes_k64(s.B, s.T, s.Dh);
   const int block = k64 ? 128 : 256;
-  PackedRef ref{nullptr, nullptr, s.cu, s.B, s.T / block + 1, s.T, 0};
+  const int fold_max = fold_max_of(s);
+  PackedRef ref{nullptr, nullptr, s.cu, s.B, s.T / block + 1, s.T, 0, fold_max};
   if (!lists_own(s, dev)) {
     int* count = static_cast<int*>(workspace);
     void* tiles = static_cast<char*>(workspace) + 256;
     const int order = kByKeys;
-    const cudaError_t e = launch_packed_schedule(s, block, 1, &order, &tiles, &count, dev, stream);
+    const cudaError_t e = launch_packed_schedule(s, block, fold_max, 1, &order, &tiles, &count, dev, stream);
     if (e != cudaSuccess) return e;
     ref.tiles = static_cast<PackedTile*>(tiles);
     ref.num_tiles = count;
   }
   if (s.Dh == 256) return launch_k64<256>(s, q, k, v, o, lse, ref, scale_log2, dev, stream);
-  if (k64) return launch_k64<128>(s, q, k, v, o, lse, ref, scale_log2, dev, stream);
+  if (k64)
+    return s.Dh == 128 ? launch_k64<128>(s, q, k, v, o, lse, ref, scale_log2, dev, stream)
+                       : launch_k64<64>(s, q, k, v, o, lse, ref, scale_log2, dev, stream);
   return s.Dh == 128 ? launch_wide<128>(s, q, k, v, o, lse, ref, scale_log2, dev, stream)
                      : launch_wide<64>(s, q, k, v, o, lse, ref, scale_log2, dev, stream);
 }

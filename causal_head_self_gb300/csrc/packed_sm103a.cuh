@@ -45,13 +45,19 @@ constexpr int kPackedQ = 1, kPackedK = 2, kPackedV = 4, kPackedO = 8, kPackedDO 
 
 struct PackedRef {
   const PackedTile* tiles;   // heaviest first; null: each CTA lists its own items
-  const int* num_tiles;
+  const int* num_tiles;      // [3] of one head each, then those of two and of four heads
   const int* cu;             // [B + 1], B and the most blocks of a sequence, for that
   int B, levels;
   int T;                     // rows of the packed tensors
   int heads_inner;           // tensors whose heads lie closer than their rows: map axes
                              // {Dh, head, rows, start} instead of {Dh, rows, start, head}
+  int fold_max;              // short sequences: up to 1 << fold_max heads lie in one tile
 };
+
+// How many heads (1 << fold) of a sequence lie in one tile: of up to 32 rows four, of up to 64 two.
+__device__ __forceinline__ int packed_fold(int len, int fold_max) {
+  return len > 64 ? 0 : min(fold_max, len > 32 ? 1 : 2);
+}
 
 // Read past L1: the list was written by the launch before this one.
 __device__ __forceinline__ PackedTile packed_tile(const PackedRef& p, int i) {
@@ -59,6 +65,33 @@ __device__ __forceinline__ PackedTile packed_tile(const PackedRef& p, int i) {
   return PackedTile{e.x, e.y, e.z, e.w};
 }
 __device__ __forceinline__ int packed_num_tiles(const PackedRef& p) { return __ldcg(p.num_tiles); }
+
+// Work items of tiles of one, two and four heads.
+__device__ __forceinline__ int3 packed_counts(const PackedRef& p) {
+  return make_int3(__ldcg(p.num_tiles), __ldcg(p.num_tiles + 1), __ldcg(p.num_tiles + 2));
+}
+__device__ __forceinline__ int packed_items(const int3& n, int Hq) {
+  return n.x * Hq + n.y * (Hq / 2) + n.z * (Hq / 4);
+}
+// Item w: tile i, its first head h.  A tile's heads come one after another: those of a group
+// share their K/V tiles in L2.
+__device__ __forceinline__ void packed_item_of(const int3& n, int Hq, int w, int& i, int& h) {
+  int fold = 0, first = 0;
+  if (w >= n.x * Hq) {
+    w -= n.x * Hq;
+    first = n.x;
+    fold = 1;
+    if (w >= n.y * (Hq / 2)) {
+      w -= n.y * (Hq / 2);
+      first += n.y;
+      fold = 2;
+    }
+  }
+  const int per = Hq >> fold;
+  i = w / per;
+  h = (w - i * per) << fold;
+  i += first;
+}
 
 __device__ __forceinline__ void tma_load_4d_hint(void* dst, const CUtensorMap* map, uint64_t* bar,
                                                  int c0, int c1, int c2, int c3, uint64_t policy) {
@@ -103,11 +136,12 @@ struct PackedOwn {
 };
 
 // Bytes of shared memory that listing takes (it may be a buffer of the kernel's).
-constexpr int kOwnScratch = 8 * kOwnLevels + 4 * (kOwnLevels + 1) + 3 * 4 * kOwnSequences + 16;
+constexpr int kOwnScratch = 8 * kOwnLevels + 4 * (kOwnLevels + 1) + 3 * 4 * kOwnSequences + 32;
 
 // All threads of the CTA.  Items are numbered by block, the last (under a
-// causal mask: the heaviest) first, then by sequence, then by head; item_of(k,
-// items) is the number of this CTA's k-th.  For each block number the threads
+// causal mask: the heaviest) first, then by sequence, then by head, and after
+// them those of two heads and of four; item_of(k, items) is the number of this
+// CTA's k-th.  For each block number the threads
 // make the mask of the sequences that have it and the count of tiles from it
 // on; then a lane per item finds its block by bisection and its sequence as a
 // bit of the mask.
@@ -118,7 +152,8 @@ __device__ __forceinline__ void packed_list_own(const PackedRef& p, int Hq, void
   int* tiles = reinterpret_cast<int*>(mask + kOwnLevels);              // [kOwnSequences] each one's
   int* start = tiles + kOwnSequences;
   int* len = start + kOwnSequences;
-  int* from = len + kOwnSequences;                                     // [levels + 1]
+  unsigned* folded = reinterpret_cast<unsigned*>(len + kOwnSequences);  // [4] masks by fold
+  int* from = reinterpret_cast<int*>(folded + 4);                      // [levels + 1]
   const int t = threadIdx.x;
   bool bad = false;
   if (t < kOwnSequences) {
@@ -128,9 +163,17 @@ __device__ __forceinline__ void packed_list_own(const PackedRef& p, int Hq, void
       n = __ldcg(p.cu + t + 1) - a;
       bad = a < 0 || n < 0 || n > p.T - a;
     }
+    const int fold = bad || n == 0 ? 0 : packed_fold(n, p.fold_max);
     start[t] = a;
     len[t] = n;
-    tiles[t] = bad ? 0 : (n + 127) / 128 * 128 / BLOCK + ((n + 127) / 128 * 128 % BLOCK != 0);
+    tiles[t] = bad || fold ? 0
+                           : (n + 127) / 128 * 128 / BLOCK + ((n + 127) / 128 * 128 % BLOCK != 0);
+    const unsigned two = __ballot_sync(0xffffffffu, fold == 1);
+    const unsigned four = __ballot_sync(0xffffffffu, fold == 2);
+    if (t % 32 == 0) {
+      folded[t / 32] = two;
+      folded[2 + t / 32] = four;
+    }
   }
   if (__syncthreads_or(bad)) {
     if (t == 0) own.count = 0;
@@ -153,19 +196,31 @@ __device__ __forceinline__ void packed_list_own(const PackedRef& p, int Hq, void
   }
   __syncthreads();
   if (t < 32) {
-    const int items = from[0] * Hq, w = item_of(t, items);
+    const uint64_t two = folded[0] | (uint64_t)folded[1] << 32;
+    const uint64_t four = folded[2] | (uint64_t)folded[3] << 32;
+    const int3 n = make_int3(from[0], __popcll(two), __popcll(four));
+    const int items = packed_items(n, Hq), w = item_of(t, items);
     const bool mine = w < items;
     if (mine) {
-      const int i = w / Hq;
-      int lo = 0, hi = p.levels;   // from[lo] > i >= from[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (from[mid] > i) lo = mid; else hi = mid;
+      int i, h, lo = 0;
+      packed_item_of(n, Hq, w, i, h);
+      uint64_t m = two;
+      int r = i - n.x;   // the r-th sequence of the mask
+      if (r >= n.y) {
+        m = four;
+        r -= n.y;
+      } else if (r < 0) {
+        int hi = p.levels;   // from[lo] > i >= from[hi]
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) / 2;
+          if (from[mid] > i) lo = mid; else hi = mid;
+        }
+        m = mask[lo];
+        r = i - from[lo + 1];
       }
-      uint64_t m = mask[lo];
-      for (int r = i - from[lo + 1]; r > 0; --r) m &= m - 1;
+      for (; r > 0; --r) m &= m - 1;
       const int b = __ffsll((long long)m) - 1;
-      own.item[t] = make_int4(start[b], len[b], lo, w - i * Hq);
+      own.item[t] = make_int4(start[b], len[b], lo, h);
     }
     const unsigned all = __ballot_sync(0xffffffffu, mine);
     if (t == 0) own.count = __popc(all);
@@ -187,9 +242,10 @@ struct PackedSchedule {
   int B, T;
   int block;       // rows per tile: 128 or 256
   int causal, window;
+  int fold_max;    // see PackedRef
   PackedTile* tiles[2];   // one list per order (block x of the grid makes list x)
   int order[2];
-  int* num_tiles[2];
+  int* num_tiles[2];   // three counts each
   int* error_word;
 };
 

@@ -1,6 +1,6 @@
 // prefill_k64_sm103a.cuh -- causal prefill with one 128-row sub-tile per
 // work item and 64-key tiles, on the 5th-generation tensor cores (sm_103a).
-// Two instances:
+// Three instances:
 //
 //   Dh = 256 (the Gemma head size).  The accumulator O of one 128-row
 //   sub-tile takes 256 of the 512 tensor-memory columns, so the two-sub-tile
@@ -24,6 +24,9 @@
 //   the tensor core busy through it.  The output leaves through bulk tensor
 //   stores from the staging tiles.
 //
+//   Dh = 64, packed short sequences: as Dh 128 (256 tensor-memory columns, of
+//   which S takes 128 and O the last 64).
+//
 // S is double-buffered, so the S MMA of the next key tile runs while the
 // softmax works on the current one.  P (bf16) is written over the first 32
 // columns of its S buffer and read from there by the P.V MMA.
@@ -33,7 +36,11 @@
 // TMA load, one warp issues every MMA, four warps run the softmax and the
 // epilogue (thread t owns row t).  Masks, the lazy maximum and the
 // chunked-prefill offset follow that kernel, and so does the form over packed
-// sequences (PK = true).  Every wait is bounded.
+// sequences (PK = true).  There the rows of a sequence of up to 64 or 32 rows
+// take half or a quarter of a tile, and two or four query heads of one K/V head
+// lie one below another in it ("folded"): as many items fewer, and as many
+// fewer copies of K and V (256 sequences of 64, 32 heads on 8 of 128: 86 ->
+// FFFF us).  Every wait is bounded.
 #pragma once
 
 #include <cstdint>
@@ -61,11 +68,12 @@ struct PrefillK64Params {
   int fault;            // test hook: 1 = the first K tile is never loaded
   PackedRef pk;         // PK: the sequences' tiles (128 rows each), and o's strides in elements
   long long o_row, o_head;
+  int q_rows;           // PK: rows of a Q copy: 128, or 32 where tiles may be folded
 };
 
 template <int DH_>
 struct PrefillK64Cfg {
-  static_assert(DH_ == 128 || DH_ == 256, "head size 128 or 256");
+  static_assert(DH_ == 64 || DH_ == 128 || DH_ == 256, "head size 64, 128 or 256");
   static constexpr int DH = DH_;
   static constexpr int kBoxes = DH / 64;               // 64-column boxes per row
   static constexpr int kKeys = 64;                     // keys per tile
@@ -85,7 +93,7 @@ struct PrefillK64Cfg {
   // Dh 128: the output goes through shared memory and bulk tensor stores
   // (32 rows x 64 columns per box and softmax warp).  Dh 256 has no shared
   // memory left for it and stores from registers.
-  static constexpr bool kTmaStore = DH == 128;
+  static constexpr bool kTmaStore = DH <= 128;
   static constexpr int kStageBytes = kTmaStore ? 4 * 32 * 128 : 0;
   // Two CTAs and their shared memory fit an SM only without the 1 KiB
   // alignment slack: that instance takes the dynamic shared memory as placed
@@ -129,7 +137,11 @@ struct PrefillK64Tile {
   int q0, lo, hi;
   int bh, bh_kv;             // PK: the heads alone
   int Sq, Skv, q_off;
-  int start, pad;            // PK: the sequence's first row, and the rows of padding ahead of it
+  int start, pad;            // PK: the sequence's first row, and the keys of padding ahead of it
+  // PK: 1 << fold heads lie in the tile, `rows` rows each, qpad of them padding; a head's row r
+  // is query q0 + r + shift where keys are counted
+  int fold, qpad, shift;
+  __device__ __forceinline__ int rows() const { return 128 >> fold; }
   __device__ __forceinline__ int pos_first(const PrefillK64Params& p) const { return q_off + q0; }
   __device__ __forceinline__ int pos_last(const PrefillK64Params& p) const {
     return q_off + min(q0 + 127, Sq - 1);
@@ -160,15 +172,24 @@ __device__ __forceinline__ int prefill_k64_cta_item(int k, int num_items) {
   return k < n ? prefill_k64_item(n - 1 - k, c, G) : num_items;
 }
 
-// Rows, keys and place of a packed tile's item, without its key tiles.
+// Rows, keys and place of a packed tile's item (its first head h), without its key tiles.
 __device__ __forceinline__ void prefill_k64_place(PrefillK64Tile& t, const PackedTile& e, int h,
-                                                  int group) {
+                                                  const PrefillK64Params& p) {
   t.bh = h;
-  t.bh_kv = h / group;
-  t.Sq = t.Skv = e.len + e.pad();
+  t.bh_kv = h / p.group;
   t.q_off = 0;
   t.start = e.start;
-  t.pad = e.pad();
+  t.fold = packed_fold(e.len, p.pk.fold_max);
+  if (t.fold) {   // one tile of 64 keys, the last of which is the head's last row
+    t.Sq = t.Skv = 64;
+    t.pad = 64 - e.len;
+    t.qpad = t.rows() - e.len;
+    t.shift = 64 - t.rows();
+  } else {
+    t.Sq = t.Skv = e.len + e.pad();
+    t.pad = t.qpad = e.pad();
+    t.shift = 0;
+  }
 }
 
 // Query block qb, and the key tiles that it sees.
@@ -189,9 +210,10 @@ __device__ __forceinline__ PrefillK64Tile prefill_k64_tile_of(const PrefillK64Pa
   int qb;
   if constexpr (PK) {
     // a tile's heads one after another: those of a group share their K/V tiles in L2
-    const int i = w / p.Hq;
+    int i, h;
+    packed_item_of(packed_counts(p.pk), p.Hq, w, i, h);
     const PackedTile e = packed_tile(p.pk, i);
-    prefill_k64_place(t, e, w - i * p.Hq, p.group);
+    prefill_k64_place(t, e, h, p);
     qb = e.blk;
   } else {
     const int blk = w / p.per_qb;
@@ -202,7 +224,7 @@ __device__ __forceinline__ PrefillK64Tile prefill_k64_tile_of(const PrefillK64Pa
     t.Sq = p.Sq;
     t.Skv = p.Skv;
     t.q_off = p.q_off;
-    t.start = t.pad = 0;
+    t.start = t.pad = t.fold = t.qpad = t.shift = 0;
   }
   prefill_k64_span<PK>(t, p, qb);
   return t;
@@ -217,7 +239,7 @@ struct PrefillK64Items {
   __device__ __forceinline__ PrefillK64Items(const PrefillK64Params& p_,
                                              const PrefillK64Smem<DH, PK>& sm_)
       : p(p_), sm(sm_), n(p_.num_items) {
-    if constexpr (PK) n = p.pk.tiles ? packed_num_tiles(p.pk) * p.Hq : sm.own.count;
+    if constexpr (PK) n = p.pk.tiles ? packed_items(packed_counts(p.pk), p.Hq) : sm.own.count;
   }
   __device__ __forceinline__ bool at(int k, int& w) const {
     w = PK && !p.pk.tiles ? k : prefill_k64_cta_item(k, n);
@@ -228,7 +250,7 @@ struct PrefillK64Items {
       if (!p.pk.tiles) {
         const int4 e = sm.own.item[w];
         PrefillK64Tile t;
-        prefill_k64_place(t, PackedTile{e.x, e.y, e.z, 0}, e.w, p.group);
+        prefill_k64_place(t, PackedTile{e.x, e.y, e.z, 0}, e.w, p);
         prefill_k64_span<PK>(t, p, e.z);
         return t;
       }
@@ -276,10 +298,12 @@ __device__ __forceinline__ void prefill_k64_producer(PrefillK64Smem<DH, PK>& sm,
     mbar_arrive_expect_tx(&sm.q_full, q_in_range ? (uint32_t)Cfg::kQBytes : 0u);
     for (int hf = 0; q_in_range && hf < Cfg::kBoxes; ++hf)
       // (read once: evict-first, leaving L2 to the K/V tiles that are re-read)
-      if constexpr (PK)
-        packed_load(sm.q + hf * Cfg::kQBox, map_q, &sm.q_full, hf * 64, tile.start, tile.pad,
-                    tile.q0, tile.bh, p.pk.heads_inner & kPackedQ, policy_evict_first());
-      else
+      if constexpr (PK) {
+        for (int r = 0; r < 128; r += p.q_rows)
+          packed_load(sm.q + hf * Cfg::kQBox + r * 128, map_q, &sm.q_full, hf * 64, tile.start,
+                      tile.qpad, tile.q0 + (r & (tile.rows() - 1)), tile.bh + (r >> (7 - tile.fold)),
+                      p.pk.heads_inner & kPackedQ, policy_evict_first());
+      } else
         tma_load_3d_hint(sm.q + hf * Cfg::kQBox, map_q, &sm.q_full, hf * 64, tile.q0, tile.bh,
                          policy_evict_first());
     ++nq;
@@ -447,7 +471,8 @@ __device__ __forceinline__ void prefill_k64_softmax(PrefillK64Smem<DH, PK>& sm, 
     int w;
     if (!items.at(it, w)) break;
     const PrefillK64Tile tile = items.item(w);
-    const int row = tile.pos_first(p) + t;   // this thread's query position
+    // this thread's query position
+    const int row = tile.pos_first(p) + (PK ? (t & (tile.rows() - 1)) + tile.shift : t);
 
     float m_run = -INFINITY, l_run = 0.f;
     for (int j = tile.lo; j <= tile.hi; ++j, ++tt) {
@@ -548,16 +573,18 @@ __device__ __forceinline__ void prefill_k64_softmax(PrefillK64Smem<DH, PK>& sm, 
     ++finished;
     tc_fence_after_sync();
     const float inv_l = 1.0f / l_run;
-    const int orow = tile.q0 + t;   // output row within the chunk
+    // output row within the chunk (PK: of this warp's head, whose rows the warp's are among)
+    const int orow = tile.q0 + (PK ? t & (tile.rows() - 1) : t);
+    const int head = PK ? tile.bh + ((32 * warp) >> (7 - tile.fold)) : tile.bh;
     uint4* dst = reinterpret_cast<uint4*>(
-        p.o + (PK ? (tile.start + orow - tile.pad) * p.o_row + tile.bh * p.o_head
+        p.o + (PK ? (tile.start + orow - tile.qpad) * p.o_row + head * p.o_head
                   : ((long long)tile.bh * p.Sq + orow) * Cfg::DH));
-    const bool store = PK ? orow >= tile.pad : orow < tile.Sq;
+    const bool store = PK ? orow >= tile.qpad : orow < tile.Sq;
     // PK: a warp whose rows begin with padding stores the others itself
-    const bool mixed = PK && orow - lane < tile.pad;
+    const bool mixed = PK && orow - lane < tile.qpad;
     // sum_j exp(s_ij) = 2^m_run * l_run (m_run in units of log2)
     if (p.lse != nullptr && store)
-      p.lse[PK ? (size_t)tile.bh * p.pk.T + tile.start + orow - tile.pad
+      p.lse[PK ? (size_t)head * p.pk.T + tile.start + orow - tile.qpad
                : (size_t)tile.bh * p.Sq + orow] =
           (m_run + __log2f(l_run)) * 0.69314718055994531f;
     // (the output is not read again by this kernel: evict-first, leaving L2
@@ -593,13 +620,12 @@ __device__ __forceinline__ void prefill_k64_softmax(PrefillK64Smem<DH, PK>& sm, 
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          const int row = tile.q0 + 32 * warp;
           if constexpr (PK) {
             if (!mixed)
-              packed_store(map_o, stg, 64 * h, tile.start, tile.pad, row, tile.bh,
+              packed_store(map_o, stg, 64 * h, tile.start, tile.qpad, orow, head,
                            p.pk.heads_inner & kPackedO, out_policy);
           } else {
-            tma_store_3d_hint(map_o, stg, 64 * h, row, tile.bh, out_policy);
+            tma_store_3d_hint(map_o, stg, 64 * h, tile.q0 + 32 * warp, tile.bh, out_policy);
           }
           bulk_commit_group();
         }

@@ -83,9 +83,10 @@ def test_strides(Dh, kind):
     assert all(torch.equal(a.contiguous(), b) for a, b in zip(grads, grads2))
 
 
-@pytest.mark.parametrize("Dh,n", [(64, 768), (128, 768), (128, 2560), (256, 768)])
+@pytest.mark.parametrize("Dh,n", [(64, 2560), (128, 768), (128, 2560), (256, 768)])
 def test_one_sequence_is_the_batch_form(Dh, n):
-    # whole blocks: the same kernels over the same tiles, so the same bits
+    # whole blocks, at lengths that both forms give to one kernel: over the same tiles, so the same
+    # bits
     gen = torch.Generator("cuda").manual_seed(5)
     q, k, v = ref.layouts(n, 8, 2, Dh, "heads_first", gen)
     dout = ref.layouts(n, 8, 2, Dh, "heads_first", gen)[0]
@@ -148,6 +149,24 @@ def test_several_items_a_cta(Dh, lens):
     ref.check(o[real], want[real], bound[real], "causal")
     ref.check(p[real], whole[real], wide[real], "not causal")
     assert outside_is(o, 7, cu) and outside_is(p, 7, cu)
+
+
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 7), (False, 0)])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (6, 1), (4, 2), (16, 2), (3, 3)])
+@pytest.mark.parametrize("Dh", [64, 128, 256])
+def test_short_sequences(Dh, Hq, Hkv, causal, window):
+    # lengths about those where two and four heads share a tile, few sequences and many
+    few = [1, 2, 31, 32, 33, 63, 64, 65, 0, 100, 16, 129, 300, 5]
+    for lens in (few, few * 6):
+        q, k, v, dout, cu, T = case(lens, Hq, Hkv, Dh, "heads_first" if Dh == 128 else "fused", seed=Hq)
+        o, lse = torch.full_like(dout, 7), torch.full((Hq, T), 7.0, device="cuda")
+        chs.attn_fwd_packed(q, k, v, i32(cu), o, lse, causal=causal, window=window)
+        assert chs.attn_status() == chs.ATTN_OK
+        real = slice(cu[0], cu[-1])
+        want, L, bound = ref.attention(q, k, v, cu, causal, window)
+        ref.check(o[real], want[real], bound[real], len(lens))
+        assert float((lse[:, real] - L[:, real]).abs().max()) < ref.F
+        assert outside_is(o, 7, cu) and outside_is(lse, 7, cu, 1)
 
 
 def test_workspaces():
