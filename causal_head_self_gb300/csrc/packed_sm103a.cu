@@ -130,12 +130,29 @@ cudaError_t launch_k64(const PackedShape& s, const PackedRows& q, const PackedRo
                     stream, m.q, m.k, m.v, m.o, p);
 }
 
-// Head sizes 64 and 128: the 64-key kernel up to this many rows per sequence on average.
-constexpr int kPackedK64MeanRows64 = 1536, kPackedK64MeanRows128 = 1536;
+// Head sizes 64 and 128: the 64-key kernel up to this many rows per sequence on average.  Its
+// items are half as long, two CTAs share an SM, and it reads K and V twice as often: longer
+// sequences, and more K/V heads, are for the ping-pong kernel's 256-row items.  In us, 64-key
+// against ping-pong, 32 query heads, 15000 to 16384 rows in all:
+//   Dh 64,  32 K/V heads: 74 : 81 (768 rows each), 124 : 123 (1024), 158 : 148 (1536);
+//           16: 229 : 246 (3000), 318 : 315 (4096);  8: 286 : 315 (4096), 536 : 575 (8192),
+//           2233 : 2180 (16384);  1: 534 : 575 (8192), 2054 : 2180 (16384);
+//   Dh 128, 32: 129 : 114 (768; of two sequences of 1024, whose K and V stay in L2, the 64-key
+//           kernel is 7 % faster);  16: 169 : 188 (1024), 209 : 184 (1536);  8: 188 : 204 (1536),
+//           238 : 252 (2048), 302 : 282 (3000);  1: 177 : 198 (1536), 227 : 222 (2048).
+constexpr long long kL2KeyBytes = 96ll << 20;   // K and V that L2 keeps beside the rest
 
-bool takes_k64(int B, int T, int Dh) {
-  return Dh == 256 ||
-         T <= (long long)(Dh == 64 ? kPackedK64MeanRows64 : kPackedK64MeanRows128) * B;
+bool takes_k64(const PackedShape& s) {
+  if (s.Dh == 256) return true;
+  const int group = s.Hq / s.Hkv;
+  long long rows;
+  if (s.Dh == 64)
+    rows = group >= 4 ? 12288 : group >= 2 ? 3500 : 900;
+  else if (group >= 2)
+    rows = group >= 4 ? 2048 : 1280;
+  else
+    rows = 4ll * s.T * s.Hkv * s.Dh <= kL2KeyBytes ? 1536 : 512;
+  return s.T <= rows * s.B;
 }
 
 // Two or four query heads of a K/V head in one tile of a short sequence, where sequences are
@@ -144,14 +161,14 @@ constexpr int kFoldMeanRows = 256;
 
 int fold_max_of(const PackedShape& s) {
   const int group = s.Hq / s.Hkv;
-  if (!takes_k64(s.B, s.T, s.Dh) || s.T > (long long)kFoldMeanRows * s.B) return 0;
+  if (!takes_k64(s) || s.T > (long long)kFoldMeanRows * s.B) return 0;
   return group % 4 == 0 ? 2 : group % 2 == 0 ? 1 : 0;
 }
 
 // Does each CTA list its own items?  Few sequences, no more than a lane's item each per CTA, and
 // a causal mask (under which the last blocks are the heaviest).
 bool lists_own(const PackedShape& s, const DeviceInfo& dev) {
-  const bool k64 = takes_k64(s.B, s.T, s.Dh);
+  const bool k64 = takes_k64(s);
   const int block = k64 ? 128 : 256;
   const int ctas = (k64 && s.Dh <= 128 ? 2 : 1) * dev.num_sms;
   const long long items = ((long long)s.T / block + s.B) * s.Hq;
@@ -171,7 +188,7 @@ cudaError_t launch_fwd_packed(const PackedShape& s, const PackedRows& q, const P
                               const PackedRows& v, const PackedRows& o, float* lse,
                               void* workspace, float scale_log2, const DeviceInfo& dev,
                               cudaStream_t stream) {
-  const bool k64 = takes_k64(s.B, s.T, s.Dh);
+  const bool k64 = takes_k64(s);
   const int block = k64 ? 128 : 256;
   const int fold_max = fold_max_of(s);
   PackedRef ref{nullptr, nullptr, s.cu, s.B, s.T / block + 1, s.T, 0, fold_max};

@@ -85,8 +85,6 @@ def test_strides(Dh, kind):
 
 @pytest.mark.parametrize("Dh,n", [(64, 2560), (128, 768), (128, 2560), (256, 768)])
 def test_one_sequence_is_the_batch_form(Dh, n):
-    # whole blocks, at lengths that both forms give to one kernel: over the same tiles, so the same
-    # bits
     gen = torch.Generator("cuda").manual_seed(5)
     q, k, v = ref.layouts(n, 8, 2, Dh, "heads_first", gen)
     dout = ref.layouts(n, 8, 2, Dh, "heads_first", gen)[0]
@@ -97,9 +95,10 @@ def test_one_sequence_is_the_batch_form(Dh, n):
     o2, lse2 = chs.attn_fwd_lse(*batch[:3], window=333)
     grads2 = chs.attn_bwd(*batch[:3], o2, batch[3], lse2, window=333)
     assert chs.attn_status() == chs.ATTN_OK
-    assert torch.equal(o.transpose(0, 1)[None], o2) and torch.equal(lse[None], lse2)
-    # (the gradients differ by what the batch form rounds in the first two blocks)
-    bounds = ref.attention(q, k, v, [0, n], True, 333, dout=dout)[4]
+    # each within its bound of the same values (the two may choose tiles of other sizes)
+    _, _, bound, _, bounds = ref.attention(q, k, v, [0, n], True, 333, dout=dout)
+    assert bool(((o.double() - o2[0].transpose(0, 1).double()).abs() <= 2 * bound).all())
+    assert float((lse - lse2[0]).abs().max()) < 2 * ref.F
     for a, b, bound in zip(grads, grads2, bounds):
         assert bool(((a.double() - b[0].transpose(0, 1).double()).abs() <= 2 * bound).all())
 
