@@ -128,8 +128,9 @@ struct __align__(1024) Bwd256KvSmem {
 // Item w: 128-key block kb (earliest, i.e. heaviest under a causal mask,
 // first) of K/V head bkv = b * Hkv + g.
 template <bool PK>
-__device__ __forceinline__ BwdKvItem bwd256_kv_item_of(const BwdParams& p, int w) {
-  BwdKvItem r = bwd_kv_place_of<PK>(p, w);
+__device__ __forceinline__ BwdKvItem bwd256_kv_item_of(const BwdParams& p, int w,
+                                                       const PackedTile& e) {
+  BwdKvItem r = bwd_kv_place_of<PK>(p, w, e);
   bwd256_qblocks_of(p, r.seq, r.kb, r.lo, r.hi);
   return r;
 }
@@ -148,10 +149,12 @@ __device__ __forceinline__ void bwd256_kv_producer(Bwd256KvSmem<DK>& sm, const B
   int items = 0;
   bool ok = true;
   const int num_items = bwd_num_items<PK>(p, p.Hkv);
+  PackedTile next = bwd_tile_ahead<PK>(p, 0, p.Hkv, num_items);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
     if (w >= num_items) break;
-    const BwdKvItem I = bwd256_kv_item_of<PK>(p, w);
+    const BwdKvItem I = bwd256_kv_item_of<PK>(p, w, next);
+    next = bwd_tile_ahead<PK>(p, it + 1, p.Hkv, num_items);
     if (items > 0 && !(ok = mbar_wait(&sm.kv_empty, (uint32_t)(items - 1) & 1u, abort))) break;
     // (checked builds: a key block of the sequence, of a K/V head of the batch)
     const bool kv_in_range = attn_check(I.kb >= 0 && 128 * I.kb < I.seq.S && I.bkv >= 0 &&
@@ -298,10 +301,12 @@ __device__ __forceinline__ void bwd256_kv_issuer(Bwd256KvSmem<DK>& sm, const Bwd
   int items = 0;
   bool ok = true;
   const int num_items = bwd_num_items<PK>(p, p.Hkv);
+  PackedTile next = bwd_tile_ahead<PK>(p, 0, p.Hkv, num_items);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
     if (w >= num_items) break;
-    const BwdKvItem I = bwd256_kv_item_of<PK>(p, w);
+    const BwdKvItem I = bwd256_kv_item_of<PK>(p, w, next);
+    next = bwd_tile_ahead<PK>(p, it + 1, p.Hkv, num_items);
     const int N = p.group * (I.hi - I.lo + 1);
     if (!(ok = wait_all(&sm.kv_full, (uint32_t)items & 1u))) break;
     tc_fence_after_sync();
@@ -374,10 +379,12 @@ __device__ __forceinline__ void bwd256_kv_softmax(Bwd256KvSmem<DK>& sm, const Bw
   int items = 0;
   bool ok = true;
   const int num_items = bwd_num_items<PK>(p, p.Hkv);
+  PackedTile next = bwd_tile_ahead<PK>(p, 0, p.Hkv, num_items);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
     if (w >= num_items) break;
-    const BwdKvItem I = bwd256_kv_item_of<PK>(p, w);
+    const BwdKvItem I = bwd256_kv_item_of<PK>(p, w, next);
+    next = bwd_tile_ahead<PK>(p, it + 1, p.Hkv, num_items);
     const int j = 128 * I.kb + t;   // this thread's key
     for (int hh = 0; ok && hh < p.group; ++hh) {
       for (int qb = I.lo; qb <= I.hi; ++qb, ++u) {
@@ -598,8 +605,9 @@ struct __align__(1024) Bwd256QSmem {
 // Item w: 128-row query block qb (latest, i.e. heaviest under a causal
 // mask, first) of query head bh.
 template <bool PK>
-__device__ __forceinline__ BwdQItem bwd256_q_item_of(const BwdParams& p, int w) {
-  BwdQItem r = bwd_q_place_of<PK>(p, w);
+__device__ __forceinline__ BwdQItem bwd256_q_item_of(const BwdParams& p, int w,
+                                                     const PackedTile& e) {
+  BwdQItem r = bwd_q_place_of<PK>(p, w, e);
   bwd256_kblocks_of(p, r.seq, r.qb, r.lo, r.hi);
   return r;
 }
@@ -618,10 +626,12 @@ __device__ __forceinline__ void bwd256_dq_producer(Bwd256QSmem& sm, const BwdPar
   int items = 0;
   bool ok = true;
   const int num_items = bwd_num_items<PK>(p, p.Hq);
+  PackedTile next = bwd_tile_ahead<PK>(p, 0, p.Hq, num_items);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
     if (w >= num_items) break;
-    const BwdQItem I = bwd256_q_item_of<PK>(p, w);
+    const BwdQItem I = bwd256_q_item_of<PK>(p, w, next);
+    next = bwd_tile_ahead<PK>(p, it + 1, p.Hq, num_items);
     if (items > 0 && !(ok = mbar_wait(&sm.q_empty, (uint32_t)(items - 1) & 1u, abort))) break;
     // (checked builds: a query block of the sequence, of a query head of the batch)
     const bool q_in_range = attn_check(I.qb >= 0 && 128 * I.qb < I.seq.S && I.bh >= 0 &&
@@ -726,10 +736,12 @@ __device__ __forceinline__ void bwd256_dq_issuer(Bwd256QSmem& sm, const BwdParam
   int items = 0;
   bool ok = true;
   const int num_items = bwd_num_items<PK>(p, p.Hq);
+  PackedTile next = bwd_tile_ahead<PK>(p, 0, p.Hq, num_items);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
     if (w >= num_items) break;
-    const BwdQItem I = bwd256_q_item_of<PK>(p, w);
+    const BwdQItem I = bwd256_q_item_of<PK>(p, w, next);
+    next = bwd_tile_ahead<PK>(p, it + 1, p.Hq, num_items);
     const int N = I.hi - I.lo + 1;
     if (!(ok = wait_all(&sm.q_full, (uint32_t)items & 1u))) break;
     // Q's first half into tensor memory, once the previous item's S MMAs
@@ -802,13 +814,22 @@ __device__ __forceinline__ void bwd256_dq_softmax(Bwd256QSmem& sm, const BwdPara
   int items = 0;
   bool ok = true;
   const int num_items = bwd_num_items<PK>(p, p.Hq);
+  float2 ahead = make_float2(0.f, 0.f);
+  PackedTile next = bwd_tile_ahead<PK>(p, 0, p.Hq, num_items);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
     if (w >= num_items) break;
-    const BwdQItem I = bwd256_q_item_of<PK>(p, w);
+    const BwdQItem I = bwd256_q_item_of<PK>(p, w, next);
+    next = bwd_tile_ahead<PK>(p, it + 1, p.Hq, num_items);
     const int i = 128 * I.qb + t;   // this thread's query
-    const float L = p.lse2[(size_t)I.bh * p.S_pad + (I.seq.stat + i)];
-    const float Di = p.delta[(size_t)I.bh * p.S_pad + (I.seq.stat + i)];
+    float L, Di;
+    if (PK && it > 0) {
+      L = ahead.x;
+      Di = ahead.y;
+    } else {
+      L = p.lse2[(size_t)I.bh * p.S_pad + (I.seq.stat + i)];
+      Di = p.delta[(size_t)I.bh * p.S_pad + (I.seq.stat + i)];
+    }
     const float2 negL = make_float2(-L, -L), negD = make_float2(-Di, -Di);
     for (int kb = I.lo; kb <= I.hi; ++kb, ++u) {
       if (!(ok = mbar_wait(&sm.s_full, u & 1u, abort))) break;
@@ -876,6 +897,9 @@ __device__ __forceinline__ void bwd256_dq_softmax(Bwd256QSmem& sm, const BwdPara
       mbar_arrive(&sm.ds_full[b]);
     }
     if (!ok) break;
+
+    // PK: the next item's statistics, an epilogue ahead
+    if constexpr (PK) ahead = bwd_stats_ahead(p, it + 1, num_items, next, t);
 
     // ---- epilogue: scale * dQ of query i (the warpgroups take alternate chunks)
     if (!(ok = mbar_wait(&sm.acc_final, (uint32_t)items & 1u, abort))) break;

@@ -394,16 +394,27 @@ struct BwdKvItem {
   BwdSeq seq;
 };
 
-// (without lo and hi)
+// PK: the tile of the CTA's k-th item, if there is one.  Each role reads it an item ahead (a
+// read of L2 takes a few hundred ns, and an item of a short sequence no more than a few us).
 template <bool PK>
-__device__ __forceinline__ BwdKvItem bwd_kv_place_of(const BwdParams& p, int w) {
+__device__ __forceinline__ PackedTile bwd_tile_ahead(const BwdParams& p, int k, int heads,
+                                                     int num_items) {
+  if constexpr (PK) {
+    const int w = bwd_item(k, blockIdx.x, gridDim.x);
+    if (w < num_items) return packed_tile(p.pk, w / heads);
+  }
+  return PackedTile{};
+}
+
+// (without lo and hi; PK: of tile e)
+template <bool PK>
+__device__ __forceinline__ BwdKvItem bwd_kv_place_of(const BwdParams& p, int w,
+                                                     const PackedTile& e) {
   BwdKvItem r;
   if constexpr (PK) {
-    const int i = w / p.Hkv;
-    const PackedTile e = packed_tile(p.pk, i);
     r.kb = e.blk;
     r.b = 0;
-    r.g = r.bkv = w - i * p.Hkv;
+    r.g = r.bkv = w - w / p.Hkv * p.Hkv;
     r.seq = bwd_seq_of<PK>(p, e);
     return r;
   }
@@ -417,8 +428,9 @@ __device__ __forceinline__ BwdKvItem bwd_kv_place_of(const BwdParams& p, int w) 
 }
 
 template <bool PK>
-__device__ __forceinline__ BwdKvItem bwd_kv_item_of(const BwdParams& p, int w) {
-  BwdKvItem r = bwd_kv_place_of<PK>(p, w);
+__device__ __forceinline__ BwdKvItem bwd_kv_item_of(const BwdParams& p, int w,
+                                                    const PackedTile& e) {
+  BwdKvItem r = bwd_kv_place_of<PK>(p, w, e);
   bwd_qblocks_of(p, r.seq, r.kb, r.lo, r.hi);
   return r;
 }
@@ -436,10 +448,12 @@ __device__ __forceinline__ void bwd_dkdv_producer(BwdKvSmem<DH>& sm, const BwdPa
   int items = 0;
   bool ok = true;
   const int num_items = bwd_num_items<PK>(p, p.Hkv);
+  PackedTile next = bwd_tile_ahead<PK>(p, 0, p.Hkv, num_items);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
     if (w >= num_items) break;
-    const BwdKvItem I = bwd_kv_item_of<PK>(p, w);
+    const BwdKvItem I = bwd_kv_item_of<PK>(p, w, next);
+    next = bwd_tile_ahead<PK>(p, it + 1, p.Hkv, num_items);
     if (items > 0 && !(ok = mbar_wait(&sm.kv_empty, (uint32_t)(items - 1) & 1u, abort))) break;
     // (checked builds: a key block of the sequence, of a K/V head of the batch)
     const bool kv_in_range = attn_check(I.kb >= 0 && 128 * I.kb < I.seq.S && I.bkv >= 0 &&
@@ -537,10 +551,12 @@ __device__ __forceinline__ void bwd_dkdv_issuer(BwdKvSmem<DH>& sm, const BwdPara
   int items = 0;
   bool ok = true;
   const int num_items = bwd_num_items<PK>(p, p.Hkv);
+  PackedTile next = bwd_tile_ahead<PK>(p, 0, p.Hkv, num_items);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
     if (w >= num_items) break;
-    const BwdKvItem I = bwd_kv_item_of<PK>(p, w);
+    const BwdKvItem I = bwd_kv_item_of<PK>(p, w, next);
+    next = bwd_tile_ahead<PK>(p, it + 1, p.Hkv, num_items);
     const int N = p.group * (I.hi - I.lo + 1);
     if (!(ok = wait_all(&sm.kv_full, (uint32_t)items & 1u))) break;
     ++items;
@@ -616,10 +632,12 @@ __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdPar
   int items = 0;
   bool ok = true;
   const int num_items = bwd_num_items<PK>(p, p.Hkv);
+  PackedTile next = bwd_tile_ahead<PK>(p, 0, p.Hkv, num_items);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
     if (w >= num_items) break;
-    const BwdKvItem I = bwd_kv_item_of<PK>(p, w);
+    const BwdKvItem I = bwd_kv_item_of<PK>(p, w, next);
+    next = bwd_tile_ahead<PK>(p, it + 1, p.Hkv, num_items);
     const int j = 128 * I.kb + t;   // this thread's key
     for (int hh = 0; ok && hh < p.group; ++hh) {
       for (int qb = I.lo; qb <= I.hi; ++qb, ++u) {
@@ -854,15 +872,14 @@ struct BwdQItem {
   BwdSeq seq;
 };
 
-// (without lo and hi)
+// (without lo and hi; PK: of tile e)
 template <bool PK>
-__device__ __forceinline__ BwdQItem bwd_q_place_of(const BwdParams& p, int w) {
+__device__ __forceinline__ BwdQItem bwd_q_place_of(const BwdParams& p, int w,
+                                                   const PackedTile& e) {
   BwdQItem r;
   if constexpr (PK) {
-    const int i = w / p.Hq;
-    const PackedTile e = packed_tile(p.pk, i);
     r.qb = e.blk;
-    r.bh = w - i * p.Hq;
+    r.bh = w - w / p.Hq * p.Hq;
     r.bkv = r.bh / p.group;
     r.seq = bwd_seq_of<PK>(p, e);
     return r;
@@ -878,8 +895,9 @@ __device__ __forceinline__ BwdQItem bwd_q_place_of(const BwdParams& p, int w) {
 }
 
 template <bool PK>
-__device__ __forceinline__ BwdQItem bwd_q_item_of(const BwdParams& p, int w) {
-  BwdQItem r = bwd_q_place_of<PK>(p, w);
+__device__ __forceinline__ BwdQItem bwd_q_item_of(const BwdParams& p, int w,
+                                                  const PackedTile& e) {
+  BwdQItem r = bwd_q_place_of<PK>(p, w, e);
   bwd_kblocks_of(p, r.seq, r.qb, r.lo, r.hi);
   return r;
 }
@@ -898,10 +916,12 @@ __device__ __forceinline__ void bwd_dq_producer(BwdQSmem<DH>& sm, const BwdParam
   int items = 0;
   bool ok = true;
   const int num_items = bwd_num_items<PK>(p, p.Hq);
+  PackedTile next = bwd_tile_ahead<PK>(p, 0, p.Hq, num_items);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
     if (w >= num_items) break;
-    const BwdQItem I = bwd_q_item_of<PK>(p, w);
+    const BwdQItem I = bwd_q_item_of<PK>(p, w, next);
+    next = bwd_tile_ahead<PK>(p, it + 1, p.Hq, num_items);
     if (items > 0 && !(ok = mbar_wait(&sm.q_empty, (uint32_t)(items - 1) & 1u, abort))) break;
     // (checked builds: a query block of the sequence, of a query head of the batch)
     const bool q_in_range = attn_check(I.qb >= 0 && 128 * I.qb < I.seq.S && I.bh >= 0 &&
@@ -984,10 +1004,12 @@ __device__ __forceinline__ void bwd_dq_issuer(BwdQSmem<DH>& sm, const BwdParams&
   int items = 0;
   bool ok = true;
   const int num_items = bwd_num_items<PK>(p, p.Hq);
+  PackedTile next = bwd_tile_ahead<PK>(p, 0, p.Hq, num_items);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
     if (w >= num_items) break;
-    const BwdQItem I = bwd_q_item_of<PK>(p, w);
+    const BwdQItem I = bwd_q_item_of<PK>(p, w, next);
+    next = bwd_tile_ahead<PK>(p, it + 1, p.Hq, num_items);
     const int N = I.hi - I.lo + 1;
     if (!(ok = wait_all(&sm.q_full, (uint32_t)items & 1u))) break;
     ++items;
@@ -1042,6 +1064,15 @@ __device__ __forceinline__ void bwd_dq_issuer(BwdQSmem<DH>& sm, const BwdParams&
   bwd_wait_drain(&sm.mma_done, 0);
 }
 
+// PK: lse2 and D of row t of the CTA's k-th item, whose tile is e.
+__device__ __forceinline__ float2 bwd_stats_ahead(const BwdParams& p, int k, int num_items,
+                                                  const PackedTile& e, int t) {
+  const int w = bwd_item(k, blockIdx.x, gridDim.x);
+  if (w >= num_items) return make_float2(0.f, 0.f);
+  const size_t at = (size_t)(w - w / p.Hq * p.Hq) * p.S_pad + (e.stat + 128 * e.blk + t);
+  return make_float2(p.lse2[at], p.delta[at]);
+}
+
 // Element-wise work of the dQ pass (warps 0-7; thread t of warpgroup wg owns
 // query row 128 qb + t and key columns kCols wg .. kCols (wg + 1) - 1):
 // P = exp2(S * scale*log2e - lse2_i) (0 where masked), kept in fp32
@@ -1063,13 +1094,22 @@ __device__ __forceinline__ void bwd_dq_softmax(BwdQSmem<DH>& sm, const BwdParams
   int items = 0;
   bool ok = true;
   const int num_items = bwd_num_items<PK>(p, p.Hq);
+  float2 ahead = make_float2(0.f, 0.f);
+  PackedTile next = bwd_tile_ahead<PK>(p, 0, p.Hq, num_items);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
     if (w >= num_items) break;
-    const BwdQItem I = bwd_q_item_of<PK>(p, w);
+    const BwdQItem I = bwd_q_item_of<PK>(p, w, next);
+    next = bwd_tile_ahead<PK>(p, it + 1, p.Hq, num_items);
     const int i = 128 * I.qb + t;   // this thread's query
-    const float L = p.lse2[(size_t)I.bh * p.S_pad + (I.seq.stat + i)];
-    const float Di = p.delta[(size_t)I.bh * p.S_pad + (I.seq.stat + i)];
+    float L, Di;
+    if (PK && it > 0) {
+      L = ahead.x;
+      Di = ahead.y;
+    } else {
+      L = p.lse2[(size_t)I.bh * p.S_pad + (I.seq.stat + i)];
+      Di = p.delta[(size_t)I.bh * p.S_pad + (I.seq.stat + i)];
+    }
     const float2 negL = make_float2(-L, -L), negD = make_float2(-Di, -Di);
     for (int kb = I.lo; kb <= I.hi; ++kb, ++u) {
       if (!(ok = mbar_wait(&sm.s_full, u & 1u, abort))) break;
@@ -1150,6 +1190,9 @@ __device__ __forceinline__ void bwd_dq_softmax(BwdQSmem<DH>& sm, const BwdParams
       mbar_arrive(&sm.ds_full[b]);
     }
     if (!ok) break;
+
+    // PK: the next item's statistics, an epilogue ahead
+    if constexpr (PK) ahead = bwd_stats_ahead(p, it + 1, num_items, next, t);
 
     // ---- epilogue: scale * dQ of query i, this warpgroup's chunks of the columns
     if (!(ok = mbar_wait(&sm.acc_final, (uint32_t)items & 1u, abort))) break;
