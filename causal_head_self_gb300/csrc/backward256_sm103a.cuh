@@ -127,7 +127,7 @@ struct __align__(1024) Bwd256KvSmem {
 
 // Item w: 128-key block kb (earliest, i.e. heaviest under a causal mask,
 // first) of K/V head bkv = b * Hkv + g.
-template <bool PK>
+template <int PK>
 __device__ __forceinline__ BwdKvItem bwd256_kv_item_of(const BwdParams& p, int w,
                                                        const PackedTile& e) {
   BwdKvItem r = bwd_kv_place_of<PK>(p, w, e);
@@ -135,7 +135,7 @@ __device__ __forceinline__ BwdKvItem bwd256_kv_item_of(const BwdParams& p, int w
   return r;
 }
 
-template <bool DK, bool PK>
+template <bool DK, int PK>
 __device__ __forceinline__ void bwd256_kv_producer(Bwd256KvSmem<DK>& sm, const BwdParams& p,
                                                    const CUtensorMap* map_q,
                                                    const CUtensorMap* map_k,
@@ -148,13 +148,14 @@ __device__ __forceinline__ void bwd256_kv_producer(Bwd256KvSmem<DK>& sm, const B
   uint32_t u = 0, q_loaded = 0, q_par = 0, d_loaded = 0, d_par = 0;
   int items = 0;
   bool ok = true;
-  const int num_items = bwd_num_items<PK>(p, p.Hkv);
-  PackedTile next = bwd_tile_ahead<PK>(p, 0, p.Hkv, num_items);
+  const int3 counts = bwd_counts<PK>(p);
+  const int num_items = bwd_num_kv_items<PK>(p, counts);
+  PackedTile next = bwd_tile_ahead<PK, false>(p, 0, num_items, counts);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
     if (w >= num_items) break;
     const BwdKvItem I = bwd256_kv_item_of<PK>(p, w, next);
-    next = bwd_tile_ahead<PK>(p, it + 1, p.Hkv, num_items);
+    next = bwd_tile_ahead<PK, false>(p, it + 1, num_items, counts);
     if (items > 0 && !(ok = mbar_wait(&sm.kv_empty, (uint32_t)(items - 1) & 1u, abort))) break;
     // (checked builds: a key block of the sequence, of a K/V head of the batch)
     const bool kv_in_range = attn_check(I.kb >= 0 && 128 * I.kb < I.seq.S && I.bkv >= 0 &&
@@ -227,7 +228,7 @@ __device__ __forceinline__ void bwd256_kv_producer(Bwd256KvSmem<DK>& sm, const B
 // overwritten two steps later, after the accumulation MMA that read it
 // (issued before, in order) and after the element-wise warps are done with
 // it (the accumulation waited for them).
-template <bool DK, bool PK>
+template <bool DK, int PK>
 __device__ __forceinline__ void bwd256_kv_issuer(Bwd256KvSmem<DK>& sm, const BwdParams& p,
                                                  volatile int* abort) {
   using Cfg = Bwd256Cfg;
@@ -300,13 +301,14 @@ __device__ __forceinline__ void bwd256_kv_issuer(Bwd256KvSmem<DK>& sm, const Bwd
   uint32_t u = 0;
   int items = 0;
   bool ok = true;
-  const int num_items = bwd_num_items<PK>(p, p.Hkv);
-  PackedTile next = bwd_tile_ahead<PK>(p, 0, p.Hkv, num_items);
+  const int3 counts = bwd_counts<PK>(p);
+  const int num_items = bwd_num_kv_items<PK>(p, counts);
+  PackedTile next = bwd_tile_ahead<PK, false>(p, 0, num_items, counts);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
     if (w >= num_items) break;
     const BwdKvItem I = bwd256_kv_item_of<PK>(p, w, next);
-    next = bwd_tile_ahead<PK>(p, it + 1, p.Hkv, num_items);
+    next = bwd_tile_ahead<PK, false>(p, it + 1, num_items, counts);
     const int N = p.group * (I.hi - I.lo + 1);
     if (!(ok = wait_all(&sm.kv_full, (uint32_t)items & 1u))) break;
     tc_fence_after_sync();
@@ -365,7 +367,7 @@ __device__ __forceinline__ void bwd256_kv_issuer(Bwd256KvSmem<DK>& sm, const Bwd
 // writes it as bf16 pairs over S^T, the dK pass keeps it in fp32 and writes
 // dS^T = P^T o (dP^T - D[query]) as bf16 pairs over dP^T.  Per item: dV, or
 // scale * dK, out (the two warpgroups take alternate 32-column chunks).
-template <bool DK, bool PK>
+template <bool DK, int PK>
 __device__ __forceinline__ void bwd256_kv_softmax(Bwd256KvSmem<DK>& sm, const BwdParams& p,
                                                   uint32_t tbase, volatile int* abort, int warp,
                                                   int lane) {
@@ -378,13 +380,14 @@ __device__ __forceinline__ void bwd256_kv_softmax(Bwd256KvSmem<DK>& sm, const Bw
   uint32_t u = 0;
   int items = 0;
   bool ok = true;
-  const int num_items = bwd_num_items<PK>(p, p.Hkv);
-  PackedTile next = bwd_tile_ahead<PK>(p, 0, p.Hkv, num_items);
+  const int3 counts = bwd_counts<PK>(p);
+  const int num_items = bwd_num_kv_items<PK>(p, counts);
+  PackedTile next = bwd_tile_ahead<PK, false>(p, 0, num_items, counts);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
     if (w >= num_items) break;
     const BwdKvItem I = bwd256_kv_item_of<PK>(p, w, next);
-    next = bwd_tile_ahead<PK>(p, it + 1, p.Hkv, num_items);
+    next = bwd_tile_ahead<PK, false>(p, it + 1, num_items, counts);
     const int j = 128 * I.kb + t;   // this thread's key
     for (int hh = 0; ok && hh < p.group; ++hh) {
       for (int qb = I.lo; qb <= I.hi; ++qb, ++u) {
@@ -501,7 +504,7 @@ __device__ __forceinline__ void bwd256_kv_softmax(Bwd256KvSmem<DK>& sm, const Bw
   }
 }
 
-template <bool DK, bool PK = false>
+template <bool DK, int PK = 0>
 __global__ void __launch_bounds__(Bwd256Cfg::kThreads, 1)
     attn_bwd256_kv(const __grid_constant__ CUtensorMap map_q,
                    const __grid_constant__ CUtensorMap map_k,
@@ -604,15 +607,15 @@ struct __align__(1024) Bwd256QSmem {
 
 // Item w: 128-row query block qb (latest, i.e. heaviest under a causal
 // mask, first) of query head bh.
-template <bool PK>
+template <int PK>
 __device__ __forceinline__ BwdQItem bwd256_q_item_of(const BwdParams& p, int w,
-                                                     const PackedTile& e) {
-  BwdQItem r = bwd_q_place_of<PK>(p, w, e);
+                                                     const PackedTile& e, const int3& n) {
+  BwdQItem r = bwd_q_place_of<PK>(p, w, e, n);
   bwd256_kblocks_of(p, r.seq, r.qb, r.lo, r.hi);
   return r;
 }
 
-template <bool PK>
+template <int PK>
 __device__ __forceinline__ void bwd256_dq_producer(Bwd256QSmem& sm, const BwdParams& p,
                                                    const CUtensorMap* map_q,
                                                    const CUtensorMap* map_k,
@@ -625,13 +628,14 @@ __device__ __forceinline__ void bwd256_dq_producer(Bwd256QSmem& sm, const BwdPar
   uint32_t u = 0, k_loaded = 0, k_par = 0, v_loaded = 0, v_par = 0;
   int items = 0;
   bool ok = true;
-  const int num_items = bwd_num_items<PK>(p, p.Hq);
-  PackedTile next = bwd_tile_ahead<PK>(p, 0, p.Hq, num_items);
+  const int3 counts = bwd_counts<PK>(p);
+  const int num_items = bwd_num_q_items<PK>(p, counts);
+  PackedTile next = bwd_tile_ahead<PK, true>(p, 0, num_items, counts);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
     if (w >= num_items) break;
-    const BwdQItem I = bwd256_q_item_of<PK>(p, w, next);
-    next = bwd_tile_ahead<PK>(p, it + 1, p.Hq, num_items);
+    const BwdQItem I = bwd256_q_item_of<PK>(p, w, next, counts);
+    next = bwd_tile_ahead<PK, true>(p, it + 1, num_items, counts);
     if (items > 0 && !(ok = mbar_wait(&sm.q_empty, (uint32_t)(items - 1) & 1u, abort))) break;
     // (checked builds: a query block of the sequence, of a query head of the batch)
     const bool q_in_range = attn_check(I.qb >= 0 && 128 * I.qb < I.seq.S && I.bh >= 0 &&
@@ -680,7 +684,7 @@ __device__ __forceinline__ void bwd256_dq_producer(Bwd256QSmem& sm, const BwdPar
 // S(n+1) once the element-wise warps have read S(n), dP(n+1) into the other
 // dP buffer, then dQ(n) once dS(n) is written over dP(n) (as in the Dh <= 128
 // dQ pass).  A key block is released after dQ, a value block after its dP.
-template <bool PK>
+template <int PK>
 __device__ __forceinline__ void bwd256_dq_issuer(Bwd256QSmem& sm, const BwdParams& p,
                                                  volatile int* abort) {
   using Cfg = Bwd256Cfg;
@@ -735,13 +739,14 @@ __device__ __forceinline__ void bwd256_dq_issuer(Bwd256QSmem& sm, const BwdParam
   uint32_t u = 0;
   int items = 0;
   bool ok = true;
-  const int num_items = bwd_num_items<PK>(p, p.Hq);
-  PackedTile next = bwd_tile_ahead<PK>(p, 0, p.Hq, num_items);
+  const int3 counts = bwd_counts<PK>(p);
+  const int num_items = bwd_num_q_items<PK>(p, counts);
+  PackedTile next = bwd_tile_ahead<PK, true>(p, 0, num_items, counts);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
     if (w >= num_items) break;
-    const BwdQItem I = bwd256_q_item_of<PK>(p, w, next);
-    next = bwd_tile_ahead<PK>(p, it + 1, p.Hq, num_items);
+    const BwdQItem I = bwd256_q_item_of<PK>(p, w, next, counts);
+    next = bwd_tile_ahead<PK, true>(p, it + 1, num_items, counts);
     const int N = I.hi - I.lo + 1;
     if (!(ok = wait_all(&sm.q_full, (uint32_t)items & 1u))) break;
     // Q's first half into tensor memory, once the previous item's S MMAs
@@ -800,7 +805,7 @@ __device__ __forceinline__ void bwd256_dq_issuer(Bwd256QSmem& sm, const BwdParam
 // query row 128 qb + t and key columns 32 wg .. 32 wg + 31 of each 64-key
 // block): P = exp2(S * scale*log2e - lse2_i) (0 where masked), kept in fp32;
 // dS = P o (dP - D_i) as bf16 pairs over dP.  Per item: scale * dQ out.
-template <bool PK>
+template <int PK>
 __device__ __forceinline__ void bwd256_dq_softmax(Bwd256QSmem& sm, const BwdParams& p,
                                                   uint32_t tbase, volatile int* abort, int warp,
                                                   int lane) {
@@ -813,14 +818,15 @@ __device__ __forceinline__ void bwd256_dq_softmax(Bwd256QSmem& sm, const BwdPara
   uint32_t u = 0;
   int items = 0;
   bool ok = true;
-  const int num_items = bwd_num_items<PK>(p, p.Hq);
+  const int3 counts = bwd_counts<PK>(p);
+  const int num_items = bwd_num_q_items<PK>(p, counts);
   float2 ahead = make_float2(0.f, 0.f);
-  PackedTile next = bwd_tile_ahead<PK>(p, 0, p.Hq, num_items);
+  PackedTile next = bwd_tile_ahead<PK, true>(p, 0, num_items, counts);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
     if (w >= num_items) break;
-    const BwdQItem I = bwd256_q_item_of<PK>(p, w, next);
-    next = bwd_tile_ahead<PK>(p, it + 1, p.Hq, num_items);
+    const BwdQItem I = bwd256_q_item_of<PK>(p, w, next, counts);
+    next = bwd_tile_ahead<PK, true>(p, it + 1, num_items, counts);
     const int i = 128 * I.qb + t;   // this thread's query
     float L, Di;
     if (PK && it > 0) {
@@ -899,7 +905,7 @@ __device__ __forceinline__ void bwd256_dq_softmax(Bwd256QSmem& sm, const BwdPara
     if (!ok) break;
 
     // PK: the next item's statistics, an epilogue ahead
-    if constexpr (PK) ahead = bwd_stats_ahead(p, it + 1, num_items, next, t);
+    if constexpr (PK) ahead = bwd_stats_ahead<PK>(p, it + 1, num_items, next, t, counts);
 
     // ---- epilogue: scale * dQ of query i (the warpgroups take alternate chunks)
     if (!(ok = mbar_wait(&sm.acc_final, (uint32_t)items & 1u, abort))) break;
@@ -917,7 +923,7 @@ __device__ __forceinline__ void bwd256_dq_softmax(Bwd256QSmem& sm, const BwdPara
   }
 }
 
-template <bool PK = false>
+template <int PK = 0>
 __global__ void __launch_bounds__(Bwd256Cfg::kThreads, 1)
     attn_bwd256_dq(const __grid_constant__ CUtensorMap map_q,
                    const __grid_constant__ CUtensorMap map_k,

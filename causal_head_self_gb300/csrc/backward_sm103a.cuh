@@ -38,11 +38,13 @@
 // next warp's lane 0 issues every TMA copy, the last warp every MMA (one
 // elected lane).  Every wait is bounded.
 //
-// PK = true is the same over packed sequences (packed_sm103a.cuh): an item's
+// PK = 1 is the same over packed sequences (packed_sm103a.cuh): an item's
 // rows, keys and place come from the lists of tiles (one heaviest first for
 // each pass) instead of the launch's shape; rows are counted with the
 // sequence's padding in front, for lse2 and D too.  Padded queries have
-// lse2 = +inf and so weigh nothing; padded keys are masked.  In a batch of
+// lse2 = +inf and so weigh nothing; padded keys are masked.  PK = 2, for
+// sequences that are short on average, is that with folded tiles: two or four
+// query heads of a short sequence in one block of queries.  In a batch of
 // short sequences few keys share a query's weight, each term of a gradient's
 // sum is large, and so is what the terms' rounding to bf16 leaves: twice the
 // final rounding's error in squares.  P and dS of a sequence's first two query
@@ -90,23 +92,56 @@ struct BwdSeq {
   int start;   // PK: first row
   int pad;     // PK: rows of padding ahead of it
   int stat;    // PK: first row of its lse2 and D
+  // PK: 1 << fold heads of a short sequence lie one below another in a block of queries (as in
+  // prefill_k64_sm103a.cuh), rows() rows each: the last of the padded block, which keys are
+  // counted by
+  int fold;
+  __device__ __forceinline__ int rows() const { return 128 >> fold; }
+  // padded row of row t of a block of queries, and its head among the block's
+  __device__ __forceinline__ int row_of(int block, int t) const {
+    return 128 * block + 128 - rows() + (t & (rows() - 1));
+  }
+  __device__ __forceinline__ int head_of(int t) const { return t >> (7 - fold); }
 };
 
-template <bool PK>
-__device__ __forceinline__ int bwd_num_items(const BwdParams& p, int heads) {
-  return PK ? packed_num_tiles(p.pk) * heads : p.num_items;
+// PK: the pass's tiles (of one, two and four heads).  An item of the dK/dV pass is a tile's K/V
+// head, one of the dQ pass a folded tile's heads.
+template <int PK>
+__device__ __forceinline__ int3 bwd_counts(const BwdParams& p) {
+  if constexpr (PK == 2) return packed_counts(p.pk);
+  return make_int3(PK ? packed_num_tiles(p.pk) : 0, 0, 0);
+}
+template <int PK>
+__device__ __forceinline__ int bwd_num_kv_items(const BwdParams& p, const int3& n) {
+  return PK ? (n.x + n.y + n.z) * p.Hkv : p.num_items;
+}
+template <int PK>
+__device__ __forceinline__ int bwd_num_q_items(const BwdParams& p, const int3& n) {
+  return PK == 2 ? packed_items(n, p.Hq) : PK ? n.x * p.Hq : p.num_items;
+}
+// Item w of the dQ pass: tile i, its (first) head h.
+template <int PK>
+__device__ __forceinline__ void bwd_q_item_at(const BwdParams& p, const int3& n, int w, int& i,
+                                              int& h) {
+  if constexpr (PK == 2) {
+    packed_item_of(n, p.Hq, w, i, h);
+  } else {
+    i = w / p.Hq;
+    h = w - i * p.Hq;
+  }
 }
 
-template <bool PK>
+template <int PK>
 __device__ __forceinline__ BwdSeq bwd_seq_of(const BwdParams& p, const PackedTile& e) {
   if constexpr (PK)
-    return BwdSeq{e.len + e.pad(), (e.len + 127) / 128, e.start, e.pad(), e.stat};
-  return BwdSeq{p.S, p.nblk, 0, 0, 0};
+    return BwdSeq{e.len + e.pad(), (e.len + 127) / 128, e.start, e.pad(), e.stat,
+                  PK == 2 ? packed_fold(e.len, p.pk.fold_max) : 0};
+  return BwdSeq{p.S, p.nblk, 0, 0, 0, 0};
 }
 
 // Rows [row, row + R), columns c .. c + 63 of a head: of `bh` in a batch, of
 // head bh of the packed sequence.
-template <bool PK>
+template <int PK>
 __device__ __forceinline__ void bwd_load(void* dst, const CUtensorMap* map, uint64_t* bar, int c,
                                          int row, int bh, const BwdParams& p, const BwdSeq& q,
                                          int tensor, uint64_t policy) {
@@ -116,7 +151,7 @@ __device__ __forceinline__ void bwd_load(void* dst, const CUtensorMap* map, uint
     tma_load_3d_hint(dst, map, bar, c, row, bh, policy);
 }
 // (the resident blocks, loaded once per item)
-template <bool PK>
+template <int PK>
 __device__ __forceinline__ void bwd_load_once(void* dst, const CUtensorMap* map, uint64_t* bar,
                                               int c, int row, int bh, const BwdParams& p,
                                               const BwdSeq& q, int tensor) {
@@ -127,20 +162,37 @@ __device__ __forceinline__ void bwd_load_once(void* dst, const CUtensorMap* map,
     tma_load_3d(dst, map, bar, c, row, bh);
 }
 
+// A block of queries (Q or dO), columns c .. c + 63: of head bh, or (PK) of the heads from bh on
+// that it is folded of.
+template <int PK>
+__device__ __forceinline__ void bwd_load_queries(uint8_t* dst, const CUtensorMap* map,
+                                                 uint64_t* bar, int c, int block, int bh,
+                                                 const BwdParams& p, const BwdSeq& q, int tensor,
+                                                 uint64_t policy) {
+  if constexpr (PK) {
+    // (copies of 32 rows where tiles may be folded)
+    for (int r = 0; r < 128; r += PK == 2 ? 32 : 128)
+      packed_load(dst + r * 128, map, bar, c, q.start, q.pad, q.row_of(block, r), bh + q.head_of(r),
+                  p.pk.heads_inner & tensor, policy);
+  } else {
+    tma_load_3d_hint(dst, map, bar, c, 128 * block, bh, policy);
+  }
+}
+
 // (checked builds: a packed sequence lies inside the packed tensors)
-template <bool PK>
+template <int PK>
 __device__ __forceinline__ bool bwd_inside(const BwdParams& p, const BwdSeq& q) {
   return !PK || (q.start >= 0 && q.start <= p.pk.T - (q.S - q.pad));
 }
 
 // Is row i one whose gradient is stored?
-template <bool PK>
+template <int PK>
 __device__ __forceinline__ bool bwd_real(const BwdSeq& q, int i) {
   return PK ? i >= q.pad : i < q.S;
 }
 
 // Where row i of a gradient lies.
-template <bool PK>
+template <int PK>
 __device__ __forceinline__ size_t bwd_row(const BwdSeq& q, int bh, int i, int DH, long long row,
                                           long long head) {
   if constexpr (PK) return (size_t)((q.start + (long long)(i - q.pad)) * row + bh * head);
@@ -184,7 +236,7 @@ __host__ __device__ constexpr uint32_t bwd_low_col(int kk) {
 
 // PK: do P and dS of these query blocks (of 128 rows) enter the products in two parts?
 constexpr int kBwdExactBlocks = 2;
-template <bool PK>
+template <int PK>
 __device__ __forceinline__ bool bwd_two_parts(int qb) { return PK && qb < kBwdExactBlocks; }
 
 // What bf16 leaves of (a, b), whose rounded pair is `hi`, as a pair.
@@ -266,7 +318,8 @@ __global__ void __launch_bounds__(256)
   griddep_wait();
   griddep_launch_dependents();
   const int tile = blockIdx.x / Hq, h = blockIdx.x - tile * Hq;
-  if (tile >= packed_num_tiles(pk)) return;
+  const int3 n = packed_counts(pk);
+  if (tile >= n.x + n.y + n.z) return;
   const PackedTile e = packed_tile(pk, tile);
   const int sub = threadIdx.x % kLanes, r0 = threadIdx.x / kLanes;
   const __nv_bfloat16* po = o + h * o_head + 8 * sub;
@@ -396,18 +449,22 @@ struct BwdKvItem {
 
 // PK: the tile of the CTA's k-th item, if there is one.  Each role reads it an item ahead (a
 // read of L2 takes a few hundred ns, and an item of a short sequence no more than a few us).
-template <bool PK>
-__device__ __forceinline__ PackedTile bwd_tile_ahead(const BwdParams& p, int k, int heads,
-                                                     int num_items) {
+template <int PK, bool Q>
+__device__ __forceinline__ PackedTile bwd_tile_ahead(const BwdParams& p, int k, int num_items,
+                                                     const int3& n) {
   if constexpr (PK) {
     const int w = bwd_item(k, blockIdx.x, gridDim.x);
-    if (w < num_items) return packed_tile(p.pk, w / heads);
+    if (w < num_items) {
+      int i = w / p.Hkv, h;
+      if (Q) bwd_q_item_at<PK>(p, n, w, i, h);
+      return packed_tile(p.pk, i);
+    }
   }
   return PackedTile{};
 }
 
 // (without lo and hi; PK: of tile e)
-template <bool PK>
+template <int PK>
 __device__ __forceinline__ BwdKvItem bwd_kv_place_of(const BwdParams& p, int w,
                                                      const PackedTile& e) {
   BwdKvItem r;
@@ -427,7 +484,7 @@ __device__ __forceinline__ BwdKvItem bwd_kv_place_of(const BwdParams& p, int w,
   return r;
 }
 
-template <bool PK>
+template <int PK>
 __device__ __forceinline__ BwdKvItem bwd_kv_item_of(const BwdParams& p, int w,
                                                     const PackedTile& e) {
   BwdKvItem r = bwd_kv_place_of<PK>(p, w, e);
@@ -435,7 +492,7 @@ __device__ __forceinline__ BwdKvItem bwd_kv_item_of(const BwdParams& p, int w,
   return r;
 }
 
-template <int DH, bool PK>
+template <int DH, int PK>
 __device__ __forceinline__ void bwd_dkdv_producer(BwdKvSmem<DH>& sm, const BwdParams& p,
                                                   const CUtensorMap* map_q,
                                                   const CUtensorMap* map_k,
@@ -447,13 +504,14 @@ __device__ __forceinline__ void bwd_dkdv_producer(BwdKvSmem<DH>& sm, const BwdPa
   uint32_t u = 0, loaded = 0, par = 0;
   int items = 0;
   bool ok = true;
-  const int num_items = bwd_num_items<PK>(p, p.Hkv);
-  PackedTile next = bwd_tile_ahead<PK>(p, 0, p.Hkv, num_items);
+  const int3 counts = bwd_counts<PK>(p);
+  const int num_items = bwd_num_kv_items<PK>(p, counts);
+  PackedTile next = bwd_tile_ahead<PK, false>(p, 0, num_items, counts);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
     if (w >= num_items) break;
     const BwdKvItem I = bwd_kv_item_of<PK>(p, w, next);
-    next = bwd_tile_ahead<PK>(p, it + 1, p.Hkv, num_items);
+    next = bwd_tile_ahead<PK, false>(p, it + 1, num_items, counts);
     if (items > 0 && !(ok = mbar_wait(&sm.kv_empty, (uint32_t)(items - 1) & 1u, abort))) break;
     // (checked builds: a key block of the sequence, of a K/V head of the batch)
     const bool kv_in_range = attn_check(I.kb >= 0 && 128 * I.kb < I.seq.S && I.bkv >= 0 &&
@@ -469,7 +527,8 @@ __device__ __forceinline__ void bwd_dkdv_producer(BwdKvSmem<DH>& sm, const BwdPa
       }
     }
     ++items;
-    for (int hh = 0; ok && hh < p.group; ++hh) {
+    const int rows = I.seq.rows(), heads = 1 << I.seq.fold;   // (128 and 1 but for folded tiles)
+    for (int hh = 0; ok && hh < p.group; hh += heads) {
       const int bh = I.b * p.Hq + I.g * p.group + hh;
       for (int qb = I.lo; qb <= I.hi; ++qb, ++u) {
         const int st = (int)(u & 1u);
@@ -478,19 +537,22 @@ __device__ __forceinline__ void bwd_dkdv_producer(BwdKvSmem<DH>& sm, const BwdPa
         const size_t row0 = (size_t)bh * p.S_pad + (I.seq.stat + 128 * qb);
         // (checked builds: a query block of the sequence, of a query head of
         // the batch, whose per-row statistics lie inside the workspace)
-        const bool in_range = attn_check(qb >= 0 && 128 * qb < I.seq.S && bh >= 0 && bh < p.B * p.Hq &&
-                                             row0 + 128 <= (size_t)p.B * p.Hq * p.S_pad,
+        const bool in_range = attn_check(qb >= 0 && 128 * qb < I.seq.S && bh >= 0 &&
+                                             bh + heads <= p.B * p.Hq &&
+                                             row0 + (size_t)(heads - 1) * p.S_pad + 128 <=
+                                                 (size_t)p.B * p.Hq * p.S_pad,
                                          p.error_word);
         mbar_arrive_expect_tx(&sm.q_full[st], in_range ? 2u * Cfg::kTile + 2u * 512u : 0u);
         for (int hf = 0; in_range && hf < kBoxes; ++hf) {
-          bwd_load<PK>(sm.q[st] + hf * Cfg::kBox, map_q, &sm.q_full[st], 64 * hf, 128 * qb,
-                            bh, p, I.seq, kPackedQ, keep);
-          bwd_load<PK>(sm.dO[st] + hf * Cfg::kBox, map_do, &sm.q_full[st], 64 * hf, 128 * qb,
-                            bh, p, I.seq, kPackedDO, keep);
+          bwd_load_queries<PK>(sm.q[st] + hf * Cfg::kBox, map_q, &sm.q_full[st], 64 * hf, qb, bh,
+                               p, I.seq, kPackedQ, keep);
+          bwd_load_queries<PK>(sm.dO[st] + hf * Cfg::kBox, map_do, &sm.q_full[st], 64 * hf, qb, bh,
+                               p, I.seq, kPackedDO, keep);
         }
-        if (in_range) {
-          bulk_load(sm.lse2[st], p.lse2 + row0, 512, &sm.q_full[st], keep);
-          bulk_load(sm.dlt[st], p.delta + row0, 512, &sm.q_full[st], keep);
+        for (int x = 0; in_range && x < heads; ++x) {
+          const size_t at = row0 + (size_t)x * p.S_pad + (128 - rows);
+          bulk_load(sm.lse2[st] + x * rows, p.lse2 + at, 4 * rows, &sm.q_full[st], keep);
+          bulk_load(sm.dlt[st] + x * rows, p.delta + at, 4 * rows, &sm.q_full[st], keep);
         }
         loaded |= 1u << st;
         par = (par & ~(1u << st)) | (ph << st);
@@ -508,7 +570,7 @@ __device__ __forceinline__ void bwd_dkdv_producer(BwdKvSmem<DH>& sm, const BwdPa
 // S(n+1) (its columns held P(n), which dV(n), issued before it, reads),
 // dK(n) once dS(n) is written, dP(n+1) (its columns held dS(n)).  The
 // element-wise work of step n+1 therefore overlaps dK(n) and dP(n+1).
-template <int DH, bool PK>
+template <int DH, int PK>
 __device__ __forceinline__ void bwd_dkdv_issuer(BwdKvSmem<DH>& sm, const BwdParams& p,
                                                 volatile int* abort) {
   using Cfg = BwdCfg<DH>;
@@ -550,14 +612,15 @@ __device__ __forceinline__ void bwd_dkdv_issuer(BwdKvSmem<DH>& sm, const BwdPara
   uint32_t u = 0;
   int items = 0;
   bool ok = true;
-  const int num_items = bwd_num_items<PK>(p, p.Hkv);
-  PackedTile next = bwd_tile_ahead<PK>(p, 0, p.Hkv, num_items);
+  const int3 counts = bwd_counts<PK>(p);
+  const int num_items = bwd_num_kv_items<PK>(p, counts);
+  PackedTile next = bwd_tile_ahead<PK, false>(p, 0, num_items, counts);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
     if (w >= num_items) break;
     const BwdKvItem I = bwd_kv_item_of<PK>(p, w, next);
-    next = bwd_tile_ahead<PK>(p, it + 1, p.Hkv, num_items);
-    const int N = p.group * (I.hi - I.lo + 1);
+    next = bwd_tile_ahead<PK, false>(p, it + 1, num_items, counts);
+    const int N = (PK ? p.group >> I.seq.fold : p.group) * (I.hi - I.lo + 1);
     if (!(ok = wait_all(&sm.kv_full, (uint32_t)items & 1u))) break;
     ++items;
     if (!(ok = wait_all(&sm.q_full[u & 1u], (u >> 1) & 1u))) break;
@@ -617,7 +680,7 @@ __device__ __forceinline__ void bwd_store32(__nv_bfloat16* dst, const uint32_t (
 // (0 where masked), written as bf16 pairs (see bwd_packed_col) and kept in
 // fp32 registers; then dS^T = P^T o (dP^T - D[query]), as bf16 pairs over dP^T.
 // Per item: the first half of the warpgroups write dV, the second scale * dK.
-template <int DH, bool PK>
+template <int DH, int PK>
 __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdParams& p,
                                                  uint32_t tbase, volatile int* abort, int warp,
                                                  int lane) {
@@ -631,15 +694,17 @@ __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdPar
   uint32_t u = 0;
   int items = 0;
   bool ok = true;
-  const int num_items = bwd_num_items<PK>(p, p.Hkv);
-  PackedTile next = bwd_tile_ahead<PK>(p, 0, p.Hkv, num_items);
+  const int3 counts = bwd_counts<PK>(p);
+  const int num_items = bwd_num_kv_items<PK>(p, counts);
+  PackedTile next = bwd_tile_ahead<PK, false>(p, 0, num_items, counts);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
     if (w >= num_items) break;
     const BwdKvItem I = bwd_kv_item_of<PK>(p, w, next);
-    next = bwd_tile_ahead<PK>(p, it + 1, p.Hkv, num_items);
+    next = bwd_tile_ahead<PK, false>(p, it + 1, num_items, counts);
     const int j = 128 * I.kb + t;   // this thread's key
-    for (int hh = 0; ok && hh < p.group; ++hh) {
+    const int heads = 1 << I.seq.fold;
+    for (int hh = 0; ok && hh < p.group; hh += heads) {
       for (int qb = I.lo; qb <= I.hi; ++qb, ++u) {
         const int st = (int)(u & 1u);
         // the stage's lse2 / D (bulk copies counted on q_full)
@@ -651,8 +716,13 @@ __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdPar
         // visible query columns of key j: c in [clo, chi] of this warpgroup's
         // columns (query i = 128 qb + kCols wg + c)
         const bool msk = bwd_needs_mask(p, I.seq, qb, I.kb);
-        const int i0 = 128 * qb + Cfg::kCols * wg;
-        int clo = 0, chi = Cfg::kCols - 1;
+        int i0 = 128 * qb + Cfg::kCols * wg;
+        int clo = 0, chi = Cfg::kCols - 1, column = -1;   // c & column counts within a head
+        if (PK == 2 && I.seq.fold) {
+          i0 = 128 - I.seq.rows();
+          column = I.seq.rows() - 1;
+          chi = column;
+        }
         if (p.causal) clo = j - i0;                                     // i >= j
         if (p.window > 0) chi = min(chi, j - i0 + p.window - 1);        // i - j < W
         chi = min(chi, I.seq.S - 1 - i0);                                   // i < S
@@ -679,8 +749,10 @@ __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdPar
                   h ? make_float2(-l.z, -l.w) : make_float2(-l.x, -l.y));
               float a = ex2_approx(xs.x), b = ex2_approx(xs.y);
               if (msk) {
-                a = zero_unless_le(a, (uint32_t)(col - clo), span);
-                b = zero_unless_le(b, (uint32_t)(col + 1 - clo), span);
+                const int at = PK == 2 ? col & column : col;
+                const int at1 = PK == 2 ? (col + 1) & column : col + 1;
+                a = zero_unless_le(a, (uint32_t)(at - clo), span);
+                b = zero_unless_le(b, (uint32_t)(at1 - clo), span);
               }
               pf[col] = a;
               pf[col + 1] = b;
@@ -776,7 +848,7 @@ __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdPar
   }
 }
 
-template <int DH, bool PK = false>
+template <int DH, int PK = 0>
 __global__ void __launch_bounds__(BwdCfg<DH>::kThreads, 1)
     attn_bwd_dkdv(const __grid_constant__ CUtensorMap map_q,
                   const __grid_constant__ CUtensorMap map_k,
@@ -873,13 +945,14 @@ struct BwdQItem {
 };
 
 // (without lo and hi; PK: of tile e)
-template <bool PK>
-__device__ __forceinline__ BwdQItem bwd_q_place_of(const BwdParams& p, int w,
-                                                   const PackedTile& e) {
+template <int PK>
+__device__ __forceinline__ BwdQItem bwd_q_place_of(const BwdParams& p, int w, const PackedTile& e,
+                                                   const int3& n) {
   BwdQItem r;
   if constexpr (PK) {
+    int i;
+    bwd_q_item_at<PK>(p, n, w, i, r.bh);
     r.qb = e.blk;
-    r.bh = w - w / p.Hq * p.Hq;
     r.bkv = r.bh / p.group;
     r.seq = bwd_seq_of<PK>(p, e);
     return r;
@@ -894,15 +967,15 @@ __device__ __forceinline__ BwdQItem bwd_q_place_of(const BwdParams& p, int w,
   return r;
 }
 
-template <bool PK>
-__device__ __forceinline__ BwdQItem bwd_q_item_of(const BwdParams& p, int w,
-                                                  const PackedTile& e) {
-  BwdQItem r = bwd_q_place_of<PK>(p, w, e);
+template <int PK>
+__device__ __forceinline__ BwdQItem bwd_q_item_of(const BwdParams& p, int w, const PackedTile& e,
+                                                  const int3& n) {
+  BwdQItem r = bwd_q_place_of<PK>(p, w, e, n);
   bwd_kblocks_of(p, r.seq, r.qb, r.lo, r.hi);
   return r;
 }
 
-template <int DH, bool PK>
+template <int DH, int PK>
 __device__ __forceinline__ void bwd_dq_producer(BwdQSmem<DH>& sm, const BwdParams& p,
                                                 const CUtensorMap* map_q, const CUtensorMap* map_k,
                                                 const CUtensorMap* map_v,
@@ -915,13 +988,14 @@ __device__ __forceinline__ void bwd_dq_producer(BwdQSmem<DH>& sm, const BwdParam
   uint32_t ks = 0, kph = 0;   // K stage and its phase for block u (u % 3, (u / 3) & 1)
   int items = 0;
   bool ok = true;
-  const int num_items = bwd_num_items<PK>(p, p.Hq);
-  PackedTile next = bwd_tile_ahead<PK>(p, 0, p.Hq, num_items);
+  const int3 counts = bwd_counts<PK>(p);
+  const int num_items = bwd_num_q_items<PK>(p, counts);
+  PackedTile next = bwd_tile_ahead<PK, true>(p, 0, num_items, counts);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
     if (w >= num_items) break;
-    const BwdQItem I = bwd_q_item_of<PK>(p, w, next);
-    next = bwd_tile_ahead<PK>(p, it + 1, p.Hq, num_items);
+    const BwdQItem I = bwd_q_item_of<PK>(p, w, next, counts);
+    next = bwd_tile_ahead<PK, true>(p, it + 1, num_items, counts);
     if (items > 0 && !(ok = mbar_wait(&sm.q_empty, (uint32_t)(items - 1) & 1u, abort))) break;
     // (checked builds: a query block of the sequence, of a query head of the batch)
     const bool q_in_range = attn_check(I.qb >= 0 && 128 * I.qb < I.seq.S && I.bh >= 0 &&
@@ -929,10 +1003,15 @@ __device__ __forceinline__ void bwd_dq_producer(BwdQSmem<DH>& sm, const BwdParam
                                        p.error_word);
     mbar_arrive_expect_tx(&sm.q_full, q_in_range ? 2u * Cfg::kTile : 0u);
     for (int hf = 0; q_in_range && hf < kBoxes; ++hf) {
-      bwd_load_once<PK>(sm.q + hf * Cfg::kBox, map_q, &sm.q_full, 64 * hf, 128 * I.qb, I.bh,
-                             p, I.seq, kPackedQ);
-      bwd_load_once<PK>(sm.dO + hf * Cfg::kBox, map_do, &sm.q_full, 64 * hf, 128 * I.qb,
-                             I.bh, p, I.seq, kPackedDO);
+      if constexpr (PK) {
+        bwd_load_queries<PK>(sm.q + hf * Cfg::kBox, map_q, &sm.q_full, 64 * hf, I.qb, I.bh, p,
+                             I.seq, kPackedQ, policy_evict_first());
+        bwd_load_queries<PK>(sm.dO + hf * Cfg::kBox, map_do, &sm.q_full, 64 * hf, I.qb, I.bh, p,
+                             I.seq, kPackedDO, policy_evict_first());
+      } else {
+        tma_load_3d(sm.q + hf * Cfg::kBox, map_q, &sm.q_full, 64 * hf, 128 * I.qb, I.bh);
+        tma_load_3d(sm.dO + hf * Cfg::kBox, map_do, &sm.q_full, 64 * hf, 128 * I.qb, I.bh);
+      }
     }
     ++items;
     for (int kb = I.lo; kb <= I.hi; ++kb, ++u) {
@@ -975,7 +1054,7 @@ __device__ __forceinline__ void bwd_dq_producer(BwdQSmem<DH>& sm, const BwdParam
 // it, has read dS(n) there.  A value block is released when its dP is done,
 // a key block only after dQ: three key stages let block n+2's keys load
 // while blocks n and n+1 are in use.
-template <int DH, bool PK>
+template <int DH, int PK>
 __device__ __forceinline__ void bwd_dq_issuer(BwdQSmem<DH>& sm, const BwdParams& p,
                                               volatile int* abort) {
   using Cfg = BwdCfg<DH>;
@@ -1003,13 +1082,14 @@ __device__ __forceinline__ void bwd_dq_issuer(BwdQSmem<DH>& sm, const BwdParams&
   uint32_t u = 0;
   int items = 0;
   bool ok = true;
-  const int num_items = bwd_num_items<PK>(p, p.Hq);
-  PackedTile next = bwd_tile_ahead<PK>(p, 0, p.Hq, num_items);
+  const int3 counts = bwd_counts<PK>(p);
+  const int num_items = bwd_num_q_items<PK>(p, counts);
+  PackedTile next = bwd_tile_ahead<PK, true>(p, 0, num_items, counts);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
     if (w >= num_items) break;
-    const BwdQItem I = bwd_q_item_of<PK>(p, w, next);
-    next = bwd_tile_ahead<PK>(p, it + 1, p.Hq, num_items);
+    const BwdQItem I = bwd_q_item_of<PK>(p, w, next, counts);
+    next = bwd_tile_ahead<PK, true>(p, it + 1, num_items, counts);
     const int N = I.hi - I.lo + 1;
     if (!(ok = wait_all(&sm.q_full, (uint32_t)items & 1u))) break;
     ++items;
@@ -1065,11 +1145,15 @@ __device__ __forceinline__ void bwd_dq_issuer(BwdQSmem<DH>& sm, const BwdParams&
 }
 
 // PK: lse2 and D of row t of the CTA's k-th item, whose tile is e.
+template <int PK>
 __device__ __forceinline__ float2 bwd_stats_ahead(const BwdParams& p, int k, int num_items,
-                                                  const PackedTile& e, int t) {
+                                                  const PackedTile& e, int t, const int3& n) {
   const int w = bwd_item(k, blockIdx.x, gridDim.x);
   if (w >= num_items) return make_float2(0.f, 0.f);
-  const size_t at = (size_t)(w - w / p.Hq * p.Hq) * p.S_pad + (e.stat + 128 * e.blk + t);
+  const BwdSeq q = bwd_seq_of<PK>(p, e);
+  int i, h;
+  bwd_q_item_at<PK>(p, n, w, i, h);
+  const size_t at = (size_t)(h + q.head_of(t)) * p.S_pad + (q.stat + q.row_of(e.blk, t));
   return make_float2(p.lse2[at], p.delta[at]);
 }
 
@@ -1078,7 +1162,7 @@ __device__ __forceinline__ float2 bwd_stats_ahead(const BwdParams& p, int k, int
 // P = exp2(S * scale*log2e - lse2_i) (0 where masked), kept in fp32
 // registers; dS = P o (dP - D_i) as bf16 pairs over dP (see bwd_packed_col).
 // Per item: scale * dQ out, the 32-column chunks dealt to the warpgroups.
-template <int DH, bool PK>
+template <int DH, int PK>
 __device__ __forceinline__ void bwd_dq_softmax(BwdQSmem<DH>& sm, const BwdParams& p,
                                                uint32_t tbase, volatile int* abort, int warp,
                                                int lane) {
@@ -1093,22 +1177,25 @@ __device__ __forceinline__ void bwd_dq_softmax(BwdQSmem<DH>& sm, const BwdParams
   uint32_t u = 0;
   int items = 0;
   bool ok = true;
-  const int num_items = bwd_num_items<PK>(p, p.Hq);
+  const int3 counts = bwd_counts<PK>(p);
+  const int num_items = bwd_num_q_items<PK>(p, counts);
   float2 ahead = make_float2(0.f, 0.f);
-  PackedTile next = bwd_tile_ahead<PK>(p, 0, p.Hq, num_items);
+  PackedTile next = bwd_tile_ahead<PK, true>(p, 0, num_items, counts);
   for (int it = 0; ok; ++it) {
     const int w = bwd_item(it, blockIdx.x, gridDim.x);
     if (w >= num_items) break;
-    const BwdQItem I = bwd_q_item_of<PK>(p, w, next);
-    next = bwd_tile_ahead<PK>(p, it + 1, p.Hq, num_items);
-    const int i = 128 * I.qb + t;   // this thread's query
+    const BwdQItem I = bwd_q_item_of<PK>(p, w, next, counts);
+    next = bwd_tile_ahead<PK, true>(p, it + 1, num_items, counts);
+    // this thread's query, and its head
+    const int i = PK ? I.seq.row_of(I.qb, t) : 128 * I.qb + t;
+    const int bh = PK ? I.bh + I.seq.head_of(t) : I.bh;
     float L, Di;
     if (PK && it > 0) {
       L = ahead.x;
       Di = ahead.y;
     } else {
-      L = p.lse2[(size_t)I.bh * p.S_pad + (I.seq.stat + i)];
-      Di = p.delta[(size_t)I.bh * p.S_pad + (I.seq.stat + i)];
+      L = p.lse2[(size_t)bh * p.S_pad + (I.seq.stat + i)];
+      Di = p.delta[(size_t)bh * p.S_pad + (I.seq.stat + i)];
     }
     const float2 negL = make_float2(-L, -L), negD = make_float2(-Di, -Di);
     for (int kb = I.lo; kb <= I.hi; ++kb, ++u) {
@@ -1192,14 +1279,14 @@ __device__ __forceinline__ void bwd_dq_softmax(BwdQSmem<DH>& sm, const BwdParams
     if (!ok) break;
 
     // PK: the next item's statistics, an epilogue ahead
-    if constexpr (PK) ahead = bwd_stats_ahead(p, it + 1, num_items, next, t);
+    if constexpr (PK) ahead = bwd_stats_ahead<PK>(p, it + 1, num_items, next, t, counts);
 
     // ---- epilogue: scale * dQ of query i, this warpgroup's chunks of the columns
     if (!(ok = mbar_wait(&sm.acc_final, (uint32_t)items & 1u, abort))) break;
     ++items;
     tc_fence_after_sync();
     const bool store = bwd_real<PK>(I.seq, i);
-    const size_t row = bwd_row<PK>(I.seq, I.bh, i, DH, p.dq_row, p.dq_head);
+    const size_t row = bwd_row<PK>(I.seq, bh, i, DH, p.dq_row, p.dq_head);
 #pragma unroll 1
     for (int c = wg; c < DH / 32; c += Cfg::kWG) {
       uint32_t r[32];
@@ -1210,7 +1297,7 @@ __device__ __forceinline__ void bwd_dq_softmax(BwdQSmem<DH>& sm, const BwdParams
   }
 }
 
-template <int DH, bool PK = false>
+template <int DH, int PK = 0>
 __global__ void __launch_bounds__(BwdCfg<DH>::kThreads, 1)
     attn_bwd_dq(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                 const __grid_constant__ CUtensorMap map_v,

@@ -140,6 +140,18 @@ struct PackedShape {
   const int* cu;   // [B + 1] first rows of the sequences, and the last one's end
 };
 
+// Two or four query heads of a K/V head go into one tile of a short sequence (as 1 << the
+// result), where sequences have up to mean_rows rows on average: Q then comes in copies of 32
+// rows.  The forward pass loses nothing by it (sequences of 100 to 256 rows: the same time);
+// the backward's kernels take 13 % longer (297 us instead of 263 for 128 sequences of 128) and
+// win at 64 rows (164 instead of 203) and below.
+constexpr int kFoldMeanRows = 256, kFoldMeanRowsBackward = 96;
+inline int packed_fold_max(const PackedShape& s, int mean_rows) {
+  const int group = s.Hq / s.Hkv;
+  if (s.T > (long long)mean_rows * s.B) return 0;
+  return group % 4 == 0 ? 2 : group % 2 == 0 ? 1 : 0;
+}
+
 // Device memory that the calls need: the lists of tiles, and the backward's row statistics.
 size_t fwd_packed_workspace_bytes(const PackedShape& s, const DeviceInfo& dev);
 size_t bwd_packed_workspace_bytes(int B, int Hq, int T);

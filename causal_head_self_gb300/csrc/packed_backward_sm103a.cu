@@ -45,26 +45,26 @@ cudaError_t launch_prep(const PackedShape& s, const PackedRows& o, const PackedR
                     (long long)p.S_pad, o.row, o.head, dout.row, dout.head);
 }
 
-template <int DH>
+template <int DH, int PK>
 cudaError_t launch_passes(const PackedShape& s, const BwdMaps& m, const BwdParams& pk,
                           const BwdParams& pq, const DeviceInfo& dev, cudaStream_t stream) {
   constexpr size_t smem_kv = bwd_dkdv_smem_bytes<DH>(), smem_q = bwd_dq_smem_bytes<DH>();
   static std::atomic<int> configured[kMaxDevices];
   cudaError_t e = configure_once(configured, dev.device, [] {
-    cudaError_t r = cudaFuncSetAttribute(attn_bwd_dkdv<DH, true>,
+    cudaError_t r = cudaFuncSetAttribute(attn_bwd_dkdv<DH, PK>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_kv);
     if (r != cudaSuccess) return r;
-    return cudaFuncSetAttribute(attn_bwd_dq<DH, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(attn_bwd_dq<DH, PK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)smem_q);
   });
   if (e != cudaSuccess) return e;
   const long long most = packed_max_tiles(s.B, s.T);
   const int grid_kv = (int)(most * s.Hkv < dev.num_sms ? most * s.Hkv : dev.num_sms);
-  e = launch_pdl(attn_bwd_dkdv<DH, true>, dim3(grid_kv), dim3(BwdCfg<DH>::kThreads), smem_kv,
+  e = launch_pdl(attn_bwd_dkdv<DH, PK>, dim3(grid_kv), dim3(BwdCfg<DH>::kThreads), smem_kv,
                  stream, m.q, m.k, m.v, m.dout, pk);
   if (e != cudaSuccess) return e;
   const int grid_q = (int)(most * s.Hq < dev.num_sms ? most * s.Hq : dev.num_sms);
-  return launch_pdl(attn_bwd_dq<DH, true>, dim3(grid_q), dim3(BwdCfg<DH>::kThreads), smem_q,
+  return launch_pdl(attn_bwd_dq<DH, PK>, dim3(grid_q), dim3(BwdCfg<DH>::kThreads), smem_q,
                     stream, m.q, m.k, m.v, m.dout, pq);
 }
 
@@ -76,26 +76,26 @@ cudaError_t launch_passes256(const PackedShape& s, const BwdMaps& small_q, const
                    smem_dq = bwd256_dq_smem_bytes();
   static std::atomic<int> configured[kMaxDevices];
   cudaError_t e = configure_once(configured, dev.device, [] {
-    cudaError_t r = cudaFuncSetAttribute(attn_bwd256_kv<false, true>,
+    cudaError_t r = cudaFuncSetAttribute(attn_bwd256_kv<false, 1>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_dv);
     if (r != cudaSuccess) return r;
-    r = cudaFuncSetAttribute(attn_bwd256_kv<true, true>,
+    r = cudaFuncSetAttribute(attn_bwd256_kv<true, 1>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_dk);
     if (r != cudaSuccess) return r;
-    return cudaFuncSetAttribute(attn_bwd256_dq<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(attn_bwd256_dq<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)smem_dq);
   });
   if (e != cudaSuccess) return e;
   const long long most = packed_max_tiles(s.B, s.T);
   const int grid_kv = (int)(most * s.Hkv < dev.num_sms ? most * s.Hkv : dev.num_sms);
-  e = launch_pdl(attn_bwd256_kv<false, true>, dim3(grid_kv), dim3(Cfg::kThreads), smem_dv, stream,
+  e = launch_pdl(attn_bwd256_kv<false, 1>, dim3(grid_kv), dim3(Cfg::kThreads), smem_dv, stream,
                  small_q.q, small_q.k, small_q.v, small_q.dout, pk);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(attn_bwd256_kv<true, true>, dim3(grid_kv), dim3(Cfg::kThreads), smem_dk, stream,
+  e = launch_pdl(attn_bwd256_kv<true, 1>, dim3(grid_kv), dim3(Cfg::kThreads), smem_dk, stream,
                  small_q.q, small_q.k, small_q.v, small_q.dout, pk);
   if (e != cudaSuccess) return e;
   const int grid_q = (int)(most * s.Hq < dev.num_sms ? most * s.Hq : dev.num_sms);
-  return launch_pdl(attn_bwd256_dq<true>, dim3(grid_q), dim3(Cfg::kThreads), smem_dq, stream,
+  return launch_pdl(attn_bwd256_dq<1>, dim3(grid_q), dim3(Cfg::kThreads), smem_dq, stream,
                     small_k.q, small_k.k, small_k.v, small_k.dout, pq);
 }
 
@@ -115,13 +115,16 @@ cudaError_t launch_bwd_packed(const PackedShape& s, const PackedRows& q, const P
   int* counts[2] = {reinterpret_cast<int*>(ws), reinterpret_cast<int*>(ws) + 4};
   void* lists[2] = {ws + 256, ws + 256 + list_bytes(s.B, s.T)};
   const int order[2] = {kByQueries, kByKeys};
+  // two or four heads of short sequences in one block of queries, as in the forward pass (head
+  // size 256 streams blocks of 64 queries, which a short sequence does not waste)
+  const int fold_max = s.Dh == 256 ? 0 : packed_fold_max(s, kFoldMeanRowsBackward);
   // the maps first: nothing is launched where one cannot be made
   BwdMaps m, m2;
   if (s.Dh == 256 ? !bwd_maps(&m, s, q, k, v, dout, 64, 128) ||
                         !bwd_maps(&m2, s, q, k, v, dout, 128, 64)
-                  : !bwd_maps(&m, s, q, k, v, dout, 128, 128))
+                  : !bwd_maps(&m, s, q, k, v, dout, fold_max ? 32 : 128, 128))
     return cudaErrorInvalidValue;
-  cudaError_t e = launch_packed_schedule(s, 128, 0, 2, order, lists, counts, dev, stream);
+  cudaError_t e = launch_packed_schedule(s, 128, fold_max, 2, order, lists, counts, dev, stream);
   if (e != cudaSuccess) return e;
   BwdParams p{};
   p.B = 1;
@@ -149,15 +152,18 @@ cudaError_t launch_bwd_packed(const PackedShape& s, const PackedRows& q, const P
   p.error_word = dev.error_word;
   p.fault = dev.fault;
   BwdParams pk = p, pq = p;
-  pk.pk = PackedRef{static_cast<PackedTile*>(lists[0]), counts[0], s.cu, s.B, 0, s.T, m.heads_inner, 0};
-  pq.pk = PackedRef{static_cast<PackedTile*>(lists[1]), counts[1], s.cu, s.B, 0, s.T, m.heads_inner, 0};
+  pk.pk = PackedRef{static_cast<PackedTile*>(lists[0]), counts[0], s.cu, s.B, 0, s.T, m.heads_inner, fold_max};
+  pq.pk = PackedRef{static_cast<PackedTile*>(lists[1]), counts[1], s.cu, s.B, 0, s.T, m.heads_inner, fold_max};
   e = s.Dh == 256   ? launch_prep<256>(s, o, dout, lse, pq, dev, stream)
       : s.Dh == 128 ? launch_prep<128>(s, o, dout, lse, pq, dev, stream)
                     : launch_prep<64>(s, o, dout, lse, pq, dev, stream);
   if (e != cudaSuccess) return e;
   if (s.Dh == 256) return launch_passes256(s, m, m2, pk, pq, dev, stream);
-  return s.Dh == 128 ? launch_passes<128>(s, m, pk, pq, dev, stream)
-                     : launch_passes<64>(s, m, pk, pq, dev, stream);
+  if (fold_max)
+    return s.Dh == 128 ? launch_passes<128, 2>(s, m, pk, pq, dev, stream)
+                       : launch_passes<64, 2>(s, m, pk, pq, dev, stream);
+  return s.Dh == 128 ? launch_passes<128, 1>(s, m, pk, pq, dev, stream)
+                     : launch_passes<64, 1>(s, m, pk, pq, dev, stream);
 }
 
 }  // namespace chs

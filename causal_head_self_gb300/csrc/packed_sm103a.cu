@@ -155,16 +155,6 @@ bool takes_k64(const PackedShape& s) {
   return s.T <= rows * s.B;
 }
 
-// Two or four query heads of a K/V head in one tile of a short sequence, where sequences are
-// short on average (Q then comes in boxes of 32 rows).
-constexpr int kFoldMeanRows = 256;
-
-int fold_max_of(const PackedShape& s) {
-  const int group = s.Hq / s.Hkv;
-  if (!takes_k64(s) || s.T > (long long)kFoldMeanRows * s.B) return 0;
-  return group % 4 == 0 ? 2 : group % 2 == 0 ? 1 : 0;
-}
-
 // Does each CTA list its own items?  Few sequences, no more than a lane's item each per CTA, and
 // a causal mask (under which the last blocks are the heaviest).
 bool lists_own(const PackedShape& s, const DeviceInfo& dev) {
@@ -190,7 +180,7 @@ cudaError_t launch_fwd_packed(const PackedShape& s, const PackedRows& q, const P
                               cudaStream_t stream) {
   const bool k64 = takes_k64(s);
   const int block = k64 ? 128 : 256;
-  const int fold_max = fold_max_of(s);
+  const int fold_max = takes_k64(s) ? packed_fold_max(s, kFoldMeanRows) : 0;
   PackedRef ref{nullptr, nullptr, s.cu, s.B, s.T / block + 1, s.T, 0, fold_max};
   if (!lists_own(s, dev)) {
     int* count = static_cast<int*>(workspace);

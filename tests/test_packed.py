@@ -155,6 +155,7 @@ def test_several_items_a_cta(Dh, lens):
 @pytest.mark.parametrize("Dh", [64, 128, 256])
 def test_short_sequences(Dh, Hq, Hkv, causal, window):
     # lengths about those where two and four heads share a tile, few sequences and many
+    # (62 rows on average: folded in the backward pass too)
     few = [1, 2, 31, 32, 33, 63, 64, 65, 0, 100, 16, 129, 300, 5]
     for lens in (few, few * 6):
         q, k, v, dout, cu, T = case(lens, Hq, Hkv, Dh, "heads_first" if Dh == 128 else "fused", seed=Hq)
@@ -162,8 +163,14 @@ def test_short_sequences(Dh, Hq, Hkv, causal, window):
         chs.attn_fwd_packed(q, k, v, i32(cu), o, lse, causal=causal, window=window)
         assert chs.attn_status() == chs.ATTN_OK
         real = slice(cu[0], cu[-1])
-        want, L, bound = ref.attention(q, k, v, cu, causal, window)
+        grads = [torch.full_like(x, 7) for x in (dout, k, v)]
+        chs.attn_bwd_packed(q, k, v, o, dout, lse, i32(cu), *grads, causal=causal, window=window)
+        assert chs.attn_status() == chs.ATTN_OK
+        want, L, bound, dwant, dbound = ref.attention(q, k, v, cu, causal, window, dout=dout)
         ref.check(o[real], want[real], bound[real], len(lens))
+        for name, got, w, b in zip(("dq", "dk", "dv"), grads, dwant, dbound):
+            ref.check(got[real], w[real], b[real], name)
+            assert outside_is(got, 7, cu)
         assert float((lse[:, real] - L[:, real]).abs().max()) < ref.F
         assert outside_is(o, 7, cu) and outside_is(lse, 7, cu, 1)
 
