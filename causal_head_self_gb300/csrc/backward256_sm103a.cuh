@@ -335,7 +335,7 @@ __device__ __forceinline__ void bwd256_kv_issuer(Bwd256KvSmem<DK>& sm, const Bwd
     if (N == 1) mma_commit_warp(k_done);
     int qb = I.lo;   // step n's query block (of one head after another)
     for (int n = 0; n < N; ++n, ++u) {
-      const bool two = bwd_two_parts<PK>(qb / 2);
+      const bool two = bwd_two_parts<PK>(p, qb / 2);
       if (PK) qb = qb == I.hi ? I.lo : qb + 1;
       if (n + 1 < N) {
         if (!(ok = issue_scores(u + 1))) break;
@@ -434,7 +434,7 @@ __device__ __forceinline__ void bwd256_kv_softmax(Bwd256KvSmem<DK>& sm, const Bw
             w16[e] = pack_bf16x2(a, c);
           }
         }
-        const bool two = bwd_two_parts<PK>(qb / 2);
+        const bool two = bwd_two_parts<PK>(p, qb / 2);
         auto low = [&](uint32_t to) {   // the low parts of pf's pairs
           uint32_t l16[16];
 #pragma unroll
@@ -787,7 +787,7 @@ __device__ __forceinline__ void bwd256_dq_issuer(Bwd256QSmem& sm, const BwdParam
         mma_bf16_ts_warp(Cfg::kColAcc, Cfg::kColDP + 64 * (u & 1u) + bwd256_packed_col(kk),
                          dk_mn + kst(u) * kStage + kk * (2048 >> 4), idesc_acc,
                          (n > 0 || kk > 0) ? 1u : 0u);
-      if (PK && bwd_two_parts<PK>(I.qb)) {
+      if (PK && bwd_two_parts<PK>(p, I.qb)) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           mma_bf16_ts_warp(Cfg::kColAcc, Cfg::kColDP + 64 * (u & 1u) + bwd256_low_col(kk),
@@ -892,7 +892,7 @@ __device__ __forceinline__ void bwd256_dq_softmax(Bwd256QSmem& sm, const BwdPara
         }
       }
       tmem_st_32x32b_x16(colDP, w16);
-      if (PK && bwd_two_parts<PK>(I.qb)) {   // (as in the dV and dK passes)
+      if (PK && bwd_two_parts<PK>(p, I.qb)) {   // (as in the dV and dK passes)
 #pragma unroll
         for (int e = 0; e < 16; ++e)
           w16[e] = bwd_low_pair(pf[2 * e], pf[2 * e + 1], w16[e]);

@@ -50,8 +50,9 @@
 // final rounding's error in squares.  P and dS of a sequence's first two query
 // blocks (where most of the gradients' size lies in long sequences too) enter
 // the products as two bf16 parts, hi + lo, 2^-16 of each: two more products for
-// those blocks.  (dQ of 24 documents of 16 to 2048 rows: 1.5 times the error of
-// a single rounding of the result before, KKKK times with it.)
+// those blocks, and under a short window for all.  (dQ of 24 documents of 16 to
+// 2048 rows: 1.5 times the error of a single rounding of the result before,
+// 1.25 times with it.)  D of queries that see few keys: attn_bwd_prep_packed.
 #pragma once
 
 #include <cstdint>
@@ -82,6 +83,7 @@ struct BwdParams {
   // PK: the pass's tiles of 128 rows; S, nblk and num_items are then each
   // item's own; strides in elements between rows and heads of dq, dk and dv
   PackedRef pk;
+  int two_parts;          // PK: P and dS in two parts in every block (few keys per query)
   long long dq_row, dq_head, dk_row, dk_head, dv_row, dv_head;
 };
 
@@ -237,7 +239,9 @@ __host__ __device__ constexpr uint32_t bwd_low_col(int kk) {
 // PK: do P and dS of these query blocks (of 128 rows) enter the products in two parts?
 constexpr int kBwdExactBlocks = 2;
 template <int PK>
-__device__ __forceinline__ bool bwd_two_parts(int qb) { return PK && qb < kBwdExactBlocks; }
+__device__ __forceinline__ bool bwd_two_parts(const BwdParams& p, int qb) {
+  return PK && (qb < kBwdExactBlocks || p.two_parts);
+}
 
 // What bf16 leaves of (a, b), whose rounded pair is `hi`, as a pair.
 __device__ __forceinline__ uint32_t bwd_low_pair(float a, float b, uint32_t hi) {
@@ -304,27 +308,164 @@ __global__ void __launch_bounds__(256)
 }
 
 // The same over packed sequences: one block per listed tile of 128 rows and
-// query head, o and dO at their strides, lse [Hq, T].
+// query head, tensors at their strides, lse [Hq, T].
+//
+// D = dO . o is only as exact as o, which the forward pass rounded to bf16.
+// Where a query sees few keys o is large, and D's error then outweighs all
+// others (gradients of sequences of a dozen rows: twice the error of a single
+// rounding of the result, with it 1.1 times).  So D of a query whose keys lie
+// within 32 rows (kPrepKeys: the first rows of a sequence, and all rows under a
+// window of up to 32) comes from its definition instead, D = sum_j p_ij dP_ij:
+// one warp per 16 rows makes S and dP of the keys about them with mma.sync (a
+// 16 x 8 tile; a tcgen05 tile is 128 rows), each thread's 16-byte loads giving
+// the same eight values of both operands, in whatever order the product runs.
+// That is a launch of its own (it wants registers, the other rows' launch
+// wants threads), beside which the other rows' runs.
+struct BwdPrepPacked {
+  const __nv_bfloat16 *q, *k, *v, *o, *dout;
+  long long q_row, q_head, k_row, k_head, v_row, v_head, o_row, o_head, do_row, do_head;
+  const float* lse;
+  float *lse2, *delta;
+  PackedRef pk;
+  const int* cu;
+  int B, Hq, group, causal, window;
+  long long S_pad;
+  float scale_log2;
+};
+
+constexpr int kPrepKeys = 32;
+
+// Is D of the sequence's row i made from P and dP?
+__device__ __forceinline__ bool bwd_prep_exact(const BwdPrepPacked& p, int len, int i) {
+  if (!p.causal) return i >= 0 && len <= kPrepKeys;
+  return i >= 0 && (i < kPrepKeys || (p.window > 0 && p.window <= kPrepKeys));
+}
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+      " {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// D of rows i0 .. i0 + 15 (a warp's) from keys j0 .. j1 - 1, 16 at a time: half a row of 128
+// values of each operand is on its way before the first product.
 template <int DH>
-__global__ void __launch_bounds__(256)
-    attn_bwd_prep_packed(const __nv_bfloat16* __restrict__ o,
-                         const __nv_bfloat16* __restrict__ dout, const float* __restrict__ lse,
-                         float* __restrict__ lse2, float* __restrict__ delta, const PackedRef pk,
-                         int Hq, long long S_pad, long long o_row, long long o_head,
-                         long long do_row, long long do_head) {
+__device__ __forceinline__ void bwd_prep_rows(const BwdPrepPacked& p, const PackedTile& e, int h,
+                                              int i0, int j0, int j1, int lane) {
+  const int g = lane / 4, c = lane % 4;   // rows i0 + g and i0 + g + 8; columns 2 c, 2 c + 1
+  const int hk = h / p.group;
+  auto row = [&](const __nv_bfloat16* x, long long rs, long long hs, int head, int i, int at) {
+    if (i < 0 || i >= e.len) return make_uint4(0u, 0u, 0u, 0u);
+    return *reinterpret_cast<const uint4*>(x + (e.start + (long long)i) * rs + head * hs + at);
+  };
+  bool exact[2];
+  float l2[2], sum[2] = {0.f, 0.f};
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int i = i0 + g + 8 * half;
+    exact[half] = i < e.len && bwd_prep_exact(p, e.len, i);
+    l2[half] = exact[half] ? p.lse[(size_t)h * p.pk.T + e.start + i] * 1.4426950408889634f : 0.f;
+  }
+#pragma unroll 1
+  for (; j0 < j1; j0 += 16) {
+    if (j0 + 15 < 0 || j0 >= e.len) continue;
+    float s[2][4], d[2][4];
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) s[n][x] = d[n][x] = 0.f;
+#pragma unroll 1
+    for (int at = 8 * c; at < DH; at += 64) {
+      uint4 q[2][2], dy[2][2], k[2][2], v[2][2];   // [32 values][rows g and g + 8, or key tile]
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          q[x][n] = row(p.q, p.q_row, p.q_head, h, i0 + g + 8 * n, at + 32 * x);
+          dy[x][n] = row(p.dout, p.do_row, p.do_head, h, i0 + g + 8 * n, at + 32 * x);
+          k[x][n] = row(p.k, p.k_row, p.k_head, hk, j0 + 8 * n + g, at + 32 * x);
+          v[x][n] = row(p.v, p.v_row, p.v_head, hk, j0 + 8 * n + g, at + 32 * x);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          mma_16816(s[n], q[x][0].x, q[x][1].x, q[x][0].y, q[x][1].y, k[x][n].x, k[x][n].y);
+          mma_16816(s[n], q[x][0].z, q[x][1].z, q[x][0].w, q[x][1].w, k[x][n].z, k[x][n].w);
+          mma_16816(d[n], dy[x][0].x, dy[x][1].x, dy[x][0].y, dy[x][1].y, v[x][n].x, v[x][n].y);
+          mma_16816(d[n], dy[x][0].z, dy[x][1].z, dy[x][0].w, dy[x][1].w, v[x][n].z, v[x][n].w);
+        }
+      }
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int i = i0 + g + 8 * half, j = j0 + 8 * n + 2 * c + x;
+          const bool seen = j >= 0 && j < e.len && (!p.causal || j <= i) &&
+                            (p.window == 0 || i - j < p.window);
+          const float w = ex2_approx(fmaf(s[n][2 * half + x], p.scale_log2, -l2[half]));
+          sum[half] += seen ? w * d[n][2 * half + x] : 0.f;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    float x = sum[half];
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    x += __shfl_xor_sync(0xffffffffu, x, 2);
+    if (exact[half] && c == 0)
+      p.delta[(size_t)h * p.S_pad + (e.stat + e.pad() + i0 + g + 8 * half)] = x;
+  }
+}
+
+// The rows whose D comes from P and dP, 16 a warp: under a short window a tile's, one tile and
+// head a block; else the sequence's first ones, one sequence and four heads a block.
+constexpr int kFewHeads = 4;
+template <int DH>
+__global__ void __launch_bounds__(256, 2) attn_bwd_prep_few(const BwdPrepPacked p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int3 n = packed_counts(p.pk);
+  if (n.x + n.y + n.z == 0) return;   // (nothing to do, or offsets that are not sound)
+  if (p.causal && p.window > 0 && p.window <= kPrepKeys) {
+    const int tile = blockIdx.x / p.Hq, h = blockIdx.x - tile * p.Hq;
+    if (tile >= n.x + n.y + n.z) return;
+    const PackedTile e = packed_tile(p.pk, tile);
+    const int i0 = 128 * e.blk - e.pad() + 16 * warp;
+    if (i0 > -16) bwd_prep_rows<DH>(p, e, h, i0, i0 - kPrepKeys, i0 + 16, lane);
+    return;
+  }
+  const int blocks = (p.Hq + kFewHeads - 1) / kFewHeads;
+  const int b = blockIdx.x / blocks, h = kFewHeads * (blockIdx.x - b * blocks) + warp / 2;
+  const int start = p.cu[b], len = p.cu[b + 1] - start, i0 = 16 * (warp % 2);
+  if (h >= p.Hq || i0 >= len || (!p.causal && len > kPrepKeys)) return;
+  const PackedTile e{start, len, 0, packed_stat(start, b)};
+  bwd_prep_rows<DH>(p, e, h, i0, 0, p.causal ? i0 + 16 : kPrepKeys, lane);
+}
+
+template <int DH>
+__device__ __forceinline__ void bwd_prep_tile(const BwdPrepPacked& p) {
   constexpr int kLanes = DH / 8;
   constexpr int kRowsPerSet = 256 / kLanes;
   constexpr int kSets = 128 / kRowsPerSet;
-  griddep_wait();
-  griddep_launch_dependents();
-  const int tile = blockIdx.x / Hq, h = blockIdx.x - tile * Hq;
-  const int3 n = packed_counts(pk);
+  const int tile = blockIdx.x / p.Hq, h = blockIdx.x - tile * p.Hq;
+  const int3 n = packed_counts(p.pk);
   if (tile >= n.x + n.y + n.z) return;
-  const PackedTile e = packed_tile(pk, tile);
+  const PackedTile e = packed_tile(p.pk, tile);
   const int sub = threadIdx.x % kLanes, r0 = threadIdx.x / kLanes;
-  const __nv_bfloat16* po = o + h * o_head + 8 * sub;
-  const __nv_bfloat16* pd = dout + h * do_head + 8 * sub;
-  const size_t to = (size_t)h * S_pad + (e.stat + 128 * e.blk);
+  const __nv_bfloat16* po = p.o + h * p.o_head + 8 * sub;
+  const __nv_bfloat16* pd = p.dout + h * p.do_head + 8 * sub;
+  const size_t to = (size_t)h * p.S_pad + (e.stat + 128 * e.blk);
+  const int first = 128 * e.blk - e.pad();   // the block's first row, counted from the sequence's
   constexpr int kBatch = kSets < kPrepRowSets ? kSets : kPrepRowSets;
 #pragma unroll 1
   for (int s = 0; s < kSets; s += kBatch) {
@@ -332,12 +473,12 @@ __global__ void __launch_bounds__(256)
     bool valid[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const int i = 128 * e.blk + (s + k) * kRowsPerSet + r0 - e.pad();
+      const int i = first + (s + k) * kRowsPerSet + r0;
       valid[k] = i >= 0;
       a[k] = b[k] = make_uint4(0u, 0u, 0u, 0u);
       if (valid[k]) {
-        a[k] = *reinterpret_cast<const uint4*>(po + (e.start + (long long)i) * o_row);
-        b[k] = *reinterpret_cast<const uint4*>(pd + (e.start + (long long)i) * do_row);
+        a[k] = *reinterpret_cast<const uint4*>(po + (e.start + (long long)i) * p.o_row);
+        b[k] = *reinterpret_cast<const uint4*>(pd + (e.start + (long long)i) * p.do_row);
       }
     }
 #pragma unroll
@@ -352,15 +493,24 @@ __global__ void __launch_bounds__(256)
       }
 #pragma unroll
       for (int m = kLanes / 2; m > 0; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
-      const int r = (s + k) * kRowsPerSet + r0;
+      const int r = (s + k) * kRowsPerSet + r0, i = first + r;
       if (sub == 0) {
-        delta[to + r] = valid[k] ? acc : 0.f;
-        lse2[to + r] = valid[k] ? lse[(size_t)h * pk.T + e.start + 128 * e.blk + r - e.pad()] *
-                                      1.4426950408889634f
-                                : __int_as_float(0x7f800000);
+        if (!bwd_prep_exact(p, e.len, i)) p.delta[to + r] = valid[k] ? acc : 0.f;
+        p.lse2[to + r] = valid[k] ? p.lse[(size_t)h * p.pk.T + e.start + i] * 1.4426950408889634f
+                                  : __int_as_float(0x7f800000);
       }
     }
   }
+}
+
+template <int DH>
+__global__ void __launch_bounds__(256) attn_bwd_prep_packed(const BwdPrepPacked p) {
+  // beside the launch of the other rows, which started once the lists and the inputs were
+  // complete and whose results this one does not read; it ends after that one, so that the
+  // passes see the results of both
+  griddep_launch_dependents();
+  bwd_prep_tile<DH>(p);
+  griddep_wait();
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -633,7 +783,7 @@ __device__ __forceinline__ void bwd_dkdv_issuer(BwdKvSmem<DH>& sm, const BwdPara
     int qb = I.lo;   // step n's query block (of one head after another)
     for (int n = 0; n < N; ++n, ++u) {
       const uint64_t st = u & 1u, st1 = (u + 1) & 1u;
-      const bool two = bwd_two_parts<PK>(qb);
+      const bool two = bwd_two_parts<PK>(p, qb);
       if (PK) qb = qb == I.hi ? I.lo : qb + 1;
       if (!(ok = wait_all(&sm.p_full, u & 1u))) break;
       tc_fence_after_sync();
@@ -761,7 +911,7 @@ __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdPar
           }
           tmem_st_32x32b_x16(colS + 16 * c, w16);
         }
-        const bool two = bwd_two_parts<PK>(qb);
+        const bool two = bwd_two_parts<PK>(p, qb);
         if (PK && two) {   // (every score of this thread's is in registers)
 #pragma unroll
           for (int c = 0; c < Cfg::kChunks; ++c) {
@@ -1130,7 +1280,7 @@ __device__ __forceinline__ void bwd_dq_issuer(BwdQSmem<DH>& sm, const BwdParams&
         mma_bf16_ts_warp(Cfg::kColA0, col_dp(st) + bwd_packed_col(kk),
                          dk_mn + kst(u) * kStage + kk * (2048 >> 4),
                          idesc_acc, (n > 0 || kk > 0) ? 1u : 0u);
-      if (PK && bwd_two_parts<PK>(I.qb)) {
+      if (PK && bwd_two_parts<PK>(p, I.qb)) {
 #pragma unroll
         for (int kk = 0; kk < 128 / 16; ++kk)
           mma_bf16_ts_warp(Cfg::kColA0, col_dp(st) + bwd_low_col(kk),
@@ -1260,7 +1410,7 @@ __device__ __forceinline__ void bwd_dq_softmax(BwdQSmem<DH>& sm, const BwdParams
         }
         tmem_st_32x32b_x16(colDP + 16 * c, w16);
       }
-      if (PK && bwd_two_parts<PK>(I.qb)) {   // (as in the dK/dV pass)
+      if (PK && bwd_two_parts<PK>(p, I.qb)) {   // (as in the dK/dV pass)
 #pragma unroll
         for (int c = 0; c < Cfg::kChunks; ++c) {
           uint32_t w16[16];

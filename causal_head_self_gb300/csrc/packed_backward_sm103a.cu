@@ -34,15 +34,32 @@ bool bwd_maps(BwdMaps* m, const PackedShape& s, const PackedRows& q, const Packe
 }
 
 template <int DH>
-cudaError_t launch_prep(const PackedShape& s, const PackedRows& o, const PackedRows& dout,
-                        const float* lse, const BwdParams& p, const DeviceInfo& dev,
-                        cudaStream_t stream) {
+cudaError_t launch_prep(const PackedShape& s, const PackedRows& q, const PackedRows& k,
+                        const PackedRows& v, const PackedRows& o, const PackedRows& dout,
+                        const float* lse, const BwdParams& p, cudaStream_t stream) {
+  auto bf = [](const PackedRows& x) { return static_cast<const __nv_bfloat16*>(x.data); };
+  BwdPrepPacked a{bf(q),  bf(k),  bf(v),  bf(o),  bf(dout), q.row,    q.head,    k.row, k.head,
+                  v.row,  v.head, o.row,  o.head, dout.row, dout.head};
+  a.lse = lse;
+  a.lse2 = const_cast<float*>(p.lse2);
+  a.delta = const_cast<float*>(p.delta);
+  a.pk = p.pk;
+  a.Hq = s.Hq;
+  a.group = p.group;
+  a.causal = s.causal;
+  a.window = s.window;
+  a.S_pad = p.S_pad;
+  a.scale_log2 = p.scale_log2;
+  a.cu = s.cu;
+  a.B = s.B;
   const long long blocks = packed_max_tiles(s.B, s.T) * s.Hq;
-  return launch_pdl(attn_bwd_prep_packed<DH>, dim3((unsigned)blocks), dim3(256), 0, stream,
-                    static_cast<const __nv_bfloat16*>(o.data),
-                    static_cast<const __nv_bfloat16*>(dout.data), lse,
-                    const_cast<float*>(p.lse2), const_cast<float*>(p.delta), p.pk, s.Hq,
-                    (long long)p.S_pad, o.row, o.head, dout.row, dout.head);
+  const long long few = s.causal && s.window > 0 && s.window <= kPrepKeys
+                            ? blocks
+                            : (long long)s.B * ((s.Hq + kFewHeads - 1) / kFewHeads);
+  const cudaError_t e =
+      launch_pdl(attn_bwd_prep_few<DH>, dim3((unsigned)few), dim3(256), 0, stream, a);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attn_bwd_prep_packed<DH>, dim3((unsigned)blocks), dim3(256), 0, stream, a);
 }
 
 template <int DH, int PK>
@@ -136,6 +153,9 @@ cudaError_t launch_bwd_packed(const PackedShape& s, const PackedRows& q, const P
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.S_pad = (int)stat_rows(s.B, s.T);
   p.group = s.Hq / s.Hkv;
+  // a window this short leaves every query few keys
+  constexpr int kShortWindow = 256;
+  p.two_parts = s.window > 0 && s.window <= kShortWindow;
   float* stats = reinterpret_cast<float*>(ws + 256 + 2 * list_bytes(s.B, s.T));
   p.lse2 = stats;
   p.delta = stats + (size_t)s.Hq * p.S_pad;
@@ -154,9 +174,9 @@ cudaError_t launch_bwd_packed(const PackedShape& s, const PackedRows& q, const P
   BwdParams pk = p, pq = p;
   pk.pk = PackedRef{static_cast<PackedTile*>(lists[0]), counts[0], s.cu, s.B, 0, s.T, m.heads_inner, fold_max};
   pq.pk = PackedRef{static_cast<PackedTile*>(lists[1]), counts[1], s.cu, s.B, 0, s.T, m.heads_inner, fold_max};
-  e = s.Dh == 256   ? launch_prep<256>(s, o, dout, lse, pq, dev, stream)
-      : s.Dh == 128 ? launch_prep<128>(s, o, dout, lse, pq, dev, stream)
-                    : launch_prep<64>(s, o, dout, lse, pq, dev, stream);
+  e = s.Dh == 256   ? launch_prep<256>(s, q, k, v, o, dout, lse, pq, stream)
+      : s.Dh == 128 ? launch_prep<128>(s, q, k, v, o, dout, lse, pq, stream)
+                    : launch_prep<64>(s, q, k, v, o, dout, lse, pq, stream);
   if (e != cudaSuccess) return e;
   if (s.Dh == 256) return launch_passes256(s, m, m2, pk, pq, dev, stream);
   if (fold_max)

@@ -109,9 +109,7 @@ __global__ void __launch_bounds__(kScheduleThreads)
   __syncthreads();
   for (int b = warp; b < p.B; b += kWarps) {
     const int a = p.cu[b], len = p.cu[b + 1] - a, n = (len + p.block - 1) >> blk_shift;
-    // rows of the earlier sequences, each rounded up to 128: at most a + 127 b, so a
-    // sequence may start at the next multiple of 128 and no two meet
-    const int stat = (int)(((long long)a + 127ll * b + 127) / 128 * 128);
+    const int stat = packed_stat(a, b);
     const int fold = packed_fold(len, fold_max);
     for (int i = lane; i < n; i += 32) {
       const int at = atomicAdd(&hist[bin_of(padded(len), i, fold)], 1);

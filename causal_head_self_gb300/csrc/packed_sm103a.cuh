@@ -40,6 +40,13 @@ struct __align__(16) PackedTile {
   __device__ __forceinline__ int pad() const { return -len & 127; }
 };
 
+// PackedTile::stat of sequence b, whose first row is `start`: rows of the earlier sequences, each
+// rounded up to 128, are at most start + 127 b, so a sequence may start at the next multiple of
+// 128 and no two meet.
+__device__ __forceinline__ int packed_stat(int start, int b) {
+  return (int)(((long long)start + 127ll * b + 127) / 128 * 128);
+}
+
 // Tensors, as bits of PackedRef::heads_inner.
 constexpr int kPackedQ = 1, kPackedK = 2, kPackedV = 4, kPackedO = 8, kPackedDO = 16;
 
