@@ -132,7 +132,7 @@ __device__ __forceinline__ void packed_store(const CUtensorMap* map, const void*
 
 // With few sequences a CTA finds its own work items faster than another launch
 // lists them all, and the call needs no workspace (16 short requests: 11.5 us
-// with the launch, NNNN without; on the host 22 and MMMM).
+// with the launch, 10.2 without; on the host 22 and 11).
 constexpr int kOwnSequences = 64;   // one bit each
 constexpr int kOwnLevels = 1024;    // blocks of the longest sequence, at most
 constexpr int kOwnItems = 32;       // per CTA, at most: one lane each

@@ -40,7 +40,7 @@
 // take half or a quarter of a tile, and two or four query heads of one K/V head
 // lie one below another in it ("folded"): as many items fewer, and as many
 // fewer copies of K and V (256 sequences of 64, 32 heads on 8 of 128: 86 ->
-// FFFF us).  Every wait is bounded.
+// 67 us).  Every wait is bounded.
 #pragma once
 
 #include <cstdint>

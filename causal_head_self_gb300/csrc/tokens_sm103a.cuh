@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kRopeThreads)
 // order: pages are read from the stack below its old top and from columns
 // that shrinking sequences leave, and written above the old top and to
 // columns that growing sequences gain.  Many tokens' positions and slots
-// (262144 of 2048 sequences: 63 us on eight SMs, PPPP so) are left to a second
+// (262144 of 2048 sequences: 63 us on eight SMs, 13 so) are left to a second
 // launch on every SM, which finds all it needs in the first one's results.
 
 struct PlanParams {
