@@ -496,7 +496,12 @@ __device__ __forceinline__ void bwd256_kv_softmax(Bwd256KvSmem<DK>& sm, const Bw
       uint32_t r[32];
       tmem_ld_32x32b_x32(lane_addr + Cfg::kColAcc + 32 * c, r);
       tmem_ld_wait(r);
-      if (store) bwd_store32(dst + 32 * c, r, mul);
+      if (store) {
+        if (PK && p.wide)
+          bwd_store32_wide(dst + 32 * c, r, mul);
+        else
+          bwd_store32(dst + 32 * c, r, mul);
+      }
     }
     // the next item's first accumulation overwrites the accumulator only
     // after this thread's next arrive on p_full / ds_full, which follows
@@ -918,7 +923,12 @@ __device__ __forceinline__ void bwd256_dq_softmax(Bwd256QSmem& sm, const BwdPara
       uint32_t r[32];
       tmem_ld_32x32b_x32(lane_addr + Cfg::kColAcc + 32 * c, r);
       tmem_ld_wait(r);
-      if (store) bwd_store32(p.dq + row + 32 * c, r, p.scale);
+      if (store) {
+        if (PK && p.wide)
+          bwd_store32_wide(p.dq + row + 32 * c, r, p.scale);
+        else
+          bwd_store32(p.dq + row + 32 * c, r, p.scale);
+      }
     }
   }
 }

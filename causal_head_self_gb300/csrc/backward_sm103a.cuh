@@ -83,6 +83,7 @@ struct BwdParams {
   // PK: the pass's tiles of 128 rows; S, nblk and num_items are then each
   // item's own; strides in elements between rows and heads of dq, dk and dv
   PackedRef pk;
+  int wide;               // PK: rows of dq, dk and dv are 32-byte aligned
   int two_parts;          // PK: P and dS in two parts in every block (few keys per query)
   long long dq_row, dq_head, dk_row, dk_head, dv_row, dv_head;
 };
@@ -810,6 +811,22 @@ __device__ __forceinline__ void bwd_dkdv_issuer(BwdKvSmem<DH>& sm, const BwdPara
   bwd_wait_drain(&sm.mma_done, 0);
 }
 
+// The same with two 32-byte stores, dst 32-byte aligned.  A row is a thread's, so each store
+// instruction touches 32 rows: half as many of them, of whole sectors.
+__device__ __forceinline__ void bwd_store32_wide(__nv_bfloat16* dst, const uint32_t (&r)[32],
+                                                 float mul) {
+  const uint64_t policy = policy_evict_first();
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      w[e] = pack_bf16x2(__uint_as_float(r[16 * q + 2 * e]) * mul,
+                         __uint_as_float(r[16 * q + 2 * e + 1]) * mul);
+    st_global_v8_hint(dst + 16 * q, w, policy);
+  }
+}
+
 // Store 32 fp32 accumulator columns (times `mul`) as bf16 to dst (16-byte aligned).
 __device__ __forceinline__ void bwd_store32(__nv_bfloat16* dst, const uint32_t (&r)[32], float mul) {
   uint4* d = reinterpret_cast<uint4*>(dst);
@@ -991,7 +1008,12 @@ __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdPar
       uint32_t r[32];
       tmem_ld_32x32b_x32(colA + 32 * c, r);
       tmem_ld_wait(r);
-      if (store) bwd_store32(dst + 32 * c, r, mul);
+      if (store) {
+        if (PK && p.wide)
+          bwd_store32_wide(dst + 32 * c, r, mul);
+        else
+          bwd_store32(dst + 32 * c, r, mul);
+      }
     }
     // the next item's first dV / dK overwrite the accumulators only after
     // this thread's next arrive on p_full / ds_full, which follows these loads
@@ -1442,7 +1464,12 @@ __device__ __forceinline__ void bwd_dq_softmax(BwdQSmem<DH>& sm, const BwdParams
       uint32_t r[32];
       tmem_ld_32x32b_x32(lane_addr + Cfg::kColA0 + 32 * c, r);
       tmem_ld_wait(r);
-      if (store) bwd_store32(p.dq + row + 32 * c, r, p.scale);
+      if (store) {
+        if (PK && p.wide)
+          bwd_store32_wide(p.dq + row + 32 * c, r, p.scale);
+        else
+          bwd_store32(p.dq + row + 32 * c, r, p.scale);
+      }
     }
   }
 }

@@ -169,6 +169,10 @@ cudaError_t launch_bwd_packed(const PackedShape& s, const PackedRows& q, const P
   p.dk_head = dk.head;
   p.dv_row = dv.row;
   p.dv_head = dv.head;
+  p.wide = 1;
+  for (const PackedRows* x : {&dq, &dk, &dv})
+    if ((reinterpret_cast<uintptr_t>(x->data) & 31) != 0 || x->row % 16 != 0 || x->head % 16 != 0)
+      p.wide = 0;
   p.error_word = dev.error_word;
   p.fault = dev.fault;
   BwdParams pk = p, pq = p;

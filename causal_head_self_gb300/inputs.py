@@ -102,6 +102,15 @@ WORKLOADS = {
                                       lmin=16384, lmax=32768, budget=4096, recent=512, seed=19),
     "evict_kv8_b4_t32768_d128": dict(kind="evict", B=4, Hkv=8, Tmax=32768, page=64, Dh=128,
                                      lmin=16384, lmax=32768, budget=4096, recent=512, seed=19),
+    # packed sequences: documents of very different lengths, short requests, and the queries and
+    # keys of a packed batch with their positions
+    "packed_gqa_h32kv8_d128_docs24": dict(kind="packed", Hq=32, Hkv=8, Dh=128, seed=20,
+                                          lens=[1900, 50, 17, 400, 900, 33, 120, 700, 260, 1500, 80,
+                                                22, 610, 1100, 45, 300, 2000, 150, 70, 500, 28, 1300,
+                                                95, 210]),
+    "packed_gqa_h32kv8_d128_short256": dict(kind="packed", Hq=32, Hkv=8, Dh=128, seed=21,
+                                            lens=[64] * 256),
+    "rope_h32kv8_t16384_d128": dict(kind="rope", Hq=32, Hkv=8, Dh=128, T=16384, seed=22),
 }
 
 

@@ -67,6 +67,26 @@ def main(argv=None):
         for _ in range(args.iters):
             chs.attn_cache_evict(kp, vp, weights, table, sl, w["budget"], w["recent"],
                                  table_out=to, weights_out=kept)
+    elif w["kind"] == "packed":
+        first = [0]
+        for n in w["lens"]:
+            first.append(first[-1] + n)
+        T, Hq, Hkv = first[-1], w["Hq"], w["Hkv"]
+        cu = torch.tensor(first, dtype=torch.int32, device=dev)
+        x = inputs.device_normal_bf16((1, 1, T, (2 * Hq + 2 * Hkv) * w["Dh"]), w["seed"], dev)
+        q, k, v, dout = x.view(T, -1, w["Dh"]).split((Hq, Hkv, Hkv, Hq), 1)
+        lse = torch.empty((Hq, T), device=dev)
+        for _ in range(args.iters):
+            o = chs.attn_fwd_packed(q, k, v, cu, None, lse)
+            chs.attn_bwd_packed(q, k, v, o, dout, lse, cu)
+    elif w["kind"] == "rope":
+        T, Hq, Hkv = w["T"], w["Hq"], w["Hkv"]
+        x = inputs.device_normal_bf16((1, 1, T, (Hq + Hkv) * w["Dh"]), w["seed"], dev)
+        q, k = x.view(T, -1, w["Dh"]).split((Hq, Hkv), 1)
+        positions = torch.arange(T, dtype=torch.int32, device=dev)
+        frequencies = chs.attn_rope_frequencies(w["Dh"], device=dev)
+        for _ in range(args.iters):
+            chs.attn_rope(q, k, positions, frequencies)
     else:
         q, kc, vc, sl = (x.to(dev) for x in inputs.workload_inputs(args.workload))
         o = torch.empty_like(q)
