@@ -59,6 +59,8 @@ class AttnError(RuntimeError):
 def load():
     """Load (once) and return the ctypes handle of the built library."""
     global _lib
+    if _lib is not None:   # (set once everything about it is)
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

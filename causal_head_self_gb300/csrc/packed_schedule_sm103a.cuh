@@ -26,8 +26,10 @@ __global__ void __launch_bounds__(kScheduleThreads)
   griddep_wait();
   griddep_launch_dependents();
   __syncthreads();
-  const int blk_shift = p.block == 256 ? 8 : 7, order = p.order[blockIdx.x];
-  PackedTile* tiles = p.tiles[blockIdx.x];
+  const int blk_shift = p.block == 256 ? 8 : 7;
+  const int order = blockIdx.x ? p.order[1] : p.order[0];
+  PackedTile* tiles = blockIdx.x ? p.tiles[1] : p.tiles[0];
+  int* num_tiles = blockIdx.x ? p.num_tiles[1] : p.num_tiles[0];
 
   // are the offsets sound, and how long is the longest sequence?
   int longest = 0;
@@ -42,7 +44,7 @@ __global__ void __launch_bounds__(kScheduleThreads)
   if (lane == 0) atomicMax(&most, longest);
   __syncthreads();
   if (bad) {
-    if (t < 3) p.num_tiles[blockIdx.x][t] = 0;
+    if (t < 3) num_tiles[t] = 0;
     if (t == 0) {
       atomicExch(p.error_word, 1);   // ATTN_ERR_INVALID_ARG
     }
@@ -69,12 +71,26 @@ __global__ void __launch_bounds__(kScheduleThreads)
     }
     return (max_cost - (hi - lo + 1)) >> shift;
   };
-  // a warp per sequence, a lane per block
-  for (int b = warp; b < p.B; b += kWarps) {
-    const int rows = p.cu[b + 1] - p.cu[b], fold = packed_fold(rows, fold_max);
-    const int len = padded(rows), n = (len + p.block - 1) >> blk_shift;
-    for (int i = lane; i < n; i += 32) atomicAdd(&hist[bin_of(len, i, fold)], 1);
-  }
+  // every block of every sequence once: a lane takes a short sequence, the warp a long one
+  auto all_blocks = [&](auto&& take) {
+    constexpr int kShort = 4;   // blocks
+    for (int b0 = 32 * warp; b0 < p.B; b0 += 32 * kWarps) {
+      const int b = b0 + lane;
+      const int a = b < p.B ? p.cu[b] : 0, rows = b < p.B ? p.cu[b + 1] - a : 0;
+      const int n = (padded(rows) + p.block - 1) >> blk_shift;
+      if (n <= kShort)
+        for (int i = 0; i < n; ++i) take(b, a, rows, i);
+      for (unsigned m = __ballot_sync(0xffffffffu, n > kShort); m != 0; m &= m - 1) {
+        const int src = __ffs(m) - 1;
+        const int a1 = __shfl_sync(0xffffffffu, a, src), rows1 = __shfl_sync(0xffffffffu, rows, src);
+        const int n1 = __shfl_sync(0xffffffffu, n, src);
+        for (int i = lane; i < n1; i += 32) take(b0 + src, a1, rows1, i);
+      }
+    }
+  };
+  all_blocks([&](int, int, int rows, int i) {
+    atomicAdd(&hist[bin_of(padded(rows), i, packed_fold(rows, fold_max))], 1);
+  });
   __syncthreads();
   // where each bin's tiles start
   static_assert(kScheduleBins == 2 * kScheduleThreads, "two bins a thread");
@@ -101,21 +117,15 @@ __global__ void __launch_bounds__(kScheduleThreads)
   hist[2 * t] = before;
   hist[2 * t + 1] = before + h0;
   if (t == kScheduleThreads - 1) {
-    int* n = p.num_tiles[blockIdx.x];
-    n[0] = before;
-    n[1] = h0;
-    n[2] = h1;
+    num_tiles[0] = before;
+    num_tiles[1] = h0;
+    num_tiles[2] = h1;
   }
   __syncthreads();
-  for (int b = warp; b < p.B; b += kWarps) {
-    const int a = p.cu[b], len = p.cu[b + 1] - a, n = (len + p.block - 1) >> blk_shift;
-    const int stat = packed_stat(a, b);
-    const int fold = packed_fold(len, fold_max);
-    for (int i = lane; i < n; i += 32) {
-      const int at = atomicAdd(&hist[bin_of(padded(len), i, fold)], 1);
-      *reinterpret_cast<int4*>(tiles + at) = make_int4(a, len, i, stat);
-    }
-  }
+  all_blocks([&](int b, int a, int rows, int i) {
+    const int at = atomicAdd(&hist[bin_of(padded(rows), i, packed_fold(rows, fold_max))], 1);
+    *reinterpret_cast<int4*>(tiles + at) = make_int4(a, rows, i, packed_stat(a, b));
+  });
 }
 
 }  // namespace chs

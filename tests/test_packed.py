@@ -243,7 +243,10 @@ def test_no_rows_and_no_sequences():
     o = torch.full_like(y, 7)
     chs.attn_fwd_packed(y, y, y, i32([0]), o)
     assert bool((o == 7).all())
-    chs.attn_fwd_packed(y, y, y, i32([3, 3, 3]), o)
+    for cu in (i32([3, 3, 3]), i32([6] * 100)):
+        chs.attn_fwd_packed(y, y, y, cu, o)
+        lse = torch.zeros(4, 6, device="cuda")
+        chs.attn_bwd_packed(y, y, y, y, y, lse, cu, o, torch.empty_like(o), torch.empty_like(o))
     assert bool((o == 7).all()) and chs.attn_status() == chs.ATTN_OK
 
 

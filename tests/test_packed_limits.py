@@ -55,6 +55,33 @@ def test_tensors_of_2_31_elements():
     assert float(near.max()) <= 2 * 2.0 ** -8 * 1.5 * float(kept.double().abs().max())
 
 
+def test_a_sequence_of_more_blocks_than_the_listing_has_bins():
+    T, W = 300000, 64
+    d = torch.device("cuda")
+    q, k, v, dout = (inputs.device_normal_bf16((1, 1, T, 64), i, d)[0, 0].view(T, 1, 64) for i in range(4))
+    cu, lse = [0, 299000, 299001, T], torch.zeros(1, T, device=d)
+    for causal_window in (W, 0):   # (without a window as a check of the listing alone: one head)
+        o = chs.attn_fwd_packed(q, k, v, i32(cu), None, lse, window=causal_window)
+        grads = chs.attn_bwd_packed(q, k, v, o, dout, lse, i32(cu), window=causal_window)
+        assert chs.attn_status() == chs.ATTN_OK
+        assert not o.isnan().any() and not any(g.isnan().any() for g in grads)
+        for at in (5, 127, 150000, 298990, 299000, T - 3):
+            lo = max(a for a in cu if a <= at)
+            hi = min(z for z in cu if z > at)
+            if causal_window:
+                a, z = max(lo, at - W + 1), min(hi, at + W)
+                want, _, bound, dwant, dbound = ref.attention(q[a:z], k[a:z], v[a:z], [0, z - a], True, W,
+                                                              dout=dout[a:z])
+                for got, w, b in zip((o, *grads), (want, *dwant), (bound, *dbound)):
+                    ref.check(got[at], w[at - a], b[at - a], at)
+            else:
+                rows = slice(lo, at + 1)
+                p = torch.softmax(k[rows, 0].double() @ q[at, 0].double() / 8, 0)
+                y, size = p @ v[rows, 0].double(), p @ v[rows, 0].double().abs()
+                assert bool(((o[at, 0].double() - y).abs() <= (1 + ref.U) * (ref.U + ref.F) * size
+                             + ref.U * y.abs()).all())
+
+
 def test_pools_of_2_31_elements():
     P, Hkv, page, Dh, T = 32768, 8, 64, 128, 300
     kp = torch.zeros(P, Hkv, page, Dh, dtype=torch.bfloat16, device="cuda")
