@@ -459,9 +459,10 @@ __device__ __forceinline__ void bwd_prep_tile(const BwdPrepPacked& p) {
   constexpr int kRowsPerSet = 256 / kLanes;
   constexpr int kSets = 128 / kRowsPerSet;
   const int tile = blockIdx.x / p.Hq, h = blockIdx.x - tile * p.Hq;
+  // (the list has room for every block's tile: its entry and the counts come at once)
+  const PackedTile e = packed_tile(p.pk, tile);
   const int3 n = packed_counts(p.pk);
   if (tile >= n.x + n.y + n.z) return;
-  const PackedTile e = packed_tile(p.pk, tile);
   const int sub = threadIdx.x % kLanes, r0 = threadIdx.x / kLanes;
   const __nv_bfloat16* po = p.o + h * p.o_head + 8 * sub;
   const __nv_bfloat16* pd = p.dout + h * p.do_head + 8 * sub;
@@ -471,13 +472,16 @@ __device__ __forceinline__ void bwd_prep_tile(const BwdPrepPacked& p) {
 #pragma unroll 1
   for (int s = 0; s < kSets; s += kBatch) {
     uint4 a[kBatch], b[kBatch];
+    float l[kBatch];
     bool valid[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int i = first + (s + k) * kRowsPerSet + r0;
       valid[k] = i >= 0;
       a[k] = b[k] = make_uint4(0u, 0u, 0u, 0u);
+      l[k] = __int_as_float(0x7f800000);
       if (valid[k]) {
+        if (sub == 0) l[k] = p.lse[(size_t)h * p.pk.T + e.start + i];
         a[k] = *reinterpret_cast<const uint4*>(po + (e.start + (long long)i) * p.o_row);
         b[k] = *reinterpret_cast<const uint4*>(pd + (e.start + (long long)i) * p.do_row);
       }
@@ -497,8 +501,7 @@ __device__ __forceinline__ void bwd_prep_tile(const BwdPrepPacked& p) {
       const int r = (s + k) * kRowsPerSet + r0, i = first + r;
       if (sub == 0) {
         if (!bwd_prep_exact(p, e.len, i)) p.delta[to + r] = valid[k] ? acc : 0.f;
-        p.lse2[to + r] = valid[k] ? p.lse[(size_t)h * p.pk.T + e.start + i] * 1.4426950408889634f
-                                  : __int_as_float(0x7f800000);
+        p.lse2[to + r] = l[k] * 1.4426950408889634f;
       }
     }
   }
