@@ -416,8 +416,9 @@ typedef struct {
  *     none, so the calls may run on several streams at the same time and in
  *     several captured graphs.
  *   - No sequence's result depends on another's rows, infinities and NaN
- *     included.  Within a sequence an infinity or NaN in K or V can reach the
- *     rows of its 128-row block that the mask hides it from, as in attn_fwd.
+ *     included.  Within a sequence an infinity or NaN in a row (of K and V, in
+ *     the backward pass of any tensor) can reach the rows of its 128-row block
+ *     that the mask hides it from, as in attn_fwd and attn_bwd.
  *   - The same inputs give the same bits.
  *   - B == 0 or T == 0 is a no-op.
  */
@@ -541,7 +542,8 @@ int attn_rope_frequencies(unsigned long long* turns, float* amplitude, int rotar
  * length outside [0, cols * page], before or after, latches
  * ATTN_ERR_INVALID_ARG and leaves that sequence as it is.  A used page number
  * outside [0, num_pages) latches it too and gives slots of -1.
- * Up to 8192 sequences (ATTN_ERR_UNSUPPORTED).  B == 0 is a no-op.
+ * A page that is given back belongs to one sequence.  Up to 8192 sequences
+ * (ATTN_ERR_UNSUPPORTED).  B == 0 is a no-op.
  */
 int attn_cache_plan(const int* delta, const int* seqlens, int* seqlens_out, int* table,
                     int* free_pages, const int* num_free, int* num_free_out, int* cu_seqlens,

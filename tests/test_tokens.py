@@ -170,6 +170,24 @@ def test_rope_append(Dh, rot, interleaved, scaling, factor, T, k_out):
     assert torch.equal(kp, expect_k) and torch.equal(vp, expect_v)
 
 
+def test_rope_append_of_a_decode_step():
+    # [B, H, 1, Dh], as attn_decode_paged takes the queries
+    gen = torch.Generator("cuda").manual_seed(4)
+    B, Hq, Hkv, Dh, page = 5, 4, 2, 128, 8
+    q, k, v = (torch.randn(B, h, 1, Dh, generator=gen, device="cuda").to(torch.bfloat16)
+               for h in (Hq, Hkv, Hkv))
+    pos, slots = i32([[7], [100000], [0], [-1], [12]]), i32([[5], [31], [0], [-1], [-1]])
+    kp, vp = pools(4, Hkv, page, Dh)
+    handle = chs.attn_rope_frequencies(Dh)
+    want_q, want_k = chs.attn_rope(q, k, pos, handle, q.clone(), k.clone())
+    qo, _ = chs.attn_rope_append(q, k, v, pos, handle, kp, vp, slots)
+    assert chs.attn_status() == chs.ATTN_OK and qo is q and torch.equal(q, want_q)
+    for b, s in enumerate([5, 31, 0]):
+        assert torch.equal(kp[s // page, :, s % page], want_k[b, :, 0])
+        assert torch.equal(vp[s // page, :, s % page], v[b, :, 0])
+    assert int((vp != 7).sum()) == 3 * Hkv * Dh
+
+
 def test_slots_outside_the_pools():
     q = torch.ones(4, 2, 64, dtype=torch.bfloat16, device="cuda")
     kp, vp = pools(3, 2, 8, 64)
