@@ -363,7 +363,7 @@ __device__ __forceinline__ void bwd_prep_rows(const BwdPrepPacked& p, const Pack
     return *reinterpret_cast<const uint4*>(x + (e.start + (long long)i) * rs + head * hs + at);
   };
   bool exact[2];
-  float l2[2], sum[2] = {0.f, 0.f};
+  float l2[2], sum[2] = {0.f, 0.f}, mass[2] = {0.f, 0.f};
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     const int i = i0 + g + 8 * half;
@@ -413,17 +413,22 @@ __device__ __forceinline__ void bwd_prep_rows(const BwdPrepPacked& p, const Pack
                             (p.window == 0 || i - j < p.window);
           const float w = ex2_approx(fmaf(s[n][2 * half + x], p.scale_log2, -l2[half]));
           sum[half] += seen ? w * d[n][2 * half + x] : 0.f;
+          mass[half] += seen ? w : 0.f;
         }
       }
     }
   }
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    float x = sum[half];
+    float x = sum[half], y = mass[half];
     x += __shfl_xor_sync(0xffffffffu, x, 1);
+    y += __shfl_xor_sync(0xffffffffu, y, 1);
     x += __shfl_xor_sync(0xffffffffu, x, 2);
+    y += __shfl_xor_sync(0xffffffffu, y, 2);
+    // (the weights' sum is 1 but for lse's rounding, which the passes' weights have too: divided
+    // by it, the row's dS sum to 0)
     if (exact[half] && c == 0)
-      p.delta[(size_t)h * p.S_pad + (e.stat + e.pad() + i0 + g + 8 * half)] = x;
+      p.delta[(size_t)h * p.S_pad + (e.stat + e.pad() + i0 + g + 8 * half)] = x / y;
   }
 }
 
