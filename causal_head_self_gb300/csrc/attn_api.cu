@@ -1121,14 +1121,17 @@ extern "C" int attn_cache_plan(const int* delta, const int* seqlens, int* seqlen
   if (T < 0 || T > kMostRows || capacity < 1 || capacity > kMostRows) return ATTN_ERR_INVALID_ARG;
   if ((long long)num_pages * page > kMostRows) return ATTN_ERR_INVALID_ARG;   // slots are 32-bit
   if (B > chs::cache_plan_max_sequences()) return ATTN_ERR_UNSUPPORTED;
-  if (B == 0) return ATTN_OK;
-  if (!usable(delta, 4) || !usable(seqlens, 4) || !usable(seqlens_out, 4) || !usable(table, 4) ||
+  // (of no sequences: no lengths and no table)
+  if ((B > 0 && (!usable(delta, 4) || !usable(seqlens, 4) || !usable(seqlens_out, 4) ||
+                 !usable(table, 4))) ||
       !usable(free_pages, 4) || !usable(num_free, 4) || !usable(num_free_out, 4) ||
       !usable(cu_seqlens, 4) || (T > 0 && (!usable(positions, 4) || !usable(slots, 4))))
     return ATTN_ERR_INVALID_ARG;
   const size_t lens = (size_t)B * 4, rows = (size_t)T * 4;
-  const Span in[] = {{delta, lens}, {seqlens, lens}, {num_free, 4}};
-  const Span out[] = {{seqlens_out, lens}, {num_free_out, 4}, {table, (size_t)B * cols * 4},
+  const Span in[] = {{B > 0 ? delta : nullptr, lens}, {B > 0 ? seqlens : nullptr, lens},
+                     {num_free, 4}};
+  const Span out[] = {{B > 0 ? seqlens_out : nullptr, lens}, {num_free_out, 4},
+                      {B > 0 ? table : nullptr, (size_t)B * cols * 4},
                       {free_pages, (size_t)capacity * 4}, {cu_seqlens, lens + 4},
                       {T > 0 ? positions : nullptr, rows}, {T > 0 ? slots : nullptr, rows}};
   for (int i = 0; i < 7; ++i) {

@@ -543,7 +543,8 @@ int attn_rope_frequencies(unsigned long long* turns, float* amplitude, int rotar
  * ATTN_ERR_INVALID_ARG and leaves that sequence as it is.  A used page number
  * outside [0, num_pages) latches it too and gives slots of -1.
  * A page that is given back belongs to one sequence.  Up to 8192 sequences
- * (ATTN_ERR_UNSUPPORTED).  B == 0 is a no-op.
+ * (ATTN_ERR_UNSUPPORTED).  B == 0 is a step of no tokens: cu_seqlens[0] is 0,
+ * positions and slots are -1.
  */
 int attn_cache_plan(const int* delta, const int* seqlens, int* seqlens_out, int* table,
                     int* free_pages, const int* num_free, int* num_free_out, int* cu_seqlens,

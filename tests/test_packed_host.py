@@ -209,7 +209,7 @@ def test_plan_refusals(lib):
                 dict(cols=1 << 20, page=1 << 11), dict(P=1 << 27), dict(T=2 ** 31 - 1)):
         assert plan(lib, **bad) == INVALID, bad
     assert plan(lib, page=12) == UNSUPPORTED and plan(lib, B=8193) == UNSUPPORTED
-    assert plan(lib, B=0) == OK
+    assert plan(lib, {"free": None}, B=0) == INVALID and plan(lib, {"cu": None}, B=0) == INVALID
     names = ["delta", "seqlens", "seqlens_out", "table", "free", "num_free", "num_free_out", "cu",
              "positions", "slots"]
     outputs = ["seqlens_out", "table", "free", "num_free_out", "cu", "positions", "slots"]

@@ -299,6 +299,18 @@ def test_plan_is_all_or_nothing():
     assert got[2] == [29, 30, 31, 40]
 
 
+@pytest.mark.parametrize("T", [0, 1, 5000, 20000])
+def test_a_plan_of_no_sequences(T):
+    none, table = i32([]), torch.empty((0, 4), dtype=torch.int32, device="cuda")
+    num_free, height = i32([2]), i32([-9])
+    out = [torch.full((n,), 7, dtype=torch.int32, device="cuda") for n in (1, T, T)]
+    cu, positions, slots = chs.attn_cache_plan(none, none, table, i32([5, 6, 7]), num_free, rows=T, page=8,
+                                               num_pages=9, num_free_out=height, cu_seqlens=out[0],
+                                               positions=out[1], slots=out[2])
+    assert chs.attn_status() == chs.ATTN_OK and height.tolist() == [2]
+    assert cu.tolist() == [0] and bool((positions == -1).all()) and bool((slots == -1).all())
+
+
 @pytest.mark.parametrize("n,d", [(-1, 3), (25, 0), (20, 5), (5, -6), (2 ** 31 - 1, 1), (0, -(2 ** 31))])
 def test_a_length_out_of_range_leaves_its_sequence(n, d):
     got, state, _ = plan([5, n, 9], [1, d, 8], [[3, -1, -1], [8, 9, 9], [4, 5, -1]], [6, 7], 10)
