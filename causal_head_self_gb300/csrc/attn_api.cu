@@ -189,8 +189,8 @@ bool encode_bf16_rows_map(CUtensorMap* map, const void* base, int Dh, int rows, 
 bool encode_packed_map(CUtensorMap* map, const PackedRows& x, int Dh, int T, int box_rows,
                        bool padded, bool* heads_inner) {
   // strides of an axis with one entry do not matter: any that the map takes
-  const long long head = x.H == 1 ? (x.row > Dh ? x.row : Dh) : x.head;
-  const long long row = T == 1 ? (x.H == 1 ? Dh : x.head) : x.row;
+  const long long head = x.H > 1 ? x.head : T > 1 ? x.row : Dh;
+  const long long row = T > 1 ? x.row : head;
   // the axes in the order of their strides
   *heads_inner = x.H > 1 && head < row;
   const cuuint64_t R = (cuuint64_t)row * 2, H = (cuuint64_t)head * 2;

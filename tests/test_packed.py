@@ -83,6 +83,25 @@ def test_strides(Dh, kind):
     assert all(torch.equal(a.contiguous(), b) for a, b in zip(grads, grads2))
 
 
+@pytest.mark.parametrize("Dh", [64, 128, 256])
+@pytest.mark.parametrize("stride", [4, 8, 9999])
+def test_one_row_of_one_head(Dh, stride):
+    # an axis of one entry has any stride: softmax over one key, whose gradient is 0 but dv's
+    x = torch.randn(4, Dh, device="cuda").to(torch.bfloat16)
+    q, k, v, dout = (y.as_strided((1, 1, Dh), (stride, stride + 3, 1)) for y in x)
+    o, lse = torch.zeros(1, 1, Dh, device="cuda", dtype=torch.bfloat16), torch.zeros(1, 1, device="cuda")
+    out = [torch.zeros_like(o) for _ in range(3)]
+    places = [y.as_strided((1, 1, Dh), (stride, stride + 3, 1)) for y in (o, *out)]
+    chs.attn_fwd_packed(q, k, v, i32([0, 1]), places[0], lse)
+    chs.attn_bwd_packed(q, k, v, places[0], dout, lse, i32([0, 1]), *places[1:])
+    assert chs.attn_status() == chs.ATTN_OK
+    assert torch.equal(o[0, 0], v[0, 0]) and torch.equal(out[2][0, 0], dout[0, 0])
+    want, L, bound, dwant, dbound = ref.attention(q, k, v, [0, 1], dout=dout)
+    assert abs(float(lse) - float(L)) < ref.F
+    for got, w, b in zip(out, dwant, dbound):
+        ref.check(got, w, b)
+
+
 @pytest.mark.parametrize("Dh,n", [(64, 2560), (128, 768), (128, 2560), (256, 768)])
 def test_one_sequence_is_the_batch_form(Dh, n):
     gen = torch.Generator("cuda").manual_seed(5)
