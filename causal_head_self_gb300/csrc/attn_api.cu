@@ -834,22 +834,38 @@ bool rows_same(const Rows& a, const Rows& b) {
          a.head() == b.head();
 }
 
-// May the two share an element?  Heads of one wider tensor (a projection's output, split into
-// queries, keys and values) lie between one another: rows at one stride, each within its own
-// part of it.
+// How far x reaches from each multiple of `step` that it starts at, if its strides of at least
+// `step` are multiples of it; else more than `step`.
+long long reach(const Rows& x, long long step) {
+  long long n = x.Dh;
+  const long long stride[] = {x.batch(), x.row(), x.head()};
+  const int count[] = {x.B, x.S, x.H};
+  for (int i = 0; i < 3; ++i) {
+    if (stride[i] < step)
+      n += (count[i] - 1) * stride[i];
+    else if (stride[i] % step != 0)
+      return step + 1;
+  }
+  return n;
+}
+
+// May the two share an element?  Parts of one wider tensor (a projection's output, split into
+// queries, keys and values along its heads, or along an axis around or inside them) lie between
+// one another: at one of the strides, each within its own part of every step.
 bool rows_overlap(const Rows& a, const Rows& b) {
   if (a.empty() || b.empty()) return false;
   if (!overlaps(a.t->data, a.bytes(), b.t->data, b.bytes())) return false;
-  const long long R = a.row();
-  const bool one_stride = a.S > 1 && b.row() == R && (a.B == 1 || a.batch() == a.S * R) &&
-                          (b.B == 1 || b.batch() == b.S * R);
-  if (!one_stride) return true;
-  const long long wa = (a.H - 1) * a.head() + a.Dh, wb = (b.H - 1) * b.head() + b.Dh;
-  const long long bytes = (long long)(reinterpret_cast<uintptr_t>(b.t->data) -
-                                      reinterpret_cast<uintptr_t>(a.t->data));
-  const long long step = 2 * R;
-  const long long d = ((bytes % step) + step) % step / 2;   // b's place in a's row
-  return !(wa <= R && wb <= R && d >= wa && d + wb <= R);
+  const long long between = (long long)(reinterpret_cast<uintptr_t>(b.t->data) -
+                                        reinterpret_cast<uintptr_t>(a.t->data)) / 2;
+  for (const Rows* x : {&a, &b}) {
+    for (const long long step : {x->batch(), x->row(), x->head()}) {
+      if (step <= 0) continue;
+      const long long wa = reach(a, step), wb = reach(b, step);
+      const long long d = (between % step + step) % step;   // b's place in a's step
+      if (wa <= step && wb <= step && d >= wa && d + wb <= step) return false;
+    }
+  }
+  return true;
 }
 
 bool rows_overlap(const Rows& a, const void* p, size_t bytes) {

@@ -406,8 +406,8 @@ typedef struct {
  * In the packed calls below:
  *   - Strides are at least Dh.  The elements of an output are distinct, and
  *     apart from every other tensor's (ATTN_ERR_INVALID_ARG otherwise);
- *     tensors between one another (slices of one wider tensor along its heads)
- *     are apart.
+ *     tensors between one another (slices of one wider tensor along its heads,
+ *     or along an axis around or inside them) are apart.
  *   - Offsets that are not ascending within [0, T] latch ATTN_ERR_INVALID_ARG
  *     for attn_status(), and nothing is written.
  *   - workspace: device, 256-byte aligned, of at least the bytes that the

@@ -83,6 +83,32 @@ def test_strides(Dh, kind):
     assert all(torch.equal(a.contiguous(), b) for a, b in zip(grads, grads2))
 
 
+@pytest.mark.parametrize("axis", [0, 1, 2, 3])
+@pytest.mark.parametrize("Dh", [64, 128, 256])
+def test_parts_of_one_tensor(Dh, axis):
+    # q, k, v and their gradients are parts of one tensor each: [3, T, H, Dh], [T, 3, H, Dh],
+    # [T, H, 3, Dh], [H, 3, T, Dh]
+    gen = torch.Generator("cuda").manual_seed(9)
+    H, cu = 3, [0, 200, 201, 330]
+    T = cu[-1]
+    shape = [(3, T, H, Dh), (T, 3, H, Dh), (T, H, 3, Dh), (H, 3, T, Dh)][axis]
+    x = torch.randn(shape, generator=gen, device="cuda").to(torch.bfloat16)
+    dx = torch.zeros_like(x)
+
+    def parts(y):
+        return y.unbind(axis) if axis < 3 else [z.transpose(0, 1) for z in y.unbind(1)]
+    q, k, v = parts(x)
+    dout = torch.randn(T, H, Dh, generator=gen, device="cuda").to(torch.bfloat16)
+    lse = torch.zeros(H, T, device="cuda")
+    o = chs.attn_fwd_packed(q, k, v, i32(cu), None, lse)
+    chs.attn_bwd_packed(q, k, v, o, dout, lse, i32(cu), *parts(dx))
+    assert chs.attn_status() == chs.ATTN_OK
+    same = [y.contiguous() for y in (q, k, v)]
+    assert torch.equal(o, chs.attn_fwd_packed(*same, i32(cu)))
+    for a, b in zip(parts(dx), chs.attn_bwd_packed(*same, o, dout, lse, i32(cu))):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("Dh", [64, 128, 256])
 @pytest.mark.parametrize("stride", [4, 8, 9999])
 def test_one_row_of_one_head(Dh, stride):

@@ -114,6 +114,32 @@ def test_slices_of_one_tensor_are_apart(lib):
     assert fwd(lib, tensors=t, **few) == INVALID
 
 
+@pytest.mark.parametrize("order", ["rows, part, head", "rows, head, part", "part, rows, head",
+                                   "part, head, rows", "head, part, rows"])
+def test_parts_of_one_tensor_are_apart(lib, order):
+    # as many K/V heads as query heads: q, k, v (and their gradients) are the three parts of a
+    # tensor with an axis of them, wherever that lies
+    T, H, Dh, size = 40, 4, 128, dict(rows=40, part=3, head=4)
+    step, at = {}, Dh
+    for axis in reversed(order.split(", ")):
+        step[axis], at = at, at * size[axis]
+
+    def part(i, n, by=0):
+        return rows(i, data=ptr(i) + 2 * (n * step["part"] + by), row=step["rows"], head=step["head"])
+    t = dict(q=part(0, 0), k=part(0, 1), v=part(0, 2), o=rows(2), dout=rows(3), dq=part(1, 0),
+             dk=part(1, 1), dv=part(1, 2))
+    few = dict(ws_bytes=256, Hkv=H)   # the workspace's size is the last check
+    assert bwd(lib, tensors=t, **few) == SCRATCH
+    for off in (-8, 8):
+        assert bwd(lib, tensors=dict(t, dk=part(1, 1, off)), **few) == INVALID
+    assert bwd(lib, tensors=dict(t, dv=part(1, 1)), **few) == INVALID
+    assert bwd(lib, tensors=dict(t, dv=part(0, 2)), **few) == INVALID
+    # a rotation in place (one that is sound would be launched: only what is refused here)
+    inside = dict(B=1, S=T, Hq=H, Hkv=H, q=part(0, 0), qo=part(0, 0), k=part(0, 1), ko=part(0, 1))
+    assert rope(lib, **dict(inside, ko=part(0, 1, 8))) == INVALID
+    assert rope(lib, **dict(inside, k=part(0, 0, 64), ko=part(0, 0, 64))) == INVALID
+
+
 def test_packed_workspace_queries(lib):
     # (the forward's answer depends on the GPU: only its refusals here)
     n = ctypes.c_size_t()

@@ -106,6 +106,23 @@ def test_rope_of_a_batch(Dh, rot):
         close(y, turned(x, pos[:, None], frequencies(rot)))
 
 
+@pytest.mark.parametrize("axis", [1, 2])
+def test_rope_inside_one_tensor(axis):
+    # queries and keys as parts of a projection's output [T, 3, H, Dh] or [T, H, 3, Dh], in place
+    gen = torch.Generator("cuda").manual_seed(2)
+    T, H, Dh = 70, 3, 128
+    x = torch.randn((T, 3, H, Dh) if axis == 1 else (T, H, 3, Dh), generator=gen,
+                    device="cuda").to(torch.bfloat16)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    handle = chs.attn_rope_frequencies(Dh)
+    q, k, v = x.unbind(axis)
+    want = chs.attn_rope(q.contiguous(), k.contiguous(), pos, handle)
+    kept = v.clone()
+    chs.attn_rope(q, k, pos, handle, q, k)
+    assert chs.attn_status() == chs.ATTN_OK
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(v, kept)
+
+
 def test_rope_gradient_and_infinities():
     # <turn(x), y> = <x, turn back(y)>: the inverse carries gradients; values that are not
     # turned are copied whatever they are
