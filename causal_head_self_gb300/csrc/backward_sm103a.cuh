@@ -865,7 +865,7 @@ __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdPar
   const uint32_t lane_addr = tbase + ((uint32_t)((warp % 4) * 32) << 16);
   const uint32_t colS = lane_addr + Cfg::kColS + Cfg::kCols * wg;   // this warpgroup's scores
   const uint32_t colDP = lane_addr + Cfg::kColDP + Cfg::kCols * wg;
-  const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
+  const float2 neg_sl2 = make_float2(-p.scale_log2, -p.scale_log2);
   uint32_t u = 0;
   int items = 0;
   bool ok = true;
@@ -884,10 +884,15 @@ __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdPar
         const int st = (int)(u & 1u);
         // the stage's lse2 / D (bulk copies counted on q_full)
         if (!(ok = mbar_wait(&sm.q_full[st], (u >> 1) & 1u, abort))) break;
+        // (read ahead of the wait for the scores: a row of columns' values for every lane takes
+        // the shared memory's whole bandwidth for half as long as the exponentials take)
+        const uint32_t at_l = smem_u32(sm.lse2[st] + Cfg::kCols * wg);
+        const uint32_t at_d = smem_u32(sm.dlt[st] + Cfg::kCols * wg);
+        float4 l[Cfg::kCols / 4];
+#pragma unroll
+        for (int c = 0; c < Cfg::kCols / 4; ++c) l[c] = ld_shared_f4(at_l + 16 * c);
         if (!(ok = mbar_wait(&sm.s_full, u & 1u, abort))) break;
         tc_fence_after_sync();
-        const float4* L4 = reinterpret_cast<const float4*>(sm.lse2[st] + Cfg::kCols * wg);
-        const float4* D4 = reinterpret_cast<const float4*>(sm.dlt[st] + Cfg::kCols * wg);
         // visible query columns of key j: c in [clo, chi] of this warpgroup's
         // columns (query i = 128 qb + kCols wg + c)
         const bool msk = bwd_needs_mask(p, I.seq, qb, I.kb);
@@ -910,30 +915,31 @@ __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdPar
 #pragma unroll
         for (int c = 0; c < Cfg::kChunks; ++c) tmem_ld_wait(x[c]);
         float pf[Cfg::kCols];   // P^T of this row's columns (fp32)
+        // (the mask in a loop of its own: a branch at every pair would keep the exponentials of
+        // one pair from overlapping the next one's)
+#pragma unroll
+        for (int col = 0; col < Cfg::kCols; col += 2) {
+          const int c = col / 32, k = col % 32;
+          const float4 l4 = l[col / 4];
+          const float2 xs = __ffma2_rn(
+              make_float2(__uint_as_float(x[c][k]), __uint_as_float(x[c][k + 1])), neg_sl2,
+              col % 4 ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y));
+          pf[col] = ex2_approx(-xs.x);   // (the sign is the instruction's)
+          pf[col + 1] = ex2_approx(-xs.y);
+        }
+        if (msk) {
+#pragma unroll
+          for (int col = 0; col < Cfg::kCols; ++col) {
+            const int at = PK == 2 ? col & column : col;
+            pf[col] = zero_unless_le(pf[col], (uint32_t)(at - clo), span);
+          }
+        }
 #pragma unroll
         for (int c = 0; c < Cfg::kChunks; ++c) {
           uint32_t w16[16];
 #pragma unroll
-          for (int e4 = 0; e4 < 8; ++e4) {
-            const float4 l = L4[8 * c + e4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int e = 2 * e4 + h, col = 32 * c + 2 * e;
-              const float2 xs = __ffma2_rn(
-                  make_float2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), sl2,
-                  h ? make_float2(-l.z, -l.w) : make_float2(-l.x, -l.y));
-              float a = ex2_approx(xs.x), b = ex2_approx(xs.y);
-              if (msk) {
-                const int at = PK == 2 ? col & column : col;
-                const int at1 = PK == 2 ? (col + 1) & column : col + 1;
-                a = zero_unless_le(a, (uint32_t)(at - clo), span);
-                b = zero_unless_le(b, (uint32_t)(at1 - clo), span);
-              }
-              pf[col] = a;
-              pf[col + 1] = b;
-              w16[e] = pack_bf16x2(a, b);
-            }
-          }
+          for (int e = 0; e < 16; ++e)
+            w16[e] = pack_bf16x2(pf[32 * c + 2 * e], pf[32 * c + 2 * e + 1]);
           tmem_st_32x32b_x16(colS + 16 * c, w16);
         }
         const bool two = bwd_two_parts<PK>(p, qb);
@@ -953,6 +959,9 @@ __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdPar
         tc_fence_before_sync();
         mbar_arrive(&sm.p_full);
 
+        float4 dd4[8];   // D of a chunk's columns, a chunk ahead
+#pragma unroll
+        for (int e4 = 0; e4 < 8; ++e4) dd4[e4] = ld_shared_f4(at_d + 16 * e4);
         if (!(ok = mbar_wait(&sm.dp_full, u & 1u, abort))) break;
         tc_fence_after_sync();
 #pragma unroll
@@ -963,7 +972,8 @@ __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdPar
           uint32_t w16[16];
 #pragma unroll
           for (int e4 = 0; e4 < 8; ++e4) {
-            const float4 d = D4[8 * c + e4];
+            const float4 d = dd4[e4];
+            if (c + 1 < Cfg::kChunks) dd4[e4] = ld_shared_f4(at_d + 128 * (c + 1) + 16 * e4);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int e = 2 * e4 + h, col = 32 * c + 2 * e;
@@ -1407,13 +1417,13 @@ __device__ __forceinline__ void bwd_dq_softmax(BwdQSmem<DH>& sm, const BwdParams
         const int col = 2 * e, c = col / 32, k = col % 32;
         const float2 xs = __ffma2_rn(make_float2(__uint_as_float(x[c][k]), __uint_as_float(x[c][k + 1])),
                                      sl2, negL);
-        float a = ex2_approx(xs.x), b = ex2_approx(xs.y);
-        if (msk) {
-          a = zero_unless_le(a, (uint32_t)(col - clo), span);
-          b = zero_unless_le(b, (uint32_t)(col + 1 - clo), span);
-        }
-        pf[col] = a;
-        pf[col + 1] = b;
+        pf[col] = ex2_approx(xs.x);
+        pf[col + 1] = ex2_approx(xs.y);
+      }
+      if (msk) {   // (a loop of its own, as in the dK/dV pass)
+#pragma unroll
+        for (int col = 0; col < Cfg::kCols; ++col)
+          pf[col] = zero_unless_le(pf[col], (uint32_t)(col - clo), span);
       }
 
       const uint32_t b = u & 1u;   // this block's dP buffer
