@@ -376,7 +376,7 @@ __device__ __forceinline__ void bwd256_kv_softmax(Bwd256KvSmem<DK>& sm, const Bw
   const int wg = warp / 4;
   const int t = (warp % 4) * 32 + lane;
   const uint32_t lane_addr = tbase + ((uint32_t)((warp % 4) * 32) << 16);
-  const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
+  const float2 neg_sl2 = make_float2(-p.scale_log2, -p.scale_log2);
   uint32_t u = 0;
   int items = 0;
   bool ok = true;
@@ -396,6 +396,11 @@ __device__ __forceinline__ void bwd256_kv_softmax(Bwd256KvSmem<DK>& sm, const Bw
         // the step's lse2 / D (bulk copies counted on the Q or the dO stage)
         uint64_t* stat_full = DK ? &sm.q_full[st] : &sm.do_full[st];
         if (!(ok = mbar_wait(stat_full, (u / Smem::kStagesStat) & 1u, abort))) break;
+        const uint32_t at_l = smem_u32(sm.lse2[st] + Cfg::kCols * wg);
+        const uint32_t at_d = smem_u32(sm.dlt[st] + Cfg::kCols * wg);
+        float4 l[8];   // (ahead of the wait, as in backward_sm103a.cuh)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) l[c] = ld_shared_f4(at_l + 16 * c);
         if (!(ok = mbar_wait(&sm.s_full[b], (u >> 1) & 1u, abort))) break;
         tc_fence_after_sync();
         // visible query columns of key j: c in [clo, chi] (query i = 64 qb + 32 wg + c)
@@ -407,8 +412,6 @@ __device__ __forceinline__ void bwd256_kv_softmax(Bwd256KvSmem<DK>& sm, const Bw
         const uint32_t span = chi >= clo ? (uint32_t)(chi - clo) : 0u;
         if (chi < clo) clo = 1 << 30;
         const bool msk = clo > 0 || chi < Cfg::kCols - 1;
-        const float4* L4 = reinterpret_cast<const float4*>(sm.lse2[st] + Cfg::kCols * wg);
-        const float4* D4 = reinterpret_cast<const float4*>(sm.dlt[st] + Cfg::kCols * wg);
         const uint32_t colS = lane_addr + Cfg::kColS + 64 * b + Cfg::kCols * wg;
         uint32_t x[32];
         tmem_ld_32x32b_x32(colS, x);
@@ -416,24 +419,21 @@ __device__ __forceinline__ void bwd256_kv_softmax(Bwd256KvSmem<DK>& sm, const Bw
         float pf[Cfg::kCols];
         uint32_t w16[16];
 #pragma unroll
-        for (int e4 = 0; e4 < 8; ++e4) {
-          const float4 l = L4[e4];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int e = 2 * e4 + h, col = 2 * e;
-            const float2 xs = __ffma2_rn(
-                make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sl2,
-                h ? make_float2(-l.z, -l.w) : make_float2(-l.x, -l.y));
-            float a = ex2_approx(xs.x), c = ex2_approx(xs.y);
-            if (msk) {
-              a = zero_unless_le(a, (uint32_t)(col - clo), span);
-              c = zero_unless_le(c, (uint32_t)(col + 1 - clo), span);
-            }
-            pf[col] = a;
-            pf[col + 1] = c;
-            w16[e] = pack_bf16x2(a, c);
-          }
+        for (int col = 0; col < Cfg::kCols; col += 2) {
+          const float4 l4 = l[col / 4];
+          const float2 xs = __ffma2_rn(
+              make_float2(__uint_as_float(x[col]), __uint_as_float(x[col + 1])), neg_sl2,
+              col % 4 ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y));
+          pf[col] = ex2_approx(-xs.x);
+          pf[col + 1] = ex2_approx(-xs.y);
         }
+        if (msk) {
+#pragma unroll
+          for (int col = 0; col < Cfg::kCols; ++col)
+            pf[col] = zero_unless_le(pf[col], (uint32_t)(col - clo), span);
+        }
+#pragma unroll
+        for (int e = 0; !DK && e < 16; ++e) w16[e] = pack_bf16x2(pf[2 * e], pf[2 * e + 1]);
         const bool two = bwd_two_parts<PK>(p, qb / 2);
         auto low = [&](uint32_t to) {   // the low parts of pf's pairs
           uint32_t l16[16];
@@ -450,6 +450,9 @@ __device__ __forceinline__ void bwd256_kv_softmax(Bwd256KvSmem<DK>& sm, const Bw
           mbar_arrive(&sm.p_full[b]);
           continue;
         }
+        float4 d4[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) d4[c] = ld_shared_f4(at_d + 16 * c);
         if (!(ok = mbar_wait(&sm.dp_full[b], (u >> 1) & 1u, abort))) break;
         tc_fence_after_sync();
         const uint32_t colDP = lane_addr + Cfg::kColDP + 64 * b + Cfg::kCols * wg;
@@ -458,7 +461,7 @@ __device__ __forceinline__ void bwd256_kv_softmax(Bwd256KvSmem<DK>& sm, const Bw
         tmem_ld_wait(y);
 #pragma unroll
         for (int e4 = 0; e4 < 8; ++e4) {
-          const float4 d = D4[e4];
+          const float4 d = d4[e4];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int e = 2 * e4 + h, col = 2 * e;
@@ -868,13 +871,13 @@ __device__ __forceinline__ void bwd256_dq_softmax(Bwd256QSmem& sm, const BwdPara
         const int col = 2 * e;
         const float2 xs = __ffma2_rn(make_float2(__uint_as_float(x[col]), __uint_as_float(x[col + 1])),
                                      sl2, negL);
-        float a = ex2_approx(xs.x), c = ex2_approx(xs.y);
-        if (msk) {
-          a = zero_unless_le(a, (uint32_t)(col - clo), span);
-          c = zero_unless_le(c, (uint32_t)(col + 1 - clo), span);
-        }
-        pf[col] = a;
-        pf[col + 1] = c;
+        pf[col] = ex2_approx(xs.x);
+        pf[col + 1] = ex2_approx(xs.y);
+      }
+      if (msk) {
+#pragma unroll
+        for (int col = 0; col < Cfg::kCols; ++col)
+          pf[col] = zero_unless_le(pf[col], (uint32_t)(col - clo), span);
       }
       const uint32_t b = u & 1u;   // this block's dP buffer
       const uint32_t colDP = lane_addr + Cfg::kColDP + 64 * b + Cfg::kCols * wg;
