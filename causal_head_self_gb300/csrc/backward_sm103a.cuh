@@ -220,6 +220,11 @@ struct BwdCfg {
   // takes the columns of the dK/dV pass's second accumulator
   static constexpr uint32_t kColDP1 = kColA1;
   static_assert(kColA0 + DH <= kColDP1, "dQ accumulator and the second dP buffer");
+  // the dK/dV pass at Dh 64: its accumulators side by side leave room for a second S buffer, and
+  // shared memory for a third stage of queries
+  static constexpr int kBufsS = DH == 64 ? 2 : 1, kStagesQ = DH == 64 ? 3 : 2;
+  static constexpr uint32_t kColAcc1 = kColA0 + DH, kColS1 = 384;
+  static_assert(kBufsS == 1 || kColAcc1 + DH <= kColS1, "two S buffers");
 };
 
 // Where the bf16 pairs of columns 16 kk .. 16 kk + 15 of a 128-column S or dP
@@ -588,13 +593,14 @@ struct __align__(1024) BwdKvSmem {
   using Cfg = BwdCfg<DH>;
   uint8_t k[Cfg::kTile];           // this item's key block (stays)
   uint8_t v[Cfg::kTile];           // this item's value block (stays)
-  uint8_t q[2][Cfg::kTile];        // query blocks, two stages
-  uint8_t dO[2][Cfg::kTile];       // their output gradients
-  float lse2[2][128];              // their log-sum-exps (log2 units)
-  float dlt[2][128];               // their D_i
+  uint8_t q[Cfg::kStagesQ][Cfg::kTile];    // query blocks
+  uint8_t dO[Cfg::kStagesQ][Cfg::kTile];   // their output gradients
+  float lse2[Cfg::kStagesQ][128];          // their log-sum-exps (log2 units)
+  float dlt[Cfg::kStagesQ][128];           // their D_i
   uint64_t kv_full, kv_empty;
-  uint64_t q_full[2], q_empty[2];
-  uint64_t s_full, dp_full, p_full, ds_full, acc_final, mma_done;
+  uint64_t q_full[Cfg::kStagesQ], q_empty[Cfg::kStagesQ];
+  uint64_t s_full[Cfg::kBufsS], p_full[Cfg::kBufsS];
+  uint64_t dp_full, ds_full, acc_final, mma_done;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -690,8 +696,8 @@ __device__ __forceinline__ void bwd_dkdv_producer(BwdKvSmem<DH>& sm, const BwdPa
     for (int hh = 0; ok && hh < p.group; hh += heads) {
       const int bh = I.b * p.Hq + I.g * p.group + hh;
       for (int qb = I.lo; qb <= I.hi; ++qb, ++u) {
-        const int st = (int)(u & 1u);
-        const uint32_t ph = (u >> 1) & 1u;
+        const int st = (int)(u % (uint32_t)Cfg::kStagesQ);
+        const uint32_t ph = (u / (uint32_t)Cfg::kStagesQ) & 1u;
         if (!(ok = mbar_wait(&sm.q_empty[st], ph ^ 1u, abort))) break;
         const size_t row0 = (size_t)bh * p.S_pad + (I.seq.stat + 128 * qb);
         // (checked builds: a query block of the sequence, of a query head of
@@ -720,7 +726,7 @@ __device__ __forceinline__ void bwd_dkdv_producer(BwdKvSmem<DH>& sm, const BwdPa
   }
   // every copy this thread started has landed before the CTA may exit
   if (items > 0) bwd_wait_drain(&sm.kv_full, (uint32_t)(items - 1) & 1u);
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < Cfg::kStagesQ; ++i)
     if (loaded & (1u << i)) bwd_wait_drain(&sm.q_full[i], (par >> i) & 1u);
 }
 
@@ -729,6 +735,8 @@ __device__ __forceinline__ void bwd_dkdv_producer(BwdKvSmem<DH>& sm, const BwdPa
 // S(n+1) (its columns held P(n), which dV(n), issued before it, reads),
 // dK(n) once dS(n) is written, dP(n+1) (its columns held dS(n)).  The
 // element-wise work of step n+1 therefore overlaps dK(n) and dP(n+1).
+// With two S buffers (Dh 64) S(n+1) goes first: its columns held P(n-1), and
+// the scores of the next step are there when the element-wise warps are.
 template <int DH, int PK>
 __device__ __forceinline__ void bwd_dkdv_issuer(BwdKvSmem<DH>& sm, const BwdParams& p,
                                                 volatile int* abort) {
@@ -744,6 +752,12 @@ __device__ __forceinline__ void bwd_dkdv_issuer(BwdKvSmem<DH>& sm, const BwdPara
   const uint64_t dq_mn = kMnMajor | (smem_u32(sm.q[0]) >> 4);
   const uint64_t ddo_mn = kMnMajor | (smem_u32(sm.dO[0]) >> 4);
   constexpr uint64_t kStage = Cfg::kTile >> 4;   // q[1] - q[0] (and dO) in descriptor units
+  constexpr bool kTwoS = Cfg::kBufsS == 2;
+  auto stage = [](uint32_t x) { return x % (uint32_t)Cfg::kStagesQ; };
+  auto stage_ph = [](uint32_t x) { return (x / (uint32_t)Cfg::kStagesQ) & 1u; };
+  auto buf = [](uint32_t x) { return kTwoS ? x & 1u : 0u; };             // of S and P
+  auto buf_ph = [](uint32_t x) { return (kTwoS ? x >> 1 : x) & 1u; };
+  auto col_s = [&](uint32_t x) { return buf(x) ? Cfg::kColS1 : Cfg::kColS; };
   // D (128 x 128) = A (128 x DH) B^T, both K-major (DH contiguous)
   auto mma_nt = [&](uint32_t d, uint64_t a, uint64_t b) {
 #pragma unroll
@@ -782,30 +796,31 @@ __device__ __forceinline__ void bwd_dkdv_issuer(BwdKvSmem<DH>& sm, const BwdPara
     const int N = (PK ? p.group >> I.seq.fold : p.group) * (I.hi - I.lo + 1);
     if (!(ok = wait_all(&sm.kv_full, (uint32_t)items & 1u))) break;
     ++items;
-    if (!(ok = wait_all(&sm.q_full[u & 1u], (u >> 1) & 1u))) break;
-    tc_fence_after_sync();
-    mma_nt(Cfg::kColS, dk_, dq_k + (u & 1u) * kStage);
-    mma_commit_warp(&sm.s_full);
-    mma_nt(Cfg::kColDP, dv_, ddo_k + (u & 1u) * kStage);
+    // S of step x
+    auto scores = [&](uint32_t x) -> bool {
+      if (!wait_all(&sm.q_full[stage(x)], stage_ph(x))) return false;
+      tc_fence_after_sync();
+      mma_nt(col_s(x), dk_, dq_k + stage(x) * kStage);                   // S^T = K Q^T
+      mma_commit_warp(&sm.s_full[buf(x)]);
+      return true;
+    };
+    if (!(ok = scores(u))) break;
+    mma_nt(Cfg::kColDP, dv_, ddo_k + stage(u) * kStage);
     mma_commit_warp(&sm.dp_full);
     if (N == 1) mma_commit_warp(&sm.kv_empty);
     int qb = I.lo;   // step n's query block (of one head after another)
     for (int n = 0; n < N; ++n, ++u) {
-      const uint64_t st = u & 1u, st1 = (u + 1) & 1u;
+      const uint64_t st = stage(u), st1 = stage(u + 1);
       const bool two = bwd_two_parts<PK>(p, qb);
       if (PK) qb = qb == I.hi ? I.lo : qb + 1;
-      if (!(ok = wait_all(&sm.p_full, u & 1u))) break;
+      if (kTwoS && n + 1 < N && !(ok = scores(u + 1))) break;
+      if (!(ok = wait_all(&sm.p_full[buf(u)], buf_ph(u)))) break;
       tc_fence_after_sync();
-      mma_acc(Cfg::kColA0, Cfg::kColS, ddo_mn + st * kStage, n == 0, two);   // dV += P^T dO
-      if (n + 1 < N) {
-        if (!(ok = wait_all(&sm.q_full[st1], ((u + 1) >> 1) & 1u))) break;
-        tc_fence_after_sync();
-        mma_nt(Cfg::kColS, dk_, dq_k + st1 * kStage);                  // S^T(n+1) = K Q^T
-        mma_commit_warp(&sm.s_full);
-      }
+      mma_acc(Cfg::kColA0, col_s(u), ddo_mn + st * kStage, n == 0, two);     // dV += P^T dO
+      if (!kTwoS && n + 1 < N && !(ok = scores(u + 1))) break;
       if (!(ok = wait_all(&sm.ds_full, u & 1u))) break;
       tc_fence_after_sync();
-      mma_acc(Cfg::kColA1, Cfg::kColDP, dq_mn + st * kStage, n == 0, two);   // dK += dS^T Q
+      mma_acc(Cfg::kColAcc1, Cfg::kColDP, dq_mn + st * kStage, n == 0, two); // dK += dS^T Q
       mma_commit_warp(&sm.q_empty[st]);
       if (n + 1 < N) {
         mma_nt(Cfg::kColDP, dv_, ddo_k + st1 * kStage);                 // dP^T(n+1) = V dO^T
@@ -863,7 +878,7 @@ __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdPar
   const int wg = warp / 4;
   const int t = (warp % 4) * 32 + lane;
   const uint32_t lane_addr = tbase + ((uint32_t)((warp % 4) * 32) << 16);
-  const uint32_t colS = lane_addr + Cfg::kColS + Cfg::kCols * wg;   // this warpgroup's scores
+  constexpr bool kTwoS = Cfg::kBufsS == 2;
   const uint32_t colDP = lane_addr + Cfg::kColDP + Cfg::kCols * wg;
   const float2 neg_sl2 = make_float2(-p.scale_log2, -p.scale_log2);
   uint32_t u = 0;
@@ -881,9 +896,12 @@ __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdPar
     const int heads = 1 << I.seq.fold;
     for (int hh = 0; ok && hh < p.group; hh += heads) {
       for (int qb = I.lo; qb <= I.hi; ++qb, ++u) {
-        const int st = (int)(u & 1u);
+        const int st = (int)(u % (uint32_t)Cfg::kStagesQ);
+        // this step's S buffer, its phase, and this warpgroup's scores in it
+        const uint32_t b = kTwoS ? u & 1u : 0u, ph = (kTwoS ? u >> 1 : u) & 1u;
+        const uint32_t colS = lane_addr + (b ? Cfg::kColS1 : Cfg::kColS) + Cfg::kCols * wg;
         // the stage's lse2 / D (bulk copies counted on q_full)
-        if (!(ok = mbar_wait(&sm.q_full[st], (u >> 1) & 1u, abort))) break;
+        if (!(ok = mbar_wait(&sm.q_full[st], (u / (uint32_t)Cfg::kStagesQ) & 1u, abort))) break;
         // (read ahead of the wait for the scores: a row of columns' values for every lane takes
         // the shared memory's whole bandwidth for half as long as the exponentials take)
         const uint32_t at_l = smem_u32(sm.lse2[st] + Cfg::kCols * wg);
@@ -891,7 +909,7 @@ __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdPar
         float4 l[Cfg::kCols / 4];
 #pragma unroll
         for (int c = 0; c < Cfg::kCols / 4; ++c) l[c] = ld_shared_f4(at_l + 16 * c);
-        if (!(ok = mbar_wait(&sm.s_full, u & 1u, abort))) break;
+        if (!(ok = mbar_wait(&sm.s_full[b], ph, abort))) break;
         tc_fence_after_sync();
         // visible query columns of key j: c in [clo, chi] of this warpgroup's
         // columns (query i = 128 qb + kCols wg + c)
@@ -957,7 +975,7 @@ __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdPar
         }
         tmem_st_wait();
         tc_fence_before_sync();
-        mbar_arrive(&sm.p_full);
+        mbar_arrive(&sm.p_full[b]);
 
         float4 dd4[8];   // D of a chunk's columns, a chunk ahead
 #pragma unroll
@@ -1019,7 +1037,7 @@ __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdPar
     const bool is_dv = wg < kHalf;
     __nv_bfloat16* dst = is_dv ? p.dv + bwd_row<PK>(I.seq, I.bkv, j, DH, p.dv_row, p.dv_head)
                                : p.dk + bwd_row<PK>(I.seq, I.bkv, j, DH, p.dk_row, p.dk_head);
-    const uint32_t colA = lane_addr + (is_dv ? Cfg::kColA0 : Cfg::kColA1);
+    const uint32_t colA = lane_addr + (is_dv ? Cfg::kColA0 : Cfg::kColAcc1);
     const float mul = is_dv ? 1.0f : p.scale;
 #pragma unroll 1
     for (int c = wg % kHalf; c < DH / 32; c += kHalf) {
@@ -1062,13 +1080,15 @@ __global__ void __launch_bounds__(BwdCfg<DH>::kThreads, 1)
     sm.abort_flag = 0;
     mbar_init(&sm.kv_full, 1);
     mbar_init(&sm.kv_empty, 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < Cfg::kStagesQ; ++i) {
       mbar_init(&sm.q_full[i], 1);
       mbar_init(&sm.q_empty[i], 1);
     }
-    mbar_init(&sm.s_full, 1);
+    for (int i = 0; i < Cfg::kBufsS; ++i) {
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], Cfg::kEW);
+    }
     mbar_init(&sm.dp_full, 1);
-    mbar_init(&sm.p_full, Cfg::kEW);
     mbar_init(&sm.ds_full, Cfg::kEW);
     mbar_init(&sm.acc_final, 1);
     mbar_init(&sm.mma_done, 1);
