@@ -432,8 +432,10 @@ __device__ __forceinline__ void bwd256_kv_softmax(Bwd256KvSmem<DK>& sm, const Bw
           for (int col = 0; col < Cfg::kCols; ++col)
             pf[col] = zero_unless_le(pf[col], (uint32_t)(col - clo), span);
         }
+        if constexpr (!DK) {
 #pragma unroll
-        for (int e = 0; !DK && e < 16; ++e) w16[e] = pack_bf16x2(pf[2 * e], pf[2 * e + 1]);
+          for (int e = 0; e < 16; ++e) w16[e] = pack_bf16x2(pf[2 * e], pf[2 * e + 1]);
+        }
         const bool two = bwd_two_parts<PK>(p, qb / 2);
         auto low = [&](uint32_t to) {   // the low parts of pf's pairs
           uint32_t l16[16];

@@ -864,9 +864,12 @@ __device__ __forceinline__ void bwd_store32(__nv_bfloat16* dst, const uint32_t (
   }
 }
 
-// Element-wise work of the dK/dV pass (warps 0-7; thread t of warpgroup wg
-// owns key row k0 + t, tensor-memory lane t, and query columns
-// kCols wg .. kCols (wg + 1) - 1).  Per step: P^T = exp2(S^T * scale*log2e - lse2[query])
+// Element-wise work of the dK/dV pass (warps 0-7; warpgroup wg owns query
+// columns kCols wg .. kCols (wg + 1) - 1, each warp 32 key rows, which are its
+// tensor-memory lanes).  A thread has 16 columns of four rows: with a row each
+// it would need lse2 and D of every column, and reading them took the shared
+// memory's whole bandwidth for twice as long as the exponentials take (128
+// lanes x 128 columns x 2 values a step).  Per step: P^T = exp2(S^T * scale*log2e - lse2[query])
 // (0 where masked), written as bf16 pairs (see bwd_packed_col) and kept in
 // fp32 registers; then dS^T = P^T o (dP^T - D[query]), as bf16 pairs over dP^T.
 // Per item: the first half of the warpgroups write dV, the second scale * dK.
@@ -879,6 +882,8 @@ __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdPar
   const int t = (warp % 4) * 32 + lane;
   const uint32_t lane_addr = tbase + ((uint32_t)((warp % 4) * 32) << 16);
   constexpr bool kTwoS = Cfg::kBufsS == 2;
+  static_assert(Cfg::kCols == 64, "two halves of 16 lanes x 64 columns per warp");
+  const int c2 = 2 * (lane % 4);   // this thread's first column of every eight
   const uint32_t colDP = lane_addr + Cfg::kColDP + Cfg::kCols * wg;
   const float2 neg_sl2 = make_float2(-p.scale_log2, -p.scale_log2);
   uint32_t u = 0;
@@ -892,7 +897,8 @@ __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdPar
     if (w >= num_items) break;
     const BwdKvItem I = bwd_kv_item_of<PK>(p, w, next);
     next = bwd_tile_ahead<PK, false>(p, it + 1, num_items, counts);
-    const int j = 128 * I.kb + t;   // this thread's key
+    const int j = 128 * I.kb + t;   // the key that this thread stores
+    const int j0 = 128 * I.kb + 32 * (warp % 4) + lane / 4;   // those it computes: j0 + 0, 8, 16, 24
     const int heads = 1 << I.seq.fold;
     for (int hh = 0; ok && hh < p.group; hh += heads) {
       for (int qb = I.lo; qb <= I.hi; ++qb, ++u) {
@@ -902,125 +908,109 @@ __device__ __forceinline__ void bwd_dkdv_softmax(BwdKvSmem<DH>& sm, const BwdPar
         const uint32_t colS = lane_addr + (b ? Cfg::kColS1 : Cfg::kColS) + Cfg::kCols * wg;
         // the stage's lse2 / D (bulk copies counted on q_full)
         if (!(ok = mbar_wait(&sm.q_full[st], (u / (uint32_t)Cfg::kStagesQ) & 1u, abort))) break;
-        // (read ahead of the wait for the scores: a row of columns' values for every lane takes
-        // the shared memory's whole bandwidth for half as long as the exponentials take)
-        const uint32_t at_l = smem_u32(sm.lse2[st] + Cfg::kCols * wg);
-        const uint32_t at_d = smem_u32(sm.dlt[st] + Cfg::kCols * wg);
-        float4 l[Cfg::kCols / 4];
+        // (read ahead of the wait for the scores)
+        const uint32_t at_l = smem_u32(sm.lse2[st] + Cfg::kCols * wg + c2);
+        const uint32_t at_d = smem_u32(sm.dlt[st] + Cfg::kCols * wg + c2);
+        float2 l[8];
 #pragma unroll
-        for (int c = 0; c < Cfg::kCols / 4; ++c) l[c] = ld_shared_f4(at_l + 16 * c);
+        for (int k = 0; k < 8; ++k) l[k] = ld_shared_f2(at_l + 32 * k);
         if (!(ok = mbar_wait(&sm.s_full[b], ph, abort))) break;
         tc_fence_after_sync();
-        // visible query columns of key j: c in [clo, chi] of this warpgroup's
-        // columns (query i = 128 qb + kCols wg + c)
-        const bool msk = bwd_needs_mask(p, I.seq, qb, I.kb);
-        int i0 = 128 * qb + Cfg::kCols * wg;
-        int clo = 0, chi = Cfg::kCols - 1, column = -1;   // c & column counts within a head
-        if (PK == 2 && I.seq.fold) {
-          i0 = 128 - I.seq.rows();
-          column = I.seq.rows() - 1;
-          chi = column;
-        }
-        if (p.causal) clo = j - i0;                                     // i >= j
-        if (p.window > 0) chi = min(chi, j - i0 + p.window - 1);        // i - j < W
-        chi = min(chi, I.seq.S - 1 - i0);                                   // i < S
-        const uint32_t span = chi >= clo ? (uint32_t)(chi - clo) : 0u;
-        if (chi < clo) clo = 1 << 30;
 
-        uint32_t x[Cfg::kChunks][32];
+        uint32_t x[2][32];
 #pragma unroll
-        for (int c = 0; c < Cfg::kChunks; ++c) tmem_ld_32x32b_x32(colS + 32 * c, x[c]);
+        for (int h = 0; h < 2; ++h) tmem_ld_16x256b_x8(colS + (h << 20), x[h]);
 #pragma unroll
-        for (int c = 0; c < Cfg::kChunks; ++c) tmem_ld_wait(x[c]);
-        float pf[Cfg::kCols];   // P^T of this row's columns (fp32)
+        for (int h = 0; h < 2; ++h) tmem_ld_wait(x[h]);
+        float pf[2][32];   // P^T (fp32)
         // (the mask in a loop of its own: a branch at every pair would keep the exponentials of
         // one pair from overlapping the next one's)
 #pragma unroll
-        for (int col = 0; col < Cfg::kCols; col += 2) {
-          const int c = col / 32, k = col % 32;
-          const float4 l4 = l[col / 4];
-          const float2 xs = __ffma2_rn(
-              make_float2(__uint_as_float(x[c][k]), __uint_as_float(x[c][k + 1])), neg_sl2,
-              col % 4 ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y));
-          pf[col] = ex2_approx(-xs.x);   // (the sign is the instruction's)
-          pf[col + 1] = ex2_approx(-xs.y);
-        }
-        if (msk) {
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int col = 0; col < Cfg::kCols; ++col) {
-            const int at = PK == 2 ? col & column : col;
-            pf[col] = zero_unless_le(pf[col], (uint32_t)(at - clo), span);
+          for (int e = 0; e < 32; e += 2) {
+            const float2 xs =
+                __ffma2_rn(make_float2(__uint_as_float(x[h][e]), __uint_as_float(x[h][e + 1])),
+                           neg_sl2, l[e / 4]);
+            pf[h][e] = ex2_approx(-xs.x);   // (the sign is the instruction's)
+            pf[h][e + 1] = ex2_approx(-xs.y);
           }
         }
+        if (bwd_needs_mask(p, I.seq, qb, I.kb)) {
+          int i0 = 128 * qb + Cfg::kCols * wg, most = Cfg::kCols - 1, column = -1;
+          if (PK == 2 && I.seq.fold) {   // columns count within a head
+            i0 = 128 - I.seq.rows();
+            column = most = I.seq.rows() - 1;
+          }
+          most = min(most, I.seq.S - 1 - i0);                                // i < S
 #pragma unroll
-        for (int c = 0; c < Cfg::kChunks; ++c) {
-          uint32_t w16[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            w16[e] = pack_bf16x2(pf[32 * c + 2 * e], pf[32 * c + 2 * e + 1]);
-          tmem_st_32x32b_x16(colS + 16 * c, w16);
-        }
-        const bool two = bwd_two_parts<PK>(p, qb);
-        if (PK && two) {   // (every score of this thread's is in registers)
-#pragma unroll
-          for (int c = 0; c < Cfg::kChunks; ++c) {
-            uint32_t w16[16];
+          for (int h = 0; h < 4; ++h) {
+            // visible query columns of key row + 8 h: [clo, chi] of this warpgroup's (query
+            // i = 128 qb + kCols wg + c)
+            const int j = j0 + 8 * h;
+            int clo = 0, chi = most;
+            if (p.causal) clo = j - i0;                                      // i >= j
+            if (p.window > 0) chi = min(chi, j - i0 + p.window - 1);         // i - j < W
+            const uint32_t span = chi >= clo ? (uint32_t)(chi - clo) : 0u;
+            if (chi < clo) clo = 1 << 30;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float a = pf[32 * c + 2 * e], b = pf[32 * c + 2 * e + 1];
-              w16[e] = bwd_low_pair(a, b, pack_bf16x2(a, b));
+              int at = 8 * (e / 2) + c2 + e % 2;
+              if (PK == 2) at &= column;
+              float& y = pf[h / 2][4 * (e / 2) + 2 * (h % 2) + e % 2];
+              y = zero_unless_le(y, (uint32_t)(at - clo), span);
             }
-            tmem_st_32x32b_x16(colS + Cfg::kCols / 2 + 16 * c, w16);
           }
         }
+        const bool two = bwd_two_parts<PK>(p, qb);
+        // pf as bf16 pairs over the columns it came from, its low parts behind them
+        auto write = [&](uint32_t col) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t w16[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w16[e] = pack_bf16x2(pf[h][2 * e], pf[h][2 * e + 1]);
+            tmem_st_16x128b_x8(col + (h << 20), w16);
+          }
+          if (PK && two) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t w16[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float a = pf[h][2 * e], b = pf[h][2 * e + 1];
+                w16[e] = bwd_low_pair(a, b, pack_bf16x2(a, b));
+              }
+              tmem_st_16x128b_x8(col + (h << 20) + Cfg::kCols / 2, w16);
+            }
+          }
+        };
+        write(colS);   // (every score of this thread's is in registers)
         tmem_st_wait();
         tc_fence_before_sync();
         mbar_arrive(&sm.p_full[b]);
 
-        float4 dd4[8];   // D of a chunk's columns, a chunk ahead
+        float2 d[8];
 #pragma unroll
-        for (int e4 = 0; e4 < 8; ++e4) dd4[e4] = ld_shared_f4(at_d + 16 * e4);
+        for (int k = 0; k < 8; ++k) d[k] = ld_shared_f2(at_d + 32 * k);
         if (!(ok = mbar_wait(&sm.dp_full, u & 1u, abort))) break;
         tc_fence_after_sync();
 #pragma unroll
-        for (int c = 0; c < Cfg::kChunks; ++c) {
-          uint32_t y[32];
-          tmem_ld_32x32b_x32(colDP + 32 * c, y);
-          tmem_ld_wait(y);
-          uint32_t w16[16];
+        for (int h = 0; h < 2; ++h) tmem_ld_16x256b_x8(colDP + (h << 20), x[h]);
 #pragma unroll
-          for (int e4 = 0; e4 < 8; ++e4) {
-            const float4 d = dd4[e4];
-            if (c + 1 < Cfg::kChunks) dd4[e4] = ld_shared_f4(at_d + 128 * (c + 1) + 16 * e4);
+        for (int h = 0; h < 2; ++h) {
+          tmem_ld_wait(x[h]);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int e = 2 * e4 + h, col = 32 * c + 2 * e;
-              const float2 dd = __fadd2_rn(
-                  make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])),
-                  h ? make_float2(-d.z, -d.w) : make_float2(-d.x, -d.y));
-              const float2 ds = __fmul2_rn(make_float2(pf[col], pf[col + 1]), dd);
-              w16[e] = pack_bf16x2(ds.x, ds.y);
-              if (PK) {   // (the weights are not needed any more)
-                pf[col] = ds.x;
-                pf[col + 1] = ds.y;
-              }
-            }
-          }
-          // (the pairs land on columns this thread loaded in chunk 0)
-          tmem_st_32x32b_x16(colDP + 16 * c, w16);
-        }
-        if (PK && two) {
-#pragma unroll
-          for (int c = 0; c < Cfg::kChunks; ++c) {
-            uint32_t w16[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float a = pf[32 * c + 2 * e], b = pf[32 * c + 2 * e + 1];
-              w16[e] = bwd_low_pair(a, b, pack_bf16x2(a, b));
-            }
-            tmem_st_32x32b_x16(colDP + Cfg::kCols / 2 + 16 * c, w16);
+          for (int e = 0; e < 32; e += 2) {
+            const float2 dd = __fadd2_rn(
+                make_float2(__uint_as_float(x[h][e]), __uint_as_float(x[h][e + 1])),
+                make_float2(-d[e / 4].x, -d[e / 4].y));
+            const float2 ds = __fmul2_rn(make_float2(pf[h][e], pf[h][e + 1]), dd);
+            pf[h][e] = ds.x;   // (the weights are not needed any more)
+            pf[h][e + 1] = ds.y;
           }
         }
+        write(colDP);
         tmem_st_wait();
         tc_fence_before_sync();
         mbar_arrive(&sm.ds_full);
