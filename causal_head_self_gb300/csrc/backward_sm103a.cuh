@@ -32,8 +32,9 @@
 // in exchange for a deterministic result.
 //
 // Roles: the first 4 kWG warps run the element-wise work and the epilogues,
-// kWG warpgroups on kWG column ranges of the same 128 rows (thread t of each
-// owns tensor-memory lane t), so each does a share of every step's
+// kWG warpgroups on kWG column ranges of the same 128 rows (a warp of each has
+// 32 tensor-memory lanes; a thread of the dQ pass one of them, of the dK/dV
+// pass 16 columns of four), so each does a share of every step's
 // exponentials and the shares run side by side (kWG = 2: two halves); the
 // next warp's lane 0 issues every TMA copy, the last warp every MMA (one
 // elected lane).  Every wait is bounded.

@@ -143,8 +143,8 @@ struct PackedShape {
 // Two or four query heads of a K/V head go into one tile of a short sequence (as 1 << the
 // result), where sequences have up to mean_rows rows on average: Q then comes in copies of 32
 // rows.  The forward pass loses nothing by it (sequences of 100 to 256 rows: the same time);
-// the backward's kernels take 13 % longer (297 us instead of 263 for 128 sequences of 128) and
-// win at 64 rows (164 instead of 203) and below.
+// the backward's kernels take 13 % longer over 128 sequences of 128 and win at 64 rows (a fifth
+// of the time) and below.
 constexpr int kFoldMeanRows = 256, kFoldMeanRowsBackward = 96;
 inline int packed_fold_max(const PackedShape& s, int mean_rows) {
   const int group = s.Hq / s.Hkv;
