@@ -1,6 +1,7 @@
 // attn_api.cu -- the C ABI declared in include/attn.h: argument checks,
 // per-device state (SM count, latched error word, decode workspace), tensor
 // maps, and the kernel launches.  No torch types cross this boundary.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -915,7 +916,18 @@ extern "C" int attn_fwd_packed_workspace(int B, int Hq, int T, int Dh, int causa
   if (!bytes) return ATTN_ERR_INVALID_ARG;
   DeviceState* st = nullptr;
   if ((rc = device_state(&st)) != ATTN_OK) return rc;
-  *bytes = chs::fwd_packed_workspace_bytes(s, launch_info(st));
+  const chs::DeviceInfo dev = launch_info(st);
+  // a call's kernel, and with it the need for a list, goes by its K/V heads too: the most that
+  // any number of them takes
+  size_t most = 0;
+  for (long long g = 1; g * g <= Hq; ++g) {
+    if (Hq % g != 0) continue;
+    for (const int kv : {(int)g, Hq / (int)g}) {
+      s.Hkv = kv;
+      most = std::max(most, chs::fwd_packed_workspace_bytes(s, dev));
+    }
+  }
+  *bytes = most;
   return ATTN_OK;
 }
 

@@ -436,8 +436,9 @@ int attn_fwd_packed(const attn_rows_t* q, const attn_rows_t* k, const attn_rows_
                     size_t workspace_bytes, int B, int Hq, int Hkv, int T, int Dh, int causal,
                     int window, float scale, cudaStream_t stream);
 
-/* The workspace of an attn_fwd_packed call on the current device, in bytes: a list of
- * blocks; 0 for causal calls of few sequences, whose workspace may be NULL. */
+/* The workspace of an attn_fwd_packed call on the current device, in bytes, with any number of
+ * K/V heads: a list of blocks; 0 for causal calls of few sequences, whose workspace may be
+ * NULL. */
 int attn_fwd_packed_workspace(int B, int Hq, int T, int Dh, int causal, size_t* bytes);
 
 /*
