@@ -339,9 +339,15 @@ struct BwdPrepPacked {
   int B, Hq, group, causal, window;
   long long S_pad;
   float scale_log2;
+  int* error_word;
 };
 
 constexpr int kPrepKeys = 32;
+
+// (checked builds: `rows` statistics from `at` on lie inside the workspace)
+__device__ __forceinline__ bool bwd_prep_inside(const BwdPrepPacked& p, size_t at, int rows) {
+  return attn_check(at + rows <= (size_t)p.Hq * p.S_pad, p.error_word);
+}
 
 // Is D of the sequence's row i made from P and dP?
 __device__ __forceinline__ bool bwd_prep_exact(const BwdPrepPacked& p, int len, int i) {
@@ -365,6 +371,9 @@ __device__ __forceinline__ void bwd_prep_rows(const BwdPrepPacked& p, const Pack
                                               int i0, int j0, int j1, int lane) {
   const int g = lane / 4, c = lane % 4;   // rows i0 + g and i0 + g + 8; columns 2 c, 2 c + 1
   const int hk = h / p.group;
+  // (checked builds: a sequence and a head of the packed tensors)
+  if (!attn_check(e.start >= 0 && e.len <= p.pk.T - e.start && h >= 0 && h < p.Hq, p.error_word))
+    return;
   auto row = [&](const __nv_bfloat16* x, long long rs, long long hs, int head, int i, int at) {
     if (i < 0 || i >= e.len) return make_uint4(0u, 0u, 0u, 0u);
     return *reinterpret_cast<const uint4*>(x + (e.start + (long long)i) * rs + head * hs + at);
@@ -434,8 +443,8 @@ __device__ __forceinline__ void bwd_prep_rows(const BwdPrepPacked& p, const Pack
     y += __shfl_xor_sync(0xffffffffu, y, 2);
     // (the weights' sum is 1 but for lse's rounding, which the passes' weights have too: divided
     // by it, the row's dS sum to 0)
-    if (exact[half] && c == 0)
-      p.delta[(size_t)h * p.S_pad + (e.stat + e.pad() + i0 + g + 8 * half)] = x / y;
+    const size_t at = (size_t)h * p.S_pad + (e.stat + e.pad() + i0 + g + 8 * half);
+    if (exact[half] && c == 0 && bwd_prep_inside(p, at, 1)) p.delta[at] = x / y;
   }
 }
 
@@ -480,6 +489,10 @@ __device__ __forceinline__ void bwd_prep_tile(const BwdPrepPacked& p) {
   const __nv_bfloat16* pd = p.dout + h * p.do_head + 8 * sub;
   const size_t to = (size_t)h * p.S_pad + (e.stat + 128 * e.blk);
   const int first = 128 * e.blk - e.pad();   // the block's first row, counted from the sequence's
+  // (checked builds: the block's rows are the sequence's, and that lies in the packed tensors)
+  if (!attn_check(e.start >= 0 && e.len <= p.pk.T - e.start && first + 128 <= e.len, p.error_word) ||
+      !bwd_prep_inside(p, to, 128))
+    return;
   constexpr int kBatch = kSets < kPrepRowSets ? kSets : kPrepRowSets;
 #pragma unroll 1
   for (int s = 0; s < kSets; s += kBatch) {

@@ -50,6 +50,7 @@ cudaError_t launch_prep(const PackedShape& s, const PackedRows& q, const PackedR
   a.window = s.window;
   a.S_pad = p.S_pad;
   a.scale_log2 = p.scale_log2;
+  a.error_word = p.error_word;
   a.cu = s.cu;
   a.B = s.B;
   const long long blocks = packed_max_tiles(s.B, s.T) * s.Hq;

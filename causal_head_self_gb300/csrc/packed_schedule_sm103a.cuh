@@ -124,7 +124,9 @@ __global__ void __launch_bounds__(kScheduleThreads)
   __syncthreads();
   all_blocks([&](int b, int a, int rows, int i) {
     const int at = atomicAdd(&hist[bin_of(padded(rows), i, packed_fold(rows, fold_max))], 1);
-    *reinterpret_cast<int4*>(tiles + at) = make_int4(a, rows, i, packed_stat(a, b));
+    // (checked builds: the list has room for the tile)
+    if (attn_check(at >= 0 && at < p.capacity, p.error_word))
+      *reinterpret_cast<int4*>(tiles + at) = make_int4(a, rows, i, packed_stat(a, b));
   });
 }
 

@@ -23,6 +23,7 @@ cudaError_t launch_packed_schedule(const PackedShape& s, int block, int fold_max
     p.order[i] = order[i];
     p.num_tiles[i] = counts[i];
   }
+  p.capacity = (int)packed_max_tiles(s.B, s.T);
   p.error_word = dev.error_word;
   return launch_pdl(attn_packed_schedule, dim3(lists), dim3(kScheduleThreads), 0, stream, p);
 }

@@ -251,6 +251,7 @@ struct PackedSchedule {
   int causal, window;
   int fold_max;    // see PackedRef
   PackedTile* tiles[2];   // one list per order (block x of the grid makes list x)
+  int capacity;           // tiles that a list has room for
   int order[2];
   int* num_tiles[2];   // three counts each
   int* error_word;

@@ -133,6 +133,11 @@ __global__ void __launch_bounds__(kRopeThreads)
     }
   }
   const int batch = p.div_s.div(row), i = row - batch * p.S;
+  // (checked builds: a row of the batch, and a head's values)
+  if (!attn_check(batch >= 0 && i >= 0 && i < p.S && at_a >= 0 && at_a + 8 <= p.Dh && at_b >= 8 &&
+                      at_b + 8 <= p.Dh,
+                  p.error_word))
+    return;
   long long page_at = -1;   // of head 0 in a pool
   long long page_head = 0;
   if (APPEND) {
@@ -143,6 +148,11 @@ __global__ void __launch_bounds__(kRopeThreads)
       const int pg = p.div_page.div(slot), page = (int)p.div_page.d;
       page_head = (long long)page * p.Dh;
       page_at = pg * (p.Hkv * page_head) + (long long)(slot - pg * page) * p.Dh;
+      // (checked builds: every head's row lies inside the pools)
+      if (!attn_check(page_at >= 0 && page_at + (p.Hkv - 1) * page_head + p.Dh <=
+                                          (long long)p.slot_end * p.Hkv * p.Dh,
+                      p.error_word))
+        page_at = -1;
     }
   }
   auto load = [&](const __nv_bfloat16* x) {
@@ -341,12 +351,17 @@ __global__ void __launch_bounds__(kPlanThreads)
     for (int i = T0; p.fill && i < p.T; i += TN) p.positions[i] = p.slots[i] = -1;
     return;
   }
+  // (checked builds: column col of sequence b lies inside the table)
+  auto in_table = [&](int b, int col) {
+    return attn_check(b >= 0 && b < p.B && col >= 0 && col < p.cols, p.error_word);
+  };
   // entry i of the stack after the pages given back were pushed
   auto stack = [&](int i) {
+    if (!attn_check(i >= 0 && i < top + given, p.error_word)) return -1;
     if (i < top) return p.free_pages[i];
     const int r = i - top, b = plan_find(give, p.B, r);
-    const int after = pages_of(rows[b]) - (give[b + 1] - give[b]);
-    return p.table[(size_t)b * p.cols + after + (r - give[b])];
+    const int col = pages_of(rows[b]) - (give[b + 1] - give[b]) + (r - give[b]);
+    return in_table(b, col) ? p.table[(size_t)b * p.cols + col] : -1;
   };
   auto pop = [&](int i) { return stack(top + (int)given - 1 - i); };
   for (int b = T0; b < p.B; b += TN) {
@@ -357,16 +372,20 @@ __global__ void __launch_bounds__(kPlanThreads)
   if (T0 == 0) *p.num_free_out = top + (int)(given - taken);
   for (int i = T0; i < (int)taken; i += TN) {
     const int b = plan_find(take, p.B, i);
-    p.table[(size_t)b * p.cols + pages_of(rows[b]) + (i - take[b])] = pop(i);
+    const int col = pages_of(rows[b]) + (i - take[b]);
+    if (in_table(b, col)) p.table[(size_t)b * p.cols + col] = pop(i);
   }
-  for (int i = top + T0; i < top + (int)(given - taken); i += TN) p.free_pages[i] = stack(i);
+  for (int i = top + T0; i < top + (int)(given - taken); i += TN)
+    if (attn_check(i < p.capacity, p.error_word)) p.free_pages[i] = stack(i);
   for (int i = T0; p.fill && i < p.T; i += TN) {
     int pos = -1, slot = -1;
     if (i < (int)tokens) {
       const int b = plan_find(tok, p.B, i), held = pages_of(rows[b]);
       pos = rows[b] + (i - tok[b]);
       const int col = p.div_page.div(pos);
-      const int pg = col < held ? p.table[(size_t)b * p.cols + col] : pop(take[b] + col - held);
+      const int pg = !in_table(b, col) ? -1
+                     : col < held      ? p.table[(size_t)b * p.cols + col]
+                                       : pop(take[b] + col - held);
       if ((unsigned)pg < (unsigned)p.num_pages)
         slot = pg * p.page + (pos - col * p.page);
       else
@@ -410,7 +429,8 @@ __global__ void __launch_bounds__(kFillThreads)
       }
       pos[e] = p.seqlens_out[b] - (next - first) + (i - first);
       const int col = p.div_page.div(pos[e]);
-      const int pg = p.table[(size_t)b * p.cols + col];
+      const bool in = attn_check(b < p.B && col >= 0 && col < p.cols, p.error_word);
+      const int pg = in ? p.table[(size_t)b * p.cols + col] : -1;
       if ((unsigned)pg < (unsigned)p.num_pages)
         slot[e] = pg * p.page + (pos[e] - col * p.page);
       else
