@@ -705,8 +705,10 @@ def attn_fwd_packed(q, k, v, cu_seqlens, o=None, lse=None, *, causal=True, windo
 def attn_bwd_packed(q, k, v, o, dout, lse, cu_seqlens, dq=None, dk=None, dv=None, *, causal=True,
                     window=0, scale=0.0, workspace=None, stream=None):
     """Backward pass of attn_fwd_packed: (dq, dk, dv) from its inputs, the o and
-    lse [Hq,T] it gave, and dout = dL/do.  The gradients may be slices of one
-    wider tensor, as q, k and v may; rows of no sequence are not written."""
+    lse [Hq,T] it gave for them (not ones joined from several sets of keys:
+    queries of few keys take nothing from o), and dout = dL/do.  The gradients
+    may be slices of one wider tensor, as q, k and v may; rows of no sequence
+    are not written."""
     window = _int32("window", window)
     B, Hq, Hkv, T, Dh, device = _packed_shape(q, k, cu_seqlens)
     wide, narrow = (T, Hq, Dh), (T, Hkv, Dh)
@@ -744,7 +746,10 @@ def attn_rope_frequencies(rotary_dim, base=10000.0, *, scaling="none", factor=1.
     pair i, scaled for a longer context by "linear", "base", "turns" (pairs by
     the turns they make over original_len: kept from `high` on, divided by
     factor up to `low`, blended between; high is 4) or "yarn" (the same with an
-    amplitude, high 32); see include/attn.h."""
+    amplitude, high 32).  Both blend linearly in the turns, as YaRN was
+    published; models whose own code blends linearly in the pair's number have
+    other frequencies, which a RopeFrequencies takes as they are.  See
+    include/attn.h."""
     if scaling not in _SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}")
     if high is None:

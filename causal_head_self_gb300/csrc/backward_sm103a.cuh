@@ -53,7 +53,7 @@
 // the products as two bf16 parts, hi + lo, 2^-16 of each: two more products for
 // those blocks, and under a short window for all.  (dQ of 24 documents of 16 to
 // 2048 rows: 1.5 times the error of a single rounding of the result before,
-// 1.25 times with it.)  D of queries that see few keys: attn_bwd_prep_packed.
+// 1.25 times with it.)  D of queries that see few keys: attn_bwd_prep_few.
 #pragma once
 
 #include <cstdint>

@@ -24,7 +24,7 @@
 //   the tensor core busy through it.  The output leaves through bulk tensor
 //   stores from the staging tiles.
 //
-//   Dh = 64, packed short sequences: as Dh 128 (256 tensor-memory columns, of
+//   Dh = 64, packed sequences alone: as Dh 128 (256 tensor-memory columns, of
 //   which S takes 128 and O the last 64).
 //
 // S is double-buffered, so the S MMA of the next key tile runs while the
@@ -90,7 +90,7 @@ struct PrefillK64Cfg {
   static constexpr int kWarpProducer = 4, kWarpIssuer = 5;
   // S buffer b at kColS + 64 b, O in the allocation's last DH columns
   static constexpr uint32_t kColS = 0, kColO = kTmemCols - DH;
-  // Dh 128: the output goes through shared memory and bulk tensor stores
+  // Dh 64 and 128: the output goes through shared memory and bulk tensor stores
   // (32 rows x 64 columns per box and softmax warp).  Dh 256 has no shared
   // memory left for it and stores from registers.
   static constexpr bool kTmaStore = DH <= 128;
@@ -113,7 +113,7 @@ struct PrefillK64Smem {
   uint8_t q[Cfg::kQBytes];
   uint8_t k[Cfg::kStagesK][Cfg::kTileBytes];
   uint8_t v[Cfg::kStagesV][Cfg::kTileBytes];
-  // per softmax warp (Dh 128): its 32 output rows x 64 columns of bf16,
+  // per softmax warp (Dh 64 and 128): its 32 output rows x 64 columns of bf16,
   // 128-byte swizzled (the layout of one box of the output's tensor map)
   uint8_t ostage[Cfg::kStageBytes > 0 ? Cfg::kStageBytes : 1];
   uint64_t q_full, q_empty;
@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(PrefillK64Cfg<DH>::kThreads, PrefillK64Cfg<DH>
     attn_prefill_k64_sm103a(const __grid_constant__ CUtensorMap map_q,
                             const __grid_constant__ CUtensorMap map_k,
                             const __grid_constant__ CUtensorMap map_v,
-                            const __grid_constant__ CUtensorMap map_o,   // Dh 128 only
+                            const __grid_constant__ CUtensorMap map_o,   // Dh 64 and 128
                             const PrefillK64Params p) {
   using Cfg = PrefillK64Cfg<DH>;
   extern __shared__ uint8_t smem_raw[];

@@ -420,6 +420,9 @@ typedef struct {
  *     the backward pass of any tensor) can reach the rows of its 128-row block
  *     that the mask hides it from, as in attn_fwd and attn_bwd.
  *   - The same inputs give the same bits.
+ *   - Which kernels run goes by T / B, the rows per sequence with the rows of
+ *     no sequence and the empty places counted.  It costs time where a few long
+ *     sequences stand among many empty places, or short ones in a long buffer.
  *   - B == 0 or T == 0 is a no-op.
  */
 
@@ -429,6 +432,8 @@ typedef struct {
  * of them (causal = 0).
  *   q, o  [T, Hq, Dh],  k, v  [T, Hkv, Dh]
  *   lse   [Hq, T]  (device, fp32, written) or NULL: as in attn_fwd_lse
+ * Where the softmax weights meet V they are rounded to bf16 (2^-8 of each, as
+ * in attn_fwd); their sum, and lse, are of fp32 ones.
  * Work is listed on the GPU, so the call reads no lengths on the host.
  */
 int attn_fwd_packed(const attn_rows_t* q, const attn_rows_t* k, const attn_rows_t* v,
@@ -445,6 +450,16 @@ int attn_fwd_packed_workspace(int B, int Hq, int T, int Dh, int causal, size_t* 
  * attn_bwd_packed -- attn_bwd of every sequence: dq [T, Hq, Dh], dk and dv
  * [T, Hkv, Dh] (summed over the query heads of each group) from q, k, v, the
  * o and lse that attn_fwd_packed gave for them, and dout = dL/do.
+ * P and dS enter their products rounded to bf16 (2^-8 of each, as in attn_bwd),
+ * but in two bf16 parts (2^-16) for the queries of a sequence's first two
+ * 128-row blocks, of which the first is the short one, and for all under a
+ * window of up to 256.
+ * D_i is dO_i . o_i with o as it was rounded, but for queries whose keys all
+ * lie within 32 rows (causal: a sequence's first 32 rows, and all under a
+ * window of up to 32; else all of a sequence of up to 32) it is
+ * sum_j p_ij dP_ij / sum_j p_ij, and o is not used.  So o and lse that were
+ * joined from several sets of keys, of which k and v are one, do not give that
+ * set's part of the gradient here (in attn_bwd they do).
  */
 int attn_bwd_packed(const attn_rows_t* q, const attn_rows_t* k, const attn_rows_t* v,
                     const attn_rows_t* o, const attn_rows_t* dout, const float* lse,
@@ -508,6 +523,9 @@ int attn_rope_append(const attn_rows_t* q, const attn_rows_t* q_out, int Hq, con
  *                     the context it was trained on: f_i from r = high on,
  *                     f_i / factor up to r = low, linear in r between them;
  *   ATTN_ROPE_YARN    the same, with amplitude 0.1 ln(factor) + 1.
+ * (The blend is linear in r, as YaRN was published.  A model whose own code
+ * blends linearly in the pair's number i, between two rounded numbers, has
+ * other frequencies: give attn_rope those, made on the host.)
  * A host call: turns [rotary_dim / 2] and amplitude are host memory.
  */
 enum { ATTN_ROPE_NONE = 0, ATTN_ROPE_LINEAR, ATTN_ROPE_BASE, ATTN_ROPE_TURNS, ATTN_ROPE_YARN };
@@ -543,7 +561,11 @@ int attn_rope_frequencies(unsigned long long* turns, float* amplitude, int rotar
  * length outside [0, cols * page], before or after, latches
  * ATTN_ERR_INVALID_ARG and leaves that sequence as it is.  A used page number
  * outside [0, num_pages) latches it too and gives slots of -1.
- * A page that is given back belongs to one sequence.  Up to 8192 sequences
+ * A page that is given back belongs to one sequence.  Attention of the new
+ * tokens is attn_fwd_packed's where their sequences held nothing before, and
+ * attn_decode_paged's of one token per sequence; several tokens of a sequence
+ * that holds rows already are planned and written, but no call attends from
+ * them to the pages.  Up to 8192 sequences
  * (ATTN_ERR_UNSUPPORTED).  B == 0 is a step of no tokens: cu_seqlens[0] is 0,
  * positions and slots are -1.
  */
@@ -563,7 +585,8 @@ int attn_status(cudaStream_t stream);
 /*
  * attn_debug_inject_fault -- test hook for the failure path; the pages
  * describe no such call.  Every later attn_fwd / attn_decode /
- * attn_decode_noalloc / attn_bwd launch in this process runs with the given fault until
+ * attn_decode_noalloc / attn_bwd launch (attn_fwd_packed as attn_fwd,
+ * attn_bwd_packed as attn_bwd) in this process runs with the given fault until
  * it is reset with kind 0:
  *   0  none (the default)
  *   1  attn_fwd: the producer never loads the first K tile of each CTA's
